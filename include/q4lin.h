@@ -218,6 +218,93 @@ int q4lin_linear_pair(const uint8_t* wq_a, const uint16_t* scales_a, const uint8
 int q4lin_fused_route(int op, int64_t N, int64_t K, int64_t T);
 
 /*
+ * LinearLora: the shared projection with the low-rank adapters of many requests beside it,
+ *   y[t] = bf16( W x[t] + sc[a] * B_a (A_a x[t]) ),  a = adapter_ids[t],
+ * each token with an adapter of its own; the second term joins the FP32 sum before the one
+ * bf16 rounding.  W, scales, x, y, N, K, T as q4lin_linear.
+ *   lora_a          device, bf16 [L, R, K], 16-byte aligned
+ *   lora_b          device, bf16 [L, N, R], 16-byte aligned
+ *   adapter_ids     device, int32 [T]; an id outside [0, L) means no adapter
+ *   adapter_scales  device, fp32 [L], or NULL (every scale 1)
+ *   ranks           device, int32 [L], or NULL (every rank R): adapter a uses the first
+ *                   ranks[a] (taken into [0, R]) rows of A_a and columns of B_a; the others
+ *                   are not used, whatever bits they hold
+ *   R               multiple of 8, 0 .. 256 (otherwise Q4LIN_ERR_UNSUPPORTED_SHAPE)
+ *   workspace       device, >= q4lin_lora_workspace_bytes(N, K, T, L, R), 256-byte aligned
+ * A x is formed in FP32 from the bf16 values; up to 32 tokens the second product is FP32
+ * too, beyond (the tile route) A x enters it as two bf16 terms (relative error 2^-17).
+ * Two kernels up to 32 tokens, three or four beyond.  L == 0, R == 0: q4lin_linear alone
+ * (with its workspace).  K == 0: y = +0.  q4lin_lora_route: the route the call takes (as
+ * q4lin_select_route), -1 for sizes it refuses.
+ */
+size_t q4lin_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int64_t L, int64_t R);
+int q4lin_lora_route(int64_t N, int64_t K, int64_t T, int64_t R);
+int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const uint16_t* lora_a,
+                      const uint16_t* lora_b, const int32_t* adapter_ids, const float* adapter_scales,
+                      const int32_t* ranks, uint16_t* y, int64_t N, int64_t K, int64_t T, int64_t L, int64_t R,
+                      void* workspace, void* stream);
+
+/*
+ * Mixture-of-experts layer with Q4_G64_FP16 experts, for a few tokens.
+ *
+ * Router:  l[t, e] = sum_h x[t, h] w_router[e, h] (+ bias[e]) in FP32, p = softmax(l[t, :]);
+ * ids[t, 0 .. top_k) are the experts with the largest l, largest first (ties: the lowest
+ * expert first), weights their p, divided by their sum if renormalize is not 0.  An expert
+ * whose l is -inf or NaN is never chosen; where fewer than top_k can be, the choices left
+ * over are id -1 with weight 0.  An l of +inf counts as the limit (equal shares among them).
+ *   x bf16 [T, H]; w_router bf16 [E, H]; bias fp32 [E] or NULL; ids int32 [T, top_k] and
+ *   weights fp32 [T, top_k] (outputs)
+ *   1 <= E <= 1024, 1 <= top_k <= min(16, E) (otherwise Q4LIN_ERR_UNSUPPORTED_SHAPE)
+ *
+ * Experts:  y[t] = bf16( sum_j weights[t, j] W_down,e (silu(W_gate,e x[t]) * (W_up,e x[t])) ),
+ * e = ids[t, j], summed over j in order; a choice whose id lies outside [0, E) adds nothing
+ * (a token without any gives +0).  All sums FP32; the intermediate vector enters W_down's
+ * product as two bf16 terms (relative error 2^-17).
+ *   wq_gate_up uint8 [E, 2F, Hp/2], scales_gate_up fp16 [E, 2F, Hp/64]: per expert, gate
+ *     rows [0, F), then up rows; wq_down uint8 [E, H, Fp/2], scales_down fp16 [E, H, Fp/64]
+ *     (Hp, Fp: H, F rounded up to 128); y bf16 [T, H] (must not overlap x)
+ *   H and F multiples of 8; E * 2F and E * H below 2^31
+ *   workspace: >= q4lin_moe_workspace_bytes(T, H, F, E, top_k), 256-byte aligned
+ * Any T runs; the kernels are made for a few tokens (every expert that some token chose is
+ * read once per pass of at most 512 / top_k tokens).  F == 0: y = +0.
+ *
+ * q4lin_moe is both in one call (three kernels): ids and weights are outputs.  All of its
+ * arguments are checked before anything is launched.
+ */
+int q4lin_moe_router(const uint16_t* x, const uint16_t* w_router, const float* bias, int32_t* ids, float* weights,
+                     int64_t T, int64_t H, int64_t E, int top_k, int renormalize, void* stream);
+size_t q4lin_moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int top_k);
+int q4lin_moe_experts(const uint16_t* x, const int32_t* ids, const float* weights, const uint8_t* wq_gate_up,
+                      const uint16_t* scales_gate_up, const uint8_t* wq_down, const uint16_t* scales_down, uint16_t* y,
+                      int64_t T, int64_t H, int64_t F, int64_t E, int top_k, void* workspace, void* stream);
+int q4lin_moe(const uint16_t* x, const uint16_t* w_router, const float* bias, const uint8_t* wq_gate_up,
+              const uint16_t* scales_gate_up, const uint8_t* wq_down, const uint16_t* scales_down, int32_t* ids,
+              float* weights, uint16_t* y, int64_t T, int64_t H, int64_t F, int64_t E, int top_k, int renormalize,
+              void* workspace, void* stream);
+
+/*
+ * Head norms with the position rotation, in one pass over the query and key heads of a
+ * projection's output.  For every token t and head v of D values:
+ *   z_i = v_i / sqrt(mean_j v_j^2 + eps) * weight_i,
+ * then the first rot columns are rotated by the angles of position p = positions[t]
+ * (cos_sin[p]: rot / 2 cosines, then rot / 2 sines):
+ *   interleaved 0: (z_i, z_{i + rot/2}) by angle i;  1: (z_{2i}, z_{2i+1}) by angle i.
+ * FP32, one rounding to bf16.
+ *   q bf16, row t at q + t * ldq, its Hq heads D apart; k likewise (Hk heads, ldk); outputs
+ *     q_out / k_out with strides ldq_out / ldk_out.  Rows may be slices of a packed row.  An
+ *     output may be its input (same pointer and stride); otherwise they must not overlap.
+ *   q_weight, k_weight bf16 [D]; cos_sin fp32 [P, rot], 16-byte aligned; positions int32 [T]
+ *   D a multiple of 8 up to 256; rot a multiple of 16, 0 .. D; strides (in elements)
+ *     multiples of 8 and at least heads * D; q, k, weights and outputs 16-byte aligned.
+ * A token whose position lies outside [0, P) is left out: its outputs stay untouched.
+ * Hq or Hk may be 0 (that side's pointers are not used).  One kernel, no workspace.
+ */
+int q4lin_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* q_weight,
+                       const uint16_t* k_weight, const float* cos_sin, const int32_t* positions, uint16_t* q_out,
+                       int64_t ldq_out, uint16_t* k_out, int64_t ldk_out, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                       int64_t rot, int64_t P, float eps, int interleaved, void* stream);
+
+/*
  * Kernels one q4lin_linear_qtype call of this format and shape launches (0 for a
  * shape it refuses or an unknown format); Q4G64 is q4lin_kernel_launches.
  */

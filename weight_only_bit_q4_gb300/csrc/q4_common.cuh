@@ -34,6 +34,33 @@ __device__ __forceinline__ uint4 ld_nc_u4(const void* p) {
   return v;
 }
 
+// Coherent global loads (no read-only path), for data that an earlier kernel of the stream
+// may have written after this kernel became resident; volatile, so that they stay behind
+// the dependency wait before them.
+__device__ __forceinline__ uint4 ld_global_u4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_global_f4(const void* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint2 ld_global_u2(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t ld_global_u32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ float fp16_bits_to_float(uint16_t b) {
   return __half2float(__ushort_as_half(b));
 }

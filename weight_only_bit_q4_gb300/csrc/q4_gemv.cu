@@ -15,6 +15,7 @@
 // which costs one FMA per weight and token; the group scale multiplies the
 // chunk partial once.  All arithmetic is FP32.
 #include "q4_internal.h"
+#include "q4_lora.cuh"
 #include "q4_sm100.cuh"
 
 namespace q4 {
@@ -221,12 +222,12 @@ struct StreamLayout {
 // (16-byte aligned; a block's run of scales plus up to 15 bytes of alignment
 // slack on either side).
 __host__ __device__ inline StreamLayout stream_layout(int64_t K, int tt, int rb, int64_t rows_cap, int nj, int slots,
-                                                      int nfull, int fmt = kFmtQ4) {
+                                                      int nfull, int fmt = kFmtQ4, int64_t lora_floats = 0) {
   StreamLayout L;
   const int64_t Kp = (K + 127) & ~(int64_t)127;   // the planes' stored width
   L.x_off = 0;
   L.part_off = (uint32_t)(tt * K * 2);
-  L.bar_off = (uint32_t)((L.part_off + rows_cap * nj * tt * 4 + 15) / 16 * 16);
+  L.bar_off = (uint32_t)((L.part_off + (rows_cap * nj * tt + lora_floats) * 4 + 15) / 16 * 16);
   L.code_off = (L.bar_off + 8 + (uint32_t)(nfull + slots) * 8 + 127) / 128 * 128;
   L.code_stride = (uint32_t)((rb * fmt_code_row(fmt, Kp) + 127) / 128 * 128);
   L.high_off = L.code_off + (uint32_t)slots * L.code_stride;
@@ -289,11 +290,18 @@ __device__ __forceinline__ float reduce_rows(const float (&acc)[RB], int lane, i
   return a[0];
 }
 
-template <int RB, int TT, bool kPad, int FMT>
+// kLora (one token, Q4): y also takes the token's low-rank adapter (q4_lora.cuh).  The shrink
+// kernel before this one waits for its own predecessor before it lets this kernel launch, so
+// everything but u is final when this kernel starts: the weights and x are streamed at once,
+// and the producer warp, once its copies are issued, waits for u and forms the rows' second
+// product (N x rank, a few thousand FMAs per CTA) beside the consumers, for the final sum.
+template <int RB, int TT, bool kPad, int FMT, bool kLora = false>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 q4_gemv_stream_kernel(const uint8_t* __restrict__ wq, const uint16_t* __restrict__ scales,
                       const uint16_t* __restrict__ x, uint16_t* __restrict__ y, int64_t N, int64_t K,
-                      int64_t rows_cap, int nj, int nw, int slots, int nfull, const uint8_t* __restrict__ wh) {
+                      int64_t rows_cap, int nj, int nw, int slots, int nfull, const uint8_t* __restrict__ wh,
+                      const LoraArgs lo) {
+  static_assert(!kLora || (TT == 1 && FMT == kFmtQ4), "adapters: one token, Q4");
   // A lane's chunk: 32 weights for one token, 16 for several, so the x values of
   // every token fit in registers.  Its codes are 16 / 8 bytes (4-bit low plane;
   // W8: 32 / 16 bytes), its high bits 4 / 2 bytes (Q5) or 8 / 4 bytes (Q6).
@@ -334,8 +342,8 @@ q4_gemv_stream_kernel(const uint8_t* __restrict__ wq, const uint16_t* __restrict
     for (int64_t off = a0; off < a1; off += 32768)
       bulk_prefetch_l2(sc_plane + off, (uint32_t)(a1 - off < 32768 ? a1 - off : 32768));
   }
-  pdl_wait_previous();  // before any global-memory read that must see the previous kernel's writes
-  const StreamLayout L = stream_layout(K, TT, RB, rows_cap, nj, slots, nfull, FMT);
+  if constexpr (!kLora) pdl_wait_previous();  // before any global-memory read that must see the previous kernel's writes
+  const StreamLayout L = stream_layout(K, TT, RB, rows_cap, nj, slots, nfull, FMT, kLora ? rows_cap + lo.R : 0);
   float* part = reinterpret_cast<float*>(smem + L.part_off);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t xbar = sbase + L.bar_off;
@@ -387,6 +395,29 @@ q4_gemv_stream_kernel(const uint8_t* __restrict__ wq, const uint16_t* __restrict
         mbar_drain(full0 + 8u * (d % nfull), (d / nfull) & 1);
     }
     __syncwarp();
+    if constexpr (kLora) {
+      float* term = part + rows_cap * nj;   // [rows_cap] second product, then u [R]
+      float* us = term + rows_cap;
+      int rank = 0;
+      const int ad = lora_adapter(lo, 0, &rank);
+      const int nrow = (int)(r1 - r0);
+      const uint16_t* B = lo.b + ((int64_t)(ad < 0 ? 0 : ad) * N + r0) * lo.R;
+      if (ad >= 0 && lane == 0 && nrow > 0)
+        bulk_prefetch_l2(B, (uint32_t)(nrow * lo.R * 2 < 262144 ? nrow * lo.R * 2 : 262144));
+      pdl_wait_previous();   // u
+      if (ad >= 0) {
+        for (int r = lane; r < lo.R; r += 32) us[r] = lora_u(lo, 1, 0, r);
+        __syncwarp();
+        for (int row = lane; row < nrow; row += 32) {
+          float v = 0.f;
+          for (int q = 0; q < rank; q += 8) v = lora_dot8(ld_global_u4(B + (int64_t)row * lo.R + q), us + q, rank - q, v);
+          term[row] = v;
+        }
+      } else {
+        for (int row = lane; row < nrow; row += 32) term[row] = 0.f;
+      }
+      __syncwarp();
+    }
   } else if (warp - 1 < nw) {
     const int w = warp - 1;
     const int items = nb * nj;
@@ -561,6 +592,7 @@ q4_gemv_stream_kernel(const uint8_t* __restrict__ wq, const uint16_t* __restrict
     const int64_t row = r / TT, t = r - (r / TT) * TT;
     float v = 0.f;
     for (int jj = 0; jj < nj; ++jj) v += part[(row * nj + jj) * TT + t];
+    if constexpr (kLora) v += part[rows_cap * nj + row];
     y[t * N + r0 + row] = float_to_bf16_bits(v);
   }
 }
@@ -584,7 +616,7 @@ struct StreamPlan {
 // warp reloads x per row decoded: 6144 x 5120 T = 3 takes 13.4 us with them,
 // 15.7 us with 4-row blocks); the ring gets as many slots as the shared-memory
 // budget holds (at least 2).
-static bool stream_plan(int64_t N, int64_t K, int64_t T, int nsm, StreamPlan* p, int fmt = kFmtQ4) {
+static bool stream_plan(int64_t N, int64_t K, int64_t T, int nsm, StreamPlan* p, int fmt = kFmtQ4, int lora_rank = 0) {
   if (N < 1 || K < 8 || T < 1 || T > 4) return false;
   p->fmt = fmt;
   p->tt = (int)T;
@@ -610,7 +642,8 @@ static bool stream_plan(int64_t N, int64_t K, int64_t T, int nsm, StreamPlan* p,
   const int lead = p->nw / p->nj + (p->nw % p->nj != 0 ? 1 : 0);
   const int64_t budget = kStreamSmemBudget;
   if (T * K * 2 > budget) return false;
-  const StreamLayout L0 = stream_layout(K, p->tt, p->rb, p->rows_cap, p->nj, 0, lead, fmt);
+  const int64_t lora_floats = lora_rank > 0 ? p->rows_cap + lora_rank : 0;
+  const StreamLayout L0 = stream_layout(K, p->tt, p->rb, p->rows_cap, p->nj, 0, lead, fmt, lora_floats);
   const int64_t per = (int64_t)L0.code_stride + L0.high_stride + L0.sc_stride + 16;
   if ((int64_t)L0.code_off + 128 > budget) return false;
   int64_t s = (budget - L0.code_off - 128) / per;
@@ -618,7 +651,7 @@ static bool stream_plan(int64_t N, int64_t K, int64_t T, int nsm, StreamPlan* p,
   if (s < 2) return false;
   p->slots = (int)s;
   p->nfull = p->slots + lead;
-  p->bytes = stream_layout(K, p->tt, p->rb, p->rows_cap, p->nj, p->slots, p->nfull, fmt).bytes;
+  p->bytes = stream_layout(K, p->tt, p->rb, p->rows_cap, p->nj, p->slots, p->nfull, fmt, lora_floats).bytes;
   return p->bytes <= budget;
 }
 
@@ -633,13 +666,13 @@ static int device_sms() {
   return n;
 }
 
-template <int RB, int TT, bool kPad, int FMT>
+template <int RB, int TT, bool kPad, int FMT, bool kLora = false>
 static int gemv_stream_launch_cfg(const LinearArgs& a, const StreamPlan& pl) {
   static bool attr[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_gemv_stream_kernel<RB, TT, kPad, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cuda_check(cudaFuncSetAttribute(q4_gemv_stream_kernel<RB, TT, kPad, FMT, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)kStreamSmemBudget),
                    "gemv: cudaFuncSetAttribute"))
       return Q4LIN_ERR_CUDA;
@@ -656,8 +689,9 @@ static int gemv_stream_launch_cfg(const LinearArgs& a, const StreamPlan& pl) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_gemv_stream_kernel<RB, TT, kPad, FMT>, a.wq, a.scales, a.x, a.y, a.N, a.K,
-                                       pl.rows_cap, pl.nj, pl.nw, pl.slots, pl.nfull, a.wh),
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_gemv_stream_kernel<RB, TT, kPad, FMT, kLora>, a.wq, a.scales, a.x, a.y, a.N,
+                                       a.K, pl.rows_cap, pl.nj, pl.nw, pl.slots, pl.nfull, a.wh,
+                                       kLora ? *a.lora : LoraArgs{}),
                     "gemv: streaming kernel launch");
 }
 
@@ -690,6 +724,22 @@ static int gemv_stream_launch(const LinearArgs& a) {
     case 2: return gemv_stream_launch_tt<2>(a, pl);
     case 3: return gemv_stream_launch_tt<3>(a, pl);
     default: return gemv_stream_launch_tt<4>(a, pl);
+  }
+}
+
+bool gemv_lora_ok(int64_t N, int64_t K, int R) {
+  StreamPlan pl;
+  return stream_plan(N, K, 1, device_sms(), &pl, kFmtQ4, R);
+}
+
+int gemv_lora_launch(const LinearArgs& a) {
+  StreamPlan pl;
+  if (!stream_plan(a.N, a.K, 1, device_sms(), &pl, kFmtQ4, a.lora->R)) return Q4LIN_ERR_INVALID_ARG;
+  const bool pad = a.K % 128 != 0;
+  switch (pl.rb) {
+    case 8: return pad ? gemv_stream_launch_cfg<8, 1, true, kFmtQ4, true>(a, pl) : gemv_stream_launch_cfg<8, 1, false, kFmtQ4, true>(a, pl);
+    case 4: return pad ? gemv_stream_launch_cfg<4, 1, true, kFmtQ4, true>(a, pl) : gemv_stream_launch_cfg<4, 1, false, kFmtQ4, true>(a, pl);
+    default: return pad ? gemv_stream_launch_cfg<2, 1, true, kFmtQ4, true>(a, pl) : gemv_stream_launch_cfg<2, 1, false, kFmtQ4, true>(a, pl);
   }
 }
 

@@ -12,6 +12,17 @@ namespace q4 {
 int cuda_check(cudaError_t e, const char* where);
 void set_error_detail(const char* what);
 
+// Low-rank adapters of LinearLora: y += scales[a] B_a (A_a x), a = ids[t].
+struct LoraArgs {
+  const uint16_t* a;      // [L, R, K] bf16
+  const uint16_t* b;      // [L, N, R] bf16
+  const int32_t* ids;     // [T]; outside [0, L): no adapter
+  const float* scales;    // [L] or NULL (1)
+  const int32_t* ranks;   // [L] or NULL (R); clamped to [0, R]
+  float* u;               // [ks, T, R] partial sums of A x along K, already scaled
+  int L, R, ks;
+};
+
 struct LinearArgs {
   const uint8_t* wq;
   const uint16_t* scales;
@@ -30,7 +41,16 @@ struct LinearArgs {
   const uint16_t* scales_b = nullptr;
   uint16_t* y_b = nullptr;
   int64_t n_b = 0;
+  // LinearLora: the adapters (GEMV and warp-MMA routes apply them in their epilogues; on the
+  // tile route, mode 3, the accumulators start from the FP32 term delta [T, N])
+  const LoraArgs* lora = nullptr;
+  const float* delta = nullptr;
 };
+
+// The adapters' two products beside the projection (q4_lora.cu).
+int lora_splits(int64_t K, int64_t T);
+int lora_shrink_launch(const LoraArgs& lo, const uint16_t* x, int64_t K, int64_t T, cudaStream_t stream);
+int lora_expand_launch(const LoraArgs& lo, float* delta, int64_t N, int64_t T, cudaStream_t stream);
 
 // The weight planes are stored for K rounded up to a multiple of 128
 // (linear-benchmark.md section 4, K_pad); columns k >= K are padding.
@@ -43,6 +63,9 @@ int gemv_launch_count(int64_t N, int64_t K, int64_t T);
 // Whether the streaming kernel (1..4 tokens, one launch) has a shared-memory plan for
 // (N, K, T) on the current device.
 bool gemv_stream_ok(int64_t N, int64_t K, int64_t T, int fmt = 0);
+// One token with an adapter of rank R on the streaming GEMV (LinearArgs::lora).
+bool gemv_lora_ok(int64_t N, int64_t K, int R);
+int gemv_lora_launch(const LinearArgs& a);
 // The sibling formats (fmt 1..3) run on the streaming GEMV only.
 int gemv_launch_fmt(const LinearArgs& a);
 
@@ -86,7 +109,48 @@ int mma_launch_count(int64_t N, int64_t K, int64_t T, int fmt = 0);
 // (swiglu: LinearSwiGLU with N = F output rows over a 2F-row weight)
 bool mma_fused_supported(int64_t N, int64_t K, int64_t T, int fmt = 0, bool swiglu = false);
 int mma_launch(const LinearArgs& a, bool fused = false);
+// LinearLora on the two-kernel form, up to 32 tokens: the operand pass also runs the shrink
+// product, the streaming kernel's band epilogue adds the second one.
+bool mma_lora_supported(int64_t N, int64_t K, int64_t T, int R);
+size_t mma_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int R);
 int mma_status(int* value, bool clear);
+
+// Query / key head norms with the position rotation (strides in elements).
+struct QkArgs {
+  const uint16_t *q, *k, *q_weight, *k_weight;
+  const float* table;      // [P, rot] fp32: cosines, then sines
+  const int32_t* pos;      // [T]
+  uint16_t *q_out, *k_out;
+  int64_t ldq, ldk, ldqo, ldko;
+  int64_t T, Hq, Hk, D, rot, P;
+  float eps;
+  bool interleaved;
+  cudaStream_t stream;
+};
+int qk_norm_rope_launch(const QkArgs& a);
+
+// Mixture-of-experts layer with Q4 experts (any T in passes of at most 512 (token, choice) slots).
+struct MoeArgs {
+  const uint16_t* x;          // [T, H]
+  const uint16_t* w_router;   // [E, H] (router only)
+  const float* bias;          // [E] or NULL (router only)
+  int32_t* ids_out;           // [T, k] (router only)
+  float* weights_out;
+  const int32_t* ids;         // [T, k] (experts only)
+  const float* weights;
+  const uint8_t *wq_gu, *wq_dn;    // [E, 2F, Hp/2], [E, H, Fp/2]
+  const uint16_t *s_gu, *s_dn;     // [E, 2F, Hp/64], [E, H, Fp/64]
+  uint16_t* y;                // [T, H]
+  int64_t T, H, F, E;
+  int k, renorm;
+  void* workspace;
+  cudaStream_t stream;
+};
+size_t moe_workspace_bytes(int64_t T, int64_t F, int k);
+int moe_launch_count(int64_t T, int k);   // of the experts' part
+int moe_router_launch(const MoeArgs& a);
+int moe_experts_launch(const MoeArgs& a);
+int moe_status(int* value, bool clear);
 
 // Reads (and optionally clears) the device error word of one translation unit.
 int gemv_status(int* value, bool clear);

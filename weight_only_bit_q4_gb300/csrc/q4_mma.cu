@@ -55,6 +55,7 @@
 // Q4LIN_ERR_TIMEOUT, every role skips its remaining work but still passes the
 // band barriers, and the producer drains the copies it issued before exiting.
 #include "q4_internal.h"
+#include "q4_lora.cuh"
 #include "q4_sm100.cuh"
 
 namespace q4 {
@@ -99,6 +100,8 @@ struct MmaParams {
                                          // the fused form's whole-K buffers)
   uint32_t scl_off, scl_bytes;           // the two band scale buffers
   uint32_t red_off, gate_off, bar_off;
+  uint32_t lora_off;                     // LinearLora: u [8 NT, R] fp32, then the tokens' adapters and ranks
+  LoraArgs lora;                         // LinearLora: the adapters (ids and u of this pass's tokens)
 };
 
 // Shared-memory layout of one launch.  Stages hold a chunk's code sub-boxes and (two-kernel
@@ -107,13 +110,13 @@ struct MmaParams {
 struct MmaLayout {
   uint32_t code_bytes, hi_bytes, xf_bytes, zs_bytes, stage_bytes, scl_bytes, red_bytes;
   uint32_t fx_off, fx_bytes, fz_off, fz_bytes;
-  uint32_t scl_off, red_off, gate_off, bar_off, total;
+  uint32_t scl_off, red_off, gate_off, lora_off, bar_off, total;
 };
 
 // fbytes: B-fragment bytes per lane per group and token tile (Q4: 32, four MMAs; W8: 16, two)
 __host__ __device__ inline MmaLayout mma_layout(int nt, int br, int ks, int mt, int stages, int lanes, int64_t Kp,
                                                 int fbytes = 32, int64_t srb = 0, bool fused = false,
-                                                int galloc = 0, bool swiglu = false, int hb = 0) {
+                                                int galloc = 0, bool swiglu = false, int hb = 0, int lora_rank = 0) {
   MmaLayout L;
   L.code_bytes = (uint32_t)(ks * br * 128);  // ks sub-boxes of br rows x 128 bytes (128-byte swizzle)
   L.hi_bytes = (uint32_t)(ks * br * 32 * hb);   // Q5 / Q6: ks sub-boxes of br rows x 32 hb bytes
@@ -134,7 +137,9 @@ __host__ __device__ inline MmaLayout mma_layout(int nt, int br, int ks, int mt, 
   // LinearSwiGLU: a gate band's FP32 sums wait here for the matching up band
   L.gate_off = L.red_off + L.red_bytes;
   const uint32_t gate_bytes = swiglu ? (uint32_t)(mt * 16 * 8 * nt * 4) : 0u;
-  L.bar_off = (L.gate_off + gate_bytes + 15) / 16 * 16;
+  L.lora_off = (L.gate_off + gate_bytes + 15) / 16 * 16;
+  const uint32_t lora_bytes = lora_rank > 0 ? (uint32_t)(8 * nt * (lora_rank * 4 + 8)) : 0u;
+  L.bar_off = (L.lora_off + lora_bytes + 15) / 16 * 16;
   L.total = L.bar_off + (uint32_t)(2 * stages + 4) * 8 + 16;
   return L;
 }
@@ -331,10 +336,13 @@ __device__ __forceinline__ void mma_operand_convert(int tp, int galloc, int lane
   }
 }
 
-template <int NT, int FMT>
+// kLora: the CTAs past `blocks` run the adapters' shrink product instead (q4_lora.cuh), so
+// that it costs no launch of its own and runs beside the conversion.
+template <int NT, int FMT, bool kLora = false>
 __global__ void __launch_bounds__(kPrepThreads)
 q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, float* __restrict__ zs,
-                   int64_t K, int tp, int galloc, int lanes, int early) {
+                   int64_t K, int tp, int galloc, int lanes, int early, int blocks, const LoraArgs lo) {
+  static_assert(!kLora || kPrepThreads == kShrinkThreads, "the shrink product's CTA size");
   // Wait for the previous kernel (it may write x, or still read these buffers).  The
   // streaming kernel launches after that wait (late order: it copies weight rows as soon
   // as it starts) or before it (early order: it only prefetches them into L2 until its
@@ -342,9 +350,17 @@ q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, flo
   if (early) pdl_launch_dependents();
   pdl_wait_previous();
   if (!early) pdl_launch_dependents();
+  if constexpr (kLora) {
+    if ((int)blockIdx.x >= blocks) {
+      __shared__ float red[kShrinkWarps * 8 * kShrinkRanks];
+      const int q = (int)blockIdx.x - blocks;
+      lora_shrink_tile(lo, x, K, tp, q / lo.ks, q % lo.ks, red);
+      return;
+    }
+  }
   const int64_t units = (int64_t)8 * NT * galloc * 4;   // a multiple of 32: whole warps take part
   for (int64_t u = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x; u - (threadIdx.x & 31) < units;
-       u += (int64_t)gridDim.x * kPrepThreads)
+       u += (int64_t)blocks * kPrepThreads)
   {
     uint4 q[2];
     mma_operand_load<NT, FMT>(x, K, tp, galloc, u, u < units, q);
@@ -357,12 +373,17 @@ q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, flo
 // consumer warps run the operand pass themselves, every CTA for all groups, into shared
 // memory, while the producer streams the weight rows -- one launch, no workspace, and no
 // wait for a second kernel's completion.  Always the early launch order.
-template <int NT, int FMT, bool kFuse = false, bool kSwi = false>
+// kLora (two-kernel form, Q4): the band epilogue adds the adapters' second product, row by row
+// and token by token on the CUDA cores (rows x tokens x rank FMAs per band: 20k at 40 rows, 32
+// tokens, rank 16, against 6.5M MMA products); the idle lanes of the producer warp pull the
+// CTA's rows of every B that a token needs into L2 meanwhile.
+template <int NT, int FMT, bool kFuse = false, bool kSwi = false, bool kLora = false>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_high,
               const MmaParams p) {
   static_assert(!kFuse || NT == 1, "the fused operand pass covers one token tile");
   static_assert(!kSwi || (kFuse && FMT == 0), "LinearSwiGLU: the one-launch Q4 form");
+  static_assert(!kLora || (!kFuse && FMT == 0), "LinearLora: the two-kernel Q4 form");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -524,6 +545,20 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
           mbar_drain(sfull0 + 8u * (q & 1), (uint32_t)((q >> 1) & 1));
       }
     }
+    if constexpr (kLora) {
+      if (lane > 0) {
+        if (p.early) pdl_wait_previous();   // late order: everything but the prep kernel's output is final
+        for (int t = lane - 1; t < p.tp; t += 31) {
+          int rank = 0;
+          const int a = lora_adapter(p.lora, t, &rank);
+          bool seen = a < 0;
+          for (int q = 0; q < t && !seen; ++q) seen = (int)ld_global_u32(p.lora.ids + q) == a;
+          const int64_t bytes = (r1 - r0) * p.lora.R * 2;
+          if (!seen && bytes > 0)
+            bulk_prefetch_l2(p.lora.b + ((int64_t)a * p.N + r0) * p.lora.R, (uint32_t)(bytes < 262144 ? bytes : 262144));
+        }
+      }
+    }
     __syncwarp();
     return;
   }
@@ -670,6 +705,23 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     }
     named_bar_sync(kRedBar, (uint32_t)(WC * 32));
     if (b == 0) pdl_wait_previous();  // the exponents are the prep kernel's; every earlier kernel is done
+    if constexpr (kLora) {
+      if (b == 0) {  // u, adapter and rank of every token
+        float* us = reinterpret_cast<float*>(smem + p.lora_off);
+        int* ad = reinterpret_cast<int*>(us + 8 * NT * p.lora.R);
+        for (int t = wc * 32 + lane; t < p.tp; t += WC * 32) {
+          int rank = 0;
+          ad[2 * t] = lora_adapter(p.lora, t, &rank);
+          ad[2 * t + 1] = rank;
+        }
+        for (int e = wc * 32 + lane; e < p.tp * p.lora.R; e += WC * 32) {
+          const int t = e / p.lora.R;
+          int rank = 0;   // (u of a token without an adapter is not written)
+          us[e] = lora_adapter(p.lora, t, &rank) >= 0 ? lora_u(p.lora, p.tp, t, e - t * p.lora.R) : 0.f;
+        }
+        named_bar_sync(kRedBar, (uint32_t)(WC * 32));
+      }
+    }
     if (ok && !*abort_flag) {
       float* gate = reinterpret_cast<float*>(smem + p.gate_off);
       const int64_t yrow = kSwi ? r0 + (int64_t)(b >> 1) * BR : R0;  // output row of band row 0
@@ -685,6 +737,18 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
         if constexpr (kSwi) {  // y = silu(g) * u, silu(g) = g / (1 + e^-g), in FP32
           const float g = gate[rw * TP + t];
           v = g / (1.f + expf(-g)) * v;
+        }
+        if constexpr (kLora) {
+          const float* us = reinterpret_cast<const float*>(smem + p.lora_off);
+          const int* ad = reinterpret_cast<const int*>(us + 8 * NT * p.lora.R);
+          const int a = ad[2 * t], rank = ad[2 * t + 1];
+          if (a >= 0) {
+            const uint16_t* br = p.lora.b + ((int64_t)a * p.N + yrow + rw) * p.lora.R;
+            float w = 0.f;
+            for (int q = 0; q < rank; q += 8)
+              w = lora_dot8(ld_global_u4(br + q), us + t * p.lora.R + q, rank - q, w);
+            v += w;
+          }
         }
         if (p.r != nullptr) v += __uint_as_float((uint32_t)p.r[gi] << 16);
         p.y[gi] = float_to_bf16_bits(v);
@@ -719,7 +783,7 @@ int mma_early_order(int fmt, int lanes, int nt) { return (fmt == 0 && nt == 1 &&
 // form (at most 8 tokens, the whole-K B fragments in shared memory), for callers without a
 // workspace; otherwise the operand pass and its workspace.
 bool mma_plan_for(int64_t N, int64_t K, int64_t T, int sms, MmaPlan* pl, int fmt = 0, bool fused = false,
-                  bool swiglu = false) {
+                  bool swiglu = false, int lora_rank = 0) {
   if (N < 1 || K < 8 || T < 1 || fmt < 0 || fmt > 3) return false;
   if (fused && (fmt == 1 || fmt == 2)) return false;   // (no fused operation takes Q5 / Q6)
   const int hb = (fmt == 1 || fmt == 2) ? fmt : 0;       // Q5 / Q6 high bits per weight
@@ -760,7 +824,7 @@ bool mma_plan_for(int64_t N, int64_t K, int64_t T, int sms, MmaPlan* pl, int fmt
     int stages = 8;
     for (; stages >= 2; --stages) {
       const MmaLayout L = mma_layout(pl->nt, br, ks, pl->mt, stages, pl->lanes, Kp, pl->fbytes, pl->srb, false, 0,
-                                     false, hb);
+                                     false, hb, lora_rank);
       if (L.total + 1024 <= kMmaSmem) break;
     }
     if (stages < 2) continue;
@@ -768,7 +832,8 @@ bool mma_plan_for(int64_t N, int64_t K, int64_t T, int sms, MmaPlan* pl, int fmt
     pl->nchunks = nchunks;
     pl->stages = stages;
     pl->galloc = nchunks * chunk_groups;
-    pl->L = mma_layout(pl->nt, br, ks, pl->mt, stages, pl->lanes, Kp, pl->fbytes, pl->srb, false, 0, false, hb);
+    pl->L = mma_layout(pl->nt, br, ks, pl->mt, stages, pl->lanes, Kp, pl->fbytes, pl->srb, false, 0, false, hb,
+                       lora_rank);
     pl->fused = 0;
     if (!fused) return true;
     // the whole-K B fragments beside at least two code stages (else fewer sub-boxes per chunk)
@@ -804,13 +869,13 @@ size_t mma_ws_zs(const MmaPlan& pl) { return ((size_t)pl.galloc * pl.nt * 64 + 2
 size_t mma_ws_total(const MmaPlan& pl) { return pl.fused ? 0 : mma_ws_xf(pl) + mma_ws_zs(pl); }
 
 // Opt a streaming-kernel instantiation into the large dynamic shared memory, once per device.
-template <int NT, int FMT, bool kFuse, bool kSwi = false>
+template <int NT, int FMT, bool kFuse, bool kSwi = false, bool kLora = false>
 int mma_kernel_attrs() {
   static bool attr[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_mma_kernel<NT, FMT, kFuse, kSwi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cuda_check(cudaFuncSetAttribute(q4_mma_kernel<NT, FMT, kFuse, kSwi, kLora>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)kMmaSmem),
                    "mma: cudaFuncSetAttribute"))
       return Q4LIN_ERR_CUDA;
@@ -824,7 +889,11 @@ int mma_launch_pass(const LinearArgs& a, const MmaPlan& pl, const CUtensorMap& t
                     int tp) {
   const bool fused = NT == 1 && pl.fused && (FMT == 0 || FMT == 3);
   const bool swi = FMT == 0 && fused && a.mode == 1;
+  const bool lora = FMT == 0 && a.lora != nullptr;
   int rc0 = Q4LIN_OK;
+  if constexpr (FMT == 0)
+    if (lora) rc0 = mma_kernel_attrs<NT, 0, false, false, true>();
+  if (rc0 != Q4LIN_OK) return rc0;
   if constexpr (FMT == 0 || FMT == 3)
     rc0 = swi ? mma_kernel_attrs<1, 0, true, true>()
               : fused ? mma_kernel_attrs<1, FMT, true>() : mma_kernel_attrs<NT, FMT, false>();
@@ -849,12 +918,21 @@ int mma_launch_pass(const LinearArgs& a, const MmaPlan& pl, const CUtensorMap& t
     cfg.stream = a.stream;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, FMT>, a.x + t0 * a.K, xf, zs, a.K, tp,
-                                      pl.galloc, pl.lanes, pl.early),
-                   "mma: prep kernel launch"))
-      return Q4LIN_ERR_CUDA;
+    cudaError_t e = cudaSuccess;
+    const int nb = (int)blocks;
+    if (!lora) {
+      e = cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, FMT>, a.x + t0 * a.K, xf, zs, a.K, tp, pl.galloc, pl.lanes,
+                             pl.early, nb, LoraArgs{});
+    } else if constexpr (FMT == 0) {   // (one pass: the caller keeps it to 32 tokens)
+      cfg.gridDim.x = (unsigned)(nb + (tp + 7) / 8 * a.lora->ks);
+      e = cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, 0, true>, a.x, xf, zs, a.K, tp, pl.galloc, pl.lanes, pl.early, nb,
+                             *a.lora);
+    }
+    if (cuda_check(e, "mma: prep kernel launch")) return Q4LIN_ERR_CUDA;
   }
   MmaParams p{};
+  if (lora) p.lora = *a.lora;
+  p.lora_off = pl.L.lora_off;
   p.wq = a.wq;
   p.scales = a.scales;
   p.xf = xf;
@@ -897,6 +975,9 @@ int mma_launch_pass(const LinearArgs& a, const MmaPlan& pl, const CUtensorMap& t
     if (swi) return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<1, 0, true, true>, tm, th, p), "mma: kernel launch");
     if (fused) return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<1, FMT, true>, tm, th, p), "mma: kernel launch");
   }
+  if constexpr (FMT == 0)
+    if (lora)
+      return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, 0, false, false, true>, tm, th, p), "mma: kernel launch");
   return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, FMT, false>, tm, th, p), "mma: kernel launch");
 }
 
@@ -930,6 +1011,17 @@ size_t mma_workspace_bytes(int64_t N, int64_t K, int64_t T, int fmt) {
   return mma_ws_total(pl);
 }
 
+bool mma_lora_supported(int64_t N, int64_t K, int64_t T, int R) {
+  MmaPlan pl;
+  return T <= 32 && mma_plan_for(N, K, T, mma_sm_count(), &pl, 0, false, false, R);
+}
+
+size_t mma_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int R) {
+  MmaPlan pl;
+  if (!mma_plan_for(N, K, T, mma_sm_count(), &pl, 0, false, false, R)) return 0;
+  return mma_ws_total(pl);
+}
+
 int mma_launch_count(int64_t, int64_t, int64_t T, int) { return 2 * (int)((T + 31) / 32); }
 
 bool mma_fused_supported(int64_t N, int64_t K, int64_t T, int fmt, bool swiglu) {
@@ -940,7 +1032,7 @@ bool mma_fused_supported(int64_t N, int64_t K, int64_t T, int fmt, bool swiglu) 
 int mma_launch(const LinearArgs& a, bool fused) {
   MmaPlan pl;
   const bool swiglu = a.mode == 1;
-  if (a.mode == 2 || (swiglu && a.fmt != 0) || !mma_plan_for(a.N, a.K, a.T, mma_sm_count(), &pl, a.fmt, fused, swiglu)) {
+  if (a.mode == 2 || (swiglu && a.fmt != 0) || !mma_plan_for(a.N, a.K, a.T, mma_sm_count(), &pl, a.fmt, fused, swiglu, a.lora != nullptr ? a.lora->R : 0)) {
     set_error_detail("mma: no shared-memory plan for this format and shape");
     return Q4LIN_ERR_UNSUPPORTED_SHAPE;
   }

@@ -98,9 +98,11 @@ struct TcParams {
   //     the rest W_b's (codes in the high-plane map slot, scales_b, y_b, n_b).
   int mode;
   uint32_t tiles_a;
+  //   mode 3, LinearLora: the accumulators start from the FP32 term delta [T, N].
   const uint16_t* scales_b;
   uint16_t* y_b;
   int64_t n_b;
+  const float* delta;
 };
 
 // Named barrier of the accumulate warps for the SwiGLU exchange (after the issue ring and kAccBar).
@@ -586,6 +588,21 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
     float2 acc[kCols / 2];
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+    if constexpr (MODE == 3) {
+      // LinearLora: the sums start from the adapters' FP32 term, read while the pipeline
+      // fills (added in the epilogue instead, as LinearAdd's residual is, the reads would
+      // stand at the end of the tile)
+      const int64_t row = m0 + r_acc;
+      if (crank == 0 && row < n_rows) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const int64_t t = t0 + cq * kCols + j;
+          const float v = t < p.T ? __uint_as_float(ld_global_u32(p.delta + t * n_rows + row)) : 0.f;
+          if (j & 1) acc[j / 2].y = v;
+          else acc[j / 2].x = v;
+        }
+      }
+    }
     bool acc_ok = true;
     // weight row of this tile row (SwiGLU: gate rows then up rows), and whether it is a real row
     const int64_t row = MODE == 1 ? (r_acc < 64 ? m0 + r_acc : p.N + m0 + (r_acc - 64)) : m0 + r_acc;
@@ -1043,7 +1060,7 @@ int launch_tile(const LinearArgs& a, int splitk, int64_t tile_base, int64_t n_ti
                          : a.mode == 2 ? tiles_a + (uint32_t)((a.n_b + kTileM - 1) / kTileM)
                                        : tiles_a;
   const TcParams p{a.scales, a.y, xe, rf, a.r, a.N, Kp, a.T, (int)((a.K + 63) / 64), splitk, (uint32_t)tile_base,
-                   tiles_m, a.mode, tiles_a, a.scales_b, a.y_b, a.n_b};
+                   tiles_m, a.mode, tiles_a, a.scales_b, a.y_b, a.n_b, a.delta};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_tiles, 1, (unsigned)splitk);
   cfg.blockDim = dim3(L::threads, 1, 1);
@@ -1318,6 +1335,15 @@ int tc_launch(const LinearArgs& a, int route) {
         case 64: return launch_tile<64, false, 0, 1>(a, splitk, base, n);
         case 32: return launch_tile<32, false, 0, 1>(a, splitk, base, n);
         default: return launch_tile<16, false, 0, 1>(a, splitk, base, n);
+      }
+    }
+    if (a.mode == 3) {
+      switch (pl.bn) {
+        case 256: return launch_tile<256, false, 0, 3>(a, splitk, base, n);
+        case 128: return launch_tile<128, false, 0, 3>(a, splitk, base, n);
+        case 64: return launch_tile<64, false, 0, 3>(a, splitk, base, n);
+        case 32: return launch_tile<32, false, 0, 3>(a, splitk, base, n);
+        default: return launch_tile<16, false, 0, 3>(a, splitk, base, n);
       }
     }
     if (a.mode == 2) {

@@ -34,6 +34,7 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t)1 << 40;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int validate_sizes(int64_t N, int64_t K, int64_t T) {
   if (N < 0 || K < 0 || T < 0) return Q4LIN_ERR_INVALID_ARG;
@@ -258,9 +259,263 @@ bool fused_op_on_mma(int64_t N, int64_t K, int64_t T, bool swiglu = false) {
   return N > 0 && K > 0 && T > 0 && T <= kFusedMmaMaxT && q4::mma_fused_supported(N, K, T, 0, swiglu);
 }
 
+// Common end of an entry point: every failure leaves a detail text.
+int finish(int st) {
+  if (st != Q4LIN_OK && q4::g_detail[0] == 0) q4::set_error_detail(q4lin_status_string(st));
+  return st;
+}
+
+int refuse(const char* why, int st = Q4LIN_ERR_INVALID_ARG) {
+  q4::set_error_detail(why);
+  return st;
+}
+
+constexpr int64_t kMaxRows = (int64_t)1 << 31;   // tensor-map coordinates and 32-bit unit counts
+constexpr int64_t kMaxExperts = 1024;
+constexpr int kMaxTopK = 16;
+
+int check_workspace(size_t need, const void* workspace) {
+  if (need > 0 && workspace == nullptr) return Q4LIN_ERR_WORKSPACE;
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return Q4LIN_ERR_MISALIGNED;
+  return Q4LIN_OK;
+}
+
+int validate_router(const void* x, const void* w, const float* bias, const void* ids, const void* weights, int64_t T,
+                    int64_t H, int64_t E, int top_k) {
+  if (T < 0 || H < 0 || E < 1 || top_k < 1) return refuse("moe: T, H >= 0, E >= 1 and top_k >= 1 are needed");
+  if (E > kMaxExperts || top_k > kMaxTopK || top_k > E)
+    return refuse("moe: at most 1024 experts and top_k <= min(16, E)", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  const int st = validate_sizes(E, H, T);
+  if (st != Q4LIN_OK) return st;
+  if (T == 0) return Q4LIN_OK;
+  if (T > (int64_t)1 << 24) return Q4LIN_ERR_INVALID_ARG;
+  if (ids == nullptr || weights == nullptr || (H > 0 && (x == nullptr || w == nullptr))) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned4(ids) || !aligned4(weights) || !aligned4(bias) || (H > 0 && (!aligned16(x) || !aligned16(w))))
+    return Q4LIN_ERR_MISALIGNED;
+  return Q4LIN_OK;
+}
+
+int validate_experts(const void* x, const void* ids, const void* weights, const void* wq_gu, const void* s_gu,
+                     const void* wq_dn, const void* s_dn, const void* y, int64_t T, int64_t H, int64_t F, int64_t E,
+                     int top_k) {
+  if (T < 0 || H < 0 || F < 0 || E < 1 || top_k < 1) return refuse("moe: T, H, F >= 0, E >= 1 and top_k >= 1 are needed");
+  if (E > kMaxExperts || top_k > kMaxTopK)
+    return refuse("moe: at most 1024 experts and top_k <= 16", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if (F > kMaxDim / 2048 || H > kMaxDim / 2048) return Q4LIN_ERR_INVALID_ARG;
+  int st = validate_sizes(E * 2 * F, H, T);
+  if (st == Q4LIN_OK) st = validate_sizes(E * H, F, T);
+  if (st != Q4LIN_OK) return st;
+  if (E * 2 * F >= kMaxRows || E * H >= kMaxRows || T > (int64_t)1 << 24 ||
+      F / 8 * (T < 512 ? T * top_k + E : 512 + E) >= kMaxRows)
+    return refuse("moe: the experts' rows exceed the 32-bit row coordinates", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if (T == 0 || H == 0) return Q4LIN_OK;
+  if (y == nullptr) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned16(y)) return Q4LIN_ERR_MISALIGNED;
+  if (F == 0) return Q4LIN_OK;
+  const void* const all[] = {x, wq_gu, s_gu, wq_dn, s_dn};
+  for (const void* q : all)
+    if (q == nullptr) return Q4LIN_ERR_INVALID_ARG;
+  if (ids == nullptr || weights == nullptr) return Q4LIN_ERR_INVALID_ARG;
+  for (const void* q : all)
+    if (!aligned16(q)) return Q4LIN_ERR_MISALIGNED;
+  if (!aligned4(ids) || !aligned4(weights)) return Q4LIN_ERR_MISALIGNED;
+  return Q4LIN_OK;
+}
+
+// LinearLora: the route of the shared projection, with the adapters applied in it.
+int lora_route(int64_t N, int64_t K, int64_t T, int R) {
+  if (T == 1 && q4::gemv_lora_ok(N, K, R)) return Q4LIN_ROUTE_GEMV;
+  if (T <= kMmaMaxT && q4::mma_lora_supported(N, K, T, R)) return Q4LIN_ROUTE_STREAM_MMA;
+  if (q4::tc_supported(N, K, T) && N < (int64_t)1 << 26) return Q4LIN_ROUTE_TC_SPLITK;
+  return -1;
+}
+
+int validate_lora_sizes(int64_t N, int64_t K, int64_t T, int64_t L, int64_t R) {
+  const int st = validate_sizes(N, K, T);
+  if (st != Q4LIN_OK) return st;
+  if (L < 0 || R < 0 || L > (int64_t)1 << 30) return Q4LIN_ERR_INVALID_ARG;
+  if (R % 8 != 0 || R > 256) {
+    q4::set_error_detail("linear_lora: the adapters' rank R must be a multiple of 8 up to 256");
+    return Q4LIN_ERR_UNSUPPORTED_SHAPE;
+  }
+  if ((double)L * (double)R * (double)K > 9.0e17 || (double)L * (double)R * (double)N > 9.0e17) return Q4LIN_ERR_INVALID_ARG;
+  if (T >= (int64_t)1 << 28) return Q4LIN_ERR_UNSUPPORTED_SHAPE;
+  return Q4LIN_OK;
+}
+
+size_t lora_u_bytes(int64_t K, int64_t T, int64_t R) {
+  return round256((size_t)q4::lora_splits(K, T) * (size_t)T * (size_t)R * 4);
+}
+
+int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const uint16_t* lora_a, const uint16_t* lora_b,
+             const int32_t* ids, const float* lora_scales, const int32_t* ranks, uint16_t* y, int64_t N, int64_t K,
+             int64_t T, int64_t L, int64_t R, void* workspace, void* stream) {
+  int st = validate_lora_sizes(N, K, T, L, R);
+  if (st == Q4LIN_OK) st = validate(wq, scales, x, y, N, K, T);
+  if (st != Q4LIN_OK || N == 0 || T == 0) return st;
+  // no adapter at all (or an empty sum): the projection alone
+  if (L == 0 || R == 0 || K == 0) return run_impl(Q4LIN_ROUTE_AUTO, wq, scales, x, y, N, K, T, workspace, stream);
+  if (lora_a == nullptr || lora_b == nullptr || ids == nullptr) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned16(lora_a) || !aligned16(lora_b) || !aligned4(ids) || !aligned4(lora_scales) || !aligned4(ranks))
+    return Q4LIN_ERR_MISALIGNED;
+  const int route = lora_route(N, K, T, (int)R);
+  if (route < 0) return refuse("linear_lora: no route plans this shape", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if ((st = check_workspace(q4lin_lora_workspace_bytes(N, K, T, L, R), workspace)) != Q4LIN_OK) return st;
+  if ((st = check_device()) != Q4LIN_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t ub = lora_u_bytes(K, T, R);
+  const q4::LoraArgs lo{lora_a, lora_b, ids, lora_scales, ranks, reinterpret_cast<float*>(ws), (int)L, (int)R,
+                        q4::lora_splits(K, T)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  q4::LinearArgs a{wq, scales, x, y, N, K, T, ws + ub, s};
+  a.lora = &lo;
+  if (route == Q4LIN_ROUTE_STREAM_MMA) return q4::mma_launch(a);
+  if ((st = q4::lora_shrink_launch(lo, x, K, T, s)) != Q4LIN_OK) return st;
+  if (route == Q4LIN_ROUTE_GEMV) return q4::gemv_lora_launch(a);
+  float* delta = reinterpret_cast<float*>(ws + ub);
+  if ((st = q4::lora_expand_launch(lo, delta, N, T, s)) != Q4LIN_OK) return st;
+  a.workspace = nullptr;
+  a.delta = delta;
+  a.mode = 3;
+  return q4::tc_launch(a, Q4LIN_ROUTE_TC_SPLITK);
+}
+
+int run_router(const uint16_t* x, const uint16_t* w, const float* bias, int32_t* ids, float* weights, int64_t T, int64_t H,
+               int64_t E, int top_k, int renormalize, void* stream) {
+  int st = validate_router(x, w, bias, ids, weights, T, H, E, top_k);
+  if (st != Q4LIN_OK || T == 0) return st;
+  if ((st = check_device()) != Q4LIN_OK) return st;
+  q4::MoeArgs a{};
+  a.x = x; a.w_router = w; a.bias = bias; a.ids_out = ids; a.weights_out = weights;
+  a.T = T; a.H = H; a.E = E; a.k = top_k; a.renorm = renormalize != 0;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return q4::moe_router_launch(a);
+}
+
+int run_experts(const uint16_t* x, const int32_t* ids, const float* weights, const uint8_t* wq_gu, const uint16_t* s_gu,
+                const uint8_t* wq_dn, const uint16_t* s_dn, uint16_t* y, int64_t T, int64_t H, int64_t F, int64_t E,
+                int top_k, void* workspace, void* stream) {
+  int st = validate_experts(x, ids, weights, wq_gu, s_gu, wq_dn, s_dn, y, T, H, F, E, top_k);
+  if (st != Q4LIN_OK || T == 0 || H == 0) return st;
+  if ((st = check_workspace(q4lin_moe_workspace_bytes(T, H, F, E, top_k), workspace)) != Q4LIN_OK) return st;
+  if ((st = check_device()) != Q4LIN_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (F == 0) return q4::cuda_check(cudaMemsetAsync(y, 0, (size_t)T * (size_t)H * 2, s), "zero fill of y");
+  q4::MoeArgs a{};
+  a.x = x; a.ids = ids; a.weights = weights;
+  a.wq_gu = wq_gu; a.s_gu = s_gu; a.wq_dn = wq_dn; a.s_dn = s_dn; a.y = y;
+  a.T = T; a.H = H; a.F = F; a.E = E; a.k = top_k;
+  a.workspace = workspace;
+  a.stream = s;
+  return q4::moe_experts_launch(a);
+}
+
+int run_qk(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* q_weight,
+           const uint16_t* k_weight, const float* cos_sin, const int32_t* positions, uint16_t* q_out, int64_t ldqo,
+           uint16_t* k_out, int64_t ldko, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t P, float eps,
+           int interleaved, void* stream) {
+  if (T < 0 || Hq < 0 || Hk < 0 || D < 0 || rot < 0 || P < 0) return Q4LIN_ERR_INVALID_ARG;
+  if (!(eps >= 0.f)) return refuse("qk_norm_rope: eps must be a number >= 0");
+  if (D % 8 != 0 || D > 256 || rot % 16 != 0 || rot > D)
+    return refuse("qk_norm_rope: D a multiple of 8 up to 256, rot a multiple of 16 up to D", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if (Hq > 65536 || Hk > 65536 || T > kMaxDim || P > (int64_t)1 << 31) return Q4LIN_ERR_INVALID_ARG;
+  if (T == 0 || D == 0 || Hq + Hk == 0) return Q4LIN_OK;
+  if (positions == nullptr || (rot > 0 && cos_sin == nullptr)) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned4(positions) || (rot > 0 && !aligned16(cos_sin))) return Q4LIN_ERR_MISALIGNED;
+  struct Side { const void *in, *w, *out; int64_t heads, ldi, ldo; };
+  const Side sides[2] = {{q, q_weight, q_out, Hq, ldq, ldqo}, {k, k_weight, k_out, Hk, ldk, ldko}};
+  for (const Side& d : sides) {
+    if (d.heads == 0) continue;
+    if (d.in == nullptr || d.w == nullptr || d.out == nullptr) return Q4LIN_ERR_INVALID_ARG;
+    if (!aligned16(d.in) || !aligned16(d.w) || !aligned16(d.out)) return Q4LIN_ERR_MISALIGNED;
+    if (d.ldi < d.heads * D || d.ldo < d.heads * D || d.ldi > kMaxDim || d.ldo > kMaxDim ||
+        (double)T * (double)d.ldi > 9.0e17 || (double)T * (double)d.ldo > 9.0e17)
+      return refuse("qk_norm_rope: a row stride is shorter than the heads of a row (or overflows)");
+    if (d.ldi % 8 != 0 || d.ldo % 8 != 0) return Q4LIN_ERR_MISALIGNED;
+  }
+  const int st = check_device();
+  if (st != Q4LIN_OK) return st;
+  q4::QkArgs a{q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, ldq, ldk, ldqo, ldko,
+               T, Hq, Hk, D, rot, P, eps, interleaved != 0, static_cast<cudaStream_t>(stream)};
+  return q4::qk_norm_rope_launch(a);
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t q4lin_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int64_t L, int64_t R) {
+  if (validate_lora_sizes(N, K, T, L, R) != Q4LIN_OK || N == 0 || K == 0 || T == 0) return 0;
+  if (L == 0 || R == 0) return q4lin_workspace_bytes(N, K, T);
+  const size_t ub = lora_u_bytes(K, T, R);
+  switch (lora_route(N, K, T, (int)R)) {
+    case Q4LIN_ROUTE_GEMV: return ub;
+    case Q4LIN_ROUTE_STREAM_MMA: return ub + round256(q4::mma_lora_workspace_bytes(N, K, T, (int)R));
+    case Q4LIN_ROUTE_TC_SPLITK: return ub + round256((size_t)T * (size_t)N * 4);
+    default: return 0;
+  }
+}
+
+int q4lin_lora_route(int64_t N, int64_t K, int64_t T, int64_t R) {
+  if (validate_lora_sizes(N, K, T, 1, R) != Q4LIN_OK) return -1;
+  if (R == 0 || N == 0 || K == 0 || T == 0) return q4lin_select_route(N, K, T);
+  return lora_route(N, K, T, (int)R);
+}
+
+int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const uint16_t* lora_a,
+                      const uint16_t* lora_b, const int32_t* adapter_ids, const float* adapter_scales,
+                      const int32_t* ranks, uint16_t* y, int64_t N, int64_t K, int64_t T, int64_t L, int64_t R,
+                      void* workspace, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_lora(wq, scales, x, lora_a, lora_b, adapter_ids, adapter_scales, ranks, y, N, K, T, L, R, workspace,
+                         stream));
+}
+
+int q4lin_moe_router(const uint16_t* x, const uint16_t* w_router, const float* bias, int32_t* ids, float* weights,
+                     int64_t T, int64_t H, int64_t E, int top_k, int renormalize, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_router(x, w_router, bias, ids, weights, T, H, E, top_k, renormalize, stream));
+}
+
+size_t q4lin_moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int top_k) {
+  if (T < 1 || H < 1 || F < 1 || E < 1 || E > kMaxExperts || top_k < 1 || top_k > kMaxTopK) return 0;
+  if (F > kMaxDim / 2048 || H > kMaxDim / 2048 || T > (int64_t)1 << 24) return 0;
+  return q4::moe_workspace_bytes(T, F, top_k);
+}
+
+int q4lin_moe_experts(const uint16_t* x, const int32_t* ids, const float* weights, const uint8_t* wq_gate_up,
+                      const uint16_t* scales_gate_up, const uint8_t* wq_down, const uint16_t* scales_down, uint16_t* y,
+                      int64_t T, int64_t H, int64_t F, int64_t E, int top_k, void* workspace, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y, T, H, F, E, top_k,
+                            workspace, stream));
+}
+
+int q4lin_moe(const uint16_t* x, const uint16_t* w_router, const float* bias, const uint8_t* wq_gate_up,
+              const uint16_t* scales_gate_up, const uint8_t* wq_down, const uint16_t* scales_down, int32_t* ids,
+              float* weights, uint16_t* y, int64_t T, int64_t H, int64_t F, int64_t E, int top_k, int renormalize,
+              void* workspace, void* stream) {
+  q4::set_error_detail("");
+  // both parts' arguments before the first launch
+  int st = validate_router(x, w_router, bias, ids, weights, T, H, E, top_k);
+  if (st == Q4LIN_OK)
+    st = validate_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y, T, H, F, E, top_k);
+  if (st == Q4LIN_OK) st = check_workspace(q4lin_moe_workspace_bytes(T, H, F, E, top_k), workspace);
+  if (st == Q4LIN_OK) st = run_router(x, w_router, bias, ids, weights, T, H, E, top_k, renormalize, stream);
+  if (st == Q4LIN_OK)
+    st = run_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y, T, H, F, E, top_k, workspace,
+                     stream);
+  return finish(st);
+}
+
+int q4lin_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* q_weight,
+                       const uint16_t* k_weight, const float* cos_sin, const int32_t* positions, uint16_t* q_out,
+                       int64_t ldq_out, uint16_t* k_out, int64_t ldk_out, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                       int64_t rot, int64_t P, float eps, int interleaved, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_qk(q, ldq, k, ldk, q_weight, k_weight, cos_sin, positions, q_out, ldq_out, k_out, ldk_out, T, Hq, Hk, D,
+                       rot, P, eps, interleaved, stream));
+}
 
 int q4lin_qtype_route(int qtype, int64_t N, int64_t K, int64_t T) {
   if (qtype == Q4LIN_QTYPE_Q4G64) return q4lin_select_route(N, K, T);
@@ -513,6 +768,8 @@ static int read_status(bool clear) {
   if (v) worst = v;
   if (q4::mma_status(&v, clear) != Q4LIN_OK) return Q4LIN_ERR_CUDA;
   if (v) worst = v;
+  if (q4::moe_status(&v, clear) != Q4LIN_OK) return Q4LIN_ERR_CUDA;
+  if (v) worst = v;
   return worst;
 }
 
@@ -546,7 +803,7 @@ int q4lin_diag_wait_expiry(uint32_t limit, int* out, void* stream) {
   return q4::wait_expiry(limit, out, static_cast<cudaStream_t>(stream));
 }
 
-const char* q4lin_version(void) { return "0.2.0"; }
+const char* q4lin_version(void) { return "0.3.0"; }
 
 const char* q4lin_last_error_detail(void) { return q4::g_detail; }
 

@@ -27,7 +27,9 @@ EXPORTS = ("q4lin_workspace_bytes", "q4lin_linear", "q4lin_linear_route", "q4lin
            "q4lin_status_string",
            "q4lin_device_status", "q4lin_clear_device_status", "q4lin_last_error_detail",
            "q4lin_hbm_read_probe", "q4lin_diag_wait_expiry", "q4lin_linear_swiglu", "q4lin_linear_pair",
-           "q4lin_qtype_workspace_bytes", "q4lin_host_workspace_bytes", "q4lin_linear_host", "q4lin_fused_route", "q4lin_qtype_route", "q4lin_version")
+           "q4lin_qtype_workspace_bytes", "q4lin_host_workspace_bytes", "q4lin_linear_host", "q4lin_fused_route", "q4lin_qtype_route", "q4lin_version",
+           "q4lin_lora_workspace_bytes", "q4lin_lora_route", "q4lin_linear_lora", "q4lin_moe_router",
+           "q4lin_moe_workspace_bytes", "q4lin_moe_experts", "q4lin_moe", "q4lin_qk_norm_rope")
 
 _lib = None
 
@@ -104,6 +106,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.q4lin_qtype_route.restype = ctypes.c_int
     lib.q4lin_fused_route.argtypes = [ctypes.c_int, i64, i64, i64]
     lib.q4lin_fused_route.restype = ctypes.c_int
+    ci, cf = ctypes.c_int, ctypes.c_float
+    lib.q4lin_lora_workspace_bytes.argtypes = [i64] * 5
+    lib.q4lin_lora_workspace_bytes.restype = sz
+    lib.q4lin_lora_route.argtypes = [i64] * 4
+    lib.q4lin_lora_route.restype = ci
+    lib.q4lin_linear_lora.argtypes = [vp] * 9 + [i64] * 5 + [vp, vp]
+    lib.q4lin_linear_lora.restype = ci
+    lib.q4lin_moe_router.argtypes = [vp] * 5 + [i64] * 3 + [ci, ci, vp]
+    lib.q4lin_moe_router.restype = ci
+    lib.q4lin_moe_workspace_bytes.argtypes = [i64] * 4 + [ci]
+    lib.q4lin_moe_workspace_bytes.restype = sz
+    lib.q4lin_moe_experts.argtypes = [vp] * 8 + [i64] * 4 + [ci, vp, vp]
+    lib.q4lin_moe_experts.restype = ci
+    lib.q4lin_moe.argtypes = [vp] * 10 + [i64] * 4 + [ci, ci, vp, vp]
+    lib.q4lin_moe.restype = ci
+    lib.q4lin_qk_norm_rope.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64] + [i64] * 6 + [cf, ci, vp]
+    lib.q4lin_qk_norm_rope.restype = ci
     lib.q4lin_version.argtypes = []
     lib.q4lin_version.restype = ctypes.c_char_p
     if path is None:
@@ -396,3 +415,234 @@ def linear_pair(wq_a, scales_a, wq_b, scales_b, x, y_a=None, y_b=None, stream=No
     if st != OK:
         raise Q4LinError(st)
     return y_a, y_b
+
+
+# ---------------------------------------------------------------- operators around the projections
+# These are called once or more per token of a decode step, where the host's time per call
+# counts: each tensor is checked once, with attribute reads only, and pointers go to the
+# library as plain integers.
+
+def _stream_ptr(stream, device):
+    import torch
+
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _need(name, t, dtype, shape):
+    """A contiguous CUDA tensor of this dtype and shape; returns its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor {dtype} {tuple(shape)}; got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _need_bits16(name, t, shape):
+    """fp16 scales, or their bit patterns in a 2-byte integer type."""
+    if t.element_size() != 2 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-byte CUDA tensor {tuple(shape)}; got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _scratch(workspace, need, device):
+    """(address, the tensor that keeps it alive) of at least ``need`` workspace bytes."""
+    import torch
+
+    if need == 0:
+        return None, None
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes")
+    return workspace.data_ptr(), workspace
+
+
+def lora_workspace_bytes(N: int, K: int, T: int, L: int, R: int) -> int:
+    """Workspace bytes of linear_lora for N x K weights, T tokens, L adapters of rank up to R."""
+    return int(load().q4lin_lora_workspace_bytes(N, K, T, L, R))
+
+
+def lora_route(N: int, K: int, T: int, R: int) -> int:
+    """Route linear_lora takes (as select_route), -1 for sizes it refuses."""
+    return int(load().q4lin_lora_route(N, K, T, R))
+
+
+def linear_lora(wq, scales, x, lora_a, lora_b, adapter_ids, adapter_scales=None, ranks=None, y=None, workspace=None,
+                stream=None):
+    """Y[T, N] = W X + scale_a B_a (A_a X), token by token with the adapter a = adapter_ids[t].
+
+    wq, scales, x as ``linear``; lora_a bf16 [L, R, K]; lora_b bf16 [L, N, R]; adapter_ids
+    int32 [T] (outside [0, L): no adapter); adapter_scales fp32 [L] or None; ranks int32 [L]
+    or None (the first ranks[a] rows of A_a and columns of B_a are used); R a multiple of 8
+    up to 256.  ``y`` (bf16 [T, N]) and ``workspace`` (uint8, >= lora_workspace_bytes) are
+    allocated here if not given.
+    """
+    import torch
+
+    bf16 = torch.bfloat16
+    T, K = x.shape
+    L, R, _ = lora_a.shape
+    N = wq.shape[0]
+    Kp = (K + 127) // 128 * 128
+    lib = load()
+    dev = x.device
+    if y is None:
+        y = torch.empty((T, N), dtype=bf16, device=dev)
+    ws, ws_keep = _scratch(workspace, lib.q4lin_lora_workspace_bytes(N, K, T, L, R), dev)
+    st = lib.q4lin_linear_lora(
+        _need("wq", wq, torch.uint8, (N, Kp // 2)), _need_bits16("scales", scales, (N, Kp // 64)), _need("x", x, bf16, (T, K)),
+        _need("lora_a", lora_a, bf16, (L, R, K)), _need("lora_b", lora_b, bf16, (L, N, R)),
+        _need("adapter_ids", adapter_ids, torch.int32, (T,)),
+        None if adapter_scales is None else _need("adapter_scales", adapter_scales, torch.float32, (L,)),
+        None if ranks is None else _need("ranks", ranks, torch.int32, (L,)), _need("y", y, bf16, (T, N)),
+        N, K, T, L, R, ws, _stream_ptr(stream, dev))
+    if st != OK:
+        raise Q4LinError(st)
+    return y
+
+
+def moe_workspace_bytes(T: int, H: int, F: int, E: int, top_k: int) -> int:
+    """Workspace bytes of moe / moe_experts."""
+    return int(load().q4lin_moe_workspace_bytes(T, H, F, E, top_k))
+
+
+def moe_router(x, w_router, top_k: int, bias=None, renormalize: bool = True, ids=None, weights=None, stream=None):
+    """The top_k experts of every token and their softmax weights: (ids int32 [T, top_k], weights fp32 [T, top_k]).
+
+    x bf16 [T, H]; w_router bf16 [E, H]; bias fp32 [E] added to the logits (-inf: the expert is
+    never chosen) or None.  Where fewer than top_k experts can be chosen, id -1 with weight 0.
+    """
+    import torch
+
+    T, H = x.shape
+    E = w_router.shape[0]
+    dev = x.device
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    st = load().q4lin_moe_router(
+        _need("x", x, torch.bfloat16, (T, H)), _need("w_router", w_router, torch.bfloat16, (E, H)),
+        None if bias is None else _need("bias", bias, torch.float32, (E,)), _need("ids", ids, torch.int32, (T, top_k)),
+        _need("weights", weights, torch.float32, (T, top_k)), T, H, E, top_k, 1 if renormalize else 0,
+        _stream_ptr(stream, dev))
+    if st != OK:
+        raise Q4LinError(st)
+    return ids, weights
+
+
+def _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H):
+    """Checked addresses of the experts' planes, E and F."""
+    import torch
+
+    E, F2 = wq_gate_up.shape[:2]
+    if F2 % 2:
+        raise ValueError("wq_gate_up holds an even number of rows per expert: gate rows, then up rows")
+    F = F2 // 2
+    Hp, Fp = (H + 127) // 128 * 128, (F + 127) // 128 * 128
+    return (_need("wq_gate_up", wq_gate_up, torch.uint8, (E, F2, Hp // 2)),
+            _need_bits16("scales_gate_up", scales_gate_up, (E, F2, Hp // 64)),
+            _need("wq_down", wq_down, torch.uint8, (E, H, Fp // 2)),
+            _need_bits16("scales_down", scales_down, (E, H, Fp // 64)), E, F)
+
+
+def moe_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y=None, workspace=None, stream=None):
+    """Y[T, H] = sum_j weights[t, j] W_down,e (silu(W_gate,e x) * (W_up,e x)), e = ids[t, j].
+
+    x bf16 [T, H]; ids int32 and weights fp32 [T, top_k] (an id outside [0, E): that choice adds
+    nothing); wq_gate_up uint8 [E, 2F, Hp/2] (gate rows, then up rows), wq_down uint8 [E, H, Fp/2]
+    with their fp16 scales per 64 columns (Hp, Fp: H, F rounded up to 128).
+    """
+    import torch
+
+    T, H = x.shape
+    k = ids.shape[1]
+    gu, gus, dn, dns, E, F = _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H)
+    lib = load()
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    ws, ws_keep = _scratch(workspace, lib.q4lin_moe_workspace_bytes(T, H, F, E, k), x.device)
+    st = lib.q4lin_moe_experts(
+        _need("x", x, torch.bfloat16, (T, H)), _need("ids", ids, torch.int32, (T, k)),
+        _need("weights", weights, torch.float32, (T, k)), gu, gus, dn, dns, _need("y", y, torch.bfloat16, (T, H)),
+        T, H, F, E, k, ws, _stream_ptr(stream, x.device))
+    if st != OK:
+        raise Q4LinError(st)
+    return y
+
+
+def moe(x, w_router, wq_gate_up, scales_gate_up, wq_down, scales_down, top_k: int, bias=None, renormalize: bool = True,
+        y=None, ids=None, weights=None, workspace=None, stream=None):
+    """The whole mixture-of-experts layer, ``moe_router`` then ``moe_experts`` in one call: (y, ids, weights)."""
+    import torch
+
+    T, H = x.shape
+    dev = x.device
+    gu, gus, dn, dns, E, F = _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H)
+    lib = load()
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    ws, ws_keep = _scratch(workspace, lib.q4lin_moe_workspace_bytes(T, H, F, E, top_k), dev)
+    st = lib.q4lin_moe(
+        _need("x", x, torch.bfloat16, (T, H)), _need("w_router", w_router, torch.bfloat16, (E, H)),
+        None if bias is None else _need("bias", bias, torch.float32, (E,)), gu, gus, dn, dns,
+        _need("ids", ids, torch.int32, (T, top_k)), _need("weights", weights, torch.float32, (T, top_k)),
+        _need("y", y, torch.bfloat16, (T, H)), T, H, F, E, top_k, 1 if renormalize else 0, ws, _stream_ptr(stream, dev))
+    if st != OK:
+        raise Q4LinError(st)
+    return y, ids, weights
+
+
+def _rows(name, t, D):
+    """Address, row stride and heads of bf16 rows [T, heads * D] or [T, heads, D], contiguous within a row."""
+    import torch
+
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() == 3:
+        if t.shape[2] != D or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+            raise ValueError(f"{name}: the heads of a row must lie side by side, {D} values each")
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * D, t.shape[1]
+    if t.dim() != 2 or t.shape[1] % D or t.stride(1) != 1:
+        raise ValueError(f"{name} must be [T, heads * {D}] or [T, heads, {D}] with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], t.shape[1] // D
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                 k_out=None, stream=None):
+    """RMS norm of every query and key head, then the rotation by the token's position: (q_out, k_out).
+
+    q bf16 [T, Hq * D] (or [T, Hq, D]) and k likewise, rows of any stride (slices of a packed
+    projection output); q_weight, k_weight bf16 [D]; cos_sin fp32 [P, rot] (rot / 2 cosines, then
+    sines); positions int32 [T] (outside [0, P): the token's outputs are not written).  ``q_out``
+    and ``k_out`` may be q and k (in place); allocated here if not given.
+    """
+    import torch
+
+    D = q_weight.shape[0]
+    T = q.shape[0]
+    P, rot = cos_sin.shape
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    qp, ldq, hq = _rows("q", q, D)
+    kp, ldk, hk = _rows("k", k, D)
+    qo, ldqo, hqo = _rows("q_out", q_out, D)
+    ko, ldko, hko = _rows("k_out", k_out, D)
+    if (hqo, hko) != (hq, hk) or k.shape[0] != T or q_out.shape[0] != T or k_out.shape[0] != T:
+        raise ValueError("q, k and their outputs must have the same tokens and heads")
+    bf16 = torch.bfloat16
+    st = load().q4lin_qk_norm_rope(
+        qp, ldq, kp, ldk, _need("q_weight", q_weight, bf16, (D,)), _need("k_weight", k_weight, bf16, (D,)),
+        _need("cos_sin", cos_sin, torch.float32, (P, rot)), _need("positions", positions, torch.int32, (T,)), qo, ldqo, ko,
+        ldko, T, hq, hk, D, rot, P, eps, 1 if interleaved else 0, _stream_ptr(stream, q.device))
+    if st != OK:
+        raise Q4LinError(st)
+    return q_out, k_out
