@@ -95,6 +95,9 @@ bool tc_supported(int64_t N, int64_t K, int64_t T);
 // driver's encoder is unavailable or refuses the arguments.
 bool encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
+// A 4-D tensor map (extents, byte strides of dimensions 1..3, box).
+bool encode_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+                   const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle);
 
 // Streaming warp-MMA route (a few tokens; any T in passes of 32): an operand pass
 // writes X as fp16 MMA fragments into the workspace, then one persistent kernel
@@ -146,10 +149,10 @@ struct MoeArgs {
   void* workspace;
   cudaStream_t stream;
 };
-size_t moe_workspace_bytes(int64_t T, int64_t F, int k);
-int moe_launch_count(int64_t T, int k);   // of the experts' part
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int k);
+// With a workspace the router also runs the experts' first operand pass into it (prepared).
 int moe_router_launch(const MoeArgs& a);
-int moe_experts_launch(const MoeArgs& a);
+int moe_experts_launch(const MoeArgs& a, bool prepared);
 int moe_status(int* value, bool clear);
 
 // Reads (and optionally clears) the device error word of one translation unit.

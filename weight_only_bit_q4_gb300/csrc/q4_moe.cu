@@ -10,30 +10,42 @@
 // Three kernels chained by programmatic dependent launch.  Bound: the packed weights of
 // the experts that some token chose, each read once; the kernels below therefore sort
 // the (token, choice) slots by expert and stream each chosen expert's rows once for all
-// of its tokens (8 token columns per MMA tile, up to kMaxNT tiles at a time).
+// of its tokens (tiles of 8 NT token columns).
 //
-// Products.  mma.sync m16n8k16 on bf16 operands with FP32 accumulation.  A: the codes as
-// exact bf16 integers q - 8 (|q - 8| <= 8): a masked nibble pair OR-ed into the mantissa
-// of 128 is the bf16 pair 128 + q, minus 136.  B, gate/up: x as it is (bf16), so every
-// product is exact.  B, down: h in FP32 is split into two bf16 terms h = hi + lo (relative
-// error 2^-17; one bf16 rounding of h alone would put about 1e-3 rms(y) of error into y),
-// two MMAs.  The 64 weights of a scale group go through four (eight) MMAs into a fresh
-// accumulator D, then acc += s D in FP32.
+// Products.  mma.sync m16n8k16 (fp16 x fp16 -> fp32); the 64 weights of a scale group go
+// through four MMAs into a fresh D, then acc += s D in FP32.  A: a masked nibble pair is the
+// fp16 subnormal pattern q 2^-24 (16 q 2^-24 for the odd nibbles, which meet B / 16), one AND
+// per two weights.  B: the vector v as fp16 at a power of two 2^-e that puts its largest |v|
+// in [2^14, 2^15); D starts from the group's zero-point term -8 2^-24 sum v, and 2^(24 + e) is
+// undone on the FP32 sum.
+//   gate/up: v = x (bf16), exact down to 2^-32 of the largest |x| and within 2^-40 of it
+//     below: every product is exact.
+//   down: v = h (FP32), rounded once to fp16 (relative error at most 2^-11, about 1.5e-4
+//     rms(y) in y, a tenth of y's own bf16 rounding; a bf16 h would put 1e-3 rms(y) there).
 //
 // Operand layout, as in the streaming warp-MMA route: the K order inside an MMA is free as
 // long as A and B agree, so thread (g = lane / 4, c = lane % 4) takes the 16 weights
 // k = 16 c .. 16 c + 15 of a group (8 code bytes per row) and the same 16 values of token
-// column g (two 16-byte loads), and pairs them as the nibble masks do: (k, k + 4).
+// column g (two 16-byte loads of fragments stored in the pairs (k, k + 4) of the masks).
 //
-// A unit is 16 MMA rows = two boxes of 8 weight rows: gate rows f0 .. f0 + 7 over up rows
-// f0 .. f0 + 7 (a thread then holds g and u of the same f and token), or 16 rows of
-// W_down.  Box row of MMA row g is 2g mod 8 (+ 1 from g = 4): in the 128-byte-swizzled
-// box the 8-byte code loads of a half warp then hit 16 different bank pairs.
+// A unit is 16 MT MMA rows = two boxes of 8 MT weight rows: gate rows f0 .. over up rows
+// f0 .. (a thread then holds g and u of the same f and token), or 16 MT rows of W_down.
+// Box row of MMA row g is 2g mod 8 (+ 1 from g = 4): in the 128-byte-swizzled box the
+// 8-byte code loads of a half warp then hit 16 different bank pairs.
 //
 // Streaming.  Every warp owns a ring of shared-memory slots, one sub-box (two boxes of
-// 8 rows x 256 weights, 2 KB, TMA) each, and works through its own sequence of
-// (unit, sub-box): lane 0 refills a slot as soon as the warp has read it, across unit
-// borders, so no warp waits for another and the ring is the only buffering.
+// 8 MT rows x 256 weights, TMA) each, and works through its own sequence of (unit,
+// sub-box): lane 0 refills a slot as soon as the warp has read it, across unit borders, so
+// no warp waits for another and the ring is the only buffering.
+//
+// Two forms, by the number of slots S = T top_k of a pass:
+//   S <= kLatSlots: latency.  MT = 1, the K range of a unit shared by up to 4 warps (partial
+//     sums joined in shared memory); every CTA of the down product converts all of h itself,
+//     owns whole units and adds its slots' sums in shared memory.
+//   otherwise: throughput.  MT = 2 (each B fragment feeds
+//     two MMA row tiles); the (tile, unit) pairs are dealt evenly over all CTAs, a kernel
+//     between the two products converts h, the slots' sums of the down product go to the
+//     workspace and a last kernel adds them in the order of the choices.
 //
 // Every mbarrier wait is bounded (kSpinLimit): on expiry the kernel records
 // Q4LIN_ERR_TIMEOUT, the warps stop computing, pass the CTA barriers and drain the
@@ -47,11 +59,12 @@ namespace {
 
 __device__ int g_moe_status = 0;
 
-constexpr int kMoeWarps = 8;
+constexpr int kMaxNT = 2;                   // token tiles of 8 handled together (4 spill)
+constexpr int kLatSlots = 16;               // up to here the latency form
+constexpr int kMaxParts = 4;                // warps that share the K range of an item, at most
+constexpr int kMoeWarps = 16;
 constexpr int kMoeThreads = 32 * kMoeWarps;
-constexpr int kBoxBytes = 8 * 128;
-constexpr int kSlotBytes = 2 * kBoxBytes;   // one sub-box: 16 rows x 256 weights
-constexpr int kMaxNT = 4;                   // token tiles of 8 handled together
+__host__ __device__ constexpr int slot_bytes(int mt) { return 2 * 8 * mt * 128; }
 constexpr int kMaxSlots = 512;              // (token, choice) pairs per pass
 constexpr int kMaxExperts = 1024;
 
@@ -68,51 +81,183 @@ struct RouterParams {
   float* weights;         // [T, k]
   int64_t T, H;
   int E, k, renorm;
+  // the operand pass of the experts' first pass, beside the router (prep_tokens 0: none)
+  uint8_t* xf;            // fragments, zero-point terms, powers of two: see moe_prep_token
+  float* zs;
+  float* ft;
+  int prep_tokens;
+  int clusters;           // clusters that route; the CTAs of the others prepare one token each
+  int parts;              // shares of H per expert (E * parts <= 128, or 1)
 };
 
-// One cluster per kRouteTokens tokens: its 128 warps share the experts, a warp's lanes
-// share H; the logits meet in the shared memory of the cluster's first CTA, whose first
-// warps pick the top_k of one token each.
+// Eight values (k .. k + 7) as fp16 at scale s1 (s16 = s1 / 16 for the odd ones) in B-fragment
+// order -- registers (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16 -- and the sum of what the MMA
+// will see of them.
+__device__ __forceinline__ uint4 moe_fragment(const float (&f)[8], float s1, float s16, float& sum) {
+  uint32_t b[4];
+  sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float sc = (q & 1) ? s16 : s1;
+    const __half lo = __float2half_rn(f[q] * sc), hi = __float2half_rn(f[q + 4] * sc);
+    b[q] = (uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16);
+    sum += (__half2float(lo) + __half2float(hi)) * ((q & 1) ? 16.f : 1.f);
+  }
+  return make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+constexpr float kZeroTerm = -8.f * 5.9604644775390625e-8f;   // -8 2^-24
+
+// Where run i of 8 K values goes inside a column's fragments: group i / 8 (128 bytes), the
+// first or second 8 of thread c = (i % 8) / 2.
+__device__ __forceinline__ int moe_fragment_at(int i) { return (i >> 3) * 128 + (i & 1) * 64 + ((i & 7) >> 1) * 16; }
+
+// Operand pass of one token, by all threads of a CTA (a multiple of 32, at most 512): x as
+// fp16 fragments, zeros past H; per group its zero-point term; and 2^(24 + e).  Tokens
+// holding Inf or NaN keep e = 0 so that those values propagate.
+__device__ __forceinline__ void moe_prep_token(const uint16_t* x, int64_t H, uint8_t* xf, float* zs, float* ft) {
+  __shared__ uint32_t wmax[16];
+  const int tid = threadIdx.x, nth = blockDim.x;
+  const int nv = (int)(H / 8), nv64 = (int)((H + 63) / 64) * 8;
+  uint32_t m2 = 0;
+  for (int i = tid; i < nv; i += nth) {
+    const uint4 v = ld_global_u4(x + 8 * (int64_t)i);
+    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  const uint32_t own = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+  if ((tid & 31) == 0) wmax[tid >> 5] = own;
+  __syncthreads();
+  uint32_t mx = wmax[0];
+  for (int w = 1; w < nth / 32; ++w) mx = max(mx, wmax[w]);
+  const int E = (int)(mx >> 7);   // bf16 biased exponent of the largest |x|
+  const int e = (mx == 0 || E == 255) ? 0 : min(max(E - 141, -100), 100);
+  const float s1 = exp2i(-e), s16 = exp2i(-e - 4);
+  // 8 values per thread; the 8 threads of a group are adjacent lanes (nv64 is a multiple of 8)
+  for (int i = tid; i - (tid & 31) < nv64; i += nth) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (i < nv) v = ld_global_u4(x + 8 * (int64_t)i);
+    const float f[8] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y), bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)};
+    float sum;
+    const uint4 b = moe_fragment(f, s1, s16, sum);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (i < nv64) {
+      *reinterpret_cast<uint4*>(xf + moe_fragment_at(i)) = b;
+      if ((i & 7) == 0) zs[i >> 3] = kZeroTerm * sum;
+    }
+  }
+  if (tid == 0) *ft = exp2i(24 + e);
+}
+
+// The same of one slot's h (FP32, F values), by one warp.
+__device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf, float* zs, float* ft) {
+  const int lane = threadIdx.x & 31;
+  const int nv = F / 8, nv64 = (F + 63) / 64 * 8;
+  uint32_t mx = 0;   // FP32 magnitude bits
+  for (int i = lane; i < 2 * nv; i += 32) {
+    const uint4 v = ld_global_u4(h + 4 * i);
+    mx = max(max(max(mx, v.x & 0x7FFFFFFFu), max(v.y & 0x7FFFFFFFu, v.z & 0x7FFFFFFFu)), v.w & 0x7FFFFFFFu);
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  const int E = (int)(mx >> 23);
+  const int e = (mx == 0 || E == 255) ? 0 : min(max(E - 141, -100), 100);
+  const float s1 = exp2i(-e), s16 = exp2i(-e - 4);
+  for (int i = lane; i - lane < nv64; i += 32) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
+    if (i < nv) {
+      a = ld_global_f4(h + 8 * i);
+      c = ld_global_f4(h + 8 * i + 4);
+    }
+    const float f[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+    float sum;
+    const uint4 b = moe_fragment(f, s1, s16, sum);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (i < nv64) {
+      *reinterpret_cast<uint4*>(hf + moe_fragment_at(i)) = b;
+      if ((i & 7) == 0) zs[i >> 3] = kZeroTerm * sum;
+    }
+  }
+  if (lane == 0) *ft = exp2i(24 + e);
+}
+
+__host__ __device__ inline int64_t moe_groups(int64_t H) { return (H + 63) / 64; }
+__host__ __device__ inline int64_t moe_zs_pitch(int64_t H) { return (moe_groups(H) + 3) / 4 * 4; }
+
+__device__ __forceinline__ void moe_prep_at(const RouterParams& p, int64_t t) {
+  moe_prep_token(p.x + t * p.H, p.H, p.xf + (size_t)t * moe_groups(p.H) * 128, p.zs + t * moe_zs_pitch(p.H), p.ft + t);
+}
+
+// The operand pass alone (experts whose routing the caller has done): one CTA per token.
+__global__ void __launch_bounds__(256) q4_moe_prep_kernel(const RouterParams p) {
+  pdl_launch_dependents();
+  pdl_wait_previous();
+  moe_prep_at(p, blockIdx.x);
+}
+
+// One cluster per TT tokens: its 128 warps share the experts (with few experts several warps
+// share the H of one), a warp's lanes share its H; the sums meet in the shared memory of the
+// cluster's first CTA, whose first warps pick the top_k of one token each.
 template <int TT>
-__global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads)
+__global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads, 2)
 q4_moe_router_kernel(const RouterParams p) {
   __shared__ float logit[TT][kMaxExperts];
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int64_t t0 = (int64_t)(blockIdx.x / kRouteCluster) * TT;
+  if ((int)blockIdx.x >= p.clusters * kRouteCluster) {   // whole clusters
+    pdl_wait_previous();
+    const int t = (int)blockIdx.x - p.clusters * kRouteCluster;
+    if (t < p.prep_tokens) moe_prep_at(p, t);
+    return;
+  }
   cluster_sync();   // every CTA of the cluster runs before its shared memory is written
   pdl_wait_previous();
   constexpr int kWarps = kRouteThreads / 32;
   const int64_t nv = p.H / 8;
-  for (int e = warp * kRouteCluster + (int)rank; e < p.E; e += kRouteCluster * kWarps) {
+  for (int w = warp * kRouteCluster + (int)rank; w < p.E * p.parts; w += kRouteCluster * kWarps) {
+    const int e = w / p.parts, part = w - e * p.parts;
+    const int64_t i0 = nv * part / p.parts, i1 = nv * (part + 1) / p.parts;
     float acc[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = 0.f;
     const uint16_t* wr = p.w + (int64_t)e * p.H;
-#pragma unroll 4
-    for (int64_t i = lane; i < nv; i += 32) {
-      const uint4 wv = ld_global_u4(wr + 8 * i);
-      const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+    constexpr int kAhead = TT == 1 ? 4 : 2;   // loads of this many steps in flight
+    for (int64_t i = i0 + lane; i < i1; i += 32 * kAhead) {
+      uint4 wv[kAhead], xv[kAhead][TT];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int64_t tt = t0 + t < p.T ? t0 + t : p.T - 1;
-        const uint4 xv = ld_global_u4(p.x + tt * p.H + 8 * i);
-        const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+      for (int q = 0; q < kAhead; ++q) {
+        const bool in = i + 32 * q < i1;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        wv[q] = in ? ld_global_u4(wr + 8 * (i + 32 * q)) : zero;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          acc[t] = fmaf(bf16lo(ww[q]), bf16lo(xx[q]), acc[t]);
-          acc[t] = fmaf(bf16hi(ww[q]), bf16hi(xx[q]), acc[t]);
+        for (int t = 0; t < TT; ++t) {
+          const int64_t tt = t0 + t < p.T ? t0 + t : p.T - 1;
+          xv[q][t] = in ? ld_global_u4(p.x + tt * p.H + 8 * (i + 32 * q)) : zero;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const uint32_t ww[4] = {wv[q].x, wv[q].y, wv[q].z, wv[q].w};
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const uint32_t xx[4] = {xv[q][t].x, xv[q][t].y, xv[q][t].z, xv[q][t].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[t] = fmaf(bf16lo(ww[k]), bf16lo(xx[k]), acc[t]);
+            acc[t] = fmaf(bf16hi(ww[k]), bf16hi(xx[k]), acc[t]);
+          }
         }
       }
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = warp_sum(acc[t]);
     if (lane == 0) {
-      const float b = p.bias != nullptr ? __uint_as_float(ld_global_u32(p.bias + e)) : 0.f;
+      const float b = p.bias != nullptr && part == 0 ? __uint_as_float(ld_global_u32(p.bias + e)) : 0.f;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const uint32_t dst = mapa_shared(smem_u32(&logit[t][e]), 0);
+      for (int t = 0; t < TT; ++t) {   // part after part: [parts][E]
+        const uint32_t dst = mapa_shared(smem_u32(&logit[t][part * p.E + e]), 0);
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(acc[t] + b) : "memory");
       }
     }
@@ -124,9 +269,11 @@ q4_moe_router_kernel(const RouterParams p) {
   constexpr float kNone = -INFINITY;   // never chosen: -inf, NaN and what is already chosen
   float m = kNone;
   for (int e = lane; e < p.E; e += 32) {
-    const float v = lg[e];
-    if (!(v > kNone)) lg[e] = kNone;   // NaN too
-    else m = fmaxf(m, v);
+    float v = lg[e];
+    for (int q = 1; q < p.parts; ++q) v += lg[q * p.E + e];
+    v = v > kNone ? v : kNone;   // NaN too
+    lg[e] = v;
+    m = fmaxf(m, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -138,34 +285,44 @@ q4_moe_router_kernel(const RouterParams p) {
   }
   z = warp_sum(z);
   __syncwarp();
-  float chosen = 0.f, mine = 0.f;   // lane j keeps pick j (k <= 32)
-  int mine_id = -1;
-  for (int j = 0; j < p.k; ++j) {
-    float best = kNone;
-    int at = -1;
+  // Each lane keeps its own best (as an order-preserving integer) and looks for the next one
+  // only after it was picked.
+  auto key_of = [](float v) {   // larger float, larger key; kNone is the smallest that occurs
+    const uint32_t b = __float_as_uint(v);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  };
+  uint32_t key = 0u;
+  int at = p.E;
+  auto scan = [&]() {
+    key = 0u;
+    at = p.E;
     for (int e = lane; e < p.E; e += 32) {
       const float v = lg[e];
-      if (v > best) {
-        best = v;
+      const uint32_t q = key_of(v);
+      if (v > kNone && q > key) {
+        key = q;
         at = e;
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-      if (oa >= 0 && (at < 0 || ov > best || (ov == best && oa < at))) {
-        best = ov;
-        at = oa;
-      }
-    }
-    const float pe = at >= 0 ? ex(best) : 0.f;
+  };
+  scan();
+  float chosen = 0.f, mine = 0.f;   // lane j keeps pick j (k <= 32)
+  int mine_id = -1;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+    if (top == 0u) break;   // none left
+    const int id = __reduce_min_sync(0xffffffffu, key == top ? at : p.E);
+    const uint32_t b = (top & 0x80000000u) ? top & 0x7FFFFFFFu : ~top;
+    const float pe = ex(__uint_as_float(b));
     chosen += pe;
     if (lane == j) {
       mine = pe;
-      mine_id = at;
+      mine_id = id;
     }
-    if (at >= 0 && lane == (at & 31)) lg[at] = kNone;
+    if (lane == (id & 31)) {
+      lg[id] = kNone;
+      scan();
+    }
     __syncwarp();
   }
   if (lane < p.k) {
@@ -177,24 +334,32 @@ q4_moe_router_kernel(const RouterParams p) {
 
 // ----------------------------------------------------------------- slots by expert
 struct MoeParams {
-  const uint16_t* x;       // [T, H] bf16 (first token of the pass)
+  const uint8_t* xf;       // operand pass: fragments [T][groups][128], terms [T][pitch], powers [T]
+  const float* zs;
+  const float* ft;
   const int32_t* ids;      // [T, k]
   const float* weights;    // [T, k]
   const uint16_t* s_gu;    // [E, 2F, Hp/64]
   const uint16_t* s_dn;    // [E, H, Fp/64]
-  uint16_t* h_hi;          // [T k, F] bf16 high and low terms of h
-  uint16_t* h_lo;
+  float* h;                // [T k][F]
+  uint8_t* hf;             // throughput form: h as fragments, terms and powers (like xf, zs, ft)
+  float* hz;
+  float* hft;
+  float* part;             // throughput form: [T k][H] sums of the down product
   uint16_t* y;             // [T, H]
   int64_t H, F;
   int E, k, slots;         // slots = T k of this pass
   int depth;               // ring slots per warp
+  uint32_t bar_off, cnt_off, wcnt_off, order_off, tiles_off, misc_off, sum_off, frag_off;   // shared memory
+  uint32_t frag_pitch;     // latency form, down: bytes per slot of the fragments in shared memory
 };
 
 // Shared-memory lists of one CTA: the tiles (up to 8 kMaxNT slots of one expert) in
 // expert order.
 struct MoeLists {
-  int* cnt;        // [E] slots per expert, then the fill positions
-  int* order;      // [slots] slot numbers by expert
+  int* cnt;        // [E] first positions
+  uint8_t* wcnt;   // [16][E] slots per warp and expert
+  int* order;      // [slots] by expert: slot number | token << 16
   int2* tiles;     // [max tiles] (expert, first position | count << 16)
   int* ntiles;
 };
@@ -208,21 +373,17 @@ __host__ __device__ inline int moe_max_tiles(int slots, int E, int per) {
 // whose id is outside [0, E) are left out.  Inside an expert the slots keep their order: the
 // units of a tile are spread over CTAs, which must all put the same slots into it.
 __device__ __forceinline__ void moe_build_lists(const MoeParams& p, const MoeLists& L, int per) {
-  const int tid = threadIdx.x;
-  for (int e = tid; e < p.E; e += kMoeThreads) L.cnt[e] = 0;
-  __syncthreads();
-  for (int s = tid; s < p.slots; s += kMoeThreads) {
-    const int e = (int)ld_global_u32(p.ids + s);
-    if (e >= 0 && e < p.E) atomicAdd(&L.cnt[e], 1);
-  }
-  __syncthreads();
-  if (tid < 32) {  // exclusive sums over the experts, 32 at a time
-    int base = 0, tbase = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + tid;
-      const int n = e < p.E ? L.cnt[e] : 0;
-      const int nt = (n + per - 1) / per;
-      int a = n, b = nt;
+  const int tid = threadIdx.x, nth = blockDim.x;
+  if (p.slots <= 32) {   // one warp, one load: experts in the order of their first slots
+    if (tid < 32) {
+      int e = tid < p.slots ? (int)ld_global_u32(p.ids + tid) : -1;
+      if (e >= p.E) e = -1;
+      const bool on = e >= 0;
+      const unsigned same = __match_any_sync(0xffffffffu, on ? e : -1);
+      const int n = __popc(same), rank = __popc(same & ((1u << tid) - 1u));
+      const bool lead = on && rank == 0;
+      int a = lead ? n : 0, b = lead ? (n + per - 1) / per : 0;
+      const int slots_here = a, tiles_here = b;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int a2 = __shfl_up_sync(0xffffffffu, a, o), b2 = __shfl_up_sync(0xffffffffu, b, o);
@@ -231,162 +392,210 @@ __device__ __forceinline__ void moe_build_lists(const MoeParams& p, const MoeLis
           b += b2;
         }
       }
+      const int pos = a - slots_here;
+      const int base = __shfl_sync(0xffffffffu, pos, __ffs(same) - 1);
+      if (on) L.order[base + rank] = tid | (tid / p.k) << 16;
+      for (int i = 0; i < tiles_here; ++i) {
+        const int left = n - i * per;
+        L.tiles[b - tiles_here + i] = make_int2(e, (pos + i * per) | ((left < per ? left : per) << 16));
+      }
+      if (tid == 31) *L.ntiles = b;
+    }
+    __syncthreads();
+    return;
+  }
+  // One slot per thread (S <= kMaxSlots = the threads of the throughput form): ranks inside a
+  // warp by matching, counts per (warp, expert), then sums over the warps and the experts.
+  const int warp = tid >> 5, lane = tid & 31, warps = nth / 32;
+  uint32_t* z = reinterpret_cast<uint32_t*>(L.wcnt);
+  for (int i = tid; i < (warps * p.E + 3) / 4; i += nth) z[i] = 0u;
+  int e = tid < p.slots ? (int)ld_global_u32(p.ids + tid) : -1;
+  if (e < 0 || e >= p.E) e = -1;
+  __syncthreads();
+  const unsigned same = __match_any_sync(0xffffffffu, e);
+  const int rank = __popc(same & ((1u << lane) - 1u));
+  if (e >= 0 && rank == 0) L.wcnt[warp * p.E + e] = (uint8_t)__popc(same);
+  __syncthreads();
+  if (warp == 0) {  // exclusive sums over the experts, 32 at a time
+    int base = 0, tbase = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int x = e0 + lane;
+      int n = 0;
+      if (x < p.E)
+        for (int w = 0; w < warps; ++w) n += L.wcnt[w * p.E + x];
+      const int nt = (n + per - 1) / per;
+      int a = n, b = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a2 = __shfl_up_sync(0xffffffffu, a, o), b2 = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+          a += a2;
+          b += b2;
+        }
+      }
       const int pos = base + a - n, tp = tbase + b - nt;
       for (int i = 0; i < nt; ++i) {
         const int left = n - i * per;
-        L.tiles[tp + i] = make_int2(e, (pos + i * per) | ((left < per ? left : per) << 16));
+        L.tiles[tp + i] = make_int2(x, (pos + i * per) | ((left < per ? left : per) << 16));
       }
-      if (e < p.E) L.cnt[e] = pos;
+      if (x < p.E) L.cnt[x] = pos;
       base += __shfl_sync(0xffffffffu, a, 31);
       tbase += __shfl_sync(0xffffffffu, b, 31);
     }
-    if (tid == 0) *L.ntiles = tbase;
+    if (lane == 0) *L.ntiles = tbase;
   }
   __syncthreads();
-  if (tid < 32) {  // fill in slot order, 32 slots at a time: rank among the equal ids of the 32
-    for (int s0 = 0; s0 < p.slots; s0 += 32) {
-      const int s = s0 + tid;
-      int e = s < p.slots ? (int)ld_global_u32(p.ids + s) : -1;
-      if (e >= p.E) e = -1;
-      const unsigned same = __match_any_sync(0xffffffffu, e);
-      const int at = e >= 0 ? L.cnt[e] : 0;
-      __syncwarp();
-      if (e >= 0) {
-        L.order[at + __popc(same & ((1u << tid) - 1u))] = s;
-        if ((same >> tid) == 1u) L.cnt[e] = at + __popc(same);   // the highest lane of the id
-      }
-      __syncwarp();
-    }
+  if (e >= 0) {
+    int at = L.cnt[e] + rank;
+    for (int w = 0; w < warp; ++w) at += L.wcnt[w * p.E + e];
+    L.order[at] = tid | (tid / p.k) << 16;
   }
   __syncthreads();
 }
 
 // ----------------------------------------------------------------- the product of a unit
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// D = A . B + C
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Code words w0, w1 (weights k .. k + 15) as eight bf16 pairs q - 8: (k, k + 4), (k + 1, k + 5),
-// (k + 2, k + 6), (k + 3, k + 7), and the same of k + 8.
-__device__ __forceinline__ void decode_pairs_bf16(uint2 w, uint32_t (&a)[8]) {
+// The 16 weights of two code words as eight A registers, pairs (k, k + 4), (k + 1, k + 5),
+// (k + 2, k + 6), (k + 3, k + 7) and the same of k + 8: fp16 patterns q 2^-24 (even registers)
+// and 16 q 2^-24 (odd ones).
+__device__ __forceinline__ void decode_pairs(uint2 w, uint32_t (&a)[8]) {
+  const uint32_t v0 = w.x >> 8, v1 = w.y >> 8;
+  a[0] = w.x & 0x000F000Fu;
+  a[1] = w.x & 0x00F000F0u;
+  a[2] = v0 & 0x000F000Fu;
+  a[3] = v0 & 0x00F000F0u;
+  a[4] = w.y & 0x000F000Fu;
+  a[5] = w.y & 0x00F000F0u;
+  a[6] = v1 & 0x000F000Fu;
+  a[7] = v1 & 0x00F000F0u;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// What a warp holds of one unit while it runs through the unit's K range: where its rows'
+// scales and its B columns start.  Plain loads (not the volatile ones) in the loops, so that
+// the compiler can overlap the groups of a sub-box; the waits before them are compiler
+// barriers.
+template <int NT, int MT>
+struct MoeUnit {
+  const uint16_t* s0[MT];    // scales of MMA rows g and g + 8
+  const uint16_t* s1[MT];
+  const uint8_t* b[NT];      // fragments of thread column g
+  const float* z[NT][2];     // zero-point terms of token columns 2c, 2c + 1
+};
+
+// acc[m][n] += the products of the sub-box with the groups G0 .. G0 + 3 (kFull: all of them
+// exist).
+template <int NT, int MT, bool kFull>
+__device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t (&off)[4], int G0, int groups,
+                                            const MoeUnit<NT, MT>& un, int nt, float (&acc)[MT][NT][4]) {
+  __half2 s0[MT][2], s1[MT][2];   // (the plane rows hold an even number of scales)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a[i] = bf16x2_sub136(((w.x >> (4 * i)) & 0x000F000Fu) | 0x43004300u);
-    a[4 + i] = bf16x2_sub136(((w.y >> (4 * i)) & 0x000F000Fu) | 0x43004300u);
-  }
-}
-
-// 8 consecutive bf16 values as the four pairs of decode_pairs_bf16.
-__device__ __forceinline__ void pair_up(uint4 v, uint32_t* b) {
-  b[0] = __byte_perm(v.x, v.z, 0x5410);
-  b[1] = __byte_perm(v.x, v.z, 0x7632);
-  b[2] = __byte_perm(v.y, v.w, 0x5410);
-  b[3] = __byte_perm(v.y, v.w, 0x7632);
-}
-
-__device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-
-// acc[n] += the products of one sub-box (256 K values from k0) of one unit with the token
-// columns of its tiles.  brow[n]: this thread's column of tile n (NULL: an empty column);
-// with kSplit, blow[n] holds the low terms.
-template <int NT, bool kSplit>
-__device__ __forceinline__ void moe_sub_box(uint32_t slot, int g, int c, int64_t k0, int64_t K, const float (&sa)[4],
-                                            const float (&sb)[4], const uint16_t* const (&brow)[NT],
-                                            const uint16_t* const (&blow)[NT], int nt, float (&acc)[NT][4]) {
-  const int r = (2 * g & 7) + (g >> 2);
-  const uint32_t row0 = slot + (uint32_t)r * 128u, row1 = row0 + kBoxBytes;
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (kFull || G0 + 2 * i < groups) {
+        s0[m][i] = *reinterpret_cast<const __half2*>(un.s0[m] + G0 + 2 * i);
+        s1[m][i] = *reinterpret_cast<const __half2*>(un.s1[m] + G0 + 2 * i);
+      }
+    }
+  float4 z[NT][2];   // the four groups' terms (the rows are padded to a multiple of four)
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) z[n][j] = *reinterpret_cast<const float4*>(un.z[n][j] + G0);
 #pragma unroll
   for (int gl = 0; gl < 4; ++gl) {
-    const int64_t kg = k0 + 64 * gl;
-    if (kg >= K) break;
-    const uint32_t off = ((((uint32_t)(2 * gl + (c >> 1))) ^ (uint32_t)r) << 4) | (uint32_t)((c & 1) << 3);
-    uint32_t a0[8], a1[8];
-    decode_pairs_bf16(lds_v2(row0 + off), a0);
-    decode_pairs_bf16(lds_v2(row1 + off), a1);
-    const int64_t kt = kg + 16 * c;   // this thread's 16 values; K is a multiple of 8
+    const int G = G0 + gl;
+    if (!kFull && G >= groups) break;
+    uint32_t a0[MT][8], a1[MT][8];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      decode_pairs(*reinterpret_cast<const uint2*>(slot + off[gl] + 1024 * m), a0[m]);
+      decode_pairs(*reinterpret_cast<const uint2*>(slot + off[gl] + 1024 * (MT + m)), a1[m]);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (NT > 1 && n >= nt) break;
-      const bool v0 = brow[n] != nullptr && kt < K, v1 = brow[n] != nullptr && kt + 8 < K;
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      uint32_t b[8];
-      pair_up(v0 ? ld_global_u4(brow[n] + kt) : zero, b);
-      pair_up(v1 ? ld_global_u4(brow[n] + kt + 8) : zero, b + 4);
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint8_t* at = un.b[n] + (size_t)G * 128;
+      const uint4 b0 = *reinterpret_cast<const uint4*>(at), b1 = *reinterpret_cast<const uint4*>(at + 64);
+      const float za = gl == 0 ? z[n][0].x : gl == 1 ? z[n][0].y : gl == 2 ? z[n][0].z : z[n][0].w;
+      const float zb = gl == 0 ? z[n][1].x : gl == 1 ? z[n][1].y : gl == 2 ? z[n][1].z : z[n][1].w;
+      const float zz[4] = {za, zb, za, zb};
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) mma_bf16(d, a0[i], a1[i], a0[i + 1], a1[i + 1], b[i], b[i + 1]);
-      if constexpr (kSplit) {
-        pair_up(v0 ? ld_global_u4(blow[n] + kt) : zero, b);
-        pair_up(v1 ? ld_global_u4(blow[n] + kt + 8) : zero, b + 4);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) mma_bf16(d, a0[i], a1[i], a0[i + 1], a1[i + 1], b[i], b[i + 1]);
+      for (int m = 0; m < MT; ++m) {
+        float d[4];
+        mma_f16_16816(d, a0[m][0], a1[m][0], a0[m][1], a1[m][1], b0.x, b0.y, zz);
+        mma_f16_16816(d, a0[m][2], a1[m][2], a0[m][3], a1[m][3], b0.z, b0.w, d);
+        mma_f16_16816(d, a0[m][4], a1[m][4], a0[m][5], a1[m][5], b1.x, b1.y, d);
+        mma_f16_16816(d, a0[m][6], a1[m][6], a0[m][7], a1[m][7], b1.z, b1.w, d);
+        const float sa = (gl & 1) ? __high2float(s0[m][gl >> 1]) : __low2float(s0[m][gl >> 1]);
+        const float sb = (gl & 1) ? __high2float(s1[m][gl >> 1]) : __low2float(s1[m][gl >> 1]);
+        acc[m][n][0] = fmaf(sa, d[0], acc[m][n][0]);
+        acc[m][n][1] = fmaf(sa, d[1], acc[m][n][1]);
+        acc[m][n][2] = fmaf(sb, d[2], acc[m][n][2]);
+        acc[m][n][3] = fmaf(sb, d[3], acc[m][n][3]);
       }
-      acc[n][0] = fmaf(sa[gl], d[0], acc[n][0]);
-      acc[n][1] = fmaf(sa[gl], d[1], acc[n][1]);
-      acc[n][2] = fmaf(sb[gl], d[2], acc[n][2]);
-      acc[n][3] = fmaf(sb[gl], d[3], acc[n][3]);
     }
   }
 }
 
-// The four group scales of a row from group G on (the plane rows hold an even number of
-// scales, so pairs are 4-byte aligned; groups past the row read as zero).
-__device__ __forceinline__ void load_scales(const uint16_t* row, int G, int groups, uint32_t (&w)[2]) {
-  w[0] = G < groups ? ld_global_u32(row + G) : 0u;
-  w[1] = G + 2 < groups ? ld_global_u32(row + G + 2) : 0u;
+// Shared-memory layout: rings (1024-byte aligned), barriers, lists, then the latency form's
+// exchange buffer -- gate/up, the accumulators of the K parts (one 16-byte word per thread,
+// two rounds); down, the slots' sums of every K part -- and, down, h of every slot.
+__host__ inline uint32_t moe_layout(MoeParams& p, int per, int mt, bool down, bool lat) {
+  p.bar_off = (uint32_t)(kMoeWarps * p.depth * slot_bytes(mt));
+  p.cnt_off = p.bar_off + (uint32_t)(kMoeWarps * p.depth * 8);
+  p.wcnt_off = p.cnt_off + (p.slots <= 32 ? 0u : (uint32_t)p.E * 4);
+  p.tiles_off = (p.wcnt_off + (p.slots <= 32 ? 0u : (uint32_t)(kMoeWarps * p.E + 4)) + 7) / 8 * 8;
+  p.order_off = p.tiles_off + (uint32_t)moe_max_tiles(p.slots, p.E, per) * 8;
+  p.misc_off = p.order_off + (uint32_t)p.slots * 4;
+  p.sum_off = (p.misc_off + 16 + 15) / 16 * 16;
+  p.frag_off = p.sum_off + (lat ? (down ? (uint32_t)(kMaxParts * p.slots * 64) : (uint32_t)(2 * kMoeThreads * 16)) : 0u);
+  p.frag_pitch = 0;
+  if (!(lat && down)) return p.frag_off;
+  // h of every slot: fragments (64 bytes of padding put two columns' 64-byte reads on
+  // different banks), zero-point terms, and one power of two
+  p.frag_pitch = (uint32_t)(moe_groups(p.F) * 128 + 64);
+  return p.frag_off + (uint32_t)p.slots * (p.frag_pitch + (uint32_t)moe_zs_pitch(p.F) * 4 + 4);
 }
 
-__device__ __forceinline__ void scales_f32(const uint32_t (&w)[2], float (&s)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    s[2 * i] = fp16_bits_to_float((uint16_t)(w[i] & 0xFFFFu));
-    s[2 * i + 1] = fp16_bits_to_float((uint16_t)(w[i] >> 16));
-  }
-}
-
-// Shared-memory layout: rings (1024-byte aligned), barriers, lists, then (down) the slot sums.
-struct MoeLayout {
-  uint32_t bar_off, cnt_off, order_off, tiles_off, misc_off, sum_off, total;
-};
-
-__host__ __device__ inline MoeLayout moe_layout(int depth, int E, int slots, int per, bool down) {
-  MoeLayout L;
-  L.bar_off = (uint32_t)(kMoeWarps * depth * kSlotBytes);
-  L.cnt_off = L.bar_off + (uint32_t)(kMoeWarps * depth * 8);
-  L.tiles_off = (L.cnt_off + (uint32_t)E * 4 + 7) / 8 * 8;
-  L.order_off = L.tiles_off + (uint32_t)moe_max_tiles(slots, E, per) * 8;
-  L.misc_off = L.order_off + (uint32_t)slots * 4;
-  L.sum_off = (L.misc_off + 8 + 15) / 16 * 16;
-  L.total = L.sum_off + (down ? (uint32_t)slots * 64 : 0u);
-  return L;
-}
-
-// kDown false: gate/up units, h written; true: down units, y written.
-template <int NT, bool kDown>
-__global__ void __launch_bounds__(kMoeThreads, 2)
+// kDown false: gate/up units, h written; true: down units, y (latency) or part written.
+template <int NT, int MT, bool kDown, bool kLat>
+__global__ void __launch_bounds__(kMoeThreads, 1)
 q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  constexpr int kPer = 8 * NT;
-  const MoeLayout S = moe_layout(p.depth, p.E, p.slots, kPer, kDown);
+  constexpr int kPer = 8 * NT, kRows = 8 * MT;
+  constexpr uint32_t kSlot = slot_bytes(MT);
   MoeLists L;
-  L.cnt = reinterpret_cast<int*>(smem + S.cnt_off);
-  L.order = reinterpret_cast<int*>(smem + S.order_off);
-  L.tiles = reinterpret_cast<int2*>(smem + S.tiles_off);
-  L.ntiles = reinterpret_cast<int*>(smem + S.misc_off);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S.misc_off + 4);
+  L.cnt = reinterpret_cast<int*>(smem + p.cnt_off);
+  L.wcnt = smem + p.wcnt_off;
+  L.order = reinterpret_cast<int*>(smem + p.order_off);
+  L.tiles = reinterpret_cast<int2*>(smem + p.tiles_off);
+  L.ntiles = reinterpret_cast<int*>(smem + p.misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.misc_off + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMoeWarps * p.depth; ++i) mbar_init(sbase + S.bar_off + 8u * (uint32_t)i, 1);
+    for (int i = 0; i < kMoeWarps * p.depth; ++i) mbar_init(sbase + p.bar_off + 8u * (uint32_t)i, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm);
@@ -404,176 +613,355 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   moe_build_lists(p, L, kPer);
   const int ntiles = *L.ntiles;
 
-  const int64_t K = kDown ? p.F : p.H;
-  const int nsb = (int)((K + 255) / 256);
-  const int groups = (int)((K + 63) / 64), grow = (int)(((K + 127) / 128 * 128) / 64);
+  const int K = (int)(kDown ? p.F : p.H);
+  const int nsb = (K + 255) / 256;
+  const int groups = (K + 63) / 64, grow = (K + 127) / 128 * 2;
   const int64_t rows_e = kDown ? p.H : 2 * p.F;                        // weight rows per expert
-  const int nu = (int)(kDown ? (p.H + 15) / 16 : p.F / 8);              // units per expert
+  const int64_t last_row = (int64_t)p.E * rows_e - 1;
+  const int nu = (int)(kDown ? (p.H + 2 * kRows - 1) / (2 * kRows) : (p.F + kRows - 1) / kRows);   // units per expert
   const uint16_t* scales = kDown ? p.s_dn : p.s_gu;
-  // Units of this CTA.  Gate/up: (tile, unit) pairs in tile order, a contiguous range per CTA
-  // (its warps then share one expert's tokens), dealt to the warps in turn.  Down: every
-  // gridDim-th unit with all tiles, the tiles dealt to the warps.  (The host bounds
-  // nu * tiles below 2^31.)
-  int u0, u1;
-  if constexpr (!kDown) {
-    const int64_t all = (int64_t)nu * ntiles;
-    u0 = (int)((int64_t)blockIdx.x * all / gridDim.x);
-    u1 = (int)((int64_t)(blockIdx.x + 1) * all / gridDim.x);
-  } else {
-    u0 = (int)blockIdx.x;
-    u1 = nu;
+  // Work.  Latency form, down: whole units [u0, u1), all tiles of each.  Otherwise a range
+  // [u0, u1) of the numbers tile * nu + unit, so that a CTA's warps share an expert's tokens
+  // (the host bounds nu * tiles below 2^31).  kp warps share the K range of an item.
+  constexpr bool kOwn = kDown && kLat;
+  const int64_t all = kOwn ? nu : (int64_t)nu * ntiles;
+  const int u0 = (int)((int64_t)blockIdx.x * all / gridDim.x), u1 = (int)((int64_t)(blockIdx.x + 1) * all / gridDim.x);
+  int kp = 1;
+  if constexpr (kLat) {   // the same for every CTA (down: for every unit)
+    const int items = kOwn ? ntiles : (int)((all + gridDim.x - 1) / gridDim.x);
+    kp = items > 0 ? kMoeWarps / items : 1;
+    kp = kp < 1 ? 1 : kp > kMaxParts ? kMaxParts : kp;
+    if (kp > nsb) kp = nsb;
   }
-  // this warp's items: unit u0 + warp, + 8, ... (gate/up); per unit, tiles warp, warp + 8, ... (down)
-  const int per_unit = ntiles > warp ? (ntiles - warp + kMoeWarps - 1) / kMoeWarps : 0;
-  auto row_base = [&](int tile, int unit, int64_t& row0, int64_t& row1) {
-    row0 = (int64_t)L.tiles[tile].x * rows_e + (kDown ? 16 : 8) * (int64_t)unit;
-    row1 = row0 + (kDown ? 8 : p.F);
+  const int wpr = kMoeWarps / kp;                    // items per round of the warps
+  const int wnum = warp / kp, kpart = warp - wnum * kp;
+  const int sb0 = nsb * kpart / kp, sb1 = nsb * (kpart + 1) / kp;
+  // The items of this warp, in order: a position that steps without divisions.
+  struct Pos {
+    int tile, unit, left;   // left: numbers to the end of the range (kOwn: units to its end)
   };
-  const uint32_t ring0 = sbase + (uint32_t)(warp * p.depth * kSlotBytes);
-  const uint32_t bars = sbase + S.bar_off + (uint32_t)(warp * p.depth * 8);
-  // ---- issue side (lane 0): the warp's items once more, sub-box by sub-box, `depth` ahead
-  int is_unit = kDown ? u0 : 0, is_tile = kDown ? warp : 0, is_flat = u0 + warp, is_sb = 0, is_slot = 0;
-  int64_t is_row0 = 0, is_row1 = 0;
-  int64_t issued = 0;
-  bool more = kDown ? (u0 < nu && per_unit > 0) : is_flat < u1;
-  auto issue = [&]() {
-    if (is_sb == 0) {
-      if constexpr (!kDown) {
-        is_tile = is_flat / nu;
-        is_unit = is_flat - is_tile * nu;
+  auto start = [&]() -> Pos {
+    if constexpr (kOwn) return {wnum, u0, wnum < ntiles && wnum < wpr ? u1 - u0 : 0};
+    const int u = u0 + wnum;
+    const int tile = nu > 0 ? u / nu : 0;
+    return {tile, u - tile * nu, wnum < wpr ? u1 - u : 0};
+  };
+  auto step = [&](Pos& q) {
+    if constexpr (kOwn) {
+      q.tile += wpr;
+      if (q.tile >= ntiles) {
+        q.tile = wnum;
+        ++q.unit;
+        --q.left;
       }
-      row_base(is_tile, is_unit, is_row0, is_row1);
+    } else {
+      q.left -= wpr;
+      q.unit += wpr;
+      while (q.unit >= nu) {
+        q.unit -= nu;
+        ++q.tile;
+      }
     }
-    const uint32_t bar = bars + 8u * (uint32_t)is_slot, dst = ring0 + (uint32_t)is_slot * kSlotBytes;
-    mbar_expect_tx(bar, kSlotBytes);
-    tma_load_2d(dst, &tm, bar, is_sb * 128, (int32_t)is_row0);
-    tma_load_2d(dst + kBoxBytes, &tm, bar, is_sb * 128, (int32_t)is_row1);
+  };
+  uint8_t* ring = smem + (size_t)(warp * p.depth) * kSlot;
+  const uint32_t bars = sbase + p.bar_off + (uint32_t)(warp * p.depth * 8);
+  // ---- issue side (lane 0): the warp's items once more, sub-box by sub-box, `depth` ahead
+  Pos is = start();
+  int is_sb = sb0, is_slot = 0, is_row = 0, is_exp = 0;
+  int64_t issued = 0;
+  auto issue = [&]() {
+    if (is_sb == sb0) {
+      is_exp = L.tiles[is.tile].x;
+      is_row = (kDown ? 2 * kRows : kRows) * is.unit;
+    }
+    const uint32_t bar = bars + 8u * (uint32_t)is_slot;
+    mbar_expect_tx(bar, kSlot);
+    tma_load_4d(smem_u32(ring) + (uint32_t)is_slot * kSlot, &tm, bar, is_sb * 128, is_row, 0, is_exp);   // rows past the expert's: zeros
     ++issued;
     if (++is_slot == p.depth) is_slot = 0;
-    if (++is_sb == nsb) {
-      is_sb = 0;
-      if constexpr (!kDown) {
-        is_flat += kMoeWarps;
-        more = is_flat < u1;
-      } else {
-        is_tile += kMoeWarps;
-        if (is_tile >= ntiles) {
-          is_tile = warp;
-          is_unit += (int)gridDim.x;
-          more = is_unit < nu;
-        }
-      }
+    if (++is_sb == sb1) {
+      is_sb = sb0;
+      step(is);
     }
   };
   if (lane == 0)
-    for (int d = 0; d < p.depth && more; ++d) issue();
+    for (int d = 0; d < p.depth && is.left > 0; ++d) issue();
+  // scale lines of a unit's rows: one row per lane
+  const int nl = (sb1 - sb0) * 8 / 128 + 1;   // 128-byte lines past the first, at most
+  auto scale_row = [&](const Pos& q) -> const uint8_t* {
+    const int64_t base = (int64_t)L.tiles[q.tile].x * rows_e + (int64_t)q.unit * (kDown ? 2 * kRows : kRows);
+    int64_t row = base + (kDown || lane < kRows ? lane : p.F + lane - kRows);
+    row = row < last_row ? row : last_row;
+    return reinterpret_cast<const uint8_t*>(scales + row * grow + 4 * sb0);
+  };
+  auto for_scale_lines = [&](const Pos& q, auto&& f) {
+    if (lane < 2 * kRows) {
+      const uint8_t* a = scale_row(q);
+      const int most = (grow - 4 * sb0) * 2 - 4;
+      for (int i = 0; i <= nl; ++i) f(a + (128 * i < most ? 128 * i : most));
+    }
+  };
+  const Pos first_item = start();
+  if (first_item.left > 0) for_scale_lines(first_item, [&](const uint8_t* a) { prefetch_l2(a); });
+  // The B columns: x of a token (gate/up) or h of a slot (down), fragments, terms and powers.
+  const uint8_t* frag = kDown ? p.hf : p.xf;
+  const float* zero = kDown ? p.hz : p.zs;
+  const float* power = kDown ? p.hft : p.ft;
+  const int64_t fpitch = kOwn ? (int64_t)p.frag_pitch : (int64_t)groups * 128, zpitch = moe_zs_pitch(K);
   if constexpr (kDown) pdl_wait_previous();
+  if constexpr (kOwn) {   // a warp per slot (at most kLatSlots) converts h
+    float* zsm = reinterpret_cast<float*>(smem + p.frag_off + p.slots * p.frag_pitch);
+    float* fsm = zsm + p.slots * zpitch;
+    if (warp < p.slots)
+      moe_prep_slot(p.h + (int64_t)warp * K, K, smem + p.frag_off + warp * p.frag_pitch, zsm + warp * zpitch, fsm + warp);
+    frag = smem + p.frag_off;
+    zero = zsm;
+    power = fsm;
+    __syncthreads();
+  }
 
   bool ok = true;
   int slot = 0;
   uint32_t phase = 0;
-  float* sums = reinterpret_cast<float*>(smem + S.sum_off);   // down: [slots][16]
-  // down: one round per unit; gate/up: a single round over the CTA's range
-  for (int round = kDown ? u0 : 0; round < (kDown ? nu : 1); round += kDown ? (int)gridDim.x : 1) {
-    const int i_end = kDown ? ntiles : u1;
-    for (int i = kDown ? warp : u0 + warp; i < i_end; i += kMoeWarps) {
-      const int tile = kDown ? i : i / nu, unit = kDown ? round : i - tile * nu;
-      const int2 tl = L.tiles[tile];
-      const int first = tl.y & 0xFFFF, count = tl.y >> 16;
-      const int nt = (count + 7) / 8;
-      const int r = (2 * g & 7) + (g >> 2);
-      int64_t row0, row1;
-      row_base(tile, unit, row0, row1);
-      if (kDown && 16 * (int64_t)unit + 8 >= p.H) row1 = row0;   // no second box: its results are dropped
-      row0 += r;
-      row1 += r;
-      const uint16_t* srow0 = scales + row0 * grow;
-      const uint16_t* srow1 = scales + row1 * grow;
-      const uint16_t* brow[NT];
-      const uint16_t* blow[NT];
+  float* sums = reinterpret_cast<float*>(smem + p.sum_off);
+  const int r = (2 * g & 7) + (g >> 2);
+  uint32_t off[4];   // this thread's code bytes of the sub-box's four groups, in the swizzled box
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int s = 8 * n + g < count ? L.order[first + 8 * n + g] : -1;
-        brow[n] = blow[n] = nullptr;
-        if (s >= 0) {
-          brow[n] = kDown ? p.h_hi + (int64_t)s * p.F : p.x + (int64_t)(s / p.k) * p.H;
-          if (kDown) blow[n] = p.h_lo + (int64_t)s * p.F;
+  for (int gl = 0; gl < 4; ++gl)
+    off[gl] = (uint32_t)r * 128u + (((((uint32_t)(2 * gl + (c >> 1))) ^ (uint32_t)r) << 4) | (uint32_t)((c & 1) << 3));
+  int last_tile = -1;
+  // products of an item over this warp's K part; next: the item after it
+  auto compute = [&](const Pos& q, const Pos& next, float (&acc)[MT][NT][4], int& first, int& count) {
+    const int2 tl = L.tiles[q.tile];
+    first = tl.y & 0xFFFF;
+    count = tl.y >> 16;
+    const int nt = (count + 7) / 8;
+    MoeUnit<NT, MT> un;
+    const int64_t row0 = (int64_t)tl.x * rows_e + (int64_t)q.unit * (kDown ? 2 * kRows : kRows);
+    const int64_t row1 = row0 + (kDown ? (int64_t)kRows : p.F);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      // rows past the plane (a last, partly filled unit): their results are dropped
+      const int64_t q0 = row0 + 8 * m + r, q1 = row1 + 8 * m + r;
+      un.s0[m] = scales + (q0 < last_row ? q0 : last_row) * grow;
+      un.s1[m] = scales + (q1 < last_row ? q1 : last_row) * grow;
+    }
+    // empty columns take the tile's first slot; their results are dropped
+    auto column = [&](int i) {   // slot (down) or token of column i
+      const int o = L.order[first + (i < count ? i : 0)];
+      return kDown ? o & 0xFFFF : o >> 16;
+    };
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      un.b[n] = frag + column(8 * n + g) * fpitch + 16 * c;
+      un.z[n][0] = zero + column(8 * n + 2 * c) * zpitch;
+      un.z[n][1] = zero + column(8 * n + 2 * c + 1) * zpitch;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+    // One touch of every line that the loops below read beside the ring -- the scales of the
+    // unit's rows and, of a new tile, the columns' K range -- all in flight together: they are
+    // then found in L1 (a warp would otherwise wait for L2 or memory at every group).  The next
+    // unit's scales start on their way to L2.
+    {
+      uint32_t touch = 0;
+      for_scale_lines(q, [&](const uint8_t* a) { touch |= ld_global_u32(a); });
+      if (!kOwn && q.tile != last_tile) {
+        const int cols = count < kPer ? count : kPer;
+        for (int i = 0; i < cols; ++i) {
+          const uint8_t* a = frag + column(i) * fpitch;
+          for (int G = 4 * sb0 + lane; G < 4 * sb1 && G < groups; G += 32) touch |= ld_global_u32(a + (int64_t)G * 128);
         }
       }
-      float acc[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-      uint32_t w0[2], w1[2];
-      load_scales(srow0, 0, groups, w0);
-      load_scales(srow1, 0, groups, w1);
-      for (int sb = 0; sb < nsb; ++sb) {
-        float sa[4], sc[4];
-        scales_f32(w0, sa);
-        scales_f32(w1, sc);
-        if (sb + 1 < nsb) {   // the next sub-box's scales
-          load_scales(srow0, 4 * (sb + 1), groups, w0);
-          load_scales(srow1, 4 * (sb + 1), groups, w1);
+      last_tile = q.tile;
+      asm volatile("" ::"r"(touch));
+      if (next.left > 0) for_scale_lines(next, [&](const uint8_t* a) { prefetch_l2(a); });
+    }
+    for (int sb = sb0; sb < sb1; ++sb) {
+      // every lane polls: one instruction for the warp, and no exchange of the answer
+      if (ok && !mbar_try_wait(bars + 8u * (uint32_t)slot, phase))
+        ok = warp_wait(bars + 8u * (uint32_t)slot, phase, abort_flag, &g_moe_status);
+      if (ok) {
+        if (4 * (sb + 1) <= groups)
+          moe_sub_box<NT, MT, true>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
+        else
+          moe_sub_box<NT, MT, false>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
+        __syncwarp();
+        if (lane == 0 && is.left > 0) issue();   // refill the slot just read
+        if (++slot == p.depth) {
+          slot = 0;
+          phase ^= 1;
         }
-        ok = ok && warp_wait(bars + 8u * (uint32_t)slot, phase, abort_flag, &g_moe_status);
-        if (ok) {
-          moe_sub_box<NT, kDown>(ring0 + (uint32_t)slot * kSlotBytes, g, c, 256 * (int64_t)sb, K, sa, sc, brow, blow, nt, acc);
-          __syncwarp();
-          if (lane == 0 && more) issue();   // refill the slot just read
-          if (++slot == p.depth) {
-            slot = 0;
-            phase ^= 1;
+      }
+    }
+  };
+
+  Pos pos = start();
+  if constexpr (!kDown) {
+    int parity = 0;
+    // with K parts, all warps pass the same rounds (they meet to join their sums)
+    for (int base = u0; base < u1; base += wpr) {
+      const bool have = pos.left > 0;
+      if (kp == 1 && !have) break;
+      const Pos q = pos;
+      if (have) step(pos);
+      float acc[MT][NT][4];
+      int first = 0, count = 0;
+      if (have) compute(q, pos, acc, first, count);
+      if constexpr (kLat) {
+        if (kp > 1) {   // part 0 adds the others' accumulators, in order
+          float4* ex = reinterpret_cast<float4*>(sums) + parity * kMoeThreads;
+          parity ^= 1;
+          if (have && kpart > 0) ex[threadIdx.x] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][0][2], acc[0][0][3]);
+          __syncthreads();
+          if (!have || kpart > 0) continue;
+          for (int i = 1; i < kp; ++i) {
+            const float4 v = ex[threadIdx.x + 32 * i];
+            acc[0][0][0] += v.x;
+            acc[0][0][1] += v.y;
+            acc[0][0][2] += v.z;
+            acc[0][0][3] += v.w;
           }
         }
       }
       if (!ok) continue;
-      // ---- the unit's results: thread (g, c) holds MMA rows g, g + 8 of token columns 2c, 2c + 1
+      // thread (g, c) holds gate and up of row f of token columns 2c, 2c + 1
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (NT > 1 && n >= nt) break;
+        if (NT > 1 && 8 * n >= count) break;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int col = 8 * n + 2 * c + j;
           if (col >= count) continue;
-          const int s = L.order[first + col];
-          if constexpr (kDown) {
-            sums[s * 16 + r] = acc[n][j];
-            sums[s * 16 + 8 + r] = acc[n][2 + j];
-          } else {
-            const float gt = acc[n][j], up = acc[n][2 + j];
+          const int o = L.order[first + col];
+          const float F = power[o >> 16];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const int64_t f = kRows * (int64_t)q.unit + 8 * m;
+            if (f >= p.F) continue;
+            const float gt = F * acc[m][n][j], up = F * acc[m][n][2 + j];
             const float h = gt / (1.f + expf(-gt)) * up;
-            const uint16_t hi = float_to_bf16_bits(h);
-            const float rest = h - __uint_as_float((uint32_t)hi << 16);
-            const int64_t o = (int64_t)s * p.F + 8 * (int64_t)unit + r;
-            p.h_hi[o] = hi;
-            // an infinite or NaN h has no low term
-            p.h_lo[o] = fabsf(h) < INFINITY ? float_to_bf16_bits(rest) : (uint16_t)0;
+            p.h[(int64_t)(o & 0xFFFF) * p.F + f + r] = h;
           }
         }
       }
     }
-    if constexpr (kDown) {
-      __syncthreads();
-      const int64_t n0 = 16 * (int64_t)round;
-      const int tokens = p.slots / p.k;
-      if (!*abort_flag) {
-        for (int e = threadIdx.x; e < tokens * 16; e += kMoeThreads) {
-          const int t = e >> 4, rr = e & 15;
-          if (n0 + rr >= p.H) continue;
-          float v = 0.f;
-          for (int j = 0; j < p.k; ++j) {   // in the order of the choices
-            const int s = t * p.k + j;
-            const int id = (int)ld_global_u32(p.ids + s);
-            if (id >= 0 && id < p.E) v = fmaf(__uint_as_float(ld_global_u32(p.weights + s)), sums[s * 16 + rr], v);
+  } else {
+    auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (NT > 1 && 8 * n >= count) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = 8 * n + 2 * c + j;
+          if (col >= count) continue;
+          const int s = L.order[first + col] & 0xFFFF;
+          const float F = power[s];
+          if constexpr (kLat) {
+            sums[(kpart * p.slots + s) * 16 + r] = F * acc[0][n][j];
+            sums[(kpart * p.slots + s) * 16 + 8 + r] = F * acc[0][n][2 + j];
+          } else {
+            const int64_t n0 = 2 * kRows * (int64_t)unit;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const int64_t ra = n0 + 8 * m + r, rb = ra + kRows;
+              if (ra < p.H) p.part[(int64_t)s * p.H + ra] = F * acc[m][n][j];
+              if (rb < p.H) p.part[(int64_t)s * p.H + rb] = F * acc[m][n][2 + j];
+            }
           }
-          p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
         }
       }
-      __syncthreads();   // the sums are free again
+    };
+    if constexpr (!kLat) {
+      while (pos.left > 0) {
+        const Pos q = pos;
+        step(pos);
+        float acc[MT][NT][4];
+        int first, count;
+        compute(q, pos, acc, first, count);
+        if (ok) store(acc, first, count, q.unit);
+      }
+    } else {
+      const int tokens = p.slots / p.k;
+      for (int unit = u0; unit < u1; ++unit) {   // (without any tile: y = +0)
+        while (pos.left > 0 && pos.unit == unit) {
+          const Pos q = pos;
+          step(pos);
+          float acc[MT][NT][4];
+          int first, count;
+          compute(q, pos, acc, first, count);
+          if (ok) store(acc, first, count, unit);
+        }
+        __syncthreads();
+        if (!*abort_flag) {   // y of the unit's rows: the slots' sums in the order of the choices
+          const int64_t n0 = 16 * (int64_t)unit;
+          for (int e = threadIdx.x; e < tokens * 16; e += kMoeThreads) {
+            const int t = e >> 4, rr = e & 15;
+            if (n0 + rr >= p.H) continue;
+            float v = 0.f;
+            for (int j = 0; j < p.k; ++j) {
+              const int s = t * p.k + j;
+              const int id = p.ids[s];
+              const float w = p.weights[s];
+              if (id < 0 || id >= p.E) continue;
+              float part = 0.f;
+              for (int i = 0; i < kp; ++i) part += sums[(i * p.slots + s) * 16 + rr];
+              v = fmaf(w, part, v);
+            }
+            p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
+          }
+        }
+        __syncthreads();   // the sums are free again
+      }
     }
   }
   if (!ok && lane == 0)   // aborted: let the copies already issued land before the CTA exits
     for (int64_t d = issued > p.depth ? issued - p.depth : 0; d < issued; ++d)
       mbar_drain(bars + 8u * (uint32_t)(d % p.depth), (uint32_t)((d / p.depth) & 1));
+}
+
+// Throughput form, between the products: a warp per slot converts h.
+__global__ void __launch_bounds__(256) q4_moe_convert_kernel(const MoeParams p) {
+  pdl_launch_dependents();
+  pdl_wait_previous();
+  const int s = (int)(blockIdx.x * 8 + (threadIdx.x >> 5));
+  if (s >= p.slots) return;
+  const int id = (int)ld_global_u32(p.ids + s);
+  if (id < 0 || id >= p.E) return;   // (its h was not written)
+  moe_prep_slot(p.h + (int64_t)s * p.F, (int)p.F, p.hf + s * moe_groups(p.F) * 128, p.hz + s * moe_zs_pitch(p.F), p.hft + s);
+}
+
+// Throughput form, after the down product: y[t, n] = sum_j p[t, j] part[t k + j, n] in the order
+// of the choices; four columns per thread (H is a multiple of 8).
+constexpr int kReduceThreads = 256;
+
+__global__ void __launch_bounds__(kReduceThreads) q4_moe_reduce_kernel(const MoeParams p) {
+  pdl_launch_dependents();
+  pdl_wait_previous();
+  const int q = (int)(p.H / 4);
+  const int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x;
+  const int64_t t = i / q;
+  if (t >= p.slots / p.k) return;
+  const int64_t n = 4 * (i - t * q);
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int j = 0; j < p.k; ++j) {
+    const int64_t s = t * p.k + j;
+    const int id = (int)ld_global_u32(p.ids + s);
+    if (id < 0 || id >= p.E) continue;   // (its part was not written)
+    const float w = __uint_as_float(ld_global_u32(p.weights + s));
+    const float4 f = ld_global_f4(p.part + s * p.H + n);
+    v[0] = fmaf(w, f.x, v[0]);
+    v[1] = fmaf(w, f.y, v[1]);
+    v[2] = fmaf(w, f.z, v[2]);
+    v[3] = fmaf(w, f.w, v[3]);
+  }
+  uint2 o;
+  o.x = (uint32_t)float_to_bf16_bits(v[0]) | ((uint32_t)float_to_bf16_bits(v[1]) << 16);
+  o.y = (uint32_t)float_to_bf16_bits(v[2]) | ((uint32_t)float_to_bf16_bits(v[3]) << 16);
+  *reinterpret_cast<uint2*>(p.y + t * p.H + n) = o;
 }
 
 int moe_sm_count() {
@@ -587,45 +975,99 @@ int moe_sm_count() {
   return n;
 }
 
-constexpr int kMoeSmem = 112 * 1024;   // dynamic shared memory at most (two CTAs per SM)
+// Dynamic shared memory at most: what is left of the SM's 256 KB is the L1 that the B columns
+// and scales are found in.
+constexpr int kMoeSmem = 150 * 1024;
 
-template <int NT, bool kDown>
+// (the down product of the throughput form starts after the conversion kernel, whose early
+// launch lets it begin before the gate/up product is complete: it reads h and what follows from
+// it only after its wait, and everything else it reads is final by then)
+template <int NT, int MT, bool kDown, bool kLat>
 int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaStream_t stream) {
   static bool attr[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, kDown>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem),
+    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, MT, kDown, kLat>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kMoeSmem),
                    "moe: cudaFuncSetAttribute"))
       return Q4LIN_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
   }
   MoeParams p = p0;
-  p.depth = 8;
-  MoeLayout L = moe_layout(p.depth, p.E, p.slots, 8 * NT, kDown);
-  while (p.depth > 2 && L.total + 1024 > kMoeSmem) L = moe_layout(--p.depth, p.E, p.slots, 8 * NT, kDown);
-  if (L.total + 1024 > kMoeSmem) {
+  p.depth = 4;
+  uint32_t bytes = moe_layout(p, 8 * NT, MT, kDown, kLat);
+  while (p.depth > 2 && bytes + 1024 > kMoeSmem) {
+    --p.depth;
+    bytes = moe_layout(p, 8 * NT, MT, kDown, kLat);
+  }
+  if (bytes + 1024 > kMoeSmem) {
     set_error_detail("moe: the slot lists do not fit shared memory");
     return Q4LIN_ERR_UNSUPPORTED_SHAPE;
+  }
+  int grid = sms;
+  if (kDown && kLat) {   // whole units
+    const int64_t nu = (p.H + 15) / 16;
+    if (grid > nu) grid = (int)nu;
   }
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * sms), 1, 1);
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kMoeThreads, 1, 1);
-  cfg.dynamicSmemBytes = L.total + 1024;
+  cfg.dynamicSmemBytes = bytes + 1024;
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<NT, kDown>, tm, p), kDown ? "moe: down kernel launch" : "moe: gate/up kernel launch");
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<NT, MT, kDown, kLat>, tm, p),
+                    kDown ? "moe: down kernel launch" : "moe: gate/up kernel launch");
 }
 
 template <bool kDown>
-int moe_kernel_nt(int nt, const CUtensorMap& tm, const MoeParams& p, int sms, cudaStream_t stream) {
-  if (nt <= 1) return moe_kernel_launch<1, kDown>(tm, p, sms, stream);
-  if (nt <= 2) return moe_kernel_launch<2, kDown>(tm, p, sms, stream);
-  return moe_kernel_launch<kMaxNT, kDown>(tm, p, sms, stream);
+int moe_kernel_form(bool lat, int nt, const CUtensorMap& tm, const MoeParams& p, int sms, cudaStream_t stream) {
+  if (lat) return moe_kernel_launch<1, 1, kDown, true>(tm, p, sms, stream);
+  if (nt <= 1) return moe_kernel_launch<1, 2, kDown, false>(tm, p, sms, stream);
+  return moe_kernel_launch<kMaxNT, 2, kDown, false>(tm, p, sms, stream);
+}
+
+// The latency form holds every slot's h in shared memory beside the rings.
+bool moe_latency_form(int slots, int64_t F) {
+  return slots <= kLatSlots && (int64_t)slots * (moe_groups(F) * 128 + 64 + moe_zs_pitch(F) * 4 + 4) <= 48 * 1024;
+}
+
+// Workspace parts of one pass, each 256-byte aligned.
+struct MoeWs {
+  size_t xf, zs, ft, h, hf, hz, hft, part, total;
+};
+
+MoeWs moe_ws(int tokens, int64_t H, int64_t F, int k) {
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  const size_t S = (size_t)tokens * (size_t)k;
+  const bool lat = moe_latency_form((int)S, F);
+  MoeWs w;
+  w.xf = 0;
+  w.zs = w.xf + up((size_t)tokens * (size_t)moe_groups(H) * 128);
+  w.ft = w.zs + up((size_t)tokens * (size_t)moe_zs_pitch(H) * 4);
+  w.h = w.ft + up((size_t)tokens * 4);
+  w.hf = w.h + up(S * (size_t)F * 4);
+  w.hz = w.hf + (lat ? 0 : up(S * (size_t)moe_groups(F) * 128));
+  w.hft = w.hz + (lat ? 0 : up(S * (size_t)moe_zs_pitch(F) * 4));
+  w.part = w.hft + (lat ? 0 : up(S * 4));
+  w.total = w.part + (lat ? 0 : up(S * (size_t)H * 4));
+  return w;
+}
+
+cudaLaunchConfig_t moe_config(unsigned blocks, unsigned threads, cudaStream_t stream, cudaLaunchAttribute* at) {
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
 }
 
 }  // namespace
@@ -635,29 +1077,42 @@ int moe_pass_tokens(int64_t T, int k) {
   return (int)(T < most ? T : most);
 }
 
-size_t moe_workspace_bytes(int64_t T, int64_t F, int k) {
-  const size_t one = ((size_t)moe_pass_tokens(T, k) * (size_t)k * (size_t)F * 2 + 255) / 256 * 256;
-  return 2 * one;
-}
-
-int moe_launch_count(int64_t T, int k) {
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int k) {
   const int tp = moe_pass_tokens(T, k);
-  return 2 * (int)((T + tp - 1) / tp);
+  const size_t first = moe_ws(tp, H, F, k).total;
+  // a last, shorter pass may take the other form, whose parts are fewer
+  return first;
 }
 
 int moe_router_launch(const MoeArgs& a) {
-  RouterParams p{a.x, a.w_router, a.bias, a.ids_out, a.weights_out, a.T, a.H, (int)a.E, a.k, a.renorm};
+  RouterParams p{};
+  p.x = a.x;
+  p.w = a.w_router;
+  p.bias = a.bias;
+  p.ids = a.ids_out;
+  p.weights = a.weights_out;
+  p.T = a.T;
+  p.H = a.H;
+  p.E = (int)a.E;
+  p.k = a.k;
+  p.renorm = a.renorm;
   const int tt = a.T < kRouteTokens ? (a.T == 1 ? 1 : 2) : kRouteTokens;
   const int64_t clusters = (a.T + tt - 1) / tt;
+  p.clusters = (int)clusters;
+  p.parts = a.E >= 128 ? 1 : (int)(128 / a.E);
+  int64_t prep = 0;
+  if (a.workspace != nullptr) {   // the whole layer: the experts' first operand pass beside the router
+    const int tp = moe_pass_tokens(a.T, a.k);
+    const MoeWs w = moe_ws(tp, a.H, a.F, a.k);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.xf = ws + w.xf;
+    p.zs = reinterpret_cast<float*>(ws + w.zs);
+    p.ft = reinterpret_cast<float*>(ws + w.ft);
+    p.prep_tokens = tp;
+    prep = (tp + kRouteCluster - 1) / kRouteCluster;
+  }
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * kRouteCluster), 1, 1);
-  cfg.blockDim = dim3(kRouteThreads, 1, 1);
-  cfg.stream = a.stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const cudaLaunchConfig_t cfg = moe_config((unsigned)((clusters + prep) * kRouteCluster), kRouteThreads, a.stream, at);
   cudaError_t e;
   switch (tt) {
     case 1: e = cudaLaunchKernelEx(&cfg, q4_moe_router_kernel<1>, p); break;
@@ -667,40 +1122,74 @@ int moe_router_launch(const MoeArgs& a) {
   return cuda_check(e, "moe: router kernel launch");
 }
 
-int moe_experts_launch(const MoeArgs& a) {
+int moe_experts_launch(const MoeArgs& a, bool prepared) {
   const int64_t Hp = k_pad(a.H), Fp = k_pad(a.F);
-  CUtensorMap gu, dn;
-  if (!encode_map_2d(&gu, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_gu, (uint64_t)(Hp / 2), (uint64_t)(a.E * 2 * a.F),
-                     (uint64_t)(Hp / 2), 128, 8, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map_2d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn, (uint64_t)(Fp / 2), (uint64_t)(a.E * a.H),
-                     (uint64_t)(Fp / 2), 128, 8, CU_TENSOR_MAP_SWIZZLE_128B)) {
-    set_error_detail("moe: cuTensorMapEncodeTiled failed (or is unavailable)");
-    return Q4LIN_ERR_CUDA;
-  }
   const int sms = moe_sm_count();
   const int pass = moe_pass_tokens(a.T, a.k);
-  const size_t one = moe_workspace_bytes(a.T, a.F, a.k) / 2;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   for (int64_t t0 = 0; t0 < a.T; t0 += pass) {
     const int tp = (int)(a.T - t0 < pass ? a.T - t0 : pass);
+    const bool lat = moe_latency_form(tp * a.k, a.F);
+    const uint32_t box = lat ? 8 : 16;
+    // (code bytes, rows, gate / up, expert): one copy brings the gate rows and the up rows of a
+    // unit (down: one run of twice as many rows)
+    CUtensorMap gu, dn;
+    const uint64_t gd[4] = {(uint64_t)(Hp / 2), (uint64_t)a.F, 2, (uint64_t)a.E};
+    const uint64_t gs[3] = {(uint64_t)(Hp / 2), (uint64_t)(a.F * (Hp / 2)), (uint64_t)(2 * a.F * (Hp / 2))};
+    const uint64_t dd[4] = {(uint64_t)(Fp / 2), (uint64_t)a.H, 1, (uint64_t)a.E};
+    const uint64_t ds[3] = {(uint64_t)(Fp / 2), (uint64_t)(a.H * (Fp / 2)), (uint64_t)(a.H * (Fp / 2))};
+    const uint32_t gb[4] = {128, box, 2, 1}, db[4] = {128, 2 * box, 1, 1};
+    if (!encode_map_4d(&gu, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_gu, gd, gs, gb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_map_4d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn, dd, ds, db, CU_TENSOR_MAP_SWIZZLE_128B)) {
+      set_error_detail("moe: cuTensorMapEncodeTiled failed (or is unavailable)");
+      return Q4LIN_ERR_CUDA;
+    }
+    const MoeWs w = moe_ws(tp, a.H, a.F, a.k);
+    if (!prepared || t0 > 0) {
+      RouterParams r{};
+      r.x = a.x + t0 * a.H;
+      r.H = a.H;
+      r.xf = ws + w.xf;
+      r.zs = reinterpret_cast<float*>(ws + w.zs);
+      r.ft = reinterpret_cast<float*>(ws + w.ft);
+      cudaLaunchAttribute at[1];
+      const cudaLaunchConfig_t cfg = moe_config((unsigned)tp, 256, a.stream, at);
+      if (cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_prep_kernel, r), "moe: operand pass launch")) return Q4LIN_ERR_CUDA;
+    }
     MoeParams p{};
-    p.x = a.x + t0 * a.H;
+    p.xf = ws + w.xf;
+    p.zs = reinterpret_cast<const float*>(ws + w.zs);
+    p.ft = reinterpret_cast<const float*>(ws + w.ft);
     p.ids = a.ids + t0 * a.k;
     p.weights = a.weights + t0 * a.k;
     p.s_gu = a.s_gu;
     p.s_dn = a.s_dn;
-    p.h_hi = reinterpret_cast<uint16_t*>(ws);
-    p.h_lo = reinterpret_cast<uint16_t*>(ws + one);
+    p.h = reinterpret_cast<float*>(ws + w.h);
+    p.hf = ws + w.hf;
+    p.hz = reinterpret_cast<float*>(ws + w.hz);
+    p.hft = reinterpret_cast<float*>(ws + w.hft);
+    p.part = reinterpret_cast<float*>(ws + w.part);
     p.y = a.y + t0 * a.H;
     p.H = a.H;
     p.F = a.F;
     p.E = (int)a.E;
     p.k = a.k;
     p.slots = tp * a.k;
-    // token tiles handled together: as many as one expert can get when every token chooses it
-    const int nt = (tp + 7) / 8;
-    if (const int rc = moe_kernel_nt<false>(nt, gu, p, sms, a.stream)) return rc;
-    if (const int rc = moe_kernel_nt<true>(nt, dn, p, sms, a.stream)) return rc;
+    // token tiles handled together: two where an expert gets more than a few slots on average
+    const int nt = (int64_t)tp * a.k > 6 * a.E ? 2 : 1;
+    if (const int rc = moe_kernel_form<false>(lat, nt, gu, p, sms, a.stream)) return rc;
+    if (!lat) {
+      cudaLaunchAttribute at[1];
+      const cudaLaunchConfig_t cfg = moe_config((unsigned)((p.slots + 7) / 8), 256, a.stream, at);
+      if (cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_convert_kernel, p), "moe: conversion launch")) return Q4LIN_ERR_CUDA;
+    }
+    if (const int rc = moe_kernel_form<true>(lat, nt, dn, p, sms, a.stream)) return rc;
+    if (!lat) {
+      cudaLaunchAttribute at[1];
+      const int64_t n = (int64_t)tp * (a.H / 4);
+      const cudaLaunchConfig_t cfg = moe_config((unsigned)((n + kReduceThreads - 1) / kReduceThreads), kReduceThreads, a.stream, at);
+      if (cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_reduce_kernel, p), "moe: reduction launch")) return Q4LIN_ERR_CUDA;
+    }
   }
   return Q4LIN_OK;
 }

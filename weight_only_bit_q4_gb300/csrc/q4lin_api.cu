@@ -381,20 +381,22 @@ int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const
 }
 
 int run_router(const uint16_t* x, const uint16_t* w, const float* bias, int32_t* ids, float* weights, int64_t T, int64_t H,
-               int64_t E, int top_k, int renormalize, void* stream) {
+               int64_t E, int top_k, int renormalize, void* stream, int64_t F = 0, void* workspace = nullptr) {
   int st = validate_router(x, w, bias, ids, weights, T, H, E, top_k);
   if (st != Q4LIN_OK || T == 0) return st;
   if ((st = check_device()) != Q4LIN_OK) return st;
   q4::MoeArgs a{};
   a.x = x; a.w_router = w; a.bias = bias; a.ids_out = ids; a.weights_out = weights;
   a.T = T; a.H = H; a.E = E; a.k = top_k; a.renorm = renormalize != 0;
+  a.F = F;
+  a.workspace = workspace;
   a.stream = static_cast<cudaStream_t>(stream);
   return q4::moe_router_launch(a);
 }
 
 int run_experts(const uint16_t* x, const int32_t* ids, const float* weights, const uint8_t* wq_gu, const uint16_t* s_gu,
                 const uint8_t* wq_dn, const uint16_t* s_dn, uint16_t* y, int64_t T, int64_t H, int64_t F, int64_t E,
-                int top_k, void* workspace, void* stream) {
+                int top_k, void* workspace, void* stream, bool prepared = false) {
   int st = validate_experts(x, ids, weights, wq_gu, s_gu, wq_dn, s_dn, y, T, H, F, E, top_k);
   if (st != Q4LIN_OK || T == 0 || H == 0) return st;
   if ((st = check_workspace(q4lin_moe_workspace_bytes(T, H, F, E, top_k), workspace)) != Q4LIN_OK) return st;
@@ -407,7 +409,7 @@ int run_experts(const uint16_t* x, const int32_t* ids, const float* weights, con
   a.T = T; a.H = H; a.F = F; a.E = E; a.k = top_k;
   a.workspace = workspace;
   a.stream = s;
-  return q4::moe_experts_launch(a);
+  return q4::moe_experts_launch(a, prepared);
 }
 
 int run_qk(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* q_weight,
@@ -480,7 +482,7 @@ int q4lin_moe_router(const uint16_t* x, const uint16_t* w_router, const float* b
 size_t q4lin_moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int top_k) {
   if (T < 1 || H < 1 || F < 1 || E < 1 || E > kMaxExperts || top_k < 1 || top_k > kMaxTopK) return 0;
   if (F > kMaxDim / 2048 || H > kMaxDim / 2048 || T > (int64_t)1 << 24) return 0;
-  return q4::moe_workspace_bytes(T, F, top_k);
+  return q4::moe_workspace_bytes(T, H, F, top_k);
 }
 
 int q4lin_moe_experts(const uint16_t* x, const int32_t* ids, const float* weights, const uint8_t* wq_gate_up,
@@ -501,10 +503,11 @@ int q4lin_moe(const uint16_t* x, const uint16_t* w_router, const float* bias, co
   if (st == Q4LIN_OK)
     st = validate_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y, T, H, F, E, top_k);
   if (st == Q4LIN_OK) st = check_workspace(q4lin_moe_workspace_bytes(T, H, F, E, top_k), workspace);
-  if (st == Q4LIN_OK) st = run_router(x, w_router, bias, ids, weights, T, H, E, top_k, renormalize, stream);
+  if (st == Q4LIN_OK) st = run_router(x, w_router, bias, ids, weights, T, H, E, top_k, renormalize, stream, F,
+                                       F > 0 ? workspace : nullptr);
   if (st == Q4LIN_OK)
     st = run_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y, T, H, F, E, top_k, workspace,
-                     stream);
+                     stream, true);
   return finish(st);
 }
 
