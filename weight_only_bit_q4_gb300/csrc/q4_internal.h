@@ -42,13 +42,15 @@ struct LinearArgs {
   uint16_t* y_b = nullptr;
   int64_t n_b = 0;
   // LinearLora: the adapters (GEMV and warp-MMA routes apply them in their epilogues; on the
-  // tile route, mode 3, the accumulators start from the FP32 term delta [T, N])
+  // tile route, mode 3, the accumulators start from the FP32 term delta [T, lora_delta_pitch(N)])
   const LoraArgs* lora = nullptr;
   const float* delta = nullptr;
 };
 
 // The adapters' two products beside the projection (q4_lora.cu).
-int lora_splits(int64_t K, int64_t T);
+int lora_splits(int64_t K, int64_t T, int64_t L);
+int64_t lora_shrink_grid(const LoraArgs& lo, int64_t T);   // CTAs
+int64_t lora_delta_pitch(int64_t N);                        // floats per token row of delta
 int lora_shrink_launch(const LoraArgs& lo, const uint16_t* x, int64_t K, int64_t T, cudaStream_t stream);
 int lora_expand_launch(const LoraArgs& lo, float* delta, int64_t N, int64_t T, cudaStream_t stream);
 

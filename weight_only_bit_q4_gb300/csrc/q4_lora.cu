@@ -14,87 +14,146 @@ namespace {
 
 __global__ void __launch_bounds__(kShrinkThreads)
 q4_lora_shrink_kernel(const LoraArgs lo, const uint16_t* x, int64_t K, int64_t T) {
-  __shared__ float red[kShrinkWarps * 8 * kShrinkRanks];
+  __shared__ float red[kShrinkFloats];
+  __shared__ LoraLists L;
   // The next kernel launches after the wait: when it starts, everything before this call
   // is complete and only u is still being written.
   pdl_wait_previous();
   pdl_launch_dependents();
-  lora_shrink_tile(lo, x, K, T, blockIdx.x / lo.ks, (int)(blockIdx.x % lo.ks), red);
+  lora_shrink_block(lo, x, K, T, blockIdx.x, L, red);
 }
 
-// One CTA: 8 tokens x kExpandRows weight rows.  MMA rows are weight rows, columns tokens,
-// K the ranks; u enters as two bf16 terms u = hi + lo (relative error 2^-17), B as it is.
+// One CTA: a tile of up to 16 tokens of one adapter (MMA rows) x `rows` weight rows.  u enters
+// as two bf16 terms u = hi + lo (relative error 2^-17), B as it is.  A warp forms 32 weight
+// rows at a time as four MMA column tiles whose columns are dealt so that a thread ends with
+// 8 consecutive rows of a token: column g of tile i is weight row 8 (g / 2) + 2 i + g % 2.
 constexpr int kExpandThreads = 256;
-constexpr int kExpandRows = 1024;
+constexpr int kExpandTokens = 16;
+constexpr int kExpandPitch = kLoraMaxRank / 2 + 4;   // 32-bit words per token
 
 __global__ void __launch_bounds__(kExpandThreads)
-q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t N, int64_t T) {
-  __shared__ uint32_t uh[8 * kLoraMaxRank], ul[8 * kLoraMaxRank];   // bf16 pairs' halves, one word per value
+q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N, int64_t T, int rows) {
+  __shared__ LoraLists L;
+  __shared__ __align__(16) uint32_t uh[kExpandTokens * kExpandPitch], ul[kExpandTokens * kExpandPitch];   // bf16 pairs
+  // The shrink kernel lets this one launch after its own wait: everything but u is final, so
+  // the lists are built and the first rows of B fetched while it works.  The tile kernel
+  // launches next, under the same promise.
   pdl_launch_dependents();
-  pdl_wait_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int64_t t0 = 8 * (int64_t)blockIdx.x;
-  int rank = 0;
-  const int mine = t0 + g < T ? lora_adapter(lo, t0 + g, &rank) : -1;
-  const unsigned active = __ballot_sync(0xffffffffu, mine >= 0 && c == 0);
-  const int Rp = (lo.R + 15) / 16 * 16;
-  for (int e = threadIdx.x; e < 8 * Rp; e += kExpandThreads) {
-    const int col = e / Rp, r = e % Rp;
-    float v = 0.f;
-    if (r < lo.R && ((active >> (4 * col)) & 1u)) v = lora_u(lo, T, t0 + col, r);
-    const uint16_t hi = float_to_bf16_bits(v);
-    const float rest = v - __uint_as_float((uint32_t)hi << 16);
-    uh[col * kLoraMaxRank + r] = hi;
-    ul[col * kLoraMaxRank + r] = fabsf(v) < INFINITY ? float_to_bf16_bits(rest) : 0u;
-  }
-  __syncthreads();
-  const int64_t nb = (int64_t)blockIdx.y * kExpandRows;
-  for (int64_t n0 = nb + 16 * warp; n0 < nb + kExpandRows && n0 < N; n0 += 16 * (kExpandThreads / 32)) {
-    const int64_t ra_ = n0 + g, rb_ = n0 + g + 8;
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    unsigned todo = active;
-    while (todo) {
-      const int lead = __ffs(todo) - 1;
-      const int a = __shfl_sync(0xffffffffu, mine, lead);
-      const int ra = __shfl_sync(0xffffffffu, rank, lead);
-      todo &= ~__ballot_sync(0xffffffffu, mine == a && c == 0);
-      const uint16_t* B = lo.b + (int64_t)a * N * lo.R;
-      const bool col_in = mine == a;
-      for (int r0 = 0; r0 < ra; r0 += 16) {
-        const int r = r0 + 4 * c;      // this thread's four ranks
-        const int left = ra - r;
-        auto row = [&](int64_t n) {
-          uint2 v = make_uint2(0u, 0u);
-          if (n < N && left > 0) {
-            v = ld_global_u2(B + n * lo.R + r);   // r + 3 < R: R is a multiple of 8
-            if (left < 4) {                       // what is past the adapter's rank is not used
-              if (left < 2) v.x &= 0xFFFFu;
-              if (left < 3) v.y = 0u;
-              else v.y &= 0xFFFFu;
-            }
-          }
-          return v;
-        };
-        const uint2 p = row(ra_), q = row(rb_);
-        uint32_t h[4] = {0u, 0u, 0u, 0u}, l[4] = {0u, 0u, 0u, 0u};
-        if (col_in) {
+  const int n0 = (int)(T < kLoraChunk ? T : kLoraChunk);
+  const int tiles = lora_max_tiles(n0, kExpandTokens, lo.L);
+  const int64_t chunk = blockIdx.x / tiles;
+  const int tile = (int)(blockIdx.x - chunk * tiles);
+  const int64_t t0 = chunk * kLoraChunk;
+  lora_build_lists<true>(lo, t0, (int)(T - t0 < kLoraChunk ? T - t0 : kLoraChunk), kExpandTokens, L);
+  if (tile >= L.ntiles) return;
+  const int a = L.adapter[tile], rank = L.rank[tile], first = L.first[tile], count = L.count[tile];
+  const int64_t nb = (int64_t)blockIdx.y * rows;
+  const uint16_t* B = lo.b + (int64_t)(a == kNoAdapter ? 0 : a) * N * lo.R;
+  const int row_g = 8 * (g >> 1) + (g & 1);   // + 2 i: the weight row of column g of tile i
+  // the four B fragments of rows n0r .. n0r + 31 for the ranks from r0 on
+  auto load_b = [&](int64_t n0r, int r0, uint2 (&b)[4]) {
+    const int r = r0 + 4 * c, left = rank - r;   // this thread's four ranks
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h[i] = uh[g * kLoraMaxRank + r + i];
-            l[i] = ul[g * kLoraMaxRank + r + i];
-          }
-        }
-        lora_mma(d, p.x, q.x, p.y, q.y, h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        lora_mma(d, p.x, q.x, p.y, q.y, l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+    for (int i = 0; i < 4; ++i) {
+      b[i] = make_uint2(0u, 0u);
+      const int64_t row = n0r + row_g + 2 * i;
+      if (row < N && left > 0) b[i] = ld_global_u2(B + row * lo.R + r);   // R is a multiple of 8
+    }
+  };
+  auto trim = [&](int r0, uint2 (&b)[4]) {   // what lies past the adapter's rank is not used
+    const int left = rank - (r0 + 4 * c);
+    if (left < 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (left < 2) b[i].x &= 0xFFFFu;
+        if (left < 3) b[i].y = 0u;
+        else b[i].y &= 0xFFFFu;
       }
     }
+  };
+  auto multiply = [&](int r0, uint2 (&b)[4], float (&d)[4][4]) {
+    trim(r0, b);
+    const int at = g * kExpandPitch + (r0 + 4 * c) / 2, at8 = at + 8 * kExpandPitch;
+    const uint2 h0 = *reinterpret_cast<const uint2*>(uh + at), h8 = *reinterpret_cast<const uint2*>(uh + at8);
+    const uint2 l0 = *reinterpret_cast<const uint2*>(ul + at), l8 = *reinterpret_cast<const uint2*>(ul + at8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lora_mma(d[i], h0.x, h8.x, h0.y, h8.y, b[i].x, b[i].y);
+      lora_mma(d[i], l0.x, l8.x, l0.y, l8.y, b[i].x, b[i].y);
+    }
+  };
+  // Row steps of 32 per warp; four fragment sets in flight: four row steps of one rank step
+  // (rank <= 16), or one row step of four rank steps.
+  constexpr int kStride = 32 * (kExpandThreads / 32);
+  const bool narrow = rank <= 16;
+  const int64_t n1 = nb + 32 * warp;
+  uint2 b[4][4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (narrow ? q * kStride < rows : 16 * q < rank) load_b(narrow ? n1 + q * kStride : n1, narrow ? 0 : 16 * q, b[q]);
+  }
+  pdl_wait_previous();
+  const int words = (rank + 15) / 16 * 8;   // whole steps of 16 ranks
+  for (int e = threadIdx.x; e < kExpandTokens * words; e += kExpandThreads) {
+    const int col = e / words, w = e - col * words;
+    uint32_t h = 0u, l = 0u;
+    if (col < count) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 2 * w + j;
+        const float v = r < rank ? lora_u(lo, T, t0 + L.order[first + col], r) : 0.f;
+        const uint32_t hi = float_to_bf16_bits(v);
+        const float rest = v - __uint_as_float(hi << 16);
+        h |= hi << (16 * j);
+        l |= (fabsf(v) < INFINITY ? (uint32_t)float_to_bf16_bits(rest) : 0u) << (16 * j);
+      }
+    }
+    uh[col * kExpandPitch + w] = h;
+    ul[col * kExpandPitch + w] = l;
+  }
+  __syncthreads();
+  // rows n0r + 8c .. + 7 of tokens g and g + 8 (the pitch is a multiple of 8 floats: whole
+  // vectors, past N too)
+  auto store = [&](int64_t n0r, const float (&d)[4][4]) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t t = t0 + 2 * c + j;
-      if (t >= T) continue;
-      if (ra_ < N) delta[t * N + ra_] = d[j];
-      if (rb_ < N) delta[t * N + rb_] = d[2 + j];
+      const int col = g + 8 * j;
+      if (col < count && n0r + 8 * c < pitch) {
+        float4* o = reinterpret_cast<float4*>(delta + (t0 + L.order[first + col]) * pitch + n0r + 8 * c);
+        o[0] = make_float4(d[0][2 * j], d[0][2 * j + 1], d[1][2 * j], d[1][2 * j + 1]);
+        o[1] = make_float4(d[2][2 * j], d[2][2 * j + 1], d[3][2 * j], d[3][2 * j + 1]);
+      }
     }
+  };
+  if (narrow) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t n0r = n1 + q * kStride;
+      if (q * kStride >= rows || n0r >= N) break;
+      float d[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+      if (rank > 0) multiply(0, b[q], d);
+      store(n0r, d);
+    }
+    return;
+  }
+  for (int64_t n0r = n1; n0r < nb + rows && n0r < N; n0r += kStride) {
+    float d[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+    for (int r0 = 0; r0 < rank; r0 += 64) {
+      if (n0r > n1 || r0 > 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r0 + 16 * q < rank) load_b(n0r, r0 + 16 * q, b[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (r0 + 16 * q < rank) multiply(r0 + 16 * q, b[q], d);
+    }
+    store(n0r, d);
   }
 }
 
@@ -112,28 +171,38 @@ cudaLaunchConfig_t pdl_config(dim3 grid, unsigned threads, cudaStream_t stream, 
 
 }  // namespace
 
-// K shares of the shrink pass: at most as many as keep a share at 256 K values (one step per
-// warp), and no more CTAs than about two per SM.
-int lora_splits(int64_t K, int64_t T) {
-  const int64_t tiles = (T + 7) / 8;
+// K shares of the shrink product: at most as many as keep a share at 256 K values (one step per
+// warp), and no more CTAs than about two per SM if every tile that the tokens may make is there.
+int lora_splits(int64_t K, int64_t T, int64_t L) {
+  LoraArgs one{};
+  one.L = (int)L;
+  one.ks = 1;
   int64_t ks = (K + 255) / 256;
-  const int64_t most = 304 / tiles;
+  const int64_t most = 304 / lora_shrink_blocks(one, T);
   if (ks > most) ks = most;
   return (int)(ks < 1 ? 1 : ks);
 }
 
+int64_t lora_shrink_grid(const LoraArgs& lo, int64_t T) { return lora_shrink_blocks(lo, T); }
+
+int64_t lora_delta_pitch(int64_t N) { return (N + 7) / 8 * 8; }
+
 int lora_shrink_launch(const LoraArgs& lo, const uint16_t* x, int64_t K, int64_t T, cudaStream_t stream) {
-  const int64_t blocks = (T + 7) / 8 * lo.ks;
   cudaLaunchAttribute at[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks, 1, 1), kShrinkThreads, stream, at);
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)lora_shrink_blocks(lo, T), 1, 1), kShrinkThreads, stream, at);
   return cuda_check(cudaLaunchKernelEx(&cfg, q4_lora_shrink_kernel, lo, x, K, T), "lora: shrink kernel launch");
 }
 
 int lora_expand_launch(const LoraArgs& lo, float* delta, int64_t N, int64_t T, cudaStream_t stream) {
+  const int n0 = (int)(T < kLoraChunk ? T : kLoraChunk);
+  const int64_t tiles = (T + kLoraChunk - 1) / kLoraChunk * lora_max_tiles(n0, kExpandTokens, lo.L);
+  // a warp's 32 rows per CTA where that fills the GPU about once, else four times as many
+  const int rows = tiles * ((N + 255) / 256) <= 608 ? 256 : 1024;
   cudaLaunchAttribute at[1];
-  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((T + 7) / 8), (unsigned)((N + kExpandRows - 1) / kExpandRows), 1),
-                                            kExpandThreads, stream, at);
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_lora_expand_kernel, lo, delta, N, T), "lora: expand kernel launch");
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)tiles, (unsigned)((N + rows - 1) / rows), 1), kExpandThreads,
+                                            stream, at);
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_lora_expand_kernel, lo, delta, lora_delta_pitch(N), N, T, rows),
+                    "lora: expand kernel launch");
 }
 
 }  // namespace q4

@@ -352,9 +352,9 @@ q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, flo
   if (!early) pdl_launch_dependents();
   if constexpr (kLora) {
     if ((int)blockIdx.x >= blocks) {
-      __shared__ float red[kShrinkWarps * 8 * kShrinkRanks];
-      const int q = (int)blockIdx.x - blocks;
-      lora_shrink_tile(lo, x, K, tp, q / lo.ks, q % lo.ks, red);
+      __shared__ float red[kShrinkFloats];
+      __shared__ LoraLists L;
+      lora_shrink_block(lo, x, K, tp, (int)blockIdx.x - blocks, L, red);
       return;
     }
   }
@@ -375,8 +375,8 @@ q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, flo
 // wait for a second kernel's completion.  Always the early launch order.
 // kLora (two-kernel form, Q4): the band epilogue adds the adapters' second product, row by row
 // and token by token on the CUDA cores (rows x tokens x rank FMAs per band: 20k at 40 rows, 32
-// tokens, rank 16, against 6.5M MMA products); the idle lanes of the producer warp pull the
-// CTA's rows of every B that a token needs into L2 meanwhile.
+// tokens, rank 16, against 6.5M MMA products); the consumer warps first pull the CTA's rows
+// of every B that a token needs into L2.
 template <int NT, int FMT, bool kFuse = false, bool kSwi = false, bool kLora = false>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_high,
@@ -545,20 +545,6 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
           mbar_drain(sfull0 + 8u * (q & 1), (uint32_t)((q >> 1) & 1));
       }
     }
-    if constexpr (kLora) {
-      if (lane > 0) {
-        if (p.early) pdl_wait_previous();   // late order: everything but the prep kernel's output is final
-        for (int t = lane - 1; t < p.tp; t += 31) {
-          int rank = 0;
-          const int a = lora_adapter(p.lora, t, &rank);
-          bool seen = a < 0;
-          for (int q = 0; q < t && !seen; ++q) seen = (int)ld_global_u32(p.lora.ids + q) == a;
-          const int64_t bytes = (r1 - r0) * p.lora.R * 2;
-          if (!seen && bytes > 0)
-            bulk_prefetch_l2(p.lora.b + ((int64_t)a * p.N + r0) * p.lora.R, (uint32_t)(bytes < 262144 ? bytes : 262144));
-        }
-      }
-    }
     __syncwarp();
     return;
   }
@@ -591,6 +577,20 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     named_bar_sync(kConvBar, (uint32_t)(kMaxConsumers * 32));
   }
   if (warp - 1 >= WC) return;
+  if constexpr (kLora) {
+    // while the first stages land: this CTA's rows of every B that a token needs, to L2
+    if (p.early) pdl_wait_previous();   // late order: everything but the prep kernel's output is final
+    const int64_t bytes = (r1 - r0) * p.lora.R * 2;
+    if (lane == 0 && bytes > 0) {
+      for (int t = warp - 1; t < p.tp; t += WC) {
+        int rank = 0;
+        const int a = lora_adapter(p.lora, t, &rank);
+        if (a >= 0)
+          bulk_prefetch_l2(p.lora.b + ((int64_t)a * p.N + r0) * p.lora.R, (uint32_t)(bytes < 262144 ? bytes : 262144));
+      }
+    }
+    __syncwarp();
+  }
 
   // ------------------------------------------------------------- consumers
   const int wc = warp - 1;
@@ -924,7 +924,7 @@ int mma_launch_pass(const LinearArgs& a, const MmaPlan& pl, const CUtensorMap& t
       e = cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, FMT>, a.x + t0 * a.K, xf, zs, a.K, tp, pl.galloc, pl.lanes,
                              pl.early, nb, LoraArgs{});
     } else if constexpr (FMT == 0) {   // (one pass: the caller keeps it to 32 tokens)
-      cfg.gridDim.x = (unsigned)(nb + (tp + 7) / 8 * a.lora->ks);
+      cfg.gridDim.x = (unsigned)(nb + lora_shrink_grid(*a.lora, tp));
       e = cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, 0, true>, a.x, xf, zs, a.K, tp, pl.galloc, pl.lanes, pl.early, nb,
                              *a.lora);
     }

@@ -98,7 +98,8 @@ struct TcParams {
   //     the rest W_b's (codes in the high-plane map slot, scales_b, y_b, n_b).
   int mode;
   uint32_t tiles_a;
-  //   mode 3, LinearLora: the accumulators start from the FP32 term delta [T, N].
+  //   mode 3, LinearLora: the accumulators start from the FP32 term delta
+  //     [T, N rounded up to 8].
   const uint16_t* scales_b;
   uint16_t* y_b;
   int64_t n_b;
@@ -305,7 +306,9 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait_previous();  // before the first TMA load, scale load or output store
+  // before the first TMA load, scale load or output store (LinearLora: the kernels of this call
+  // before it launch it when everything but delta is final; only delta's readers wait)
+  if (MODE != 3 || warp >= 12) pdl_wait_previous();
 
   if (wg == 0) {
     if constexpr (NACC == 4) setmaxnreg_dec<R::ctl>();
@@ -597,7 +600,7 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
           const int64_t t = t0 + cq * kCols + j;
-          const float v = t < p.T ? __uint_as_float(ld_global_u32(p.delta + t * n_rows + row)) : 0.f;
+          const float v = t < p.T ? __uint_as_float(ld_global_u32(p.delta + t * ((n_rows + 7) / 8 * 8) + row)) : 0.f;
           if (j & 1) acc[j / 2].y = v;
           else acc[j / 2].x = v;
         }

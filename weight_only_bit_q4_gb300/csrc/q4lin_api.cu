@@ -343,8 +343,8 @@ int validate_lora_sizes(int64_t N, int64_t K, int64_t T, int64_t L, int64_t R) {
   return Q4LIN_OK;
 }
 
-size_t lora_u_bytes(int64_t K, int64_t T, int64_t R) {
-  return round256((size_t)q4::lora_splits(K, T) * (size_t)T * (size_t)R * 4);
+size_t lora_u_bytes(int64_t K, int64_t T, int64_t L, int64_t R) {
+  return round256((size_t)q4::lora_splits(K, T, L) * (size_t)T * (size_t)R * 4);
 }
 
 int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const uint16_t* lora_a, const uint16_t* lora_b,
@@ -363,9 +363,9 @@ int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const
   if ((st = check_workspace(q4lin_lora_workspace_bytes(N, K, T, L, R), workspace)) != Q4LIN_OK) return st;
   if ((st = check_device()) != Q4LIN_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t ub = lora_u_bytes(K, T, R);
+  const size_t ub = lora_u_bytes(K, T, L, R);
   const q4::LoraArgs lo{lora_a, lora_b, ids, lora_scales, ranks, reinterpret_cast<float*>(ws), (int)L, (int)R,
-                        q4::lora_splits(K, T)};
+                        q4::lora_splits(K, T, L)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   q4::LinearArgs a{wq, scales, x, y, N, K, T, ws + ub, s};
   a.lora = &lo;
@@ -449,11 +449,11 @@ extern "C" {
 size_t q4lin_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int64_t L, int64_t R) {
   if (validate_lora_sizes(N, K, T, L, R) != Q4LIN_OK || N == 0 || K == 0 || T == 0) return 0;
   if (L == 0 || R == 0) return q4lin_workspace_bytes(N, K, T);
-  const size_t ub = lora_u_bytes(K, T, R);
+  const size_t ub = lora_u_bytes(K, T, L, R);
   switch (lora_route(N, K, T, (int)R)) {
     case Q4LIN_ROUTE_GEMV: return ub;
     case Q4LIN_ROUTE_STREAM_MMA: return ub + round256(q4::mma_lora_workspace_bytes(N, K, T, (int)R));
-    case Q4LIN_ROUTE_TC_SPLITK: return ub + round256((size_t)T * (size_t)N * 4);
+    case Q4LIN_ROUTE_TC_SPLITK: return ub + round256((size_t)T * (size_t)q4::lora_delta_pitch(N) * 4);
     default: return 0;
   }
 }
