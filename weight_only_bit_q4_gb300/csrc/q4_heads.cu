@@ -13,12 +13,14 @@
 // Bound: the bytes of the heads, read once and written once (2 + 2 per value); the
 // table rows and norm weights are shared by all heads of a token.
 //
-// Split: LPH = 8, 16 or 32 lanes own one head, 8 columns (one 16-byte load) each, so the
-// mean of squares and the exchange with the partner column of the halves form are
-// shuffles inside a warp.  A lane group takes up to kHeads heads of one token whose
-// loads are issued together, and holds the token's (c, s) of its columns in registers
-// for all of them; with few tokens a group takes one head, so that even one token
-// spreads over the lanes of several CTAs.
+// Split: LPH = 8, 16 or 32 lanes own one head, 8 columns each as two runs of four (8-byte
+// loads): in the halves form the columns 4 l .. and rot/2 + 4 l .., so that a rotation stays
+// inside a thread, otherwise 8 adjacent columns.  A lane group takes up to kHeads heads of one
+// token whose loads are issued together, and holds the token's (c, s) of its columns and the
+// norm weights in registers for all of them; with few tokens a group takes one head, so that
+// even one token spreads over the lanes of several CTAs.  Arithmetic on pairs (packed FP32):
+// the pass is close enough to the issue rate that scalar arithmetic and partner shuffles
+// cost it a third.
 #include "q4_internal.h"
 #include "q4_sm100.cuh"
 
@@ -42,6 +44,21 @@ struct QkParams {
   float eps;
 };
 
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 template <int LPH, bool kInter>
 __global__ void __launch_bounds__(kQkThreads) q4_qk_norm_rope_kernel(const QkParams p) {
   pdl_launch_dependents();
@@ -53,92 +70,92 @@ __global__ void __launch_bounds__(kQkThreads) q4_qk_norm_rope_kernel(const QkPar
   // whole lane groups leave together; the shuffles below name only their own lanes
   const unsigned mask = LPH == 32 ? 0xffffffffu : ((1u << (LPH & 31)) - 1u) << ((threadIdx.x & 31) / LPH * LPH);
   if (t >= p.T) return;
-  const int32_t pos = (int32_t)ld_global_u32(p.pos + t);
-  if (pos < 0 || pos >= p.P) return;   // padding: this token's outputs stay as they are
-  const int col = 8 * l, half = p.rot / 2;
-  const bool in = col < p.D, turned = col < p.rot;
-  float c[8], s[8];
-  if (turned) {
-    const float* row = p.table + (int64_t)pos * p.rot;
-    if constexpr (kInter) {
-      const float4 cc = ld_global_f4(row + col / 2), ss = ld_global_f4(row + half + col / 2);
-      const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = cv[i / 2];
-        s[i] = (i & 1) ? sv[i / 2] : -sv[i / 2];
-      }
-    } else {
-      const bool second = col >= half;
-      const float* base = row + (second ? col - half : col);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const float4 cc = ld_global_f4(base + 4 * v), ss = ld_global_f4(base + half + 4 * v);
-        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          c[4 * v + i] = cv[i];
-          s[4 * v + i] = second ? sv[i] : -sv[i];
-        }
-      }
-    }
-  }
-  // the lane that holds the partner columns (halves form); others exchange with themselves
-  const int self = threadIdx.x & 31;
-  const int mate = kInter || !turned ? self : self + (col < half ? half / 8 : -(half / 8));
-  const float inv_d = 1.f / (float)p.D;
-
-  for (int h0 = part; h0 < p.heads; h0 += kHeads * p.gpt) {
-    uint4 v[kHeads];
+  const int half = p.rot / 2;
+  const bool in = 8 * l < p.D, turned = 8 * l < p.rot;
+  const int c0 = !kInter && turned ? 4 * l : 8 * l, c1 = !kInter && turned ? half + 4 * l : 8 * l + 4;
+  // head h: the query rows, then (h counted on) the key rows
+  const uint16_t* src_q = p.src[0] + t * p.lds[0];
+  const uint16_t* src_k = p.src[1] + t * p.lds[1] - (int64_t)p.hq * p.D;
+  uint16_t* dst_q = p.dst[0] + t * p.ldd[0];
+  uint16_t* dst_k = p.dst[1] + t * p.ldd[1] - (int64_t)p.hq * p.D;
+  // the heads' loads first: they depend on nothing, the table's on the position
+  uint2 v0[kHeads], v1[kHeads];
+  auto load_heads = [&](int h0) {
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int h = h0 + j * p.gpt;
-      const int side = h >= p.hq;
-      const int hh = side ? h - p.hq : h;
-      v[j] = in && h < p.heads ? ld_global_u4(p.src[side] + t * p.lds[side] + (int64_t)hh * p.D + col)
-                               : make_uint4(0u, 0u, 0u, 0u);
+      v0[j] = v1[j] = make_uint2(0u, 0u);
+      if (in && h < p.heads) {
+        const uint16_t* s = (h < p.hq ? src_q : src_k) + h * p.D;
+        v0[j] = ld_global_u2(s + c0);
+        v1[j] = ld_global_u2(s + c1);
+      }
     }
+  };
+  load_heads(part);
+  const int32_t pos = (int32_t)ld_global_u32(p.pos + t);
+  uint2 wq0 = make_uint2(0u, 0u), wq1 = wq0, wk0 = wq0, wk1 = wq0;
+  if (in) {
+    if (p.hq > 0) {
+      wq0 = ld_global_u2(p.w[0] + c0);
+      wq1 = ld_global_u2(p.w[0] + c1);
+    }
+    if (p.hq < p.heads) {
+      wk0 = ld_global_u2(p.w[1] + c0);
+      wk1 = ld_global_u2(p.w[1] + c1);
+    }
+  }
+  if (pos < 0 || pos >= p.P) return;   // padding: this token's outputs stay as they are
+  // four angles: of columns c0 .. c0 + 3 (halves), or of the pairs 8l / 2 .. + 3 (interleaved)
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (turned) {
+    const float* row = p.table + (int64_t)pos * p.rot + 4 * l;
+    c = ld_global_f4(row);
+    s = ld_global_f4(row + half);
+  }
+  const float inv_d = 1.f / (float)p.D;
+
+  for (int h0 = part; h0 < p.heads; h0 += kHeads * p.gpt) {
+    if (h0 != part) load_heads(h0);
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
       const int h = h0 + j * p.gpt;
       if (h >= p.heads) break;   // uniform over the lane group
-      const int side = h >= p.hq;
-      const int hh = side ? h - p.hq : h;
-      const uint32_t raw[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-      float a[8], ss = 0.f;
+      const bool key = h >= p.hq;
+      float2 a[4] = {unpack2(v0[j].x), unpack2(v0[j].y), unpack2(v1[j].x), unpack2(v1[j].y)};
+      float2 q = fmul2(a[0], a[0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[2 * i] = bf16lo(raw[i]);
-        a[2 * i + 1] = bf16hi(raw[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss);
+      for (int i = 1; i < 4; ++i) q = ffma2(a[i], a[i], q);
+      float ss = q.x + q.y;
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
       const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-      uint32_t wr[4] = {0u, 0u, 0u, 0u};
+      const float2 rr = make_float2(r, r);
+      a[0] = fmul2(fmul2(a[0], rr), unpack2(key ? wk0.x : wq0.x));
+      a[1] = fmul2(fmul2(a[1], rr), unpack2(key ? wk0.y : wq0.y));
+      a[2] = fmul2(fmul2(a[2], rr), unpack2(key ? wk1.x : wq1.x));
+      a[3] = fmul2(fmul2(a[3], rr), unpack2(key ? wk1.y : wq1.y));
+      if (turned) {   // (columns past rot keep their bits: an infinity there does not meet a zero sine)
+        if constexpr (kInter) {
+          const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            a[i] = make_float2(fmaf(a[i].x, cv[i], -a[i].y * sv[i]), fmaf(a[i].y, cv[i], a[i].x * sv[i]));
+        } else {
+          const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)}, sn[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 u = a[i], w = a[2 + i];
+            a[i] = ffma2(u, cc[i], fmul2(make_float2(-w.x, -w.y), sn[i]));
+            a[2 + i] = ffma2(w, cc[i], fmul2(u, sn[i]));
+          }
+        }
+      }
       if (in) {
-        const uint4 wv = ld_global_u4(p.w[side] + col);
-        wr[0] = wv.x; wr[1] = wv.y; wr[2] = wv.z; wr[3] = wv.w;
+        uint16_t* d = (key ? dst_k : dst_q) + h * p.D;
+        *reinterpret_cast<uint2*>(d + c0) = make_uint2(pack2(a[0]), pack2(a[1]));
+        *reinterpret_cast<uint2*>(d + c1) = make_uint2(pack2(a[2]), pack2(a[3]));
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[2 * i] = a[2 * i] * r * bf16lo(wr[i]);
-        a[2 * i + 1] = a[2 * i + 1] * r * bf16hi(wr[i]);
-      }
-      float z[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = kInter ? a[i ^ 1] : __shfl_sync(mask, a[i], mate);
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float y0 = turned ? fmaf(a[i], c[i], z[i] * s[i]) : a[i];
-        const float y1 = turned ? fmaf(a[i + 1], c[i + 1], z[i + 1] * s[i + 1]) : a[i + 1];
-        o[i / 2] = (uint32_t)float_to_bf16_bits(y0) | ((uint32_t)float_to_bf16_bits(y1) << 16);
-      }
-      if (in)
-        *reinterpret_cast<uint4*>(p.dst[side] + t * p.ldd[side] + (int64_t)hh * p.D + col) =
-            make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }

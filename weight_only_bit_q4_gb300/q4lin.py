@@ -422,12 +422,22 @@ def linear_pair(wq_a, scales_a, wq_b, scales_b, x, y_a=None, y_b=None, stream=No
 # counts: each tensor is checked once, with attribute reads only, and pointers go to the
 # library as plain integers.
 
-def _stream_ptr(stream, device):
-    import torch
+_torch = None
 
+
+def _t():
+    """torch, imported at the first call (the binding itself loads without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _stream_ptr(stream, device):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _t()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(name, t, dtype, shape):
@@ -448,11 +458,10 @@ def _need_bits16(name, t, shape):
 
 def _scratch(workspace, need, device):
     """(address, the tensor that keeps it alive) of at least ``need`` workspace bytes."""
-    import torch
-
     if need == 0:
         return None, None
     if workspace is None:
+        torch = _t()
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes")
@@ -479,8 +488,7 @@ def linear_lora(wq, scales, x, lora_a, lora_b, adapter_ids, adapter_scales=None,
     up to 256.  ``y`` (bf16 [T, N]) and ``workspace`` (uint8, >= lora_workspace_bytes) are
     allocated here if not given.
     """
-    import torch
-
+    torch = _t()
     bf16 = torch.bfloat16
     T, K = x.shape
     L, R, _ = lora_a.shape
@@ -514,8 +522,7 @@ def moe_router(x, w_router, top_k: int, bias=None, renormalize: bool = True, ids
     x bf16 [T, H]; w_router bf16 [E, H]; bias fp32 [E] added to the logits (-inf: the expert is
     never chosen) or None.  Where fewer than top_k experts can be chosen, id -1 with weight 0.
     """
-    import torch
-
+    torch = _t()
     T, H = x.shape
     E = w_router.shape[0]
     dev = x.device
@@ -535,8 +542,7 @@ def moe_router(x, w_router, top_k: int, bias=None, renormalize: bool = True, ids
 
 def _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H):
     """Checked addresses of the experts' planes, E and F."""
-    import torch
-
+    torch = _t()
     E, F2 = wq_gate_up.shape[:2]
     if F2 % 2:
         raise ValueError("wq_gate_up holds an even number of rows per expert: gate rows, then up rows")
@@ -555,8 +561,7 @@ def moe_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_dow
     nothing); wq_gate_up uint8 [E, 2F, Hp/2] (gate rows, then up rows), wq_down uint8 [E, H, Fp/2]
     with their fp16 scales per 64 columns (Hp, Fp: H, F rounded up to 128).
     """
-    import torch
-
+    torch = _t()
     T, H = x.shape
     k = ids.shape[1]
     gu, gus, dn, dns, E, F = _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H)
@@ -576,8 +581,7 @@ def moe_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_dow
 def moe(x, w_router, wq_gate_up, scales_gate_up, wq_down, scales_down, top_k: int, bias=None, renormalize: bool = True,
         y=None, ids=None, weights=None, workspace=None, stream=None):
     """The whole mixture-of-experts layer, ``moe_router`` then ``moe_experts`` in one call: (y, ids, weights)."""
-    import torch
-
+    torch = _t()
     T, H = x.shape
     dev = x.device
     gu, gus, dn, dns, E, F = _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H)
@@ -599,19 +603,19 @@ def moe(x, w_router, wq_gate_up, scales_gate_up, wq_down, scales_down, top_k: in
     return y, ids, weights
 
 
-def _rows(name, t, D):
+def _rows(name, t, D, bf16):
     """Address, row stride and heads of bf16 rows [T, heads * D] or [T, heads, D], contiguous within a row."""
-    import torch
-
-    if t.dtype is not torch.bfloat16 or not t.is_cuda:
+    if t.dtype is not bf16 or not t.is_cuda:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() == 3:
-        if t.shape[2] != D or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
-            raise ValueError(f"{name}: the heads of a row must lie side by side, {D} values each")
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * D, t.shape[1]
-    if t.dim() != 2 or t.shape[1] % D or t.stride(1) != 1:
-        raise ValueError(f"{name} must be [T, heads * {D}] or [T, heads, {D}] with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1], t.shape[1] // D
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        n = shape[1]
+        if D == 0 or n % D or stride[1] != 1:
+            raise ValueError(f"{name} must be [T, heads * {D}] or [T, heads, {D}] with contiguous rows")
+        return t.data_ptr(), stride[0] if shape[0] > 1 else n, n // D
+    if len(shape) != 3 or shape[2] != D or stride[2] != 1 or (shape[1] > 1 and stride[1] != D):
+        raise ValueError(f"{name}: the heads of a row must lie side by side, {D} values each")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * D, shape[1]
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6, interleaved: bool = False, q_out=None,
@@ -623,8 +627,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     sines); positions int32 [T] (outside [0, P): the token's outputs are not written).  ``q_out``
     and ``k_out`` may be q and k (in place); allocated here if not given.
     """
-    import torch
-
+    torch = _t()
     D = q_weight.shape[0]
     T = q.shape[0]
     P, rot = cos_sin.shape
@@ -632,13 +635,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    qp, ldq, hq = _rows("q", q, D)
-    kp, ldk, hk = _rows("k", k, D)
-    qo, ldqo, hqo = _rows("q_out", q_out, D)
-    ko, ldko, hko = _rows("k_out", k_out, D)
+    bf16 = torch.bfloat16
+    qp, ldq, hq = _rows("q", q, D, bf16)
+    kp, ldk, hk = _rows("k", k, D, bf16)
+    qo, ldqo, hqo = _rows("q_out", q_out, D, bf16)
+    ko, ldko, hko = _rows("k_out", k_out, D, bf16)
     if (hqo, hko) != (hq, hk) or k.shape[0] != T or q_out.shape[0] != T or k_out.shape[0] != T:
         raise ValueError("q, k and their outputs must have the same tokens and heads")
-    bf16 = torch.bfloat16
     st = load().q4lin_qk_norm_rope(
         qp, ldq, kp, ldk, _need("q_weight", q_weight, bf16, (D,)), _need("k_weight", k_weight, bf16, (D,)),
         _need("cos_sin", cos_sin, torch.float32, (P, rot)), _need("positions", positions, torch.int32, (T,)), qo, ldqo, ko,
