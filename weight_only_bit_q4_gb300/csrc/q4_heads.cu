@@ -28,8 +28,8 @@ namespace q4 {
 
 namespace {
 
-constexpr int kQkThreads = 256;
-constexpr int kHeads = 4;   // heads in flight per lane group
+constexpr int kQkThreads = 128;
+constexpr int kHeads = 5;   // heads in flight per lane group
 
 struct QkParams {
   const uint16_t* src[2];
