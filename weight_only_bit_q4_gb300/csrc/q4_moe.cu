@@ -41,7 +41,9 @@
 // Two forms, by the number of slots S = T top_k of a pass:
 //   S <= kLatSlots: latency.  MT = 1, the K range of a unit shared by up to 4 warps (partial
 //     sums joined in shared memory); every CTA of the down product converts all of h itself,
-//     owns whole units and adds its slots' sums in shared memory.
+//     owns whole units and adds its slots' sums in shared memory.  (At 80 registers a down CTA
+//     of 8 warps fits beside the gate/up CTA and starts early, but both then spill and run at
+//     half speed: one token of 8 of 64 experts took 25.8 us against 22.2.)
 //   otherwise: throughput.  MT = 2 (each B fragment feeds
 //     two MMA row tiles); the (tile, unit) pairs are dealt evenly over all CTAs, a kernel
 //     between the two products converts h, the slots' sums of the down product go to the
@@ -63,7 +65,6 @@ constexpr int kMaxNT = 2;                   // token tiles of 8 handled together
 constexpr int kLatSlots = 16;               // up to here the latency form
 constexpr int kMaxParts = 4;                // warps that share the K range of an item, at most
 constexpr int kMoeWarps = 16;
-constexpr int kMoeThreads = 32 * kMoeWarps;
 __host__ __device__ constexpr int slot_bytes(int mt) { return 2 * 8 * mt * 128; }
 constexpr int kMaxSlots = 512;              // (token, choice) pairs per pass
 constexpr int kMaxExperts = 1024;
@@ -149,26 +150,49 @@ __device__ __forceinline__ void moe_prep_token(const uint16_t* x, int64_t H, uin
   if (tid == 0) *ft = exp2i(24 + e);
 }
 
-// The same of one slot's h (FP32, F values), by one warp.
-__device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf, float* zs, float* ft) {
-  const int lane = threadIdx.x & 31;
+// The same of one slot's h (FP32, F values), by kLanes adjacent lanes of a warp or a whole CTA
+// of kLanes threads (`share`: its exchange buffer).  Up to 8 kRuns kLanes values are read once
+// and held in registers between the maximum and the conversion.
+template <int kLanes, int kRuns>
+__device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf, float* zs, float* ft, uint32_t* share) {
+  const int lane = threadIdx.x % kLanes;
   const int nv = F / 8, nv64 = (F + 63) / 64 * 8;
+  float4 keep[kRuns][2];
   uint32_t mx = 0;   // FP32 magnitude bits
-  for (int i = lane; i < 2 * nv; i += 32) {
-    const uint4 v = ld_global_u4(h + 4 * i);
-    mx = max(max(max(mx, v.x & 0x7FFFFFFFu), max(v.y & 0x7FFFFFFFu, v.z & 0x7FFFFFFFu)), v.w & 0x7FFFFFFFu);
+  auto load = [&](int i, float4 (&v)[2]) {
+    v[0] = v[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < nv) {
+      v[0] = ld_global_f4(h + 8 * (int64_t)i);
+      v[1] = ld_global_f4(h + 8 * (int64_t)i + 4);
+    }
+  };
+  auto magnitude = [&](const float4 (&v)[2]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      mx = max(max(max(mx, __float_as_uint(v[q].x) & 0x7FFFFFFFu), max(__float_as_uint(v[q].y) & 0x7FFFFFFFu, __float_as_uint(v[q].z) & 0x7FFFFFFFu)),
+               __float_as_uint(v[q].w) & 0x7FFFFFFFu);
+  };
+#pragma unroll
+  for (int u = 0; u < kRuns; ++u) load(lane + u * kLanes, keep[u]);
+#pragma unroll
+  for (int u = 0; u < kRuns; ++u) magnitude(keep[u]);
+  for (int i = lane + kRuns * kLanes; i < nv; i += kLanes) {
+    float4 v[2];
+    load(i, v);
+    magnitude(v);
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
+  if constexpr (kLanes > 32) {
+    if ((threadIdx.x & 31) == 0) share[threadIdx.x >> 5] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kLanes / 32; ++w) mx = max(mx, share[w]);
+  }
   const int E = (int)(mx >> 23);
   const int e = (mx == 0 || E == 255) ? 0 : min(max(E - 141, -100), 100);
   const float s1 = exp2i(-e), s16 = exp2i(-e - 4);
-  for (int i = lane; i - lane < nv64; i += 32) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
-    if (i < nv) {
-      a = ld_global_f4(h + 8 * i);
-      c = ld_global_f4(h + 8 * i + 4);
-    }
-    const float f[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  auto convert = [&](int i, const float4 (&v)[2]) {   // whole warps; the 8 lanes of a group are adjacent
+    const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     float sum;
     const uint4 b = moe_fragment(f, s1, s16, sum);
 #pragma unroll
@@ -177,6 +201,14 @@ __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf
       *reinterpret_cast<uint4*>(hf + moe_fragment_at(i)) = b;
       if ((i & 7) == 0) zs[i >> 3] = kZeroTerm * sum;
     }
+  };
+#pragma unroll
+  for (int u = 0; u < kRuns; ++u)
+    if (u * kLanes < nv64) convert(lane + u * kLanes, keep[u]);
+  for (int i0 = kRuns * kLanes; i0 < nv64; i0 += kLanes) {
+    float4 v[2];
+    load(i0 + lane, v);
+    convert(i0 + lane, v);
   }
   if (lane == 0) *ft = exp2i(24 + e);
 }
@@ -193,6 +225,71 @@ __global__ void __launch_bounds__(256) q4_moe_prep_kernel(const RouterParams p) 
   pdl_launch_dependents();
   pdl_wait_previous();
   moe_prep_at(p, blockIdx.x);
+}
+
+// The top_k of one token's logits (lg: `parts` sums of each expert, part after part), by one
+// warp.  kV: values per lane.  Each lane keeps its values as order-preserving integers (0: never
+// chosen -- -inf, NaN, what is already chosen) and its best one; a pick is a warp maximum of the
+// keys and a minimum over the experts that have it.
+template <int kV>
+__device__ __forceinline__ void moe_pick(const RouterParams& p, const float* lg, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[kV];
+  uint32_t best = 0u;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = 0u;
+    if (e < p.E) {
+      float v = lg[e];
+      for (int q = 1; q < p.parts; ++q) v += lg[q * p.E + e];
+      const uint32_t b = __float_as_uint(v);
+      if (v > -INFINITY) key[i] = (b & 0x80000000u) ? ~b : b | 0x80000000u;
+      best = max(best, key[i]);
+    }
+  }
+  auto value = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k); };
+  const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+  const float m = value(top);
+  auto ex = [&](uint32_t k) { return k == top ? 1.f : expf(value(k) - m); };   // m may be +inf
+  float z = 0.f;
+  if (!p.renorm) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+      if (key[i] != 0u) z += ex(key[i]);
+    z = warp_sum(z);
+  }
+  uint32_t mine = 0u;   // lane j keeps pick j (k <= 32)
+  int mine_id = -1;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t k = __reduce_max_sync(0xffffffffu, best);
+    if (k == 0u) break;   // none left
+    int at = p.E;
+    if (best == k) {
+#pragma unroll
+      for (int i = kV - 1; i >= 0; --i)
+        if (key[i] == k) at = lane + 32 * i;
+    }
+    const int id = __reduce_min_sync(0xffffffffu, at);
+    if (lane == j) {
+      mine = k;
+      mine_id = id;
+    }
+    if (lane == (id & 31)) {
+      best = 0u;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        if (lane + 32 * i == id) key[i] = 0u;
+        best = max(best, key[i]);
+      }
+    }
+  }
+  const float pe = mine != 0u ? ex(mine) : 0.f;
+  if (p.renorm) z = warp_sum(pe);
+  if (lane < p.k) {
+    p.ids[t * p.k + lane] = mine_id;
+    p.weights[t * p.k + lane] = mine_id >= 0 ? pe / z : 0.f;
+  }
 }
 
 // One cluster per TT tokens: its 128 warps share the experts (with few experts several warps
@@ -265,71 +362,8 @@ q4_moe_router_kernel(const RouterParams p) {
   cluster_sync();
   if (rank != 0 || warp >= TT || t0 + warp >= p.T) return;
   // ---- one warp per token: softmax statistics, then top_k picks
-  float* lg = logit[warp];
-  constexpr float kNone = -INFINITY;   // never chosen: -inf, NaN and what is already chosen
-  float m = kNone;
-  for (int e = lane; e < p.E; e += 32) {
-    float v = lg[e];
-    for (int q = 1; q < p.parts; ++q) v += lg[q * p.E + e];
-    v = v > kNone ? v : kNone;   // NaN too
-    lg[e] = v;
-    m = fmaxf(m, v);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  auto ex = [&](float v) { return v == m ? 1.f : expf(v - m); };   // m may be +inf
-  float z = 0.f;
-  for (int e = lane; e < p.E; e += 32) {
-    const float v = lg[e];
-    if (v > kNone) z += ex(v);
-  }
-  z = warp_sum(z);
-  __syncwarp();
-  // Each lane keeps its own best (as an order-preserving integer) and looks for the next one
-  // only after it was picked.
-  auto key_of = [](float v) {   // larger float, larger key; kNone is the smallest that occurs
-    const uint32_t b = __float_as_uint(v);
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  };
-  uint32_t key = 0u;
-  int at = p.E;
-  auto scan = [&]() {
-    key = 0u;
-    at = p.E;
-    for (int e = lane; e < p.E; e += 32) {
-      const float v = lg[e];
-      const uint32_t q = key_of(v);
-      if (v > kNone && q > key) {
-        key = q;
-        at = e;
-      }
-    }
-  };
-  scan();
-  float chosen = 0.f, mine = 0.f;   // lane j keeps pick j (k <= 32)
-  int mine_id = -1;
-  for (int j = 0; j < p.k; ++j) {
-    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-    if (top == 0u) break;   // none left
-    const int id = __reduce_min_sync(0xffffffffu, key == top ? at : p.E);
-    const uint32_t b = (top & 0x80000000u) ? top & 0x7FFFFFFFu : ~top;
-    const float pe = ex(__uint_as_float(b));
-    chosen += pe;
-    if (lane == j) {
-      mine = pe;
-      mine_id = id;
-    }
-    if (lane == (id & 31)) {
-      lg[id] = kNone;
-      scan();
-    }
-    __syncwarp();
-  }
-  if (lane < p.k) {
-    const int64_t o = (t0 + warp) * p.k + lane;
-    p.ids[o] = mine_id;
-    p.weights[o] = mine_id >= 0 ? mine / (p.renorm ? chosen : z) : 0.f;
-  }
+  if (p.E <= 128) moe_pick<4>(p, logit[warp], t0 + warp);   // (four values per lane, in registers)
+  else moe_pick<kMaxExperts / 32>(p, logit[warp], t0 + warp);
 }
 
 // ----------------------------------------------------------------- slots by expert
@@ -560,30 +594,31 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
 // exchange buffer -- gate/up, the accumulators of the K parts (one 16-byte word per thread,
 // two rounds); down, the slots' sums of every K part -- and, down, h of every slot.
 __host__ inline uint32_t moe_layout(MoeParams& p, int per, int mt, bool down, bool lat) {
-  p.bar_off = (uint32_t)(kMoeWarps * p.depth * slot_bytes(mt));
-  p.cnt_off = p.bar_off + (uint32_t)(kMoeWarps * p.depth * 8);
+  constexpr int warps = kMoeWarps;
+  p.bar_off = (uint32_t)(warps * p.depth * slot_bytes(mt));
+  p.cnt_off = p.bar_off + (uint32_t)(warps * p.depth * 8);
   p.wcnt_off = p.cnt_off + (p.slots <= 32 ? 0u : (uint32_t)p.E * 4);
-  p.tiles_off = (p.wcnt_off + (p.slots <= 32 ? 0u : (uint32_t)(kMoeWarps * p.E + 4)) + 7) / 8 * 8;
+  p.tiles_off = (p.wcnt_off + (p.slots <= 32 ? 0u : (uint32_t)(warps * p.E + 4)) + 7) / 8 * 8;
   p.order_off = p.tiles_off + (uint32_t)moe_max_tiles(p.slots, p.E, per) * 8;
   p.misc_off = p.order_off + (uint32_t)p.slots * 4;
   p.sum_off = (p.misc_off + 16 + 15) / 16 * 16;
-  p.frag_off = p.sum_off + (lat ? (down ? (uint32_t)(kMaxParts * p.slots * 64) : (uint32_t)(2 * kMoeThreads * 16)) : 0u);
+  p.frag_off = p.sum_off + (lat ? (down ? (uint32_t)(kMaxParts * p.slots * 64) : (uint32_t)(2 * 32 * warps * 16)) : 0u);
   p.frag_pitch = 0;
   if (!(lat && down)) return p.frag_off;
   // h of every slot: fragments (64 bytes of padding put two columns' 64-byte reads on
-  // different banks), zero-point terms, and one power of two
+  // different banks), zero-point terms, one power of two; the slot's weight and whether it counts
   p.frag_pitch = (uint32_t)(moe_groups(p.F) * 128 + 64);
-  return p.frag_off + (uint32_t)p.slots * (p.frag_pitch + (uint32_t)moe_zs_pitch(p.F) * 4 + 4);
+  return p.frag_off + (uint32_t)p.slots * (p.frag_pitch + (uint32_t)moe_zs_pitch(p.F) * 4 + 12);
 }
 
 // kDown false: gate/up units, h written; true: down units, y (latency) or part written.
 template <int NT, int MT, bool kDown, bool kLat>
-__global__ void __launch_bounds__(kMoeThreads, 1)
+__global__ void __launch_bounds__(32 * kMoeWarps, 1)
 q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  constexpr int kPer = 8 * NT, kRows = 8 * MT;
+  constexpr int kPer = 8 * NT, kRows = 8 * MT, kWarps = kMoeWarps, kThreads = 32 * kWarps;
   constexpr uint32_t kSlot = slot_bytes(MT);
   MoeLists L;
   L.cnt = reinterpret_cast<int*>(smem + p.cnt_off);
@@ -594,12 +629,15 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + p.misc_off + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kMoeWarps * p.depth; ++i) mbar_init(sbase + p.bar_off + 8u * (uint32_t)i, 1);
-    *abort_flag = 0;
+  if (lane == 0) {   // a warp's barriers are its own
+    for (int i = 0; i < p.depth; ++i) mbar_init(sbase + p.bar_off + 8u * (uint32_t)(warp * p.depth + i), 1);
     fence_mbar_init();
-    prefetch_tmap(&tm);
+    if (warp == 0) {
+      *abort_flag = 0;
+      prefetch_tmap(&tm);
+    }
   }
+  __syncwarp();
   // Order of the chain: the gate/up kernel waits for everything before it, then lets the
   // down kernel launch.  So when the down kernel starts, ids, weights and planes are final
   // and only h is still being written: it sorts the slots and fills its rings before its
@@ -624,18 +662,18 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   // [u0, u1) of the numbers tile * nu + unit, so that a CTA's warps share an expert's tokens
   // (the host bounds nu * tiles below 2^31).  kp warps share the K range of an item.
   constexpr bool kOwn = kDown && kLat;
-  const int64_t all = kOwn ? nu : (int64_t)nu * ntiles;
-  const int u0 = (int)((int64_t)blockIdx.x * all / gridDim.x), u1 = (int)((int64_t)(blockIdx.x + 1) * all / gridDim.x);
+  const int all = kOwn ? nu : nu * ntiles, grid = (int)gridDim.x, bid = (int)blockIdx.x;
+  const int share = all / grid, more = all - share * grid;   // the first `more` CTAs take one more
+  const int u0 = bid * share + (bid < more ? bid : more), u1 = u0 + share + (bid < more ? 1 : 0);
   int kp = 1;
   if constexpr (kLat) {   // the same for every CTA (down: for every unit)
-    const int items = kOwn ? ntiles : (int)((all + gridDim.x - 1) / gridDim.x);
-    kp = items > 0 ? kMoeWarps / items : 1;
-    kp = kp < 1 ? 1 : kp > kMaxParts ? kMaxParts : kp;
-    if (kp > nsb) kp = nsb;
+    const int items = kOwn ? ntiles : share + (more > 0 ? 1 : 0);
+    while (kp < kMaxParts && 2 * kp * items <= kWarps && 2 * kp <= nsb) kp *= 2;
   }
-  const int wpr = kMoeWarps / kp;                    // items per round of the warps
-  const int wnum = warp / kp, kpart = warp - wnum * kp;
-  const int sb0 = nsb * kpart / kp, sb1 = nsb * (kpart + 1) / kp;
+  const int kps = 31 - __clz(kp);                  // kp is a power of two
+  const int wpr = kWarps >> kps;                   // items per round of the warps
+  const int wnum = warp >> kps, kpart = warp & (kp - 1);
+  const int sb0 = (nsb * kpart) >> kps, sb1 = (nsb * (kpart + 1)) >> kps;
   // The items of this warp, in order: a position that steps without divisions.
   struct Pos {
     int tile, unit, left;   // left: numbers to the end of the range (kOwn: units to its end)
@@ -701,6 +739,17 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       for (int i = 0; i <= nl; ++i) f(a + (128 * i < most ? 128 * i : most));
     }
   };
+  float* wsm = nullptr;   // kOwn: the slots' weights, and which of them count
+  int* von = nullptr;
+  if constexpr (kOwn) {
+    wsm = reinterpret_cast<float*>(smem + p.frag_off + p.slots * (p.frag_pitch + (uint32_t)moe_zs_pitch(K) * 4 + 4));
+    von = reinterpret_cast<int*>(wsm + p.slots);
+    if ((int)threadIdx.x < p.slots) {
+      const int id = p.ids[threadIdx.x];
+      wsm[threadIdx.x] = p.weights[threadIdx.x];
+      von[threadIdx.x] = id >= 0 && id < p.E;
+    }
+  }
   const Pos first_item = start();
   if (first_item.left > 0) for_scale_lines(first_item, [&](const uint8_t* a) { prefetch_l2(a); });
   // The B columns: x of a token (gate/up) or h of a slot (down), fragments, terms and powers.
@@ -709,11 +758,12 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   const float* power = kDown ? p.hft : p.ft;
   const int64_t fpitch = kOwn ? (int64_t)p.frag_pitch : (int64_t)groups * 128, zpitch = moe_zs_pitch(K);
   if constexpr (kDown) pdl_wait_previous();
-  if constexpr (kOwn) {   // a warp per slot (at most kLatSlots) converts h
+  if constexpr (kOwn) {   // a warp per slot converts h
     float* zsm = reinterpret_cast<float*>(smem + p.frag_off + p.slots * p.frag_pitch);
     float* fsm = zsm + p.slots * zpitch;
-    if (warp < p.slots)
-      moe_prep_slot(p.h + (int64_t)warp * K, K, smem + p.frag_off + warp * p.frag_pitch, zsm + warp * zpitch, fsm + warp);
+    for (int s = warp; s < p.slots; s += kWarps)
+      moe_prep_slot<32, 3>(p.h + (int64_t)s * K, K, smem + p.frag_off + s * p.frag_pitch, zsm + s * zpitch, fsm + s,
+                           nullptr);
     frag = smem + p.frag_off;
     zero = zsm;
     power = fsm;
@@ -812,7 +862,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       if (have) compute(q, pos, acc, first, count);
       if constexpr (kLat) {
         if (kp > 1) {   // part 0 adds the others' accumulators, in order
-          float4* ex = reinterpret_cast<float4*>(sums) + parity * kMoeThreads;
+          float4* ex = reinterpret_cast<float4*>(sums) + parity * kThreads;
           parity ^= 1;
           if (have && kpart > 0) ex[threadIdx.x] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][0][2], acc[0][0][3]);
           __syncthreads();
@@ -897,20 +947,21 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         __syncthreads();
         if (!*abort_flag) {   // y of the unit's rows: the slots' sums in the order of the choices
           const int64_t n0 = 16 * (int64_t)unit;
-          for (int e = threadIdx.x; e < tokens * 16; e += kMoeThreads) {
-            const int t = e >> 4, rr = e & 15;
-            if (n0 + rr >= p.H) continue;
+          // lane 16 h + row takes every second choice; the halves meet by a shuffle
+          for (int t = warp; t < tokens; t += kWarps) {
+            const int rr = lane & 15;
             float v = 0.f;
-            for (int j = 0; j < p.k; ++j) {
+#pragma unroll 4
+            for (int j = lane >> 4; j < p.k; j += 2) {
               const int s = t * p.k + j;
-              const int id = p.ids[s];
-              const float w = p.weights[s];
-              if (id < 0 || id >= p.E) continue;
               float part = 0.f;
-              for (int i = 0; i < kp; ++i) part += sums[(i * p.slots + s) * 16 + rr];
-              v = fmaf(w, part, v);
+#pragma unroll
+              for (int i = 0; i < kMaxParts; ++i)
+                if (i < kp) part += sums[(i * p.slots + s) * 16 + rr];
+              v = von[s] ? fmaf(wsm[s], part, v) : v;
             }
-            p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            if (lane < 16 && n0 + rr < p.H) p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
           }
         }
         __syncthreads();   // the sums are free again
@@ -922,15 +973,18 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       mbar_drain(bars + 8u * (uint32_t)(d % p.depth), (uint32_t)((d / p.depth) & 1));
 }
 
-// Throughput form, between the products: a warp per slot converts h.
-__global__ void __launch_bounds__(256) q4_moe_convert_kernel(const MoeParams p) {
+// Throughput form, between the products: a CTA per slot converts h.
+constexpr int kConvertThreads = 128;
+
+__global__ void __launch_bounds__(kConvertThreads) q4_moe_convert_kernel(const MoeParams p) {
+  __shared__ uint32_t share[kConvertThreads / 32];
   pdl_launch_dependents();
+  const int s = (int)blockIdx.x;
+  const int id = (int)ld_global_u32(p.ids + s);   // (the gate/up kernel launches this one after its own wait)
   pdl_wait_previous();
-  const int s = (int)(blockIdx.x * 8 + (threadIdx.x >> 5));
-  if (s >= p.slots) return;
-  const int id = (int)ld_global_u32(p.ids + s);
-  if (id < 0 || id >= p.E) return;   // (its h was not written)
-  moe_prep_slot(p.h + (int64_t)s * p.F, (int)p.F, p.hf + s * moe_groups(p.F) * 128, p.hz + s * moe_zs_pitch(p.F), p.hft + s);
+  if (id < 0 || id >= p.E) return;                // its h was not written
+  moe_prep_slot<kConvertThreads, 2>(p.h + (int64_t)s * p.F, (int)p.F, p.hf + s * moe_groups(p.F) * 128,
+                                    p.hz + s * moe_zs_pitch(p.F), p.hft + s, share);
 }
 
 // Throughput form, after the down product: y[t, n] = sum_j p[t, j] part[t k + j, n] in the order
@@ -977,7 +1031,7 @@ int moe_sm_count() {
 
 // Dynamic shared memory at most: what is left of the SM's 256 KB is the L1 that the B columns
 // and scales are found in.
-constexpr int kMoeSmem = 150 * 1024;
+constexpr uint32_t kMoeSmem = 150 * 1024;
 
 // (the down product of the throughput form starts after the conversion kernel, whose early
 // launch lets it begin before the gate/up product is complete: it reads h and what follows from
@@ -1015,7 +1069,7 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kMoeThreads, 1, 1);
+  cfg.blockDim = dim3(32 * kMoeWarps, 1, 1);
   cfg.dynamicSmemBytes = bytes + 1024;
   cfg.stream = stream;
   cfg.attrs = at;
@@ -1180,7 +1234,7 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
     if (const int rc = moe_kernel_form<false>(lat, nt, gu, p, sms, a.stream)) return rc;
     if (!lat) {
       cudaLaunchAttribute at[1];
-      const cudaLaunchConfig_t cfg = moe_config((unsigned)((p.slots + 7) / 8), 256, a.stream, at);
+      const cudaLaunchConfig_t cfg = moe_config((unsigned)p.slots, kConvertThreads, a.stream, at);
       if (cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_convert_kernel, p), "moe: conversion launch")) return Q4LIN_ERR_CUDA;
     }
     if (const int rc = moe_kernel_form<true>(lat, nt, dn, p, sms, a.stream)) return rc;

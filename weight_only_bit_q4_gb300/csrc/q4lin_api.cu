@@ -306,7 +306,7 @@ int validate_experts(const void* x, const void* ids, const void* weights, const 
   if (st == Q4LIN_OK) st = validate_sizes(E * H, F, T);
   if (st != Q4LIN_OK) return st;
   if (E * 2 * F >= kMaxRows || E * H >= kMaxRows || T > (int64_t)1 << 24 ||
-      F / 8 * (T < 512 ? T * top_k + E : 512 + E) >= kMaxRows)
+      (F / 8 + 1) * (512 + E) >= kMaxRows || (H / 8 + 1) * (512 + E) >= kMaxRows)
     return refuse("moe: the experts' rows exceed the 32-bit row coordinates", Q4LIN_ERR_UNSUPPORTED_SHAPE);
   if (T == 0 || H == 0) return Q4LIN_OK;
   if (y == nullptr) return Q4LIN_ERR_INVALID_ARG;
