@@ -10,7 +10,7 @@
 // Three kernels chained by programmatic dependent launch.  Bound: the packed weights of
 // the experts that some token chose, each read once; the kernels below therefore sort
 // the (token, choice) slots by expert and stream each chosen expert's rows once for all
-// of its tokens (tiles of 8 NT token columns).
+// of its tokens (tiles of up to 8 NT token columns).
 //
 // Products.  mma.sync m16n8k16 (fp16 x fp16 -> fp32); the 64 weights of a scale group go
 // through four MMAs into a fresh D, then acc += s D in FP32.  A: a masked nibble pair is the
@@ -36,7 +36,9 @@
 // Streaming.  Every warp owns a ring of shared-memory slots, one sub-box (two boxes of
 // 8 MT rows x 256 weights, TMA) each, and works through its own sequence of (unit,
 // sub-box): lane 0 refills a slot as soon as the warp has read it, across unit borders, so
-// no warp waits for another and the ring is the only buffering.
+// no warp waits for another.  The columns of a CTA's next few tiles lie in shared memory
+// beside the rings (bulk copies); read through L1 instead they cost the whole layer 15 us of
+// 103 at 64 tokens x 8 of 128 experts.
 //
 // Two forms, by the number of slots S = T top_k of a pass:
 //   S <= kLatSlots: latency.  MT = 1, the K range of a unit shared by up to 4 warps (partial
@@ -384,8 +386,10 @@ struct MoeParams {
   int64_t H, F;
   int E, k, slots;         // slots = T k of this pass
   int depth;               // ring slots per warp
-  uint32_t bar_off, cnt_off, wcnt_off, order_off, tiles_off, misc_off, sum_off, frag_off;   // shared memory
-  uint32_t frag_pitch;     // latency form, down: bytes per slot of the fragments in shared memory
+  int per;                 // columns per tile, at most (8 NT, fewer where a column is long)
+  int gtiles;              // tiles whose columns lie in shared memory together
+  uint32_t col_bytes;      // shared memory of a column
+  uint32_t bar_off, cnt_off, wcnt_off, order_off, tiles_off, misc_off, sum_off, col_off;   // shared memory
 };
 
 // Shared-memory lists of one CTA: the tiles (up to 8 kMaxNT slots of one expert) in
@@ -520,12 +524,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // What a warp holds of one unit while it runs through the unit's K range: where its rows'
-// scales and its B columns start.  Plain loads (not the volatile ones) in the loops, so that
-// the compiler can overlap the groups of a sub-box; the waits before them are compiler
-// barriers.
+// scales (global memory) and its B columns (shared memory) start.  Plain loads (not the
+// volatile ones) in the loops, so that the compiler can overlap the groups of a sub-box; the
+// waits before them are compiler barriers.
 template <int NT, int MT>
 struct MoeUnit {
   const uint16_t* s0[MT];    // scales of MMA rows g and g + 8
@@ -590,35 +600,40 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
   }
 }
 
-// Shared-memory layout: rings (1024-byte aligned), barriers, lists, then the latency form's
-// exchange buffer -- gate/up, the accumulators of the K parts (one 16-byte word per thread,
-// two rounds); down, the slots' sums of every K part -- and, down, h of every slot.
-__host__ inline uint32_t moe_layout(MoeParams& p, int per, int mt, bool down, bool lat) {
-  constexpr int warps = kMoeWarps;
-  p.bar_off = (uint32_t)(warps * p.depth * slot_bytes(mt));
-  p.cnt_off = p.bar_off + (uint32_t)(warps * p.depth * 8);
+// A column in shared memory: the fragments, then the zero-point terms, an odd number of 64-byte
+// units in all, so that the 64-byte reads of neighbouring columns meet different banks.
+__host__ __device__ inline uint32_t moe_column_bytes(int64_t K) {
+  return (uint32_t)((moe_groups(K) * 128 + moe_zs_pitch(K) * 4 + 127) / 128 * 128 + 64);
+}
+
+// Shared-memory layout: rings (1024-byte aligned), barriers (the rings', then the columns'),
+// lists, the latency form's exchange buffer -- gate/up, the accumulators of the K parts (one
+// 16-byte word per thread, two rounds); down, the slots' sums of every K part, their powers of
+// two, weights and whether they count -- and the columns: gtiles tiles of them (latency form,
+// down: every slot's).
+__host__ inline uint32_t moe_layout(MoeParams& p, int mt, bool down, bool lat) {
+  p.bar_off = (uint32_t)(kMoeWarps * p.depth * slot_bytes(mt));
+  p.cnt_off = p.bar_off + (uint32_t)(kMoeWarps * p.depth * 8 + 8);
   p.wcnt_off = p.cnt_off + (p.slots <= 32 ? 0u : (uint32_t)p.E * 4);
-  p.tiles_off = (p.wcnt_off + (p.slots <= 32 ? 0u : (uint32_t)(warps * p.E + 4)) + 7) / 8 * 8;
-  p.order_off = p.tiles_off + (uint32_t)moe_max_tiles(p.slots, p.E, per) * 8;
+  p.tiles_off = (p.wcnt_off + (p.slots <= 32 ? 0u : (uint32_t)(kMoeWarps * p.E + 4)) + 7) / 8 * 8;
+  p.order_off = p.tiles_off + (uint32_t)moe_max_tiles(p.slots, p.E, p.per) * 8;
   p.misc_off = p.order_off + (uint32_t)p.slots * 4;
   p.sum_off = (p.misc_off + 16 + 15) / 16 * 16;
-  p.frag_off = p.sum_off + (lat ? (down ? (uint32_t)(kMaxParts * p.slots * 64) : (uint32_t)(2 * 32 * warps * 16)) : 0u);
-  p.frag_pitch = 0;
-  if (!(lat && down)) return p.frag_off;
-  // h of every slot: fragments (64 bytes of padding put two columns' 64-byte reads on
-  // different banks), zero-point terms, one power of two; the slot's weight and whether it counts
-  p.frag_pitch = (uint32_t)(moe_groups(p.F) * 128 + 64);
-  return p.frag_off + (uint32_t)p.slots * (p.frag_pitch + (uint32_t)moe_zs_pitch(p.F) * 4 + 12);
+  uint32_t at = p.sum_off;
+  if (lat) at += down ? (uint32_t)(p.slots * (kMaxParts * 64 + 12)) : (uint32_t)(2 * 32 * kMoeWarps * 16);
+  p.col_off = (at + 127) / 128 * 128;
+  return p.col_off + (uint32_t)(down && lat ? p.slots : p.gtiles * p.per) * p.col_bytes;
 }
 
 // kDown false: gate/up units, h written; true: down units, y (latency) or part written.
 template <int NT, int MT, bool kDown, bool kLat>
 __global__ void __launch_bounds__(32 * kMoeWarps, 1)
 q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  constexpr int kPer = 8 * NT, kRows = 8 * MT, kWarps = kMoeWarps, kThreads = 32 * kWarps;
+  constexpr int kRows = 8 * MT, kWarps = kMoeWarps, kThreads = 32 * kWarps;
+  const int kPer = p.per;
+  const uint32_t col_bar = sbase + p.bar_off + 8u * (uint32_t)(kWarps * p.depth);
   constexpr uint32_t kSlot = slot_bytes(MT);
   MoeLists L;
   L.cnt = reinterpret_cast<int*>(smem + p.cnt_off);
@@ -631,11 +646,12 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   const int g = lane >> 2, c = lane & 3;
   if (lane == 0) {   // a warp's barriers are its own
     for (int i = 0; i < p.depth; ++i) mbar_init(sbase + p.bar_off + 8u * (uint32_t)(warp * p.depth + i), 1);
-    fence_mbar_init();
-    if (warp == 0) {
+    if (warp == 0) {   // (the columns' barrier: every warp's, behind the lists' CTA barriers)
+      mbar_init(col_bar, 1);
       *abort_flag = 0;
       prefetch_tmap(&tm);
     }
+    fence_mbar_init();
   }
   __syncwarp();
   // Order of the chain: the gate/up kernel waits for everything before it, then lets the
@@ -674,15 +690,36 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   const int wpr = kWarps >> kps;                   // items per round of the warps
   const int wnum = warp >> kps, kpart = warp & (kp - 1);
   const int sb0 = (nsb * kpart) >> kps, sb1 = (nsb * (kpart + 1)) >> kps;
+  // The numbers are worked off in groups of gtiles tiles, whose columns lie in shared memory
+  // together: group by group, numbers group start + wnum, + wpr, ...
+  const int tile_a = !kOwn && nu > 0 ? u0 / nu : 0;
+  auto group_end = [&](int tile0) { return tile0 + p.gtiles < ntiles && (tile0 + p.gtiles) * nu < u1 ? (tile0 + p.gtiles) * nu : u1; };
   // The items of this warp, in order: a position that steps without divisions.
   struct Pos {
-    int tile, unit, left;   // left: numbers to the end of the range (kOwn: units to its end)
+    int tile, unit, left;   // left: more than 0 while inside the range (kOwn: units to its end)
+    int tile0, gend;        // the group's first tile and end
+  };
+  // moves q from number u of its group on to the first one that is this warp's
+  auto settle = [&](Pos& q, int u) {
+    while (u >= q.gend && q.gend < u1) {
+      q.tile0 += p.gtiles;
+      u = q.gend + wnum;
+      q.gend = group_end(q.tile0);
+      q.tile = q.tile0;
+      q.unit = u - q.tile * nu;
+    }
+    q.left = wnum < wpr ? (u < u1 ? u1 - u : 0) : 0;
+    if (q.left > 0)
+      while (q.unit >= nu) {
+        q.unit -= nu;
+        ++q.tile;
+      }
   };
   auto start = [&]() -> Pos {
-    if constexpr (kOwn) return {wnum, u0, wnum < ntiles && wnum < wpr ? u1 - u0 : 0};
-    const int u = u0 + wnum;
-    const int tile = nu > 0 ? u / nu : 0;
-    return {tile, u - tile * nu, wnum < wpr ? u1 - u : 0};
+    if constexpr (kOwn) return {wnum, u0, wnum < ntiles && wnum < wpr ? u1 - u0 : 0, 0, 0};
+    Pos q{tile_a, u0 + wnum - tile_a * nu, 0, tile_a, group_end(tile_a)};
+    if (u0 < u1) settle(q, u0 + wnum);
+    return q;
   };
   auto step = [&](Pos& q) {
     if constexpr (kOwn) {
@@ -693,12 +730,8 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         --q.left;
       }
     } else {
-      q.left -= wpr;
       q.unit += wpr;
-      while (q.unit >= nu) {
-        q.unit -= nu;
-        ++q.tile;
-      }
+      settle(q, u1 - q.left + wpr);
     }
   };
   uint8_t* ring = smem + (size_t)(warp * p.depth) * kSlot;
@@ -742,7 +775,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   float* wsm = nullptr;   // kOwn: the slots' weights, and which of them count
   int* von = nullptr;
   if constexpr (kOwn) {
-    wsm = reinterpret_cast<float*>(smem + p.frag_off + p.slots * (p.frag_pitch + (uint32_t)moe_zs_pitch(K) * 4 + 4));
+    wsm = reinterpret_cast<float*>(smem + p.sum_off) + p.slots * (kMaxParts * 16 + 1);
     von = reinterpret_cast<int*>(wsm + p.slots);
     if ((int)threadIdx.x < p.slots) {
       const int id = p.ids[threadIdx.x];
@@ -752,23 +785,40 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   }
   const Pos first_item = start();
   if (first_item.left > 0) for_scale_lines(first_item, [&](const uint8_t* a) { prefetch_l2(a); });
-  // The B columns: x of a token (gate/up) or h of a slot (down), fragments, terms and powers.
+  // The B columns: x of a token (gate/up) or h of a slot (down): fragments, terms and powers.
   const uint8_t* frag = kDown ? p.hf : p.xf;
   const float* zero = kDown ? p.hz : p.zs;
   const float* power = kDown ? p.hft : p.ft;
-  const int64_t fpitch = kOwn ? (int64_t)p.frag_pitch : (int64_t)groups * 128, zpitch = moe_zs_pitch(K);
+  const uint32_t fbytes = (uint32_t)groups * 128u, zbytes = (uint32_t)moe_zs_pitch(K) * 4u;
+  uint8_t* cols = smem + p.col_off;
   if constexpr (kDown) pdl_wait_previous();
   if constexpr (kOwn) {   // a warp per slot converts h
-    float* zsm = reinterpret_cast<float*>(smem + p.frag_off + p.slots * p.frag_pitch);
-    float* fsm = zsm + p.slots * zpitch;
-    for (int s = warp; s < p.slots; s += kWarps)
-      moe_prep_slot<32, 3>(p.h + (int64_t)s * K, K, smem + p.frag_off + s * p.frag_pitch, zsm + s * zpitch, fsm + s,
-                           nullptr);
-    frag = smem + p.frag_off;
-    zero = zsm;
+    float* fsm = reinterpret_cast<float*>(smem + p.sum_off) + p.slots * kMaxParts * 16;
+    for (int s = warp; s < p.slots; s += kWarps) {
+      uint8_t* at = cols + s * p.col_bytes;
+      moe_prep_slot<32, 3>(p.h + (int64_t)s * K, K, at, reinterpret_cast<float*>(at + fbytes), fsm + s, nullptr);
+    }
     power = fsm;
     __syncthreads();
   }
+  // warp 0: the columns of the tiles from tile0 to the one of number gend - 1, tile after tile
+  auto stage_columns = [&](int tile0, int gend) {
+    const int last = (gend - 1) / nu;
+    int n = 0;
+    for (int t = tile0; t <= last; ++t) n += L.tiles[t].y >> 16;
+    if (lane == 0) mbar_expect_tx(col_bar, (uint32_t)n * (fbytes + zbytes));
+    __syncwarp();
+    for (int t = tile0; t <= last; ++t) {
+      const int2 tl = L.tiles[t];
+      if (lane < (tl.y >> 16)) {
+        const int o = L.order[(tl.y & 0xFFFF) + lane];
+        const int64_t src = kDown ? o & 0xFFFF : o >> 16;
+        const uint32_t dst = smem_u32(cols) + (uint32_t)((t - tile0) * kPer + lane) * p.col_bytes;
+        bulk_g2s(dst, frag + src * fbytes, fbytes, col_bar);
+        bulk_g2s(dst + fbytes, reinterpret_cast<const uint8_t*>(zero) + src * zbytes, zbytes, col_bar);
+      }
+    }
+  };
 
   bool ok = true;
   int slot = 0;
@@ -779,7 +829,6 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
 #pragma unroll
   for (int gl = 0; gl < 4; ++gl)
     off[gl] = (uint32_t)r * 128u + (((((uint32_t)(2 * gl + (c >> 1))) ^ (uint32_t)r) << 4) | (uint32_t)((c & 1) << 3));
-  int last_tile = -1;
   // products of an item over this warp's K part; next: the item after it
   auto compute = [&](const Pos& q, const Pos& next, float (&acc)[MT][NT][4], int& first, int& count) {
     const int2 tl = L.tiles[q.tile];
@@ -796,39 +845,23 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       un.s0[m] = scales + (q0 < last_row ? q0 : last_row) * grow;
       un.s1[m] = scales + (q1 < last_row ? q1 : last_row) * grow;
     }
-    // empty columns take the tile's first slot; their results are dropped
-    auto column = [&](int i) {   // slot (down) or token of column i
-      const int o = L.order[first + (i < count ? i : 0)];
-      return kDown ? o & 0xFFFF : o >> 16;
+    // empty columns take the tile's first one; their results are dropped
+    const uint8_t* tcols = cols + (kOwn ? 0u : (uint32_t)((q.tile - q.tile0) * kPer) * p.col_bytes);
+    auto column = [&](int i) -> const uint8_t* {
+      const int k = i < count ? i : 0;
+      return tcols + (uint32_t)(kOwn ? L.order[first + k] & 0xFFFF : k) * p.col_bytes;
     };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      un.b[n] = frag + column(8 * n + g) * fpitch + 16 * c;
-      un.z[n][0] = zero + column(8 * n + 2 * c) * zpitch;
-      un.z[n][1] = zero + column(8 * n + 2 * c + 1) * zpitch;
+      un.b[n] = column(8 * n + g) + 16 * c;
+      un.z[n][0] = reinterpret_cast<const float*>(column(8 * n + 2 * c) + fbytes);
+      un.z[n][1] = reinterpret_cast<const float*>(column(8 * n + 2 * c + 1) + fbytes);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-    // One touch of every line that the loops below read beside the ring -- the scales of the
-    // unit's rows and, of a new tile, the columns' K range -- all in flight together: they are
-    // then found in L1 (a warp would otherwise wait for L2 or memory at every group).  The next
-    // unit's scales start on their way to L2.
-    {
-      uint32_t touch = 0;
-      for_scale_lines(q, [&](const uint8_t* a) { touch |= ld_global_u32(a); });
-      if (!kOwn && q.tile != last_tile) {
-        const int cols = count < kPer ? count : kPer;
-        for (int i = 0; i < cols; ++i) {
-          const uint8_t* a = frag + column(i) * fpitch;
-          for (int G = 4 * sb0 + lane; G < 4 * sb1 && G < groups; G += 32) touch |= ld_global_u32(a + (int64_t)G * 128);
-        }
-      }
-      last_tile = q.tile;
-      asm volatile("" ::"r"(touch));
-      if (next.left > 0) for_scale_lines(next, [&](const uint8_t* a) { prefetch_l2(a); });
-    }
+    if (next.left > 0) for_scale_lines(next, [&](const uint8_t* a) { prefetch_l2(a); });   // the next unit's scales
     for (int sb = sb0; sb < sb1; ++sb) {
       // every lane polls: one instruction for the warp, and no exchange of the answer
       if (ok && !mbar_try_wait(bars + 8u * (uint32_t)slot, phase))
@@ -848,12 +881,24 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
     }
   };
 
+  // The columns of the group at hand (not kOwn): staged once all warps are past the one before.
+  int group = 0;
+  auto enter_group = [&](int tile0, int gend) {
+    if (group > 0) __syncthreads();
+    if (warp == 0) stage_columns(tile0, gend);
+    if (ok) ok = warp_wait(col_bar, (uint32_t)(group & 1), abort_flag, &g_moe_status);
+    ++group;
+  };
   Pos pos = start();
   if constexpr (!kDown) {
     int parity = 0;
+    int tile0 = tile_a, gstart = u0;
+    while (gstart < u1) {
+    const int gend = group_end(tile0);
+    enter_group(tile0, gend);
     // with K parts, all warps pass the same rounds (they meet to join their sums)
-    for (int base = u0; base < u1; base += wpr) {
-      const bool have = pos.left > 0;
+    for (int base = gstart; base < gend; base += wpr) {
+      const bool have = pos.left > 0 && pos.tile0 == tile0;
       if (kp == 1 && !have) break;
       const Pos q = pos;
       if (have) step(pos);
@@ -898,6 +943,9 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         }
       }
     }
+    gstart = gend;
+    tile0 += p.gtiles;
+    }
   } else {
     auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit) {
 #pragma unroll
@@ -925,13 +973,16 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       }
     };
     if constexpr (!kLat) {
-      while (pos.left > 0) {
-        const Pos q = pos;
-        step(pos);
-        float acc[MT][NT][4];
-        int first, count;
-        compute(q, pos, acc, first, count);
-        if (ok) store(acc, first, count, q.unit);
+      for (int tile0 = tile_a, gstart = u0; gstart < u1; gstart = group_end(tile0), tile0 += p.gtiles) {
+        enter_group(tile0, group_end(tile0));
+        while (pos.left > 0 && pos.tile0 == tile0) {
+          const Pos q = pos;
+          step(pos);
+          float acc[MT][NT][4];
+          int first, count;
+          compute(q, pos, acc, first, count);
+          if (ok) store(acc, first, count, q.unit);
+        }
       }
     } else {
       const int tokens = p.slots / p.k;
@@ -968,6 +1019,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       }
     }
   }
+  if (!ok && threadIdx.x == 0 && group > 0) mbar_drain(col_bar, (uint32_t)((group - 1) & 1));
   if (!ok && lane == 0)   // aborted: let the copies already issued land before the CTA exits
     for (int64_t d = issued > p.depth ? issued - p.depth : 0; d < issued; ++d)
       mbar_drain(bars + 8u * (uint32_t)(d % p.depth), (uint32_t)((d / p.depth) & 1));
@@ -1029,9 +1081,8 @@ int moe_sm_count() {
   return n;
 }
 
-// Dynamic shared memory at most: what is left of the SM's 256 KB is the L1 that the B columns
-// and scales are found in.
-constexpr uint32_t kMoeSmem = 150 * 1024;
+// Dynamic shared memory at most; what is left of the SM's 256 KB is the L1 of the scales.
+constexpr uint32_t kMoeSmem = 208 * 1024;
 
 // (the down product of the throughput form starts after the conversion kernel, whose early
 // launch lets it begin before the gate/up product is complete: it reads h and what follows from
@@ -1043,21 +1094,48 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
     if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, MT, kDown, kLat>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kMoeSmem),
+                                        (int)kMoeSmem),
                    "moe: cudaFuncSetAttribute"))
       return Q4LIN_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
   }
+  // Columns of one or two tiles beside rings of two slots per warp; then as many slots (up to
+  // four) as there is room for.  Long columns: fewer per tile.
   MoeParams p = p0;
-  p.depth = 4;
-  uint32_t bytes = moe_layout(p, 8 * NT, MT, kDown, kLat);
-  while (p.depth > 2 && bytes + 1024 > kMoeSmem) {
-    --p.depth;
-    bytes = moe_layout(p, 8 * NT, MT, kDown, kLat);
+  p.col_bytes = moe_column_bytes(kDown ? p.F : p.H);
+  p.per = 8 * NT;
+  p.depth = 2;
+  p.gtiles = kDown && kLat ? 1 : 2;
+  uint32_t bytes = moe_layout(p, MT, kDown, kLat);
+  if (bytes > kMoeSmem && p.gtiles > 1) {
+    p.gtiles = 1;
+    bytes = moe_layout(p, MT, kDown, kLat);
   }
-  if (bytes + 1024 > kMoeSmem) {
-    set_error_detail("moe: the slot lists do not fit shared memory");
+  while (bytes > kMoeSmem && p.per > 1) {
+    --p.per;
+    bytes = moe_layout(p, MT, kDown, kLat);
+  }
+  if (bytes > kMoeSmem) {
+    set_error_detail("moe: a column of this length does not fit shared memory beside the rings");
     return Q4LIN_ERR_UNSUPPORTED_SHAPE;
+  }
+  while (p.depth < 4) {
+    MoeParams q = p;
+    ++q.depth;
+    const uint32_t more = moe_layout(q, MT, kDown, kLat);
+    if (more > kMoeSmem) break;
+    p = q;
+    bytes = more;
+  }
+  if (!(kDown && kLat)) {   // more tiles together, where they are short
+    while (p.gtiles < 8) {
+      MoeParams q = p;
+      ++q.gtiles;
+      const uint32_t more = moe_layout(q, MT, kDown, kLat);
+      if (more > kMoeSmem) break;
+      p = q;
+      bytes = more;
+    }
   }
   int grid = sms;
   if (kDown && kLat) {   // whole units
@@ -1070,7 +1148,7 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(32 * kMoeWarps, 1, 1);
-  cfg.dynamicSmemBytes = bytes + 1024;
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
@@ -1087,7 +1165,7 @@ int moe_kernel_form(bool lat, int nt, const CUtensorMap& tm, const MoeParams& p,
 
 // The latency form holds every slot's h in shared memory beside the rings.
 bool moe_latency_form(int slots, int64_t F) {
-  return slots <= kLatSlots && (int64_t)slots * (moe_groups(F) * 128 + 64 + moe_zs_pitch(F) * 4 + 4) <= 48 * 1024;
+  return slots <= kLatSlots && (int64_t)slots * moe_column_bytes(F) <= 64 * 1024;
 }
 
 // Workspace parts of one pass, each 256-byte aligned.
