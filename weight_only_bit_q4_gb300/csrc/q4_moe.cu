@@ -894,57 +894,57 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
     int parity = 0;
     int tile0 = tile_a, gstart = u0;
     while (gstart < u1) {
-    const int gend = group_end(tile0);
-    enter_group(tile0, gend);
-    // with K parts, all warps pass the same rounds (they meet to join their sums)
-    for (int base = gstart; base < gend; base += wpr) {
-      const bool have = pos.left > 0 && pos.tile0 == tile0;
-      if (kp == 1 && !have) break;
-      const Pos q = pos;
-      if (have) step(pos);
-      float acc[MT][NT][4];
-      int first = 0, count = 0;
-      if (have) compute(q, pos, acc, first, count);
-      if constexpr (kLat) {
-        if (kp > 1) {   // part 0 adds the others' accumulators, in order
-          float4* ex = reinterpret_cast<float4*>(sums) + parity * kThreads;
-          parity ^= 1;
-          if (have && kpart > 0) ex[threadIdx.x] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][0][2], acc[0][0][3]);
-          __syncthreads();
-          if (!have || kpart > 0) continue;
-          for (int i = 1; i < kp; ++i) {
-            const float4 v = ex[threadIdx.x + 32 * i];
-            acc[0][0][0] += v.x;
-            acc[0][0][1] += v.y;
-            acc[0][0][2] += v.z;
-            acc[0][0][3] += v.w;
+      const int gend = group_end(tile0);
+      enter_group(tile0, gend);
+      // with K parts, all warps pass the same rounds (they meet to join their sums)
+      for (int base = gstart; base < gend; base += wpr) {
+        const bool have = pos.left > 0 && pos.tile0 == tile0;
+        if (kp == 1 && !have) break;
+        const Pos q = pos;
+        if (have) step(pos);
+        float acc[MT][NT][4];
+        int first = 0, count = 0;
+        if (have) compute(q, pos, acc, first, count);
+        if constexpr (kLat) {
+          if (kp > 1) {   // part 0 adds the others' accumulators, in order
+            float4* ex = reinterpret_cast<float4*>(sums) + parity * kThreads;
+            parity ^= 1;
+            if (have && kpart > 0) ex[threadIdx.x] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][0][2], acc[0][0][3]);
+            __syncthreads();
+            if (!have || kpart > 0) continue;
+            for (int i = 1; i < kp; ++i) {
+              const float4 v = ex[threadIdx.x + 32 * i];
+              acc[0][0][0] += v.x;
+              acc[0][0][1] += v.y;
+              acc[0][0][2] += v.z;
+              acc[0][0][3] += v.w;
+            }
+          }
+        }
+        if (!ok) continue;
+        // thread (g, c) holds gate and up of row f of token columns 2c, 2c + 1
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (NT > 1 && 8 * n >= count) break;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int col = 8 * n + 2 * c + j;
+            if (col >= count) continue;
+            const int o = L.order[first + col];
+            const float F = power[o >> 16];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const int64_t f = kRows * (int64_t)q.unit + 8 * m;
+              if (f >= p.F) continue;
+              const float gt = F * acc[m][n][j], up = F * acc[m][n][2 + j];
+              const float h = gt / (1.f + expf(-gt)) * up;
+              p.h[(int64_t)(o & 0xFFFF) * p.F + f + r] = h;
+            }
           }
         }
       }
-      if (!ok) continue;
-      // thread (g, c) holds gate and up of row f of token columns 2c, 2c + 1
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (NT > 1 && 8 * n >= count) break;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = 8 * n + 2 * c + j;
-          if (col >= count) continue;
-          const int o = L.order[first + col];
-          const float F = power[o >> 16];
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const int64_t f = kRows * (int64_t)q.unit + 8 * m;
-            if (f >= p.F) continue;
-            const float gt = F * acc[m][n][j], up = F * acc[m][n][2 + j];
-            const float h = gt / (1.f + expf(-gt)) * up;
-            p.h[(int64_t)(o & 0xFFFF) * p.F + f + r] = h;
-          }
-        }
-      }
-    }
-    gstart = gend;
-    tile0 += p.gtiles;
+      gstart = gend;
+      tile0 += p.gtiles;
     }
   } else {
     auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit) {
@@ -1103,7 +1103,7 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   // four) as there is room for.  Long columns: fewer per tile.
   MoeParams p = p0;
   p.col_bytes = moe_column_bytes(kDown ? p.F : p.H);
-  p.per = 8 * NT;
+  p.per = 8 * NT < p.slots / p.k ? 8 * NT : p.slots / p.k;   // (an expert gets a token once, as a rule)
   p.depth = 2;
   p.gtiles = kDown && kLat ? 1 : 2;
   uint32_t bytes = moe_layout(p, MT, kDown, kLat);
