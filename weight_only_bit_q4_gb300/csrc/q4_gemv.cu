@@ -406,7 +406,7 @@ q4_gemv_stream_kernel(const uint8_t* __restrict__ wq, const uint16_t* __restrict
         bulk_prefetch_l2(B, (uint32_t)(nrow * lo.R * 2 < 262144 ? nrow * lo.R * 2 : 262144));
       pdl_wait_previous();   // u
       if (ad >= 0) {
-        for (int r = lane; r < lo.R; r += 32) us[r] = lora_u(lo, 1, 0, r);
+        for (int r = lane; r < lo.R; r += 32) us[r] = lora_u<24>(lo, 1, 0, r);
         __syncwarp();
         for (int row = lane; row < nrow; row += 32) {
           float v = 0.f;

@@ -21,7 +21,9 @@ struct LoraArgs {
   const int32_t* ranks;   // [L] or NULL (R); clamped to [0, R]
   float* u;               // [ks, T, R] partial sums of A x along K, already scaled
   int L, R, ks;
+  void* tiles;            // tile route: lora_records(T, L) records of kLoraTileBytes; else NULL
 };
+constexpr int kLoraTileBytes = 48;
 
 struct LinearArgs {
   const uint8_t* wq;
@@ -50,6 +52,7 @@ struct LinearArgs {
 // The adapters' two products beside the projection (q4_lora.cu).
 int lora_splits(int64_t K, int64_t T, int64_t L);
 int64_t lora_shrink_grid(const LoraArgs& lo, int64_t T);   // CTAs
+int64_t lora_records(int64_t T, int64_t L);
 int64_t lora_delta_pitch(int64_t N);                        // floats per token row of delta
 int lora_shrink_launch(const LoraArgs& lo, const uint16_t* x, int64_t K, int64_t T, cudaStream_t stream);
 int lora_expand_launch(const LoraArgs& lo, float* delta, int64_t N, int64_t T, cudaStream_t stream);

@@ -28,26 +28,23 @@ q4_lora_shrink_kernel(const LoraArgs lo, const uint16_t* x, int64_t K, int64_t T
 // rows at a time as four MMA column tiles whose columns are dealt so that a thread ends with
 // 8 consecutive rows of a token: column g of tile i is weight row 8 (g / 2) + 2 i + g % 2.
 constexpr int kExpandThreads = 256;
-constexpr int kExpandTokens = 16;
+constexpr int kExpandTokens = kShrinkTokens;
 constexpr int kExpandPitch = kLoraMaxRank / 2 + 4;   // 32-bit words per token
 
-__global__ void __launch_bounds__(kExpandThreads)
-q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N, int64_t T, int rows) {
-  __shared__ LoraLists L;
+__global__ void __launch_bounds__(kExpandThreads, 3)   // three CTAs per SM: one wave, mostly
+q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N, int64_t T, int rows, int tiles) {
   __shared__ __align__(16) uint32_t uh[kExpandTokens * kExpandPitch], ul[kExpandTokens * kExpandPitch];   // bf16 pairs
-  // The shrink kernel lets this one launch after its own wait: everything but u is final, so
-  // the lists are built and the first rows of B fetched while it works.  The tile kernel
-  // launches next, under the same promise.
+  // (The tile kernel launches next: the shrink kernel let this one launch after its own wait, so
+  // everything but u, the tile records and delta is final by then.)
   pdl_launch_dependents();
+  pdl_wait_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int n0 = (int)(T < kLoraChunk ? T : kLoraChunk);
-  const int tiles = lora_max_tiles(n0, kExpandTokens, lo.L);
-  const int64_t chunk = blockIdx.x / tiles;
-  const int tile = (int)(blockIdx.x - chunk * tiles);
-  const int64_t t0 = chunk * kLoraChunk;
-  lora_build_lists<true>(lo, t0, (int)(T - t0 < kLoraChunk ? T - t0 : kLoraChunk), kExpandTokens, L);
-  if (tile >= L.ntiles) return;
-  const int a = L.adapter[tile], rank = L.rank[tile], first = L.first[tile], count = L.count[tile];
+  const LoraTile* rec = static_cast<const LoraTile*>(lo.tiles) + blockIdx.x;
+  const uint4 head = ld_global_u4(rec);
+  const int a = (int)head.x, rank = (int)head.y, count = (int)head.z;
+  if (a < 0) return;
+  const int64_t t0 = (int64_t)(blockIdx.x / tiles) * kLoraChunk;
+  const short* order = rec->order;
   const int64_t nb = (int64_t)blockIdx.y * rows;
   const uint16_t* B = lo.b + (int64_t)(a == kNoAdapter ? 0 : a) * N * lo.R;
   const int row_g = 8 * (g >> 1) + (g & 1);   // + 2 i: the weight row of column g of tile i
@@ -93,7 +90,6 @@ q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N,
   for (int q = 0; q < 4; ++q) {
     if (narrow ? q * kStride < rows : 16 * q < rank) load_b(narrow ? n1 + q * kStride : n1, narrow ? 0 : 16 * q, b[q]);
   }
-  pdl_wait_previous();
   const int words = (rank + 15) / 16 * 8;   // whole steps of 16 ranks
   for (int e = threadIdx.x; e < kExpandTokens * words; e += kExpandThreads) {
     const int col = e / words, w = e - col * words;
@@ -102,7 +98,7 @@ q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N,
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = 2 * w + j;
-        const float v = r < rank ? lora_u(lo, T, t0 + L.order[first + col], r) : 0.f;
+        const float v = r < rank ? lora_u(lo, T, t0 + order[col], r) : 0.f;
         const uint32_t hi = float_to_bf16_bits(v);
         const float rest = v - __uint_as_float(hi << 16);
         h |= hi << (16 * j);
@@ -120,7 +116,7 @@ q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N,
     for (int j = 0; j < 2; ++j) {
       const int col = g + 8 * j;
       if (col < count && n0r + 8 * c < pitch) {
-        float4* o = reinterpret_cast<float4*>(delta + (t0 + L.order[first + col]) * pitch + n0r + 8 * c);
+        float4* o = reinterpret_cast<float4*>(delta + (t0 + order[col]) * pitch + n0r + 8 * c);
         o[0] = make_float4(d[0][2 * j], d[0][2 * j + 1], d[1][2 * j], d[1][2 * j + 1]);
         o[1] = make_float4(d[2][2 * j], d[2][2 * j + 1], d[3][2 * j], d[3][2 * j + 1]);
       }
@@ -172,18 +168,23 @@ cudaLaunchConfig_t pdl_config(dim3 grid, unsigned threads, cudaStream_t stream, 
 }  // namespace
 
 // K shares of the shrink product: at most as many as keep a share at 256 K values (one step per
-// warp), and no more CTAs than about two per SM if every tile that the tokens may make is there.
+// warp), and about one CTA per SM for the tiles that the tokens are likely to make (each sorts its chunk first).  With more
+// than 32 tokens at most 8: the expand kernel's every CTA adds the shares of its tokens.
 int lora_splits(int64_t K, int64_t T, int64_t L) {
-  LoraArgs one{};
-  one.L = (int)L;
-  one.ks = 1;
+  const int64_t n0 = T < kLoraChunk ? T : kLoraChunk, chunks = (T + kLoraChunk - 1) / kLoraChunk;
+  const int64_t likely = chunks * (n0 / kShrinkTokens + ((L + 1 < n0 ? L + 1 : n0) + 1) / 2);
   int64_t ks = (K + 255) / 256;
-  const int64_t most = 304 / lora_shrink_blocks(one, T);
+  const int64_t most = 168 / likely;
   if (ks > most) ks = most;
+  if (T > 32 && ks > 8) ks = 8;
   return (int)(ks < 1 ? 1 : ks);
 }
 
 int64_t lora_shrink_grid(const LoraArgs& lo, int64_t T) { return lora_shrink_blocks(lo, T); }
+
+int64_t lora_records(int64_t T, int64_t L) {
+  return (T + kLoraChunk - 1) / kLoraChunk * lora_max_tiles((int)(T < kLoraChunk ? T : kLoraChunk), kShrinkTokens, L);
+}
 
 int64_t lora_delta_pitch(int64_t N) { return (N + 7) / 8 * 8; }
 
@@ -195,13 +196,14 @@ int lora_shrink_launch(const LoraArgs& lo, const uint16_t* x, int64_t K, int64_t
 
 int lora_expand_launch(const LoraArgs& lo, float* delta, int64_t N, int64_t T, cudaStream_t stream) {
   const int n0 = (int)(T < kLoraChunk ? T : kLoraChunk);
-  const int64_t tiles = (T + kLoraChunk - 1) / kLoraChunk * lora_max_tiles(n0, kExpandTokens, lo.L);
+  const int64_t tiles = lora_records(T, lo.L);
   // a warp's 32 rows per CTA where that fills the GPU about once, else four times as many
   const int rows = tiles * ((N + 255) / 256) <= 608 ? 256 : 1024;
   cudaLaunchAttribute at[1];
   const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)tiles, (unsigned)((N + rows - 1) / rows), 1), kExpandThreads,
                                             stream, at);
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_lora_expand_kernel, lo, delta, lora_delta_pitch(N), N, T, rows),
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_lora_expand_kernel, lo, delta, lora_delta_pitch(N), N, T, rows,
+                                       lora_max_tiles(n0, kExpandTokens, lo.L)),
                     "lora: expand kernel launch");
 }
 

@@ -37,18 +37,19 @@ __device__ __forceinline__ int lora_adapter(const LoraArgs& lo, int64_t t, int* 
   return r > 0 ? a : -1;
 }
 
-// sum over the K partials, in order; eight loads in flight (one after the other they cost the
+// sum over the K partials, in order; kAhead loads in flight (one after the other they cost the
 // reader a trip to L2 each)
+template <int kAhead = 8>
 __device__ __forceinline__ float lora_u(const LoraArgs& lo, int64_t T, int64_t t, int r) {
   const float* at = lo.u + t * lo.R + r;
   const int64_t step = T * lo.R;
   float v = 0.f;
-  for (int s = 0; s < lo.ks; s += 8) {
-    float f[8];
+  for (int s = 0; s < lo.ks; s += kAhead) {
+    float f[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = s + i < lo.ks ? __uint_as_float(ld_global_u32(at + (s + i) * step)) : 0.f;
+    for (int i = 0; i < kAhead; ++i) f[i] = s + i < lo.ks ? __uint_as_float(ld_global_u32(at + (s + i) * step)) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += f[i];
+    for (int i = 0; i < kAhead; ++i) v += f[i];
   }
   return v;
 }
@@ -87,7 +88,7 @@ __device__ __forceinline__ void lora_mma(float (&d)[4], uint32_t a0, uint32_t a1
 constexpr int kLoraChunk = 128;
 
 struct LoraLists {
-  int ids[kLoraChunk];        // adapter of every token (kNoAdapter: none), then sorted
+  __align__(16) int ids[kLoraChunk];   // adapter of every token (kNoAdapter: none); then tile numbers
   short order[kLoraChunk];    // token numbers in the chunk, by adapter
   int adapter[kLoraChunk];    // per tile
   short rank[kLoraChunk];
@@ -97,9 +98,8 @@ struct LoraLists {
 };
 constexpr int kNoAdapter = 0x7FFFFFFF;
 
-// All threads of a CTA of at least kLoraChunk threads; ends with a barrier.  kNone: tokens
-// without an adapter get tiles too (adapter kNoAdapter, the last ones).
-template <bool kNone>
+// All threads of a CTA of at least kLoraChunk threads; ends with a barrier.  Tokens without an
+// adapter get tiles too (adapter kNoAdapter, the last ones).
 __device__ __forceinline__ void lora_build_lists(const LoraArgs& lo, int64_t t0, int n, int per, LoraLists& L) {
   const int i = threadIdx.x;
   int id = kNoAdapter, rank = 0;
@@ -112,7 +112,7 @@ __device__ __forceinline__ void lora_build_lists(const LoraArgs& lo, int64_t t0,
       const unsigned live = n < 32 ? (1u << n) - 1u : 0xffffffffu;
       const unsigned same = __match_any_sync(0xffffffffu, id) & live;
       const int before = __popc(same & ((1u << i) - 1u)), equal = __popc(same);
-      const bool on = i < n && (kNone || id != kNoAdapter), lead = on && before == 0;
+      const bool on = i < n, lead = on && before == 0;
       const unsigned none = __ballot_sync(0xffffffffu, i < n && id == kNoAdapter);
       const unsigned leads = __ballot_sync(0xffffffffu, lead && id != kNoAdapter);
       // sorted position and tile number of the adapter's first token: sums over the leads before it
@@ -136,7 +136,7 @@ __device__ __forceinline__ void lora_build_lists(const LoraArgs& lo, int64_t t0,
       // tiles: those of the adapters, then of the tokens without one
       int total = 0;
       for (unsigned m = leads; m; m &= m - 1u) total += (__shfl_sync(0xffffffffu, equal, __ffs(m) - 1) + per - 1) / per;
-      if (kNone) total += (__popc(none) + per - 1) / per;
+      total += (__popc(none) + per - 1) / per;
       if (i == 0) L.ntiles = total;
     }
     __syncthreads();
@@ -146,11 +146,17 @@ __device__ __forceinline__ void lora_build_lists(const LoraArgs& lo, int64_t t0,
   __syncthreads();
   int less = 0, before = 0, equal = 0;
   if (i < n) {
-    for (int j = 0; j < n; ++j) {
-      const int o = L.ids[j];
-      less += o < id;
-      equal += o == id;
-      before += o == id && j < i;
+    const int4* ids = reinterpret_cast<const int4*>(L.ids);
+    for (int j = 0; j < n; j += 4) {   // (places past n hold kNoAdapter and count for nothing below)
+      const int4 o4 = ids[j / 4];
+      const int o[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bool same = o[q] == id && j + q < n;
+        less += o[q] < id;
+        equal += same;
+        before += same && j + q < i;
+      }
     }
   }
   // tile heads, numbered in sorted order
@@ -158,7 +164,7 @@ __device__ __forceinline__ void lora_build_lists(const LoraArgs& lo, int64_t t0,
   __syncthreads();
   if (i < kLoraChunk) L.ids[i] = 0;
   __syncthreads();
-  const bool head = i < n && before % per == 0 && (kNone || id != kNoAdapter);
+  const bool head = i < n && before % per == 0;
   if (i < n) L.order[pos] = (short)i;
   if (head) L.ids[pos] = 1;
   __syncthreads();
@@ -283,6 +289,14 @@ __host__ __device__ inline int lora_max_tiles(int n, int per, int64_t L) {
   return (int)(some < n ? some : n);
 }
 
+// What the expand kernel needs to know of a tile, left by the shrink kernel (lo.tiles): adapter
+// (kNoAdapter: tokens without one; -1: no such tile), rank, tokens, and their numbers in the chunk.
+struct __align__(16) LoraTile {
+  int adapter, rank, count, pad;
+  short order[kShrinkTokens];
+};
+static_assert(kLoraTileBytes == sizeof(LoraTile), "workspace of the tile records");
+
 // One CTA of the shrink product: number q of lora_shrink_blocks().
 __device__ __forceinline__ void lora_shrink_block(const LoraArgs& lo, const uint16_t* x, int64_t K, int64_t T, int64_t q,
                                                   LoraLists& L, float* red) {
@@ -293,8 +307,19 @@ __device__ __forceinline__ void lora_shrink_block(const LoraArgs& lo, const uint
   const int tile = (int)(q / lo.ks - chunk * tiles);
   const int64_t t0 = chunk * kLoraChunk;
   const int n = (int)(T - t0 < kLoraChunk ? T - t0 : kLoraChunk);
-  lora_build_lists<false>(lo, t0, n, kShrinkTokens, L);
-  if (tile < L.ntiles) lora_shrink_tile(lo, x, K, T, t0, tile, split, L, red);
+  lora_build_lists(lo, t0, n, kShrinkTokens, L);
+  const bool there = tile < L.ntiles;
+  if (lo.tiles != nullptr && split == 0 && threadIdx.x < kShrinkTokens) {
+    LoraTile* rec = static_cast<LoraTile*>(lo.tiles) + chunk * tiles + tile;
+    const int count = there ? L.count[tile] : 0;
+    rec->order[threadIdx.x] = (int)threadIdx.x < count ? L.order[L.first[tile] + threadIdx.x] : (short)0;
+    if (threadIdx.x == 0) {
+      rec->adapter = there ? L.adapter[tile] : -1;
+      rec->rank = there ? L.rank[tile] : 0;
+      rec->count = count;
+    }
+  }
+  if (there && L.adapter[tile] != kNoAdapter) lora_shrink_tile(lo, x, K, T, t0, tile, split, L, red);
 }
 
 __host__ inline int64_t lora_shrink_blocks(const LoraArgs& lo, int64_t T) {

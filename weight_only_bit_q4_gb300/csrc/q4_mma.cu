@@ -706,7 +706,7 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
     named_bar_sync(kRedBar, (uint32_t)(WC * 32));
     if (b == 0) pdl_wait_previous();  // the exponents are the prep kernel's; every earlier kernel is done
     if constexpr (kLora) {
-      if (b == 0) {  // u, adapter and rank of every token
+      if (b == 0) {
         float* us = reinterpret_cast<float*>(smem + p.lora_off);
         int* ad = reinterpret_cast<int*>(us + 8 * NT * p.lora.R);
         for (int t = wc * 32 + lane; t < p.tp; t += WC * 32) {
@@ -716,8 +716,7 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
         }
         for (int e = wc * 32 + lane; e < p.tp * p.lora.R; e += WC * 32) {
           const int t = e / p.lora.R;
-          int rank = 0;   // (u of a token without an adapter is not written)
-          us[e] = lora_adapter(p.lora, t, &rank) >= 0 ? lora_u(p.lora, p.tp, t, e - t * p.lora.R) : 0.f;
+          us[e] = lora_u<24>(p.lora, p.tp, t, e - t * p.lora.R);
         }
         named_bar_sync(kRedBar, (uint32_t)(WC * 32));
       }

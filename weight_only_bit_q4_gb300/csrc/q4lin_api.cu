@@ -347,6 +347,8 @@ size_t lora_u_bytes(int64_t K, int64_t T, int64_t L, int64_t R) {
   return round256((size_t)q4::lora_splits(K, T, L) * (size_t)T * (size_t)R * 4);
 }
 
+size_t lora_record_bytes(int64_t T, int64_t L) { return round256((size_t)q4::lora_records(T, L) * q4::kLoraTileBytes); }
+
 int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const uint16_t* lora_a, const uint16_t* lora_b,
              const int32_t* ids, const float* lora_scales, const int32_t* ranks, uint16_t* y, int64_t N, int64_t K,
              int64_t T, int64_t L, int64_t R, void* workspace, void* stream) {
@@ -364,15 +366,17 @@ int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const
   if ((st = check_device()) != Q4LIN_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t ub = lora_u_bytes(K, T, L, R);
+  // workspace: u, then (tile route) the tile records and delta, or the operand pass's buffers
+  const size_t rb = route == Q4LIN_ROUTE_TC_SPLITK ? lora_record_bytes(T, L) : 0;
   const q4::LoraArgs lo{lora_a, lora_b, ids, lora_scales, ranks, reinterpret_cast<float*>(ws), (int)L, (int)R,
-                        q4::lora_splits(K, T, L)};
+                        q4::lora_splits(K, T, L), rb > 0 ? ws + ub : nullptr};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   q4::LinearArgs a{wq, scales, x, y, N, K, T, ws + ub, s};
   a.lora = &lo;
   if (route == Q4LIN_ROUTE_STREAM_MMA) return q4::mma_launch(a);
   if ((st = q4::lora_shrink_launch(lo, x, K, T, s)) != Q4LIN_OK) return st;
   if (route == Q4LIN_ROUTE_GEMV) return q4::gemv_lora_launch(a);
-  float* delta = reinterpret_cast<float*>(ws + ub);
+  float* delta = reinterpret_cast<float*>(ws + ub + rb);
   if ((st = q4::lora_expand_launch(lo, delta, N, T, s)) != Q4LIN_OK) return st;
   a.workspace = nullptr;
   a.delta = delta;
@@ -453,7 +457,7 @@ size_t q4lin_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int64_t L, in
   switch (lora_route(N, K, T, (int)R)) {
     case Q4LIN_ROUTE_GEMV: return ub;
     case Q4LIN_ROUTE_STREAM_MMA: return ub + round256(q4::mma_lora_workspace_bytes(N, K, T, (int)R));
-    case Q4LIN_ROUTE_TC_SPLITK: return ub + round256((size_t)T * (size_t)q4::lora_delta_pitch(N) * 4);
+    case Q4LIN_ROUTE_TC_SPLITK: return ub + lora_record_bytes(T, L) + round256((size_t)T * (size_t)q4::lora_delta_pitch(N) * 4);
     default: return 0;
   }
 }
