@@ -7,7 +7,8 @@
 //             W_up, e = ids[t, j], silu(z) = z / (1 + e^-z);
 //   down      y[t, n] = bf16( sum_j p[t, j] sum_f W_down[e, n, f] h[t, j, f] ).
 //
-// Three kernels chained by programmatic dependent launch.  Bound: the packed weights of
+// The router (with the conversion of x beside it), gate/up, down and, for more slots, a sum
+// over the choices: kernels chained by programmatic dependent launch.  Bound: the packed weights of
 // the experts that some token chose, each read once; the kernels below therefore sort
 // the (token, choice) slots by expert and stream each chosen expert's rows once for all
 // of its tokens (tiles of up to 8 NT token columns).
@@ -37,8 +38,10 @@
 // 8 MT rows x 256 weights, TMA) each, and works through its own sequence of (unit,
 // sub-box): lane 0 refills a slot as soon as the warp has read it, across unit borders, so
 // no warp waits for another.  The columns of a CTA's next few tiles lie in shared memory
-// beside the rings (bulk copies); read through L1 instead they cost the whole layer 15 us of
-// 103 at 64 tokens x 8 of 128 experts.
+// beside the rings; read through L1 instead they cost the whole layer 12 us of
+// 103 at 64 tokens x 8 of 128 experts.  Gate/up copies what the operand pass has converted
+// (bulk copies; plain loads by all warps spill and cost 9 us there); down converts h itself, in
+// every CTA that needs the slot (a conversion kernel between the products took 3.6 us of 90.7).
 //
 // Two forms, by the number of slots S = T top_k of a pass:
 //   S <= kLatSlots: latency.  MT = 1, the K range of a unit shared by up to 4 warps (partial
@@ -47,9 +50,9 @@
 //     of 8 warps fits beside the gate/up CTA and starts early, but both then spill and run at
 //     half speed: one token of 8 of 64 experts took 25.8 us against 22.2.)
 //   otherwise: throughput.  MT = 2 (each B fragment feeds
-//     two MMA row tiles); the (tile, unit) pairs are dealt evenly over all CTAs, a kernel
-//     between the two products converts h, the slots' sums of the down product go to the
-//     workspace and a last kernel adds them in the order of the choices.
+//     two MMA row tiles); the (tile, unit) pairs are dealt evenly over all CTAs, the slots'
+//     sums of the down product go to the workspace and a last kernel adds them in the order of
+//     the choices.
 //
 // Every mbarrier wait is bounded (kSpinLimit): on expiry the kernel records
 // Q4LIN_ERR_TIMEOUT, the warps stop computing, pass the CTA barriers and drain the
@@ -152,11 +155,11 @@ __device__ __forceinline__ void moe_prep_token(const uint16_t* x, int64_t H, uin
   if (tid == 0) *ft = exp2i(24 + e);
 }
 
-// The same of one slot's h (FP32, F values), by kLanes adjacent lanes of a warp or a whole CTA
-// of kLanes threads (`share`: its exchange buffer).  Up to 8 kRuns kLanes values are read once
+// The same of one slot's h (FP32, F values), by one warp.  Up to 256 kRuns values are read once
 // and held in registers between the maximum and the conversion.
-template <int kLanes, int kRuns>
-__device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf, float* zs, float* ft, uint32_t* share) {
+template <int kRuns>
+__device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf, float* zs, float* ft) {
+  constexpr int kLanes = 32;
   const int lane = threadIdx.x % kLanes;
   const int nv = F / 8, nv64 = (F + 63) / 64 * 8;
   float4 keep[kRuns][2];
@@ -184,12 +187,6 @@ __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf
     magnitude(v);
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
-  if constexpr (kLanes > 32) {
-    if ((threadIdx.x & 31) == 0) share[threadIdx.x >> 5] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kLanes / 32; ++w) mx = max(mx, share[w]);
-  }
   const int E = (int)(mx >> 23);
   const int e = (mx == 0 || E == 255) ? 0 : min(max(E - 141, -100), 100);
   const float s1 = exp2i(-e), s16 = exp2i(-e - 4);
@@ -378,9 +375,6 @@ struct MoeParams {
   const uint16_t* s_gu;    // [E, 2F, Hp/64]
   const uint16_t* s_dn;    // [E, H, Fp/64]
   float* h;                // [T k][F]
-  uint8_t* hf;             // throughput form: h as fragments, terms and powers (like xf, zs, ft)
-  float* hz;
-  float* hft;
   float* part;             // throughput form: [T k][H] sums of the down product
   uint16_t* y;             // [T, H]
   int64_t H, F;
@@ -389,7 +383,7 @@ struct MoeParams {
   int per;                 // columns per tile, at most (8 NT, fewer where a column is long)
   int gtiles;              // tiles whose columns lie in shared memory together
   uint32_t col_bytes;      // shared memory of a column
-  uint32_t bar_off, cnt_off, wcnt_off, order_off, tiles_off, misc_off, sum_off, col_off;   // shared memory
+  uint32_t bar_off, cnt_off, wcnt_off, order_off, tiles_off, misc_off, pow_off, sum_off, col_off;   // shared memory
 };
 
 // Shared-memory lists of one CTA: the tiles (up to 8 kMaxNT slots of one expert) in
@@ -606,8 +600,8 @@ __host__ __device__ inline uint32_t moe_column_bytes(int64_t K) {
   return (uint32_t)((moe_groups(K) * 128 + moe_zs_pitch(K) * 4 + 127) / 128 * 128 + 64);
 }
 
-// Shared-memory layout: rings (1024-byte aligned), barriers (the rings', then the columns'),
-// lists, the latency form's exchange buffer -- gate/up, the accumulators of the K parts (one
+// Shared-memory layout: rings (1024-byte aligned) and their barriers, lists, the columns'
+// powers of two, the latency form's exchange buffer -- gate/up, the accumulators of the K parts (one
 // 16-byte word per thread, two rounds); down, the slots' sums of every K part, their powers of
 // two, weights and whether they count -- and the columns: gtiles tiles of them (latency form,
 // down: every slot's).
@@ -618,7 +612,8 @@ __host__ inline uint32_t moe_layout(MoeParams& p, int mt, bool down, bool lat) {
   p.tiles_off = (p.wcnt_off + (p.slots <= 32 ? 0u : (uint32_t)(kMoeWarps * p.E + 4)) + 7) / 8 * 8;
   p.order_off = p.tiles_off + (uint32_t)moe_max_tiles(p.slots, p.E, p.per) * 8;
   p.misc_off = p.order_off + (uint32_t)p.slots * 4;
-  p.sum_off = (p.misc_off + 16 + 15) / 16 * 16;
+  p.pow_off = p.misc_off + 16;
+  p.sum_off = (p.pow_off + (uint32_t)(p.gtiles * p.per) * 4 + 15) / 16 * 16;
   uint32_t at = p.sum_off;
   if (lat) at += down ? (uint32_t)(p.slots * (kMaxParts * 64 + 12)) : (uint32_t)(2 * 32 * kMoeWarps * 16);
   p.col_off = (at + 127) / 128 * 128;
@@ -786,9 +781,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   const Pos first_item = start();
   if (first_item.left > 0) for_scale_lines(first_item, [&](const uint8_t* a) { prefetch_l2(a); });
   // The B columns: x of a token (gate/up) or h of a slot (down): fragments, terms and powers.
-  const uint8_t* frag = kDown ? p.hf : p.xf;
-  const float* zero = kDown ? p.hz : p.zs;
-  const float* power = kDown ? p.hft : p.ft;
+  const float* power = p.ft;   // (down: set below)
   const uint32_t fbytes = (uint32_t)groups * 128u, zbytes = (uint32_t)moe_zs_pitch(K) * 4u;
   uint8_t* cols = smem + p.col_off;
   if constexpr (kDown) pdl_wait_previous();
@@ -796,26 +789,43 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
     float* fsm = reinterpret_cast<float*>(smem + p.sum_off) + p.slots * kMaxParts * 16;
     for (int s = warp; s < p.slots; s += kWarps) {
       uint8_t* at = cols + s * p.col_bytes;
-      moe_prep_slot<32, 3>(p.h + (int64_t)s * K, K, at, reinterpret_cast<float*>(at + fbytes), fsm + s, nullptr);
+      moe_prep_slot<3>(p.h + (int64_t)s * K, K, at, reinterpret_cast<float*>(at + fbytes), fsm + s);
     }
     power = fsm;
     __syncthreads();
   }
-  // warp 0: the columns of the tiles from tile0 to the one of number gend - 1, tile after tile
+  // The columns of the tiles from tile0 to the one of number gend - 1, tile after tile.  Gate/up:
+  // bulk copies by warp 0 of what the operand pass has converted.  Down: a warp per column
+  // converts h, in every CTA that needs the slot.
+  float* cpow = reinterpret_cast<float*>(smem + p.pow_off);   // down: the columns' powers
   auto stage_columns = [&](int tile0, int gend) {
     const int last = (gend - 1) / nu;
-    int n = 0;
-    for (int t = tile0; t <= last; ++t) n += L.tiles[t].y >> 16;
-    if (lane == 0) mbar_expect_tx(col_bar, (uint32_t)n * (fbytes + zbytes));
-    __syncwarp();
-    for (int t = tile0; t <= last; ++t) {
-      const int2 tl = L.tiles[t];
-      if (lane < (tl.y >> 16)) {
-        const int o = L.order[(tl.y & 0xFFFF) + lane];
-        const int64_t src = kDown ? o & 0xFFFF : o >> 16;
-        const uint32_t dst = smem_u32(cols) + (uint32_t)((t - tile0) * kPer + lane) * p.col_bytes;
-        bulk_g2s(dst, frag + src * fbytes, fbytes, col_bar);
-        bulk_g2s(dst + fbytes, reinterpret_cast<const uint8_t*>(zero) + src * zbytes, zbytes, col_bar);
+    if constexpr (kDown) {
+      int before = 0;
+      for (int t = tile0; t <= last; ++t) {
+        const int2 tl = L.tiles[t];
+        const int count = tl.y >> 16;
+        for (int i = (warp - before) & (kWarps - 1); i < count; i += kWarps) {
+          const int at = (t - tile0) * kPer + i;
+          uint8_t* dst = cols + at * p.col_bytes;
+          moe_prep_slot<3>(p.h + (int64_t)(L.order[(tl.y & 0xFFFF) + i] & 0xFFFF) * K, K, dst,
+                           reinterpret_cast<float*>(dst + fbytes), cpow + at);
+        }
+        before += count;
+      }
+    } else {
+      int n = 0;
+      for (int t = tile0; t <= last; ++t) n += L.tiles[t].y >> 16;
+      if (lane == 0) mbar_expect_tx(col_bar, (uint32_t)n * (fbytes + zbytes));
+      __syncwarp();
+      for (int t = tile0; t <= last; ++t) {
+        const int2 tl = L.tiles[t];
+        if (lane < (tl.y >> 16)) {
+          const int64_t src = L.order[(tl.y & 0xFFFF) + lane] >> 16;
+          const uint32_t dst = smem_u32(cols) + (uint32_t)((t - tile0) * kPer + lane) * p.col_bytes;
+          bulk_g2s(dst, p.xf + src * fbytes, fbytes, col_bar);
+          bulk_g2s(dst + fbytes, reinterpret_cast<const uint8_t*>(p.zs) + src * zbytes, zbytes, col_bar);
+        }
       }
     }
   };
@@ -885,8 +895,13 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   int group = 0;
   auto enter_group = [&](int tile0, int gend) {
     if (group > 0) __syncthreads();
-    if (warp == 0) stage_columns(tile0, gend);
-    if (ok) ok = warp_wait(col_bar, (uint32_t)(group & 1), abort_flag, &g_moe_status);
+    if constexpr (kDown) {
+      stage_columns(tile0, gend);
+      __syncthreads();
+    } else {
+      if (warp == 0) stage_columns(tile0, gend);
+      if (ok) ok = warp_wait(col_bar, (uint32_t)(group & 1), abort_flag, &g_moe_status);
+    }
     ++group;
   };
   Pos pos = start();
@@ -947,7 +962,8 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       tile0 += p.gtiles;
     }
   } else {
-    auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit) {
+    // pcol: the tile's first staged column
+    auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit, int pcol) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (NT > 1 && 8 * n >= count) break;
@@ -956,7 +972,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
           const int col = 8 * n + 2 * c + j;
           if (col >= count) continue;
           const int s = L.order[first + col] & 0xFFFF;
-          const float F = power[s];
+          const float F = kOwn ? power[s] : cpow[pcol + col];
           if constexpr (kLat) {
             sums[(kpart * p.slots + s) * 16 + r] = F * acc[0][n][j];
             sums[(kpart * p.slots + s) * 16 + 8 + r] = F * acc[0][n][2 + j];
@@ -981,7 +997,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
           float acc[MT][NT][4];
           int first, count;
           compute(q, pos, acc, first, count);
-          if (ok) store(acc, first, count, q.unit);
+          if (ok) store(acc, first, count, q.unit, (q.tile - q.tile0) * kPer);
         }
       }
     } else {
@@ -993,7 +1009,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
           float acc[MT][NT][4];
           int first, count;
           compute(q, pos, acc, first, count);
-          if (ok) store(acc, first, count, unit);
+          if (ok) store(acc, first, count, unit, 0);
         }
         __syncthreads();
         if (!*abort_flag) {   // y of the unit's rows: the slots' sums in the order of the choices
@@ -1019,24 +1035,12 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       }
     }
   }
-  if (!ok && threadIdx.x == 0 && group > 0) mbar_drain(col_bar, (uint32_t)((group - 1) & 1));
+  if constexpr (!kDown) {
+    if (!ok && threadIdx.x == 0 && group > 0) mbar_drain(col_bar, (uint32_t)((group - 1) & 1));
+  }
   if (!ok && lane == 0)   // aborted: let the copies already issued land before the CTA exits
     for (int64_t d = issued > p.depth ? issued - p.depth : 0; d < issued; ++d)
       mbar_drain(bars + 8u * (uint32_t)(d % p.depth), (uint32_t)((d / p.depth) & 1));
-}
-
-// Throughput form, between the products: a CTA per slot converts h.
-constexpr int kConvertThreads = 128;
-
-__global__ void __launch_bounds__(kConvertThreads) q4_moe_convert_kernel(const MoeParams p) {
-  __shared__ uint32_t share[kConvertThreads / 32];
-  pdl_launch_dependents();
-  const int s = (int)blockIdx.x;
-  const int id = (int)ld_global_u32(p.ids + s);   // (the gate/up kernel launches this one after its own wait)
-  pdl_wait_previous();
-  if (id < 0 || id >= p.E) return;                // its h was not written
-  moe_prep_slot<kConvertThreads, 2>(p.h + (int64_t)s * p.F, (int)p.F, p.hf + s * moe_groups(p.F) * 128,
-                                    p.hz + s * moe_zs_pitch(p.F), p.hft + s, share);
 }
 
 // Throughput form, after the down product: y[t, n] = sum_j p[t, j] part[t k + j, n] in the order
@@ -1084,9 +1088,6 @@ int moe_sm_count() {
 // Dynamic shared memory at most; what is left of the SM's 256 KB is the L1 of the scales.
 constexpr uint32_t kMoeSmem = 208 * 1024;
 
-// (the down product of the throughput form starts after the conversion kernel, whose early
-// launch lets it begin before the gate/up product is complete: it reads h and what follows from
-// it only after its wait, and everything else it reads is final by then)
 template <int NT, int MT, bool kDown, bool kLat>
 int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaStream_t stream) {
   static bool attr[64] = {};
@@ -1170,7 +1171,7 @@ bool moe_latency_form(int slots, int64_t F) {
 
 // Workspace parts of one pass, each 256-byte aligned.
 struct MoeWs {
-  size_t xf, zs, ft, h, hf, hz, hft, part, total;
+  size_t xf, zs, ft, h, part, total;
 };
 
 MoeWs moe_ws(int tokens, int64_t H, int64_t F, int k) {
@@ -1182,10 +1183,7 @@ MoeWs moe_ws(int tokens, int64_t H, int64_t F, int k) {
   w.zs = w.xf + up((size_t)tokens * (size_t)moe_groups(H) * 128);
   w.ft = w.zs + up((size_t)tokens * (size_t)moe_zs_pitch(H) * 4);
   w.h = w.ft + up((size_t)tokens * 4);
-  w.hf = w.h + up(S * (size_t)F * 4);
-  w.hz = w.hf + (lat ? 0 : up(S * (size_t)moe_groups(F) * 128));
-  w.hft = w.hz + (lat ? 0 : up(S * (size_t)moe_zs_pitch(F) * 4));
-  w.part = w.hft + (lat ? 0 : up(S * 4));
+  w.part = w.h + up(S * (size_t)F * 4);
   w.total = w.part + (lat ? 0 : up(S * (size_t)H * 4));
   return w;
 }
@@ -1297,9 +1295,6 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
     p.s_gu = a.s_gu;
     p.s_dn = a.s_dn;
     p.h = reinterpret_cast<float*>(ws + w.h);
-    p.hf = ws + w.hf;
-    p.hz = reinterpret_cast<float*>(ws + w.hz);
-    p.hft = reinterpret_cast<float*>(ws + w.hft);
     p.part = reinterpret_cast<float*>(ws + w.part);
     p.y = a.y + t0 * a.H;
     p.H = a.H;
@@ -1310,11 +1305,6 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
     // token tiles handled together: two where an expert gets more than a few slots on average
     const int nt = (int64_t)tp * a.k > 6 * a.E ? 2 : 1;
     if (const int rc = moe_kernel_form<false>(lat, nt, gu, p, sms, a.stream)) return rc;
-    if (!lat) {
-      cudaLaunchAttribute at[1];
-      const cudaLaunchConfig_t cfg = moe_config((unsigned)p.slots, kConvertThreads, a.stream, at);
-      if (cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_convert_kernel, p), "moe: conversion launch")) return Q4LIN_ERR_CUDA;
-    }
     if (const int rc = moe_kernel_form<true>(lat, nt, dn, p, sms, a.stream)) return rc;
     if (!lat) {
       cudaLaunchAttribute at[1];
