@@ -258,8 +258,10 @@ int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t*
  *
  * Experts:  y[t] = bf16( sum_j weights[t, j] W_down,e (silu(W_gate,e x[t]) * (W_up,e x[t])) ),
  * e = ids[t, j], summed over j in order; a choice whose id lies outside [0, E) adds nothing
- * (a token without any gives +0).  All sums FP32; the intermediate vector enters W_down's
- * product as two bf16 terms (relative error 2^-17).
+ * (a token without any gives +0).  All sums FP32.  The intermediate vector of a choice enters
+ * W_down's product rounded once to fp16 at a power of two that puts its largest magnitude in
+ * [2^14, 2^15) (relative error 2^-11); x enters W_gate's and W_up's exactly down to 2^-27 of the
+ * token's largest magnitude, and below within 2^-35 of it.
  *   wq_gate_up uint8 [E, 2F, Hp/2], scales_gate_up fp16 [E, 2F, Hp/64]: per expert, gate
  *     rows [0, F), then up rows; wq_down uint8 [E, H, Fp/2], scales_down fp16 [E, H, Fp/64]
  *     (Hp, Fp: H, F rounded up to 128); y bf16 [T, H] (must not overlap x)
@@ -268,8 +270,9 @@ int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t*
  * Any T runs; the kernels are made for a few tokens (every expert that some token chose is
  * read once per pass of at most 512 / top_k tokens).  F == 0: y = +0.
  *
- * q4lin_moe is both in one call (three kernels): ids and weights are outputs.  All of its
- * arguments are checked before anything is launched.
+ * q4lin_moe is both in one call: ids and weights are outputs, and all of its arguments are
+ * checked before anything is launched.  Three kernels for a pass of up to 16 choices
+ * (T * top_k), four beyond; q4lin_moe_experts the same.
  */
 int q4lin_moe_router(const uint16_t* x, const uint16_t* w_router, const float* bias, int32_t* ids, float* weights,
                      int64_t T, int64_t H, int64_t E, int top_k, int renormalize, void* stream);

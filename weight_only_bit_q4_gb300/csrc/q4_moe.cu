@@ -19,8 +19,8 @@
 // per two weights.  B: the vector v as fp16 at a power of two 2^-e that puts its largest |v|
 // in [2^14, 2^15); D starts from the group's zero-point term -8 2^-24 sum v, and 2^(24 + e) is
 // undone on the FP32 sum.
-//   gate/up: v = x (bf16), exact down to 2^-32 of the largest |x| and within 2^-40 of it
-//     below: every product is exact.
+//   gate/up: v = x (bf16), exact down to 2^-27 of the largest |x| and within 2^-35 of it
+//     below (the odd nibbles' sixteenth costs four bits).
 //   down: v = h (FP32), rounded once to fp16 (relative error at most 2^-11, about 1.5e-4
 //     rms(y) in y, a tenth of y's own bf16 rounding; a bf16 h would put 1e-3 rms(y) there).
 //
@@ -77,7 +77,7 @@ constexpr int kMaxExperts = 1024;
 // ----------------------------------------------------------------- router
 constexpr int kRouteCluster = 8;
 constexpr int kRouteThreads = 512;
-constexpr int kRouteTokens = 4;   // tokens per cluster
+constexpr int kRouteMma = 4;      // tokens from which the products run on the tensor cores
 
 struct RouterParams {
   const uint16_t* x;      // [T, H]
@@ -226,6 +226,13 @@ __global__ void __launch_bounds__(256) q4_moe_prep_kernel(const RouterParams p) 
   moe_prep_at(p, blockIdx.x);
 }
 
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // The top_k of one token's logits (lg: `parts` sums of each expert, part after part), by one
 // warp.  kV: values per lane.  Each lane keeps its values as order-preserving integers (0: never
 // chosen -- -inf, NaN, what is already chosen) and its best one; a pick is a warp maximum of the
@@ -308,25 +315,37 @@ q4_moe_router_kernel(const RouterParams p) {
     if (t < p.prep_tokens) moe_prep_at(p, t);
     return;
   }
-  cluster_sync();   // every CTA of the cluster runs before its shared memory is written
-  pdl_wait_previous();
   constexpr int kWarps = kRouteThreads / 32;
   const int64_t nv = p.H / 8;
-  for (int w = warp * kRouteCluster + (int)rank; w < p.E * p.parts; w += kRouteCluster * kWarps) {
+  constexpr int kAhead = TT == 1 ? 4 : 2;   // loads of this many steps in flight
+  uint4 wv[kAhead];
+  auto load_w = [&](const uint16_t* wr, int64_t i, int64_t i1) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) wv[q] = i + 32 * q < i1 ? ld_global_u4(wr + 8 * (i + 32 * q)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  const int w0 = warp * kRouteCluster + (int)rank;
+  if (w0 < p.E * p.parts) {   // the weights are no kernel's output: the first of them come early
+    const int e = w0 / p.parts, part = w0 - e * p.parts;
+    load_w(p.w + (int64_t)e * p.H, nv * part / p.parts + lane, nv * (part + 1) / p.parts);
+  }
+  cluster_sync();   // every CTA of the cluster runs before its shared memory is written
+  pdl_wait_previous();
+  bool loaded = true;
+  for (int w = w0; w < p.E * p.parts; w += kRouteCluster * kWarps) {
     const int e = w / p.parts, part = w - e * p.parts;
     const int64_t i0 = nv * part / p.parts, i1 = nv * (part + 1) / p.parts;
     float acc[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = 0.f;
     const uint16_t* wr = p.w + (int64_t)e * p.H;
-    constexpr int kAhead = TT == 1 ? 4 : 2;   // loads of this many steps in flight
     for (int64_t i = i0 + lane; i < i1; i += 32 * kAhead) {
-      uint4 wv[kAhead], xv[kAhead][TT];
+      uint4 xv[kAhead][TT];
+      if (!loaded) load_w(wr, i, i1);
+      loaded = false;
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const bool in = i + 32 * q < i1;
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        wv[q] = in ? ld_global_u4(wr + 8 * (i + 32 * q)) : zero;
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           const int64_t tt = t0 + t < p.T ? t0 + t : p.T - 1;
@@ -363,6 +382,96 @@ q4_moe_router_kernel(const RouterParams p) {
   // ---- one warp per token: softmax statistics, then top_k picks
   if (p.E <= 128) moe_pick<4>(p, logit[warp], t0 + warp);   // (four values per lane, in registers)
   else moe_pick<kMaxExperts / 32>(p, logit[warp], t0 + warp);
+}
+
+// The same for more tokens, eight to a cluster, on the tensor cores: mma.sync m16n8k16
+// (bf16 x bf16 -> FP32) over tiles of 16 experts, the H of a tile shared by a CTA's 16 warps and,
+// with few tiles, by several CTAs.  K order inside an MMA is free: thread (g, c) takes the eight
+// values k = 8 c .. 8 c + 7 of every 32, of two experts' rows and of token g, one 16-byte load each
+// for two MMAs.  The warps' sums meet in shared memory, then in the CTA of the token's rank,
+// which picks.  Latency-bound: every load of a warp's share is in flight at once up to H = 2048.
+// The router alone, against FP32 FMAs of a
+// warp per expert for four tokens: 5.2 us for 9.8 (64 tokens, 128 experts, H = 2048), 4.5 for 6.7
+// (4 tokens); from four tokens on it never lost.
+__global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads, 2)
+q4_moe_router_mma_kernel(const RouterParams p) {
+  constexpr int kWarps = kRouteThreads / 32, kSteps = 4;
+  __shared__ float logit[kMaxExperts];
+  __shared__ __align__(16) float part_sum[kWarps][16][8];
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int rank = (int)cluster_ctarank();
+  const int64_t t0 = (int64_t)(blockIdx.x / kRouteCluster) * 8;
+  if ((int)blockIdx.x >= p.clusters * kRouteCluster) {   // whole clusters
+    pdl_wait_previous();
+    const int t = (int)blockIdx.x - p.clusters * kRouteCluster;
+    if (t < p.prep_tokens) moe_prep_at(p, t);
+    return;
+  }
+  const int units = (p.E + 15) / 16 * p.parts;
+  const int steps = (int)((p.H + 31) / 32), shares = p.parts * kWarps;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 w0[kSteps], w1[kSteps];
+  auto load_w = [&](int unit, int st, int end) {
+    const int e = unit / p.parts * 16 + g;   // (rows past E: the last one again, dropped below)
+    const uint16_t* r0 = p.w + (int64_t)(e < p.E ? e : p.E - 1) * p.H;
+    const uint16_t* r1 = p.w + (int64_t)(e + 8 < p.E ? e + 8 : p.E - 1) * p.H;
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int64_t k = 32 * (int64_t)(st + q) + 8 * c;
+      const bool in = st + q < end && k < p.H;
+      w0[q] = in ? ld_global_u4(r0 + k) : zero;
+      w1[q] = in ? ld_global_u4(r1 + k) : zero;
+    }
+  };
+  auto first_step = [&](int unit, int w) { return (int)((int64_t)steps * (unit % p.parts * kWarps + w) / shares); };
+  // the weights are no kernel's output: the first of them come early
+  if (rank < units) load_w(rank, first_step(rank, warp), first_step(rank, warp + 1));
+  cluster_sync();   // every CTA of the cluster runs before its shared memory is written
+  pdl_wait_previous();
+  const uint16_t* xr = p.x + (t0 + g < p.T ? t0 + g : p.T - 1) * p.H;
+  bool loaded = true;
+  for (int unit = rank; unit < units; unit += kRouteCluster) {
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    const int end = first_step(unit, warp + 1);
+    for (int st = first_step(unit, warp); st < end; st += kSteps) {
+      uint4 xv[kSteps];
+      if (!loaded) load_w(unit, st, end);
+      loaded = false;
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q) {
+        const int64_t k = 32 * (int64_t)(st + q) + 8 * c;
+        xv[q] = st + q < end && k < p.H ? ld_global_u4(xr + k) : zero;
+      }
+#pragma unroll
+      for (int q = 0; q < kSteps; ++q) {
+        mma_bf16_16816(d, w0[q].x, w1[q].x, w0[q].y, w1[q].y, xv[q].x, xv[q].y);
+        mma_bf16_16816(d, w0[q].z, w1[q].z, w0[q].w, w1[q].w, xv[q].z, xv[q].w);
+      }
+    }
+    loaded = false;
+    *reinterpret_cast<float2*>(&part_sum[warp][g][2 * c]) = make_float2(d[0], d[1]);
+    *reinterpret_cast<float2*>(&part_sum[warp][g + 8][2 * c]) = make_float2(d[2], d[3]);
+    __syncthreads();
+    if (threadIdx.x < 128) {
+      const int e = unit / p.parts * 16 + (int)(threadIdx.x >> 3), part = unit % p.parts, t = threadIdx.x & 7;
+      float v = p.bias != nullptr && part == 0 && e < p.E ? __uint_as_float(ld_global_u32(p.bias + e)) : 0.f;
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += part_sum[w][threadIdx.x >> 3][t];
+      v += sum;
+      if (e < p.E)
+        asm volatile("st.shared::cluster.f32 [%0], %1;"
+                     ::"r"(mapa_shared(smem_u32(&logit[part * p.E + e]), (uint32_t)t)), "f"(v)
+                     : "memory");
+    }
+    __syncthreads();
+  }
+  cluster_sync();
+  if (warp != 0 || t0 + rank >= p.T) return;
+  if (p.E <= 128) moe_pick<4>(p, logit, t0 + rank);
+  else moe_pick<kMaxExperts / 32>(p, logit, t0 + rank);
 }
 
 // ----------------------------------------------------------------- slots by expert
@@ -1226,10 +1335,12 @@ int moe_router_launch(const MoeArgs& a) {
   p.E = (int)a.E;
   p.k = a.k;
   p.renorm = a.renorm;
-  const int tt = a.T < kRouteTokens ? (a.T == 1 ? 1 : 2) : kRouteTokens;
+  const int tt = a.T < kRouteMma ? (a.T == 1 ? 1 : 2) : 8;   // tokens per cluster
   const int64_t clusters = (a.T + tt - 1) / tt;
   p.clusters = (int)clusters;
-  p.parts = a.E >= 128 ? 1 : (int)(128 / a.E);
+  const int tiles = (int)((a.E + 15) / 16);
+  if (tt == 8) p.parts = tiles >= kRouteCluster ? 1 : kRouteCluster / tiles;
+  else p.parts = a.E >= 128 ? 1 : (int)(128 / a.E);
   int64_t prep = 0;
   if (a.workspace != nullptr) {   // the whole layer: the experts' first operand pass beside the router
     const int tp = moe_pass_tokens(a.T, a.k);
@@ -1247,7 +1358,7 @@ int moe_router_launch(const MoeArgs& a) {
   switch (tt) {
     case 1: e = cudaLaunchKernelEx(&cfg, q4_moe_router_kernel<1>, p); break;
     case 2: e = cudaLaunchKernelEx(&cfg, q4_moe_router_kernel<2>, p); break;
-    default: e = cudaLaunchKernelEx(&cfg, q4_moe_router_kernel<kRouteTokens>, p); break;
+    default: e = cudaLaunchKernelEx(&cfg, q4_moe_router_mma_kernel, p); break;
   }
   return cuda_check(e, "moe: router kernel launch");
 }
