@@ -233,7 +233,8 @@ int q4lin_fused_route(int op, int64_t N, int64_t K, int64_t T);
  *   workspace       device, >= q4lin_lora_workspace_bytes(N, K, T, L, R), 256-byte aligned
  * A x is formed in FP32 from the bf16 values; up to 32 tokens the second product is FP32
  * too, beyond (the tile route) A x enters it as two bf16 terms (relative error 2^-17).
- * Two kernels up to 32 tokens, three or four beyond.  L == 0, R == 0: q4lin_linear alone
+ * Inf or NaN in an adapter's used ranks reach that adapter's tokens only.  Two kernels up to 32
+ * tokens, three or four beyond.  L == 0, R == 0: q4lin_linear alone
  * (with its workspace).  K == 0: y = +0.  q4lin_lora_route: the route the call takes (as
  * q4lin_select_route), -1 for sizes it refuses.
  */

@@ -44,9 +44,12 @@ struct LinearArgs {
   uint16_t* y_b = nullptr;
   int64_t n_b = 0;
   // LinearLora: the adapters (GEMV and warp-MMA routes apply them in their epilogues; on the
-  // tile route, mode 3, the accumulators start from the FP32 term delta [T, lora_delta_pitch(N)])
+  // tile route, mode 3, the accumulators start from the FP32 term delta [T, lora_delta_pitch(N)];
+  // mode 4: the second product as lora_groups further K groups over lora_u [T][lora_groups][64])
   const LoraArgs* lora = nullptr;
   const float* delta = nullptr;
+  const uint16_t* lora_u = nullptr;
+  int lora_groups = 0;
 };
 
 // The adapters' two products beside the projection (q4_lora.cu).
@@ -56,6 +59,8 @@ int64_t lora_records(int64_t T, int64_t L);
 int64_t lora_delta_pitch(int64_t N);                        // floats per token row of delta
 int lora_shrink_launch(const LoraArgs& lo, const uint16_t* x, int64_t K, int64_t T, cudaStream_t stream);
 int lora_expand_launch(const LoraArgs& lo, float* delta, int64_t N, int64_t T, cudaStream_t stream);
+int64_t lora_groups(int64_t K, int64_t L, int64_t R);       // 64-wide groups of u as bf16 terms; 0: delta instead
+int lora_spread_launch(const LoraArgs& lo, uint16_t* u, int groups, int64_t T, cudaStream_t stream);
 
 // The weight planes are stored for K rounded up to a multiple of 128
 // (linear-benchmark.md section 4, K_pad); columns k >= K are padding.

@@ -1,7 +1,9 @@
 // The two products of the low-rank adapters that run beside the shared projection: the
 // shrink kernel (u = A x, for the decode GEMV and the tile route; the streaming warp-MMA
-// route runs it inside its operand pass) and the expand kernel (the tile route's FP32 term
-// delta[t, n] = sum_r B_a[n, r] u[t, r], from which its accumulators start).
+// route runs it inside its operand pass) and, for the tile route, either the expand kernel (the
+// FP32 term delta[t, n] = sum_r B_a[n, r] u[t, r], from which its accumulators start) or, with
+// few adapters of low rank, the spread kernel (u as an operand of the tile kernel, which takes the
+// second product as a few more K groups).
 //
 // Bound: the adapters' rows.  A few tokens read each distinct adapter's A and B once
 // (2 rank (K + N) bytes); with many tokens the FP32 term, written and read once through
@@ -153,6 +155,38 @@ q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N,
   }
 }
 
+// u as the tile route's further groups read it: [T][groups][64] bf16, groups 2 b and 2 b + 1 the
+// terms hi and lo of columns 64 b .. 64 b + 63 of all adapters' ranks side by side; a token's own
+// adapter's columns hold u, the others zeros.  A thread writes 8 columns.
+constexpr int kSpreadThreads = 256;
+
+__global__ void __launch_bounds__(kSpreadThreads)
+q4_lora_spread_kernel(const LoraArgs lo, uint16_t* u, int groups, int64_t T) {
+  pdl_launch_dependents();   // (as the expand kernel: all but u is final by now)
+  pdl_wait_previous();
+  const int chunks = groups * 4;   // of 8 columns, per token
+  const int64_t i = (int64_t)blockIdx.x * kSpreadThreads + threadIdx.x;
+  const int64_t t = i / chunks;
+  if (t >= T) return;
+  const int q = (int)(i - t * chunks), a = 8 * q / lo.R, r0 = 8 * q - a * lo.R;
+  uint4 hi = make_uint4(0u, 0u, 0u, 0u), lw = hi;
+  if (a < lo.L && (int)ld_global_u32(lo.ids + t) == a) {
+    const int rank = lo.ranks == nullptr ? lo.R : min(max((int)ld_global_u32(lo.ranks + a), 0), lo.R);
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = r0 + j < rank ? lora_u(lo, T, t, r0 + j) : 0.f;
+      h[j] = float_to_bf16_bits(v);
+      l[j] = fabsf(v) < INFINITY ? float_to_bf16_bits(v - __uint_as_float(h[j] << 16)) : 0u;
+    }
+    hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    lw = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
+  }
+  uint4* o = reinterpret_cast<uint4*>(u + (t * groups + 2 * (q >> 3)) * 64) + (q & 7);
+  o[0] = hi;
+  o[8] = lw;
+}
+
 cudaLaunchConfig_t pdl_config(dim3 grid, unsigned threads, cudaStream_t stream, cudaLaunchAttribute* at) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -205,6 +239,25 @@ int lora_expand_launch(const LoraArgs& lo, float* delta, int64_t N, int64_t T, c
   return cuda_check(cudaLaunchKernelEx(&cfg, q4_lora_expand_kernel, lo, delta, lora_delta_pitch(N), N, T, rows,
                                        lora_max_tiles(n0, kExpandTokens, lo.L)),
                     "lora: expand kernel launch");
+}
+
+// The tile route's second product as further K groups, two per 64 ranks of all adapters together
+// (hi and lo).  Against delta it saves the FP32 term's way through memory and lets the tile kernel
+// start before u is complete, but multiplies every token by every adapter, and the groups' A
+// stages come by plain loads.  Measured (K = 5120): 2 groups always win (N = 6144: 26.0 us for
+// 31.6 at T = 40, 44.8 for 55.5 at 256, 110.5 for 118.1 at 1024), 4 do from K = 4096 on (29.6 for
+// 32.0, 48.5 for 56.3, 117.5 for 118.6; K = 2048: 20.4 for 19.5), 8 lose (35.0 for 31.9).
+int64_t lora_groups(int64_t K, int64_t L, int64_t R) {
+  const int64_t g = L <= 16 ? 2 * ((L * R + 63) / 64) : 8;   // (R is at least 8)
+  return g <= 2 || (g <= 4 && K >= 4096) ? g : 0;
+}
+
+int lora_spread_launch(const LoraArgs& lo, uint16_t* u, int groups, int64_t T, cudaStream_t stream) {
+  cudaLaunchAttribute at[1];
+  const int64_t n = T * groups * 4;
+  const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((n + kSpreadThreads - 1) / kSpreadThreads), 1, 1), kSpreadThreads,
+                                            stream, at);
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_lora_spread_kernel, lo, u, groups, T), "lora: spread kernel launch");
 }
 
 }  // namespace q4

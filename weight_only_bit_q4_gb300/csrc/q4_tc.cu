@@ -71,6 +71,7 @@
 #include <mutex>
 
 #include "q4_internal.h"
+#include "q4_lora.cuh"
 #include "q4_sm100.cuh"
 
 namespace q4 {
@@ -104,6 +105,11 @@ struct TcParams {
   uint16_t* y_b;
   int64_t n_b;
   const float* delta;
+  //   mode 4, LinearLora: the adapters' second product as `ug` further groups after the nk of the
+  //     planes, scale 1: X tile u (bf16 terms hi and lo alternating, map in the high-plane slot),
+  //     A tile 64 columns of the adapters' B side by side.
+  int ug;
+  LoraArgs lo;
 };
 
 // Named barrier of the accumulate warps for the SwiGLU exchange (after the issue ring and kAccBar).
@@ -249,6 +255,7 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
   const uint32_t fin_bar = done_bar + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
+  volatile int* b_flag = reinterpret_cast<volatile int*>(smem + L::misc_off + 8);   // mode 4: B holds Inf or NaN
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -269,21 +276,24 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
   // This CTA's share of the K groups (the whole K without a split).
   const int splitk = p.splitk;
   uint32_t crank = 0;
-  int g_begin = 0, g_end = p.nk;
+  const int groups = MODE == 4 ? p.nk + p.ug : p.nk;
+  int g_begin = 0, g_end = groups;
   if (splitk > 1) {
     crank = cluster_ctarank();
     // Q5's high plane holds 8 bytes per group: shares start on even groups so every
     // TMA x coordinate into it is a multiple of 16 bytes
     auto split_at = [&](uint32_t rk) {
-      if (rk >= (uint32_t)splitk) return p.nk;
-      const int g = (int)(((int64_t)p.nk * rk) / splitk);
+      if (rk >= (uint32_t)splitk) return groups;
+      const int g = (int)(((int64_t)groups * rk) / splitk);
       return kHB == 1 ? (g & ~1) : g;
     };
     g_begin = split_at(crank);
     g_end = split_at(crank + 1);
   }
   const int ng = g_end - g_begin;
-  const int nws = (ng + kGroupsPerW - 1) / kGroupsPerW;
+  // the share's groups that come from the planes (LinearLora, mode 4: the rest are the adapters')
+  const int np = MODE == 4 ? (g_end < p.nk ? ng : g_begin < p.nk ? p.nk - g_begin : 0) : ng;
+  const int nws = (np + kGroupsPerW - 1) / kGroupsPerW;
   const int red_rounds = splitk > 1 ? (splitk - 1 + L::kRedSlots - 1) / L::kRedSlots : 0;  // split-K reduction rounds
 
   if (threadIdx.x == 0) {
@@ -296,10 +306,11 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
     mbar_init(done_bar, kAccWarps);
     mbar_init(fin_bar, 1);  // the issuer's final commit
     *abort_flag = 0;
+    if constexpr (MODE == 4) *b_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_codes);
     prefetch_tmap(&tm_x);
-    if constexpr (kHB > 0 || MODE == 2) prefetch_tmap(&tm_high);
+    if constexpr (kHB > 0 || MODE == 2 || MODE == 4) prefetch_tmap(&tm_high);
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), L::tmem_cols);
   tc_fence_before();
@@ -307,8 +318,8 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   // before the first TMA load, scale load or output store (LinearLora: the kernels of this call
-  // before it launch it when everything but delta is final; only delta's readers wait)
-  if (MODE != 3 || warp >= 12) pdl_wait_previous();
+  // before it launch it when everything but delta or u is final; only their readers wait)
+  if (MODE < 3 || (MODE == 3 && warp >= 12)) pdl_wait_previous();
 
   if (wg == 0) {
     if constexpr (NACC == 4) setmaxnreg_dec<R::ctl>();
@@ -322,9 +333,15 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
         const int s = i % SX;
         if (i >= SX && !(ok = mbar_wait(mma_done(i - SX), ring_par(i - SX), abort_flag, &g_tc_status))) break;
         mbar_expect_tx(x_full(s), L::kB);
-        tma_load_2d(sbase + L::x_off + s * L::kB, &tm_x, x_full(s), (g_begin + i) * 64, (int32_t)t0);
+        if (MODE == 4 && i >= np) {
+          if (i == np) pdl_wait_previous();
+          tma_load_2d(sbase + L::x_off + s * L::kB, &tm_high, x_full(s), (g_begin + i - p.nk) * 64, (int32_t)t0);
+        } else {
+          tma_load_2d(sbase + L::x_off + s * L::kB, &tm_x, x_full(s), (g_begin + i) * 64, (int32_t)t0);
+        }
         last = i;
       }
+      if constexpr (MODE == 4) pdl_wait_previous();   // (no share without adapter groups ends before the kernels before it)
       if (!ok)  // let every copy already issued land before shared memory is released
         for (int i = (last - SX + 1 > 0 ? last - SX + 1 : 0); i <= last; ++i) mbar_drain(x_full(i % SX), (i / SX) & 1);
     } else if (warp == 1 && lane == 0) {
@@ -493,7 +510,7 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = ws * kGroupsPerW + team + 2 * h;
-        if (i >= ng) break;
+        if (i >= np) break;
         const int sa = i % SA;
         // the slot's previous group (i - SA, same team) must have been consumed by its MMA
         if (i >= SA) ok = ok && warp_wait(mma_done(i - SA), ring_par(i - SA), abort_flag, &g_tc_status);
@@ -571,6 +588,73 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
       if constexpr (kW8) {  // the team's chunks of this stage are read
         __syncwarp();
         if (lane == 0) mbar_arrive(c_empty(slot));
+      }
+    }
+    if constexpr (MODE == 4) {
+      // The adapters' groups: column 8 q of the stage (q = chunk number over all adapters) is rank
+      // 8 q mod R of adapter 8 q / R.  What lies past an adapter's rank is zero whatever bits it
+      // holds; Inf and NaN are zero too (they would reach the other adapters' tokens as 0 * Inf)
+      // and leave a mark: the epilogue then adds them to their own adapter's tokens.
+      const int R8 = p.lo.R;
+      bool bad = false;
+      auto trim = [&](uint32_t w, int left) -> uint32_t {   // left: ranks from this pair on
+        if (left < 2) w = left < 1 ? 0u : w & 0xFFFFu;
+        if ((w & 0x7F80u) == 0x7F80u) {
+          w &= 0xFFFF0000u;
+          bad = true;
+        }
+        if ((w & 0x7F800000u) == 0x7F800000u) {
+          w &= 0xFFFFu;
+          bad = true;
+        }
+        return w;
+      };
+      for (int i = np + ((np ^ team) & 1); i < ng; i += 2) {
+        const int sa = i % SA;
+        if (i >= SA) ok = ok && warp_wait(mma_done(i - SA), ring_par(i - SA), abort_flag, &g_tc_status);
+        if (ok) {
+          tc_fence_after();
+          const int q0 = ((g_begin + i - p.nk) >> 1) * 8;
+          constexpr int kAtOnce = L::kATmem ? 8 : 4;   // chunks in flight
+          uint32_t v[4 * kAtOnce];
+#pragma unroll
+          for (int j0 = 0; j0 < 8; j0 += kAtOnce) {
+            int left[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+              const int at = 8 * (q0 + j0 + j), a = at / R8, r0 = at - a * R8;
+              uint4 b = make_uint4(0u, 0u, 0u, 0u);
+              left[j] = 0;
+              if (drow_ok && a < p.lo.L) {
+                left[j] = (p.lo.ranks == nullptr ? R8 : (int)ld_global_u32(p.lo.ranks + a)) - r0;
+                b = ld_global_u4(p.lo.b + ((int64_t)a * p.N + drow) * R8 + r0);
+              }
+              v[4 * j] = b.x;
+              v[4 * j + 1] = b.y;
+              v[4 * j + 2] = b.z;
+              v[4 * j + 3] = b.w;
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[4 * j + k] = trim(v[4 * j + k], left[j] - 2 * k);
+              if constexpr (!L::kATmem)
+                st_shared_v4(sbase + L::a_off + sa * kABytes + r * 128 + (((j0 + j) ^ (r & 7)) << 4),
+                             make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+            }
+          }
+          if (bad) *b_flag = 1;
+          if constexpr (L::kATmem) {
+            tmem_st32(a_lane + (uint32_t)(sa * 32), v);
+            tmem_st_wait();
+          } else {
+            fence_proxy_async();
+          }
+        }
+        ok = ok && warp_wait(x_full(i % SX), (i / SX) & 1, abort_flag, &g_tc_status);
+        tc_fence_before();
+        __syncwarp();
+        named_bar_arrive(issue_bar(i), L::issue_threads);
       }
     }
     __syncwarp();
@@ -675,7 +759,7 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
       // 4-byte boundary); the next pair is fetched as soon as the current one is used.
       const uint32_t* srow = reinterpret_cast<const uint32_t*>(scl + (row_ok ? row : 0) * (p.Kp >> 6));
       int pcur = g_begin >> 1;
-      uint32_t s_cur = row_ok ? __ldg(srow + pcur) : 0u;
+      uint32_t s_cur = row_ok && (MODE != 4 || 2 * pcur < p.nk) ? __ldg(srow + pcur) : 0u;
       uint32_t s_nxt = (row_ok && 2 * (pcur + 1) < p.nk) ? __ldg(srow + pcur + 1) : 0u;
       // the first NB groups find their accumulator buffers free
       for (int i = 0; i < NB && i < ng; ++i) named_bar_arrive(issue_bar(i), L::issue_threads);
@@ -686,7 +770,8 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
           s_cur = s_nxt;
           s_nxt = (row_ok && 2 * (pcur + 1) < p.nk) ? __ldg(srow + pcur + 1) : 0u;
         }
-        const float sf = fp16_bits_to_float((uint16_t)((ga & 1) ? (s_cur >> 16) : (s_cur & 0xFFFFu)));
+        float sf = fp16_bits_to_float((uint16_t)((ga & 1) ? (s_cur >> 16) : (s_cur & 0xFFFFu)));
+        if (MODE == 4 && i >= np) sf = 1.f;
         const float2 s2 = make_float2(sf, sf);
         acc_ok = acc_ok && warp_wait(mma_done(i), ring_par(i), abort_flag, &g_tc_status);
         bool released = false;
@@ -740,11 +825,12 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
           if (i + NB < ng) named_bar_arrive(issue_bar(i + NB), L::issue_threads);  // buffer b is free for group i + NB
         }
       }
-
     }
 
     // ----------------------------------------------------------- split-K reduction across the cluster
     __syncwarp();
+    int b_marked = 0;   // LinearLora, mode 4: some CTA of the tile left products out
+    if constexpr (MODE == 4) b_marked = *b_flag;
     // rounds of kRedSlots partial tiles; rank 0 adds them in rank order (deterministic)
     for (int rr = 0; rr < red_rounds; ++rr) {
       const int q0 = 1 + rr * L::kRedSlots;
@@ -759,6 +845,11 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
           const uint32_t off = ((((int)crank - q0) * (BN / 4) + (cq * kCols + c) / 4) * kTileM + r_acc) * 16;
           st_cluster_v4(remote0 + off, acc[c / 2].x, acc[c / 2].y, acc[c / 2 + 1].x, acc[c / 2 + 1].y);
         }
+      }
+      if constexpr (MODE == 4) {
+        if (rr == 0 && crank == 0)
+          for (int q = 1; q < splitk; ++q)
+            b_marked |= (int)ld_cluster_u32(mapa_shared(sbase + L::misc_off + 8, (uint32_t)q));
       }
       cluster_sync();  // this round's partial sums have landed in rank 0
       if (crank == 0) {
@@ -806,6 +897,24 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
           const int64_t t = t0 + cq * kCols + j;
           const float v = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
           if (t < p.T) yo[t * n_rows + row] = float_to_bf16_bits(v);
+        }
+        if constexpr (MODE == 4) {
+          if (b_marked) {   // (not in the usual course) the Inf and NaN products that the A stages left out
+            pdl_wait_previous();   // u
+#pragma unroll 1
+            for (int j = 0; j < kCols; ++j) {
+              const int64_t t = t0 + cq * kCols + j;
+              int rank;
+              const int a = t < p.T ? lora_adapter(p.lo, t, &rank) : -1;
+              if (a < 0) continue;
+              float v = 0.f;
+              for (int k = 0; k < rank; ++k) {
+                const uint32_t b = __ldg(p.lo.b + ((int64_t)a * p.N + row) * p.lo.R + k);
+                if ((b & 0x7F80u) == 0x7F80u) v += lora_u<1>(p.lo, p.T, t, k) * __uint_as_float(b << 16);
+              }
+              if (v != 0.f) yo[t * n_rows + row] = float_to_bf16_bits(__uint_as_float((uint32_t)yo[t * n_rows + row] << 16) + v);
+            }
+          }
         }
       } else {
         // LinearAdd: the residual joins the FP32 sum.  R may be Y, so each element is read
@@ -1065,6 +1174,12 @@ int launch_tile(const LinearArgs& a, int splitk, int64_t tile_base, int64_t n_ti
       set_error_detail("tc: cuTensorMapEncodeTiled failed for the second weight");
       return Q4LIN_ERR_CUDA;
     }
+  } else if (a.mode == 4) {  // LinearLora: u, [T][ug][64] bf16
+    if (!make_map_2d(&tm_high, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_u, (uint64_t)a.lora_groups * 64, (uint64_t)a.T,
+                     (uint64_t)a.lora_groups * 128, 64, BN)) {
+      set_error_detail("tc: cuTensorMapEncodeTiled failed for the adapters' u");
+      return Q4LIN_ERR_CUDA;
+    }
   } else {
     tm_high = tm_codes;  // unused
   }
@@ -1075,7 +1190,8 @@ int launch_tile(const LinearArgs& a, int splitk, int64_t tile_base, int64_t n_ti
                          : a.mode == 2 ? tiles_a + (uint32_t)((a.n_b + kTileM - 1) / kTileM)
                                        : tiles_a;
   const TcParams p{a.scales, a.y, xe, rf, a.r, a.N, Kp, a.T, (int)((a.K + 63) / 64), splitk, (uint32_t)tile_base,
-                   tiles_m, a.mode, tiles_a, a.scales_b, a.y_b, a.n_b, a.delta};
+                   tiles_m, a.mode, tiles_a, a.scales_b, a.y_b, a.n_b, a.delta,
+                   a.lora_groups, a.lora != nullptr ? *a.lora : LoraArgs{}};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_tiles, 1, (unsigned)splitk);
   cfg.blockDim = dim3(L::threads, 1, 1);
@@ -1359,6 +1475,15 @@ int tc_launch(const LinearArgs& a, int route) {
         case 64: return launch_tile<64, false, 0, 3>(a, splitk, base, n);
         case 32: return launch_tile<32, false, 0, 3>(a, splitk, base, n);
         default: return launch_tile<16, false, 0, 3>(a, splitk, base, n);
+      }
+    }
+    if (a.mode == 4) {
+      switch (pl.bn) {
+        case 256: return launch_tile<256, false, 0, 4>(a, splitk, base, n);
+        case 128: return launch_tile<128, false, 0, 4>(a, splitk, base, n);
+        case 64: return launch_tile<64, false, 0, 4>(a, splitk, base, n);
+        case 32: return launch_tile<32, false, 0, 4>(a, splitk, base, n);
+        default: return launch_tile<16, false, 0, 4>(a, splitk, base, n);
       }
     }
     if (a.mode == 2) {

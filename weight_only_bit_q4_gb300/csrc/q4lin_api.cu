@@ -367,7 +367,8 @@ int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t ub = lora_u_bytes(K, T, L, R);
   // workspace: u, then (tile route) the tile records and delta, or the operand pass's buffers
-  const size_t rb = route == Q4LIN_ROUTE_TC_SPLITK ? lora_record_bytes(T, L) : 0;
+  const int64_t groups = route == Q4LIN_ROUTE_TC_SPLITK ? q4::lora_groups(K, L, R) : 0;
+  const size_t rb = route == Q4LIN_ROUTE_TC_SPLITK && groups == 0 ? lora_record_bytes(T, L) : 0;
   const q4::LoraArgs lo{lora_a, lora_b, ids, lora_scales, ranks, reinterpret_cast<float*>(ws), (int)L, (int)R,
                         q4::lora_splits(K, T, L), rb > 0 ? ws + ub : nullptr};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -376,9 +377,17 @@ int run_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t* x, const
   if (route == Q4LIN_ROUTE_STREAM_MMA) return q4::mma_launch(a);
   if ((st = q4::lora_shrink_launch(lo, x, K, T, s)) != Q4LIN_OK) return st;
   if (route == Q4LIN_ROUTE_GEMV) return q4::gemv_lora_launch(a);
+  a.workspace = nullptr;
+  if (groups > 0) {
+    uint16_t* u = reinterpret_cast<uint16_t*>(ws + ub);
+    if ((st = q4::lora_spread_launch(lo, u, (int)groups, T, s)) != Q4LIN_OK) return st;
+    a.lora_u = u;
+    a.lora_groups = (int)groups;
+    a.mode = 4;
+    return q4::tc_launch(a, Q4LIN_ROUTE_TC_SPLITK);
+  }
   float* delta = reinterpret_cast<float*>(ws + ub + rb);
   if ((st = q4::lora_expand_launch(lo, delta, N, T, s)) != Q4LIN_OK) return st;
-  a.workspace = nullptr;
   a.delta = delta;
   a.mode = 3;
   return q4::tc_launch(a, Q4LIN_ROUTE_TC_SPLITK);
@@ -457,7 +466,9 @@ size_t q4lin_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int64_t L, in
   switch (lora_route(N, K, T, (int)R)) {
     case Q4LIN_ROUTE_GEMV: return ub;
     case Q4LIN_ROUTE_STREAM_MMA: return ub + round256(q4::mma_lora_workspace_bytes(N, K, T, (int)R));
-    case Q4LIN_ROUTE_TC_SPLITK: return ub + lora_record_bytes(T, L) + round256((size_t)T * (size_t)q4::lora_delta_pitch(N) * 4);
+    case Q4LIN_ROUTE_TC_SPLITK:
+      if (const int64_t g = q4::lora_groups(K, L, R)) return ub + round256((size_t)T * (size_t)g * 128);
+      return ub + lora_record_bytes(T, L) + round256((size_t)T * (size_t)q4::lora_delta_pitch(N) * 4);
     default: return 0;
   }
 }
