@@ -1153,29 +1153,47 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
 }
 
 // Throughput form, after the down product: y[t, n] = sum_j p[t, j] part[t k + j, n] in the order
-// of the choices; four columns per thread (H is a multiple of 8).
-constexpr int kReduceThreads = 256;
+// of the choices; four columns per thread (H is a multiple of 8).  The choices (final since the
+// gate/up kernel) are read before the wait, and eight parts are in flight at once: one after the
+// other, each behind its choice, they cost about 1.5 us more at 64 tokens x 8.
+constexpr int kReduceThreads = 128;
 
 __global__ void __launch_bounds__(kReduceThreads) q4_moe_reduce_kernel(const MoeParams p) {
   pdl_launch_dependents();
-  pdl_wait_previous();
+  constexpr int kAtOnce = 8;
   const int q = (int)(p.H / 4);
   const int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x;
   const int64_t t = i / q;
-  if (t >= p.slots / p.k) return;
+  const bool mine = t < p.slots / p.k;
   const int64_t n = 4 * (i - t * q);
+  float w[kAtOnce];
+  bool on[kAtOnce];   // (the part of a choice outside [0, E) was not written)
+  auto choices = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const bool in = mine && j0 + j < p.k;
+      const int id = in ? (int)ld_global_u32(p.ids + t * p.k + j0 + j) : -1;
+      w[j] = in ? __uint_as_float(ld_global_u32(p.weights + t * p.k + j0 + j)) : 0.f;
+      on[j] = id >= 0 && id < p.E;
+    }
+  };
+  choices(0);
+  pdl_wait_previous();
+  if (!mine) return;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int j = 0; j < p.k; ++j) {
-    const int64_t s = t * p.k + j;
-    const int id = (int)ld_global_u32(p.ids + s);
-    if (id < 0 || id >= p.E) continue;   // (its part was not written)
-    const float w = __uint_as_float(ld_global_u32(p.weights + s));
-    const float4 f = ld_global_f4(p.part + s * p.H + n);
-    v[0] = fmaf(w, f.x, v[0]);
-    v[1] = fmaf(w, f.y, v[1]);
-    v[2] = fmaf(w, f.z, v[2]);
-    v[3] = fmaf(w, f.w, v[3]);
+  for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
+    if (j0 > 0) choices(j0);
+    float4 f[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) f[j] = on[j] ? ld_global_f4(p.part + (t * p.k + j0 + j) * p.H + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      if (!on[j]) continue;
+      v[0] = fmaf(w[j], f[j].x, v[0]);
+      v[1] = fmaf(w[j], f[j].y, v[1]);
+      v[2] = fmaf(w[j], f[j].z, v[2]);
+      v[3] = fmaf(w[j], f[j].w, v[3]);
+    }
   }
   uint2 o;
   o.x = (uint32_t)float_to_bf16_bits(v[0]) | ((uint32_t)float_to_bf16_bits(v[1]) << 16);
