@@ -503,7 +503,10 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
       }
       // The code slot is free once both teams have their chunks in registers (a TMA
       // refill must not race the reads above); W8G32 reads its chunks below.
+      // (The fence keeps the reads before the arrival: without it a build of the Q6 form read the
+      // second group's chunks after the arrival, and now and then got the refill's.)
       if constexpr (!kW8) {
+        __threadfence_block();
         __syncwarp();
         if (lane == 0) mbar_arrive(c_empty(slot));
       }
