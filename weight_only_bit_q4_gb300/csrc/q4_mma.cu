@@ -54,6 +54,8 @@
 // Every mbarrier wait is bounded (kSpinLimit): on expiry the kernel records
 // Q4LIN_ERR_TIMEOUT, every role skips its remaining work but still passes the
 // band barriers, and the producer drains the copies it issued before exiting.
+#include <type_traits>
+
 #include "q4_internal.h"
 #include "q4_lora.cuh"
 #include "q4_sm100.cuh"
@@ -100,8 +102,18 @@ struct MmaParams {
                                          // the fused form's whole-K buffers)
   uint32_t scl_off, scl_bytes;           // the two band scale buffers
   uint32_t red_off, gate_off, bar_off;
-  uint32_t lora_off;                     // LinearLora: u [8 NT, R] fp32, then the tokens' adapters and ranks
-  LoraArgs lora;                         // LinearLora: the adapters (ids and u of this pass's tokens)
+};
+
+// LinearLora (a type of its own: with these fields the plain layer's parameters cost it 0.5 us)
+struct MmaLoraParams : MmaParams {
+  uint32_t lora_off;   // u [8 NT, R] fp32, then the tokens' adapters and ranks
+  LoraArgs lora;       // the adapters (ids and u of this pass's tokens)
+};
+template <bool kLora> using MmaArgs = std::conditional_t<kLora, MmaLoraParams, MmaParams>;
+struct PrepNoLora {};
+struct PrepLora {
+  int blocks;   // CTAs that convert
+  LoraArgs lo;
 };
 
 // Shared-memory layout of one launch.  Stages hold a chunk's code sub-boxes and (two-kernel
@@ -336,12 +348,12 @@ __device__ __forceinline__ void mma_operand_convert(int tp, int galloc, int lane
   }
 }
 
-// kLora: the CTAs past `blocks` run the adapters' shrink product instead (q4_lora.cuh), so
+// kLora: the CTAs past pl.blocks run the adapters' shrink product instead (q4_lora.cuh), so
 // that it costs no launch of its own and runs beside the conversion.
 template <int NT, int FMT, bool kLora = false>
 __global__ void __launch_bounds__(kPrepThreads)
 q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, float* __restrict__ zs,
-                   int64_t K, int tp, int galloc, int lanes, int early, int blocks, const LoraArgs lo) {
+                   int64_t K, int tp, int galloc, int lanes, int early, const std::conditional_t<kLora, PrepLora, PrepNoLora> pl) {
   static_assert(!kLora || kPrepThreads == kShrinkThreads, "the shrink product's CTA size");
   // Wait for the previous kernel (it may write x, or still read these buffers).  The
   // streaming kernel launches after that wait (late order: it copies weight rows as soon
@@ -351,14 +363,16 @@ q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, flo
   pdl_wait_previous();
   if (!early) pdl_launch_dependents();
   if constexpr (kLora) {
-    if ((int)blockIdx.x >= blocks) {
+    if ((int)blockIdx.x >= pl.blocks) {
       __shared__ float red[kShrinkFloats];
       __shared__ LoraLists L;
-      lora_shrink_block(lo, x, K, tp, (int)blockIdx.x - blocks, L, red);
+      lora_shrink_block(pl.lo, x, K, tp, (int)blockIdx.x - pl.blocks, L, red);
       return;
     }
   }
   const int64_t units = (int64_t)8 * NT * galloc * 4;   // a multiple of 32: whole warps take part
+  unsigned blocks = gridDim.x;
+  if constexpr (kLora) blocks = (unsigned)pl.blocks;
   for (int64_t u = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x; u - (threadIdx.x & 31) < units;
        u += (int64_t)blocks * kPrepThreads)
   {
@@ -380,7 +394,7 @@ q4_mma_prep_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ xf, flo
 template <int NT, int FMT, bool kFuse = false, bool kSwi = false, bool kLora = false>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_high,
-              const MmaParams p) {
+              const MmaArgs<kLora> p) {
   static_assert(!kFuse || NT == 1, "the fused operand pass covers one token tile");
   static_assert(!kSwi || (kFuse && FMT == 0), "LinearSwiGLU: the one-launch Q4 form");
   static_assert(!kLora || (!kFuse && FMT == 0), "LinearLora: the two-kernel Q4 form");
@@ -918,20 +932,17 @@ int mma_launch_pass(const LinearArgs& a, const MmaPlan& pl, const CUtensorMap& t
     cfg.attrs = at;
     cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
-    const int nb = (int)blocks;
     if (!lora) {
       e = cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, FMT>, a.x + t0 * a.K, xf, zs, a.K, tp, pl.galloc, pl.lanes,
-                             pl.early, nb, LoraArgs{});
+                             pl.early, PrepNoLora{});
     } else if constexpr (FMT == 0) {   // (one pass: the caller keeps it to 32 tokens)
-      cfg.gridDim.x = (unsigned)(nb + lora_shrink_grid(*a.lora, tp));
-      e = cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, 0, true>, a.x, xf, zs, a.K, tp, pl.galloc, pl.lanes, pl.early, nb,
-                             *a.lora);
+      cfg.gridDim.x = (unsigned)(blocks + lora_shrink_grid(*a.lora, tp));
+      e = cudaLaunchKernelEx(&cfg, q4_mma_prep_kernel<NT, 0, true>, a.x, xf, zs, a.K, tp, pl.galloc, pl.lanes, pl.early,
+                             PrepLora{(int)blocks, *a.lora});
     }
     if (cuda_check(e, "mma: prep kernel launch")) return Q4LIN_ERR_CUDA;
   }
   MmaParams p{};
-  if (lora) p.lora = *a.lora;
-  p.lora_off = pl.L.lora_off;
   p.wq = a.wq;
   p.scales = a.scales;
   p.xf = xf;
@@ -975,8 +986,13 @@ int mma_launch_pass(const LinearArgs& a, const MmaPlan& pl, const CUtensorMap& t
     if (fused) return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<1, FMT, true>, tm, th, p), "mma: kernel launch");
   }
   if constexpr (FMT == 0)
-    if (lora)
-      return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, 0, false, false, true>, tm, th, p), "mma: kernel launch");
+    if (lora) {
+      MmaLoraParams q{};
+      static_cast<MmaParams&>(q) = p;
+      q.lora_off = pl.L.lora_off;
+      q.lora = *a.lora;
+      return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, 0, false, false, true>, tm, th, q), "mma: kernel launch");
+    }
   return cuda_check(cudaLaunchKernelEx(&cfg, q4_mma_kernel<NT, FMT, false>, tm, th, p), "mma: kernel launch");
 }
 

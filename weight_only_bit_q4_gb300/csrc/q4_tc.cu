@@ -69,6 +69,7 @@
 // (still arriving where others wait), drains what it issued (again bounded)
 // and exits instead of hanging.
 #include <mutex>
+#include <type_traits>
 
 #include "q4_internal.h"
 #include "q4_lora.cuh"
@@ -99,18 +100,22 @@ struct TcParams {
   //     the rest W_b's (codes in the high-plane map slot, scales_b, y_b, n_b).
   int mode;
   uint32_t tiles_a;
-  //   mode 3, LinearLora: the accumulators start from the FP32 term delta
-  //     [T, N rounded up to 8].
   const uint16_t* scales_b;
   uint16_t* y_b;
   int64_t n_b;
+};
+
+// LinearLora.  Mode 3: the accumulators start from the FP32 term delta [T, N rounded up to 8].
+// Mode 4: the adapters' second product as `ug` further groups after the nk of the planes, scale 1:
+// X tile u (bf16 terms hi and lo alternating, map in the high-plane slot), A tile 64 columns of the
+// adapters' B side by side.  (A type of its own: with these fields the other forms' parameters cost
+// them 1 us at T = 1024.)
+struct TcLoraParams : TcParams {
   const float* delta;
-  //   mode 4, LinearLora: the adapters' second product as `ug` further groups after the nk of the
-  //     planes, scale 1: X tile u (bf16 terms hi and lo alternating, map in the high-plane slot),
-  //     A tile 64 columns of the adapters' B side by side.
   int ug;
   LoraArgs lo;
 };
+template <int MODE> using TcArgs = std::conditional_t<MODE >= 3, TcLoraParams, TcParams>;
 
 // Named barrier of the accumulate warps for the SwiGLU exchange (after the issue ring and kAccBar).
 constexpr uint32_t kSwiBar = 10;
@@ -224,7 +229,7 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* v) {
 template <int BN, bool kFold, int FMT, int MODE = 0>
 __global__ void __launch_bounds__(TcSmem<BN, kFold, FMT>::threads, 1)
 q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_x,
-             const __grid_constant__ CUtensorMap tm_high, const TcParams p) {
+             const __grid_constant__ CUtensorMap tm_high, const TcArgs<MODE> p) {
   using L = TcSmem<BN, kFold, FMT>;
   constexpr int kHB = L::kHB;
   constexpr bool kW8 = L::kW8;
@@ -276,7 +281,8 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
   // This CTA's share of the K groups (the whole K without a split).
   const int splitk = p.splitk;
   uint32_t crank = 0;
-  const int groups = MODE == 4 ? p.nk + p.ug : p.nk;
+  int groups = p.nk;
+  if constexpr (MODE == 4) groups += p.ug;
   int g_begin = 0, g_end = groups;
   if (splitk > 1) {
     crank = cluster_ctarank();
@@ -1192,9 +1198,14 @@ int launch_tile(const LinearArgs& a, int splitk, int64_t tile_base, int64_t n_ti
   const uint32_t tiles_m = a.mode == 1 ? (uint32_t)((a.N + kTileM / 2 - 1) / (kTileM / 2))
                          : a.mode == 2 ? tiles_a + (uint32_t)((a.n_b + kTileM - 1) / kTileM)
                                        : tiles_a;
-  const TcParams p{a.scales, a.y, xe, rf, a.r, a.N, Kp, a.T, (int)((a.K + 63) / 64), splitk, (uint32_t)tile_base,
-                   tiles_m, a.mode, tiles_a, a.scales_b, a.y_b, a.n_b, a.delta,
-                   a.lora_groups, a.lora != nullptr ? *a.lora : LoraArgs{}};
+  TcArgs<MODE> p{};
+  static_cast<TcParams&>(p) = TcParams{a.scales, a.y, xe, rf, a.r, a.N, Kp, a.T, (int)((a.K + 63) / 64), splitk,
+                                       (uint32_t)tile_base, tiles_m, a.mode, tiles_a, a.scales_b, a.y_b, a.n_b};
+  if constexpr (MODE >= 3) {
+    p.delta = a.delta;
+    p.ug = a.lora_groups;
+    p.lo = *a.lora;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_tiles, 1, (unsigned)splitk);
   cfg.blockDim = dim3(L::threads, 1, 1);
