@@ -990,6 +990,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
           moe_sub_box<NT, MT, true>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
         else
           moe_sub_box<NT, MT, false>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
+        __threadfence_block();   // every lane's reads of the slot lie before its refill
         __syncwarp();
         if (lane == 0 && is.left > 0) issue();   // refill the slot just read
         if (++slot == p.depth) {
