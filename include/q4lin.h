@@ -261,7 +261,8 @@ int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t*
  * e = ids[t, j], summed over j in order; a choice whose id lies outside [0, E) adds nothing
  * (a token without any gives +0).  All sums FP32.  The intermediate vector of a choice enters
  * W_down's product rounded once to fp16 at a power of two that puts its largest magnitude in
- * [2^14, 2^15) (relative error 2^-11); x enters W_gate's and W_up's exactly down to 2^-27 of the
+ * [2^14, 2^15) (relative error 2^-11, up to 2e-4 of the token's rms(y) in y; F <= 512: as two
+ * such terms, 2^-22); x enters W_gate's and W_up's exactly down to 2^-27 of the
  * token's largest magnitude, and below within 2^-35 of it.
  *   wq_gate_up uint8 [E, 2F, Hp/2], scales_gate_up fp16 [E, 2F, Hp/64]: per expert, gate
  *     rows [0, F), then up rows; wq_down uint8 [E, H, Fp/2], scales_down fp16 [E, H, Fp/64]

@@ -21,8 +21,9 @@
 // undone on the FP32 sum.
 //   gate/up: v = x (bf16), exact down to 2^-27 of the largest |x| and within 2^-35 of it
 //     below (the odd nibbles' sixteenth costs four bits).
-//   down: v = h (FP32), rounded once to fp16 (relative error at most 2^-11, about 1.5e-4
-//     rms(y) in y, a tenth of y's own bf16 rounding; a bf16 h would put 1e-3 rms(y) there).
+//   down: v = h (FP32), as two fp16 terms where F is short (moe_two_terms), else rounded once
+//     to fp16 (relative error at most 2^-11, about 2e-4 rms(y) in y, a tenth of y's own bf16
+//     rounding; a bf16 h would put 1e-3 rms(y) there).
 //
 // Operand layout, as in the streaming warp-MMA route: the K order inside an MMA is free as
 // long as A and B agree, so thread (g = lane / 4, c = lane % 4) takes the 16 weights
@@ -43,7 +44,7 @@
 // (bulk copies; plain loads by all warps spill and cost 9 us there); down converts h itself, in
 // every CTA that needs the slot (a conversion kernel between the products took 3.6 us of 90.7).
 //
-// Two forms, by the number of slots S = T top_k of a pass:
+// Three forms, by the number of slots S = T top_k of a pass and the items of a CTA:
 //   S <= kLatSlots: latency.  MT = 1, the K range of a unit shared by up to 4 warps (partial
 //     sums joined in shared memory); every CTA of the down product converts all of h itself,
 //     owns whole units and adds its slots' sums in shared memory.  (At 80 registers a down CTA
@@ -52,7 +53,9 @@
 //   otherwise: throughput.  MT = 2 (each B fragment feeds
 //     two MMA row tiles); the (tile, unit) pairs are dealt evenly over all CTAs, the slots'
 //     sums of the down product go to the workspace and a last kernel adds them in the order of
-//     the choices.
+//     the choices;
+//   or, for a product with few items per CTA, joined (moe_joins): the same with MT = 1 and the K
+//     range of an item shared by up to 4 warps, as in the latency form, whose gate/up it is.
 //
 // Every mbarrier wait is bounded (kSpinLimit): on expiry the kernel records
 // Q4LIN_ERR_TIMEOUT, the warps stop computing, pass the CTA barriers and drain the
@@ -68,6 +71,7 @@ __device__ int g_moe_status = 0;
 
 constexpr int kMaxNT = 2;                   // token tiles of 8 handled together (4 spill)
 constexpr int kLatSlots = 16;               // up to here the latency form
+enum { kThroughput = 0, kLatency = 1, kJoined = 2 };
 constexpr int kMaxParts = 4;                // warps that share the K range of an item, at most
 constexpr int kMoeWarps = 16;
 __host__ __device__ constexpr int slot_bytes(int mt) { return 2 * 8 * mt * 128; }
@@ -109,6 +113,26 @@ __device__ __forceinline__ uint4 moe_fragment(const float (&f)[8], float s1, flo
     b[q] = (uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16);
     sum += (__half2float(lo) + __half2float(hi)) * ((q & 1) ? 16.f : 1.f);
   }
+  return make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// The same as two fp16 terms v = hi + lo (relative error 2^-22).
+__device__ __forceinline__ uint4 moe_fragment2(const float (&f)[8], float s1, float s16, uint4& low, float& sum) {
+  uint32_t b[4], l[4];
+  sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float sc = (q & 1) ? s16 : s1;
+    const float v0 = f[q] * sc, v1 = f[q + 4] * sc;
+    const __half h0 = __float2half_rn(v0), h1 = __float2half_rn(v1);
+    // (Inf and NaN: the first term alone)
+    const __half l0 = __float2half_rn(fabsf(v0) < INFINITY ? v0 - __half2float(h0) : 0.f);
+    const __half l1 = __float2half_rn(fabsf(v1) < INFINITY ? v1 - __half2float(h1) : 0.f);
+    b[q] = (uint32_t)__half_as_ushort(h0) | ((uint32_t)__half_as_ushort(h1) << 16);
+    l[q] = (uint32_t)__half_as_ushort(l0) | ((uint32_t)__half_as_ushort(l1) << 16);
+    sum += ((__half2float(h0) + __half2float(h1)) + (__half2float(l0) + __half2float(l1))) * ((q & 1) ? 16.f : 1.f);
+  }
+  low = make_uint4(l[0], l[1], l[2], l[3]);
   return make_uint4(b[0], b[1], b[2], b[3]);
 }
 
@@ -157,7 +181,7 @@ __device__ __forceinline__ void moe_prep_token(const uint16_t* x, int64_t H, uin
 
 // The same of one slot's h (FP32, F values), by one warp.  Up to 256 kRuns values are read once
 // and held in registers between the maximum and the conversion.
-template <int kRuns>
+template <int kRuns, bool kTwo>
 __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf, float* zs, float* ft) {
   constexpr int kLanes = 32;
   const int lane = threadIdx.x % kLanes;
@@ -193,11 +217,14 @@ __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf
   auto convert = [&](int i, const float4 (&v)[2]) {   // whole warps; the 8 lanes of a group are adjacent
     const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     float sum;
-    const uint4 b = moe_fragment(f, s1, s16, sum);
+    uint4 b, low;
+    if constexpr (kTwo) b = moe_fragment2(f, s1, s16, low, sum);
+    else b = moe_fragment(f, s1, s16, sum);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (i < nv64) {
       *reinterpret_cast<uint4*>(hf + moe_fragment_at(i)) = b;
+      if constexpr (kTwo) *reinterpret_cast<uint4*>(hf + 16 * nv64 + moe_fragment_at(i)) = low;   // (second terms behind the first)
       if ((i & 7) == 0) zs[i >> 3] = kZeroTerm * sum;
     }
   };
@@ -649,7 +676,7 @@ struct MoeUnit {
 
 // acc[m][n] += the products of the sub-box with the groups G0 .. G0 + 3 (kFull: all of them
 // exist).
-template <int NT, int MT, bool kFull>
+template <int NT, int MT, bool kFull, bool kTwo>
 __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t (&off)[4], int G0, int groups,
                                             const MoeUnit<NT, MT>& un, int nt, float (&acc)[MT][NT][4]) {
   __half2 s0[MT][2], s1[MT][2];   // (the plane rows hold an even number of scales)
@@ -682,6 +709,11 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
       if (NT > 1 && n >= nt) break;
       const uint8_t* at = un.b[n] + (size_t)G * 128;
       const uint4 b0 = *reinterpret_cast<const uint4*>(at), b1 = *reinterpret_cast<const uint4*>(at + 64);
+      uint4 c0, c1;   // kTwo: the second terms, the same weights
+      if constexpr (kTwo) {
+        c0 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128);
+        c1 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128 + 64);
+      }
       const float za = gl == 0 ? z[n][0].x : gl == 1 ? z[n][0].y : gl == 2 ? z[n][0].z : z[n][0].w;
       const float zb = gl == 0 ? z[n][1].x : gl == 1 ? z[n][1].y : gl == 2 ? z[n][1].z : z[n][1].w;
       const float zz[4] = {za, zb, za, zb};
@@ -692,6 +724,12 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
         mma_f16_16816(d, a0[m][2], a1[m][2], a0[m][3], a1[m][3], b0.z, b0.w, d);
         mma_f16_16816(d, a0[m][4], a1[m][4], a0[m][5], a1[m][5], b1.x, b1.y, d);
         mma_f16_16816(d, a0[m][6], a1[m][6], a0[m][7], a1[m][7], b1.z, b1.w, d);
+        if constexpr (kTwo) {
+          mma_f16_16816(d, a0[m][0], a1[m][0], a0[m][1], a1[m][1], c0.x, c0.y, d);
+          mma_f16_16816(d, a0[m][2], a1[m][2], a0[m][3], a1[m][3], c0.z, c0.w, d);
+          mma_f16_16816(d, a0[m][4], a1[m][4], a0[m][5], a1[m][5], c1.x, c1.y, d);
+          mma_f16_16816(d, a0[m][6], a1[m][6], a0[m][7], a1[m][7], c1.z, c1.w, d);
+        }
         const float sa = (gl & 1) ? __high2float(s0[m][gl >> 1]) : __low2float(s0[m][gl >> 1]);
         const float sb = (gl & 1) ? __high2float(s1[m][gl >> 1]) : __low2float(s1[m][gl >> 1]);
         acc[m][n][0] = fmaf(sa, d[0], acc[m][n][0]);
@@ -703,10 +741,10 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
   }
 }
 
-// A column in shared memory: the fragments, then the zero-point terms, an odd number of 64-byte
+// A column in shared memory: the fragments (down: of both terms), then the zero-point terms, an odd number of 64-byte
 // units in all, so that the 64-byte reads of neighbouring columns meet different banks.
-__host__ __device__ inline uint32_t moe_column_bytes(int64_t K) {
-  return (uint32_t)((moe_groups(K) * 128 + moe_zs_pitch(K) * 4 + 127) / 128 * 128 + 64);
+__host__ __device__ inline uint32_t moe_column_bytes(int64_t K, int terms) {
+  return (uint32_t)((terms * moe_groups(K) * 128 + moe_zs_pitch(K) * 4 + 127) / 128 * 128 + 64);
 }
 
 // Shared-memory layout: rings (1024-byte aligned) and their barriers, lists, the columns'
@@ -714,7 +752,21 @@ __host__ __device__ inline uint32_t moe_column_bytes(int64_t K) {
 // 16-byte word per thread, two rounds); down, the slots' sums of every K part, their powers of
 // two, weights and whether they count -- and the columns: gtiles tiles of them (latency form,
 // down: every slot's).
-__host__ inline uint32_t moe_layout(MoeParams& p, int mt, bool down, bool lat) {
+// Warps that share the K range of an item, where a CTA's `items` are dealt to its warps in rounds:
+// as few as pass all items in the shortest time (rounds / parts).
+__host__ __device__ inline int moe_parts(int items, int nsb) {
+  int best = 1, cost = kMaxParts * ((items + kMoeWarps - 1) / kMoeWarps);
+  for (int kp = 2; kp <= kMaxParts && kp <= nsb; kp *= 2) {
+    const int c = kMaxParts / kp * ((items * kp + kMoeWarps - 1) / kMoeWarps);
+    if (c < cost) {
+      best = kp;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+__host__ inline uint32_t moe_layout(MoeParams& p, int mt, bool down, int form) {
   p.bar_off = (uint32_t)(kMoeWarps * p.depth * slot_bytes(mt));
   p.cnt_off = p.bar_off + (uint32_t)(kMoeWarps * p.depth * 8 + 8);
   p.wcnt_off = p.cnt_off + (p.slots <= 32 ? 0u : (uint32_t)p.E * 4);
@@ -724,13 +776,14 @@ __host__ inline uint32_t moe_layout(MoeParams& p, int mt, bool down, bool lat) {
   p.pow_off = p.misc_off + 16;
   p.sum_off = (p.pow_off + (uint32_t)(p.gtiles * p.per) * 4 + 15) / 16 * 16;
   uint32_t at = p.sum_off;
-  if (lat) at += down ? (uint32_t)(p.slots * (kMaxParts * 64 + 12)) : (uint32_t)(2 * 32 * kMoeWarps * 16);
+  const bool own = down && form == kLatency;
+  if (form != kThroughput) at += own ? (uint32_t)(p.slots * (kMaxParts * 64 + 12)) : (uint32_t)(2 * 32 * kMoeWarps * 16);
   p.col_off = (at + 127) / 128 * 128;
-  return p.col_off + (uint32_t)(down && lat ? p.slots : p.gtiles * p.per) * p.col_bytes;
+  return p.col_off + (uint32_t)(own ? p.slots : p.gtiles * p.per) * p.col_bytes;
 }
 
 // kDown false: gate/up units, h written; true: down units, y (latency) or part written.
-template <int NT, int MT, bool kDown, bool kLat>
+template <int NT, int MT, bool kDown, int kForm, bool kTwo>
 __global__ void __launch_bounds__(32 * kMoeWarps, 1)
 q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -781,15 +834,15 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   // Work.  Latency form, down: whole units [u0, u1), all tiles of each.  Otherwise a range
   // [u0, u1) of the numbers tile * nu + unit, so that a CTA's warps share an expert's tokens
   // (the host bounds nu * tiles below 2^31).  kp warps share the K range of an item.
-  constexpr bool kOwn = kDown && kLat;
+  constexpr bool kOwn = kDown && kForm == kLatency, kJoin = kForm != kThroughput && !kOwn;
   const int all = kOwn ? nu : nu * ntiles, grid = (int)gridDim.x, bid = (int)blockIdx.x;
   const int share = all / grid, more = all - share * grid;   // the first `more` CTAs take one more
   const int u0 = bid * share + (bid < more ? bid : more), u1 = u0 + share + (bid < more ? 1 : 0);
   int kp = 1;
-  if constexpr (kLat) {   // the same for every CTA (down: for every unit)
-    const int items = kOwn ? ntiles : share + (more > 0 ? 1 : 0);
-    while (kp < kMaxParts && 2 * kp * items <= kWarps && 2 * kp <= nsb) kp *= 2;
+  if constexpr (kOwn) {   // the same for every unit
+    while (kp < kMaxParts && 2 * kp * ntiles <= kWarps && 2 * kp <= nsb) kp *= 2;
   }
+  if constexpr (kJoin) kp = moe_parts(share + (more > 0 ? 1 : 0), nsb);   // the same for every CTA
   const int kps = 31 - __clz(kp);                  // kp is a power of two
   const int wpr = kWarps >> kps;                   // items per round of the warps
   const int wnum = warp >> kps, kpart = warp & (kp - 1);
@@ -891,14 +944,14 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   if (first_item.left > 0) for_scale_lines(first_item, [&](const uint8_t* a) { prefetch_l2(a); });
   // The B columns: x of a token (gate/up) or h of a slot (down): fragments, terms and powers.
   const float* power = p.ft;   // (down: set below)
-  const uint32_t fbytes = (uint32_t)groups * 128u, zbytes = (uint32_t)moe_zs_pitch(K) * 4u;
+  const uint32_t fbytes = (uint32_t)groups * (kTwo ? 256u : 128u), zbytes = (uint32_t)moe_zs_pitch(K) * 4u;
   uint8_t* cols = smem + p.col_off;
   if constexpr (kDown) pdl_wait_previous();
   if constexpr (kOwn) {   // a warp per slot converts h
     float* fsm = reinterpret_cast<float*>(smem + p.sum_off) + p.slots * kMaxParts * 16;
     for (int s = warp; s < p.slots; s += kWarps) {
       uint8_t* at = cols + s * p.col_bytes;
-      moe_prep_slot<3>(p.h + (int64_t)s * K, K, at, reinterpret_cast<float*>(at + fbytes), fsm + s);
+      moe_prep_slot<3, kTwo>(p.h + (int64_t)s * K, K, at, reinterpret_cast<float*>(at + fbytes), fsm + s);
     }
     power = fsm;
     __syncthreads();
@@ -917,7 +970,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         for (int i = (warp - before) & (kWarps - 1); i < count; i += kWarps) {
           const int at = (t - tile0) * kPer + i;
           uint8_t* dst = cols + at * p.col_bytes;
-          moe_prep_slot<3>(p.h + (int64_t)(L.order[(tl.y & 0xFFFF) + i] & 0xFFFF) * K, K, dst,
+          moe_prep_slot<3, kTwo>(p.h + (int64_t)(L.order[(tl.y & 0xFFFF) + i] & 0xFFFF) * K, K, dst,
                            reinterpret_cast<float*>(dst + fbytes), cpow + at);
         }
         before += count;
@@ -987,9 +1040,9 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         ok = warp_wait(bars + 8u * (uint32_t)slot, phase, abort_flag, &g_moe_status);
       if (ok) {
         if (4 * (sb + 1) <= groups)
-          moe_sub_box<NT, MT, true>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
+          moe_sub_box<NT, MT, true, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
         else
-          moe_sub_box<NT, MT, false>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
+          moe_sub_box<NT, MT, false, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
         __threadfence_block();   // every lane's reads of the slot lie before its refill
         __syncwarp();
         if (lane == 0 && is.left > 0) issue();   // refill the slot just read
@@ -1015,7 +1068,55 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
     ++group;
   };
   Pos pos = start();
-  if constexpr (!kDown) {
+  auto activate = [&](const float (&acc)[MT][NT][4], int first, int count, int unit) {
+    // thread (g, c) holds gate and up of row f of token columns 2c, 2c + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (NT > 1 && 8 * n >= count) break;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = 8 * n + 2 * c + j;
+        if (col >= count) continue;
+        const int o = L.order[first + col];
+        const float F = power[o >> 16];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int64_t f = kRows * (int64_t)unit + 8 * m;
+          if (f >= p.F) continue;
+          const float gt = F * acc[m][n][j], up = F * acc[m][n][2 + j];
+          const float h = gt / (1.f + expf(-gt)) * up;
+          p.h[(int64_t)(o & 0xFFFF) * p.F + f + r] = h;
+        }
+      }
+    }
+  };
+  // pcol: the tile's first staged column
+  auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit, int pcol) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (NT > 1 && 8 * n >= count) break;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = 8 * n + 2 * c + j;
+        if (col >= count) continue;
+        const int s = L.order[first + col] & 0xFFFF;
+        const float F = kOwn ? power[s] : cpow[pcol + col];
+        if constexpr (kOwn) {
+          sums[(kpart * p.slots + s) * 16 + r] = F * acc[0][n][j];
+          sums[(kpart * p.slots + s) * 16 + 8 + r] = F * acc[0][n][2 + j];
+        } else {
+          const int64_t n0 = 2 * kRows * (int64_t)unit;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const int64_t ra = n0 + 8 * m + r, rb = ra + kRows;
+            if (ra < p.H) p.part[(int64_t)s * p.H + ra] = F * acc[m][n][j];
+            if (rb < p.H) p.part[(int64_t)s * p.H + rb] = F * acc[m][n][2 + j];
+          }
+        }
+      }
+    }
+  };
+  if constexpr (!kOwn) {
     int parity = 0;
     int tile0 = tile_a, gstart = u0;
     while (gstart < u1) {
@@ -1030,7 +1131,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         float acc[MT][NT][4];
         int first = 0, count = 0;
         if (have) compute(q, pos, acc, first, count);
-        if constexpr (kLat) {
+        if constexpr (kJoin) {
           if (kp > 1) {   // part 0 adds the others' accumulators, in order
             float4* ex = reinterpret_cast<float4*>(sums) + parity * kThreads;
             parity ^= 1;
@@ -1046,103 +1147,45 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
             }
           }
         }
-        if (!ok) continue;
-        // thread (g, c) holds gate and up of row f of token columns 2c, 2c + 1
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (NT > 1 && 8 * n >= count) break;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int col = 8 * n + 2 * c + j;
-            if (col >= count) continue;
-            const int o = L.order[first + col];
-            const float F = power[o >> 16];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const int64_t f = kRows * (int64_t)q.unit + 8 * m;
-              if (f >= p.F) continue;
-              const float gt = F * acc[m][n][j], up = F * acc[m][n][2 + j];
-              const float h = gt / (1.f + expf(-gt)) * up;
-              p.h[(int64_t)(o & 0xFFFF) * p.F + f + r] = h;
-            }
-          }
-        }
+        if (!ok || !have) continue;
+        if constexpr (kDown) store(acc, first, count, q.unit, (q.tile - q.tile0) * kPer);
+        else activate(acc, first, count, q.unit);
       }
       gstart = gend;
       tile0 += p.gtiles;
     }
   } else {
-    // pcol: the tile's first staged column
-    auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit, int pcol) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (NT > 1 && 8 * n >= count) break;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = 8 * n + 2 * c + j;
-          if (col >= count) continue;
-          const int s = L.order[first + col] & 0xFFFF;
-          const float F = kOwn ? power[s] : cpow[pcol + col];
-          if constexpr (kLat) {
-            sums[(kpart * p.slots + s) * 16 + r] = F * acc[0][n][j];
-            sums[(kpart * p.slots + s) * 16 + 8 + r] = F * acc[0][n][2 + j];
-          } else {
-            const int64_t n0 = 2 * kRows * (int64_t)unit;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const int64_t ra = n0 + 8 * m + r, rb = ra + kRows;
-              if (ra < p.H) p.part[(int64_t)s * p.H + ra] = F * acc[m][n][j];
-              if (rb < p.H) p.part[(int64_t)s * p.H + rb] = F * acc[m][n][2 + j];
-            }
-          }
-        }
+    const int tokens = p.slots / p.k;
+    for (int unit = u0; unit < u1; ++unit) {   // (without any tile: y = +0)
+      while (pos.left > 0 && pos.unit == unit) {
+        const Pos q = pos;
+        step(pos);
+        float acc[MT][NT][4];
+        int first, count;
+        compute(q, pos, acc, first, count);
+        if (ok) store(acc, first, count, unit, 0);
       }
-    };
-    if constexpr (!kLat) {
-      for (int tile0 = tile_a, gstart = u0; gstart < u1; gstart = group_end(tile0), tile0 += p.gtiles) {
-        enter_group(tile0, group_end(tile0));
-        while (pos.left > 0 && pos.tile0 == tile0) {
-          const Pos q = pos;
-          step(pos);
-          float acc[MT][NT][4];
-          int first, count;
-          compute(q, pos, acc, first, count);
-          if (ok) store(acc, first, count, q.unit, (q.tile - q.tile0) * kPer);
-        }
-      }
-    } else {
-      const int tokens = p.slots / p.k;
-      for (int unit = u0; unit < u1; ++unit) {   // (without any tile: y = +0)
-        while (pos.left > 0 && pos.unit == unit) {
-          const Pos q = pos;
-          step(pos);
-          float acc[MT][NT][4];
-          int first, count;
-          compute(q, pos, acc, first, count);
-          if (ok) store(acc, first, count, unit, 0);
-        }
-        __syncthreads();
-        if (!*abort_flag) {   // y of the unit's rows: the slots' sums in the order of the choices
-          const int64_t n0 = 16 * (int64_t)unit;
-          // lane 16 h + row takes every second choice; the halves meet by a shuffle
-          for (int t = warp; t < tokens; t += kWarps) {
-            const int rr = lane & 15;
-            float v = 0.f;
+      __syncthreads();
+      if (!*abort_flag) {   // y of the unit's rows: the slots' sums in the order of the choices
+        const int64_t n0 = 16 * (int64_t)unit;
+        // lane 16 h + row takes every second choice; the halves meet by a shuffle
+        for (int t = warp; t < tokens; t += kWarps) {
+          const int rr = lane & 15;
+          float v = 0.f;
 #pragma unroll 4
-            for (int j = lane >> 4; j < p.k; j += 2) {
-              const int s = t * p.k + j;
-              float part = 0.f;
+          for (int j = lane >> 4; j < p.k; j += 2) {
+            const int s = t * p.k + j;
+            float part = 0.f;
 #pragma unroll
-              for (int i = 0; i < kMaxParts; ++i)
-                if (i < kp) part += sums[(i * p.slots + s) * 16 + rr];
-              v = von[s] ? fmaf(wsm[s], part, v) : v;
-            }
-            v += __shfl_xor_sync(0xffffffffu, v, 16);
-            if (lane < 16 && n0 + rr < p.H) p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
+            for (int i = 0; i < kMaxParts; ++i)
+              if (i < kp) part += sums[(i * p.slots + s) * 16 + rr];
+            v = von[s] ? fmaf(wsm[s], part, v) : v;
           }
+          v += __shfl_xor_sync(0xffffffffu, v, 16);
+          if (lane < 16 && n0 + rr < p.H) p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
         }
-        __syncthreads();   // the sums are free again
       }
+      __syncthreads();   // the sums are free again
     }
   }
   if constexpr (!kDown) {
@@ -1216,13 +1259,13 @@ int moe_sm_count() {
 // Dynamic shared memory at most; what is left of the SM's 256 KB is the L1 of the scales.
 constexpr uint32_t kMoeSmem = 208 * 1024;
 
-template <int NT, int MT, bool kDown, bool kLat>
+template <int NT, int MT, bool kDown, int kForm, bool kTwo = false>
 int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaStream_t stream) {
   static bool attr[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, MT, kDown, kLat>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, MT, kDown, kForm, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)kMoeSmem),
                    "moe: cudaFuncSetAttribute"))
       return Q4LIN_ERR_CUDA;
@@ -1231,18 +1274,18 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   // Columns of one or two tiles beside rings of two slots per warp; then as many slots (up to
   // four) as there is room for.  Long columns: fewer per tile.
   MoeParams p = p0;
-  p.col_bytes = moe_column_bytes(kDown ? p.F : p.H);
+  p.col_bytes = moe_column_bytes(kDown ? p.F : p.H, kTwo ? 2 : 1);
   p.per = 8 * NT < p.slots / p.k ? 8 * NT : p.slots / p.k;   // (an expert gets a token once, as a rule)
   p.depth = 2;
-  p.gtiles = kDown && kLat ? 1 : 2;
-  uint32_t bytes = moe_layout(p, MT, kDown, kLat);
+  p.gtiles = kDown && kForm == kLatency ? 1 : 2;
+  uint32_t bytes = moe_layout(p, MT, kDown, kForm);
   if (bytes > kMoeSmem && p.gtiles > 1) {
     p.gtiles = 1;
-    bytes = moe_layout(p, MT, kDown, kLat);
+    bytes = moe_layout(p, MT, kDown, kForm);
   }
   while (bytes > kMoeSmem && p.per > 1) {
     --p.per;
-    bytes = moe_layout(p, MT, kDown, kLat);
+    bytes = moe_layout(p, MT, kDown, kForm);
   }
   if (bytes > kMoeSmem) {
     set_error_detail("moe: a column of this length does not fit shared memory beside the rings");
@@ -1251,23 +1294,23 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   while (p.depth < 4) {
     MoeParams q = p;
     ++q.depth;
-    const uint32_t more = moe_layout(q, MT, kDown, kLat);
+    const uint32_t more = moe_layout(q, MT, kDown, kForm);
     if (more > kMoeSmem) break;
     p = q;
     bytes = more;
   }
-  if (!(kDown && kLat)) {   // more tiles together, where they are short
+  if (!(kDown && kForm == kLatency)) {   // more tiles together, where they are short
     while (p.gtiles < 8) {
       MoeParams q = p;
       ++q.gtiles;
-      const uint32_t more = moe_layout(q, MT, kDown, kLat);
+      const uint32_t more = moe_layout(q, MT, kDown, kForm);
       if (more > kMoeSmem) break;
       p = q;
       bytes = more;
     }
   }
   int grid = sms;
-  if (kDown && kLat) {   // whole units
+  if (kDown && kForm == kLatency) {   // whole units
     const int64_t nu = (p.H + 15) / 16;
     if (grid > nu) grid = (int)nu;
   }
@@ -1281,20 +1324,45 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<NT, MT, kDown, kLat>, tm, p),
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<NT, MT, kDown, kForm, kTwo>, tm, p),
                     kDown ? "moe: down kernel launch" : "moe: gate/up kernel launch");
 }
 
+// h in two fp16 terms (2^-22) or one (2^-11; up to 2e-4 of the token's rms(y) in y).  The second
+// term's products make the down product a third longer (64 tokens x 8 of 128, F = 768: the layer
+// 97 us for 85), so it has them where F is short, which is also where the tokens' rms, and with it
+// the one term's error, spreads most around the tensor's: against 8e-3 |y| + 1e-3 rms(y) one term
+// reached 1.1 of the bound at F = 40, 1.26 at 264, 0.88 at 512, 0.97 at 768, 0.91 at 1016.
+bool moe_two_terms(int64_t F) { return F <= 512; }
+
 template <bool kDown>
-int moe_kernel_form(bool lat, int nt, const CUtensorMap& tm, const MoeParams& p, int sms, cudaStream_t stream) {
-  if (lat) return moe_kernel_launch<1, 1, kDown, true>(tm, p, sms, stream);
-  if (nt <= 1) return moe_kernel_launch<1, 2, kDown, false>(tm, p, sms, stream);
-  return moe_kernel_launch<kMaxNT, 2, kDown, false>(tm, p, sms, stream);
+int moe_kernel_form(int form, int nt, const CUtensorMap& tm, const MoeParams& p, int sms, cudaStream_t stream) {
+  if constexpr (kDown)
+    if (moe_two_terms(p.F))
+      return form == kLatency ? moe_kernel_launch<1, 1, true, kLatency, true>(tm, p, sms, stream)
+                              : moe_kernel_launch<1, 1, true, kJoined, true>(tm, p, sms, stream);
+  // (the latency form's gate/up is the joined one)
+  if (form == kJoined || (form == kLatency && !kDown)) return moe_kernel_launch<1, 1, kDown, kJoined>(tm, p, sms, stream);
+  if (form == kLatency) return moe_kernel_launch<1, 1, true, kLatency>(tm, p, sms, stream);
+  if (nt <= 1) return moe_kernel_launch<1, 2, kDown, kThroughput>(tm, p, sms, stream);
+  return moe_kernel_launch<kMaxNT, 2, kDown, kThroughput>(tm, p, sms, stream);
+}
+
+// Joined or throughput, by the likely number of a CTA's items (slots spread evenly over the
+// experts).  With less than one long item per SM sub-partition the item's own latency is the
+// time, and shorter items with shared K win: down product of 19 tokens x 6 of 9, 584 x 1944, 1.1
+// items: the layer takes 30.7 us for 53.2; gate/up of 16 tokens x 2 of 8, 4096 x 1024, 3.3 items:
+// 35.3 for 44.6.  With more, the longer items' cheaper bytes do: 19 tokens x 3 of 20, 1992 x 1016,
+// 8 items: 35.9 for 33.7 (gate/up), 5.3 items at 1024 x 1024: 24.6 for 23.0; even at 4.4.
+bool moe_joins(int slots, int64_t E, int64_t rows, int sms) {
+  double none = 1.0;   // (1 - 1 / E)^slots
+  for (int i = 0; i < slots; ++i) none *= 1.0 - 1.0 / (double)E;
+  return (double)E * (1.0 - none) * (double)((rows + 15) / 16) < 4.0 * sms;
 }
 
 // The latency form holds every slot's h in shared memory beside the rings.
 bool moe_latency_form(int slots, int64_t F) {
-  return slots <= kLatSlots && (int64_t)slots * moe_column_bytes(F) <= 64 * 1024;
+  return slots <= kLatSlots && (int64_t)slots * moe_column_bytes(F, moe_two_terms(F) ? 2 : 1) <= 64 * 1024;
 }
 
 // Workspace parts of one pass, each 256-byte aligned.
@@ -1390,7 +1458,13 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
   for (int64_t t0 = 0; t0 < a.T; t0 += pass) {
     const int tp = (int)(a.T - t0 < pass ? a.T - t0 : pass);
     const bool lat = moe_latency_form(tp * a.k, a.F);
-    const uint32_t box = lat ? 8 : 16;
+    // token tiles handled together: two where an expert gets more than a few slots on average
+    const int nt = (int64_t)tp * a.k > 6 * a.E ? 2 : 1;
+    auto form_of = [&](int64_t rows) { return lat ? kLatency : moe_joins(tp * a.k, a.E, rows, sms) ? kJoined : kThroughput; };
+    const int gu_form = form_of(a.F);
+    int dn_form = form_of(a.H / 2);
+    if (dn_form == kThroughput && moe_two_terms(a.F)) dn_form = kJoined;   // (two terms have no throughput form)
+    const uint32_t gbox = gu_form == kThroughput ? 16 : 8, dbox = dn_form == kThroughput ? 16 : 8;
     // (code bytes, rows, gate / up, expert): one copy brings the gate rows and the up rows of a
     // unit (down: one run of twice as many rows)
     CUtensorMap gu, dn;
@@ -1398,7 +1472,7 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
     const uint64_t gs[3] = {(uint64_t)(Hp / 2), (uint64_t)(a.F * (Hp / 2)), (uint64_t)(2 * a.F * (Hp / 2))};
     const uint64_t dd[4] = {(uint64_t)(Fp / 2), (uint64_t)a.H, 1, (uint64_t)a.E};
     const uint64_t ds[3] = {(uint64_t)(Fp / 2), (uint64_t)(a.H * (Fp / 2)), (uint64_t)(a.H * (Fp / 2))};
-    const uint32_t gb[4] = {128, box, 2, 1}, db[4] = {128, 2 * box, 1, 1};
+    const uint32_t gb[4] = {128, gbox, 2, 1}, db[4] = {128, 2 * dbox, 1, 1};
     if (!encode_map_4d(&gu, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_gu, gd, gs, gb, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_map_4d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn, dd, ds, db, CU_TENSOR_MAP_SWIZZLE_128B)) {
       set_error_detail("moe: cuTensorMapEncodeTiled failed (or is unavailable)");
@@ -1432,10 +1506,8 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
     p.E = (int)a.E;
     p.k = a.k;
     p.slots = tp * a.k;
-    // token tiles handled together: two where an expert gets more than a few slots on average
-    const int nt = (int64_t)tp * a.k > 6 * a.E ? 2 : 1;
-    if (const int rc = moe_kernel_form<false>(lat, nt, gu, p, sms, a.stream)) return rc;
-    if (const int rc = moe_kernel_form<true>(lat, nt, dn, p, sms, a.stream)) return rc;
+    if (const int rc = moe_kernel_form<false>(gu_form, nt, gu, p, sms, a.stream)) return rc;
+    if (const int rc = moe_kernel_form<true>(dn_form, nt, dn, p, sms, a.stream)) return rc;
     if (!lat) {
       cudaLaunchAttribute at[1];
       const int64_t n = (int64_t)tp * (a.H / 4);
