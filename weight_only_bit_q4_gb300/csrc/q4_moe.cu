@@ -1035,8 +1035,9 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
     if (next.left > 0) for_scale_lines(next, [&](const uint8_t* a) { prefetch_l2(a); });   // the next unit's scales
     for (int sb = sb0; sb < sb1; ++sb) {
-      // every lane polls: one instruction for the warp, and no exchange of the answer
-      if (ok && !mbar_try_wait(bars + 8u * (uint32_t)slot, phase))
+      // every lane polls and the warp votes (a lane's answer is its own, and warp_wait wants the
+      // whole warp): two instructions where the copy has landed
+      if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bars + 8u * (uint32_t)slot, phase)))
         ok = warp_wait(bars + 8u * (uint32_t)slot, phase, abort_flag, &g_moe_status);
       if (ok) {
         if (4 * (sb + 1) <= groups)
