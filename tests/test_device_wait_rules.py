@@ -26,3 +26,27 @@ def test_a_lanes_own_poll_decides_nothing(name):
     for m in re.finditer(r"\bmbar_try_wait\(", text):
         voted = text[:m.start()].rstrip().endswith("__all_sync(0xffffffffu,")
         assert voted, text[max(0, m.start() - 80):m.end() + 40]
+
+
+@pytest.mark.parametrize("name", KERNEL_FILES)
+def test_a_stage_is_released_behind_a_fence(name):
+    """An arrival that lets a copy refill a stage comes from the helper that puts a fence between
+    the warp's reads and the arrival.  (done_bar guards no stage: it ends the tile kernel.)"""
+    for m in re.finditer(r"\bmbar_arrive\(([^;]*)\);", code(name)):
+        assert m.group(1).strip() == "done_bar", m.group(0)
+
+
+def test_the_release_helper_has_its_fence():
+    text = code("q4_sm100.cuh")
+    body = re.search(r"void warp_release\([^)]*\)\s*\{(.*?)\n\}", text, flags=re.S).group(1)
+    fence, meet, arrive = (body.index(w) for w in ("__threadfence_block();", "__syncwarp();", "mbar_arrive("))
+    assert fence < meet < arrive
+
+
+def test_a_refill_by_the_reading_warp_is_behind_a_fence():
+    """The expert kernel refills a slot from the warp that has read it, without a barrier."""
+    text = code("q4_moe.cu")
+    refills = [m.start() for m in re.finditer(r"if \(lane == 0 && is\.left > 0\) issue\(\);", text)]
+    assert refills
+    for at in refills:
+        assert re.search(r"__threadfence_block\(\);\s*__syncwarp\(\);\s*$", text[:at])

@@ -559,8 +559,7 @@ q4_gemv_stream_kernel(const uint8_t* __restrict__ wq, const uint16_t* __restrict
           for (int t = 0; t < TT; ++t) acc[i * kTP + t] = sc * ((p2[t].x + p2[t].y) + bias[t]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8u * s);
+      warp_release(empty0 + 8u * s, lane);
       int idx = 0;
       const float v = reduce_rows<RB * kTP>(acc, lane, &idx);
       const int row = idx / kTP, t = idx - (idx / kTP) * kTP;

@@ -698,11 +698,9 @@ q4_mma_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constan
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
+      warp_release(empty(s), lane);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(sempty0 + 8u * (b & 1));  // the band's scales are no longer read
+    warp_release(sempty0 + 8u * (b & 1), lane);  // the band's scales are no longer read
 
     // ---- band end: partial sums of the KS sub-boxes, summed in a fixed order
     const int TP = 8 * NT, MR = 16 * p.mt;

@@ -61,6 +61,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
+// Release of a shared-memory stage by a warp that has read it: the fence keeps every lane's
+// reads before lane 0's arrival, which lets a copy refill the stage.  Without it a build of the
+// tile kernel's Q6 form read chunks after the arrival, and now and then got the refill's.  Every
+// ring of the library is released through here: whether a build needs the fence is not to be seen
+// in its source.
+__device__ __forceinline__ void warp_release(uint32_t bar, int lane) {
+  __threadfence_block();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // Named hardware barrier over `nthreads` threads (a multiple of 32): waiting
 // warps sleep in hardware instead of polling.
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {

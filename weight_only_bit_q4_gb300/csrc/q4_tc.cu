@@ -509,13 +509,7 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
       }
       // The code slot is free once both teams have their chunks in registers (a TMA
       // refill must not race the reads above); W8G32 reads its chunks below.
-      // (The fence keeps the reads before the arrival: without it a build of the Q6 form read the
-      // second group's chunks after the arrival, and now and then got the refill's.)
-      if constexpr (!kW8) {
-        __threadfence_block();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c_empty(slot));
-      }
+      if constexpr (!kW8) warp_release(c_empty(slot), lane);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int i = ws * kGroupsPerW + team + 2 * h;
@@ -594,10 +588,7 @@ q4_tc_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant
         __syncwarp();
         named_bar_arrive(issue_bar(i), L::issue_threads);  // always: the issuer must never wait forever
       }
-      if constexpr (kW8) {  // the team's chunks of this stage are read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c_empty(slot));
-      }
+      if constexpr (kW8) warp_release(c_empty(slot), lane);  // the team's chunks of this stage are read
     }
     if constexpr (MODE == 4) {
       // The adapters' groups: column 8 q of the stage (q = chunk number over all adapters) is rank
