@@ -50,3 +50,21 @@ def test_a_refill_by_the_reading_warp_is_behind_a_fence():
     assert refills
     for at in refills:
         assert re.search(r"__threadfence_block\(\);\s*__syncwarp\(\);\s*$", text[:at])
+
+
+@pytest.mark.parametrize("kernel,load", [("q4_moe_router_kernel", "load_w"), ("q4_moe_router_mma_kernel", "load_w")])
+def test_router_weights_are_loaded_after_the_wait(kernel, load):
+    """A kernel before the router may write w_router (a cast, a merge, another projection) and may
+    let the router start before it is done: until griddepcontrol.wait its rows may be prefetched
+    into L2, not read."""
+    text = code("q4_moe.cu")
+    body = text[text.index(kernel + "(const RouterParams p)"):]
+    body = body[:body.index("\n}\n")]
+    waits = [m.start() for m in re.finditer(r"pdl_wait_previous\(\);", body)]
+    calls = [m.start() for m in re.finditer(r"(?<!auto )\b%s\(" % load, body)]
+    assert calls and waits
+    # the last wait is the routing CTAs' (the one before it belongs to the CTAs that prepare x)
+    assert min(calls) > waits[-1]
+    # (inside load_w, which is defined before the wait, stands the only other read)
+    before = re.sub(r"auto %s = .*?\n  \};" % load, "", body[:waits[-1]], flags=re.S)
+    assert not re.search(r"\bld_(global|nc)_\w+\(|__ldg\(", before)

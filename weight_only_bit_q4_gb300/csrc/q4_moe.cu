@@ -325,6 +325,12 @@ __device__ __forceinline__ void moe_pick(const RouterParams& p, const float* lg,
   }
 }
 
+// The 16-bit values [k0, k1) of a row to L2 (16-byte aligned at both ends).
+__device__ __forceinline__ void prefetch_run(const uint16_t* row, int64_t k0, int64_t k1) {
+  const int64_t bytes = 2 * (k1 - k0);
+  if (bytes > 0) bulk_prefetch_l2(row + k0, (uint32_t)(bytes < 32768 ? bytes : 32768));
+}
+
 // One cluster per TT tokens: its 128 warps share the experts (with few experts several warps
 // share the H of one), a warp's lanes share its H; the sums meet in the shared memory of the
 // cluster's first CTA, whose first warps pick the top_k of one token each.
@@ -351,13 +357,12 @@ q4_moe_router_kernel(const RouterParams p) {
     for (int q = 0; q < kAhead; ++q) wv[q] = i + 32 * q < i1 ? ld_global_u4(wr + 8 * (i + 32 * q)) : make_uint4(0u, 0u, 0u, 0u);
   };
   const int w0 = warp * kRouteCluster + (int)rank;
-  if (w0 < p.E * p.parts) {   // the weights are no kernel's output: the first of them come early
+  if (w0 < p.E * p.parts && lane == 0) {   // (to L2 only: a kernel before this one may still write them)
     const int e = w0 / p.parts, part = w0 - e * p.parts;
-    load_w(p.w + (int64_t)e * p.H, nv * part / p.parts + lane, nv * (part + 1) / p.parts);
+    prefetch_run(p.w + (int64_t)e * p.H, 8 * (nv * part / p.parts), 8 * (nv * (part + 1) / p.parts));
   }
   cluster_sync();   // every CTA of the cluster runs before its shared memory is written
   pdl_wait_previous();
-  bool loaded = true;
   for (int w = w0; w < p.E * p.parts; w += kRouteCluster * kWarps) {
     const int e = w / p.parts, part = w - e * p.parts;
     const int64_t i0 = nv * part / p.parts, i1 = nv * (part + 1) / p.parts;
@@ -367,8 +372,7 @@ q4_moe_router_kernel(const RouterParams p) {
     const uint16_t* wr = p.w + (int64_t)e * p.H;
     for (int64_t i = i0 + lane; i < i1; i += 32 * kAhead) {
       uint4 xv[kAhead][TT];
-      if (!loaded) load_w(wr, i, i1);
-      loaded = false;
+      load_w(wr, i, i1);
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const bool in = i + 32 * q < i1;
@@ -453,19 +457,21 @@ q4_moe_router_mma_kernel(const RouterParams p) {
     }
   };
   auto first_step = [&](int unit, int w) { return (int)((int64_t)steps * (unit % p.parts * kWarps + w) / shares); };
-  // the weights are no kernel's output: the first of them come early
-  if (rank < units) load_w(rank, first_step(rank, warp), first_step(rank, warp + 1));
+  // the first unit's weights to L2 (only that: a kernel before this one may still write them)
+  if (rank < units && lane < 16) {
+    const int e = rank / p.parts * 16 + lane;
+    const int64_t k1 = 32 * (int64_t)first_step(rank, warp + 1);
+    if (e < p.E) prefetch_run(p.w + (int64_t)e * p.H, 32 * (int64_t)first_step(rank, warp), k1 < p.H ? k1 : p.H);
+  }
   cluster_sync();   // every CTA of the cluster runs before its shared memory is written
   pdl_wait_previous();
   const uint16_t* xr = p.x + (t0 + g < p.T ? t0 + g : p.T - 1) * p.H;
-  bool loaded = true;
   for (int unit = rank; unit < units; unit += kRouteCluster) {
     float d[4] = {0.f, 0.f, 0.f, 0.f};
     const int end = first_step(unit, warp + 1);
     for (int st = first_step(unit, warp); st < end; st += kSteps) {
       uint4 xv[kSteps];
-      if (!loaded) load_w(unit, st, end);
-      loaded = false;
+      load_w(unit, st, end);
 #pragma unroll
       for (int q = 0; q < kSteps; ++q) {
         const int64_t k = 32 * (int64_t)(st + q) + 8 * c;
@@ -477,7 +483,6 @@ q4_moe_router_mma_kernel(const RouterParams p) {
         mma_bf16_16816(d, w0[q].z, w1[q].z, w0[q].w, w1[q].w, xv[q].z, xv[q].w);
       }
     }
-    loaded = false;
     *reinterpret_cast<float2*>(&part_sum[warp][g][2 * c]) = make_float2(d[0], d[1]);
     *reinterpret_cast<float2*>(&part_sum[warp][g + 8][2 * c]) = make_float2(d[2], d[3]);
     __syncthreads();
