@@ -187,6 +187,39 @@ def clear_device_status() -> int:
     return int(load().q4lin_clear_device_status())
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported at the first call (the binding itself loads without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _new(shape, dtype, device, stream, output=True):
+    """A tensor that a call makes for itself.
+
+    For a ``stream`` other than the current one it is that stream's: torch's allocator hands a
+    freed block out again at once on the stream it belongs to, so scratch of the current stream,
+    freed when the call returns, would be written over while the kernels on ``stream`` still use
+    it.  An output goes on to the caller and is marked as used on the current stream too.
+    """
+    torch = _t()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if output:
+        t.record_stream(current)
+    return t
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -208,6 +241,9 @@ def linear(wq, scales, x, y=None, workspace=None, stream=None, route: int = ROUT
     padding); x: bf16 [T, K]; all CUDA, contiguous.  ``y`` (bf16 [T, N]) and
     ``workspace`` (uint8, >= workspace_bytes) are allocated here with torch if
     not given.  Runs on ``stream`` (a torch.cuda.Stream) or the current stream.
+    As everywhere in this module, what is allocated here belongs to the stream of
+    the call; tensors that are passed in must be ready on it and live until it is
+    past the call.
     """
     import torch
 
@@ -222,12 +258,12 @@ def linear(wq, scales, x, y=None, workspace=None, stream=None, route: int = ROUT
     if wq.dtype != torch.uint8 or x.dtype != torch.bfloat16 or scales.element_size() != 2:
         raise ValueError("dtypes: wq uint8, scales fp16 bits, x bf16")
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        y = _new((T, N), torch.bfloat16, x.device, stream)
     elif y.shape != (T, N) or y.dtype != torch.bfloat16 or not y.is_contiguous():
         raise ValueError("y must be a contiguous bf16 [T, N] tensor")
     need = workspace_bytes(N, K, T, route)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _new(need, torch.uint8, x.device, stream, output=False)
     s = (stream or torch.cuda.current_stream(x.device)).cuda_stream
     st = linear_raw(_ptr(wq), _ptr(scales), _ptr(x), _ptr(y), N, K, T,
                     _ptr(workspace) if need else None, ctypes.c_void_p(s), route)
@@ -278,7 +314,7 @@ def linear_host(wq, scales, x_host, y_host=None, workspace=None, stream=None):
     elif y_host.is_cuda or tuple(y_host.shape) != (T, N) or y_host.element_size() != 2 or not y_host.is_contiguous():
         raise ValueError("y_host must be a contiguous 2-byte CPU [T, N] tensor (pinned)")
     if workspace is None:
-        workspace = torch.empty(max(host_workspace_bytes(N, K, T), 256), dtype=torch.uint8, device=wq.device)
+        workspace = _new(max(host_workspace_bytes(N, K, T), 256), torch.uint8, wq.device, stream, output=False)
     s = (stream or torch.cuda.current_stream(wq.device)).cuda_stream
     st = int(load().q4lin_linear_host(_ptr(wq), _ptr(scales), _ptr(x_host), _ptr(y_host), N, K, T,
                                       _ptr(workspace), ctypes.c_void_p(s)))
@@ -301,7 +337,7 @@ def linear_add(wq, scales, x, r, y=None, stream=None):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        y = _new((T, N), torch.bfloat16, x.device, stream)
     s = (stream or torch.cuda.current_stream(x.device)).cuda_stream
     st = int(load().q4lin_linear_add(_ptr(wq), _ptr(scales), _ptr(x), _ptr(r), _ptr(y), N, K, T, ctypes.c_void_p(s)))
     if st != OK:
@@ -335,9 +371,9 @@ def linear_qtype(qtype: str, planes, scales, x, y=None, stream=None):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if y is None:
-        y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)
+        y = _new((T, N), torch.bfloat16, x.device, stream)
     need = int(load().q4lin_qtype_workspace_bytes(qt, N, K, T))
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    ws = _new(need, torch.uint8, x.device, stream, output=False) if need else None
     s = (stream or torch.cuda.current_stream(x.device)).cuda_stream
     st = int(load().q4lin_linear_qtype(qt, _ptr(codes), _ptr(high) if bits else None, _ptr(scales), _ptr(x),
                                        _ptr(y), N, K, T, _ptr(ws), ctypes.c_void_p(s)))
@@ -389,7 +425,7 @@ def linear_swiglu(wq, scales, x, y=None, stream=None):
     F = n2 // 2
     _check_planes(wq, scales, K, "linear_swiglu")
     if y is None:
-        y = torch.empty((T, F), dtype=torch.bfloat16, device=x.device)
+        y = _new((T, F), torch.bfloat16, x.device, stream)
     s = (stream or torch.cuda.current_stream(x.device)).cuda_stream
     st = int(load().q4lin_linear_swiglu(_ptr(wq), _ptr(scales), _ptr(x), _ptr(y), F, K, T, ctypes.c_void_p(s)))
     if st != OK:
@@ -406,9 +442,9 @@ def linear_pair(wq_a, scales_a, wq_b, scales_b, x, y_a=None, y_b=None, stream=No
     _check_planes(wq_b, scales_b, K, "linear_pair b")
     Na, Nb = wq_a.shape[0], wq_b.shape[0]
     if y_a is None:
-        y_a = torch.empty((T, Na), dtype=torch.bfloat16, device=x.device)
+        y_a = _new((T, Na), torch.bfloat16, x.device, stream)
     if y_b is None:
-        y_b = torch.empty((T, Nb), dtype=torch.bfloat16, device=x.device)
+        y_b = _new((T, Nb), torch.bfloat16, x.device, stream)
     s = (stream or torch.cuda.current_stream(x.device)).cuda_stream
     st = int(load().q4lin_linear_pair(_ptr(wq_a), _ptr(scales_a), _ptr(wq_b), _ptr(scales_b), _ptr(x), _ptr(y_a),
                                       _ptr(y_b), Na, Nb, K, T, ctypes.c_void_p(s)))
@@ -421,18 +457,6 @@ def linear_pair(wq_a, scales_a, wq_b, scales_b, x, y_a=None, y_b=None, stream=No
 # These are called once or more per token of a decode step, where the host's time per call
 # counts: each tensor is checked once, with attribute reads only, and pointers go to the
 # library as plain integers.
-
-_torch = None
-
-
-def _t():
-    """torch, imported at the first call (the binding itself loads without it)."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
-
 
 def _stream_ptr(stream, device):
     if stream is not None:
@@ -456,13 +480,12 @@ def _need_bits16(name, t, shape):
     return t.data_ptr()
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, device, stream):
     """(address, the tensor that keeps it alive) of at least ``need`` workspace bytes."""
     if need == 0:
         return None, None
     if workspace is None:
-        torch = _t()
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _new(need, _t().uint8, device, stream, output=False)
     elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes")
     return workspace.data_ptr(), workspace
@@ -497,8 +520,8 @@ def linear_lora(wq, scales, x, lora_a, lora_b, adapter_ids, adapter_scales=None,
     lib = load()
     dev = x.device
     if y is None:
-        y = torch.empty((T, N), dtype=bf16, device=dev)
-    ws, ws_keep = _scratch(workspace, lib.q4lin_lora_workspace_bytes(N, K, T, L, R), dev)
+        y = _new((T, N), bf16, dev, stream)
+    ws, ws_keep = _scratch(workspace, lib.q4lin_lora_workspace_bytes(N, K, T, L, R), dev, stream)
     st = lib.q4lin_linear_lora(
         _need("wq", wq, torch.uint8, (N, Kp // 2)), _need_bits16("scales", scales, (N, Kp // 64)), _need("x", x, bf16, (T, K)),
         _need("lora_a", lora_a, bf16, (L, R, K)), _need("lora_b", lora_b, bf16, (L, N, R)),
@@ -527,9 +550,9 @@ def moe_router(x, w_router, top_k: int, bias=None, renormalize: bool = True, ids
     E = w_router.shape[0]
     dev = x.device
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        ids = _new((T, top_k), torch.int32, dev, stream)
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        weights = _new((T, top_k), torch.float32, dev, stream)
     st = load().q4lin_moe_router(
         _need("x", x, torch.bfloat16, (T, H)), _need("w_router", w_router, torch.bfloat16, (E, H)),
         None if bias is None else _need("bias", bias, torch.float32, (E,)), _need("ids", ids, torch.int32, (T, top_k)),
@@ -567,8 +590,8 @@ def moe_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_dow
     gu, gus, dn, dns, E, F = _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H)
     lib = load()
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    ws, ws_keep = _scratch(workspace, lib.q4lin_moe_workspace_bytes(T, H, F, E, k), x.device)
+        y = _new((T, H), torch.bfloat16, x.device, stream)
+    ws, ws_keep = _scratch(workspace, lib.q4lin_moe_workspace_bytes(T, H, F, E, k), x.device, stream)
     st = lib.q4lin_moe_experts(
         _need("x", x, torch.bfloat16, (T, H)), _need("ids", ids, torch.int32, (T, k)),
         _need("weights", weights, torch.float32, (T, k)), gu, gus, dn, dns, _need("y", y, torch.bfloat16, (T, H)),
@@ -587,12 +610,12 @@ def moe(x, w_router, wq_gate_up, scales_gate_up, wq_down, scales_down, top_k: in
     gu, gus, dn, dns, E, F = _expert_planes(wq_gate_up, scales_gate_up, wq_down, scales_down, H)
     lib = load()
     if y is None:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        y = _new((T, H), torch.bfloat16, dev, stream)
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        ids = _new((T, top_k), torch.int32, dev, stream)
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    ws, ws_keep = _scratch(workspace, lib.q4lin_moe_workspace_bytes(T, H, F, E, top_k), dev)
+        weights = _new((T, top_k), torch.float32, dev, stream)
+    ws, ws_keep = _scratch(workspace, lib.q4lin_moe_workspace_bytes(T, H, F, E, top_k), dev, stream)
     st = lib.q4lin_moe(
         _need("x", x, torch.bfloat16, (T, H)), _need("w_router", w_router, torch.bfloat16, (E, H)),
         None if bias is None else _need("bias", bias, torch.float32, (E,)), gu, gus, dn, dns,
@@ -632,9 +655,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     T = q.shape[0]
     P, rot = cos_sin.shape
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _new(q.shape, q.dtype, q.device, stream)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _new(k.shape, k.dtype, k.device, stream)
     bf16 = torch.bfloat16
     qp, ldq, hq = _rows("q", q, D, bf16)
     kp, ldk, hk = _rows("k", k, D, bf16)
