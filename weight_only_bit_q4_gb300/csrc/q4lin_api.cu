@@ -517,9 +517,11 @@ int q4lin_moe(const uint16_t* x, const uint16_t* w_router, const float* bias, co
   int st = validate_router(x, w_router, bias, ids, weights, T, H, E, top_k);
   if (st == Q4LIN_OK)
     st = validate_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y, T, H, F, E, top_k);
-  if (st == Q4LIN_OK) st = check_workspace(q4lin_moe_workspace_bytes(T, H, F, E, top_k), workspace);
+  const size_t need = q4lin_moe_workspace_bytes(T, H, F, E, top_k);
+  if (st == Q4LIN_OK) st = check_workspace(need, workspace);
+  // (the router's operand pass writes into a workspace only where one was asked for: not with H or F = 0)
   if (st == Q4LIN_OK) st = run_router(x, w_router, bias, ids, weights, T, H, E, top_k, renormalize, stream, F,
-                                       F > 0 ? workspace : nullptr);
+                                       need > 0 ? workspace : nullptr);
   if (st == Q4LIN_OK)
     st = run_experts(x, ids, weights, wq_gate_up, scales_gate_up, wq_down, scales_down, y, T, H, F, E, top_k, workspace,
                      stream, true);
