@@ -260,10 +260,9 @@ int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t*
  * Experts:  y[t] = bf16( sum_j weights[t, j] W_down,e (silu(W_gate,e x[t]) * (W_up,e x[t])) ),
  * e = ids[t, j], summed over j in order; a choice whose id lies outside [0, E) adds nothing
  * (a token without any gives +0).  All sums FP32.  The intermediate vector of a choice enters
- * W_down's product rounded once to fp16 at a power of two that puts its largest magnitude in
- * [2^14, 2^15) (relative error 2^-11, up to 2e-4 of the token's rms(y) in y; F <= 512: as two
- * such terms, 2^-22); x enters W_gate's and W_up's exactly down to 2^-27 of the
- * token's largest magnitude, and below within 2^-35 of it.
+ * W_down's product as two fp16 terms at a power of two that puts its largest magnitude in
+ * [2^14, 2^15) (relative error 2^-22, and within 2^-35 of that magnitude); x enters W_gate's and
+ * W_up's exactly down to 2^-27 of the token's largest magnitude, and below within 2^-35 of it.
  *   wq_gate_up uint8 [E, 2F, Hp/2], scales_gate_up fp16 [E, 2F, Hp/64]: per expert, gate
  *     rows [0, F), then up rows; wq_down uint8 [E, H, Fp/2], scales_down fp16 [E, H, Fp/64]
  *     (Hp, Fp: H, F rounded up to 128); y bf16 [T, H] (must not overlap x)
@@ -274,7 +273,8 @@ int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t*
  *
  * q4lin_moe is both in one call: ids and weights are outputs, and all of its arguments are
  * checked before anything is launched.  Three kernels for a pass of up to 16 choices
- * (T * top_k), four beyond; q4lin_moe_experts the same.
+ * (T * top_k) whose intermediate vectors fit shared memory together, four beyond (long F: more,
+ * its columns in several launches); q4lin_moe_experts the same.
  */
 int q4lin_moe_router(const uint16_t* x, const uint16_t* w_router, const float* bias, int32_t* ids, float* weights,
                      int64_t T, int64_t H, int64_t E, int top_k, int renormalize, void* stream);

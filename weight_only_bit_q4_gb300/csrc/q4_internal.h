@@ -159,7 +159,7 @@ struct MoeArgs {
   void* workspace;
   cudaStream_t stream;
 };
-size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int k);
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int k);
 // With a workspace the router also runs the experts' first operand pass into it (prepared).
 int moe_router_launch(const MoeArgs& a);
 int moe_experts_launch(const MoeArgs& a, bool prepared);

@@ -11,7 +11,7 @@
 // over the choices: kernels chained by programmatic dependent launch.  Bound: the packed weights of
 // the experts that some token chose, each read once; the kernels below therefore sort
 // the (token, choice) slots by expert and stream each chosen expert's rows once for all
-// of its tokens (tiles of up to 8 NT token columns).
+// of its tokens that fit a tile (up to 8 NT token columns, fewer where columns are long).
 //
 // Products.  mma.sync m16n8k16 (fp16 x fp16 -> fp32); the 64 weights of a scale group go
 // through four MMAs into a fresh D, then acc += s D in FP32.  A: a masked nibble pair is the
@@ -21,9 +21,13 @@
 // undone on the FP32 sum.
 //   gate/up: v = x (bf16), exact down to 2^-27 of the largest |x| and within 2^-35 of it
 //     below (the odd nibbles' sixteenth costs four bits).
-//   down: v = h (FP32), as two fp16 terms where F is short (moe_two_terms), else rounded once
-//     to fp16 (relative error at most 2^-11, about 2e-4 rms(y) in y, a tenth of y's own bf16
-//     rounding; a bf16 h would put 1e-3 rms(y) there).
+//   down: v = h (FP32), as two fp16 terms v = hi + lo (relative error 2^-22; one term, 2^-11,
+//     shows in y: 1e-4 of its rms, and single bf16 steps).  In a tile of up to four slots the lo
+//     terms are columns of their own, which would be empty otherwise (kPairs); in a wider one
+//     their products follow the hi terms' into the same D.  Against one term: 20.3 us for 20.2
+//     (1 token, 8 of 64, 2048 x 768), 32.7 for 32.4 (4, 2 of 8, 5120 x 1408), 33.3 for 32.2 (19,
+//     3 of 20, 1992 x 1016), 89.6 for 87.0 (64, 8 of 128, 2048 x 768), 81.9 for 72.7 with 32
+//     tokens per expert (64, 4 of 8, 2048 x 2048).
 //
 // Operand layout, as in the streaming warp-MMA route: the K order inside an MMA is free as
 // long as A and B agree, so thread (g = lane / 4, c = lane % 4) takes the 16 weights
@@ -40,22 +44,25 @@
 // sub-box): lane 0 refills a slot as soon as the warp has read it, across unit borders, so
 // no warp waits for another.  The columns of a CTA's next few tiles lie in shared memory
 // beside the rings; read through L1 instead they cost the whole layer 12 us of
-// 103 at 64 tokens x 8 of 128 experts.  Gate/up copies what the operand pass has converted
+// 103 at 64 tokens x 8 of 128 experts (one term of h).  Gate/up copies what the operand pass has converted
 // (bulk copies; plain loads by all warps spill and cost 9 us there); down converts h itself, in
 // every CTA that needs the slot (a conversion kernel between the products took 3.6 us of 90.7).
 //
-// Three forms, by the number of slots S = T top_k of a pass and the items of a CTA:
-//   S <= kLatSlots: latency.  MT = 1, the K range of a unit shared by up to 4 warps (partial
-//     sums joined in shared memory); every CTA of the down product converts all of h itself,
-//     owns whole units and adds its slots' sums in shared memory.  (At 80 registers a down CTA
-//     of 8 warps fits beside the gate/up CTA and starts early, but both then spill and run at
-//     half speed: one token of 8 of 64 experts took 25.8 us against 22.2.)
+// Three forms, by the number of slots S = T top_k of a pass and the items of a CTA (moe_plan):
+//   S <= kLatSlots, and every slot's h fits shared memory: latency.  MT = 1, the K range of a unit
+//     shared by up to 4 warps (partial sums joined in shared memory); every CTA of the down product
+//     converts all of h itself, owns whole units and adds its slots' sums in shared memory.  (At 80
+//     registers a down CTA of 8 warps fits beside the gate/up CTA and starts early, but both then
+//     spill and run at half speed: one token of 8 of 64 experts took 25.8 us against 22.2.)
 //   otherwise: throughput.  MT = 2 (each B fragment feeds
 //     two MMA row tiles); the (tile, unit) pairs are dealt evenly over all CTAs, the slots'
 //     sums of the down product go to the workspace and a last kernel adds them in the order of
 //     the choices;
-//   or, for a product with few items per CTA, joined (moe_joins): the same with MT = 1 and the K
-//     range of an item shared by up to 4 warps, as in the latency form, whose gate/up it is.
+//   or, for a product with few items per CTA (moe_joins) or with long columns, joined: the same with
+//     MT = 1 and the K range of an item shared by up to 4 warps, as in the latency form, whose
+//     gate/up it is.
+// Long F: the joined down product runs in chunks of F columns, a launch each, so that a tile keeps
+// its four or eight slots; the last kernel adds the chunks' sums.
 //
 // Every mbarrier wait is bounded (kSpinLimit): on expiry the kernel records
 // Q4LIN_ERR_TIMEOUT, the warps stop computing, pass the CTA barriers and drain the
@@ -69,7 +76,7 @@ namespace {
 
 __device__ int g_moe_status = 0;
 
-constexpr int kMaxNT = 2;                   // token tiles of 8 handled together (4 spill)
+constexpr int kMaxNT = 2;                   // column tiles of 8 handled together (4 spill)
 constexpr int kLatSlots = 16;               // up to here the latency form
 enum { kThroughput = 0, kLatency = 1, kJoined = 2 };
 constexpr int kMaxParts = 4;                // warps that share the K range of an item, at most
@@ -109,34 +116,36 @@ __device__ __forceinline__ uint4 moe_fragment(const float (&f)[8], float s1, flo
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const float sc = (q & 1) ? s16 : s1;
-    const __half lo = __float2half_rn(f[q] * sc), hi = __float2half_rn(f[q + 4] * sc);
-    b[q] = (uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16);
-    sum += (__half2float(lo) + __half2float(hi)) * ((q & 1) ? 16.f : 1.f);
+    const __half2 h = __floats2half2_rn(f[q] * sc, f[q + 4] * sc);
+    const float2 v = __half22float2(h);
+    b[q] = *reinterpret_cast<const uint32_t*>(&h);
+    sum += (v.x + v.y) * ((q & 1) ? 16.f : 1.f);
   }
   return make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// The same as two fp16 terms v = hi + lo (relative error 2^-22).
+// The same as two fp16 terms v = hi + lo (relative error 2^-22, which the sum need not follow).
 __device__ __forceinline__ uint4 moe_fragment2(const float (&f)[8], float s1, float s16, uint4& low, float& sum) {
   uint32_t b[4], l[4];
-  sum = 0.f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const float sc = (q & 1) ? s16 : s1;
     const float v0 = f[q] * sc, v1 = f[q + 4] * sc;
-    const __half h0 = __float2half_rn(v0), h1 = __float2half_rn(v1);
-    // (Inf and NaN: the first term alone)
-    const __half l0 = __float2half_rn(fabsf(v0) < INFINITY ? v0 - __half2float(h0) : 0.f);
-    const __half l1 = __float2half_rn(fabsf(v1) < INFINITY ? v1 - __half2float(h1) : 0.f);
-    b[q] = (uint32_t)__half_as_ushort(h0) | ((uint32_t)__half_as_ushort(h1) << 16);
-    l[q] = (uint32_t)__half_as_ushort(l0) | ((uint32_t)__half_as_ushort(l1) << 16);
-    sum += ((__half2float(h0) + __half2float(h1)) + (__half2float(l0) + __half2float(l1))) * ((q & 1) ? 16.f : 1.f);
+    const __half2 h = __floats2half2_rn(v0, v1);
+    const float2 r = __half22float2(h);
+    const __half2 lo = __floats2half2_rn(v0 - r.x, v1 - r.y);
+    b[q] = *reinterpret_cast<const uint32_t*>(&h);
+    l[q] = *reinterpret_cast<const uint32_t*>(&lo);
   }
+  sum = s1 * (((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7])));
   low = make_uint4(l[0], l[1], l[2], l[3]);
   return make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 constexpr float kZeroTerm = -8.f * 5.9604644775390625e-8f;   // -8 2^-24
+
+__host__ __device__ inline int64_t moe_groups(int64_t H) { return (H + 63) / 64; }
+__host__ __device__ inline int64_t moe_zs_pitch(int64_t H) { return (moe_groups(H) + 3) / 4 * 4; }
 
 // Where run i of 8 K values goes inside a column's fragments: group i / 8 (128 bytes), the
 // first or second 8 of thread c = (i % 8) / 2.
@@ -179,9 +188,11 @@ __device__ __forceinline__ void moe_prep_token(const uint16_t* x, int64_t H, uin
   if (tid == 0) *ft = exp2i(24 + e);
 }
 
-// The same of one slot's h (FP32, F values), by one warp.  Up to 256 kRuns values are read once
-// and held in registers between the maximum and the conversion.
-template <int kRuns, bool kTwo>
+// The same of one slot's h (FP32, F values), by one warp and as two terms.  The first 256 kRuns
+// values are read once and held in registers between the maximum and the conversion, the others
+// are read for both, 256 kRest at a time (together; one after the other they cost a trip to L2
+// each, but the throughput form has no registers left for more than one).
+template <int kRuns, int kRest>
 __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf, float* zs, float* ft) {
   constexpr int kLanes = 32;
   const int lane = threadIdx.x % kLanes;
@@ -201,15 +212,17 @@ __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf
       mx = max(max(max(mx, __float_as_uint(v[q].x) & 0x7FFFFFFFu), max(__float_as_uint(v[q].y) & 0x7FFFFFFFu, __float_as_uint(v[q].z) & 0x7FFFFFFFu)),
                __float_as_uint(v[q].w) & 0x7FFFFFFFu);
   };
+  for (int i0 = kRuns * kLanes; i0 < nv64; i0 += kRest * kLanes) {
+    float4 v[kRest][2];
+#pragma unroll
+    for (int u = 0; u < kRest; ++u) load(i0 + u * kLanes + lane, v[u]);
+#pragma unroll
+    for (int u = 0; u < kRest; ++u) magnitude(v[u]);
+  }
 #pragma unroll
   for (int u = 0; u < kRuns; ++u) load(lane + u * kLanes, keep[u]);
 #pragma unroll
   for (int u = 0; u < kRuns; ++u) magnitude(keep[u]);
-  for (int i = lane + kRuns * kLanes; i < nv; i += kLanes) {
-    float4 v[2];
-    load(i, v);
-    magnitude(v);
-  }
   mx = __reduce_max_sync(0xffffffffu, mx);
   const int E = (int)(mx >> 23);
   const int e = (mx == 0 || E == 255) ? 0 : min(max(E - 141, -100), 100);
@@ -217,30 +230,32 @@ __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf
   auto convert = [&](int i, const float4 (&v)[2]) {   // whole warps; the 8 lanes of a group are adjacent
     const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     float sum;
-    uint4 b, low;
-    if constexpr (kTwo) b = moe_fragment2(f, s1, s16, low, sum);
-    else b = moe_fragment(f, s1, s16, sum);
+    uint4 low;
+    const uint4 b = moe_fragment2(f, s1, s16, low, sum);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (i < nv64) {
       *reinterpret_cast<uint4*>(hf + moe_fragment_at(i)) = b;
-      if constexpr (kTwo) *reinterpret_cast<uint4*>(hf + 16 * nv64 + moe_fragment_at(i)) = low;   // (second terms behind the first)
-      if ((i & 7) == 0) zs[i >> 3] = kZeroTerm * sum;
+      *reinterpret_cast<uint4*>(hf + 16 * nv64 + moe_fragment_at(i)) = low;   // (second terms behind the first)
+      if ((i & 7) == 0) {   // (both terms' zero points with the first)
+        zs[i >> 3] = kZeroTerm * sum;
+        zs[moe_zs_pitch(F) + (i >> 3)] = 0.f;
+      }
     }
   };
 #pragma unroll
   for (int u = 0; u < kRuns; ++u)
     if (u * kLanes < nv64) convert(lane + u * kLanes, keep[u]);
-  for (int i0 = kRuns * kLanes; i0 < nv64; i0 += kLanes) {
-    float4 v[2];
-    load(i0 + lane, v);
-    convert(i0 + lane, v);
+  for (int i0 = kRuns * kLanes; i0 < nv64; i0 += kRest * kLanes) {
+    float4 v[kRest][2];
+#pragma unroll
+    for (int u = 0; u < kRest; ++u) load(i0 + u * kLanes + lane, v[u]);
+#pragma unroll
+    for (int u = 0; u < kRest; ++u)
+      if (i0 + u * kLanes < nv64) convert(i0 + u * kLanes + lane, v[u]);
   }
   if (lane == 0) *ft = exp2i(24 + e);
 }
-
-__host__ __device__ inline int64_t moe_groups(int64_t H) { return (H + 63) / 64; }
-__host__ __device__ inline int64_t moe_zs_pitch(int64_t H) { return (moe_groups(H) + 3) / 4 * 4; }
 
 __device__ __forceinline__ void moe_prep_at(const RouterParams& p, int64_t t) {
   moe_prep_token(p.x + t * p.H, p.H, p.xf + (size_t)t * moe_groups(p.H) * 128, p.zs + t * moe_zs_pitch(p.H), p.ft + t);
@@ -515,11 +530,13 @@ struct MoeParams {
   const float* weights;    // [T, k]
   const uint16_t* s_gu;    // [E, 2F, Hp/64]
   const uint16_t* s_dn;    // [E, H, Fp/64]
-  float* h;                // [T k][F]
-  float* part;             // throughput form: [T k][H] sums of the down product
+  float* h;                // [T k][F] (down: from the launch's first column on)
+  float* part;             // [chunks][T k][H] sums of the down product, but in the latency form
   uint16_t* y;             // [T, H]
   int64_t H, F;
+  int kn;                  // columns of the launch: H, or (down) a chunk of F
   int E, k, slots;         // slots = T k of this pass
+  int chunks;              // launches of the down product
   int depth;               // ring slots per warp
   int per;                 // columns per tile, at most (8 NT, fewer where a column is long)
   int gtiles;              // tiles whose columns lie in shared memory together
@@ -680,7 +697,7 @@ struct MoeUnit {
 };
 
 // acc[m][n] += the products of the sub-box with the groups G0 .. G0 + 3 (kFull: all of them
-// exist).
+// exist; kTwo: and those of the second terms, groups * 128 bytes behind the first).
 template <int NT, int MT, bool kFull, bool kTwo>
 __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t (&off)[4], int G0, int groups,
                                             const MoeUnit<NT, MT>& un, int nt, float (&acc)[MT][NT][4]) {
@@ -714,7 +731,7 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
       if (NT > 1 && n >= nt) break;
       const uint8_t* at = un.b[n] + (size_t)G * 128;
       const uint4 b0 = *reinterpret_cast<const uint4*>(at), b1 = *reinterpret_cast<const uint4*>(at + 64);
-      uint4 c0, c1;   // kTwo: the second terms, the same weights
+      uint4 c0, c1;
       if constexpr (kTwo) {
         c0 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128);
         c1 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128 + 64);
@@ -746,10 +763,11 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
   }
 }
 
-// A column in shared memory: the fragments (down: of both terms), then the zero-point terms, an odd number of 64-byte
-// units in all, so that the 64-byte reads of neighbouring columns meet different banks.
+// A column in shared memory (down: a slot's two): the fragments, then the zero-point terms, an odd
+// number of 64-byte units in all, so that the 64-byte reads of neighbouring columns meet different
+// banks.
 __host__ __device__ inline uint32_t moe_column_bytes(int64_t K, int terms) {
-  return (uint32_t)((terms * moe_groups(K) * 128 + moe_zs_pitch(K) * 4 + 127) / 128 * 128 + 64);
+  return (uint32_t)((terms * (moe_groups(K) * 128 + moe_zs_pitch(K) * 4) + 127) / 128 * 128 + 64);
 }
 
 // Shared-memory layout: rings (1024-byte aligned) and their barriers, lists, the columns'
@@ -788,11 +806,14 @@ __host__ inline uint32_t moe_layout(MoeParams& p, int mt, bool down, int form) {
 }
 
 // kDown false: gate/up units, h written; true: down units, y (latency) or part written.
-template <int NT, int MT, bool kDown, int kForm, bool kTwo>
+// kPairs (down, tiles of up to four slots): the second terms in columns of their own.
+template <int NT, int MT, bool kDown, int kForm, bool kPairs>
 __global__ void __launch_bounds__(32 * kMoeWarps, 1)
 q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
+  static_assert(!kPairs || (kDown && NT == 1), "pairs of columns: the down product, one column tile");
+  constexpr bool kTwo = kDown && !kPairs;   // the second terms' products follow the first
   constexpr int kRows = 8 * MT, kWarps = kMoeWarps, kThreads = 32 * kWarps;
   const int kPer = p.per;
   const uint32_t col_bar = sbase + p.bar_off + 8u * (uint32_t)(kWarps * p.depth);
@@ -829,9 +850,10 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   moe_build_lists(p, L, kPer);
   const int ntiles = *L.ntiles;
 
-  const int K = (int)(kDown ? p.F : p.H);
+  const int K = p.kn;
   const int nsb = (K + 255) / 256;
-  const int groups = (K + 63) / 64, grow = (K + 127) / 128 * 2;
+  const int groups = (K + 63) / 64, gpad = (K + 127) / 128 * 2;
+  const int grow = (int)(((kDown ? p.F : p.H) + 127) / 128 * 2);      // scales per weight row
   const int64_t rows_e = kDown ? p.H : 2 * p.F;                        // weight rows per expert
   const int64_t last_row = (int64_t)p.E * rows_e - 1;
   const int nu = (int)(kDown ? (p.H + 2 * kRows - 1) / (2 * kRows) : (p.F + kRows - 1) / kRows);   // units per expert
@@ -901,7 +923,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   // ---- issue side (lane 0): the warp's items once more, sub-box by sub-box, `depth` ahead
   Pos is = start();
   int is_sb = sb0, is_slot = 0, is_row = 0, is_exp = 0;
-  int64_t issued = 0;
+  int issued = 0;
   auto issue = [&]() {
     if (is_sb == sb0) {
       is_exp = L.tiles[is.tile].x;
@@ -930,7 +952,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   auto for_scale_lines = [&](const Pos& q, auto&& f) {
     if (lane < 2 * kRows) {
       const uint8_t* a = scale_row(q);
-      const int most = (grow - 4 * sb0) * 2 - 4;
+      const int most = (gpad - 4 * sb0) * 2 - 4;
       for (int i = 0; i <= nl; ++i) f(a + (128 * i < most ? 128 * i : most));
     }
   };
@@ -949,14 +971,14 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   if (first_item.left > 0) for_scale_lines(first_item, [&](const uint8_t* a) { prefetch_l2(a); });
   // The B columns: x of a token (gate/up) or h of a slot (down): fragments, terms and powers.
   const float* power = p.ft;   // (down: set below)
-  const uint32_t fbytes = (uint32_t)groups * (kTwo ? 256u : 128u), zbytes = (uint32_t)moe_zs_pitch(K) * 4u;
+  const uint32_t fbytes = (uint32_t)groups * (kDown ? 256u : 128u), zbytes = (uint32_t)moe_zs_pitch(K) * 4u;
   uint8_t* cols = smem + p.col_off;
   if constexpr (kDown) pdl_wait_previous();
   if constexpr (kOwn) {   // a warp per slot converts h
     float* fsm = reinterpret_cast<float*>(smem + p.sum_off) + p.slots * kMaxParts * 16;
     for (int s = warp; s < p.slots; s += kWarps) {
       uint8_t* at = cols + s * p.col_bytes;
-      moe_prep_slot<3, kTwo>(p.h + (int64_t)s * K, K, at, reinterpret_cast<float*>(at + fbytes), fsm + s);
+      moe_prep_slot<3, MT == 1 ? 3 : 1>(p.h + s * p.F, K, at, reinterpret_cast<float*>(at + fbytes), fsm + s);
     }
     power = fsm;
     __syncthreads();
@@ -975,8 +997,8 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         for (int i = (warp - before) & (kWarps - 1); i < count; i += kWarps) {
           const int at = (t - tile0) * kPer + i;
           uint8_t* dst = cols + at * p.col_bytes;
-          moe_prep_slot<3, kTwo>(p.h + (int64_t)(L.order[(tl.y & 0xFFFF) + i] & 0xFFFF) * K, K, dst,
-                           reinterpret_cast<float*>(dst + fbytes), cpow + at);
+          moe_prep_slot<3, MT == 1 ? 3 : 1>(p.h + (L.order[(tl.y & 0xFFFF) + i] & 0xFFFF) * p.F, K, dst, reinterpret_cast<float*>(dst + fbytes),
+                           cpow + at);
         }
         before += count;
       }
@@ -1028,11 +1050,14 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       const int k = i < count ? i : 0;
       return tcols + (uint32_t)(kOwn ? L.order[first + k] & 0xFFFF : k) * p.col_bytes;
     };
+    // (kPairs: column i is the first term of slot i, column 4 + i its second)
+    const uint32_t bterm = kPairs && g >= 4 ? fbytes / 2 : 0u, zterm = kPairs && c >= 2 ? zbytes : 0u;
+    constexpr int width = kPairs ? 3 : 7;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      un.b[n] = column(8 * n + g) + 16 * c;
-      un.z[n][0] = reinterpret_cast<const float*>(column(8 * n + 2 * c) + fbytes);
-      un.z[n][1] = reinterpret_cast<const float*>(column(8 * n + 2 * c + 1) + fbytes);
+      un.b[n] = column(8 * n + (g & width)) + bterm + 16 * c;
+      un.z[n][0] = reinterpret_cast<const float*>(column(8 * n + (2 * c & width)) + fbytes + zterm);
+      un.z[n][1] = reinterpret_cast<const float*>(column(8 * n + (2 * c & width) + 1) + fbytes + zterm);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -1057,6 +1082,12 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
           phase ^= 1;
         }
       }
+    }
+    if constexpr (kPairs) {   // the second terms' sums, of columns 4 .. 7, to the threads of the first terms' (c = 0, 1)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][0][j] += __shfl_down_sync(0xffffffffu, acc[m][0][j], 2);
     }
   };
 
@@ -1198,7 +1229,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
     if (!ok && threadIdx.x == 0 && group > 0) mbar_drain(col_bar, (uint32_t)((group - 1) & 1));
   }
   if (!ok && lane == 0)   // aborted: let the copies already issued land before the CTA exits
-    for (int64_t d = issued > p.depth ? issued - p.depth : 0; d < issued; ++d)
+    for (int d = issued > p.depth ? issued - p.depth : 0; d < issued; ++d)
       mbar_drain(bars + 8u * (uint32_t)(d % p.depth), (uint32_t)((d / p.depth) & 1));
 }
 
@@ -1236,6 +1267,14 @@ __global__ void __launch_bounds__(kReduceThreads) q4_moe_reduce_kernel(const Moe
     float4 f[kAtOnce];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) f[j] = on[j] ? ld_global_f4(p.part + (t * p.k + j0 + j) * p.H + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 1; c < p.chunks; ++c) {   // (long F) the sums of the further chunks of columns, in order
+      float4 m[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        m[j] = on[j] ? ld_global_f4(p.part + ((int64_t)c * p.slots + t * p.k + j0 + j) * p.H + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) f[j] = make_float4(f[j].x + m[j].x, f[j].y + m[j].y, f[j].z + m[j].z, f[j].w + m[j].w);
+    }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       if (!on[j]) continue;
@@ -1265,55 +1304,59 @@ int moe_sm_count() {
 // Dynamic shared memory at most; what is left of the SM's 256 KB is the L1 of the scales.
 constexpr uint32_t kMoeSmem = 208 * 1024;
 
-template <int NT, int MT, bool kDown, int kForm, bool kTwo = false>
-int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaStream_t stream) {
-  static bool attr[64] = {};
-  int dev = 0;
-  if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
-  if (dev >= 64 || !attr[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, MT, kDown, kForm, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)kMoeSmem),
-                   "moe: cudaFuncSetAttribute"))
-      return Q4LIN_ERR_CUDA;
-    if (dev < 64) attr[dev] = true;
-  }
-  // Columns of one or two tiles beside rings of two slots per warp; then as many slots (up to
-  // four) as there is room for.  Long columns: fewer per tile.
-  MoeParams p = p0;
-  p.col_bytes = moe_column_bytes(kDown ? p.F : p.H, kTwo ? 2 : 1);
-  p.per = 8 * NT < p.slots / p.k ? 8 * NT : p.slots / p.k;   // (an expert gets a token once, as a rule)
+// Shared-memory plan of a launch (the tile width per, the ring's depth, the tiles held together):
+// columns of one or two tiles beside rings of two slots per warp; then as many slots (up to four)
+// as there is room for, and more tiles together, where they are short.  Long columns: fewer per
+// tile.  0: a column of this length does not fit at all.
+uint32_t moe_fit(MoeParams& p, int nt, bool down, int form) {
+  const int mt = form == kThroughput ? 2 : 1;
+  const bool own = down && form == kLatency;
+  const int tokens = p.slots / p.k;   // (an expert gets a token once, as a rule)
+  if (form != kThroughput) nt = 1;
+  p.col_bytes = moe_column_bytes(p.kn, down ? 2 : 1);
+  p.per = 8 * nt < tokens ? 8 * nt : tokens;
   p.depth = 2;
-  p.gtiles = kDown && kForm == kLatency ? 1 : 2;
-  uint32_t bytes = moe_layout(p, MT, kDown, kForm);
+  p.gtiles = own ? 1 : 2;
+  uint32_t bytes = moe_layout(p, mt, down, form);
   if (bytes > kMoeSmem && p.gtiles > 1) {
     p.gtiles = 1;
-    bytes = moe_layout(p, MT, kDown, kForm);
+    bytes = moe_layout(p, mt, down, form);
   }
   while (bytes > kMoeSmem && p.per > 1) {
     --p.per;
-    bytes = moe_layout(p, MT, kDown, kForm);
+    bytes = moe_layout(p, mt, down, form);
   }
-  if (bytes > kMoeSmem) {
-    set_error_detail("moe: a column of this length does not fit shared memory beside the rings");
-    return Q4LIN_ERR_UNSUPPORTED_SHAPE;
-  }
+  if (bytes > kMoeSmem) return 0;
   while (p.depth < 4) {
     MoeParams q = p;
     ++q.depth;
-    const uint32_t more = moe_layout(q, MT, kDown, kForm);
+    const uint32_t more = moe_layout(q, mt, down, form);
     if (more > kMoeSmem) break;
     p = q;
     bytes = more;
   }
-  if (!(kDown && kForm == kLatency)) {   // more tiles together, where they are short
-    while (p.gtiles < 8) {
-      MoeParams q = p;
-      ++q.gtiles;
-      const uint32_t more = moe_layout(q, MT, kDown, kForm);
-      if (more > kMoeSmem) break;
-      p = q;
-      bytes = more;
-    }
+  while (!own && p.gtiles < 8) {
+    MoeParams q = p;
+    ++q.gtiles;
+    const uint32_t more = moe_layout(q, mt, down, form);
+    if (more > kMoeSmem) break;
+    p = q;
+    bytes = more;
+  }
+  return bytes;
+}
+
+template <int NT, int MT, bool kDown, int kForm, bool kPairs = false>
+int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p, uint32_t bytes, int sms, cudaStream_t stream) {
+  static bool attr[64] = {};
+  int dev = 0;
+  if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
+  if (dev >= 64 || !attr[dev]) {
+    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, MT, kDown, kForm, kPairs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)kMoeSmem),
+                   "moe: cudaFuncSetAttribute"))
+      return Q4LIN_ERR_CUDA;
+    if (dev < 64) attr[dev] = true;
   }
   int grid = sms;
   if (kDown && kForm == kLatency) {   // whole units
@@ -1330,45 +1373,91 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p0, int sms, cudaS
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<NT, MT, kDown, kForm, kTwo>, tm, p),
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<NT, MT, kDown, kForm, kPairs>, tm, p),
                     kDown ? "moe: down kernel launch" : "moe: gate/up kernel launch");
 }
 
-// h in two fp16 terms (2^-22) or one (2^-11; up to 2e-4 of the token's rms(y) in y).  The second
-// term's products make the down product a third longer (64 tokens x 8 of 128, F = 768: the layer
-// 97 us for 85), so it has them where F is short, which is also where the tokens' rms, and with it
-// the one term's error, spreads most around the tensor's: against 8e-3 |y| + 1e-3 rms(y) one term
-// reached 1.1 of the bound at F = 40, 1.26 at 264, 0.88 at 512, 0.97 at 768, 0.91 at 1016.
-bool moe_two_terms(int64_t F) { return F <= 512; }
-
 template <bool kDown>
-int moe_kernel_form(int form, int nt, const CUtensorMap& tm, const MoeParams& p, int sms, cudaStream_t stream) {
-  if constexpr (kDown)
-    if (moe_two_terms(p.F))
-      return form == kLatency ? moe_kernel_launch<1, 1, true, kLatency, true>(tm, p, sms, stream)
-                              : moe_kernel_launch<1, 1, true, kJoined, true>(tm, p, sms, stream);
+int moe_kernel_form(int form, int nt, const CUtensorMap& tm, const MoeParams& p, uint32_t bytes, int sms, cudaStream_t stream) {
+  if constexpr (kDown) {
+    if (p.per <= 4) {
+      if (form == kLatency) return moe_kernel_launch<1, 1, true, kLatency, true>(tm, p, bytes, sms, stream);
+      if (form == kJoined) return moe_kernel_launch<1, 1, true, kJoined, true>(tm, p, bytes, sms, stream);
+      return moe_kernel_launch<1, 2, true, kThroughput, true>(tm, p, bytes, sms, stream);
+    }
+    if (form == kLatency) return moe_kernel_launch<1, 1, true, kLatency>(tm, p, bytes, sms, stream);
+  }
   // (the latency form's gate/up is the joined one)
-  if (form == kJoined || (form == kLatency && !kDown)) return moe_kernel_launch<1, 1, kDown, kJoined>(tm, p, sms, stream);
-  if (form == kLatency) return moe_kernel_launch<1, 1, true, kLatency>(tm, p, sms, stream);
-  if (nt <= 1) return moe_kernel_launch<1, 2, kDown, kThroughput>(tm, p, sms, stream);
-  return moe_kernel_launch<kMaxNT, 2, kDown, kThroughput>(tm, p, sms, stream);
+  if (form != kThroughput) return moe_kernel_launch<1, 1, kDown, kJoined>(tm, p, bytes, sms, stream);
+  if (nt <= 1) return moe_kernel_launch<1, 2, kDown, kThroughput>(tm, p, bytes, sms, stream);
+  return moe_kernel_launch<kMaxNT, 2, kDown, kThroughput>(tm, p, bytes, sms, stream);
 }
 
 // Joined or throughput, by the likely number of a CTA's items (slots spread evenly over the
 // experts).  With less than one long item per SM sub-partition the item's own latency is the
 // time, and shorter items with shared K win: down product of 19 tokens x 6 of 9, 584 x 1944, 1.1
-// items: the layer takes 30.7 us for 53.2; gate/up of 16 tokens x 2 of 8, 4096 x 1024, 3.3 items:
-// 35.3 for 44.6.  With more, the longer items' cheaper bytes do: 19 tokens x 3 of 20, 1992 x 1016,
-// 8 items: 35.9 for 33.7 (gate/up), 5.3 items at 1024 x 1024: 24.6 for 23.0; even at 4.4.
+// items: the layer takes 37 us for 60; 20 x 4 of 16, 1024 x 1024, 3.4 items: 25.8 for 27.2.  With
+// more, the longer items' cheaper bytes do: 64 tokens x 8 of 128, 2048 x 768, 53 items: 95.8 for
+// 89.7; 19 x 3 of 20, 1992 x 1016, 8 items: 35.5 for 33.5; even at 4.3.
 bool moe_joins(int slots, int64_t E, int64_t rows, int sms) {
   double none = 1.0;   // (1 - 1 / E)^slots
   for (int i = 0; i < slots; ++i) none *= 1.0 - 1.0 / (double)E;
   return (double)E * (1.0 - none) * (double)((rows + 15) / 16) < 4.0 * sms;
 }
 
-// The latency form holds every slot's h in shared memory beside the rings.
-bool moe_latency_form(int slots, int64_t F) {
-  return slots <= kLatSlots && (int64_t)slots * moe_column_bytes(F, moe_two_terms(F) ? 2 : 1) <= 64 * 1024;
+MoeParams moe_params(int tokens, int64_t H, int64_t F, int64_t E, int k) {
+  MoeParams p{};
+  p.H = H;
+  p.F = F;
+  p.E = (int)E;
+  p.k = k;
+  p.slots = tokens * k;
+  p.kn = (int)H;
+  p.chunks = 1;
+  return p;
+}
+
+// How a pass of `tokens` tokens runs: the forms of its two products, token tiles handled together,
+// and the chunks of F columns (a launch of the down product each) with their length.
+struct MoePlan {
+  int nt, gu_form, dn_form, chunks, len;
+};
+
+// False: a column of H values does not fit shared memory beside the rings.
+bool moe_plan(int tokens, int64_t H, int64_t F, int64_t E, int k, int sms, MoePlan* pl) {
+  const MoeParams p = moe_params(tokens, H, F, E, k);
+  // token tiles handled together: two where an expert gets more than a few slots on average
+  pl->nt = (int64_t)p.slots > 6 * E ? 2 : 1;
+  auto fit = [&](bool down, int form, int64_t columns) {   // the tile width, 0: does not fit
+    MoeParams q = p;
+    q.kn = (int)columns;
+    return moe_fit(q, pl->nt, down, form) != 0 ? q.per : 0;
+  };
+  pl->gu_form = moe_joins(p.slots, E, F, sms) || fit(false, kThroughput, H) == 0 ? kJoined : kThroughput;
+  if (fit(false, pl->gu_form, H) == 0) return false;
+  pl->chunks = 1;
+  pl->len = (int)F;
+  if (p.slots <= kLatSlots && fit(true, kLatency, F) > 0) {
+    pl->gu_form = pl->dn_form = kLatency;
+    return true;
+  }
+  // The throughput form only with whole tiles.  Narrower ones decode their rows again for every few
+  // slots, and joined they are wider (its rings are half as large): 64 tokens x 2 of 8, 5120 x 1408,
+  // 13 columns of 16 for 8: 124 us for 116; 4 x 2 of 8, 4096 x 14336, one column for two: 259 for 206.
+  const int width = 8 * pl->nt < tokens ? 8 * pl->nt : tokens;
+  pl->dn_form = moe_joins(p.slots, E, H / 2, sms) || fit(true, kThroughput, F) < width ? kJoined : kThroughput;
+  if (pl->dn_form == kThroughput) return true;
+  // Chunks of F that keep tiles of four slots, of eight where an expert gets more than four on
+  // average: 64 tokens x 2 of 8, 4096 x 14336: 777 us in one launch (two slots per tile), 629 with
+  // four, 599 with eight; 16 tokens: 291, 266, 291; 8 tokens, 6144 x 32768: 815, 637, 684.
+  const int even = p.slots > 4 * E ? 8 : 4, want = even < tokens ? even : tokens;
+  const int nsb = (int)((F + 255) / 256);
+  for (int c = 1; c <= nsb; ++c) {
+    pl->len = (nsb + c - 1) / c * 256;
+    pl->chunks = (nsb * 256 + pl->len - 1) / pl->len;
+    if (fit(true, kJoined, pl->len < F ? pl->len : F) >= want) return true;
+  }
+  return false;
 }
 
 // Workspace parts of one pass, each 256-byte aligned.
@@ -1376,17 +1465,16 @@ struct MoeWs {
   size_t xf, zs, ft, h, part, total;
 };
 
-MoeWs moe_ws(int tokens, int64_t H, int64_t F, int k) {
+MoeWs moe_ws(int tokens, int64_t H, int64_t F, int k, const MoePlan& pl) {
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   const size_t S = (size_t)tokens * (size_t)k;
-  const bool lat = moe_latency_form((int)S, F);
   MoeWs w;
   w.xf = 0;
   w.zs = w.xf + up((size_t)tokens * (size_t)moe_groups(H) * 128);
   w.ft = w.zs + up((size_t)tokens * (size_t)moe_zs_pitch(H) * 4);
   w.h = w.ft + up((size_t)tokens * 4);
   w.part = w.h + up(S * (size_t)F * 4);
-  w.total = w.part + (lat ? 0 : up(S * (size_t)H * 4));
+  w.total = w.part + (pl.dn_form == kLatency ? 0 : up((size_t)pl.chunks * S * (size_t)H * 4));
   return w;
 }
 
@@ -1409,11 +1497,18 @@ int moe_pass_tokens(int64_t T, int k) {
   return (int)(T < most ? T : most);
 }
 
-size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int k) {
-  const int tp = moe_pass_tokens(T, k);
-  const size_t first = moe_ws(tp, H, F, k).total;
-  // a last, shorter pass may take the other form, whose parts are fewer
-  return first;
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int k) {
+  const int tp = moe_pass_tokens(T, k), sms = moe_sm_count();
+  MoePlan pl;
+  if (!moe_plan(tp, H, F, E, k, sms, &pl)) return 0;
+  size_t most = moe_ws(tp, H, F, k, pl).total;
+  if (T % tp != 0) {   // a last, shorter pass, with a plan of its own
+    const int last = (int)(T % tp);
+    if (!moe_plan(last, H, F, E, k, sms, &pl)) return 0;
+    const size_t b = moe_ws(last, H, F, k, pl).total;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 int moe_router_launch(const MoeArgs& a) {
@@ -1437,7 +1532,9 @@ int moe_router_launch(const MoeArgs& a) {
   int64_t prep = 0;
   if (a.workspace != nullptr) {   // the whole layer: the experts' first operand pass beside the router
     const int tp = moe_pass_tokens(a.T, a.k);
-    const MoeWs w = moe_ws(tp, a.H, a.F, a.k);
+    MoePlan pl;
+    if (!moe_plan(tp, a.H, a.F, a.E, a.k, moe_sm_count(), &pl)) return Q4LIN_ERR_UNSUPPORTED_SHAPE;
+    const MoeWs w = moe_ws(tp, a.H, a.F, a.k, pl);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     p.xf = ws + w.xf;
     p.zs = reinterpret_cast<float*>(ws + w.zs);
@@ -1463,28 +1560,20 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   for (int64_t t0 = 0; t0 < a.T; t0 += pass) {
     const int tp = (int)(a.T - t0 < pass ? a.T - t0 : pass);
-    const bool lat = moe_latency_form(tp * a.k, a.F);
-    // token tiles handled together: two where an expert gets more than a few slots on average
-    const int nt = (int64_t)tp * a.k > 6 * a.E ? 2 : 1;
-    auto form_of = [&](int64_t rows) { return lat ? kLatency : moe_joins(tp * a.k, a.E, rows, sms) ? kJoined : kThroughput; };
-    const int gu_form = form_of(a.F);
-    int dn_form = form_of(a.H / 2);
-    if (dn_form == kThroughput && moe_two_terms(a.F)) dn_form = kJoined;   // (two terms have no throughput form)
-    const uint32_t gbox = gu_form == kThroughput ? 16 : 8, dbox = dn_form == kThroughput ? 16 : 8;
+    MoePlan pl;
+    if (!moe_plan(tp, a.H, a.F, a.E, a.k, sms, &pl)) return Q4LIN_ERR_UNSUPPORTED_SHAPE;
     // (code bytes, rows, gate / up, expert): one copy brings the gate rows and the up rows of a
     // unit (down: one run of twice as many rows)
-    CUtensorMap gu, dn;
+    const uint32_t gbox = pl.gu_form == kThroughput ? 16 : 8, dbox = pl.dn_form == kThroughput ? 16 : 8;
+    CUtensorMap gu;
     const uint64_t gd[4] = {(uint64_t)(Hp / 2), (uint64_t)a.F, 2, (uint64_t)a.E};
     const uint64_t gs[3] = {(uint64_t)(Hp / 2), (uint64_t)(a.F * (Hp / 2)), (uint64_t)(2 * a.F * (Hp / 2))};
-    const uint64_t dd[4] = {(uint64_t)(Fp / 2), (uint64_t)a.H, 1, (uint64_t)a.E};
-    const uint64_t ds[3] = {(uint64_t)(Fp / 2), (uint64_t)(a.H * (Fp / 2)), (uint64_t)(a.H * (Fp / 2))};
-    const uint32_t gb[4] = {128, gbox, 2, 1}, db[4] = {128, 2 * dbox, 1, 1};
-    if (!encode_map_4d(&gu, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_gu, gd, gs, gb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_map_4d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn, dd, ds, db, CU_TENSOR_MAP_SWIZZLE_128B)) {
+    const uint32_t gb[4] = {128, gbox, 2, 1};
+    if (!encode_map_4d(&gu, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_gu, gd, gs, gb, CU_TENSOR_MAP_SWIZZLE_128B)) {
       set_error_detail("moe: cuTensorMapEncodeTiled failed (or is unavailable)");
       return Q4LIN_ERR_CUDA;
     }
-    const MoeWs w = moe_ws(tp, a.H, a.F, a.k);
+    const MoeWs w = moe_ws(tp, a.H, a.F, a.k, pl);
     if (!prepared || t0 > 0) {
       RouterParams r{};
       r.x = a.x + t0 * a.H;
@@ -1496,7 +1585,7 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
       const cudaLaunchConfig_t cfg = moe_config((unsigned)tp, 256, a.stream, at);
       if (cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_prep_kernel, r), "moe: operand pass launch")) return Q4LIN_ERR_CUDA;
     }
-    MoeParams p{};
+    MoeParams p = moe_params(tp, a.H, a.F, a.E, a.k);
     p.xf = ws + w.xf;
     p.zs = reinterpret_cast<const float*>(ws + w.zs);
     p.ft = reinterpret_cast<const float*>(ws + w.ft);
@@ -1507,14 +1596,29 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
     p.h = reinterpret_cast<float*>(ws + w.h);
     p.part = reinterpret_cast<float*>(ws + w.part);
     p.y = a.y + t0 * a.H;
-    p.H = a.H;
-    p.F = a.F;
-    p.E = (int)a.E;
-    p.k = a.k;
-    p.slots = tp * a.k;
-    if (const int rc = moe_kernel_form<false>(gu_form, nt, gu, p, sms, a.stream)) return rc;
-    if (const int rc = moe_kernel_form<true>(dn_form, nt, dn, p, sms, a.stream)) return rc;
-    if (!lat) {
+    p.chunks = pl.chunks;
+    MoeParams g = p;
+    const uint32_t gbytes = moe_fit(g, pl.nt, false, pl.gu_form);
+    if (const int rc = moe_kernel_form<false>(pl.gu_form, pl.nt, gu, g, gbytes, sms, a.stream)) return rc;
+    for (int c = 0; c < pl.chunks; ++c) {
+      const int64_t k0 = (int64_t)c * pl.len, left = a.F - k0;
+      MoeParams d = p;
+      d.kn = (int)(left < pl.len ? left : pl.len);
+      d.h = p.h + k0;
+      d.s_dn = p.s_dn + k0 / 64;
+      d.part = p.part + (int64_t)c * p.slots * a.H;
+      CUtensorMap dn;
+      const uint64_t dd[4] = {(uint64_t)((Fp - k0) / 2), (uint64_t)a.H, 1, (uint64_t)a.E};
+      const uint64_t ds[3] = {(uint64_t)(Fp / 2), (uint64_t)(a.H * (Fp / 2)), (uint64_t)(a.H * (Fp / 2))};
+      const uint32_t db[4] = {128, 2 * dbox, 1, 1};
+      if (!encode_map_4d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn + k0 / 2, dd, ds, db, CU_TENSOR_MAP_SWIZZLE_128B)) {
+        set_error_detail("moe: cuTensorMapEncodeTiled failed (or is unavailable)");
+        return Q4LIN_ERR_CUDA;
+      }
+      const uint32_t dbytes = moe_fit(d, pl.nt, true, pl.dn_form);
+      if (const int rc = moe_kernel_form<true>(pl.dn_form, pl.nt, dn, d, dbytes, sms, a.stream)) return rc;
+    }
+    if (pl.dn_form != kLatency) {
       cudaLaunchAttribute at[1];
       const int64_t n = (int64_t)tp * (a.H / 4);
       const cudaLaunchConfig_t cfg = moe_config((unsigned)((n + kReduceThreads - 1) / kReduceThreads), kReduceThreads, a.stream, at);

@@ -497,7 +497,7 @@ int q4lin_moe_router(const uint16_t* x, const uint16_t* w_router, const float* b
 size_t q4lin_moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int top_k) {
   if (T < 1 || H < 1 || F < 1 || E < 1 || E > kMaxExperts || top_k < 1 || top_k > kMaxTopK) return 0;
   if (F > kMaxDim / 2048 || H > kMaxDim / 2048 || T > (int64_t)1 << 24) return 0;
-  return q4::moe_workspace_bytes(T, H, F, top_k);
+  return q4::moe_workspace_bytes(T, H, F, E, top_k);
 }
 
 int q4lin_moe_experts(const uint16_t* x, const int32_t* ids, const float* weights, const uint8_t* wq_gate_up,
