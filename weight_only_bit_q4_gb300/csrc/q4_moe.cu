@@ -24,9 +24,9 @@
 //   down: v = h (FP32), as two fp16 terms v = hi + lo (relative error 2^-22; one term, 2^-11,
 //     shows in y: 1e-4 of its rms, and single bf16 steps).  In a tile of up to four slots the lo
 //     terms are columns of their own, which would be empty otherwise (kPairs); in a wider one
-//     their products follow the hi terms' into the same D.  Against one term: 20.3 us for 20.2
-//     (1 token, 8 of 64, 2048 x 768), 32.7 for 32.4 (4, 2 of 8, 5120 x 1408), 33.3 for 32.2 (19,
-//     3 of 20, 1992 x 1016), 89.6 for 87.0 (64, 8 of 128, 2048 x 768), 81.9 for 72.7 with 32
+//     their products follow the hi terms' into the same D.  Against one term: 20.1 us for 20.2
+//     (1 token, 8 of 64, 2048 x 768), 32.7 for 32.4 (4, 2 of 8, 5120 x 1408), 32.9 for 32.2 (19,
+//     3 of 20, 1992 x 1016), 89.4 for 88.4 (64, 8 of 128, 2048 x 768), 82 for 72.7 with 32
 //     tokens per expert (64, 4 of 8, 2048 x 2048).
 //
 // Operand layout, as in the streaming warp-MMA route: the K order inside an MMA is free as
@@ -67,6 +67,8 @@
 // Every mbarrier wait is bounded (kSpinLimit): on expiry the kernel records
 // Q4LIN_ERR_TIMEOUT, the warps stop computing, pass the CTA barriers and drain the
 // copies that they issued.
+#include <cmath>
+
 #include "q4_internal.h"
 #include "q4_sm100.cuh"
 
@@ -1070,7 +1072,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bars + 8u * (uint32_t)slot, phase)))
         ok = warp_wait(bars + 8u * (uint32_t)slot, phase, abort_flag, &g_moe_status);
       if (ok) {
-        if (4 * (sb + 1) <= groups)
+        if (!kTwo && 4 * (sb + 1) <= groups)   // (with two terms the whole box's loads do not fit the registers)
           moe_sub_box<NT, MT, true, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
         else
           moe_sub_box<NT, MT, false, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
@@ -1239,6 +1241,9 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
 // other, each behind its choice, they cost about 1.5 us more at 64 tokens x 8.
 constexpr int kReduceThreads = 128;
 
+// kMany: the down product ran in chunks of F (with their loop in it, the kernel takes 106 registers
+// for 38, and 64 tokens x 8 of 128 took 92 us for 87).
+template <bool kMany>
 __global__ void __launch_bounds__(kReduceThreads) q4_moe_reduce_kernel(const MoeParams p) {
   pdl_launch_dependents();
   constexpr int kAtOnce = 8;
@@ -1267,7 +1272,7 @@ __global__ void __launch_bounds__(kReduceThreads) q4_moe_reduce_kernel(const Moe
     float4 f[kAtOnce];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) f[j] = on[j] ? ld_global_f4(p.part + (t * p.k + j0 + j) * p.H + n) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 1; c < p.chunks; ++c) {   // (long F) the sums of the further chunks of columns, in order
+    for (int c = 1; kMany && c < p.chunks; ++c) {   // the sums of the further chunks of columns, in order
       float4 m[kAtOnce];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
@@ -1400,8 +1405,7 @@ int moe_kernel_form(int form, int nt, const CUtensorMap& tm, const MoeParams& p,
 // more, the longer items' cheaper bytes do: 64 tokens x 8 of 128, 2048 x 768, 53 items: 95.8 for
 // 89.7; 19 x 3 of 20, 1992 x 1016, 8 items: 35.5 for 33.5; even at 4.3.
 bool moe_joins(int slots, int64_t E, int64_t rows, int sms) {
-  double none = 1.0;   // (1 - 1 / E)^slots
-  for (int i = 0; i < slots; ++i) none *= 1.0 - 1.0 / (double)E;
+  const double none = std::pow(1.0 - 1.0 / (double)E, (double)slots);
   return (double)E * (1.0 - none) * (double)((rows + 15) / 16) < 4.0 * sms;
 }
 
@@ -1597,32 +1601,43 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
     p.part = reinterpret_cast<float*>(ws + w.part);
     p.y = a.y + t0 * a.H;
     p.chunks = pl.chunks;
-    MoeParams g = p;
-    const uint32_t gbytes = moe_fit(g, pl.nt, false, pl.gu_form);
-    if (const int rc = moe_kernel_form<false>(pl.gu_form, pl.nt, gu, g, gbytes, sms, a.stream)) return rc;
-    for (int c = 0; c < pl.chunks; ++c) {
+    // a chunk of the down product: its columns, map and shared memory
+    MoeParams d;
+    CUtensorMap dn;
+    uint32_t dbytes = 0;
+    auto chunk = [&](int c) -> bool {
       const int64_t k0 = (int64_t)c * pl.len, left = a.F - k0;
-      MoeParams d = p;
+      d = p;
       d.kn = (int)(left < pl.len ? left : pl.len);
       d.h = p.h + k0;
       d.s_dn = p.s_dn + k0 / 64;
       d.part = p.part + (int64_t)c * p.slots * a.H;
-      CUtensorMap dn;
+      dbytes = moe_fit(d, pl.nt, true, pl.dn_form);
       const uint64_t dd[4] = {(uint64_t)((Fp - k0) / 2), (uint64_t)a.H, 1, (uint64_t)a.E};
       const uint64_t ds[3] = {(uint64_t)(Fp / 2), (uint64_t)(a.H * (Fp / 2)), (uint64_t)(a.H * (Fp / 2))};
       const uint32_t db[4] = {128, 2 * dbox, 1, 1};
-      if (!encode_map_4d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn + k0 / 2, dd, ds, db, CU_TENSOR_MAP_SWIZZLE_128B)) {
+      return encode_map_4d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn + k0 / 2, dd, ds, db, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    MoeParams g = p;
+    const uint32_t gbytes = moe_fit(g, pl.nt, false, pl.gu_form);
+    bool encoded = chunk(0);   // (before the first launch: the two follow one another closely)
+    if (const int rc = moe_kernel_form<false>(pl.gu_form, pl.nt, gu, g, gbytes, sms, a.stream)) return rc;
+    for (int c = 0; c < pl.chunks; ++c) {
+      if (c > 0) encoded = chunk(c);
+      if (!encoded) {
         set_error_detail("moe: cuTensorMapEncodeTiled failed (or is unavailable)");
         return Q4LIN_ERR_CUDA;
       }
-      const uint32_t dbytes = moe_fit(d, pl.nt, true, pl.dn_form);
       if (const int rc = moe_kernel_form<true>(pl.dn_form, pl.nt, dn, d, dbytes, sms, a.stream)) return rc;
     }
     if (pl.dn_form != kLatency) {
       cudaLaunchAttribute at[1];
       const int64_t n = (int64_t)tp * (a.H / 4);
       const cudaLaunchConfig_t cfg = moe_config((unsigned)((n + kReduceThreads - 1) / kReduceThreads), kReduceThreads, a.stream, at);
-      if (cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_reduce_kernel, p), "moe: reduction launch")) return Q4LIN_ERR_CUDA;
+      if (cuda_check(pl.chunks > 1 ? cudaLaunchKernelEx(&cfg, q4_moe_reduce_kernel<true>, p)
+                                   : cudaLaunchKernelEx(&cfg, q4_moe_reduce_kernel<false>, p),
+                     "moe: reduction launch"))
+        return Q4LIN_ERR_CUDA;
     }
   }
   return Q4LIN_OK;

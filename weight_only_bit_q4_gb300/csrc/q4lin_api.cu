@@ -410,10 +410,16 @@ int run_router(const uint16_t* x, const uint16_t* w, const float* bias, int32_t*
 int run_experts(const uint16_t* x, const int32_t* ids, const float* weights, const uint8_t* wq_gu, const uint16_t* s_gu,
                 const uint8_t* wq_dn, const uint16_t* s_dn, uint16_t* y, int64_t T, int64_t H, int64_t F, int64_t E,
                 int top_k, void* workspace, void* stream, bool prepared = false) {
-  int st = validate_experts(x, ids, weights, wq_gu, s_gu, wq_dn, s_dn, y, T, H, F, E, top_k);
-  if (st != Q4LIN_OK || T == 0 || H == 0) return st;
-  if ((st = check_workspace(q4lin_moe_workspace_bytes(T, H, F, E, top_k), workspace)) != Q4LIN_OK) return st;
-  if ((st = check_device()) != Q4LIN_OK) return st;
+  int st = Q4LIN_OK;
+  if (!prepared) {   // (q4lin_moe has checked everything before its router)
+    st = validate_experts(x, ids, weights, wq_gu, s_gu, wq_dn, s_dn, y, T, H, F, E, top_k);
+    if (st != Q4LIN_OK) return st;
+  }
+  if (T == 0 || H == 0) return st;
+  if (!prepared) {
+    if ((st = check_workspace(q4lin_moe_workspace_bytes(T, H, F, E, top_k), workspace)) != Q4LIN_OK) return st;
+    if ((st = check_device()) != Q4LIN_OK) return st;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (F == 0) return q4::cuda_check(cudaMemsetAsync(y, 0, (size_t)T * (size_t)H * 2, s), "zero fill of y");
   q4::MoeArgs a{};
