@@ -266,10 +266,12 @@ int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t*
  *   wq_gate_up uint8 [E, 2F, Hp/2], scales_gate_up fp16 [E, 2F, Hp/64]: per expert, gate
  *     rows [0, F), then up rows; wq_down uint8 [E, H, Fp/2], scales_down fp16 [E, H, Fp/64]
  *     (Hp, Fp: H, F rounded up to 128); y bf16 [T, H] (must not overlap x)
- *   H and F multiples of 8; E * 2F and E * H below 2^31
+ *   H and F multiples of 8; E * 2F and E * H below 2^31; H up to 48000 (longer ones, which may not
+ *     fit shared memory, are refused before anything is launched where they do not)
  *   workspace: >= q4lin_moe_workspace_bytes(T, H, F, E, top_k), 256-byte aligned
- * Any T runs; the kernels are made for a few tokens (every expert that some token chose is
- * read once per pass of at most 512 / top_k tokens).  F == 0: y = +0.
+ * Any T runs; the kernels are made for a few tokens: T runs in passes of at most 512 / top_k
+ * tokens, and a pass streams the rows of an expert once for every 8 or 16 tokens that chose it
+ * (fewer where H is long: 9 of those 16 at H = 4096, 6 at 6144).  F == 0: y = +0.
  *
  * q4lin_moe is both in one call: ids and weights are outputs, and all of its arguments are
  * checked before anything is launched.  Three kernels for a pass of up to 16 choices

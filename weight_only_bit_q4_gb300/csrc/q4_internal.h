@@ -159,6 +159,8 @@ struct MoeArgs {
   void* workspace;
   cudaStream_t stream;
 };
+// Whether every pass of these sizes has a plan (a column of H values fits shared memory).
+bool moe_supported(int64_t T, int64_t H, int64_t F, int64_t E, int k);
 size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int k);
 // With a workspace the router also runs the experts' first operand pass into it (prepared).
 int moe_router_launch(const MoeArgs& a);

@@ -1501,18 +1501,35 @@ int moe_pass_tokens(int64_t T, int k) {
   return (int)(T < most ? T : most);
 }
 
-size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int k) {
-  const int tp = moe_pass_tokens(T, k), sms = moe_sm_count();
+namespace {
+
+// The plans of a call's passes: the full one's and, where there is one, the last, shorter one's.
+// f(plan, tokens); false: a pass has none.
+template <typename Fn>
+bool moe_plans(int64_t T, int64_t H, int64_t F, int64_t E, int k, Fn&& f) {
+  const int tp = moe_pass_tokens(T, k), last = (int)(T % tp), sms = moe_sm_count();
   MoePlan pl;
-  if (!moe_plan(tp, H, F, E, k, sms, &pl)) return 0;
-  size_t most = moe_ws(tp, H, F, k, pl).total;
-  if (T % tp != 0) {   // a last, shorter pass, with a plan of its own
-    const int last = (int)(T % tp);
-    if (!moe_plan(last, H, F, E, k, sms, &pl)) return 0;
-    const size_t b = moe_ws(last, H, F, k, pl).total;
+  if (!moe_plan(tp, H, F, E, k, sms, &pl)) return false;
+  f(pl, tp);
+  if (last == 0) return true;
+  if (!moe_plan(last, H, F, E, k, sms, &pl)) return false;
+  f(pl, last);
+  return true;
+}
+
+}  // namespace
+
+bool moe_supported(int64_t T, int64_t H, int64_t F, int64_t E, int k) {
+  return moe_plans(T, H, F, E, k, [](const MoePlan&, int) {});
+}
+
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t E, int k) {
+  size_t most = 0;
+  const bool ok = moe_plans(T, H, F, E, k, [&](const MoePlan& pl, int tokens) {
+    const size_t b = moe_ws(tokens, H, F, k, pl).total;
     most = b > most ? b : most;
-  }
-  return most;
+  });
+  return ok ? most : 0;
 }
 
 int moe_router_launch(const MoeArgs& a) {

@@ -309,6 +309,8 @@ int validate_experts(const void* x, const void* ids, const void* weights, const 
       (F / 8 + 1) * (512 + E) >= kMaxRows || (H / 8 + 1) * (512 + E) >= kMaxRows)
     return refuse("moe: the experts' rows exceed the 32-bit row coordinates", Q4LIN_ERR_UNSUPPORTED_SHAPE);
   if (T == 0 || H == 0) return Q4LIN_OK;
+  if (F > 0 && !q4::moe_supported(T, H, F, E, top_k))
+    return refuse("moe: a column of H values does not fit shared memory beside the rings", Q4LIN_ERR_UNSUPPORTED_SHAPE);
   if (y == nullptr) return Q4LIN_ERR_INVALID_ARG;
   if (!aligned16(y)) return Q4LIN_ERR_MISALIGNED;
   if (F == 0) return Q4LIN_OK;
