@@ -1207,12 +1207,12 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       __syncthreads();
       if (!*abort_flag) {   // y of the unit's rows: the slots' sums in the order of the choices
         const int64_t n0 = 16 * (int64_t)unit;
-        // lane 16 h + row takes every second choice; the halves meet by a shuffle
-        for (int t = warp; t < tokens; t += kWarps) {
+        // lane 16 h + row: token 2 i + h
+        for (int t = 2 * warp + (lane >> 4); t < tokens; t += 2 * kWarps) {
           const int rr = lane & 15;
           float v = 0.f;
 #pragma unroll 4
-          for (int j = lane >> 4; j < p.k; j += 2) {
+          for (int j = 0; j < p.k; ++j) {
             const int s = t * p.k + j;
             float part = 0.f;
 #pragma unroll
@@ -1220,8 +1220,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
               if (i < kp) part += sums[(i * p.slots + s) * 16 + rr];
             v = von[s] ? fmaf(wsm[s], part, v) : v;
           }
-          v += __shfl_xor_sync(0xffffffffu, v, 16);
-          if (lane < 16 && n0 + rr < p.H) p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
+          if (n0 + rr < p.H) p.y[(int64_t)t * p.H + n0 + rr] = float_to_bf16_bits(v);
         }
       }
       __syncthreads();   // the sums are free again
