@@ -79,7 +79,8 @@ q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N,
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       lora_mma(d[i], h0.x, h8.x, h0.y, h8.y, b[i].x, b[i].y);
-      lora_mma(d[i], l0.x, l8.x, l0.y, l8.y, b[i].x, b[i].y);
+      // (an infinite B times u is the first term's: the second, 0 or of either sign, would make it NaN)
+      lora_mma(d[i], l0.x, l8.x, l0.y, l8.y, lora_finite2(b[i].x), lora_finite2(b[i].y));
     }
   };
   // Row steps of 32 per warp; four fragment sets in flight: four row steps of one rank step
@@ -101,10 +102,10 @@ q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N,
       for (int j = 0; j < 2; ++j) {
         const int r = 2 * w + j;
         const float v = r < rank ? lora_u(lo, T, t0 + order[col], r) : 0.f;
-        const uint32_t hi = float_to_bf16_bits(v);
-        const float rest = v - __uint_as_float(hi << 16);
+        uint32_t hi, lw;
+        lora_terms(v, hi, lw);
         h |= hi << (16 * j);
-        l |= (fabsf(v) < INFINITY ? (uint32_t)float_to_bf16_bits(rest) : 0u) << (16 * j);
+        l |= lw << (16 * j);
       }
     }
     uh[col * kExpandPitch + w] = h;
@@ -176,8 +177,7 @@ q4_lora_spread_kernel(const LoraArgs lo, uint16_t* u, int groups, int64_t T) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float v = r0 + j < rank ? lora_u(lo, T, t, r0 + j) : 0.f;
-      h[j] = float_to_bf16_bits(v);
-      l[j] = fabsf(v) < INFINITY ? float_to_bf16_bits(v - __uint_as_float(h[j] << 16)) : 0u;
+      lora_terms(v, h[j], l[j]);
     }
     hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     lw = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);

@@ -54,6 +54,18 @@ __device__ __forceinline__ float lora_u(const LoraArgs& lo, int64_t T, int64_t t
   return v;
 }
 
+// v as two bf16 terms (bits): hi + lo, relative error 2^-17; Inf and NaN: hi alone.
+__device__ __forceinline__ void lora_terms(float v, uint32_t& hi, uint32_t& lo) {
+  const bool finite = fabsf(v) < INFINITY;
+  hi = float_to_bf16_bits(v);
+  lo = finite ? (uint32_t)float_to_bf16_bits(v - __uint_as_float(hi << 16)) : 0u;
+}
+
+// Two bf16 values with Inf and NaN taken as zero.
+__device__ __forceinline__ uint32_t lora_finite2(uint32_t w) {
+  return w & ~__vcmpeq2(w & 0x7F807F80u, 0x7F807F80u);
+}
+
 // sum of 8 products of a row chunk of B (ranks r0 .. r0 + 7, those past `rank` left out
 // whatever bits they hold) with u
 __device__ __forceinline__ float lora_dot8(uint4 b, const float* u, int left, float v) {
