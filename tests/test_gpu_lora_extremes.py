@@ -1,5 +1,6 @@
-"""LinearLora where an adapter holds infinities, on every route: the definition's infinities with
-their signs, and its NaN.  Tokens of other adapters, and other rows, within the layer's bound (8e-3 |y| + 1e-3 rms(y))."""
+"""LinearLora where an adapter holds infinities, or A x comes close to the largest FP32 value, on
+every route: the definition's infinities with their signs, its NaN, and finite values where it has
+them.  Tokens of other adapters, and other rows, within the layer's bound (8e-3 |y| + 1e-3 rms(y))."""
 import numpy as np
 import pytest
 
@@ -41,3 +42,22 @@ def test_infinities_in_b(T, L, R):
     y, plain = y.copy(), plain.copy()
     y[bad], plain[bad] = 0, 0.0
     assert_close(y, plain, f"T={T} L={L} R={R}")
+
+
+@pytest.mark.parametrize("T,L,R", ROUTES)
+def test_a_x_between_the_largest_bf16_and_the_largest_fp32(T, L, R):
+    """u = 3.4e38 rounds to an infinite bf16; times B = 2^-120 it adds 256 to y."""
+    N, K = 200, 520
+    p = list(problem(N, K, T, L, R, 9 + T, ids=np.arange(T) % L))
+    bf = lambda e: (127 + e) << 7                            # 2^e   # noqa: E731
+    x, a, b, sc = p[2].copy(), p[3].copy(), p[4].copy(), p[6].copy()
+    x[:, 64] = bf(0)
+    a[0], b[0] = 0, 0
+    a[0, 2, 64] = bf(100)
+    b[0, :, 2] = bf(-120)
+    b[0, 5, 2] = bf(-120) | 0x8000
+    sc[0] = np.float32(3.4e38) / np.float32(2.0**100)
+    p[2], p[3], p[4], p[6] = x, a, b, sc
+    want = do.linear_lora(*p)
+    assert np.isfinite(want).all() and np.abs(want[p[5] == 0]).min() > 50
+    assert_close(y_bits(call(tuple(p))), want, f"T={T} L={L} R={R}")

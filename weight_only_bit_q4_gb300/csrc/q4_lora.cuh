@@ -54,10 +54,12 @@ __device__ __forceinline__ float lora_u(const LoraArgs& lo, int64_t T, int64_t t
   return v;
 }
 
-// v as two bf16 terms (bits): hi + lo, relative error 2^-17; Inf and NaN: hi alone.
+// v as two bf16 terms (bits): hi + lo, relative error 2^-17; Inf and NaN: hi alone.  A finite v
+// whose nearest bf16 would be infinite takes the largest finite one.
 __device__ __forceinline__ void lora_terms(float v, uint32_t& hi, uint32_t& lo) {
   const bool finite = fabsf(v) < INFINITY;
   hi = float_to_bf16_bits(v);
+  if (finite && (hi & 0x7FFFu) == 0x7F80u) --hi;
   lo = finite ? (uint32_t)float_to_bf16_bits(v - __uint_as_float(hi << 16)) : 0u;
 }
 
