@@ -129,22 +129,25 @@ __device__ __forceinline__ uint4 moe_fragment(const float (&f)[8], float s1, flo
 // The same as two fp16 terms v = hi + lo (relative error 2^-22, which the sum need not follow).
 __device__ __forceinline__ uint4 moe_fragment2(const float (&f)[8], float s1, float s16, uint4& low, float& sum) {
   uint32_t b[4], l[4];
+  float v[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const float sc = (q & 1) ? s16 : s1;
-    const float v0 = f[q] * sc, v1 = f[q + 4] * sc;
-    const __half2 h = __floats2half2_rn(v0, v1);
+    v[q] = f[q] * sc;
+    v[q + 4] = f[q + 4] * sc;
+    const __half2 h = __floats2half2_rn(v[q], v[q + 4]);
     const float2 r = __half22float2(h);
-    const __half2 lo = __floats2half2_rn(v0 - r.x, v1 - r.y);
+    const __half2 lo = __floats2half2_rn(v[q] - r.x, v[q + 4] - r.y);
     b[q] = *reinterpret_cast<const uint32_t*>(&h);
     l[q] = *reinterpret_cast<const uint32_t*>(&lo);
   }
-  sum = s1 * (((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7])));
+  sum = ((v[0] + v[4]) + (v[2] + v[6])) + 16.f * ((v[1] + v[5]) + (v[3] + v[7]));
   low = make_uint4(l[0], l[1], l[2], l[3]);
   return make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 constexpr float kZeroTerm = -8.f * 5.9604644775390625e-8f;   // -8 2^-24
+constexpr float kCodePower = 16777216.f;                       // 2^24
 
 __host__ __device__ inline int64_t moe_groups(int64_t H) { return (H + 63) / 64; }
 __host__ __device__ inline int64_t moe_zs_pitch(int64_t H) { return (moe_groups(H) + 3) / 4 * 4; }
@@ -227,7 +230,9 @@ __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf
   for (int u = 0; u < kRuns; ++u) magnitude(keep[u]);
   mx = __reduce_max_sync(0xffffffffu, mx);
   const int E = (int)(mx >> 23);
-  const int e = (mx == 0 || E == 255) ? 0 : min(max(E - 141, -100), 100);
+  // (h, the product of two sums, may have any FP32 magnitude; 2^(24 + e) might be none, so the
+  // sums take 2^24 and 2^e one after the other)
+  const int e = (mx == 0 || E == 255) ? 0 : min(max(E - 141, -126), 113);
   const float s1 = exp2i(-e), s16 = exp2i(-e - 4);
   auto convert = [&](int i, const float4 (&v)[2]) {   // whole warps; the 8 lanes of a group are adjacent
     const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
@@ -256,7 +261,7 @@ __device__ __forceinline__ void moe_prep_slot(const float* h, int F, uint8_t* hf
     for (int u = 0; u < kRest; ++u)
       if (i0 + u * kLanes < nv64) convert(i0 + u * kLanes + lane, v[u]);
   }
-  if (lane == 0) *ft = exp2i(24 + e);
+  if (lane == 0) *ft = exp2i(e);
 }
 
 __device__ __forceinline__ void moe_prep_at(const RouterParams& p, int64_t t) {
@@ -1141,15 +1146,15 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         const int s = L.order[first + col] & 0xFFFF;
         const float F = kOwn ? power[s] : cpow[pcol + col];
         if constexpr (kOwn) {
-          sums[(kpart * p.slots + s) * 16 + r] = F * acc[0][n][j];
-          sums[(kpart * p.slots + s) * 16 + 8 + r] = F * acc[0][n][2 + j];
+          sums[(kpart * p.slots + s) * 16 + r] = F * (kCodePower * acc[0][n][j]);
+          sums[(kpart * p.slots + s) * 16 + 8 + r] = F * (kCodePower * acc[0][n][2 + j]);
         } else {
           const int64_t n0 = 2 * kRows * (int64_t)unit;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const int64_t ra = n0 + 8 * m + r, rb = ra + kRows;
-            if (ra < p.H) p.part[(int64_t)s * p.H + ra] = F * acc[m][n][j];
-            if (rb < p.H) p.part[(int64_t)s * p.H + rb] = F * acc[m][n][2 + j];
+            if (ra < p.H) p.part[(int64_t)s * p.H + ra] = F * (kCodePower * acc[m][n][j]);
+            if (rb < p.H) p.part[(int64_t)s * p.H + rb] = F * (kCodePower * acc[m][n][2 + j]);
           }
         }
       }
