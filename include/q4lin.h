@@ -229,7 +229,8 @@ int q4lin_fused_route(int op, int64_t N, int64_t K, int64_t T);
  *   ranks           device, int32 [L], or NULL (every rank R): adapter a uses the first
  *                   ranks[a] (taken into [0, R]) rows of A_a and columns of B_a; the others
  *                   are not used, whatever bits they hold
- *   R               multiple of 8, 0 .. 256 (otherwise Q4LIN_ERR_UNSUPPORTED_SHAPE)
+ *   R               multiple of 8, 0 .. 256 (otherwise Q4LIN_ERR_UNSUPPORTED_SHAPE; so are more
+ *                   than 65535 * 1024 rows on the tile route, beyond 32 tokens)
  *   workspace       device, >= q4lin_lora_workspace_bytes(N, K, T, L, R), 256-byte aligned
  * A x is formed in FP32 from the bf16 values; up to 32 tokens the second product is FP32
  * too, beyond (the tile route) A x enters it as two bf16 terms (relative error 2^-17).

@@ -328,7 +328,8 @@ int validate_experts(const void* x, const void* ids, const void* weights, const 
 int lora_route(int64_t N, int64_t K, int64_t T, int R) {
   if (T == 1 && q4::gemv_lora_ok(N, K, R)) return Q4LIN_ROUTE_GEMV;
   if (T <= kMmaMaxT && q4::mma_lora_supported(N, K, T, R)) return Q4LIN_ROUTE_STREAM_MMA;
-  if (q4::tc_supported(N, K, T) && N < (int64_t)1 << 26) return Q4LIN_ROUTE_TC_SPLITK;
+  // (the second product's grid: 65535 CTAs of 1024 rows)
+  if (q4::tc_supported(N, K, T) && N <= (int64_t)65535 * 1024) return Q4LIN_ROUTE_TC_SPLITK;
   return -1;
 }
 
