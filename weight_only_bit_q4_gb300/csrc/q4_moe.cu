@@ -1367,6 +1367,10 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p, uint32_t bytes,
       return Q4LIN_ERR_CUDA;
     if (dev < 64) attr[dev] = true;
   }
+  if (bytes == 0) {   // (moe_plan leaves no such form: a kernel without its shared memory would write past it)
+    set_error_detail("moe: this form does not fit shared memory");
+    return Q4LIN_ERR_UNSUPPORTED_SHAPE;
+  }
   int grid = sms;
   if (kDown && kForm == kLatency) {   // whole units
     const int64_t nu = (p.H + 15) / 16;
