@@ -104,7 +104,7 @@ struct MmaParams {
   uint32_t red_off, gate_off, bar_off;
 };
 
-// LinearLora (a type of its own: with these fields the plain layer's parameters cost it 0.5 us)
+// LinearLora (a type of its own, as the tile kernel's, where the further fields cost the plain layer)
 struct MmaLoraParams : MmaParams {
   uint32_t lora_off;   // u [8 NT, R] fp32, then the tokens' adapters and ranks
   LoraArgs lora;       // the adapters (ids and u of this pass's tokens)

@@ -1409,9 +1409,10 @@ int moe_kernel_form(int form, int nt, const CUtensorMap& tm, const MoeParams& p,
 // Joined or throughput, by the likely number of a CTA's items (slots spread evenly over the
 // experts).  With less than one long item per SM sub-partition the item's own latency is the
 // time, and shorter items with shared K win: down product of 19 tokens x 6 of 9, 584 x 1944, 1.1
-// items: the layer takes 37 us for 60; 20 x 4 of 16, 1024 x 1024, 3.4 items: 25.8 for 27.2.  With
-// more, the longer items' cheaper bytes do: 64 tokens x 8 of 128, 2048 x 768, 53 items: 95.8 for
-// 89.7; 19 x 3 of 20, 1992 x 1016, 8 items: 35.5 for 33.5; even at 4.3.
+// items: the layer takes 37 us for 60; gate/up of 32 x 2 of 8, 2048 x 768, 2.5 items: 26.0 for
+// 32.4; of 16 x 2 of 8, 4096 x 1024, 3.3 items: 34.5 for 44.4.  With more, the longer items'
+// cheaper bytes do: 19 x 3 of 20, 1992 x 1016, 8 items: 35.4 for 32.6 in either product; 64 x 8 of
+// 128, 2048 x 768, 40 items: 108.6 for 88.8 (gate/up), 97.3 for 88.8 (down); even at 4.3.
 bool moe_joins(int slots, int64_t E, int64_t rows, int sms) {
   const double none = std::pow(1.0 - 1.0 / (double)E, (double)slots);
   return (double)E * (1.0 - none) * (double)((rows + 15) / 16) < 4.0 * sms;
@@ -1449,19 +1450,21 @@ bool moe_plan(int tokens, int64_t H, int64_t F, int64_t E, int k, int sms, MoePl
   if (fit(false, pl->gu_form, H) == 0) return false;
   pl->chunks = 1;
   pl->len = (int)F;
+  // (64 KB of columns and less: 20.4 us for 21.8, one token x 8 of 64, 2048 x 768; 134 KB: 30.6 for
+  // 35.2, 16 tokens x 1 of 8, 2048 x 2048, and 40.5 for 39.1, 2 x 8 of 16)
   if (p.slots <= kLatSlots && fit(true, kLatency, F) > 0) {
     pl->gu_form = pl->dn_form = kLatency;
     return true;
   }
   // The throughput form only with whole tiles.  Narrower ones decode their rows again for every few
   // slots, and joined they are wider (its rings are half as large): 64 tokens x 2 of 8, 5120 x 1408,
-  // 13 columns of 16 for 8: 124 us for 116; 4 x 2 of 8, 4096 x 14336, one column for two: 259 for 206.
+  // 13 columns of 16 for 8: 115 us for 109; 4 x 2 of 8, 4096 x 14336, one column for four: 259 for 170.
   const int width = 8 * pl->nt < tokens ? 8 * pl->nt : tokens;
   pl->dn_form = moe_joins(p.slots, E, H / 2, sms) || fit(true, kThroughput, F) < width ? kJoined : kThroughput;
   if (pl->dn_form == kThroughput) return true;
   // Chunks of F that keep tiles of four slots, of eight where an expert gets more than four on
-  // average: 64 tokens x 2 of 8, 4096 x 14336: 777 us in one launch (two slots per tile), 629 with
-  // four, 599 with eight; 16 tokens: 291, 266, 291; 8 tokens, 6144 x 32768: 815, 637, 684.
+  // average: 64 tokens x 2 of 8, 4096 x 14336: 716 us in one launch (two slots per tile), 592 with
+  // four, 551 with eight; 16 tokens: 274, 215, 247; 8 tokens, 6144 x 32768: 727, 588, 662.
   const int even = p.slots > 4 * E ? 8 : 4, want = even < tokens ? even : tokens;
   const int nsb = (int)((F + 255) / 256);
   for (int c = 1; c <= nsb; ++c) {

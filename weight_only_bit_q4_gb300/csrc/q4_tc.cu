@@ -108,8 +108,8 @@ struct TcParams {
 // LinearLora.  Mode 3: the accumulators start from the FP32 term delta [T, N rounded up to 8].
 // Mode 4: the adapters' second product as `ug` further groups after the nk of the planes, scale 1:
 // X tile u (bf16 terms hi and lo alternating, map in the high-plane slot), A tile 64 columns of the
-// adapters' B side by side.  (A type of its own: with these fields the other forms' parameters cost
-// them 1 us at T = 1024.)
+// adapters' B side by side.  (A type of its own: with these fields in its parameters the plain layer
+// takes 88.5 us for 87.1 at 6144 x 5120, T = 1024.)
 struct TcLoraParams : TcParams {
   const float* delta;
   int ug;
