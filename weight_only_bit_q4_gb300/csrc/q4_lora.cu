@@ -76,12 +76,19 @@ q4_lora_expand_kernel(const LoraArgs lo, float* delta, int64_t pitch, int64_t N,
     const int at = g * kExpandPitch + (r0 + 4 * c) / 2, at8 = at + 8 * kExpandPitch;
     const uint2 h0 = *reinterpret_cast<const uint2*>(uh + at), h8 = *reinterpret_cast<const uint2*>(uh + at8);
     const uint2 l0 = *reinterpret_cast<const uint2*>(ul + at), l8 = *reinterpret_cast<const uint2*>(ul + at8);
+    uint32_t top = 0u;   // largest magnitudes of this thread's B
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       lora_mma(d[i], h0.x, h8.x, h0.y, h8.y, b[i].x, b[i].y);
-      // (an infinite B times u is the first term's: the second, 0 or of either sign, would make it NaN)
-      lora_mma(d[i], l0.x, l8.x, l0.y, l8.y, lora_finite2(b[i].x), lora_finite2(b[i].y));
+      top = __vmaxu2(top, __vmaxu2(b[i].x & 0x7FFF7FFFu, b[i].y & 0x7FFF7FFFu));
     }
+    // An infinite B times u is the first term's: the second, 0 or of either sign, would make it NaN.
+    if (__any_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16) >= 0x7F80u)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = make_uint2(lora_finite2(b[i].x), lora_finite2(b[i].y));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lora_mma(d[i], l0.x, l8.x, l0.y, l8.y, b[i].x, b[i].y);
   };
   // Row steps of 32 per warp; four fragment sets in flight: four row steps of one rank step
   // (rank <= 16), or one row step of four rank steps.
