@@ -271,8 +271,8 @@ int q4lin_linear_lora(const uint8_t* wq, const uint16_t* scales, const uint16_t*
  *     fit shared memory, are refused before anything is launched where they do not)
  *   workspace: >= q4lin_moe_workspace_bytes(T, H, F, E, top_k), 256-byte aligned
  * Any T runs; the kernels are made for a few tokens: T runs in passes of at most 512 / top_k
- * tokens, and a pass streams the rows of an expert once for every 8 or 16 tokens that chose it
- * (fewer where H is long: 9 of those 16 at H = 4096, 6 at 6144).  F == 0: y = +0.
+ * tokens, and a pass streams the rows of an expert once for every 8 tokens that chose it (fewer
+ * where H is long: 7 at H = 5120, 4 at 8192).  F == 0: y = +0.
  *
  * q4lin_moe is both in one call: ids and weights are outputs, and all of its arguments are
  * checked before anything is launched.  Three kernels for a pass of up to 16 choices

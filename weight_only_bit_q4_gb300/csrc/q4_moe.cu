@@ -11,7 +11,7 @@
 // over the choices: kernels chained by programmatic dependent launch.  Bound: the packed weights of
 // the experts that some token chose, each read once; the kernels below therefore sort
 // the (token, choice) slots by expert and stream each chosen expert's rows once for all
-// of its tokens that fit a tile (up to 8 NT token columns, fewer where columns are long).
+// of its tokens that fit a tile (up to 8 token columns, fewer where columns are long).
 //
 // Products.  mma.sync m16n8k16 (fp16 x fp16 -> fp32); the 64 weights of a scale group go
 // through four MMAs into a fresh D, then acc += s D in FP32.  A: a masked nibble pair is the
@@ -33,6 +33,10 @@
 // long as A and B agree, so thread (g = lane / 4, c = lane % 4) takes the 16 weights
 // k = 16 c .. 16 c + 15 of a group (8 code bytes per row) and the same 16 values of token
 // column g (two 16-byte loads of fragments stored in the pairs (k, k + 4) of the masks).
+//
+// A warp takes one tile of 8 columns at a time.  Two (16 tokens of an expert per pass over its rows)
+// spill registers, and lost at every load: 64 tokens x 8 of 64, 2048 x 768 98 us for 70; x 2 of 8,
+// 5120 x 1408 112 for 83; 512 x 1 of 8, 4096 x 2048 305 for 218; no gain anywhere.
 //
 // A unit is 16 MT MMA rows = two boxes of 8 MT weight rows: gate rows f0 .. over up rows
 // f0 .. (a thread then holds g and u of the same f and token), or 16 MT rows of W_down.
@@ -78,7 +82,6 @@ namespace {
 
 __device__ int g_moe_status = 0;
 
-constexpr int kMaxNT = 2;                   // column tiles of 8 handled together (4 spill)
 constexpr int kLatSlots = 16;               // up to here the latency form
 enum { kThroughput = 0, kLatency = 1, kJoined = 2 };
 constexpr int kMaxParts = 4;                // warps that share the K range of an item, at most
@@ -545,13 +548,13 @@ struct MoeParams {
   int E, k, slots;         // slots = T k of this pass
   int chunks;              // launches of the down product
   int depth;               // ring slots per warp
-  int per;                 // columns per tile, at most (8 NT, fewer where a column is long)
+  int per;                 // columns per tile, at most (8, fewer where a column is long)
   int gtiles;              // tiles whose columns lie in shared memory together
   uint32_t col_bytes;      // shared memory of a column
   uint32_t bar_off, cnt_off, wcnt_off, order_off, tiles_off, misc_off, pow_off, sum_off, col_off;   // shared memory
 };
 
-// Shared-memory lists of one CTA: the tiles (up to 8 kMaxNT slots of one expert) in
+// Shared-memory lists of one CTA: the tiles (up to 8 slots of one expert) in
 // expert order.
 struct MoeLists {
   int* cnt;        // [E] first positions
@@ -695,19 +698,19 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // scales (global memory) and its B columns (shared memory) start.  Plain loads (not the
 // volatile ones) in the loops, so that the compiler can overlap the groups of a sub-box; the
 // waits before them are compiler barriers.
-template <int NT, int MT>
+template <int MT>
 struct MoeUnit {
   const uint16_t* s0[MT];    // scales of MMA rows g and g + 8
   const uint16_t* s1[MT];
-  const uint8_t* b[NT];      // fragments of thread column g
-  const float* z[NT][2];     // zero-point terms of token columns 2c, 2c + 1
+  const uint8_t* b;          // fragments of thread column g
+  const float* z[2];         // zero-point terms of token columns 2c, 2c + 1
 };
 
-// acc[m][n] += the products of the sub-box with the groups G0 .. G0 + 3 (kFull: all of them
+// acc[m] += the products of the sub-box with the groups G0 .. G0 + 3 (kFull: all of them
 // exist; kTwo: and those of the second terms, groups * 128 bytes behind the first).
-template <int NT, int MT, bool kFull, bool kTwo>
+template <int MT, bool kFull, bool kTwo>
 __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t (&off)[4], int G0, int groups,
-                                            const MoeUnit<NT, MT>& un, int nt, float (&acc)[MT][NT][4]) {
+                                            const MoeUnit<MT>& un, float (&acc)[MT][4]) {
   __half2 s0[MT][2], s1[MT][2];   // (the plane rows hold an even number of scales)
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -718,11 +721,9 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
         s1[m][i] = *reinterpret_cast<const __half2*>(un.s1[m] + G0 + 2 * i);
       }
     }
-  float4 z[NT][2];   // the four groups' terms (the rows are padded to a multiple of four)
+  float4 z[2];   // the four groups' terms (the rows are padded to a multiple of four)
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) z[n][j] = *reinterpret_cast<const float4*>(un.z[n][j] + G0);
+  for (int j = 0; j < 2; ++j) z[j] = *reinterpret_cast<const float4*>(un.z[j] + G0);
 #pragma unroll
   for (int gl = 0; gl < 4; ++gl) {
     const int G = G0 + gl;
@@ -733,39 +734,35 @@ __device__ __forceinline__ void moe_sub_box(const uint8_t* slot, const uint32_t 
       decode_pairs(*reinterpret_cast<const uint2*>(slot + off[gl] + 1024 * m), a0[m]);
       decode_pairs(*reinterpret_cast<const uint2*>(slot + off[gl] + 1024 * (MT + m)), a1[m]);
     }
+    const uint8_t* at = un.b + (size_t)G * 128;
+    const uint4 b0 = *reinterpret_cast<const uint4*>(at), b1 = *reinterpret_cast<const uint4*>(at + 64);
+    uint4 c0, c1;
+    if constexpr (kTwo) {
+      c0 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128);
+      c1 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128 + 64);
+    }
+    const float za = gl == 0 ? z[0].x : gl == 1 ? z[0].y : gl == 2 ? z[0].z : z[0].w;
+    const float zb = gl == 0 ? z[1].x : gl == 1 ? z[1].y : gl == 2 ? z[1].z : z[1].w;
+    const float zz[4] = {za, zb, za, zb};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (NT > 1 && n >= nt) break;
-      const uint8_t* at = un.b[n] + (size_t)G * 128;
-      const uint4 b0 = *reinterpret_cast<const uint4*>(at), b1 = *reinterpret_cast<const uint4*>(at + 64);
-      uint4 c0, c1;
+    for (int m = 0; m < MT; ++m) {
+      float d[4];
+      mma_f16_16816(d, a0[m][0], a1[m][0], a0[m][1], a1[m][1], b0.x, b0.y, zz);
+      mma_f16_16816(d, a0[m][2], a1[m][2], a0[m][3], a1[m][3], b0.z, b0.w, d);
+      mma_f16_16816(d, a0[m][4], a1[m][4], a0[m][5], a1[m][5], b1.x, b1.y, d);
+      mma_f16_16816(d, a0[m][6], a1[m][6], a0[m][7], a1[m][7], b1.z, b1.w, d);
       if constexpr (kTwo) {
-        c0 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128);
-        c1 = *reinterpret_cast<const uint4*>(at + (size_t)groups * 128 + 64);
+        mma_f16_16816(d, a0[m][0], a1[m][0], a0[m][1], a1[m][1], c0.x, c0.y, d);
+        mma_f16_16816(d, a0[m][2], a1[m][2], a0[m][3], a1[m][3], c0.z, c0.w, d);
+        mma_f16_16816(d, a0[m][4], a1[m][4], a0[m][5], a1[m][5], c1.x, c1.y, d);
+        mma_f16_16816(d, a0[m][6], a1[m][6], a0[m][7], a1[m][7], c1.z, c1.w, d);
       }
-      const float za = gl == 0 ? z[n][0].x : gl == 1 ? z[n][0].y : gl == 2 ? z[n][0].z : z[n][0].w;
-      const float zb = gl == 0 ? z[n][1].x : gl == 1 ? z[n][1].y : gl == 2 ? z[n][1].z : z[n][1].w;
-      const float zz[4] = {za, zb, za, zb};
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float d[4];
-        mma_f16_16816(d, a0[m][0], a1[m][0], a0[m][1], a1[m][1], b0.x, b0.y, zz);
-        mma_f16_16816(d, a0[m][2], a1[m][2], a0[m][3], a1[m][3], b0.z, b0.w, d);
-        mma_f16_16816(d, a0[m][4], a1[m][4], a0[m][5], a1[m][5], b1.x, b1.y, d);
-        mma_f16_16816(d, a0[m][6], a1[m][6], a0[m][7], a1[m][7], b1.z, b1.w, d);
-        if constexpr (kTwo) {
-          mma_f16_16816(d, a0[m][0], a1[m][0], a0[m][1], a1[m][1], c0.x, c0.y, d);
-          mma_f16_16816(d, a0[m][2], a1[m][2], a0[m][3], a1[m][3], c0.z, c0.w, d);
-          mma_f16_16816(d, a0[m][4], a1[m][4], a0[m][5], a1[m][5], c1.x, c1.y, d);
-          mma_f16_16816(d, a0[m][6], a1[m][6], a0[m][7], a1[m][7], c1.z, c1.w, d);
-        }
-        const float sa = (gl & 1) ? __high2float(s0[m][gl >> 1]) : __low2float(s0[m][gl >> 1]);
-        const float sb = (gl & 1) ? __high2float(s1[m][gl >> 1]) : __low2float(s1[m][gl >> 1]);
-        acc[m][n][0] = fmaf(sa, d[0], acc[m][n][0]);
-        acc[m][n][1] = fmaf(sa, d[1], acc[m][n][1]);
-        acc[m][n][2] = fmaf(sb, d[2], acc[m][n][2]);
-        acc[m][n][3] = fmaf(sb, d[3], acc[m][n][3]);
-      }
+      const float sa = (gl & 1) ? __high2float(s0[m][gl >> 1]) : __low2float(s0[m][gl >> 1]);
+      const float sb = (gl & 1) ? __high2float(s1[m][gl >> 1]) : __low2float(s1[m][gl >> 1]);
+      acc[m][0] = fmaf(sa, d[0], acc[m][0]);
+      acc[m][1] = fmaf(sa, d[1], acc[m][1]);
+      acc[m][2] = fmaf(sb, d[2], acc[m][2]);
+      acc[m][3] = fmaf(sb, d[3], acc[m][3]);
     }
   }
 }
@@ -814,12 +811,12 @@ __host__ inline uint32_t moe_layout(MoeParams& p, int mt, bool down, int form) {
 
 // kDown false: gate/up units, h written; true: down units, y (latency) or part written.
 // kPairs (down, tiles of up to four slots): the second terms in columns of their own.
-template <int NT, int MT, bool kDown, int kForm, bool kPairs>
+template <int MT, bool kDown, int kForm, bool kPairs>
 __global__ void __launch_bounds__(32 * kMoeWarps, 1)
 q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  static_assert(!kPairs || (kDown && NT == 1), "pairs of columns: the down product, one column tile");
+  static_assert(!kPairs || kDown, "pairs of columns: the down product");
   constexpr bool kTwo = kDown && !kPairs;   // the second terms' products follow the first
   constexpr int kRows = 8 * MT, kWarps = kMoeWarps, kThreads = 32 * kWarps;
   const int kPer = p.per;
@@ -1036,12 +1033,11 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
   for (int gl = 0; gl < 4; ++gl)
     off[gl] = (uint32_t)r * 128u + (((((uint32_t)(2 * gl + (c >> 1))) ^ (uint32_t)r) << 4) | (uint32_t)((c & 1) << 3));
   // products of an item over this warp's K part; next: the item after it
-  auto compute = [&](const Pos& q, const Pos& next, float (&acc)[MT][NT][4], int& first, int& count) {
+  auto compute = [&](const Pos& q, const Pos& next, float (&acc)[MT][4], int& first, int& count) {
     const int2 tl = L.tiles[q.tile];
     first = tl.y & 0xFFFF;
     count = tl.y >> 16;
-    const int nt = (count + 7) / 8;
-    MoeUnit<NT, MT> un;
+    MoeUnit<MT> un;
     const int64_t row0 = (int64_t)tl.x * rows_e + (int64_t)q.unit * (kDown ? 2 * kRows : kRows);
     const int64_t row1 = row0 + (kDown ? (int64_t)kRows : p.F);
 #pragma unroll
@@ -1060,16 +1056,11 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
     // (kPairs: column i is the first term of slot i, column 4 + i its second)
     const uint32_t bterm = kPairs && g >= 4 ? fbytes / 2 : 0u, zterm = kPairs && c >= 2 ? zbytes : 0u;
     constexpr int width = kPairs ? 3 : 7;
+    un.b = column(g & width) + bterm + 16 * c;
+    un.z[0] = reinterpret_cast<const float*>(column(2 * c & width) + fbytes + zterm);
+    un.z[1] = reinterpret_cast<const float*>(column((2 * c & width) + 1) + fbytes + zterm);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      un.b[n] = column(8 * n + (g & width)) + bterm + 16 * c;
-      un.z[n][0] = reinterpret_cast<const float*>(column(8 * n + (2 * c & width)) + fbytes + zterm);
-      un.z[n][1] = reinterpret_cast<const float*>(column(8 * n + (2 * c & width) + 1) + fbytes + zterm);
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
     if (next.left > 0) for_scale_lines(next, [&](const uint8_t* a) { prefetch_l2(a); });   // the next unit's scales
     for (int sb = sb0; sb < sb1; ++sb) {
       // every lane polls and the warp votes (a lane's answer is its own, and warp_wait wants the
@@ -1078,9 +1069,9 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         ok = warp_wait(bars + 8u * (uint32_t)slot, phase, abort_flag, &g_moe_status);
       if (ok) {
         if (!kTwo && 4 * (sb + 1) <= groups)   // (with two terms the whole box's loads do not fit the registers)
-          moe_sub_box<NT, MT, true, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
+          moe_sub_box<MT, true, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, acc);
         else
-          moe_sub_box<NT, MT, false, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, nt, acc);
+          moe_sub_box<MT, false, kTwo>(ring + slot * kSlot, off, 4 * sb, groups, un, acc);
         __threadfence_block();   // every lane's reads of the slot lie before its refill
         __syncwarp();
         if (lane == 0 && is.left > 0) issue();   // refill the slot just read
@@ -1094,7 +1085,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[m][0][j] += __shfl_down_sync(0xffffffffu, acc[m][0][j], 2);
+        for (int j = 0; j < 4; ++j) acc[m][j] += __shfl_down_sync(0xffffffffu, acc[m][j], 2);
     }
   };
 
@@ -1112,50 +1103,42 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
     ++group;
   };
   Pos pos = start();
-  auto activate = [&](const float (&acc)[MT][NT][4], int first, int count, int unit) {
+  auto activate = [&](const float (&acc)[MT][4], int first, int count, int unit) {
     // thread (g, c) holds gate and up of row f of token columns 2c, 2c + 1
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (NT > 1 && 8 * n >= count) break;
+    for (int j = 0; j < 2; ++j) {
+      const int col = 2 * c + j;
+      if (col >= count) continue;
+      const int o = L.order[first + col];
+      const float F = power[o >> 16];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = 8 * n + 2 * c + j;
-        if (col >= count) continue;
-        const int o = L.order[first + col];
-        const float F = power[o >> 16];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int64_t f = kRows * (int64_t)unit + 8 * m;
-          if (f >= p.F) continue;
-          const float gt = F * acc[m][n][j], up = F * acc[m][n][2 + j];
-          const float h = gt / (1.f + expf(-gt)) * up;
-          p.h[(int64_t)(o & 0xFFFF) * p.F + f + r] = h;
-        }
+      for (int m = 0; m < MT; ++m) {
+        const int64_t f = kRows * (int64_t)unit + 8 * m;
+        if (f >= p.F) continue;
+        const float gt = F * acc[m][j], up = F * acc[m][2 + j];
+        const float h = gt / (1.f + expf(-gt)) * up;
+        p.h[(int64_t)(o & 0xFFFF) * p.F + f + r] = h;
       }
     }
   };
   // pcol: the tile's first staged column
-  auto store = [&](const float (&acc)[MT][NT][4], int first, int count, int unit, int pcol) {
+  auto store = [&](const float (&acc)[MT][4], int first, int count, int unit, int pcol) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (NT > 1 && 8 * n >= count) break;
+    for (int j = 0; j < 2; ++j) {
+      const int col = 2 * c + j;
+      if (col >= count) continue;
+      const int s = L.order[first + col] & 0xFFFF;
+      const float F = kOwn ? power[s] : cpow[pcol + col];
+      if constexpr (kOwn) {
+        sums[(kpart * p.slots + s) * 16 + r] = F * (kCodePower * acc[0][j]);
+        sums[(kpart * p.slots + s) * 16 + 8 + r] = F * (kCodePower * acc[0][2 + j]);
+      } else {
+        const int64_t n0 = 2 * kRows * (int64_t)unit;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = 8 * n + 2 * c + j;
-        if (col >= count) continue;
-        const int s = L.order[first + col] & 0xFFFF;
-        const float F = kOwn ? power[s] : cpow[pcol + col];
-        if constexpr (kOwn) {
-          sums[(kpart * p.slots + s) * 16 + r] = F * (kCodePower * acc[0][n][j]);
-          sums[(kpart * p.slots + s) * 16 + 8 + r] = F * (kCodePower * acc[0][n][2 + j]);
-        } else {
-          const int64_t n0 = 2 * kRows * (int64_t)unit;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const int64_t ra = n0 + 8 * m + r, rb = ra + kRows;
-            if (ra < p.H) p.part[(int64_t)s * p.H + ra] = F * (kCodePower * acc[m][n][j]);
-            if (rb < p.H) p.part[(int64_t)s * p.H + rb] = F * (kCodePower * acc[m][n][2 + j]);
-          }
+        for (int m = 0; m < MT; ++m) {
+          const int64_t ra = n0 + 8 * m + r, rb = ra + kRows;
+          if (ra < p.H) p.part[(int64_t)s * p.H + ra] = F * (kCodePower * acc[m][j]);
+          if (rb < p.H) p.part[(int64_t)s * p.H + rb] = F * (kCodePower * acc[m][2 + j]);
         }
       }
     }
@@ -1172,22 +1155,22 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
         if (kp == 1 && !have) break;
         const Pos q = pos;
         if (have) step(pos);
-        float acc[MT][NT][4];
+        float acc[MT][4];
         int first = 0, count = 0;
         if (have) compute(q, pos, acc, first, count);
         if constexpr (kJoin) {
           if (kp > 1) {   // part 0 adds the others' accumulators, in order
             float4* ex = reinterpret_cast<float4*>(sums) + parity * kThreads;
             parity ^= 1;
-            if (have && kpart > 0) ex[threadIdx.x] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][0][2], acc[0][0][3]);
+            if (have && kpart > 0) ex[threadIdx.x] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
             __syncthreads();
             if (!have || kpart > 0) continue;
             for (int i = 1; i < kp; ++i) {
               const float4 v = ex[threadIdx.x + 32 * i];
-              acc[0][0][0] += v.x;
-              acc[0][0][1] += v.y;
-              acc[0][0][2] += v.z;
-              acc[0][0][3] += v.w;
+              acc[0][0] += v.x;
+              acc[0][1] += v.y;
+              acc[0][2] += v.z;
+              acc[0][3] += v.w;
             }
           }
         }
@@ -1204,7 +1187,7 @@ q4_moe_kernel(const __grid_constant__ CUtensorMap tm, const MoeParams p) {
       while (pos.left > 0 && pos.unit == unit) {
         const Pos q = pos;
         step(pos);
-        float acc[MT][NT][4];
+        float acc[MT][4];
         int first, count;
         compute(q, pos, acc, first, count);
         if (ok) store(acc, first, count, unit, 0);
@@ -1317,13 +1300,12 @@ constexpr uint32_t kMoeSmem = 208 * 1024;
 // columns of one or two tiles beside rings of two slots per warp; then as many slots (up to four)
 // as there is room for, and more tiles together, where they are short.  Long columns: fewer per
 // tile.  0: a column of this length does not fit at all.
-uint32_t moe_fit(MoeParams& p, int nt, bool down, int form) {
+uint32_t moe_fit(MoeParams& p, bool down, int form) {
   const int mt = form == kThroughput ? 2 : 1;
   const bool own = down && form == kLatency;
   const int tokens = p.slots / p.k;   // (an expert gets a token once, as a rule)
-  if (form != kThroughput) nt = 1;
   p.col_bytes = moe_column_bytes(p.kn, down ? 2 : 1);
-  p.per = 8 * nt < tokens ? 8 * nt : tokens;
+  p.per = tokens < 8 ? tokens : 8;
   p.depth = 2;
   p.gtiles = own ? 1 : 2;
   uint32_t bytes = moe_layout(p, mt, down, form);
@@ -1355,13 +1337,13 @@ uint32_t moe_fit(MoeParams& p, int nt, bool down, int form) {
   return bytes;
 }
 
-template <int NT, int MT, bool kDown, int kForm, bool kPairs = false>
+template <int MT, bool kDown, int kForm, bool kPairs = false>
 int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p, uint32_t bytes, int sms, cudaStream_t stream) {
   static bool attr[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !attr[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<NT, MT, kDown, kForm, kPairs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cuda_check(cudaFuncSetAttribute(q4_moe_kernel<MT, kDown, kForm, kPairs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)kMoeSmem),
                    "moe: cudaFuncSetAttribute"))
       return Q4LIN_ERR_CUDA;
@@ -1386,24 +1368,23 @@ int moe_kernel_launch(const CUtensorMap& tm, const MoeParams& p, uint32_t bytes,
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<NT, MT, kDown, kForm, kPairs>, tm, p),
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_moe_kernel<MT, kDown, kForm, kPairs>, tm, p),
                     kDown ? "moe: down kernel launch" : "moe: gate/up kernel launch");
 }
 
 template <bool kDown>
-int moe_kernel_form(int form, int nt, const CUtensorMap& tm, const MoeParams& p, uint32_t bytes, int sms, cudaStream_t stream) {
+int moe_kernel_form(int form, const CUtensorMap& tm, const MoeParams& p, uint32_t bytes, int sms, cudaStream_t stream) {
   if constexpr (kDown) {
     if (p.per <= 4) {
-      if (form == kLatency) return moe_kernel_launch<1, 1, true, kLatency, true>(tm, p, bytes, sms, stream);
-      if (form == kJoined) return moe_kernel_launch<1, 1, true, kJoined, true>(tm, p, bytes, sms, stream);
-      return moe_kernel_launch<1, 2, true, kThroughput, true>(tm, p, bytes, sms, stream);
+      if (form == kLatency) return moe_kernel_launch<1, true, kLatency, true>(tm, p, bytes, sms, stream);
+      if (form == kJoined) return moe_kernel_launch<1, true, kJoined, true>(tm, p, bytes, sms, stream);
+      return moe_kernel_launch<2, true, kThroughput, true>(tm, p, bytes, sms, stream);
     }
-    if (form == kLatency) return moe_kernel_launch<1, 1, true, kLatency>(tm, p, bytes, sms, stream);
+    if (form == kLatency) return moe_kernel_launch<1, true, kLatency>(tm, p, bytes, sms, stream);
   }
   // (the latency form's gate/up is the joined one)
-  if (form != kThroughput) return moe_kernel_launch<1, 1, kDown, kJoined>(tm, p, bytes, sms, stream);
-  if (nt <= 1) return moe_kernel_launch<1, 2, kDown, kThroughput>(tm, p, bytes, sms, stream);
-  return moe_kernel_launch<kMaxNT, 2, kDown, kThroughput>(tm, p, bytes, sms, stream);
+  if (form != kThroughput) return moe_kernel_launch<1, kDown, kJoined>(tm, p, bytes, sms, stream);
+  return moe_kernel_launch<2, kDown, kThroughput>(tm, p, bytes, sms, stream);
 }
 
 // Joined or throughput, by the likely number of a CTA's items (slots spread evenly over the
@@ -1430,21 +1411,19 @@ MoeParams moe_params(int tokens, int64_t H, int64_t F, int64_t E, int k) {
   return p;
 }
 
-// How a pass of `tokens` tokens runs: the forms of its two products, token tiles handled together,
-// and the chunks of F columns (a launch of the down product each) with their length.
+// How a pass of `tokens` tokens runs (its sizes decide alone): the forms of its two products, and the
+// chunks of F columns (a launch of the down product each) with their length.
 struct MoePlan {
-  int nt, gu_form, dn_form, chunks, len;
+  int gu_form, dn_form, chunks, len;
 };
 
 // False: a column of H values does not fit shared memory beside the rings.
 bool moe_plan(int tokens, int64_t H, int64_t F, int64_t E, int k, int sms, MoePlan* pl) {
   const MoeParams p = moe_params(tokens, H, F, E, k);
-  // token tiles handled together: two where an expert gets more than a few slots on average
-  pl->nt = (int64_t)p.slots > 6 * E ? 2 : 1;
   auto fit = [&](bool down, int form, int64_t columns) {   // the tile width, 0: does not fit
     MoeParams q = p;
     q.kn = (int)columns;
-    return moe_fit(q, pl->nt, down, form) != 0 ? q.per : 0;
+    return moe_fit(q, down, form) != 0 ? q.per : 0;
   };
   pl->gu_form = moe_joins(p.slots, E, F, sms) || fit(false, kThroughput, H) == 0 ? kJoined : kThroughput;
   if (fit(false, pl->gu_form, H) == 0) return false;
@@ -1457,9 +1436,9 @@ bool moe_plan(int tokens, int64_t H, int64_t F, int64_t E, int k, int sms, MoePl
     return true;
   }
   // The throughput form only with whole tiles.  Narrower ones decode their rows again for every few
-  // slots, and joined they are wider (its rings are half as large): 64 tokens x 2 of 8, 5120 x 1408,
-  // 13 columns of 16 for 8: 115 us for 109; 4 x 2 of 8, 4096 x 14336, one column for four: 259 for 170.
-  const int width = 8 * pl->nt < tokens ? 8 * pl->nt : tokens;
+  // slots, and joined they are wider (its rings are half as large): 4 tokens x 2 of 8, 4096 x 14336,
+  // one column for four: 259 us for 170.
+  const int width = tokens < 8 ? tokens : 8;
   pl->dn_form = moe_joins(p.slots, E, H / 2, sms) || fit(true, kThroughput, F) < width ? kJoined : kThroughput;
   if (pl->dn_form == kThroughput) return true;
   // Chunks of F that keep tiles of four slots, of eight where an expert gets more than four on
@@ -1640,23 +1619,23 @@ int moe_experts_launch(const MoeArgs& a, bool prepared) {
       d.h = p.h + k0;
       d.s_dn = p.s_dn + k0 / 64;
       d.part = p.part + (int64_t)c * p.slots * a.H;
-      dbytes = moe_fit(d, pl.nt, true, pl.dn_form);
+      dbytes = moe_fit(d, true, pl.dn_form);
       const uint64_t dd[4] = {(uint64_t)((Fp - k0) / 2), (uint64_t)a.H, 1, (uint64_t)a.E};
       const uint64_t ds[3] = {(uint64_t)(Fp / 2), (uint64_t)(a.H * (Fp / 2)), (uint64_t)(a.H * (Fp / 2))};
       const uint32_t db[4] = {128, 2 * dbox, 1, 1};
       return encode_map_4d(&dn, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq_dn + k0 / 2, dd, ds, db, CU_TENSOR_MAP_SWIZZLE_128B);
     };
     MoeParams g = p;
-    const uint32_t gbytes = moe_fit(g, pl.nt, false, pl.gu_form);
+    const uint32_t gbytes = moe_fit(g, false, pl.gu_form);
     bool encoded = chunk(0);   // (before the first launch: the two follow one another closely)
-    if (const int rc = moe_kernel_form<false>(pl.gu_form, pl.nt, gu, g, gbytes, sms, a.stream)) return rc;
+    if (const int rc = moe_kernel_form<false>(pl.gu_form, gu, g, gbytes, sms, a.stream)) return rc;
     for (int c = 0; c < pl.chunks; ++c) {
       if (c > 0) encoded = chunk(c);
       if (!encoded) {
         set_error_detail("moe: cuTensorMapEncodeTiled failed (or is unavailable)");
         return Q4LIN_ERR_CUDA;
       }
-      if (const int rc = moe_kernel_form<true>(pl.dn_form, pl.nt, dn, d, dbytes, sms, a.stream)) return rc;
+      if (const int rc = moe_kernel_form<true>(pl.dn_form, dn, d, dbytes, sms, a.stream)) return rc;
     }
     if (pl.dn_form != kLatency) {
       cudaLaunchAttribute at[1];
