@@ -313,6 +313,93 @@ int q4lin_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_
                        int64_t rot, int64_t P, float eps, int interleaved, void* stream);
 
 /*
+ * Attention over whole prompts: causal, grouped heads, sequences packed after one another.
+ * Row i of sequence s is token cu_seqlens[s] + i; with g = h / (Hq / Hk),
+ *   out[i, h] = sum_{j <= i} p_j v[j, g] / sum_{j <= i} p_j,  p_j = exp(scale q[i, h] . k[j, g]).
+ *   q, out bf16, row t at q + t * ldq, its Hq heads D apart; k, v bf16, Hk heads likewise.  Rows
+ *     may be slices of a packed row.  out must not overlap the inputs.
+ *   cu_seqlens int32 [S + 1], device, not decreasing, within [0, T] (values outside are taken into
+ *     it).  Sequences may be empty.  Rows of out before the first and behind the last one stay as
+ *     they are.
+ *   D a multiple of 8 up to 128; Hq a multiple of Hk; strides (in elements) multiples of 8 and at
+ *     least heads * D; q, k, v, out 16-byte aligned; scale finite.
+ * Scores, maxima and sums are FP32; the weights p enter the product with v as bf16 (2^-9 each).
+ * Inf and NaN in k or v reach only rows that see that token.  A row whose scores are all -inf, or
+ * one of +inf or NaN, gives NaN.  One kernel, no workspace.
+ */
+int q4lin_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                           const int32_t* cu_seqlens, uint16_t* out, int64_t ldo, int64_t T, int64_t S, int64_t Hq,
+                           int64_t Hk, int64_t D, float scale, void* stream);
+
+/*
+ * A paged cache of keys and values in 4 bits.  cache uint8 [pages, Hk, q4lin_kv4_page_bytes(D)],
+ * 16-byte aligned: a page holds 64 tokens, and for every head one record of K codes, V codes,
+ * K scales, V scales (64 D + 256 ceil(D / 64) bytes).  A value is (q - 8) * s as in the layer's
+ * weights, with one fp16 scale per token, head and 64 values (the last group may be shorter):
+ *   s = fp16(min(max |x| / 7, 65504)),  q = rint(x / s) + 8 taken into [0, 15]  (s = 0: q = 8);
+ *   a group with a value that is not finite gets a NaN scale and reads as NaN.
+ * Layout: K codes [64 tokens][D / 2 bytes], 32-bit words of 8 values (block b, low nibble first),
+ * word c * (D / 32) + j = block 4 j + c; V codes [D / 2 rows][64 bytes], row i holds values 2 i (low
+ * nibble) and 2 i + 1 of every token, token o at byte
+ * 16 * (o % 8 / 2) + 4 * (o / 16) + 2 * (o % 2) + o % 16 / 8; scales [64 tokens][ceil(D / 64)].
+ * The heads have 64, 96 or 128 values (others: Q4LIN_ERR_UNSUPPORTED_SHAPE).
+ *
+ *   page_table int32 [S, max_pages], device: page of sequence s's tokens 64 i .. 64 i + 63
+ *     (max_pages below 2^25)
+ *   positions  int32 [T]; rows int32 [T] or NULL: token t is token positions[t] of sequence rows[t]
+ *     (NULL: of sequence t)
+ * q4lin_kv4_append writes the T tokens' keys and values, q4lin_kv4_read reads tokens back as bf16.
+ * A token whose row, position or page lies outside [0, S), [0, 64 max_pages) or [0, pages) is left
+ * out: nothing is written for it.  Within a call the places that are appended to must differ.
+ *   k, v bf16, row t at k + t * ldk, its Hk heads D apart; strides multiples of 8, at least Hk * D;
+ *   16-byte aligned.  One kernel, no workspace.
+ */
+size_t q4lin_kv4_page_bytes(int64_t D);
+int q4lin_kv4_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, uint8_t* cache,
+                     const int32_t* page_table, const int32_t* rows, const int32_t* positions, int64_t T, int64_t S,
+                     int64_t max_pages, int64_t pages, int64_t Hk, int64_t D, void* stream);
+int q4lin_kv4_read(const uint8_t* cache, const int32_t* page_table, const int32_t* rows, const int32_t* positions,
+                   uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, int64_t T, int64_t S, int64_t max_pages,
+                   int64_t pages, int64_t Hk, int64_t D, void* stream);
+
+/*
+ * Attention of new tokens over the cache: q_len tokens per sequence, row s * q_len + i of q and out
+ * is token i of sequence s, which sees the first lengths[s] - (q_len - 1 - i) tokens of the cache
+ * (lengths counts the new tokens, whose keys and values are appended before):
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  head h over the cache's h / (Hq / Hk).
+ * A token that sees nothing gives zeros.  lengths int32 [S] (taken into [0, 64 max_pages]).  Tokens
+ * of a page whose id lies outside [0, pages) are left out.
+ *   q, out bf16 [S * q_len rows], strides and alignment as above; out must not overlap q
+ *   workspace: >= q4lin_kv4_workspace_bytes(...) bytes, 256-byte aligned
+ * The codes' products are exact, q enters exactly down to 2^-28 of its head's largest value, group
+ * scales, maxima and sums are FP32; each weight times its token's scale enters the product with
+ * the codes as fp16 (2^-12 of it).  A cache may hold more than 2^32 values.  Two kernels.
+ */
+size_t q4lin_kv4_workspace_bytes(int64_t S, int64_t q_len, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages);
+int q4lin_kv4_attention(const uint16_t* q, int64_t ldq, const uint8_t* cache, const int32_t* page_table,
+                        const int32_t* lengths, uint16_t* out, int64_t ldo, int64_t S, int64_t q_len, int64_t Hq,
+                        int64_t Hk, int64_t D, int64_t max_pages, int64_t pages, float scale, void* workspace,
+                        void* stream);
+
+/*
+ * What rows of logits say.  For row x of V logits, L = ln sum_v exp(x_v):
+ *   logprobs[t, j] = x[targets[t, j]] - L   (a target outside [0, V): 0),
+ *   entropy[t] = -sum_v p_v ln p_v,  p_v = exp(x_v - L),
+ *   top_ids / top_logprobs [t, 0 .. top_k): the largest logits, largest first (ties: the lowest
+ *     token first), and their x - L.
+ *   logits bf16 (fp32 = 0) or fp32 (otherwise) [T, V], row stride ld elements (>= V), aligned to
+ *     their element; targets int32 [T, n]; logprobs fp32 [T, n]; entropy fp32 [T] or NULL; top_ids
+ *     int32 and top_logprobs fp32 [T, top_k]; n >= 0, 0 <= top_k <= min(32, V)
+ * FP32.  Logits of -inf have probability 0 and are never among the top (left over places: id -1,
+ * -inf); an x of +inf counts as the limit (equal shares among them).  A row without a logit above
+ * -inf gives logprobs -inf, entropy 0, ids -1; one with a NaN gives NaN, and ids of the others.
+ * One kernel, no workspace.
+ */
+int q4lin_token_logprobs(const void* logits, int fp32, int64_t ld, const int32_t* targets, float* logprobs,
+                         float* entropy, int32_t* top_ids, float* top_logprobs, int64_t T, int64_t V, int64_t n,
+                         int top_k, void* stream);
+
+/*
  * Kernels one q4lin_linear_qtype call of this format and shape launches (0 for a
  * shape it refuses or an unknown format); Q4G64 is q4lin_kernel_launches.
  */

@@ -7,3 +7,4 @@ from .q4_oracle import (  # noqa: F401
 from . import sibling_formats  # noqa: F401,E402
 from . import fused_ops  # noqa: F401,E402
 from . import decoder_ops  # noqa: F401,E402
+from . import attention_ops  # noqa: F401,E402

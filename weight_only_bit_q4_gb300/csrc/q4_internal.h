@@ -167,6 +167,62 @@ int moe_router_launch(const MoeArgs& a);
 int moe_experts_launch(const MoeArgs& a, bool prepared);
 int moe_status(int* value, bool clear);
 
+// Attention over whole prompts: causal, packed sequences (strides in elements).
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  int64_t ldq, ldk, ldv, ldo;
+  const int32_t* cu;       // [S + 1]
+  int64_t T, S, Hq, Hk, D;
+  float scale;
+  cudaStream_t stream;
+};
+int prompt_launch(const PromptArgs& a);
+
+// The paged 4-bit cache: tokens in (append: k, v -> cache) and out (cache -> k_out, v_out).
+struct KvTokArgs {
+  const uint16_t *k, *v;
+  uint16_t *k_out, *v_out;
+  int64_t ldk, ldv;
+  uint8_t* cache;
+  const int32_t *table, *rows, *pos;
+  int64_t T, S, M, P, Hk, D;
+  cudaStream_t stream;
+};
+int64_t kv_page_bytes(int64_t D);
+int kv_tokens_launch(const KvTokArgs& a, bool append);
+// Attention of n new tokens per sequence over the cache.
+struct KvAttnArgs {
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t ldq, ldo;
+  const uint8_t* cache;
+  const int32_t *table, *len;
+  int64_t S, n, Hq, Hk, D, M, P;
+  float scale;
+  void* workspace;
+  cudaStream_t stream;
+};
+int64_t kv_passes(int64_t cols);   // passes over a head's cols = n Hq / Hk query columns
+int64_t kv_workspace_bytes(int64_t D, int64_t cols);
+int kv_attention_launch(const KvAttnArgs& a);
+int kv_status(int* value, bool clear);
+
+// Log probabilities of given tokens, entropy and top tokens of rows of logits.
+struct LogprobArgs {
+  const void* logits;
+  int64_t ld;
+  const int32_t* targets;
+  float *logprobs, *entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  int64_t T, V, n;
+  int k;
+  bool fp32;
+  cudaStream_t stream;
+};
+int logprobs_launch(const LogprobArgs& a);
+
 // Reads (and optionally clears) the device error word of one translation unit.
 int gemv_status(int* value, bool clear);
 int tc_status(int* value, bool clear);

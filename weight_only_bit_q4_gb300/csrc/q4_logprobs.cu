@@ -1,0 +1,400 @@
+// What a row of logits says: log probabilities of given tokens, the entropy, the top tokens.
+//
+// For a row x of V logits, M = max x, S = sum e^(x_v - M):
+//     logp(v) = x_v - M - ln S,     entropy = ln S - (sum e^(x_v - M) (x_v - M)) / S,
+// and the k largest x in order, ties by the lowest token.  Both terms of the entropy are >= 0,
+// so nothing cancels.  FP32 sums; every thread's are taken about a reference of its own that
+// moves only when a logit lies more than kSlack above it (the sums then hold terms up to
+// e^kSlack, far from FP32's end), and are brought to M at the end.
+//
+// Bound: the bytes of the logits, read once.  One pass: the exponentials, both sums, the
+// maximum and the candidates of the top list come from the same registers.
+//
+// Split: a row belongs to a cluster of 1 .. 8 CTAs (as many as fill the GPU, with few rows), its
+// 16-byte chunks dealt to the cluster's threads in turn; what lies before the first and behind
+// the last whole chunk goes to the first CTA's and the last CTA's single threads.  A warp's
+// chunks come in ascending order, so a list that takes only larger logits keeps ties by the
+// lowest token.  Lists: lane i of every warp holds the warp's i-th; a vote per chunk of 32
+// vectors decides whether any of its logits beats the last entry, which is rare after the
+// first few.  Warps, then CTAs (distributed shared memory) are merged in order.
+#include <cfloat>
+
+#include "q4_internal.h"
+#include "q4_sm100.cuh"
+
+namespace q4 {
+
+namespace {
+
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kMaxTop = 32;
+constexpr float kSlack = 40.f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct LpParams {
+  const void* x;
+  int64_t ld;               // row stride in elements
+  const int32_t* tok;       // [T, n]
+  float* logp;              // [T, n]
+  float* entropy;           // [T] or NULL
+  int32_t* ids;             // [T, k]
+  float* top;               // [T, k]
+  int64_t T;
+  int V, n, k, cs;          // cs: CTAs per row
+};
+
+__device__ __forceinline__ float ex2(float t) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return e;
+}
+
+__device__ __forceinline__ float2 lp_fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+// Sums about the reference m (in units of ln 2 for a): s = sum 2^t, a = sum 2^t t.
+struct Sums {
+  float m, s, a, top;   // top: the largest logit so far; -inf: none (the reference is at most FLT_MAX)
+};
+
+// The sums of `o` brought to the reference of `r` (o.m <= r.m up to rounding, or o empty).
+__device__ __forceinline__ void shift_to(float m, Sums& o) {
+  if (o.s == 0.f) {
+    o.a = 0.f;
+  } else {
+    const float t = (o.m - m) * kLog2e, f = ex2(t);
+    o.a = f == 0.f && o.s == o.s ? 0.f : f * (o.a + o.s * t);
+    o.s *= f;
+  }
+  o.m = m;
+}
+
+__device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && (uint32_t)i < (uint32_t)j); }
+
+// The warp's list: lane i holds the i-th largest (value, token), i < k; unused entries are (-inf, -1).
+struct TopList {
+  float v;
+  int id;
+};
+
+__device__ __forceinline__ void list_insert(TopList& l, float x, int id, int k, int lane) {
+  const int at = __popc(__ballot_sync(0xffffffffu, lane < k && l.v >= x));   // equal ones came before
+  const float pv = __shfl_up_sync(0xffffffffu, l.v, 1);
+  const int pi = __shfl_up_sync(0xffffffffu, l.id, 1);
+  if (lane > at) {
+    l.v = pv;
+    l.id = pi;
+  }
+  if (lane == at) {
+    l.v = x;
+    l.id = id;
+  }
+}
+
+// Merge of `lists` sorted lists of k entries (value and token arrays `stride` entries apart) into lane i's
+// i-th of the result: every lane walks one list.
+template <class Load>
+__device__ __forceinline__ TopList merge_lists(int lists, int k, int lane, Load load) {
+  int at = 0;
+  float v = -INFINITY;
+  int id = -1;
+  if (lane < lists) load(lane, 0, v, id);
+  TopList out{-INFINITY, -1};
+  for (int r = 0; r < k; ++r) {
+    float bv = v;
+    int bi = id, bl = lane;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
+      const int oi = __shfl_xor_sync(0xffffffffu, bi, o), ol = __shfl_xor_sync(0xffffffffu, bl, o);
+      if (before(ov, oi, bv, bi) || (ov == bv && oi == bi && ol < bl)) {
+        bv = ov;
+        bi = oi;
+        bl = ol;
+      }
+    }
+    if (bi < 0) break;   // (uniform: nothing is left)
+    if (lane == r) out = TopList{bv, bi};
+    if (lane == bl) {
+      ++at;
+      v = -INFINITY;
+      id = -1;
+      if (at < k) load(lane, at, v, id);
+    }
+  }
+  return out;
+}
+
+template <bool kF32>
+struct Vec;   // one 16-byte chunk as pairs of FP32 values
+template <>
+struct Vec<false> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void unpack(uint4 w, float2 (&x)[4]) {
+    x[0] = make_float2(bf16lo(w.x), bf16hi(w.x));
+    x[1] = make_float2(bf16lo(w.y), bf16hi(w.y));
+    x[2] = make_float2(bf16lo(w.z), bf16hi(w.z));
+    x[3] = make_float2(bf16lo(w.w), bf16hi(w.w));
+  }
+  static __device__ __forceinline__ float one(const void* p, int64_t i) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(static_cast<const uint16_t*>(p) + i));
+    return __uint_as_float((uint32_t)v << 16);
+  }
+};
+template <>
+struct Vec<true> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void unpack(uint4 w, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    x[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+  static __device__ __forceinline__ float one(const void* p, int64_t i) {
+    return __uint_as_float(ld_global_u32(static_cast<const uint32_t*>(p) + i));
+  }
+};
+
+// Values of `np` pairs join the sums; `vm` is their largest.
+template <int NP>
+__device__ __forceinline__ void add_values(Sums& r, float& limit, const float2 (&x)[NP], float vm) {
+  if (vm > limit) {   // (the first values at all, or far above the reference)
+    const float m = fminf(vm, FLT_MAX);
+    shift_to(m, r);
+    limit = m + kSlack;
+    if (vm == INFINITY) {   // every +inf counts as 1, whatever is finite as 0
+      limit = FLT_MAX;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const float e[2] = {x[i].x, x[i].y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) r.s += e[j] == INFINITY ? 1.f : e[j] == e[j] ? 0.f : e[j];
+      }
+      r.top = vm;
+      return;
+    }
+  }
+  r.top = fmaxf(r.top, vm);
+  const float2 neg = make_float2(-r.m, -r.m), c = make_float2(kLog2e, kLog2e);
+  float2 s = make_float2(0.f, 0.f), a = s;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const float2 t = lp_fmul2(fadd2(x[i], neg), c);
+    const float2 e = make_float2(ex2(t.x), ex2(t.y));
+    s = fadd2(s, e);
+    // (a logit of -inf adds nothing: 0 times the bounded t)
+    a = ffma2(e, make_float2(fmaxf(t.x, -1e4f), fmaxf(t.y, -1e4f)), a);
+  }
+  r.s += s.x + s.y;
+  r.a += a.x + a.y;
+}
+
+struct LpShared {
+  Sums sums[kLpWarps];
+  float lv[kLpWarps][kMaxTop];
+  int li[kLpWarps][kMaxTop];
+  Sums cta;                  // this CTA's, read by the cluster's first
+  float cv[kMaxTop];
+  int ci[kMaxTop];
+  float row[2];              // M, ln S
+};
+
+__device__ __forceinline__ Sums warp_join(Sums r) {
+  float m = r.top;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = fminf(m, FLT_MAX);
+  if (m > -INFINITY) shift_to(ref, r);
+  // a fixed tree: the same bits every time
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
+    r.a += __shfl_xor_sync(0xffffffffu, r.a, o);
+  }
+  r.m = ref;
+  r.top = m;
+  return r;
+}
+
+template <bool kF32, bool kTop>
+__global__ void __launch_bounds__(kLpThreads, 2) q4_logprobs_kernel(const LpParams p) {
+  using V = Vec<kF32>;
+  constexpr int kBatch = 4;   // chunks in flight per thread
+  __shared__ LpShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / (unsigned)p.cs;
+  const int rank = (int)(blockIdx.x - (unsigned)row * (unsigned)p.cs);
+  pdl_launch_dependents();
+  pdl_wait_previous();
+  constexpr int64_t esize = kF32 ? 4 : 2;
+  const char* x = static_cast<const char*>(p.x) + row * p.ld * esize;
+  // whole 16-byte chunks lie between `head` and `head + chunks * V::n`
+  const int head = min(p.V, (int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / esize));
+  const int chunks = (p.V - head) / V::n;
+  const char* body = x + head * esize;
+
+  Sums r{0.f, 0.f, 0.f, -INFINITY};
+  float limit = -INFINITY;
+  TopList list{-INFINITY, -1};
+  float last = -INFINITY;     // the list's last entry
+  auto offer = [&](float v, int id) {   // (uniform)
+    if (v > last) {
+      list_insert(list, v, id, p.k, lane);
+      last = __shfl_sync(0xffffffffu, list.v, p.k - 1);
+    }
+  };
+  // single logits, one per lane (first: warp 0 of the first CTA; last: the last warp of the last)
+  auto singles = [&](int from, int count) {
+    float v = -INFINITY;
+    if (lane < count) v = V::one(x, from + lane);
+    const float2 pair[1] = {make_float2(v, -INFINITY)};
+    if (lane < count) add_values<1>(r, limit, pair, v);
+    if constexpr (kTop)
+      for (int j = 0; j < count; ++j) offer(__shfl_sync(0xffffffffu, v, j), from + j);
+  };
+  if (rank == 0 && warp == 0 && head > 0) singles(0, head);
+
+  const int step = p.cs * kLpThreads;
+  for (int c0 = rank * kLpThreads + warp * 32; c0 < chunks; c0 += kBatch * step) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int c = c0 + b * step + lane;
+      if (c < chunks) w[b] = ld_global_u4(body + (int64_t)c * 16);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int c = c0 + b * step + lane;
+      float2 v[V::n / 2];
+      float vm = -INFINITY;
+      if (c < chunks) {
+        V::unpack(w[b], v);
+        vm = fmaxf(v[0].x, v[0].y);
+#pragma unroll
+        for (int i = 1; i < V::n / 2; ++i) vm = fmaxf(vm, fmaxf(v[i].x, v[i].y));
+        add_values<V::n / 2>(r, limit, v, vm);
+      }
+      if constexpr (kTop) {
+        uint32_t some = __ballot_sync(0xffffffffu, vm > last);
+        while (some) {
+          const int from = __ffs(some) - 1;
+          some &= some - 1;
+          const int id = head + (c0 + b * step + from) * V::n;
+#pragma unroll
+          for (int i = 0; i < V::n / 2; ++i) {
+            offer(__shfl_sync(0xffffffffu, v[i].x, from), id + 2 * i);
+            offer(__shfl_sync(0xffffffffu, v[i].y, from), id + 2 * i + 1);
+          }
+        }
+      }
+    }
+  }
+  const int tail = head + chunks * V::n;
+  if (rank == p.cs - 1 && warp == kLpWarps - 1 && tail < p.V) singles(tail, p.V - tail);
+
+  r = warp_join(r);
+  if (lane == 0) sh.sums[warp] = r;
+  if (kTop) {
+    sh.lv[warp][lane] = list.v;
+    sh.li[warp][lane] = list.id;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    Sums q = lane < kLpWarps ? sh.sums[lane] : Sums{0.f, 0.f, 0.f, -INFINITY};
+    q = warp_join(q);
+    if (kTop)
+      list = merge_lists(kLpWarps, p.k, lane, [&](int l, int i, float& v, int& id) { v = sh.lv[l][i]; id = sh.li[l][i]; });
+    if (p.cs > 1) {
+      if (lane == 0) sh.cta = q;
+      sh.cv[lane] = list.v;
+      sh.ci[lane] = list.id;
+    }
+    r = q;
+  }
+  if (p.cs > 1) {
+    cluster_sync();
+    if (rank == 0 && warp == 0) {
+      Sums q{0.f, 0.f, 0.f, -INFINITY};
+      if (lane < p.cs) {
+        const uint32_t at = mapa_shared(smem_u32(&sh.cta), (uint32_t)lane);
+        q.m = __uint_as_float(ld_cluster_u32(at));
+        q.s = __uint_as_float(ld_cluster_u32(at + 4));
+        q.a = __uint_as_float(ld_cluster_u32(at + 8));
+        q.top = __uint_as_float(ld_cluster_u32(at + 12));
+      }
+      r = warp_join(q);
+      if (kTop)
+        list = merge_lists(p.cs, p.k, lane, [&](int l, int i, float& v, int& id) {
+          v = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.cv[i]), (uint32_t)l)));
+          id = (int)ld_cluster_u32(mapa_shared(smem_u32(&sh.ci[i]), (uint32_t)l));
+        });
+    }
+    cluster_sync();   // no CTA leaves while its shared memory is read
+    if (rank != 0) return;
+  }
+  if (warp == 0) {
+    // r.s NaN: a logit was NaN; none above -inf: no distribution
+    const bool none = r.top == -INFINITY && r.s == r.s;
+    const float ls = logf(r.s);
+    if (lane == 0) {
+      sh.row[0] = r.top;
+      sh.row[1] = none ? INFINITY : ls;
+      if (p.entropy != nullptr) p.entropy[row] = none ? 0.f : ls - r.a / r.s * kLn2;
+    }
+    if (kTop && lane < p.k) {
+      p.ids[row * p.k + lane] = list.id;
+      p.top[row * p.k + lane] = list.id < 0 ? -INFINITY : (list.v == r.top ? 0.f : list.v - r.top) - ls;
+    }
+  }
+  __syncthreads();
+  for (int j = tid; j < p.n; j += kLpThreads) {
+    const int v = (int)ld_global_u32(p.tok + row * p.n + j);
+    float out = 0.f;   // no token: adds nothing to a sequence's sum
+    if (v >= 0 && v < p.V) {
+      const float xv = V::one(x, v);
+      out = (xv == sh.row[0] ? 0.f : xv - sh.row[0]) - sh.row[1];   // (equal: both may be infinite)
+    }
+    p.logp[row * p.n + j] = out;
+  }
+}
+
+template <bool kF32, bool kTop>
+int lp_launch(const LpParams& p, unsigned blocks, cudaStream_t stream) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)p.cs;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(kLpThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = p.cs > 1 ? 2 : 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_logprobs_kernel<kF32, kTop>, p), "token_logprobs: kernel launch");
+}
+
+}  // namespace
+
+int logprobs_launch(const LogprobArgs& a) {
+  LpParams p{a.logits, a.ld, a.targets, a.logprobs, a.entropy, a.top_ids, a.top_logprobs, a.T, (int)a.V, (int)a.n, a.k, 1};
+  // CTAs per row: as many as keep all rows' on the GPU at once, each with two batches of chunks at least
+  const int64_t chunks = a.V * (a.fp32 ? 4 : 2) / 16;
+  while (p.cs < 8 && a.T * p.cs * 2 <= 304 && chunks >= (int64_t)p.cs * 2 * kLpThreads * 2) p.cs *= 2;
+  const int64_t blocks = a.T * p.cs;
+  if (blocks > 0x7fffffff) {
+    set_error_detail("token_logprobs: too many rows for one launch");
+    return Q4LIN_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (a.fp32) return a.k > 0 ? lp_launch<true, true>(p, (unsigned)blocks, a.stream) : lp_launch<true, false>(p, (unsigned)blocks, a.stream);
+  return a.k > 0 ? lp_launch<false, true>(p, (unsigned)blocks, a.stream) : lp_launch<false, false>(p, (unsigned)blocks, a.stream);
+}
+
+}  // namespace q4

@@ -5,6 +5,7 @@
 // workspace, stream)) with a workspace capacity query (section 1.1) and a
 // format selector that rejects unsupported points (section 1.1) and returns
 // one host launcher per exact (N, K, T) (section 8.2).
+#include <cfloat>
 #include <cstdio>
 #include <cstring>
 
@@ -464,9 +465,181 @@ int run_qk(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const
   return q4::qk_norm_rope_launch(a);
 }
 
+// A tensor of `heads` heads of D values side by side in each of T rows.
+int check_rows(const char* what, const void* ptr, int64_t ld, int64_t T, int64_t heads, int64_t D) {
+  if (ptr == nullptr) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned16(ptr)) return Q4LIN_ERR_MISALIGNED;
+  if (ld < heads * D || ld > kMaxDim || (double)T * (double)ld > 9.0e17) return refuse(what);
+  if (ld % 8 != 0) return Q4LIN_ERR_MISALIGNED;
+  return Q4LIN_OK;
+}
+
+int run_prompt(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+               const int32_t* cu, uint16_t* out, int64_t ldo, int64_t T, int64_t S, int64_t Hq, int64_t Hk, int64_t D,
+               float scale, void* stream) {
+  if (T < 0 || S < 0 || Hq < 0 || Hk < 0 || D < 0) return Q4LIN_ERR_INVALID_ARG;
+  if (!(scale >= -FLT_MAX && scale <= FLT_MAX)) return refuse("prompt_attention: the scale must be a finite number");
+  if (D % 8 != 0 || D > 128) return refuse("prompt_attention: D a multiple of 8 up to 128", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if (Hq > 65536 || Hk > 65536 || T >= (int64_t)1 << 31 || S >= (int64_t)1 << 31) return Q4LIN_ERR_INVALID_ARG;
+  if (T == 0 || S == 0 || Hq == 0 || D == 0) return Q4LIN_OK;
+  if (Hk == 0 || Hq % Hk != 0) return refuse("prompt_attention: Hq must be a multiple of Hk");
+  static const char* const kShort = "prompt_attention: a row stride is shorter than the heads of a row (or overflows)";
+  int st = check_rows(kShort, q, ldq, T, Hq, D);
+  if (st == Q4LIN_OK) st = check_rows(kShort, k, ldk, T, Hk, D);
+  if (st == Q4LIN_OK) st = check_rows(kShort, v, ldv, T, Hk, D);
+  if (st == Q4LIN_OK) st = check_rows(kShort, out, ldo, T, Hq, D);
+  if (st != Q4LIN_OK) return st;
+  if (cu == nullptr) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned4(cu)) return Q4LIN_ERR_MISALIGNED;
+  if ((st = check_device()) != Q4LIN_OK) return st;
+  return q4::prompt_launch(q4::PromptArgs{q, k, v, out, ldq, ldk, ldv, ldo, cu, T, S, Hq, Hk, D, scale,
+                                          static_cast<cudaStream_t>(stream)});
+}
+
+bool kv_head_ok(int64_t D) { return D == 64 || D == 96 || D == 128; }
+
+// Sizes that the cache's three operators share.
+int validate_cache(int64_t pages, int64_t S, int64_t max_pages, int64_t Hk, int64_t D) {
+  if (pages < 0 || S < 0 || max_pages < 0 || Hk < 0) return Q4LIN_ERR_INVALID_ARG;
+  if (!kv_head_ok(D)) return refuse("kv4: heads of 64, 96 or 128 values", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if (Hk > 65536 || pages >= (int64_t)1 << 31 || S >= (int64_t)1 << 31 || max_pages >= (int64_t)1 << 25)
+    return Q4LIN_ERR_INVALID_ARG;
+  if ((double)pages * (double)Hk * 8704.0 > 9.0e17) return Q4LIN_ERR_INVALID_ARG;
+  return Q4LIN_OK;
+}
+
+int run_kv_tokens(bool append, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, uint8_t* cache,
+                  const int32_t* table, const int32_t* rows, const int32_t* pos, int64_t T, int64_t S, int64_t max_pages,
+                  int64_t pages, int64_t Hk, int64_t D, void* stream) {
+  int st = validate_cache(pages, S, max_pages, Hk, D);
+  if (st != Q4LIN_OK) return st;
+  if (T < 0 || T >= (int64_t)1 << 31) return Q4LIN_ERR_INVALID_ARG;
+  if (T == 0 || Hk == 0 || S == 0 || max_pages == 0 || pages == 0) return Q4LIN_OK;   // (no token has a place)
+  static const char* const kShort = "kv4: a row stride is shorter than the heads of a row (or overflows)";
+  st = check_rows(kShort, k, ldk, T, Hk, D);
+  if (st == Q4LIN_OK) st = check_rows(kShort, v, ldv, T, Hk, D);
+  if (st != Q4LIN_OK) return st;
+  if (cache == nullptr || table == nullptr || pos == nullptr) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned16(cache) || !aligned4(table) || !aligned4(rows) || !aligned4(pos)) return Q4LIN_ERR_MISALIGNED;
+  if ((st = check_device()) != Q4LIN_OK) return st;
+  q4::KvTokArgs a{};
+  if (append) {
+    a.k = k;
+    a.v = v;
+  } else {
+    a.k_out = const_cast<uint16_t*>(k);
+    a.v_out = const_cast<uint16_t*>(v);
+  }
+  a.ldk = ldk; a.ldv = ldv;
+  a.cache = cache;
+  a.table = table; a.rows = rows; a.pos = pos;
+  a.T = T; a.S = S; a.M = max_pages; a.P = pages; a.Hk = Hk; a.D = D;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return q4::kv_tokens_launch(a, append);
+}
+
+int validate_kv_attention(int64_t S, int64_t q_len, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages) {
+  const int st = validate_cache(0, S, max_pages, Hk, D);
+  if (st != Q4LIN_OK) return st;
+  if (q_len < 0 || Hq < 0 || Hq > 65536) return Q4LIN_ERR_INVALID_ARG;
+  if (S == 0 || q_len == 0 || Hq == 0) return Q4LIN_OK;
+  if (Hk == 0 || Hq % Hk != 0) return refuse("kv4_attention: Hq must be a multiple of Hk");
+  if (q_len > 65536 || S * q_len >= (int64_t)1 << 31 || q_len * Hq >= (int64_t)1 << 24) return Q4LIN_ERR_INVALID_ARG;
+  const int64_t passes = q4::kv_passes(q_len * (Hq / Hk));
+  if ((double)S * (double)Hk * (double)passes >= 2147483648.0)
+    return refuse("kv4_attention: too many sequences, heads and columns for one launch", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  return Q4LIN_OK;
+}
+
+int run_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* cache, const int32_t* table, const int32_t* lengths,
+                     uint16_t* out, int64_t ldo, int64_t S, int64_t q_len, int64_t Hq, int64_t Hk, int64_t D,
+                     int64_t max_pages, int64_t pages, float scale, void* workspace, void* stream) {
+  int st = validate_kv_attention(S, q_len, Hq, Hk, D, max_pages);
+  if (st == Q4LIN_OK) st = validate_cache(pages, S, max_pages, Hk, D);
+  if (st != Q4LIN_OK) return st;
+  if (!(scale >= -FLT_MAX && scale <= FLT_MAX)) return refuse("kv4_attention: the scale must be a finite number");
+  if (S == 0 || q_len == 0 || Hq == 0) return Q4LIN_OK;
+  static const char* const kShort = "kv4_attention: a row stride is shorter than the heads of a row (or overflows)";
+  st = check_rows(kShort, q, ldq, S * q_len, Hq, D);
+  if (st == Q4LIN_OK) st = check_rows(kShort, out, ldo, S * q_len, Hq, D);
+  if (st != Q4LIN_OK) return st;
+  if (lengths == nullptr || (max_pages > 0 && table == nullptr) || (pages > 0 && cache == nullptr)) return Q4LIN_ERR_INVALID_ARG;
+  if (!aligned16(cache) || !aligned4(table) || !aligned4(lengths)) return Q4LIN_ERR_MISALIGNED;
+  if ((st = check_workspace(q4lin_kv4_workspace_bytes(S, q_len, Hq, Hk, D, max_pages), workspace)) != Q4LIN_OK) return st;
+  if ((st = check_device()) != Q4LIN_OK) return st;
+  return q4::kv_attention_launch(q4::KvAttnArgs{q, out, ldq, ldo, cache, table, lengths, S, q_len, Hq, Hk, D, max_pages,
+                                                pages, scale, workspace, static_cast<cudaStream_t>(stream)});
+}
+
+int run_logprobs(const void* logits, int fp32, int64_t ld, const int32_t* targets, float* logprobs, float* entropy,
+                 int32_t* top_ids, float* top_logprobs, int64_t T, int64_t V, int64_t n, int top_k, void* stream) {
+  if (T < 0 || n < 0 || V < 1 || top_k < 0) return refuse("token_logprobs: T, n, top_k >= 0 and V >= 1 are needed");
+  if (top_k > 32 || top_k > V || V >= (int64_t)1 << 31)
+    return refuse("token_logprobs: top_k up to 32 (and V), V below 2^31", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if (n >= (int64_t)1 << 31 || T >= (int64_t)1 << 31) return Q4LIN_ERR_INVALID_ARG;
+  if (T == 0) return Q4LIN_OK;
+  if (ld < V || ld > kMaxDim || (double)T * (double)ld > 9.0e17) return refuse("token_logprobs: the row stride is shorter than V (or overflows)");
+  if (logits == nullptr || (n > 0 && (targets == nullptr || logprobs == nullptr)) ||
+      (top_k > 0 && (top_ids == nullptr || top_logprobs == nullptr)))
+    return Q4LIN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) & (fp32 ? 3u : 1u)) != 0) return Q4LIN_ERR_MISALIGNED;
+  const void* const words[] = {targets, logprobs, entropy, top_ids, top_logprobs};
+  for (const void* w : words)
+    if (!aligned4(w)) return Q4LIN_ERR_MISALIGNED;
+  const int st = check_device();
+  if (st != Q4LIN_OK) return st;
+  return q4::logprobs_launch(q4::LogprobArgs{logits, ld, targets, logprobs, entropy, top_ids, top_logprobs, T, V, n, top_k,
+                                             fp32 != 0, static_cast<cudaStream_t>(stream)});
+}
+
 }  // namespace
 
 extern "C" {
+
+int q4lin_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                           const int32_t* cu_seqlens, uint16_t* out, int64_t ldo, int64_t T, int64_t S, int64_t Hq,
+                           int64_t Hk, int64_t D, float scale, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_prompt(q, ldq, k, ldk, v, ldv, cu_seqlens, out, ldo, T, S, Hq, Hk, D, scale, stream));
+}
+
+size_t q4lin_kv4_page_bytes(int64_t D) { return kv_head_ok(D) ? (size_t)q4::kv_page_bytes(D) : 0; }
+
+int q4lin_kv4_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, uint8_t* cache,
+                     const int32_t* page_table, const int32_t* rows, const int32_t* positions, int64_t T, int64_t S,
+                     int64_t max_pages, int64_t pages, int64_t Hk, int64_t D, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_kv_tokens(true, k, ldk, v, ldv, cache, page_table, rows, positions, T, S, max_pages, pages, Hk, D, stream));
+}
+
+int q4lin_kv4_read(const uint8_t* cache, const int32_t* page_table, const int32_t* rows, const int32_t* positions,
+                   uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, int64_t T, int64_t S, int64_t max_pages,
+                   int64_t pages, int64_t Hk, int64_t D, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_kv_tokens(false, k, ldk, v, ldv, const_cast<uint8_t*>(cache), page_table, rows, positions, T, S,
+                              max_pages, pages, Hk, D, stream));
+}
+
+size_t q4lin_kv4_workspace_bytes(int64_t S, int64_t q_len, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages) {
+  if (validate_kv_attention(S, q_len, Hq, Hk, D, max_pages) != Q4LIN_OK || S == 0 || q_len == 0 || Hq == 0) return 0;
+  return round256((size_t)q4::kv_workspace_bytes(D, q_len * (Hq / Hk)));
+}
+
+int q4lin_kv4_attention(const uint16_t* q, int64_t ldq, const uint8_t* cache, const int32_t* page_table,
+                        const int32_t* lengths, uint16_t* out, int64_t ldo, int64_t S, int64_t q_len, int64_t Hq,
+                        int64_t Hk, int64_t D, int64_t max_pages, int64_t pages, float scale, void* workspace,
+                        void* stream) {
+  q4::set_error_detail("");
+  return finish(run_kv_attention(q, ldq, cache, page_table, lengths, out, ldo, S, q_len, Hq, Hk, D, max_pages, pages, scale,
+                                 workspace, stream));
+}
+
+int q4lin_token_logprobs(const void* logits, int fp32, int64_t ld, const int32_t* targets, float* logprobs,
+                         float* entropy, int32_t* top_ids, float* top_logprobs, int64_t T, int64_t V, int64_t n,
+                         int top_k, void* stream) {
+  q4::set_error_detail("");
+  return finish(run_logprobs(logits, fp32, ld, targets, logprobs, entropy, top_ids, top_logprobs, T, V, n, top_k, stream));
+}
 
 size_t q4lin_lora_workspace_bytes(int64_t N, int64_t K, int64_t T, int64_t L, int64_t R) {
   if (validate_lora_sizes(N, K, T, L, R) != Q4LIN_OK || N == 0 || K == 0 || T == 0) return 0;
@@ -799,6 +972,8 @@ static int read_status(bool clear) {
   if (v) worst = v;
   if (q4::moe_status(&v, clear) != Q4LIN_OK) return Q4LIN_ERR_CUDA;
   if (v) worst = v;
+  if (q4::kv_status(&v, clear) != Q4LIN_OK) return Q4LIN_ERR_CUDA;
+  if (v) worst = v;
   return worst;
 }
 
@@ -832,7 +1007,7 @@ int q4lin_diag_wait_expiry(uint32_t limit, int* out, void* stream) {
   return q4::wait_expiry(limit, out, static_cast<cudaStream_t>(stream));
 }
 
-const char* q4lin_version(void) { return "0.3.0"; }
+const char* q4lin_version(void) { return "0.4.0"; }
 
 const char* q4lin_last_error_detail(void) { return q4::g_detail; }
 

@@ -29,7 +29,9 @@ EXPORTS = ("q4lin_workspace_bytes", "q4lin_linear", "q4lin_linear_route", "q4lin
            "q4lin_hbm_read_probe", "q4lin_diag_wait_expiry", "q4lin_linear_swiglu", "q4lin_linear_pair",
            "q4lin_qtype_workspace_bytes", "q4lin_host_workspace_bytes", "q4lin_linear_host", "q4lin_fused_route", "q4lin_qtype_route", "q4lin_version",
            "q4lin_lora_workspace_bytes", "q4lin_lora_route", "q4lin_linear_lora", "q4lin_moe_router",
-           "q4lin_moe_workspace_bytes", "q4lin_moe_experts", "q4lin_moe", "q4lin_qk_norm_rope")
+           "q4lin_moe_workspace_bytes", "q4lin_moe_experts", "q4lin_moe", "q4lin_qk_norm_rope",
+           "q4lin_prompt_attention", "q4lin_kv4_page_bytes", "q4lin_kv4_append", "q4lin_kv4_read",
+           "q4lin_kv4_workspace_bytes", "q4lin_kv4_attention", "q4lin_token_logprobs")
 
 _lib = None
 
@@ -123,6 +125,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.q4lin_moe.restype = ci
     lib.q4lin_qk_norm_rope.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64] + [i64] * 6 + [cf, ci, vp]
     lib.q4lin_qk_norm_rope.restype = ci
+    lib.q4lin_prompt_attention.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64] + [i64] * 5 + [cf, vp]
+    lib.q4lin_prompt_attention.restype = ci
+    lib.q4lin_kv4_page_bytes.argtypes = [i64]
+    lib.q4lin_kv4_page_bytes.restype = sz
+    lib.q4lin_kv4_append.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp] + [i64] * 6 + [vp]
+    lib.q4lin_kv4_append.restype = ci
+    lib.q4lin_kv4_read.argtypes = [vp, vp, vp, vp, vp, i64, vp, i64] + [i64] * 6 + [vp]
+    lib.q4lin_kv4_read.restype = ci
+    lib.q4lin_kv4_workspace_bytes.argtypes = [i64] * 6
+    lib.q4lin_kv4_workspace_bytes.restype = sz
+    lib.q4lin_kv4_attention.argtypes = [vp, i64, vp, vp, vp, vp, i64] + [i64] * 7 + [cf, vp, vp]
+    lib.q4lin_kv4_attention.restype = ci
+    lib.q4lin_token_logprobs.argtypes = [vp, ci, i64, vp, vp, vp, vp, vp] + [i64] * 3 + [ci, vp]
+    lib.q4lin_token_logprobs.restype = ci
     lib.q4lin_version.argtypes = []
     lib.q4lin_version.restype = ctypes.c_char_p
     if path is None:
@@ -672,3 +688,201 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
     if st != OK:
         raise Q4LinError(st)
     return q_out, k_out
+
+
+# ---------------------------------------------------------------- attention, its 4-bit cache, and the logits' answers
+
+KV_PAGE = 64   # tokens of a cache page
+
+
+def _run(device, fn, *args):
+    """The library works on the current device: ``device`` becomes it for the call if it is another."""
+    torch = _t()
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != OK:
+        raise Q4LinError(st)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on one device; got {t.device} beside {device}")
+
+
+def prompt_attention(q, k, v, cu_seqlens, scale: float | None = None, out=None, stream=None):
+    """Causal attention of packed prompts, each token over its own sequence up to itself: out [T, Hq, D].
+
+    q bf16 [T, Hq, D]; k, v bf16 [T, Hk, D] (or [T, Hk * D]), Hq a multiple of Hk, D a multiple of 8 up to
+    128, rows of any stride (slices of a packed projection output); cu_seqlens int32 [S + 1] on the GPU:
+    sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (rows outside all of them are not
+    written).  ``scale`` is D ** -0.5 if not given.
+    """
+    torch = _t()
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, hq, D = q.shape
+    dev = q.device
+    if out is None:
+        out = _new((T, hq, D), torch.bfloat16, dev, stream)
+    bf16 = torch.bfloat16
+    qp, ldq, _ = _rows("q", q, D, bf16)
+    kp, ldk, hk = _rows("k", k, D, bf16)
+    vp, ldv, hv = _rows("v", v, D, bf16)
+    op, ldo, ho = _rows("out", out, D, bf16)
+    if k.shape[0] != T or v.shape[0] != T or out.shape[0] != T or hk != hv or ho != hq:
+        raise ValueError("q, k, v and out must have the same tokens; k and v, and q and out the same heads")
+    S = cu_seqlens.shape[0] - 1
+    if S < 0:
+        raise ValueError("cu_seqlens holds one value more than there are sequences")
+    _same_device(dev, k, v, cu_seqlens, out)
+    _run(dev, load().q4lin_prompt_attention, qp, ldq, kp, ldk, vp, ldv,
+         _need("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)), op, ldo, T, S, hq, hk, D,
+         D ** -0.5 if scale is None and D else scale or 0.0, _stream_ptr(stream, dev))
+    return out
+
+
+def kv4_page_bytes(D: int) -> int:
+    """Bytes that a page of the cache (KV_PAGE tokens) holds per head of D values; 0 for sizes it does not take."""
+    return int(load().q4lin_kv4_page_bytes(D))
+
+
+def _cache(cache, page_table, D):
+    """Checked addresses and sizes of a cache uint8 [pages, Hk, page bytes] and its page table int32 [S, max_pages]."""
+    torch = _t()
+    if cache.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("cache must be [pages, Hk, page bytes] and page_table [S, max_pages]")
+    P, hk, _ = cache.shape
+    S, M = page_table.shape
+    nb = load().q4lin_kv4_page_bytes(D)
+    if nb == 0:
+        raise ValueError(f"the cache takes heads of 64, 96 or 128 values, not {D}")
+    return (_need("cache", cache, torch.uint8, (P, hk, nb)), _need("page_table", page_table, torch.int32, (S, M)), P, hk, S, M)
+
+
+def kv4_append(k, v, cache, page_table, positions, rows=None, stream=None):
+    """Keys and values of T tokens into the 4-bit cache (in place); returns the cache.
+
+    k, v bf16 [T, Hk, D], rows of any stride; cache uint8 [pages, Hk, kv4_page_bytes(D)]; page_table
+    int32 [S, max_pages]: the page of each KV_PAGE tokens of a sequence; token t is token positions[t] (int32)
+    of sequence rows[t] (int32; None: of sequence t).  Tokens whose row, position or page is out of
+    range are left out; the places written to must differ.
+    """
+    torch = _t()
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hk, D]")
+    T, hk, D = k.shape
+    dev = k.device
+    cp, tp, P, hc, S, M = _cache(cache, page_table, D)
+    kp, ldk, _ = _rows("k", k, D, torch.bfloat16)
+    vp, ldv, hv = _rows("v", v, D, torch.bfloat16)
+    if hc != hk or hv != hk or v.shape[0] != T:
+        raise ValueError("k, v and the cache must have the same heads, k and v the same tokens")
+    if rows is None and T > S:
+        raise ValueError("without rows token t belongs to sequence t: more tokens than sequences")
+    _same_device(dev, v, cache, page_table, positions, rows)
+    _run(dev, load().q4lin_kv4_append, kp, ldk, vp, ldv, cp, tp,
+         None if rows is None else _need("rows", rows, torch.int32, (T,)), _need("positions", positions, torch.int32, (T,)),
+         T, S, M, P, hk, D, _stream_ptr(stream, dev))
+    return cache
+
+
+def kv4_read(cache, page_table, positions, D: int, rows=None, k=None, v=None, stream=None):
+    """What the cache holds for T tokens: (k, v) bf16 [T, Hk, D].  Arguments as ``kv4_append``; the rows of
+    tokens that are out of range are left as they are (zeros where k and v are made here)."""
+    torch = _t()
+    T = positions.shape[0]
+    dev = cache.device
+    cp, tp, P, hk, S, M = _cache(cache, page_table, D)
+
+    def fresh():
+        t = _new((T, hk, D), torch.bfloat16, dev, stream)
+        with torch.cuda.stream(stream):
+            return t.zero_()
+
+    k = fresh() if k is None else k
+    v = fresh() if v is None else v
+    kp, ldk, h1 = _rows("k", k, D, torch.bfloat16)
+    vp, ldv, h2 = _rows("v", v, D, torch.bfloat16)
+    if h1 != hk or h2 != hk or k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("k and v must have the cache's heads and a row per token")
+    if rows is None and T > S:
+        raise ValueError("without rows token t belongs to sequence t: more tokens than sequences")
+    _same_device(dev, page_table, positions, rows, k, v)
+    _run(dev, load().q4lin_kv4_read, cp, tp, None if rows is None else _need("rows", rows, torch.int32, (T,)),
+         _need("positions", positions, torch.int32, (T,)), kp, ldk, vp, ldv, T, S, M, P, hk, D, _stream_ptr(stream, dev))
+    return k, v
+
+
+def kv4_workspace_bytes(S: int, q_len: int, Hq: int, Hk: int, D: int, max_pages: int) -> int:
+    """Workspace bytes of kv4_attention."""
+    return int(load().q4lin_kv4_workspace_bytes(S, q_len, Hq, Hk, D, max_pages))
+
+
+def kv4_attention(q, cache, page_table, lengths, scale: float | None = None, out=None, workspace=None, stream=None):
+    """Attention of each sequence's newest tokens over the 4-bit cache: out [S * q_len, Hq, D].
+
+    q bf16 [S * q_len, Hq, D], rows of any stride: row s * q_len + i is the token that sees the first
+    lengths[s] - (q_len - 1 - i) tokens of sequence s (none: zeros); lengths int32 [S]; cache and
+    page_table as ``kv4_append``.  ``scale`` is D ** -0.5 if not given; ``workspace`` (uint8, >=
+    kv4_workspace_bytes) is allocated here if not given.
+    """
+    torch = _t()
+    if q.dim() != 3:
+        raise ValueError("q must be [S * q_len, Hq, D]")
+    T, hq, D = q.shape
+    dev = q.device
+    cp, tp, P, hk, S, M = _cache(cache, page_table, D)
+    n = T // S if S else 0
+    if n * S != T:
+        raise ValueError("q must hold the same number of tokens for every sequence")
+    if out is None:
+        out = _new((T, hq, D), torch.bfloat16, dev, stream)
+    qp, ldq, _ = _rows("q", q, D, torch.bfloat16)
+    op, ldo, ho = _rows("out", out, D, torch.bfloat16)
+    if ho != hq or out.shape[0] != T:
+        raise ValueError("out must have q's tokens and heads")
+    _same_device(dev, cache, page_table, lengths, out, workspace)
+    lib = load()
+    ws, ws_keep = _scratch(workspace, lib.q4lin_kv4_workspace_bytes(S, n, hq, hk, D, M), dev, stream)
+    _run(dev, lib.q4lin_kv4_attention, qp, ldq, cp, tp, _need("lengths", lengths, torch.int32, (S,)), op, ldo, S, n, hq, hk, D,
+         M, P, D ** -0.5 if scale is None else scale, ws, _stream_ptr(stream, dev))
+    return out
+
+
+def token_logprobs(logits, targets, top_k: int = 0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
+                   stream=None):
+    """Log probabilities of given tokens, the entropy and the top tokens of rows of logits:
+    (logprobs fp32 like targets, entropy fp32 [T], top_ids int32 [T, top_k], top_logprobs fp32 [T, top_k]).
+
+    logits bf16 or fp32 [T, V], rows of any stride; targets int32 [T] or [T, n] (outside [0, V): 0);
+    top_k up to 32, largest first, ties by the lowest token.  Logits of -inf are never among the top
+    (id -1, -inf where too few are left).
+    """
+    torch = _t()
+    T, V = logits.shape
+    dev = logits.device
+    if logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda or (logits.stride(1) != 1 and V > 1):
+        raise ValueError("logits must be a bf16 or fp32 CUDA tensor [T, V] with contiguous rows")
+    if targets.dim() not in (1, 2):
+        raise ValueError("targets must be [T] or [T, n]")
+    n = 1 if targets.dim() == 1 else targets.shape[1]
+    f32 = torch.float32
+    if logprobs is None:
+        logprobs = _new(targets.shape, f32, dev, stream)
+    if entropy is None:
+        entropy = _new((T,), f32, dev, stream)
+    if top_ids is None:
+        top_ids = _new((T, top_k), torch.int32, dev, stream)
+    if top_logprobs is None:
+        top_logprobs = _new((T, top_k), f32, dev, stream)
+    _same_device(dev, targets, logprobs, entropy, top_ids, top_logprobs)
+    _run(dev, load().q4lin_token_logprobs, logits.data_ptr(), 1 if logits.dtype is f32 else 0,
+         logits.stride(0) if T > 1 else V, _need("targets", targets, torch.int32, (T,) + tuple(targets.shape[1:])),
+         _need("logprobs", logprobs, f32, targets.shape), _need("entropy", entropy, f32, (T,)),
+         _need("top_ids", top_ids, torch.int32, (T, top_k)), _need("top_logprobs", top_logprobs, f32, (T, top_k)), T, V, n,
+         top_k, _stream_ptr(stream, dev))
+    return logprobs, entropy, top_ids, top_logprobs
