@@ -2,10 +2,30 @@
 //
 // For token t (row i of its sequence) and query head h of group g:
 //     y = sum_{j <= i} p_j v_j / sum_{j <= i} p_j,  p_j = 2^((q . k_j) scale log2 e - m),
-// over the tokens j of the same sequence, m the running maximum.  Scores, maxima and sums are FP32.
-// P enters the second product as bf16, its operands' type (V is bf16): 2^-9 of each weight,
-// as much as the output's own rounding.
+// over the tokens j of the same sequence.  Scores, maxima and sums are FP32.  P enters the second
+// product as bf16, its operands' type (V is bf16): 2^-9 of each weight, as much as the output's
+// own rounding.
+//
+// Bound: the tensor cores (4 D operations per query head and pair of tokens that see each other);
+// beside them the exponentials, one per pair.
+//
+// Split: a CTA (one per SM) owns two tiles of 128 query rows, A and B, that read the same keys: two
+// heads of a group where there is an even number of them, else two runs of rows of a head.  Blocks
+// of 128 keys stream through shared memory (TMA, 128-byte swizzle), from the diagonal down.
+//   warps 0-3, 4-7   softmax of A, of B: a thread owns a row.  It reads its 128 scores from tensor
+//                    memory, and writes P (bf16) over them.  The reference m moves only when a
+//                    score passes it by 2^8 (P and the sums then hold up to 2^8 times more, far
+//                    from any end); only then is the row of O in tensor memory rescaled, by the
+//                    same thread: the block's scores are complete only after the last P V.
+//   warp 8           issues the MMAs: per block and tile P V (P from tensor memory, V as an
+//                    MN-major operand), then the next block's Q K^T into the same columns.
+//                    While A's are computed, B's softmax runs, and the other way round.
+//   warp 9           issues the copies.
+//   warps 10, 11     look blocks of V that hold keys some rows must not see over for values that are
+//                    not finite (0 times infinity would reach those rows).  They become zeros for
+//                    the MMA; the rows that see such a key add it at the end.
 #include <cfloat>
+#include <cmath>
 
 #include "q4_internal.h"
 #include "q4_sm100.cuh"
@@ -14,17 +34,28 @@ namespace q4 {
 
 namespace {
 
-constexpr int kPtThreads = 128;
-constexpr int kPtM = 64, kPtN = 64;   // query rows and keys of a tile
+constexpr int kPtThreads = 384;
+constexpr int kPtTile = 128;          // rows of a tile, keys of a block
+constexpr float kPtSlack = 8.f;       // log2 of how far a score may pass its row's reference
+constexpr int kPtSoftRegs = 224, kPtOtherRegs = 56;
+// the shares of three warpgroups come out of the registers at launch (168 a thread)
+static_assert(2 * kPtSoftRegs + kPtOtherRegs <= 3 * 168, "register split");
+constexpr uint32_t kPtBoxBytes = 64 * 2 * kPtTile;   // 64 columns of a tile
+constexpr int kPtStages = 2;          // of K and of V each
+__device__ int g_prompt_status = 0;
 
 struct PtParams {
-  const uint16_t *q, *k, *v;
+  CUtensorMap mq, mk, mv;   // (D, heads, T)
+  const uint16_t* v;
   uint16_t* out;
-  int64_t ldq, ldk, ldv, ldo;
+  int64_t ldv, ldo;
   const int32_t* cu;        // [S + 1]
   int64_t T;
-  int S, Hq, G, D, tiles;
-  float c;                  // scale * log2 e
+  int S, Hq, Hk, G, D;
+  int heads2;               // 1: the tiles are two heads, 0: two runs of rows
+  int pairs;                // units per run of rows
+  float c;                  // |scale| log2 e
+  int negate;               // the scale is negative: Q enters negated
 };
 
 // Rows [a, b) of sequence s, within the tensors whatever cu holds.
@@ -35,22 +66,6 @@ __device__ __forceinline__ void pt_rows(const PtParams& p, int s, int64_t& a, in
   b = b < a ? a : b > p.T ? p.T : b;
 }
 
-__device__ __forceinline__ void pt_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
-
 __device__ __forceinline__ float pt_ex2(float t) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
@@ -58,7 +73,16 @@ __device__ __forceinline__ float pt_ex2(float t) {
 }
 
 __device__ __forceinline__ uint32_t pt_pack(float lo, float hi) {
-  return (uint32_t)float_to_bf16_bits(lo) | (uint32_t)float_to_bf16_bits(hi) << 16;
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ float2 pt_fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
 }
 
 // Whether one of eight bf16 values is infinite or NaN.
@@ -78,20 +102,20 @@ __device__ __forceinline__ uint4 finite_only(uint4 w) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// The tile `index` of all sequences' query tiles, the last tiles of a sequence first: its
-// sequence's rows and its number within the sequence.  False: there are fewer tiles.
-struct PtTile {
+// The run of rows `index` of all sequences' runs (of `rows` rows), the last runs of a sequence
+// first: its sequence's rows and its number within the sequence.  False: there are fewer.
+struct PtRun {
   int64_t a, b;
-  int tile;
+  int run;
 };
-__device__ __forceinline__ bool pt_find(const PtParams& p, int64_t index, PtTile* found, int64_t* sums) {
+__device__ __forceinline__ bool pt_find(const PtParams& p, int rows, int64_t index, PtRun* found, int64_t* sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found->tile = -1;
+  if (tid == 0) found->run = -1;
   int64_t before = 0;
   for (int s0 = 0; s0 < p.S; s0 += kPtThreads) {
     int64_t a = 0, b = 0;
     if (s0 + tid < p.S) pt_rows(p, s0 + tid, a, b);
-    const int64_t n = (b - a + kPtM - 1) / kPtM;
+    const int64_t n = (b - a + rows - 1) / rows;
     int64_t upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -110,159 +134,331 @@ __device__ __forceinline__ bool pt_find(const PtParams& p, int64_t index, PtTile
     if (index < upto && index >= upto - n) {
       found->a = a;
       found->b = b;
-      found->tile = (int)(upto - 1 - index);
+      found->run = (int)(upto - 1 - index);
     }
     before += all;
     if (index < before) break;   // (uniform)
   }
   __syncthreads();
-  return found->tile >= 0;
+  return found->run >= 0;
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kPtThreads) q4_prompt_kernel(const PtParams p) {
-  constexpr int pitch = DP * 2 + 16;   // bytes
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ PtTile found;
+__device__ __forceinline__ void pt_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int d, int h, int t) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(d), "r"(h), "r"(t)
+      : "memory");
+}
+
+// Shared-memory descriptor of V as the second operand: its rows are keys (the K dimension), 64
+// columns (N) in a 128-byte line; 8 keys are 1024 bytes, the next 64 columns a box further on.
+__device__ __forceinline__ uint64_t pt_v_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(kPtBoxBytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+template <int DB>   // 64-column boxes of a head
+struct PtSmem {
+  static constexpr uint32_t tile = DB * kPtBoxBytes;
+  static constexpr uint32_t q = 0, k = 2 * tile, v = k + kPtStages * tile, bars = v + kPtStages * tile;
+  // barriers: Q; K full, empty; V full, looked over, empty; per tile scores, P, O; all MMAs done
+  static constexpr uint32_t qf = bars, kf = qf + 8, ke = kf + 8 * kPtStages, vf = ke + 8 * kPtStages, vc = vf + 8 * kPtStages,
+                            ve = vc + 8 * kPtStages, sf = ve + 8 * kPtStages, pf = sf + 16, of = pf + 16, done = of + 16,
+                            end = done + 8;
+  static constexpr uint32_t alloc = end + 1024;   // (the base is aligned to 1024)
+};
+
+// Tensor memory: scores and P of tile x, O of tile x.
+__device__ __forceinline__ uint32_t pt_s_col(int x) { return 128u * (uint32_t)x; }
+__device__ __forceinline__ uint32_t pt_o_col(int x) { return 256u + 128u * (uint32_t)x; }
+
+template <int DB>
+__global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_constant__ PtParams p) {
+  using SM = PtSmem<DB>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PtRun found;
   __shared__ int64_t sums[kPtThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  const uint32_t sq = smem_u32(smem), sk = sq + kPtM * pitch, sv = sk + kPtN * pitch;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ volatile int odd_flag;   // V held a value that is not finite
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   pdl_launch_dependents();
+  if (tid == 0) {
+    abort_flag = 0;
+    odd_flag = 0;
+    mbar_init(base + SM::qf, 1);
+    for (int i = 0; i < kPtStages; ++i) {
+      mbar_init(base + SM::kf + 8 * i, 1);
+      mbar_init(base + SM::ke + 8 * i, 1);
+      mbar_init(base + SM::vf + 8 * i, 1);
+      mbar_init(base + SM::vc + 8 * i, 2);
+      mbar_init(base + SM::ve + 8 * i, 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(base + SM::sf + 8 * x, 1);
+      mbar_init(base + SM::pf + 8 * x, 4);
+      mbar_init(base + SM::of + 8 * x, 1);
+    }
+    mbar_init(base + SM::done, 1);
+    fence_mbar_init();
+    prefetch_tmap(&p.mq);
+    prefetch_tmap(&p.mk);
+    prefetch_tmap(&p.mv);
+  }
   pdl_wait_previous();
-  const int h = blockIdx.x % p.Hq;
-  if (!pt_find(p, blockIdx.x / p.Hq, &found, sums)) return;
-  const int64_t row0 = found.a;
-  const int len = (int)(found.b - found.a), q0 = found.tile * kPtM;
-  auto load = [&](const uint16_t* src, int64_t ld, int head, uint32_t dst, int from) {
-    for (int i = tid; i < kPtM * (DP / 8); i += kPtThreads) {
-      const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (from + r < len && d < p.D) w = ld_global_u4(src + (row0 + from + r) * ld + (int64_t)head * p.D + d);
-      st_shared_v4(dst + (uint32_t)(r * pitch + d * 2), w);
-    }
-  };
-  load(p.q, p.ldq, h, sq, q0);
+  const int unit = blockIdx.x % p.pairs;
+  const int64_t run = blockIdx.x / p.pairs;
+  const int run_rows = p.heads2 ? kPtTile : 2 * kPtTile;
+  if (!pt_find(p, run_rows, run, &found, sums)) return;   // (the whole CTA, nothing in flight)
+  if (warp == 8) tmem_alloc(smem_u32(&tmem_base), 512);
+  tc_fence_before();
   __syncthreads();
-  uint32_t qa[DP / 16][4];
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const int64_t row0 = found.a;
+  const int len = (int)(found.b - found.a);
+  // tile x: its first row and head; the blocks of keys that it sees
+  const int q0[2] = {found.run * run_rows, found.run * run_rows + (p.heads2 ? 0 : kPtTile)};
+  const int head[2] = {p.heads2 ? 2 * unit : unit, p.heads2 ? 2 * unit + 1 : unit};
+  const int n0 = (min(len, q0[0] + kPtTile) + kPtTile - 1) / kPtTile;
+  const int n1 = q0[1] < len ? (min(len, q0[1] + kPtTile) + kPtTile - 1) / kPtTile : 0;
+  const int n = max(n0, n1), hk = head[0] / p.G;
+  const int edge = q0[0] / kPtTile;    // blocks from here on hold keys that some row does not see
+  bool ok = true;
+
+  if (warp < 8) {
+    // ------------------------------------------------ softmax
+    setmaxnreg_inc<kPtSoftRegs>();
+    const int x = warp >> 2, nx = x ? n1 : n0;
+    const int row = (x ? q0[1] : q0[0]) + (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + pt_s_col(x), to = tmem + lanes + pt_o_col(x);
+    float m = -INFINITY;
+    float2 l = make_float2(0.f, 0.f);
+    const float2 c2 = make_float2(p.c, p.c);
+    for (int i = 0; i < nx && ok; ++i) {
+      const int kb = nx - 1 - i;
+      ok = warp_wait(base + SM::sf + 8 * x, (uint32_t)(i & 1), &abort_flag, &g_prompt_status);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[4][32];
 #pragma unroll
-  for (int i = 0; i < DP / 16; ++i)
-    ldsm4(qa[i], sq + (uint32_t)((warp * 16 + (lane & 15)) * pitch + i * 32 + (lane >> 4) * 16));
-  float o[DP / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, r[j]);
+      tmem_ld_wait();
+      if (kb * kPtTile + kPtTile - 1 > (x ? q0[1] : q0[0])) {
+        const int see = row - kb * kPtTile;   // keys 0 .. see of the block
 #pragma unroll
-  for (int i = 0; i < DP / 8; ++i)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-  const int rows[2] = {q0 + warp * 16 + g, q0 + warp * 16 + g + 8};
-  const int hk = h / p.G;
-  for (int k0 = 0; k0 < min(len, q0 + kPtM); k0 += kPtN) {
-    __syncthreads();
-    load(p.k, p.ldk, hk, sk, k0);
-    const bool edge = k0 + kPtN > q0;   // some rows do not see all of these keys
-    int odd = 0;
-    for (int i = tid; i < kPtN * (DP / 8); i += kPtThreads) {
-      const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (k0 + r < len && d < p.D) w = ld_global_u4(p.v + (row0 + k0 + r) * p.ldv + (int64_t)hk * p.D + d);
-      if (edge && not_finite(w)) {   // 0 times infinity would reach rows that do not see this key
-        odd = 1;
-        w = finite_only(w);
+          for (int e = 0; e < 32; ++e)
+            if (32 * j + e > see) r[j][e] = 0xFF800000u;
       }
-      st_shared_v4(sv + (uint32_t)(r * pitch + d * 2), w);
-    }
-    odd = __syncthreads_or(odd);
-    float s[kPtN / 8][4];
+      float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < kPtN / 8; ++n) {
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+        for (int e = 0; e < 32; e += 4) {
+          top = fmaxf(top, fmaxf(__uint_as_float(r[j][e]), __uint_as_float(r[j][e + 1])));
+          top2 = fmaxf(top2, fmaxf(__uint_as_float(r[j][e + 2]), __uint_as_float(r[j][e + 3])));
+        }
+      top = fmaxf(top, top2) * p.c;
+      const bool up = top > m + kPtSlack || (m == -INFINITY && top > m);
+      if (__any_sync(0xffffffffu, up)) {
+        const float f = up ? pt_ex2(m - top) : 1.f;
+        if (up) m = top;
+        l = pt_fmul2(l, make_float2(f, f));
+        if (i > 0) {   // (the first P V overwrites O)
+#pragma unroll 1
+          for (int j = 0; j < 2 * DB; ++j) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * j, o);
+            tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < DP / 16; i += 2) {
-        uint32_t b[4];
-        ldsm4(b, sk + (uint32_t)((n * 8 + (lane & 7)) * pitch + i * 32 + (lane >> 3) * 16));
-        pt_mma(s[n], qa[i], b[0], b[1]);
-        pt_mma(s[n], qa[i + 1], b[2], b[3]);
-      }
-    }
-    float top[2] = {m[0], m[1]};
-#pragma unroll
-    for (int n = 0; n < kPtN / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] *= p.c;
-        if (edge && k0 + n * 8 + 2 * c + (e & 1) > rows[e >> 1]) s[n][e] = -INFINITY;
-        top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
-      }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      const float f = top[r] == m[r] ? 1.f : pt_ex2(m[r] - top[r]);
-      m[r] = top[r];
-      l[r] *= f;
-#pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
-        o[i][2 * r] *= f;
-        o[i][2 * r + 1] *= f;
-      }
-      if (top[r] == -INFINITY) top[r] = 0.f;
-    }
-#pragma unroll
-    for (int n = 0; n < kPtN / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] = pt_ex2(s[n][e] - top[e >> 1]);
-        l[e >> 1] += s[n][e];
-      }
-#pragma unroll
-    for (int n = 0; n < kPtN / 16; ++n) {
-      const uint32_t pa[4] = {pt_pack(s[2 * n][0], s[2 * n][1]), pt_pack(s[2 * n][2], s[2 * n][3]),
-                              pt_pack(s[2 * n + 1][0], s[2 * n + 1][1]), pt_pack(s[2 * n + 1][2], s[2 * n + 1][3])};
-#pragma unroll
-      for (int i = 0; i < DP / 8; i += 2) {
-        uint32_t b[4];
-        ldsm4t(b, sv + (uint32_t)((n * 16 + (lane & 15)) * pitch + (i + (lane >> 4)) * 16));
-        pt_mma(o[i], pa, b[0], b[1]);
-        pt_mma(o[i + 1], pa, b[2], b[3]);
-      }
-    }
-    if (odd) {   // what was left out above, for the rows that see it
-      for (int j = k0; j < min(len, k0 + kPtN); ++j) {
-        const uint16_t* src = p.v + (row0 + j) * p.ldv + (int64_t)hk * p.D;
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          if (8 * i >= p.D) break;
-          const uint4 w = ld_global_u4(src + 8 * i);
-          if (!not_finite(w)) continue;
-          const uint32_t x = c == 0 ? w.x : c == 1 ? w.y : c == 2 ? w.z : w.w;
-          const float v2[2] = {bf16lo(x), bf16hi(x)};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j <= rows[e >> 1] && !(fabsf(v2[e & 1]) <= FLT_MAX)) o[i][e] += v2[e & 1];
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(to + 32 * j, o);
+          }
         }
       }
+      const float mu = m == -INFINITY ? 0.f : -m;
+      const float2 m2 = make_float2(mu, mu);
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float2 t = ffma2(make_float2(__uint_as_float(r[j + (e >> 5)][e & 31]), __uint_as_float(r[j + (e >> 5)][(e & 31) + 1])), c2, m2);
+          const float2 pr = make_float2(pt_ex2(t.x), pt_ex2(t.y));
+          l = fadd2(l, pr);
+          w[e >> 1] = pt_pack(pr.x, pr.y);
+        }
+        tmem_st32(ts + 16 * j, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_release(base + SM::pf + 8 * x, lane);
     }
-  }
+    // ------------------------------------------------ the rows of O
+    if (nx > 0 && ok) ok = warp_wait(base + SM::of + 8 * x, 0, &abort_flag, &g_prompt_status);
+    if (nx > 0 && ok) {
+      tc_fence_after();
+      const float inv = 1.f / (l.x + l.y);
+      const bool odd = odd_flag != 0;
+      uint16_t* dst = p.out + (row0 + row) * p.ldo + (int64_t)(x ? head[1] : head[0]) * p.D;
+#pragma unroll 1
+      for (int j = 0; j < 2 * DB; ++j) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * j, o);
+        tmem_ld_wait();
+        if (odd && row < len)   // the keys left out of the products, for the rows that see them
+          for (int key = edge * kPtTile; key <= row; ++key) {
+            const uint16_t* src = p.v + (row0 + key) * p.ldv + (int64_t)hk * p.D + 32 * j;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    if (rows[r] >= len) continue;
-    const float f = 1.f / l[r];
-    uint16_t* dst = p.out + (row0 + rows[r]) * p.ldo + (int64_t)h * p.D;
+            for (int b = 0; b < 4; ++b) {
+              if (32 * j + 8 * b >= p.D) break;
+              const uint4 w = ld_global_u4(src + 8 * b);
+              if (!not_finite(w)) continue;
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
-      if (8 * i < p.D) *reinterpret_cast<uint32_t*>(dst + 8 * i + 2 * c) = pt_pack(o[i][2 * r] * f, o[i][2 * r + 1] * f);
+              for (int e = 0; e < 8; ++e) {
+                const float val = e & 1 ? bf16hi(ws[e >> 1]) : bf16lo(ws[e >> 1]);
+                if (!(fabsf(val) <= FLT_MAX)) o[8 * b + e] = __float_as_uint(__uint_as_float(o[8 * b + e]) + val);
+              }
+            }
+          }
+        if (row < len)
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (32 * j + 8 * b < p.D) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pt_pack(__uint_as_float(o[8 * b + 2 * e]) * inv, __uint_as_float(o[8 * b + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + 32 * j + 8 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+      }
+    }
+    tc_fence_before();
+  } else {
+    setmaxnreg_dec<kPtOtherRegs>();
+    if (warp == 8 && lane == 0) {
+      // ---------------------------------------------- MMAs
+      const int steps = (p.D + 15) / 16;
+      const uint32_t is = idesc_kind_f16(kPtTile, kPtTile, 1) | (p.negate ? 1u << 13 : 0u);
+      const uint32_t io = idesc_kind_f16(kPtTile, steps * 16, 1) | 1u << 16;   // V is N-major
+      auto scores = [&](int x, int i) {
+        const uint32_t a = base + SM::q + (uint32_t)x * SM::tile, b = base + SM::k + (uint32_t)(i % kPtStages) * SM::tile;
+        for (int s = 0; s < steps; ++s) {
+          const uint32_t off = (uint32_t)(s >> 2) * kPtBoxBytes + (uint32_t)(s & 3) * 32;
+          mma_f16(tmem + pt_s_col(x), sw128_desc(a + off), sw128_desc(b + off), is, s > 0);
+        }
+        mma_commit(base + SM::sf + 8 * x);
+      };
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = mbar_wait(bar, parity, &abort_flag, &g_prompt_status);
+        return ok;
+      };
+      // block i of the loop is keys (n - 1 - i) * 128 on; tile x takes part from its own last block on
+      const int from[2] = {n - n0, n - n1};
+      const bool has[2] = {n0 > 0, n1 > 0};
+      if (wait(base + SM::qf, 0) && wait(base + SM::kf, 0)) {
+        for (int x = 0; x < 2; ++x)
+          if (has[x] && from[x] == 0) scores(x, 0);
+        mma_commit(base + SM::ke);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const int st = i % kPtStages;
+        const uint32_t ph = (uint32_t)(i / kPtStages) & 1u;
+        if (!wait(base + SM::vf + 8 * st, ph)) break;
+        if (n - 1 - i >= edge && !wait(base + SM::vc + 8 * st, ph)) break;
+        const bool more = i + 1 < n;
+        if (more && !wait(base + SM::kf + 8 * ((i + 1) % kPtStages), (uint32_t)((i + 1) / kPtStages) & 1u)) break;
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (has[x] && i >= from[x]) {
+            if (!wait(base + SM::pf + 8 * x, (uint32_t)(i - from[x]) & 1u)) break;
+            tc_fence_after();
+            for (int s = 0; s < kPtTile / 16; ++s)
+              mma_f16_ts(tmem + pt_o_col(x), tmem + pt_s_col(x) + 8 * s, pt_v_desc(base + SM::v + (uint32_t)st * SM::tile + 2048u * s),
+                         io, i > from[x] || s > 0);
+            if (!more) mma_commit(base + SM::of + 8 * x);
+          }
+          if (x == 1) mma_commit(base + SM::ve + 8 * st);
+          if (more && has[x] && i + 1 >= from[x]) scores(x, i + 1);
+        }
+        if (more && ok) mma_commit(base + SM::ke + 8 * ((i + 1) % kPtStages));
+      }
+      // nothing is in flight behind this
+      mma_commit(base + SM::done);
+      mbar_drain(base + SM::done, 0);
+    } else if (warp == 9 && lane == 0) {
+      // ---------------------------------------------- copies
+      mbar_expect_tx(base + SM::qf, (n1 > 0 ? 2 : 1) * SM::tile);
+      for (int x = 0; x < (n1 > 0 ? 2 : 1); ++x)
+        for (int b = 0; b < DB; ++b)
+          pt_load(base + SM::q + (uint32_t)x * SM::tile + b * kPtBoxBytes, &p.mq, base + SM::qf, 64 * b, head[x], (int)(row0 + q0[x]));
+      int issued = 0;
+      for (; issued < n; ++issued) {
+        const int st = issued % kPtStages, t = (int)row0 + (n - 1 - issued) * kPtTile;
+        const uint32_t ph = ((uint32_t)(issued / kPtStages) & 1u) ^ 1u;
+        if (issued >= kPtStages && (!mbar_wait(base + SM::ke + 8 * st, ph, &abort_flag, &g_prompt_status) ||
+                                    !mbar_wait(base + SM::ve + 8 * st, ph, &abort_flag, &g_prompt_status)))
+          break;
+        mbar_expect_tx(base + SM::kf + 8 * st, SM::tile);
+        for (int b = 0; b < DB; ++b) pt_load(base + SM::k + (uint32_t)st * SM::tile + b * kPtBoxBytes, &p.mk, base + SM::kf + 8 * st, 64 * b, hk, t);
+        mbar_expect_tx(base + SM::vf + 8 * st, SM::tile);
+        for (int b = 0; b < DB; ++b) pt_load(base + SM::v + (uint32_t)st * SM::tile + b * kPtBoxBytes, &p.mv, base + SM::vf + 8 * st, 64 * b, hk, t);
+      }
+      // the CTA does not end before its copies have landed
+      mbar_drain(base + SM::qf, 0);
+      for (int i = max(0, issued - kPtStages); i < issued; ++i) {
+        mbar_drain(base + SM::kf + 8 * (i % kPtStages), (uint32_t)(i / kPtStages) & 1u);
+        mbar_drain(base + SM::vf + 8 * (i % kPtStages), (uint32_t)(i / kPtStages) & 1u);
+      }
+    } else if (warp >= 10) {
+      // ---------------------------------------------- V at the edge
+      for (int i = 0; i < n && n - 1 - i >= edge; ++i) {
+        const int st = i % kPtStages;
+        const uint32_t ph = (uint32_t)(i / kPtStages) & 1u;
+        if (!warp_wait(base + SM::vf + 8 * st, ph, &abort_flag, &g_prompt_status)) break;
+        const uint32_t at = base + SM::v + (uint32_t)st * SM::tile;
+        for (uint32_t o = (uint32_t)(tid - 320) * 16; o < SM::tile; o += 64 * 16) {
+          const uint4 w = ld_shared_v4(at + o);
+          if (not_finite(w)) {
+            st_shared_v4(at + o, finite_only(w));
+            odd_flag = 1;
+          }
+        }
+        fence_proxy_async();
+        warp_release(base + SM::vc + 8 * st, lane);
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
   }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-template <int DP>
+// Rows of heads as a tensor (D, heads, T) of boxes of 64 columns of a head and 128 rows.
+bool pt_map(CUtensorMap* m, const void* base, int64_t D, int64_t heads, int64_t T, int64_t ld) {
+  return encode_map_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, {(uint64_t)D, (uint64_t)heads, (uint64_t)T},
+                       {(uint64_t)D * 2, (uint64_t)ld * 2}, {64, 1, kPtTile}, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int DB>
 int pt_run(const PtParams& p, unsigned blocks, cudaStream_t stream) {
-  constexpr int smem = 3 * kPtM * (DP * 2 + 16);
+  constexpr int smem = (int)PtSmem<DB>::alloc;
   static bool set[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !set[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_prompt_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+    if (cuda_check(cudaFuncSetAttribute(q4_prompt_kernel<DB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                    "prompt_attention: cudaFuncSetAttribute(max dynamic shared memory)"))
       return Q4LIN_ERR_CUDA;
     if (dev < 64) set[dev] = true;
@@ -277,21 +473,51 @@ int pt_run(const PtParams& p, unsigned blocks, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_prompt_kernel<DP>, p), "prompt_attention: kernel launch");
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_prompt_kernel<DB>, p), "prompt_attention: kernel launch");
 }
 
 }  // namespace
 
 int prompt_launch(const PromptArgs& a) {
-  PtParams p{a.q, a.k, a.v, a.out, a.ldq, a.ldk, a.ldv, a.ldo, a.cu, a.T, (int)a.S, (int)a.Hq, (int)(a.Hq / a.Hk), (int)a.D, 0,
-             a.scale * 1.4426950408889634f};
-  // tiles: at most one that is not full per sequence
-  const int64_t blocks = ((a.T + kPtM - 1) / kPtM + a.S) * a.Hq;
+  PtParams p{};
+  if (!pt_map(&p.mq, a.q, a.D, a.Hq, a.T, a.ldq) || !pt_map(&p.mk, a.k, a.D, a.Hk, a.T, a.ldk) ||
+      !pt_map(&p.mv, a.v, a.D, a.Hk, a.T, a.ldv)) {
+    set_error_detail("prompt_attention: the tensors cannot be described to the copy engine");
+    return Q4LIN_ERR_CUDA;
+  }
+  p.v = a.v;
+  p.out = a.out;
+  p.ldv = a.ldv;
+  p.ldo = a.ldo;
+  p.cu = a.cu;
+  p.T = a.T;
+  p.S = (int)a.S;
+  p.Hq = (int)a.Hq;
+  p.Hk = (int)a.Hk;
+  p.G = (int)(a.Hq / a.Hk);
+  p.D = (int)a.D;
+  p.heads2 = p.G % 2 == 0;
+  p.pairs = p.heads2 ? p.Hq / 2 : p.Hq;
+  // (a scale of 0 becomes the smallest that keeps a masked -inf one)
+  p.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, FLT_TRUE_MIN);
+  p.negate = a.scale < 0.f;
+  // runs of rows: at most one that is not full per sequence
+  const int64_t rows = p.heads2 ? kPtTile : 2 * kPtTile;
+  const int64_t blocks = ((a.T + rows - 1) / rows + a.S) * p.pairs;
   if (blocks > 0x7fffffff) {
     set_error_detail("prompt_attention: too many tokens for one launch");
     return Q4LIN_ERR_UNSUPPORTED_SHAPE;
   }
-  return a.D <= 64 ? pt_run<64>(p, (unsigned)blocks, a.stream) : pt_run<128>(p, (unsigned)blocks, a.stream);
+  return a.D <= 64 ? pt_run<1>(p, (unsigned)blocks, a.stream) : pt_run<2>(p, (unsigned)blocks, a.stream);
+}
+
+int prompt_status(int* value, bool clear) {
+  if (cudaMemcpyFromSymbol(value, g_prompt_status, sizeof(int)) != cudaSuccess) return Q4LIN_ERR_CUDA;
+  if (clear) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_prompt_status, &zero, sizeof(int)) != cudaSuccess) return Q4LIN_ERR_CUDA;
+  }
+  return Q4LIN_OK;
 }
 
 }  // namespace q4

@@ -972,6 +972,8 @@ static int read_status(bool clear) {
   if (v) worst = v;
   if (q4::moe_status(&v, clear) != Q4LIN_OK) return Q4LIN_ERR_CUDA;
   if (v) worst = v;
+  if (q4::prompt_status(&v, clear) != Q4LIN_OK) return Q4LIN_ERR_CUDA;
+  if (v) worst = v;
   if (q4::kv_status(&v, clear) != Q4LIN_OK) return Q4LIN_ERR_CUDA;
   if (v) worst = v;
   return worst;
