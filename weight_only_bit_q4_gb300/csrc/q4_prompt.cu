@@ -12,20 +12,21 @@
 // Split: a CTA (one per SM) owns two tiles of 128 query rows, A and B, that read the same keys: two
 // heads of a group where there is an even number of them, else two runs of rows of a head.  Blocks
 // of 128 keys stream through shared memory (TMA, 128-byte swizzle), from the diagonal down.
-//   warps 0-3, 4-7   softmax of A, of B: a thread owns a row.  It reads its 128 scores from tensor
+//   warps 4-7, 8-11  softmax of A, of B: a thread owns a row.  It reads its 128 scores from tensor
 //                    memory, and writes P (bf16) over them.  The reference m moves only when a
 //                    score passes it by 2^8 (P and the sums then hold up to 2^8 times more, far
 //                    from any end); only then is the row of O in tensor memory rescaled, by the
 //                    same thread: the block's scores are complete only after the last P V.
-//   warp 8           issues the MMAs: per block and tile P V (P from tensor memory, V as an
+//   warp 0           issues the MMAs: per block and tile P V (P from tensor memory, V as an
 //                    MN-major operand), then the next block's Q K^T into the same columns.
 //                    While A's are computed, B's softmax runs, and the other way round.
-//   warp 9           issues the copies.
-//   warps 10, 11     look blocks of V that hold keys some rows must not see over for values that are
+//   warp 1           issues the copies.
+//   warps 2, 3       look blocks of V that hold keys some rows must not see over for values that are
 //                    not finite (0 times infinity would reach those rows).  They become zeros for
 //                    the MMA; the rows that see such a key add it at the end.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "q4_internal.h"
 #include "q4_sm100.cuh"
@@ -41,7 +42,7 @@ constexpr int kPtSoftRegs = 224, kPtOtherRegs = 56;
 // the shares of three warpgroups come out of the registers at launch (168 a thread)
 static_assert(2 * kPtSoftRegs + kPtOtherRegs <= 3 * 168, "register split");
 constexpr uint32_t kPtBoxBytes = 64 * 2 * kPtTile;   // 64 columns of a tile
-constexpr int kPtStages = 2;          // of K and of V each
+constexpr int kPtK = 2, kPtV = 3;     // stages of K and of V (all that shared memory holds for D = 128)
 __device__ int g_prompt_status = 0;
 
 struct PtParams {
@@ -165,11 +166,10 @@ __device__ __forceinline__ uint64_t pt_v_desc(uint32_t saddr) {
 template <int DB>   // 64-column boxes of a head
 struct PtSmem {
   static constexpr uint32_t tile = DB * kPtBoxBytes;
-  static constexpr uint32_t q = 0, k = 2 * tile, v = k + kPtStages * tile, bars = v + kPtStages * tile;
-  // barriers: Q; K full, empty; V full, looked over, empty; per tile scores, P, O; all MMAs done
-  static constexpr uint32_t qf = bars, kf = qf + 8, ke = kf + 8 * kPtStages, vf = ke + 8 * kPtStages, vc = vf + 8 * kPtStages,
-                            ve = vc + 8 * kPtStages, sf = ve + 8 * kPtStages, pf = sf + 16, of = pf + 16, done = of + 16,
-                            end = done + 8;
+  static constexpr uint32_t q = 0, k = 2 * tile, v = k + kPtK * tile, bars = v + kPtV * tile;
+  // barriers: Q; K full, empty; V full, empty; per tile scores, P (with its operands), O; all MMAs done
+  static constexpr uint32_t qf = bars, kf = qf + 8, ke = kf + 8 * kPtK, vf = ke + 8 * kPtK,
+                            ve = vf + 8 * kPtV, sf = ve + 8 * kPtV, pf = sf + 16, of = pf + 16, done = of + 16, end = done + 8;
   static constexpr uint32_t alloc = end + 1024;   // (the base is aligned to 1024)
 };
 
@@ -193,16 +193,17 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
     abort_flag = 0;
     odd_flag = 0;
     mbar_init(base + SM::qf, 1);
-    for (int i = 0; i < kPtStages; ++i) {
+    for (int i = 0; i < kPtK; ++i) {
       mbar_init(base + SM::kf + 8 * i, 1);
       mbar_init(base + SM::ke + 8 * i, 1);
+    }
+    for (int i = 0; i < kPtV; ++i) {
       mbar_init(base + SM::vf + 8 * i, 1);
-      mbar_init(base + SM::vc + 8 * i, 2);
       mbar_init(base + SM::ve + 8 * i, 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(base + SM::sf + 8 * x, 1);
-      mbar_init(base + SM::pf + 8 * x, 4);
+      mbar_init(base + SM::pf + 8 * x, 6);   // four softmax warps, warps 2 and 3
       mbar_init(base + SM::of + 8 * x, 1);
     }
     mbar_init(base + SM::done, 1);
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
   const int64_t run = blockIdx.x / p.pairs;
   const int run_rows = p.heads2 ? kPtTile : 2 * kPtTile;
   if (!pt_find(p, run_rows, run, &found, sums)) return;   // (the whole CTA, nothing in flight)
-  if (warp == 8) tmem_alloc(smem_u32(&tmem_base), 512);
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_base), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -232,10 +233,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
   const int edge = q0[0] / kPtTile;    // blocks from here on hold keys that some row does not see
   bool ok = true;
 
-  if (warp < 8) {
+  if (warp >= 4) {
     // ------------------------------------------------ softmax
     setmaxnreg_inc<kPtSoftRegs>();
-    const int x = warp >> 2, nx = x ? n1 : n0;
+    const int x = (warp >> 2) - 1, nx = x ? n1 : n0;
     const int row = (x ? q0[1] : q0[0]) + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + pt_s_col(x), to = tmem + lanes + pt_o_col(x);
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
     const float2 c2 = make_float2(p.c, p.c);
     for (int i = 0; i < nx && ok; ++i) {
       const int kb = nx - 1 - i;
-      ok = warp_wait(base + SM::sf + 8 * x, (uint32_t)(i & 1), &abort_flag, &g_prompt_status);
+      ok = warp_wait_vote(base + SM::sf + 8 * x, (uint32_t)(i & 1), &abort_flag, &g_prompt_status);
       if (!ok) break;
       tc_fence_after();
       uint32_t r[4][32];
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
       warp_release(base + SM::pf + 8 * x, lane);
     }
     // ------------------------------------------------ the rows of O
-    if (nx > 0 && ok) ok = warp_wait(base + SM::of + 8 * x, 0, &abort_flag, &g_prompt_status);
+    if (nx > 0 && ok) ok = warp_wait_vote(base + SM::of + 8 * x, 0, &abort_flag, &g_prompt_status);
     if (nx > 0 && ok) {
       tc_fence_after();
       const float inv = 1.f / (l.x + l.y);
@@ -346,95 +347,151 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
     tc_fence_before();
   } else {
     setmaxnreg_dec<kPtOtherRegs>();
-    if (warp == 8 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------- MMAs
       const int steps = (p.D + 15) / 16;
       const uint32_t is = idesc_kind_f16(kPtTile, kPtTile, 1) | (p.negate ? 1u << 13 : 0u);
-      const uint32_t io = idesc_kind_f16(kPtTile, steps * 16, 1) | 1u << 16;   // V is N-major
-      auto scores = [&](int x, int i) {
-        const uint32_t a = base + SM::q + (uint32_t)x * SM::tile, b = base + SM::k + (uint32_t)(i % kPtStages) * SM::tile;
-        for (int s = 0; s < steps; ++s) {
-          const uint32_t off = (uint32_t)(s >> 2) * kPtBoxBytes + (uint32_t)(s & 3) * 32;
-          mma_f16(tmem + pt_s_col(x), sw128_desc(a + off), sw128_desc(b + off), is, s > 0);
+      const uint32_t io = idesc_kind_f16(kPtTile, 16, 1) + ((uint32_t)(steps - 1) << 18) | 1u << 16;   // N = D, V is N-major
+      // descriptors as 32-bit halves; the low one counts in 16 bytes
+      const uint64_t qd = sw128_desc(base + SM::q), kd = sw128_desc(base + SM::k), vd = pt_v_desc(base + SM::v);
+      const uint32_t kmajor = (uint32_t)(qd >> 32), nmajor = (uint32_t)(vd >> 32);
+      const bool one = elect_one();
+      auto scores = [&](auto lo, auto hi, int x, uint32_t st) {   // k-steps lo .. hi - 1 of Q K^T
+        const uint32_t a = (uint32_t)qd + (uint32_t)x * (SM::tile >> 4), b = (uint32_t)kd + st * (SM::tile >> 4);
+        if (one) {
+#pragma unroll
+          for (int s = lo.value; s < hi.value; ++s)
+            if (s < steps) {
+              constexpr uint32_t box = kPtBoxBytes >> 4;
+              mma_f16_ss(tmem + pt_s_col(x), a + (uint32_t)(s >> 2) * box + 2u * (s & 3), kmajor,
+                         b + (uint32_t)(s >> 2) * box + 2u * (s & 3), kmajor, is, s > 0);
+            }
         }
-        mma_commit(base + SM::sf + 8 * x);
+      };
+      using Lo = std::integral_constant<int, 0>;
+      using Mid = std::integral_constant<int, DB == 2 ? 5 : 2>;
+      using Hi = std::integral_constant<int, 4 * DB>;
+      auto values = [&](int x, uint32_t st, uint32_t join) {   // P V
+        const uint32_t b = (uint32_t)vd + st * (SM::tile >> 4);
+        if (one) {
+#pragma unroll
+          for (int s = 0; s < kPtTile / 16; ++s)
+            mma_f16_ts32(tmem + pt_o_col(x), tmem + pt_s_col(x) + 8u * s, b + 128u * s, nmajor, io, s > 0 ? 1u : join);
+        }
+      };
+      auto commit = [&](uint32_t bar) {
+        if (one) mma_commit(bar);
       };
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = mbar_wait(bar, parity, &abort_flag, &g_prompt_status);
+        if (ok) ok = warp_wait_vote(bar, parity, &abort_flag, &g_prompt_status);
         return ok;
       };
       // block i of the loop is keys (n - 1 - i) * 128 on; tile x takes part from its own last block on
-      const int from[2] = {n - n0, n - n1};
-      const bool has[2] = {n0 > 0, n1 > 0};
+      const int from0 = n - n0, from1 = n1 > 0 ? n - n1 : n;
+      const uint32_t pf = base + SM::pf, sf = base + SM::sf;
+      uint32_t vs = 0, ks = 0, ph0 = 0, ph1 = 0;   // stages of V of block i and of K of block i + 1; phases
       if (wait(base + SM::qf, 0) && wait(base + SM::kf, 0)) {
         for (int x = 0; x < 2; ++x)
-          if (has[x] && from[x] == 0) scores(x, 0);
-        mma_commit(base + SM::ke);
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        const int st = i % kPtStages;
-        const uint32_t ph = (uint32_t)(i / kPtStages) & 1u;
-        if (!wait(base + SM::vf + 8 * st, ph)) break;
-        if (n - 1 - i >= edge && !wait(base + SM::vc + 8 * st, ph)) break;
-        const bool more = i + 1 < n;
-        if (more && !wait(base + SM::kf + 8 * ((i + 1) % kPtStages), (uint32_t)((i + 1) / kPtStages) & 1u)) break;
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (has[x] && i >= from[x]) {
-            if (!wait(base + SM::pf + 8 * x, (uint32_t)(i - from[x]) & 1u)) break;
-            tc_fence_after();
-            for (int s = 0; s < kPtTile / 16; ++s)
-              mma_f16_ts(tmem + pt_o_col(x), tmem + pt_s_col(x) + 8 * s, pt_v_desc(base + SM::v + (uint32_t)st * SM::tile + 2048u * s),
-                         io, i > from[x] || s > 0);
-            if (!more) mma_commit(base + SM::of + 8 * x);
+          if ((x ? from1 : from0) == 0) {
+            scores(Lo{}, Hi{}, x, 0);
+            commit(sf + 8 * x);
           }
-          if (x == 1) mma_commit(base + SM::ve + 8 * st);
-          if (more && has[x] && i + 1 >= from[x]) scores(x, i + 1);
+        commit(base + SM::ke);
+      }
+      // The barrier of a tile's P stands for V of the block and K of the next one too (warps 2 and 3 wait
+      // for those).  It is looked up once in the middle of the other tile's Q K^T: a wait's own
+      // latency (some 300 cycles beside two softmax warps) then lies behind work in the queue.
+      bool there = false;
+      for (int i = 0; i < n && ok; ++i) {
+        const bool more = i + 1 < n;
+        if (more && ++ks == kPtK) ks = 0;
+        if (i >= from0) {
+          if (!there && !wait(pf, ph0)) break;
+          ph0 ^= 1u;
+          tc_fence_after();
+          values(0, vs, i > from0);
+          if (!more) commit(base + SM::of);
         }
-        if (more && ok) mma_commit(base + SM::ke + 8 * ((i + 1) % kPtStages));
+        const bool s0 = more && i + 1 >= from0, s1 = more && i + 1 >= from1;
+        if (s0) scores(Lo{}, Mid{}, 0, ks);
+        there = i >= from1 && warp_test(pf + 8, ph1);
+        if (s0) {
+          scores(Mid{}, Hi{}, 0, ks);
+          commit(sf);
+        }
+        if (i >= from1) {
+          if (!there && !wait(pf + 8, ph1)) break;
+          ph1 ^= 1u;
+          tc_fence_after();
+          values(1, vs, i > from1);
+          if (!more) commit(base + SM::of + 8);
+        }
+        commit(base + SM::ve + 8 * vs);
+        if (++vs == kPtV) vs = 0;
+        if (s1) scores(Lo{}, Mid{}, 1, ks);
+        there = s0 && warp_test(pf, ph0);
+        if (s1) {
+          scores(Mid{}, Hi{}, 1, ks);
+          commit(sf + 8);
+        }
+        if (more) commit(base + SM::ke + 8 * ks);
       }
       // nothing is in flight behind this
-      mma_commit(base + SM::done);
-      mbar_drain(base + SM::done, 0);
-    } else if (warp == 9 && lane == 0) {
+      commit(base + SM::done);
+      if (one) mbar_drain(base + SM::done, 0);
+    } else if (warp == 1 && lane == 0) {
       // ---------------------------------------------- copies
       mbar_expect_tx(base + SM::qf, (n1 > 0 ? 2 : 1) * SM::tile);
       for (int x = 0; x < (n1 > 0 ? 2 : 1); ++x)
         for (int b = 0; b < DB; ++b)
           pt_load(base + SM::q + (uint32_t)x * SM::tile + b * kPtBoxBytes, &p.mq, base + SM::qf, 64 * b, head[x], (int)(row0 + q0[x]));
-      int issued = 0;
-      for (; issued < n; ++issued) {
-        const int st = issued % kPtStages, t = (int)row0 + (n - 1 - issued) * kPtTile;
-        const uint32_t ph = ((uint32_t)(issued / kPtStages) & 1u) ^ 1u;
-        if (issued >= kPtStages && (!mbar_wait(base + SM::ke + 8 * st, ph, &abort_flag, &g_prompt_status) ||
-                                    !mbar_wait(base + SM::ve + 8 * st, ph, &abort_flag, &g_prompt_status)))
-          break;
-        mbar_expect_tx(base + SM::kf + 8 * st, SM::tile);
-        for (int b = 0; b < DB; ++b) pt_load(base + SM::k + (uint32_t)st * SM::tile + b * kPtBoxBytes, &p.mk, base + SM::kf + 8 * st, 64 * b, hk, t);
-        mbar_expect_tx(base + SM::vf + 8 * st, SM::tile);
-        for (int b = 0; b < DB; ++b) pt_load(base + SM::v + (uint32_t)st * SM::tile + b * kPtBoxBytes, &p.mv, base + SM::vf + 8 * st, 64 * b, hk, t);
+      // the loads of block i, K's and V's: a stage is free once its last use has completed
+      int ki = 0, vi = 0;
+      auto load = [&](const CUtensorMap* map, uint32_t tiles, uint32_t full, uint32_t empty, int stages, int& i) {
+        const int st = i % stages;
+        if (i >= stages && !mbar_wait(empty + 8 * st, ((uint32_t)(i / stages) & 1u) ^ 1u, &abort_flag, &g_prompt_status)) return false;
+        mbar_expect_tx(full + 8 * st, SM::tile);
+        for (int b = 0; b < DB; ++b)
+          pt_load(tiles + (uint32_t)st * SM::tile + b * kPtBoxBytes, map, full + 8 * st, 64 * b, hk, (int)row0 + (n - 1 - i) * kPtTile);
+        ++i;
+        return true;
+      };
+      while (vi < n) {   // (K of block i + 1 is wanted before V of block i)
+        if (ki < n && !load(&p.mk, base + SM::k, base + SM::kf, base + SM::ke, kPtK, ki)) break;
+        if (ki == 1 && ki < n && !load(&p.mk, base + SM::k, base + SM::kf, base + SM::ke, kPtK, ki)) break;
+        if (!load(&p.mv, base + SM::v, base + SM::vf, base + SM::ve, kPtV, vi)) break;
       }
       // the CTA does not end before its copies have landed
       mbar_drain(base + SM::qf, 0);
-      for (int i = max(0, issued - kPtStages); i < issued; ++i) {
-        mbar_drain(base + SM::kf + 8 * (i % kPtStages), (uint32_t)(i / kPtStages) & 1u);
-        mbar_drain(base + SM::vf + 8 * (i % kPtStages), (uint32_t)(i / kPtStages) & 1u);
-      }
-    } else if (warp >= 10) {
-      // ---------------------------------------------- V at the edge
-      for (int i = 0; i < n && n - 1 - i >= edge; ++i) {
-        const int st = i % kPtStages;
-        const uint32_t ph = (uint32_t)(i / kPtStages) & 1u;
-        if (!warp_wait(base + SM::vf + 8 * st, ph, &abort_flag, &g_prompt_status)) break;
-        const uint32_t at = base + SM::v + (uint32_t)st * SM::tile;
-        for (uint32_t o = (uint32_t)(tid - 320) * 16; o < SM::tile; o += 64 * 16) {
-          const uint4 w = ld_shared_v4(at + o);
-          if (not_finite(w)) {
-            st_shared_v4(at + o, finite_only(w));
-            odd_flag = 1;
+      for (int i = max(0, ki - kPtK); i < ki; ++i) mbar_drain(base + SM::kf + 8 * (i % kPtK), (uint32_t)(i / kPtK) & 1u);
+      for (int i = max(0, vi - kPtV); i < vi; ++i) mbar_drain(base + SM::vf + 8 * (i % kPtV), (uint32_t)(i / kPtV) & 1u);
+    } else if (warp >= 2) {
+      // ---------------------------------------------- V at the edge, and word that a block's operands are there
+      const int from[2] = {n - n0, n1 > 0 ? n - n1 : n};
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = warp_wait_vote(bar, parity, &abort_flag, &g_prompt_status);
+        return ok;
+      };
+      for (int i = 0; i < n && ok; ++i) {
+        if (!wait(base + SM::vf + 8 * (i % kPtV), (uint32_t)(i / kPtV) & 1u)) break;
+        if (n - 1 - i >= edge) {
+          const uint32_t at = base + SM::v + (uint32_t)(i % kPtV) * SM::tile;
+          for (uint32_t o = (uint32_t)(tid - 64) * 16; o < SM::tile; o += 64 * 16) {
+            const uint4 w = ld_shared_v4(at + o);
+            if (not_finite(w)) {
+              st_shared_v4(at + o, finite_only(w));
+              odd_flag = 1;
+            }
           }
+          fence_proxy_async();
         }
-        fence_proxy_async();
-        warp_release(base + SM::vc + 8 * st, lane);
+        if (i + 1 < n && !wait(base + SM::kf + 8 * ((i + 1) % kPtK), (uint32_t)((i + 1) / kPtK) & 1u)) break;
+        for (int x = 0; x < 2; ++x)
+          if (i >= from[x]) {
+            // (an arrival before the last phase is complete would count for that one)
+            if (i > from[x] && !wait(base + SM::pf + 8 * x, (uint32_t)(i - from[x] - 1) & 1u)) break;
+            warp_release(base + SM::pf + 8 * x, lane);
+          }
       }
     }
     __syncwarp();
@@ -442,7 +499,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
 // Rows of heads as a tensor (D, heads, T) of boxes of 64 columns of a head and 128 rows.

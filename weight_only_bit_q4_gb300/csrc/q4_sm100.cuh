@@ -61,6 +61,43 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
+// The same with every lane polling and the warp voting: no branch on one lane, no shuffle, so a
+// wait whose phase has completed already costs a query and a vote.
+__device__ __forceinline__ bool warp_wait_vote(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag)) return false;
+  }
+  *abort_flag = 1;
+  if ((threadIdx.x & 31) == 0) atomicExch(status, (int)Q4LIN_ERR_TIMEOUT);
+  return false;
+}
+
+// Whether the phase has completed, without waiting; the warp's common answer.
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
+// One lane of a converged warp, the same every time.  Code under it stays uniform to the compiler,
+// where a test of the lane's number would make it a divergent branch.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // Release of a shared-memory stage by a warp that has read it: the fence keeps every lane's
 // reads before lane 0's arrival, which lets a copy refill the stage.  Without it a build of the
 // tile kernel's Q6 form read chunks after the arrival, and now and then got the refill's.  Every
