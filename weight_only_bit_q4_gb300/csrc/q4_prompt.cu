@@ -9,8 +9,9 @@
 // Bound: the tensor cores (4 D operations per query head and pair of tokens that see each other);
 // beside them the exponentials, one per pair.
 //
-// Split: a CTA (one per SM) owns two tiles of 128 query rows, A and B, that read the same keys: two
-// heads of a group where there is an even number of them, else two runs of rows of a head.  Blocks
+// Split: a unit of work is two tiles of 128 query rows, A and B, that read the same keys: two
+// heads of a group where there is an even number of them, else two runs of rows of a head.  One CTA per
+// SM stays and takes further units off the launch as long as there are any, the costliest first.  Blocks
 // of 128 keys stream through shared memory (TMA, 128-byte swizzle), from the diagonal down.
 //   warps 4-7, 8-11  softmax of A, of B: a thread owns a row.  It reads its 128 scores from tensor
 //                    memory, and writes P (bf16) over them.  The reference m moves only when a
@@ -21,9 +22,11 @@
 //                    MN-major operand), then the next block's Q K^T into the same columns.
 //                    While A's are computed, B's softmax runs, and the other way round.
 //   warp 1           issues the copies.
-//   warps 2, 3       look blocks of V that hold keys some rows must not see over for values that are
-//                    not finite (0 times infinity would reach those rows).  They become zeros for
-//                    the MMA; the rows that see such a key add it at the end.
+//   warp 2           reports that a block's operands are there.  Before, it looks blocks of V that hold
+//                    keys some rows must not see over for values that are not finite (0 times
+//                    infinity would reach those rows): they become zeros for the MMA, and the rows
+//                    that see such a key add it at the end.
+//   warp 3           finds the units, one ahead of the other roles.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -38,7 +41,7 @@ namespace {
 constexpr int kPtThreads = 384;
 constexpr int kPtTile = 128;          // rows of a tile, keys of a block
 constexpr float kPtSlack = 8.f;       // log2 of how far a score may pass its row's reference
-constexpr int kPtSoftRegs = 224, kPtOtherRegs = 56;
+constexpr int kPtSoftRegs = 216, kPtOtherRegs = 72;
 // the shares of three warpgroups come out of the registers at launch (168 a thread)
 static_assert(2 * kPtSoftRegs + kPtOtherRegs <= 3 * 168, "register split");
 constexpr uint32_t kPtBoxBytes = 64 * 2 * kPtTile;   // 64 columns of a tile
@@ -103,45 +106,124 @@ __device__ __forceinline__ uint4 finite_only(uint4 w) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// The run of rows `index` of all sequences' runs (of `rows` rows), the last runs of a sequence
-// first: its sequence's rows and its number within the sequence.  False: there are fewer.
-struct PtRun {
-  int64_t a, b;
-  int run;
+// A unit of work: rows [row0, row0 + len) are its sequence, tiles A and B start at rows q0, q1 of it and
+// see n0, n1 blocks of keys; the query head of A (B's is the next, or the same).
+struct PtUnit {
+  int row0, len, q0, q1, head, n0, n1, there;   // there: 0 ends the CTA's work
 };
-__device__ __forceinline__ bool pt_find(const PtParams& p, int rows, int64_t index, PtRun* found, int64_t* sums) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) found->run = -1;
-  int64_t before = 0;
-  for (int s0 = 0; s0 < p.S; s0 += kPtThreads) {
-    int64_t a = 0, b = 0;
-    if (s0 + tid < p.S) pt_rows(p, s0 + tid, a, b);
-    const int64_t n = (b - a + rows - 1) / rows;
-    int64_t upto = n;
+
+// Units in the order of their cost: the last runs of all sequences first.  One warp; lane l holds the
+// numbers of runs of sequences l, l + 32, .. .  With more sequences than kPtSorted the runs are taken
+// sequence by sequence, the last run first (they are short then).
+constexpr int kPtSorted = 256;
+struct PtOrder {
+  int n[kPtSorted / 32];
+  int most, level;   // the highest number plus one; that of the last run found
+  int64_t before;    // (not sorted) runs of the sequences before s
+  int s;
+  bool sorted;
+
+  __device__ __forceinline__ void start(const PtParams& p, int rows, int lane) {
+    sorted = p.S <= kPtSorted;
+    before = 0;
+    s = most = 0;
+    if (!sorted) return;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
+    for (int k = 0; k < kPtSorted / 32; ++k) {
+      n[k] = 0;
+      if (32 * k + lane < p.S) {
+        int64_t a, b;
+        pt_rows(p, 32 * k + lane, a, b);
+        n[k] = (int)((b - a + rows - 1) / rows);
+      }
+      most = max(most, n[k]);
     }
-    __syncthreads();
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    int64_t all = 0;
-    for (int w = 0; w < kPtThreads / 32; ++w) {
-      if (w < warp) upto += sums[w];
-      all += sums[w];
-    }
-    upto += before;
-    if (index < upto && index >= upto - n) {
-      found->a = a;
-      found->b = b;
-      found->run = (int)(upto - 1 - index);
-    }
-    before += all;
-    if (index < before) break;   // (uniform)
+    level = most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
   }
-  __syncthreads();
-  return found->run >= 0;
+
+  // Runs whose number is j or more.
+  __device__ __forceinline__ int64_t runs_from(int j) const {
+    unsigned c = 0;
+#pragma unroll
+    for (int k = 0; k < kPtSorted / 32; ++k) c += (unsigned)max(0, n[k] - j);
+    return (int64_t)__reduce_add_sync(0xffffffffu, c);   // (below T / rows + S)
+  }
+
+  // Sequence and run of the index-th run; false: there are fewer.
+  __device__ __forceinline__ bool find(const PtParams& p, int rows, int64_t index, int lane, int& seq, int& run) {
+    if (sorted) {
+      if (runs_from(0) <= index) return false;
+      // the largest number whose runs and those above it are more than index: often the last one's
+      int lo = 0, hi = most;
+      if (runs_from(level) > index) lo = level;
+      else hi = level;
+      while (hi - lo > 1) {
+        const int mid = lo == level && lo > 0 ? lo + 1 : (lo + hi) / 2;
+        if (runs_from(mid) > index) lo = mid;
+        else hi = mid;
+      }
+      level = lo;
+      int rank = (int)(index - runs_from(lo + 1));
+      run = lo;
+      seq = -1;
+#pragma unroll
+      for (int k = 0; k < kPtSorted / 32; ++k) {
+        const unsigned has = __ballot_sync(0xffffffffu, n[k] > lo);
+        if (seq < 0 && rank < __popc(has)) {
+          const bool mine = (has >> lane & 1u) && __popc(has & ((1u << lane) - 1u)) == rank;
+          seq = 32 * k + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        }
+        rank -= __popc(has);
+      }
+      return true;
+    }
+    if (index < before) s = 0, before = 0;
+    for (; s < p.S; s += 32) {
+      int64_t a = 0, b = 0;
+      if (s + lane < p.S) pt_rows(p, s + lane, a, b);
+      const int runs = (int)((b - a + rows - 1) / rows);
+      int64_t upto = runs;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+      if (index < before + all) {
+        const bool mine = index < before + upto && index >= before + upto - runs;
+        const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        seq = s + from;
+        run = __shfl_sync(0xffffffffu, (int)(before + upto - 1 - index), from);
+        return true;
+      }
+      before += all;
+    }
+    return false;
+  }
+};
+
+// Takes a CTA that has not started yet off the launch: its number, or none.  The answer (16 bytes) comes
+// to shared memory with the barrier's completion.
+__device__ __forceinline__ void pt_take(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool pt_taken(uint32_t answer, uint32_t& block) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b64 lo, hi;\n\t"
+      "ld.shared.v2.b64 {lo, hi}, [%2];\n\t"
+      "mov.b128 h, {lo, hi};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  block = x;
+  return ok != 0;
 }
 
 __device__ __forceinline__ void pt_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int d, int h, int t) {
@@ -167,8 +249,9 @@ template <int DB>   // 64-column boxes of a head
 struct PtSmem {
   static constexpr uint32_t tile = DB * kPtBoxBytes;
   static constexpr uint32_t q = 0, k = 2 * tile, v = k + kPtK * tile, bars = v + kPtV * tile;
-  // barriers: Q; K full, empty; V full, empty; per tile scores, P (with its operands), O; all MMAs done
-  static constexpr uint32_t qf = bars, kf = qf + 8, ke = kf + 8 * kPtK, vf = ke + 8 * kPtK,
+  // barriers: units full, empty, time to take one; the launch's answer; Q full, empty; K full, empty; V full, empty; per
+  // tile scores, P (with its operands), O; all MMAs done
+  static constexpr uint32_t uf = bars, ue = uf + 16, go = ue + 16, tk = go + 8, qf = tk + 8, qe = qf + 8, kf = qe + 8, ke = kf + 8 * kPtK, vf = ke + 8 * kPtK,
                             ve = vf + 8 * kPtV, sf = ve + 8 * kPtV, pf = sf + 16, of = pf + 16, done = of + 16, end = done + 8;
   static constexpr uint32_t alloc = end + 1024;   // (the base is aligned to 1024)
 };
@@ -177,22 +260,27 @@ struct PtSmem {
 __device__ __forceinline__ uint32_t pt_s_col(int x) { return 128u * (uint32_t)x; }
 __device__ __forceinline__ uint32_t pt_o_col(int x) { return 256u + 128u * (uint32_t)x; }
 
+constexpr int kPtReaders = 11;   // warps that read a unit: MMAs, copies, operands, eight of softmax
+
 template <int DB>
 __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_constant__ PtParams p) {
   using SM = PtSmem<DB>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ PtRun found;
-  __shared__ int64_t sums[kPtThreads / 32];
+  __shared__ __align__(16) uint8_t answer[16];
+  __shared__ PtUnit units[2];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ volatile int odd_flag;   // V held a value that is not finite
+  __shared__ volatile int odd_flag;   // V has held a value that is not finite
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   pdl_launch_dependents();
   if (tid == 0) {
     abort_flag = 0;
     odd_flag = 0;
+    mbar_init(base + SM::go, 1);
+    mbar_init(base + SM::tk, 1);
     mbar_init(base + SM::qf, 1);
+    mbar_init(base + SM::qe, 1);
     for (int i = 0; i < kPtK; ++i) {
       mbar_init(base + SM::kf + 8 * i, 1);
       mbar_init(base + SM::ke + 8 * i, 1);
@@ -202,8 +290,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
       mbar_init(base + SM::ve + 8 * i, 1);
     }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(base + SM::uf + 8 * x, 1);
+      mbar_init(base + SM::ue + 8 * x, kPtReaders);
       mbar_init(base + SM::sf + 8 * x, 1);
-      mbar_init(base + SM::pf + 8 * x, 6);   // four softmax warps, warps 2 and 3
+      mbar_init(base + SM::pf + 8 * x, 5);   // four softmax warps, warp 2
       mbar_init(base + SM::of + 8 * x, 1);
     }
     mbar_init(base + SM::done, 1);
@@ -212,137 +302,141 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
     prefetch_tmap(&p.mk);
     prefetch_tmap(&p.mv);
   }
-  pdl_wait_previous();
-  const int unit = blockIdx.x % p.pairs;
-  const int64_t run = blockIdx.x / p.pairs;
-  const int run_rows = p.heads2 ? kPtTile : 2 * kPtTile;
-  if (!pt_find(p, run_rows, run, &found, sums)) return;   // (the whole CTA, nothing in flight)
   if (warp == 0) tmem_alloc(smem_u32(&tmem_base), 512);
+  pdl_wait_previous();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  const int64_t row0 = found.a;
-  const int len = (int)(found.b - found.a);
-  // tile x: its first row and head; the blocks of keys that it sees
-  const int q0[2] = {found.run * run_rows, found.run * run_rows + (p.heads2 ? 0 : kPtTile)};
-  const int head[2] = {p.heads2 ? 2 * unit : unit, p.heads2 ? 2 * unit + 1 : unit};
-  const int n0 = (min(len, q0[0] + kPtTile) + kPtTile - 1) / kPtTile;
-  const int n1 = q0[1] < len ? (min(len, q0[1] + kPtTile) + kPtTile - 1) / kPtTile : 0;
-  const int n = max(n0, n1), hk = head[0] / p.G;
-  const int edge = q0[0] / kPtTile;    // blocks from here on hold keys that some row does not see
   bool ok = true;
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (ok) ok = warp_wait_vote(bar, parity, &abort_flag, &g_prompt_status);
+    return ok;
+  };
+  // The CTA's units come through two slots; number `u` of them.
+  auto next_unit = [&](int u, PtUnit& w) {
+    if (!wait(base + SM::uf + 8 * (u & 1), (uint32_t)(u >> 1) & 1u)) return false;
+    w = units[u & 1];
+    warp_release(base + SM::ue + 8 * (u & 1), lane);
+    return w.there != 0;
+  };
+  PtUnit w;
 
   if (warp >= 4) {
     // ------------------------------------------------ softmax
     setmaxnreg_inc<kPtSoftRegs>();
-    const int x = (warp >> 2) - 1, nx = x ? n1 : n0;
-    const int row = (x ? q0[1] : q0[0]) + (warp & 3) * 32 + lane;
+    const int x = (warp >> 2) - 1;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + pt_s_col(x), to = tmem + lanes + pt_o_col(x);
-    float m = -INFINITY;
-    float2 l = make_float2(0.f, 0.f);
     const float2 c2 = make_float2(p.c, p.c);
-    for (int i = 0; i < nx && ok; ++i) {
-      const int kb = nx - 1 - i;
-      ok = warp_wait_vote(base + SM::sf + 8 * x, (uint32_t)(i & 1), &abort_flag, &g_prompt_status);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t r[4][32];
+    uint32_t sph = 0, oph = 0;
+    for (int u = 0; next_unit(u, w); ++u) {
+      const int nx = x ? w.n1 : w.n0, qx = x ? w.q1 : w.q0;
+      if (nx == 0) continue;
+      const int row = qx + (warp & 3) * 32 + lane;
+      float m = -INFINITY;
+      float2 l = make_float2(0.f, 0.f);
+      for (int i = 0; i < nx; ++i) {
+        const int kb = nx - 1 - i;
+        if (!wait(base + SM::sf + 8 * x, sph)) break;
+        sph ^= 1u;
+        tc_fence_after();
+        uint32_t r[4][32];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, r[j]);
-      tmem_ld_wait();
-      if (kb * kPtTile + kPtTile - 1 > (x ? q0[1] : q0[0])) {
-        const int see = row - kb * kPtTile;   // keys 0 .. see of the block
+        for (int j = 0; j < 4; ++j) tmem_ld32(ts + 32 * j, r[j]);
+        tmem_ld_wait();
+        if (kb * kPtTile + kPtTile - 1 > qx) {
+          const int see = row - kb * kPtTile;   // keys 0 .. see of the block
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * j + e > see) r[j][e] = 0xFF800000u;
+        }
+        float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * j + e > see) r[j][e] = 0xFF800000u;
-      }
-      float top = -INFINITY, top2 = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          top = fmaxf(top, fmaxf(__uint_as_float(r[j][e]), __uint_as_float(r[j][e + 1])));
-          top2 = fmaxf(top2, fmaxf(__uint_as_float(r[j][e + 2]), __uint_as_float(r[j][e + 3])));
-        }
-      top = fmaxf(top, top2) * p.c;
-      const bool up = top > m + kPtSlack || (m == -INFINITY && top > m);
-      if (__any_sync(0xffffffffu, up)) {
-        const float f = up ? pt_ex2(m - top) : 1.f;
-        if (up) m = top;
-        l = pt_fmul2(l, make_float2(f, f));
-        if (i > 0) {   // (the first P V overwrites O)
+          for (int e = 0; e < 32; e += 4) {
+            top = fmaxf(top, fmaxf(__uint_as_float(r[j][e]), __uint_as_float(r[j][e + 1])));
+            top2 = fmaxf(top2, fmaxf(__uint_as_float(r[j][e + 2]), __uint_as_float(r[j][e + 3])));
+          }
+        top = fmaxf(top, top2) * p.c;
+        const bool up = top > m + kPtSlack || (m == -INFINITY && top > m);
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? pt_ex2(m - top) : 1.f;
+          if (up) m = top;
+          l = pt_fmul2(l, make_float2(f, f));
+          if (i > 0) {   // (the first P V overwrites O)
 #pragma unroll 1
-          for (int j = 0; j < 2 * DB; ++j) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * j, o);
-            tmem_ld_wait();
+            for (int j = 0; j < 2 * DB; ++j) {
+              uint32_t o[32];
+              tmem_ld32(to + 32 * j, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(to + 32 * j, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(to + 32 * j, o);
+            }
           }
         }
-      }
-      const float mu = m == -INFINITY ? 0.f : -m;
-      const float2 m2 = make_float2(mu, mu);
+        const float mu = m == -INFINITY ? 0.f : -m;
+        const float2 m2 = make_float2(mu, mu);
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        uint32_t w[32];
+        for (int j = 0; j < 4; j += 2) {
+          uint32_t pw[32];
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const float2 t = ffma2(make_float2(__uint_as_float(r[j + (e >> 5)][e & 31]), __uint_as_float(r[j + (e >> 5)][(e & 31) + 1])), c2, m2);
-          const float2 pr = make_float2(pt_ex2(t.x), pt_ex2(t.y));
-          l = fadd2(l, pr);
-          w[e >> 1] = pt_pack(pr.x, pr.y);
+          for (int e = 0; e < 64; e += 2) {
+            const float2 t = ffma2(make_float2(__uint_as_float(r[j + (e >> 5)][e & 31]), __uint_as_float(r[j + (e >> 5)][(e & 31) + 1])), c2, m2);
+            const float2 pr = make_float2(pt_ex2(t.x), pt_ex2(t.y));
+            l = fadd2(l, pr);
+            pw[e >> 1] = pt_pack(pr.x, pr.y);
+          }
+          tmem_st32(ts + 16 * j, pw);
         }
-        tmem_st32(ts + 16 * j, w);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_release(base + SM::pf + 8 * x, lane);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      warp_release(base + SM::pf + 8 * x, lane);
-    }
-    // ------------------------------------------------ the rows of O
-    if (nx > 0 && ok) ok = warp_wait_vote(base + SM::of + 8 * x, 0, &abort_flag, &g_prompt_status);
-    if (nx > 0 && ok) {
+      // ---------------------------------------------- the rows of O
+      if (!wait(base + SM::of + 8 * x, oph)) break;
+      oph ^= 1u;
       tc_fence_after();
       const float inv = 1.f / (l.x + l.y);
       const bool odd = odd_flag != 0;
-      uint16_t* dst = p.out + (row0 + row) * p.ldo + (int64_t)(x ? head[1] : head[0]) * p.D;
+      uint16_t* dst = p.out + ((int64_t)w.row0 + row) * p.ldo + (int64_t)(w.head + (p.heads2 ? x : 0)) * p.D;
 #pragma unroll 1
       for (int j = 0; j < 2 * DB; ++j) {
         uint32_t o[32];
         tmem_ld32(to + 32 * j, o);
         tmem_ld_wait();
-        if (odd && row < len)   // the keys left out of the products, for the rows that see them
-          for (int key = edge * kPtTile; key <= row; ++key) {
-            const uint16_t* src = p.v + (row0 + key) * p.ldv + (int64_t)hk * p.D + 32 * j;
+        if (odd && row < w.len)   // the keys left out of the products, for the rows that see them
+          for (int key = w.q0 & ~(kPtTile - 1); key <= row; ++key) {
+            const uint16_t* src = p.v + ((int64_t)w.row0 + key) * p.ldv + (int64_t)(w.head / p.G) * p.D + 32 * j;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
               if (32 * j + 8 * b >= p.D) break;
-              const uint4 w = ld_global_u4(src + 8 * b);
-              if (!not_finite(w)) continue;
-              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+              const uint4 v = ld_global_u4(src + 8 * b);
+              if (!not_finite(v)) continue;
+              const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float val = e & 1 ? bf16hi(ws[e >> 1]) : bf16lo(ws[e >> 1]);
+                const float val = e & 1 ? bf16hi(vs[e >> 1]) : bf16lo(vs[e >> 1]);
                 if (!(fabsf(val) <= FLT_MAX)) o[8 * b + e] = __float_as_uint(__uint_as_float(o[8 * b + e]) + val);
               }
             }
           }
-        if (row < len)
+        if (row < w.len)
 #pragma unroll
           for (int b = 0; b < 4; ++b)
             if (32 * j + 8 * b < p.D) {
-              uint32_t w[4];
+              uint32_t ow[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w[e] = pt_pack(__uint_as_float(o[8 * b + 2 * e]) * inv, __uint_as_float(o[8 * b + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * j + 8 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+                ow[e] = pt_pack(__uint_as_float(o[8 * b + 2 * e]) * inv, __uint_as_float(o[8 * b + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + 32 * j + 8 * b) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
             }
       }
+      tc_fence_before();   // (ahead of the arrival that lets the next unit's P V overwrite O)
     }
     tc_fence_before();
   } else {
@@ -382,116 +476,243 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
       auto commit = [&](uint32_t bar) {
         if (one) mma_commit(bar);
       };
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = warp_wait_vote(bar, parity, &abort_flag, &g_prompt_status);
-        return ok;
-      };
-      // block i of the loop is keys (n - 1 - i) * 128 on; tile x takes part from its own last block on
-      const int from0 = n - n0, from1 = n1 > 0 ? n - n1 : n;
       const uint32_t pf = base + SM::pf, sf = base + SM::sf;
-      uint32_t vs = 0, ks = 0, ph0 = 0, ph1 = 0;   // stages of V of block i and of K of block i + 1; phases
-      if (wait(base + SM::qf, 0) && wait(base + SM::kf, 0)) {
-        for (int x = 0; x < 2; ++x)
-          if ((x ? from1 : from0) == 0) {
-            scores(Lo{}, Hi{}, x, 0);
-            commit(sf + 8 * x);
-          }
-        commit(base + SM::ke);
+      uint32_t vs = 0, ks = 0, kph = 0, ph0 = 0, ph1 = 0;   // stages of V's and K's next blocks; phases
+      auto next_k = [&]() {
+        if (++ks == kPtK) {
+          ks = 0;
+          kph ^= 1u;
+        }
+      };
+      // Q K^T of the first block of unit w (from there on the units' products follow one another without a
+      // break: the scores' columns are free as soon as the last unit's P V have been issued)
+      auto first = [&](int x) {
+        if ((x ? w.n1 : w.n0) == max(w.n0, w.n1)) {
+          scores(Lo{}, Hi{}, x, ks);
+          commit(sf + 8 * x);
+        }
+      };
+      auto first_done = [&]() {
+        commit(base + SM::ke + 8 * ks);
+        if (max(w.n0, w.n1) == 1) commit(base + SM::qe);
+        next_k();
+      };
+      bool have = next_unit(0, w) && wait(base + SM::qf, 0) && wait(base + SM::kf + 8 * ks, kph);
+      if (have) {
+        first(0);
+        first(1);
+        first_done();
       }
-      // The barrier of a tile's P stands for V of the block and K of the next one too (warps 2 and 3 wait
-      // for those).  It is looked up once in the middle of the other tile's Q K^T: a wait's own
-      // latency (some 300 cycles beside two softmax warps) then lies behind work in the queue.
+      // The barrier of a tile's P stands for V of the block and K of the next one too (warp 2 waits for
+      // those).  It is looked up once in the middle of the other tile's Q K^T: a wait's own latency (some
+      // 300 cycles beside two softmax warps) then lies behind work in the queue.
       bool there = false;
-      for (int i = 0; i < n && ok; ++i) {
-        const bool more = i + 1 < n;
-        if (more && ++ks == kPtK) ks = 0;
-        if (i >= from0) {
-          if (!there && !wait(pf, ph0)) break;
-          ph0 ^= 1u;
-          tc_fence_after();
-          values(0, vs, i > from0);
-          if (!more) commit(base + SM::of);
+      for (int u = 0; have && ok; ++u) {
+        const int n = max(w.n0, w.n1);
+        // block i of the loop is keys (n - 1 - i) * 128 on; tile x takes part from its own last block on
+        const int from0 = n - w.n0, from1 = w.n1 > 0 ? n - w.n1 : n;
+        for (int i = 0; i < n; ++i) {
+          const bool more = i + 1 < n;
+          if (i == max(0, n - 4)) commit(base + SM::go);
+          if (i >= from0) {
+            if (!there && !wait(pf, ph0)) break;
+            ph0 ^= 1u;
+            tc_fence_after();
+            values(0, vs, i > from0);
+            if (!more) commit(base + SM::of);
+          }
+          const bool s0 = more && i + 1 >= from0, s1 = more && i + 1 >= from1;
+          // the next unit's operands, if they are there already, else behind this unit's last product
+          bool early = false, read = false;
+          if (!more && warp_test(base + SM::uf + 8 * ((u + 1) & 1), (uint32_t)((u + 1) >> 1) & 1u)) {
+            have = next_unit(u + 1, w);
+            read = true;
+            early = true;
+            if (have && warp_test(base + SM::qf, (uint32_t)(u + 1) & 1u) && warp_test(base + SM::kf + 8 * ks, kph)) first(0);
+            else if (have) early = false;
+          }
+          if (s0) scores(Lo{}, Mid{}, 0, ks);
+          there = i >= from1 && warp_test(pf + 8, ph1);
+          if (s0) {
+            scores(Mid{}, Hi{}, 0, ks);
+            commit(sf);
+          }
+          if (i >= from1) {
+            if (!there && !wait(pf + 8, ph1)) break;
+            ph1 ^= 1u;
+            tc_fence_after();
+            values(1, vs, i > from1);
+            if (!more) commit(base + SM::of + 8);
+          }
+          commit(base + SM::ve + 8 * vs);
+          if (++vs == kPtV) vs = 0;
+          there = false;
+          if (more) {
+            if (s1) scores(Lo{}, Mid{}, 1, ks);
+            there = s0 && warp_test(pf, ph0);
+            if (s1) {
+              scores(Mid{}, Hi{}, 1, ks);
+              commit(sf + 8);
+            }
+            commit(base + SM::ke + 8 * ks);
+            if (i + 2 == n) commit(base + SM::qe);
+            next_k();
+          } else {
+            if (!early) {
+              if (!read) have = next_unit(u + 1, w);
+              if (have && wait(base + SM::qf, (uint32_t)(u + 1) & 1u) && wait(base + SM::kf + 8 * ks, kph)) first(0);
+            }
+            if (have && ok) {
+              first(1);
+              first_done();
+            }
+          }
         }
-        const bool s0 = more && i + 1 >= from0, s1 = more && i + 1 >= from1;
-        if (s0) scores(Lo{}, Mid{}, 0, ks);
-        there = i >= from1 && warp_test(pf + 8, ph1);
-        if (s0) {
-          scores(Mid{}, Hi{}, 0, ks);
-          commit(sf);
-        }
-        if (i >= from1) {
-          if (!there && !wait(pf + 8, ph1)) break;
-          ph1 ^= 1u;
-          tc_fence_after();
-          values(1, vs, i > from1);
-          if (!more) commit(base + SM::of + 8);
-        }
-        commit(base + SM::ve + 8 * vs);
-        if (++vs == kPtV) vs = 0;
-        if (s1) scores(Lo{}, Mid{}, 1, ks);
-        there = s0 && warp_test(pf, ph0);
-        if (s1) {
-          scores(Mid{}, Hi{}, 1, ks);
-          commit(sf + 8);
-        }
-        if (more) commit(base + SM::ke + 8 * ks);
       }
       // nothing is in flight behind this
       commit(base + SM::done);
       if (one) mbar_drain(base + SM::done, 0);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------------------------------------- copies
-      mbar_expect_tx(base + SM::qf, (n1 > 0 ? 2 : 1) * SM::tile);
-      for (int x = 0; x < (n1 > 0 ? 2 : 1); ++x)
-        for (int b = 0; b < DB; ++b)
-          pt_load(base + SM::q + (uint32_t)x * SM::tile + b * kPtBoxBytes, &p.mq, base + SM::qf, 64 * b, head[x], (int)(row0 + q0[x]));
-      // the loads of block i, K's and V's: a stage is free once its last use has completed
-      int ki = 0, vi = 0;
-      auto load = [&](const CUtensorMap* map, uint32_t tiles, uint32_t full, uint32_t empty, int stages, int& i) {
-        const int st = i % stages;
-        if (i >= stages && !mbar_wait(empty + 8 * st, ((uint32_t)(i / stages) & 1u) ^ 1u, &abort_flag, &g_prompt_status)) return false;
-        mbar_expect_tx(full + 8 * st, SM::tile);
-        for (int b = 0; b < DB; ++b)
-          pt_load(tiles + (uint32_t)st * SM::tile + b * kPtBoxBytes, map, full + 8 * st, 64 * b, hk, (int)row0 + (n - 1 - i) * kPtTile);
-        ++i;
+      const bool one = elect_one();
+      int kc = 0, vc = 0, qc = 0;   // blocks of K and V, and Qs, so far
+      auto load = [&](const CUtensorMap* map, uint32_t tiles, uint32_t full, uint32_t empty, int stages, int& count, int t) {
+        const int st = count % stages;
+        if (count >= stages && !wait(empty + 8 * st, ((uint32_t)(count / stages) & 1u) ^ 1u)) return false;
+        if (one) {
+          mbar_expect_tx(full + 8 * st, SM::tile);
+          for (int b = 0; b < DB; ++b)
+            pt_load(tiles + (uint32_t)st * SM::tile + b * kPtBoxBytes, map, full + 8 * st, 64 * b, w.head / p.G, t);
+        }
+        ++count;
         return true;
       };
-      while (vi < n) {   // (K of block i + 1 is wanted before V of block i)
-        if (ki < n && !load(&p.mk, base + SM::k, base + SM::kf, base + SM::ke, kPtK, ki)) break;
-        if (ki == 1 && ki < n && !load(&p.mk, base + SM::k, base + SM::kf, base + SM::ke, kPtK, ki)) break;
-        if (!load(&p.mv, base + SM::v, base + SM::vf, base + SM::ve, kPtV, vi)) break;
+      // a stage is free once its last use has completed; K of block i + 1 is wanted before V of block i
+      for (int u = 0; next_unit(u, w); ++u) {
+        const int n = max(w.n0, w.n1), tiles = w.n1 > 0 ? 2 : 1;
+        auto key = [&](int i) { return w.row0 + (n - 1 - i) * kPtTile; };
+        if (!load(&p.mk, base + SM::k, base + SM::kf, base + SM::ke, kPtK, kc, key(0))) break;
+        if (u > 0 && !wait(base + SM::qe, (uint32_t)(u - 1) & 1u)) break;
+        if (one) {
+          mbar_expect_tx(base + SM::qf, tiles * SM::tile);
+          for (int x = 0; x < tiles; ++x)
+            for (int b = 0; b < DB; ++b)
+              pt_load(base + SM::q + (uint32_t)x * SM::tile + b * kPtBoxBytes, &p.mq, base + SM::qf, 64 * b,
+                      w.head + (p.heads2 ? x : 0), w.row0 + (x ? w.q1 : w.q0));
+        }
+        qc = u + 1;
+        for (int i = 0; i < n && ok; ++i) {
+          if (i + 1 < n && !load(&p.mk, base + SM::k, base + SM::kf, base + SM::ke, kPtK, kc, key(i + 1))) break;
+          if (!load(&p.mv, base + SM::v, base + SM::vf, base + SM::ve, kPtV, vc, key(i))) break;
+        }
       }
       // the CTA does not end before its copies have landed
-      mbar_drain(base + SM::qf, 0);
-      for (int i = max(0, ki - kPtK); i < ki; ++i) mbar_drain(base + SM::kf + 8 * (i % kPtK), (uint32_t)(i / kPtK) & 1u);
-      for (int i = max(0, vi - kPtV); i < vi; ++i) mbar_drain(base + SM::vf + 8 * (i % kPtV), (uint32_t)(i / kPtV) & 1u);
-    } else if (warp >= 2) {
+      if (one) {
+        if (qc > 0) mbar_drain(base + SM::qf, (uint32_t)(qc - 1) & 1u);
+        for (int i = max(0, kc - kPtK); i < kc; ++i) mbar_drain(base + SM::kf + 8 * (i % kPtK), (uint32_t)(i / kPtK) & 1u);
+        for (int i = max(0, vc - kPtV); i < vc; ++i) mbar_drain(base + SM::vf + 8 * (i % kPtV), (uint32_t)(i / kPtV) & 1u);
+      }
+    } else if (warp == 2) {
       // ---------------------------------------------- V at the edge, and word that a block's operands are there
-      const int from[2] = {n - n0, n1 > 0 ? n - n1 : n};
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = warp_wait_vote(bar, parity, &abort_flag, &g_prompt_status);
-        return ok;
-      };
-      for (int i = 0; i < n && ok; ++i) {
-        if (!wait(base + SM::vf + 8 * (i % kPtV), (uint32_t)(i / kPtV) & 1u)) break;
-        if (n - 1 - i >= edge) {
-          const uint32_t at = base + SM::v + (uint32_t)(i % kPtV) * SM::tile;
-          for (uint32_t o = (uint32_t)(tid - 64) * 16; o < SM::tile; o += 64 * 16) {
-            const uint4 w = ld_shared_v4(at + o);
-            if (not_finite(w)) {
-              st_shared_v4(at + o, finite_only(w));
+      int kc = 0, vc = 0, arrived[2] = {0, 0};
+      for (int u = 0; next_unit(u, w); ++u) {
+        const int n = max(w.n0, w.n1), edge = w.q0 / kPtTile;   // blocks from here on hold keys that some row does not see
+        const int from[2] = {n - w.n0, w.n1 > 0 ? n - w.n1 : n};
+        ++kc;   // (K of the first block: the MMAs' own wait)
+        for (int i = 0; i < n; ++i, ++vc) {
+          if (!wait(base + SM::vf + 8 * (vc % kPtV), (uint32_t)(vc / kPtV) & 1u)) break;
+          if (n - 1 - i >= edge) {
+            const uint32_t at = base + SM::v + (uint32_t)(vc % kPtV) * SM::tile;
+            uint32_t top = 0;   // the largest magnitude's bits; 0x7F80 and above: not finite
+#pragma unroll 8
+            for (uint32_t o = (uint32_t)lane * 16; o < SM::tile; o += 32 * 16) {
+              const uint4 v = ld_shared_v4(at + o);
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            }
+            if (max(top & 0xFFFFu, top >> 16) >= 0x7F80u) {
+              for (uint32_t o = (uint32_t)lane * 16; o < SM::tile; o += 32 * 16) {
+                const uint4 v = ld_shared_v4(at + o);
+                if (not_finite(v)) st_shared_v4(at + o, finite_only(v));
+              }
               odd_flag = 1;
             }
+            fence_proxy_async();
           }
-          fence_proxy_async();
+          if (i + 1 < n) {
+            if (!wait(base + SM::kf + 8 * (kc % kPtK), (uint32_t)(kc / kPtK) & 1u)) break;
+            ++kc;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (i >= from[x]) {
+              // (an arrival before the last phase is complete would count for that one)
+              if (arrived[x] > 0 && !wait(base + SM::pf + 8 * x, (uint32_t)(arrived[x] - 1) & 1u)) break;
+              warp_release(base + SM::pf + 8 * x, lane);
+              ++arrived[x];
+            }
         }
-        if (i + 1 < n && !wait(base + SM::kf + 8 * ((i + 1) % kPtK), (uint32_t)((i + 1) / kPtK) & 1u)) break;
-        for (int x = 0; x < 2; ++x)
-          if (i >= from[x]) {
-            // (an arrival before the last phase is complete would count for that one)
-            if (i > from[x] && !wait(base + SM::pf + 8 * x, (uint32_t)(i - from[x] - 1) & 1u)) break;
-            warp_release(base + SM::pf + 8 * x, lane);
+      }
+    } else {
+      // ---------------------------------------------- units
+      // A unit is a run of rows and a head (pair); the CTA begins with its own number and takes those
+      // of CTAs that have not started, so that long and short runs even out.
+      const int rows = p.heads2 ? kPtTile : 2 * kPtTile;
+      PtOrder order;
+      order.start(p, rows, lane);
+      uint32_t block = blockIdx.x;
+      bool found = true;
+      int taken = 0;
+      for (int u = 0;; ++u) {
+        int seq = 0, run = 0;
+        if (found) {
+          found = order.find(p, rows, block / (uint32_t)p.pairs, lane, seq, run);
+          if (u >= 2 && !wait(base + SM::ue + 8 * (u & 1), ((uint32_t)(u >> 1) & 1u) ^ 1u)) break;
+          if (lane == 0) {
+            PtUnit v{};
+            if (found) {
+              int64_t a, b;
+              pt_rows(p, seq, a, b);
+              v.row0 = (int)a;
+              v.len = (int)(b - a);
+              v.q0 = run * rows;
+              v.q1 = v.q0 + (p.heads2 ? 0 : kPtTile);
+              v.head = (int)(block % (uint32_t)p.pairs) * (p.heads2 ? 2 : 1);
+              v.n0 = (min(v.len, v.q0 + kPtTile) + kPtTile - 1) / kPtTile;
+              v.n1 = v.q1 < v.len ? (min(v.len, v.q1 + kPtTile) + kPtTile - 1) / kPtTile : 0;
+              v.there = 1;
+            }
+            units[u & 1] = v;
           }
+          warp_release(base + SM::uf + 8 * (u & 1), lane);
+        }
+        // (the next unit is taken when this one is nearly done: what has been taken early cannot be
+        // evened out any more)
+        if (found && !wait(base + SM::go, (uint32_t)u & 1u)) break;
+        // (behind the last unit there may be CTAs of the launch that have nothing to do: they are taken
+        // off too, which costs less than their start)
+        if (lane == 0) {
+          fence_proxy_async();   // (the last answer has been read)
+          mbar_expect_tx(base + SM::tk, 16);
+          pt_take(smem_u32(answer), base + SM::tk);
+        }
+        __syncwarp();
+        if (!wait(base + SM::tk, (uint32_t)taken & 1u)) {
+          if (lane == 0) mbar_drain(base + SM::tk, (uint32_t)taken & 1u);
+          break;
+        }
+        ++taken;
+        const bool more = pt_taken(smem_u32(answer), block);
+        __syncwarp();
+        if (!more) {   // the end, unless the units have ended before
+          if (found) {
+            ++u;
+            if (u >= 2 && !wait(base + SM::ue + 8 * (u & 1), ((uint32_t)(u >> 1) & 1u) ^ 1u)) break;
+            if (lane == 0) units[u & 1] = PtUnit{};
+            warp_release(base + SM::uf + 8 * (u & 1), lane);
+          }
+          break;
+        }
       }
     }
     __syncwarp();
