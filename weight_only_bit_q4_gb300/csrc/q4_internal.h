@@ -208,7 +208,7 @@ struct KvAttnArgs {
   cudaStream_t stream;
 };
 int64_t kv_passes(int64_t cols);   // passes over a head's cols = n Hq / Hk query columns
-int64_t kv_workspace_bytes(int64_t D, int64_t cols);
+int64_t kv_workspace_bytes(int64_t D);
 int kv_attention_launch(const KvAttnArgs& a);
 int kv_status(int* value, bool clear);
 

@@ -11,7 +11,7 @@
 //   V  [D / 2 rows][64 bytes], row i values 2i (low nibble) and 2i + 1 of every token, token o at
 //      byte 16 c + 4 j + 2 e + h (j = o / 16, h = o % 16 / 8, c = o % 8 / 2, e = o % 2): word j of
 //      thread c holds its four tokens of k-step j, two values each.
-#include <cfloat>
+#include <type_traits>
 
 #include "q4_internal.h"
 #include "q4_sm100.cuh"
@@ -180,11 +180,12 @@ int pdl_launch(Kernel kernel, const char* what, unsigned blocks, unsigned thread
 //
 // Bound: the bytes of the codes and scales, read once per 16 columns.
 //
-// Split: the pages of all sequences and heads in a row, cut into equal shares, one per CTA (one
-// CTA per SM), whatever the lengths are; a CTA deals its pages to its warps, each with a ring of
-// record copies of its own and a running (m, sum, O).  At the end of a (sequence, head) the warps
-// join through shared memory; a (sequence, head) that lies in one CTA is finished there, others leave
-// FP32 partial sums (at most two per CTA) that a second kernel joins in order.
+// Split: the pages of all sequences and heads in a row are cut into equal shares, whatever the
+// lengths are.  A share belongs to a group of warps of a CTA (one CTA per SM; a group per 8 columns:
+// its warps take the same pages, 8 columns each) with a ring of record copies and a running
+// (m, sum, O) of its own: no barrier joins the groups.  A (sequence, head) inside one share is
+// finished there, others leave FP32 partial sums (at most two per share) that a second kernel
+// joins in order.
 struct KvParams {
   const uint16_t* q;
   uint16_t* out;
@@ -192,17 +193,17 @@ struct KvParams {
   const uint8_t* cache;
   const int32_t* table;
   const int32_t* len;
-  float* part;              // [CTAs][2][part_floats]
+  float* part;              // [shares][2][kTiles][part_floats]
   int64_t P;
-  int S, M, n, G, Hk, cols, passes;   // columns of a head (n * G) and passes of 8 NT over them
+  int S, M, n, G, Hk, cols, passes;   // columns of a head (n * G) and passes of 8 kTiles over them
   float c;                  // scale * log2 e
 };
 
-constexpr int kKvWarps = 8;
-constexpr int kKvStages = 3;
+constexpr int kKvWarps = 12;
 constexpr int kKvThreads = 32 * kKvWarps;
+constexpr int kKvRecords = 24;    // records in shared memory: 2 per warp, so 2, 4 or 8 per ring
 
-__host__ __device__ constexpr int part_floats(int D, int NT) { return 8 * NT * (D + 2); }
+__host__ __device__ constexpr int part_floats(int D) { return 8 * (D + 2); }
 
 __device__ __forceinline__ int kv_pages(const KvParams& p, int s, int& L) {
   L = (int)ld_global_u32(p.len + s);
@@ -212,69 +213,73 @@ __device__ __forceinline__ int kv_pages(const KvParams& p, int s, int& L) {
   return (L + kPage - 1) / kPage;
 }
 
-// Sequences in order, each `per` segments of its pages: all threads get the number of all units and
-// the exclusive sum before sequence s (s < 0: 0).  Threads sum runs of sequences.
-struct KvScan {
-  int64_t total, before;
-};
+// A unit is a page of a segment: a sequence's pages for a head and a pass, sequence by sequence.  (The
+// units' number is below 2^31: the entry point refuses more.)  All threads get the total; ends[t]
+// holds the units up to the end of thread t's run of sequences.
 template <int kThreads>
-__device__ __forceinline__ KvScan kv_scan(const KvParams& p, int s, int64_t* sums) {
-  const int tid = threadIdx.x;
-  int64_t all = 0, ahead = 0;
-  for (int i = tid; i < p.S; i += kThreads) {
-    int L;
-    const int64_t u = kv_pages(p, i, L);
-    all += u;
-    if (i < s) ahead += u;
-  }
+__device__ __forceinline__ int kv_scan(const KvParams& p, int* ends, int* sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (p.S + kThreads - 1) / kThreads, a = min(p.S, tid * run), b = min(p.S, a + run);
+  int upto = 0, L;
+  for (int s = a; s < b; ++s) upto += kv_pages(p, s, L);
+  upto *= p.Hk * p.passes;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
   }
-  if ((tid & 31) == 0) {
-    sums[2 * (tid >> 5)] = all;
-    sums[2 * (tid >> 5) + 1] = ahead;
-  }
+  if (lane == 31) sums[warp] = upto;
   __syncthreads();
-  KvScan r{0, 0};
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    r.total += sums[2 * w];
-    r.before += sums[2 * w + 1];
+    const int v = sums[w];
+    if (w < warp) upto += v;
+    total += v;
   }
-  const int64_t per = (int64_t)p.Hk * p.passes;
-  r.total *= per;
-  r.before *= per;
+  ends[tid] = upto;
   __syncthreads();
-  return r;
+  return total;
 }
 
 // Shares that the units are cut into: none of them is empty.
-__device__ __forceinline__ int kv_shares_used(int64_t total, int most) { return total < most ? (int)total : most; }
+__device__ __forceinline__ int kv_shares_used(int total, int most) { return total < most ? total : most; }
+__device__ __forceinline__ int kv_share_start(int total, int share, int shares) { return (int)((int64_t)total * share / shares); }
 
 // A walk over units: unit `u` is page `u - seg0` of segment `seg` (head and pass) of sequence s.
 struct KvCursor {
   int s, L, pages, seg;
-  int64_t seg0;   // first unit of the segment
-  __device__ __forceinline__ void start(const KvParams& p, int s_, int64_t first) {
-    s = s_;
-    pages = kv_pages(p, s, L);
+  int seg0;   // first unit of the segment
+  // one warp: to the sequence that holds unit u (below the total)
+  template <int kThreads>
+  __device__ __forceinline__ void start(const KvParams& p, int u, const int* ends, int lane) {
+    int t = 0;   // the first run that ends behind u
+    for (int t0 = 0; t0 < kThreads; t0 += 32) {
+      const unsigned past = __ballot_sync(0xffffffffu, ends[t0 + lane] > u);
+      if (past) {
+        t = t0 + __ffs(past) - 1;
+        break;
+      }
+    }
+    s = t * ((p.S + kThreads - 1) / kThreads);
     seg = 0;
-    seg0 = first;
+    seg0 = t > 0 ? ends[t - 1] : 0;
+    pages = kv_pages(p, s, L);
+    seek(p, u);
   }
-  // to the segment that holds unit u (u below the total)
-  __device__ __forceinline__ void seek(const KvParams& p, int64_t u) {
+  __device__ __forceinline__ void seek(const KvParams& p, int u) {
     const int per = p.Hk * p.passes;
-    while (u >= seg0 + (int64_t)(per - seg) * pages && s + 1 < p.S) {
-      seg0 += (int64_t)(per - seg) * pages;
+    while (u >= seg0 + (per - seg) * pages && s + 1 < p.S) {
+      seg0 += (per - seg) * pages;
       seg = 0;
       ++s;
       pages = kv_pages(p, s, L);
     }
-    const int k = pages > 0 ? min((int)((u - seg0) / pages), per - 1 - seg) : 0;
-    seg += k;
-    seg0 += (int64_t)k * pages;
+    if (u >= seg0 + pages && pages > 0) {
+      const int k = min((u - seg0) / pages, per - 1 - seg);
+      seg += k;
+      seg0 += k * pages;
+    }
   }
 };
 
@@ -310,136 +315,143 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // A warp's running state over the pages of a segment.
-template <int J, int NT>
+template <int J>
 struct KvState {
   static constexpr int D = 32 * J, G = kv_groups(D);
-  float o[2 * J][NT][4];    // 2^-24 sum q P s; rows of odd values 16 times that
-  float z[G][NT][4];        // the same with q = 8 everywhere
-  float mm[NT][2], l[NT][2];   // the columns' references, and this thread's tokens' sum of 2^(x - mm)
+  float o[2 * J][4];        // 2^-24 sum q P s; rows of odd values 16 times that
+  float z[G][4];            // the same with q = 8 everywhere
+  float mm[2], l[2];        // the columns' references, and this thread's tokens' sum of 2^(x - mm)
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int i = 0; i < 2 * J; ++i)
 #pragma unroll
-      for (int i = 0; i < 2 * J; ++i)
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][t][e] = 0.f;
+    for (int i = 0; i < G; ++i)
 #pragma unroll
-      for (int i = 0; i < G; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[i][t][e] = 0.f;
-      mm[t][0] = mm[t][1] = -INFINITY;
-      l[t][0] = l[t][1] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) z[i][e] = 0.f;
+    mm[0] = mm[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
   }
-  __device__ __forceinline__ void scale(int t, float f0, float f1) {
+  __device__ __forceinline__ void scale(float f0, float f1) {
 #pragma unroll
     for (int i = 0; i < 2 * J; ++i) {
-      o[i][t][0] *= f0; o[i][t][1] *= f1; o[i][t][2] *= f0; o[i][t][3] *= f1;
+      o[i][0] *= f0; o[i][1] *= f1; o[i][2] *= f0; o[i][3] *= f1;
     }
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      z[i][t][0] *= f0; z[i][t][1] *= f1; z[i][t][2] *= f0; z[i][t][3] *= f1;
+      z[i][0] *= f0; z[i][1] *= f1; z[i][2] *= f0; z[i][3] *= f1;
     }
-    l[t][0] *= f0;
-    l[t][1] *= f1;
+    l[0] *= f0;
+    l[1] *= f1;
   }
 };
 
-// The queries of a pass as B fragments, and the scores' factors.
-template <int J, int NT>
+// A tile of 8 query columns as B fragments, and the scores' factors.
+template <int J>
 struct KvQuery {
   static constexpr int G = kv_groups(32 * J);
-  uint32_t b[NT][J][4];     // b0, b1 of the word's two k-steps
-  float f[NT][2], z[NT][G][2];
-  int seen[NT][2];          // tokens that columns 2c and 2c + 1 see (columns that are not there: none)
+  uint32_t b[J][4];         // b0, b1 of the word's two k-steps
+  float f[2], z[G][2];
+  int seen[2];              // tokens that columns 2c and 2c + 1 see (columns that are not there: none)
 
-  __device__ __forceinline__ void load(const KvParams& p, const KvCursor& at, int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    const int h = at.seg / p.passes, pass = at.seg - h * p.passes;
+  __device__ __forceinline__ void load(const KvParams& p, int s, int L, int h, int col0, int lane) {
+    const int g = lane >> 2, c = lane & 3, col = col0 + g;
+    uint4 w[J];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int col = (pass * NT + t) * 8 + g;
-      uint4 w[J];
+    for (int j = 0; j < J; ++j) w[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (col < p.cols) {
+      const int i = col / p.G;
+      const uint16_t* row = p.q + ((int64_t)s * p.n + i) * p.ldq + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
 #pragma unroll
-      for (int j = 0; j < J; ++j) w[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (col < p.cols) {
-        const int i = col / p.G;
-        const uint16_t* row = p.q + ((int64_t)at.s * p.n + i) * p.ldq + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
+      for (int j = 0; j < J; ++j) w[j] = ld_global_u4(row + 8 * (4 * j + c));
+    }
+    uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < J; ++j) w[j] = ld_global_u4(row + 8 * (4 * j + c));
+    for (int j = 0; j < J; ++j)
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu),
+                                   __vmaxu2(w[j].z & 0x7FFF7FFFu, w[j].w & 0x7FFF7FFFu)));
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^-e puts the largest value (exponent field top >> 7) in [2^14, 2^15)
+    const int e = min(max((int)(top >> 7), 1), 254) - 127 - 14;
+    const int d1 = min(-e, 127);
+    const float down = exp2i(d1), down2 = exp2i(-e - d1);
+    float zg[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) zg[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+      float x[8], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = (i & 1 ? bf16hi(ws[i >> 1]) : bf16lo(ws[i >> 1]));
+        sum += x[i];
+        x[i] = x[i] * down * down2;
       }
-      uint32_t top = 0;
+      zg[j >> 1] += sum;
+      b[j][0] = pack_f16(x[0], x[4]);
+      b[j][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
+      b[j][2] = pack_f16(x[2], x[6]);
+      b[j][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
+    }
+    // (2^(24 + e) may pass FP32's range only where the scores do)
+    const float fc = exp2i(min(24 + e, 127)) * p.c;
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu),
-                                     __vmaxu2(w[j].z & 0x7FFF7FFFu, w[j].w & 0x7FFF7FFFu)));
-      top = max(top & 0xFFFFu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^-e puts the largest value (exponent field top >> 7) in [2^14, 2^15)
-      const int e = min(max((int)(top >> 7), 1), 254) - 127 - 14;
-      const int d1 = min(-e, 127);
-      const float down = exp2i(d1), down2 = exp2i(-e - d1);
-      float zg[G];
+    for (int i = 0; i < G; ++i) {
+      zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 1);
+      zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 2);
+      zg[i] *= -8.f * p.c;
+    }
 #pragma unroll
-      for (int i = 0; i < G; ++i) zg[i] = 0.f;
+    for (int k = 0; k < 2; ++k) {
+      const int from = 4 * (2 * c + k);   // a lane of column 2c + k
+      f[k] = __shfl_sync(0xffffffffu, fc, from);
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-        float x[8], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = (i & 1 ? bf16hi(ws[i >> 1]) : bf16lo(ws[i >> 1]));
-          sum += x[i];
-          x[i] = x[i] * down * down2;
-        }
-        zg[j >> 1] += sum;
-        b[t][j][0] = pack_f16(x[0], x[4]);
-        b[t][j][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
-        b[t][j][2] = pack_f16(x[2], x[6]);
-        b[t][j][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
-      }
-      // (2^(24 + e) may pass FP32's range only where the scores do)
-      const float fc = exp2i(min(24 + e, 127)) * p.c;
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 1);
-        zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 2);
-        zg[i] *= -8.f * p.c;
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int from = 4 * (2 * c + k);   // a lane of column 2c + k
-        f[t][k] = __shfl_sync(0xffffffffu, fc, from);
-#pragma unroll
-        for (int i = 0; i < G; ++i) z[t][i][k] = __shfl_sync(0xffffffffu, zg[i], from);
-        const int mine = (pass * NT + t) * 8 + 2 * c + k;
-        seen[t][k] = mine < p.cols ? at.L - p.n + 1 + mine / p.G : 0;
-      }
+      for (int i = 0; i < G; ++i) z[i][k] = __shfl_sync(0xffffffffu, zg[i], from);
+      const int mine = col0 + 2 * c + k;
+      seen[k] = mine < p.cols ? L - p.n + 1 + mine / p.G : 0;
     }
   }
 };
 
+// The scales of a token's groups.
+template <int G>
+__device__ __forceinline__ void kv_scales(uint32_t at, float (&v)[G]) {
+  if constexpr (G == 2) {
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    v[0] = f.x;
+    v[1] = f.y;
+  } else {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
+    v[0] = fp16_bits_to_float(h);
+  }
+}
+
 // One page (64 tokens from token0 on) joins the warp's state; kEnd: not every column sees all of it.
-template <int J, int NT, bool kEnd>
-__device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>& qy, uint32_t rec, int token0, int lane) {
+template <int J, bool kEnd>
+__device__ __forceinline__ void kv_page(KvState<J>& st, const KvQuery<J>& qy, uint32_t rec, int token0, int lane) {
   constexpr int D = 32 * J, G = kv_groups(D);
   constexpr uint32_t M0 = 0x000F000Fu, M1 = 0x00F000F0u;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t kbase = rec + (uint32_t)(g * (D / 2) + c * J * 4), sbase = rec + 64u * D + (uint32_t)(g * 2 * G);
-  float x[4][NT][4];
+  float x[4][4];
   float vs[4][2][G];   // V scales of this thread's tokens
   float vtop = 0.f;
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
-    float d[G][NT][4];
+    float d[G][4];
 #pragma unroll
     for (int i = 0; i < G; ++i)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[i][t][e] = 0.f;
+      for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
     uint32_t w[2][J];
+    float ks[2][G];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const uint32_t at = kbase + (uint32_t)((16 * mt + 8 * r) * (D / 2));
@@ -453,45 +465,28 @@ __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>
 #pragma unroll
         for (int j = 0; j < J; ++j) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[r][j]) : "r"(at + 4u * j));
       }
+      kv_scales<G>(sbase + (uint32_t)((16 * mt + 8 * r) * 2 * G), ks[r]);
+      kv_scales<G>(sbase + (uint32_t)((16 * mt + 8 * r) * 2 * G) + 128u * G, vs[mt][r]);
     }
-    float ks[2][G];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        uint16_t a, b;
-        const uint32_t at = sbase + (uint32_t)((16 * mt + 8 * r) * 2 * G + 2 * i);
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(at));
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(at + 128u * G));
-        ks[r][i] = fp16_bits_to_float(a);
-        vs[mt][r][i] = fp16_bits_to_float(b);
-      }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const uint32_t h0 = w[0][j] >> 8, h1 = w[1][j] >> 8;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        mma_16816(d[j >> 1][t], w[0][j] & M0, w[1][j] & M0, w[0][j] & M1, w[1][j] & M1, qy.b[t][j][0], qy.b[t][j][1]);
-        mma_16816(d[j >> 1][t], h0 & M0, h1 & M0, h0 & M1, h1 & M1, qy.b[t][j][2], qy.b[t][j][3]);
-      }
+      mma_16816(d[j >> 1], w[0][j] & M0, w[1][j] & M0, w[0][j] & M1, w[1][j] & M1, qy.b[j][0], qy.b[j][1]);
+      mma_16816(d[j >> 1], h0 & M0, h1 & M0, h0 & M1, h1 & M1, qy.b[j][2], qy.b[j][3]);
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int e = 0; e < 4; ++e) {
+      float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < G; ++i) s = fmaf(ks[e >> 1][i], fmaf(qy.f[t][e & 1], d[i][t][e], qy.z[t][i][e & 1]), s);
-        if (kEnd && token0 + 16 * mt + g + 8 * (e >> 1) >= qy.seen[t][e & 1]) s = -INFINITY;
-        x[mt][t][e] = s;
-      }
+      for (int i = 0; i < G; ++i) s = fmaf(ks[e >> 1][i], fmaf(qy.f[e & 1], d[i][e], qy.z[i][e & 1]), s);
+      if (kEnd && token0 + 16 * mt + g + 8 * (e >> 1) >= qy.seen[e & 1]) s = -INFINITY;
+      x[mt][e] = s;
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       // tokens that no column sees: whatever their scales hold, they are left out
       if (kEnd) {
-        int any = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) any = max(any, max(qy.seen[t][0], qy.seen[t][1]));
+        int any = max(qy.seen[0], qy.seen[1]);
         any = max(any, __shfl_xor_sync(0xffffffffu, any, 1));
         any = max(any, __shfl_xor_sync(0xffffffffu, any, 2));
         if (token0 + 16 * mt + g + 8 * r >= any)
@@ -502,66 +497,60 @@ __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>
       for (int i = 0; i < G; ++i) vtop = fmaxf(vtop, fabsf(vs[mt][r][i]));
     }
   }
+  float top[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    top[k] = fmaxf(fmaxf(fmaxf(x[0][k], x[0][2 + k]), fmaxf(x[1][k], x[1][2 + k])),
+                   fmaxf(fmaxf(x[2][k], x[2][2 + k]), fmaxf(x[3][k], x[3][2 + k])));
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) {
+    vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+    top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+    top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+  }
   // the page's largest V scale is below 2^ve
-#pragma unroll
-  for (int o = 4; o <= 16; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
   const float ve = (float)(max((int)(__float_as_uint(vtop) >> 23), 127 - 25) - 126);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    float top[2];
+  top[0] += ve - 14.f;
+  top[1] += ve - 14.f;
+  if (__any_sync(0xffffffffu, top[0] > st.mm[0] + 1.f || top[1] > st.mm[1] + 1.f)) {
+    float f[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      top[k] = fmaxf(fmaxf(fmaxf(x[0][t][k], x[0][t][2 + k]), fmaxf(x[1][t][k], x[1][t][2 + k])),
-                     fmaxf(fmaxf(x[2][t][k], x[2][t][2 + k]), fmaxf(x[3][t][k], x[3][t][2 + k])));
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-      top[k] += ve - 14.f;
+      const float m = fmaxf(st.mm[k], top[k]);
+      f[k] = st.mm[k] == m ? 1.f : kv_ex2(st.mm[k] - m);
+      st.mm[k] = m;
     }
-    if (__any_sync(0xffffffffu, top[0] > st.mm[t][0] + 1.f || top[1] > st.mm[t][1] + 1.f)) {
-      float f[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float m = fmaxf(st.mm[t][k], top[k]);
-        f[k] = st.mm[t][k] == m ? 1.f : kv_ex2(st.mm[t][k] - m);
-        st.mm[t][k] = m;
-      }
-      st.scale(t, f[0], f[1]);
-    }
+    st.scale(f[0], f[1]);
   }
-  // P s as B fragments: [k-step][scale group][column tile]
-  uint32_t pb[4][G][NT][2];
+  // P s as B fragments: [k-step][scale group]
+  uint32_t pb[4][G][2];
+  // (a column that has seen nothing yet: its x are -inf, its P 0)
+  const float m0 = st.mm[0] == -INFINITY ? 0.f : st.mm[0], m1 = st.mm[1] == -INFINITY ? 0.f : st.mm[1];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    // (a column that has seen nothing yet: its x are -inf, its P 0)
-    const float m0 = st.mm[t][0] == -INFINITY ? 0.f : st.mm[t][0], m1 = st.mm[t][1] == -INFINITY ? 0.f : st.mm[t][1];
+  for (int mt = 0; mt < 4; ++mt) {
+    float pr[4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      float pr[4];
+    for (int e = 0; e < 4; ++e) pr[e] = kv_ex2(x[mt][e] - (e & 1 ? m1 : m0));
+    st.l[0] += pr[0] + pr[2];
+    st.l[1] += pr[1] + pr[3];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pr[e] = kv_ex2(x[mt][t][e] - (e & 1 ? m1 : m0));
-      st.l[t][0] += pr[0] + pr[2];
-      st.l[t][1] += pr[1] + pr[3];
+    for (int i = 0; i < G; ++i)
 #pragma unroll
-      for (int i = 0; i < G; ++i)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float a = pr[2 * r] * vs[mt][r][i], b = pr[2 * r + 1] * vs[mt][r][i];
-          if (kEnd) {   // a scale that is not finite stays with the columns that see its token
-            if (x[mt][t][2 * r] == -INFINITY) a = 0.f;
-            if (x[mt][t][2 * r + 1] == -INFINITY) b = 0.f;
-          }
-          pb[mt][i][t][r] = movmatrix(pack_f16(a, b));
+      for (int r = 0; r < 2; ++r) {
+        float a = pr[2 * r] * vs[mt][r][i], b = pr[2 * r + 1] * vs[mt][r][i];
+        if (kEnd) {   // a scale that is not finite stays with the columns that see its token
+          if (x[mt][2 * r] == -INFINITY) a = 0.f;
+          if (x[mt][2 * r + 1] == -INFINITY) b = 0.f;
         }
-    }
+        pb[mt][i][r] = movmatrix(pack_f16(a, b));
+      }
   }
   const uint32_t vbase = rec + 32u * D + (uint32_t)(g * kPage + 16 * c);
 #pragma unroll
   for (int i = 0; i < G; ++i)
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        mma_16816(st.z[i][t], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, pb[s][i][t][0], pb[s][i][t][1]);
+      mma_16816(st.z[i], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, pb[s][i][0], pb[s][i][1]);
 #pragma unroll
   for (int md = 0; md < 2 * J; ++md) {
     const uint4 v = ld_shared_v4(vbase + (uint32_t)(md * 8 * kPage));
@@ -569,310 +558,226 @@ __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const uint32_t h = ws[s] >> 8;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        mma_16816(st.o[md][t], ws[s] & M0, ws[s] & M1, h & M0, h & M1, pb[s][md >> 2][t][0], pb[s][md >> 2][t][1]);
+      mma_16816(st.o[md], ws[s] & M0, ws[s] & M1, h & M0, h & M1, pb[s][md >> 2][0], pb[s][md >> 2][1]);
     }
   }
 }
 
-
-template <int J, int NT>
-struct KvSmem {
-  static constexpr int D = 32 * J;
-  static constexpr int rec = kv_record(D);
-  static constexpr int slot = part_floats(D, NT) * 4;          // a warp's state on its way to warp 0
-  static constexpr int slots = NT == 1 ? 4 : 2;
-  static constexpr int ring = kKvWarps * kKvStages * rec;
-  static constexpr int bars = ring + slots * slot;
-  static constexpr int alloc = bars + kKvWarps * kKvStages * 8 + 16;
-};
-
-// The state's columns in FP32: o [8 NT][D] in true units times 2^-mm, then mm, then l.
-template <int J, int NT>
-__device__ __forceinline__ void kv_finish_state(KvState<J, NT>& st) {
+// The state's columns in FP32: o in true units times 2^-mm, l over all tokens.
+template <int J>
+__device__ __forceinline__ void kv_finish_state(KvState<J>& st) {
   constexpr float up = 16777216.f;   // 2^24
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
+  for (int md = 0; md < 2 * J; ++md)
 #pragma unroll
-    for (int md = 0; md < 2 * J; ++md)
+    for (int e = 0; e < 4; ++e) st.o[md][e] = (st.o[md][e] - st.z[md >> 2][e]) * (e < 2 ? up : up / 16.f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        st.o[md][t][e] = (st.o[md][t][e] - st.z[md >> 2][t][e]) * (e < 2 ? up : up / 16.f);
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) st.l[t][k] += __shfl_xor_sync(0xffffffffu, st.l[t][k], o);
-  }
+    for (int o = 4; o <= 16; o <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], o);
 }
 
-template <int J, int NT, class Store>
-__device__ __forceinline__ void kv_each(const KvState<J, NT>& st, int lane, Store store) {
+// They as [8][D] values, then the references, then the sums.
+template <int J>
+__device__ __forceinline__ void kv_put(float* dst, const KvState<J>& st, int lane) {
+  constexpr int D = 32 * J;
   const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int md = 0; md < 2 * J; ++md) store(t, k, 8 * t + 2 * c + k, 16 * md + 2 * g, md);
-}
-
-template <int J, int NT>
-__device__ __forceinline__ void kv_put(float* dst, const KvState<J, NT>& st, int lane) {
-  constexpr int D = 32 * J;
-  kv_each<J, NT>(st, lane, [&](int t, int k, int col, int d, int md) {
-    *reinterpret_cast<float2*>(dst + col * D + d) = make_float2(st.o[md][t][k], st.o[md][t][2 + k]);
-  });
-  if ((lane >> 2) == 0)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        dst[8 * NT * D + 8 * t + 2 * (lane & 3) + k] = st.mm[t][k];
-        dst[8 * NT * (D + 1) + 8 * t + 2 * (lane & 3) + k] = st.l[t][k];
-      }
-}
-
-// Another state's columns (kv_put's form) join this one.
-template <int J, int NT>
-__device__ __forceinline__ void kv_join(KvState<J, NT>& st, const float* src, int lane) {
-  constexpr int D = 32 * J;
-  float fa[NT][2], fb[NT][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int md = 0; md < 2 * J; ++md)
+      *reinterpret_cast<float2*>(dst + (2 * c + k) * D + 16 * md + 2 * g) = make_float2(st.o[md][k], st.o[md][2 + k]);
+  if (g == 0)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int col = 8 * t + 2 * (lane & 3) + k;
-      const float mo = src[8 * NT * D + col], m = fmaxf(st.mm[t][k], mo);
-      // (equal references, both -inf among them, need no factor)
-      fa[t][k] = st.mm[t][k] == m ? 1.f : kv_ex2(st.mm[t][k] - m);
-      fb[t][k] = mo == m ? 1.f : kv_ex2(mo - m);
-      st.mm[t][k] = m;
-      st.l[t][k] = st.l[t][k] * fa[t][k] + src[8 * NT * (D + 1) + col] * fb[t][k];
+      dst[8 * D + 2 * c + k] = st.mm[k];
+      dst[8 * (D + 1) + 2 * c + k] = st.l[k];
     }
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int md = 0; md < 2 * J; ++md) {
-        const float2 v = *reinterpret_cast<const float2*>(src + (8 * t + 2 * (lane & 3) + k) * D + 16 * md + 2 * (lane >> 2));
-        st.o[md][t][k] = st.o[md][t][k] * fa[t][k] + v.x * fb[t][k];
-        st.o[md][t][2 + k] = st.o[md][t][2 + k] * fa[t][k] + v.y * fb[t][k];
-      }
 }
 
 // The finished columns as bf16 rows; a column that saw no token gives zeros.
-template <int J, int NT>
-__device__ __forceinline__ void kv_write(const KvParams& p, int s, int seg, const KvState<J, NT>& st, int lane) {
-  const int h = seg / p.passes, pass = seg - h * p.passes;
+template <int J>
+__device__ __forceinline__ void kv_write(const KvParams& p, int s, int h, int col0, const KvState<J>& st, int lane) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int k = 0; k < 2; ++k) {
+    const int col = col0 + 2 * (lane & 3) + k;
+    if (col >= p.cols) continue;
+    const int i = col / p.G;
+    const bool empty = st.mm[k] == -INFINITY && st.l[k] == 0.f;
+    const float r = 1.f / st.l[k];
+    uint16_t* row = p.out + ((int64_t)s * p.n + i) * p.ldo + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int col = (pass * NT + t) * 8 + 2 * (lane & 3) + k;
-      if (col >= p.cols) continue;
-      const int i = col / p.G;
-      const bool empty = st.mm[t][k] == -INFINITY && st.l[t][k] == 0.f;
-      const float r = 1.f / st.l[t][k];
-      uint16_t* row = p.out + ((int64_t)s * p.n + i) * p.ldo + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
-#pragma unroll
-      for (int md = 0; md < 2 * J; ++md) {
-        const float a = empty ? 0.f : st.o[md][t][k] * r, b = empty ? 0.f : st.o[md][t][2 + k] * r;
-        *reinterpret_cast<uint32_t*>(row + 16 * md + 2 * (lane >> 2)) =
-            (uint32_t)float_to_bf16_bits(a) | (uint32_t)float_to_bf16_bits(b) << 16;
-      }
+    for (int md = 0; md < 2 * J; ++md) {
+      const float a = empty ? 0.f : st.o[md][k] * r, b = empty ? 0.f : st.o[md][2 + k] * r;
+      *reinterpret_cast<uint32_t*>(row + 16 * md + 2 * (lane >> 2)) =
+          (uint32_t)float_to_bf16_bits(a) | (uint32_t)float_to_bf16_bits(b) << 16;
     }
+  }
 }
 
-template <int J, int NT>
+template <int J>
+struct KvSmem {
+  static constexpr int rec = kv_record(32 * J);
+  static constexpr int bars = kKvRecords * rec;                // per record: copied, free
+  static constexpr int alloc = bars + kKvRecords * 16;
+};
+
+template <int J, int kTiles>
 __global__ void __launch_bounds__(kKvThreads, 1) q4_kv_attention_kernel(const KvParams p) {
-  using SM = KvSmem<J, NT>;
+  using SM = KvSmem<J>;
+  constexpr int kRings = kKvWarps / kTiles, kStages = kKvRecords / kRings;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sums[2 * kKvWarps];
-  __shared__ int first[2];
-  __shared__ int64_t first0;
+  __shared__ int ends[kKvThreads], sums[kKvWarps];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp / kTiles, tile = warp % kTiles;
   const uint32_t base = smem_u32(smem);
-  const uint32_t ring = base + (uint32_t)(warp * kKvStages * SM::rec), bars = base + SM::bars + 8u * (uint32_t)(warp * kKvStages);
-  float* slots = reinterpret_cast<float*>(smem + SM::ring);
+  const uint32_t ring = base + (uint32_t)(group * kStages * SM::rec), bars = base + SM::bars + 16u * (uint32_t)(group * kStages);
   pdl_launch_dependents();
-  if (lane == 0)
-    for (int i = 0; i < kKvStages; ++i) mbar_init(bars + 8u * i, 1);
+  if (tid < kKvRecords) {
+    mbar_init(base + SM::bars + 16u * tid, 1);
+    mbar_init(base + SM::bars + 16u * tid + 8, kTiles);
+  }
   if (tid == 0) abort_flag = 0;
   fence_mbar_init();
   pdl_wait_previous();
-  const KvScan all = kv_scan<kKvThreads>(p, -1, sums);
-  const int shares = kv_shares_used(all.total, (int)gridDim.x);
-  if ((int)blockIdx.x >= shares) return;
-  const int64_t u0 = all.total * blockIdx.x / shares, u1 = all.total * (blockIdx.x + 1) / shares;
-  // the sequence that holds unit u0: threads sum runs of sequences, one walks its run
-  {
-    const int run = (p.S + kKvThreads - 1) / kKvThreads, a = min(p.S, tid * run), b = min(p.S, a + run);
-    const int64_t per = (int64_t)p.Hk * p.passes;
-    int64_t mine = 0;
-    int L;
-    for (int s = a; s < b; ++s) mine += kv_pages(p, s, L) * per;
-    int64_t ahead = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, ahead, o);
-      if (lane >= o) ahead += v;
-    }
-    if (lane == 31) sums[warp] = ahead;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) ahead += sums[w];
-    ahead -= mine;
-    if (u0 >= ahead && u0 < ahead + mine) {
-      for (int s = a; s < b; ++s) {
-        const int64_t u = kv_pages(p, s, L) * per;
-        if (u0 < ahead + u) {
-          first[0] = s;
-          first0 = ahead;
-          break;
-        }
-        ahead += u;
-      }
-    }
-    __syncthreads();
-  }
+  const int total = kv_scan<kKvThreads>(p, ends, sums);
+  // (few units: their shares lie in as many CTAs as there are)
+  const int shares = kv_shares_used(total, (int)gridDim.x * kRings), share = group * (int)gridDim.x + (int)blockIdx.x;
+  if (share >= shares) return;   // (no barrier of the CTA follows)
+  const int u0 = kv_share_start(total, share, shares), u1 = kv_share_start(total, share + 1, shares);
 
-  // this warp's units: u0 + warp, + kKvWarps, ..; copies run kKvStages ahead of their use
-  KvCursor ahead, here;
-  ahead.start(p, first[0], first0);
-  here = ahead;
-  int64_t next = u0 + warp;
-  int filled = 0, used = 0;
+  KvCursor here;
+  here.start<kKvThreads>(p, u0, ends, lane);
+  // copies run kStages ahead of their use; the group's first warp issues them
+  KvCursor ahead = here;
+  int next = u0, used = 0, filled = 0;
   uint32_t there = 0;       // per stage: a page was copied
   int32_t page = -1;        // of unit `next`
+  bool ok = true;
   auto look = [&]() {
     if (next < u1) {
       ahead.seek(p, next);
       page = (int32_t)ld_global_u32(p.table + (int64_t)ahead.s * p.M + (next - ahead.seg0));
     }
   };
-  auto issue = [&]() {
+  auto issue = [&]() {      // (every warp keeps the books)
     if (next >= u1) return;
-    const int st = filled % kKvStages;
+    const int st = filled % kStages;
     const bool good = page >= 0 && page < p.P;   // a page that is not there: its tokens are left out
     there = good ? there | 1u << st : there & ~(1u << st);
-    if (good && lane == 0) {
-      const uint32_t bar = bars + 8u * (uint32_t)st;
+    if (good && tile == 0 && lane == 0) {
+      const uint32_t bar = bars + 16u * (uint32_t)st;
       mbar_expect_tx(bar, SM::rec);
       bulk_load(ring + (uint32_t)(st * SM::rec), p.cache + ((int64_t)page * p.Hk + ahead.seg / p.passes) * SM::rec, SM::rec, bar);
     }
     ++filled;
-    next += kKvWarps;
+    ++next;
     look();
   };
   __syncwarp();
   look();
-  for (int i = 0; i < kKvStages; ++i) issue();
+  for (int i = 0; i < kStages; ++i) issue();
 
-  KvState<J, NT> st;
-  KvQuery<J, NT> qy;
-  uint32_t phases = 0;
-  bool ok = true;
-  for (int64_t u = u0; u < u1;) {
+  KvState<J> st;
+  KvQuery<J> qy;
+  uint32_t phases = 0;      // per stage: the parity of its next copy
+  for (int u = u0; u < u1 && ok;) {
     here.seek(p, u);
-    const int64_t end = min(here.seg0 + here.pages, u1);   // this CTA's units of the segment
-    const bool alone = end - u == 1;
-    int64_t mine = u + (warp - (int)((u - u0) % kKvWarps) + kKvWarps) % kKvWarps;
-    const bool work = mine < end;
-    if (work || (warp == 0 && !alone)) st.clear();
-    if (work) qy.load(p, here, lane);
-    for (; ok && mine < end; mine += kKvWarps) {
-      const int s = used % kKvStages;
+    const int end = min(here.seg0 + here.pages, u1);   // this share's units of the segment
+    const int h = here.seg / p.passes, col0 = ((here.seg - h * p.passes) * kTiles + tile) * 8;
+    const bool whole = end - u == here.pages;
+    st.clear();
+    qy.load(p, here.s, here.L, h, col0, lane);
+    for (; u < end; ++u) {
+      const int s = used % kStages;
       if (there >> s & 1u) {
-        ok = warp_wait(bars + 8u * (uint32_t)s, phases >> s & 1u, &abort_flag, &g_kv_status);
+        ok = warp_wait_vote(bars + 16u * (uint32_t)s, phases >> s & 1u, &abort_flag, &g_kv_status);
         if (!ok) break;
         phases ^= 1u << s;
-        const int token0 = (int)(mine - here.seg0) * kPage;
+        const int token0 = (u - here.seg0) * kPage;
         // (the last n - 1 tokens are seen by some columns only)
         if (token0 + kPage <= here.L - p.n + 1)
-          kv_page<J, NT, false>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
+          kv_page<J, false>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
         else
-          kv_page<J, NT, true>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
+          kv_page<J, true>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
       }
-      ++used;
-      __threadfence_block();
-      __syncwarp();
-      issue();
-    }
-    if (work) kv_finish_state(st);
-    const bool whole = end - u == here.pages;
-    // (a share's first segment may have begun in an earlier share, its last may go on: slots 0 and 1)
-    float* part = p.part + ((int64_t)blockIdx.x * 2 + (u == u0 ? 0 : 1)) * part_floats(32 * J, NT);
-    if (alone) {
-      if (work) {
-        if (whole) kv_write(p, here.s, here.seg, st, lane);
-        else kv_put(part, st, lane);
-      }
-    } else {
-      // warp 0 joins the others in order, as many at a time as there are slots
-      for (int w0 = 1; w0 < kKvWarps; w0 += SM::slots) {
-        if (warp >= w0 && warp < w0 + SM::slots && work) kv_put(slots + (warp - w0) * part_floats(32 * J, NT), st, lane);
-        __syncthreads();
-        if (warp == 0)
-          for (int w = w0; w < min(kKvWarps, w0 + SM::slots); ++w) {
-            const int64_t its = u + (w - (int)((u - u0) % kKvWarps) + kKvWarps) % kKvWarps;
-            if (its < end) kv_join(st, slots + (w - w0) * part_floats(32 * J, NT), lane);
+      if constexpr (kTiles == 1) {
+        ++used;
+        __threadfence_block();
+        __syncwarp();
+        issue();
+      } else {
+        // the record before this one is refilled: the group's other warps are likely done with it
+        warp_release(bars + 16u * (uint32_t)s + 8, lane);
+        const int b = used - 1;
+        ++used;
+        if (b >= 0) {
+          if (tile == 0 && next < u1) {
+            ok = warp_wait_vote(bars + 16u * (uint32_t)(b % kStages) + 8, (uint32_t)(b / kStages) & 1u, &abort_flag, &g_kv_status);
+            if (!ok) break;
           }
-        __syncthreads();
-      }
-      if (warp == 0) {
-        if (whole) kv_write(p, here.s, here.seg, st, lane);
-        else kv_put(part, st, lane);
+          issue();
+        }
       }
     }
-    u = end;
+    kv_finish_state(st);
+    if (!ok) break;
+    if (whole) {
+      kv_write(p, here.s, h, col0, st, lane);
+    } else {
+      // (a share's first segment may have begun in an earlier share, its last may go on: slots 0 and 1)
+      const int slot = here.seg0 > u0 ? 1 : 0;
+      kv_put(p.part + (((int64_t)share * 2 + slot) * kTiles + tile) * part_floats(32 * J), st, lane);
+    }
   }
   // nothing is left in flight, after a wait that ran out either
-  if (!ok)
-    for (; used < filled; ++used) {
-      const int s = used % kKvStages;
-      if ((there >> s & 1u) && lane == 0) mbar_drain(bars + 8u * (uint32_t)s, phases >> s & 1u);
-      phases ^= 1u << s;
-    }
+  if (!ok && tile == 0 && lane == 0)
+    for (int i = used; i < filled; ++i)
+      if (there >> (i % kStages) & 1u) mbar_drain(bars + 16u * (uint32_t)(i % kStages), phases >> (i % kStages) & 1u);
 }
 
 // Segments that lie in several shares, and sequences without tokens.
-template <int J, int NT>
-__global__ void __launch_bounds__(128) q4_kv_combine_kernel(const KvParams p, int most) {
+constexpr int kKvJoin = 256;
+template <int J, int kTiles>
+__global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p, int most) {
   constexpr int D = 32 * J;
-  __shared__ int64_t sums[8];
+  __shared__ int ends[kKvJoin], sums[kKvJoin / 32];
   pdl_launch_dependents();
   pdl_wait_previous();
   const int per = p.Hk * p.passes, s = blockIdx.x / per, seg = blockIdx.x - s * per;
-  const KvScan at = kv_scan<128>(p, s, sums);
-  const int shares = kv_shares_used(at.total, most);
-  int L;
+  const int total = kv_scan<kKvJoin>(p, ends, sums);
+  const int shares = kv_shares_used(total, most);
+  const int run = (p.S + kKvJoin - 1) / kKvJoin, t = s / run;
+  int L, a = t > 0 ? ends[t - 1] : 0;
+  for (int i = t * run; i < s; ++i) a += kv_pages(p, i, L) * per;
   const int pages = kv_pages(p, s, L);
   const int h = seg / p.passes, pass = seg - h * p.passes;
-  const int64_t a = at.before + (int64_t)seg * pages, b = a + pages;
-  int64_t c0 = 0, c1 = -1;
+  a += seg * pages;
+  int c0 = 0, c1 = -1;
   if (pages > 0) {
-    c0 = ((a + 1) * shares - 1) / at.total;
-    c1 = (b * shares - 1) / at.total;
+    // the shares of the segment's first and last unit
+    c0 = (int)((((int64_t)a + 1) * shares - 1) / total);
+    c1 = (int)(((int64_t)(a + pages) * shares - 1) / total);
     if (c0 == c1) return;   // finished by its share
   }
-  for (int e = threadIdx.x; e < 8 * NT * (D / 2); e += 128) {
-    const int local = e / (D / 2), d = 2 * (e - local * (D / 2)), col = pass * 8 * NT + local;
+  for (int e = threadIdx.x; e < 8 * kTiles * (D / 2); e += kKvJoin) {
+    const int local = e / (D / 2), d = 2 * (e - local * (D / 2)), col = pass * 8 * kTiles + local;
     if (col >= p.cols) break;
+    // a share's slot: 1 only where the segment begins inside it, behind another (that is its first share's case)
+    const int64_t pitch = (int64_t)2 * kTiles * part_floats(D);
+    const float* part = p.part + (local >> 3) * part_floats(D) + c0 * pitch;
+    const int64_t head = c1 >= c0 && a > kv_share_start(total, c0, shares) ? kTiles * part_floats(D) : 0;
+    const int col8 = local & 7;
     float m = -INFINITY;
-    // a share's slot: 1 only where the segment begins inside it, behind another
-    auto slot = [&](int64_t c) {
-      const int64_t u0 = at.total * c / shares;
-      return p.part + (c * 2 + (a > u0 ? 1 : 0)) * part_floats(D, NT);
-    };
-    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, slot(c)[8 * NT * D + local]);
+#pragma unroll 4
+    for (int c = 0; c <= c1 - c0; ++c) m = fmaxf(m, part[c * pitch + (c == 0 ? head : 0) + 8 * D + col8]);
     float l = 0.f, o0 = 0.f, o1 = 0.f;
-    for (int64_t c = c0; c <= c1; ++c) {
-      const float* part = slot(c);
-      const float mc = part[8 * NT * D + local], f = mc == m ? 1.f : kv_ex2(mc - m);
-      const float2 v = *reinterpret_cast<const float2*>(part + local * D + d);
-      l += part[8 * NT * (D + 1) + local] * f;
+#pragma unroll 4
+    for (int c = 0; c <= c1 - c0; ++c) {
+      const float* q = part + c * pitch + (c == 0 ? head : 0);
+      const float mc = q[8 * D + col8], f = mc == m ? 1.f : kv_ex2(mc - m);
+      const float2 v = *reinterpret_cast<const float2*>(q + col8 * D + d);
+      l += q[8 * (D + 1) + col8] * f;
       o0 += v.x * f;
       o1 += v.y * f;
     }
@@ -884,7 +789,7 @@ __global__ void __launch_bounds__(128) q4_kv_combine_kernel(const KvParams p, in
   }
 }
 
-int kv_shares() {
+int kv_sms() {
   static int cache[64] = {};
   int dev = 0, sms = 152;
   if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
@@ -894,40 +799,43 @@ int kv_shares() {
   return sms;
 }
 
-template <int J, int NT>
+template <int J, int kTiles>
 int kv_attention_run(const KvParams& p, cudaStream_t stream) {
-  using SM = KvSmem<J, NT>;
+  using SM = KvSmem<J>;
   static bool set[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !set[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_kv_attention_kernel<J, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::alloc),
+    if (cuda_check(cudaFuncSetAttribute(q4_kv_attention_kernel<J, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::alloc),
                    "kv4_attention: cudaFuncSetAttribute(max dynamic shared memory)"))
       return Q4LIN_ERR_CUDA;
     if (dev < 64) set[dev] = true;
   }
-  const int shares = kv_shares();
-  const int st = pdl_launch(q4_kv_attention_kernel<J, NT>, "kv4_attention: kernel launch", (unsigned)shares, kKvThreads, SM::alloc, stream, &p);
+  const int sms = kv_sms();
+  const int st = pdl_launch(q4_kv_attention_kernel<J, kTiles>, "kv4_attention: kernel launch", (unsigned)sms, kKvThreads, SM::alloc, stream, &p);
   if (st != Q4LIN_OK) return st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.S * p.Hk * p.passes), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.blockDim = dim3(kKvJoin, 1, 1);
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_kv_combine_kernel<J, NT>, p, shares), "kv4_attention: combine launch");
+  return cuda_check(cudaLaunchKernelEx(&cfg, q4_kv_combine_kernel<J, kTiles>, p, sms * (kKvWarps / kTiles)), "kv4_attention: combine launch");
 }
 
-int kv_tiles(int64_t cols) { return cols <= 8 ? 1 : 2; }
+// Tiles of 8 columns that share a record: all of them up to four (24 columns take a group of four, one
+// warp of it idle).
+int kv_tiles(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
 }  // namespace
 
 int64_t kv_page_bytes(int64_t D) { return kv_record((int)D); }
 
-int64_t kv_workspace_bytes(int64_t D, int64_t cols) { return (int64_t)kv_shares() * 2 * part_floats((int)D, kv_tiles(cols)) * 4; }
+// Two partial sums per share and tile: kKvWarps tiles per SM, however they are grouped.
+int64_t kv_workspace_bytes(int64_t D) { return (int64_t)kv_sms() * kKvWarps * 2 * part_floats((int)D) * 4; }
 
 int64_t kv_passes(int64_t cols) { return (cols + 8 * kv_tiles(cols) - 1) / (8 * kv_tiles(cols)); }
 
@@ -970,10 +878,14 @@ int kv_attention_launch(const KvAttnArgs& a) {
   p.cols = p.n * p.G;
   p.passes = (int)kv_passes(p.cols);
   p.c = a.scale * 1.4426950408889634f;
-  const int nt = kv_tiles(p.cols);
-  if (a.D == 64) return nt == 1 ? kv_attention_run<2, 1>(p, a.stream) : kv_attention_run<2, 2>(p, a.stream);
-  if (a.D == 96) return nt == 1 ? kv_attention_run<3, 1>(p, a.stream) : kv_attention_run<3, 2>(p, a.stream);
-  return nt == 1 ? kv_attention_run<4, 1>(p, a.stream) : kv_attention_run<4, 2>(p, a.stream);
+  const int tiles = kv_tiles(p.cols);
+  auto pick = [&](auto j) {
+    constexpr int J = decltype(j)::value;
+    return tiles == 1 ? kv_attention_run<J, 1>(p, a.stream) : tiles == 2 ? kv_attention_run<J, 2>(p, a.stream) : kv_attention_run<J, 4>(p, a.stream);
+  };
+  if (a.D == 64) return pick(std::integral_constant<int, 2>{});
+  if (a.D == 96) return pick(std::integral_constant<int, 3>{});
+  return pick(std::integral_constant<int, 4>{});
 }
 
 int kv_status(int* value, bool clear) {

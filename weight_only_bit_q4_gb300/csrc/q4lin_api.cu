@@ -546,8 +546,9 @@ int validate_kv_attention(int64_t S, int64_t q_len, int64_t Hq, int64_t Hk, int6
   if (Hk == 0 || Hq % Hk != 0) return refuse("kv4_attention: Hq must be a multiple of Hk");
   if (q_len > 65536 || S * q_len >= (int64_t)1 << 31 || q_len * Hq >= (int64_t)1 << 24) return Q4LIN_ERR_INVALID_ARG;
   const int64_t passes = q4::kv_passes(q_len * (Hq / Hk));
-  if ((double)S * (double)Hk * (double)passes >= 2147483648.0)
-    return refuse("kv4_attention: too many sequences, heads and columns for one launch", Q4LIN_ERR_UNSUPPORTED_SHAPE);
+  if ((double)S * (double)Hk * (double)passes * (double)(max_pages > 0 ? max_pages : 1) >= 2147483648.0)
+    return refuse("kv4_attention: sequences, heads and pages of the table (and passes of 32 columns) for 2^31 units or more",
+                  Q4LIN_ERR_UNSUPPORTED_SHAPE);
   return Q4LIN_OK;
 }
 
@@ -622,7 +623,7 @@ int q4lin_kv4_read(const uint8_t* cache, const int32_t* page_table, const int32_
 
 size_t q4lin_kv4_workspace_bytes(int64_t S, int64_t q_len, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages) {
   if (validate_kv_attention(S, q_len, Hq, Hk, D, max_pages) != Q4LIN_OK || S == 0 || q_len == 0 || Hq == 0) return 0;
-  return round256((size_t)q4::kv_workspace_bytes(D, q_len * (Hq / Hk)));
+  return round256((size_t)q4::kv_workspace_bytes(D));
 }
 
 int q4lin_kv4_attention(const uint16_t* q, int64_t ldq, const uint8_t* cache, const int32_t* page_table,
