@@ -52,108 +52,166 @@ __device__ __forceinline__ bool kv_slot(const KvTokParams& p, int64_t t, int64_t
   return page >= 0 && page < p.P;
 }
 
-constexpr int kTokThreads = 128;
+constexpr int kTokThreads = 256;
+constexpr int kTokTile = 64;   // tokens of a CTA
 
-// LPR lanes (8 values each) of a token's head; keys and values in turn.  The eight lanes of a
-// scale group agree on its largest magnitude by shuffles.  The quotient is an exact division:
-// x / s of an 8-bit by an 11-bit significand never comes close enough to a half for FP32's
-// rounding to reach it, so the codes are those of the definition.
+// A CTA takes 64 tokens' keys or values of one head; LPR lanes (8 values each) share a row.  V
+// codes cross shared memory between token order (a lane has 8 values of a token) and the
+// record's order (a lane has a token's byte of a row), so that tokens of a page are written and
+// read a row at a time.
+struct KvTile {
+  int64_t page[kTokTile];   // < 0: the token has no place
+  int place[kTokTile];
+};
+
+__device__ __forceinline__ void kv_places(const KvTokParams& p, KvTile& tile, int64_t t0) {
+  if (threadIdx.x < kTokTile) {
+    int64_t page = -1;
+    int o = 0;
+    const int64_t t = t0 + threadIdx.x;
+    if (t >= p.T || !kv_slot(p, t, page, o)) page = -1;
+    tile.page[threadIdx.x] = page;
+    tile.place[threadIdx.x] = o;
+  }
+}
+
+// The eight lanes of a scale group agree on its largest magnitude by shuffles.  q = rint(x / s): x
+// times 1 / s decides, unless it lies so near a half that its error (below 2^-19) could matter;
+// then the quotient itself: of an 8-bit by an 11-bit significand it is never so near a half that
+// FP32's rounding would reach it.
 template <int LPR>
 __global__ void __launch_bounds__(kTokThreads) q4_kv_append_kernel(const KvTokParams p) {
+  constexpr int kRows = kTokThreads / LPR, kPasses = kTokTile / kRows;
+  __shared__ KvTile tile;
+  __shared__ uint32_t words[kTokTile][17];
+  const int tid = threadIdx.x, b = tid % LPR;
+  const int side = (int)blockIdx.y >= p.Hk ? 1 : 0, h = (int)blockIdx.y - side * p.Hk;
+  const int64_t t0 = (int64_t)blockIdx.x * kTokTile;
   pdl_launch_dependents();
   pdl_wait_previous();
-  const int64_t unit = ((int64_t)blockIdx.x * kTokThreads + threadIdx.x) / LPR;
-  const int b = threadIdx.x % LPR;
-  const int64_t t = unit / (2 * p.Hk);
-  if (t >= p.T) return;   // (whole lane groups)
-  const int sh = (int)(unit - t * 2 * p.Hk), side = sh >= p.Hk ? 1 : 0, h = sh - side * p.Hk;
-  const unsigned mask = 0xFFu << (threadIdx.x & 24);
   const bool in = 8 * b < p.D;
-  uint4 w = make_uint4(0u, 0u, 0u, 0u);
-  if (in) w = ld_global_u4(p.src[side] + t * p.ld[side] + (int64_t)h * p.D + 8 * b);
-  int64_t page = 0;
-  int o = 0;
-  const bool ok = kv_slot(p, t, page, o);
-  const uint32_t xs[4] = {w.x, w.y, w.z, w.w};
-  uint32_t top = 0;   // magnitudes of bf16 compare as their bits; above 0x7F7F: not finite
+  const uint16_t* src = (side ? p.src[1] : p.src[0]) + (int64_t)h * p.D + 8 * b;
+  const int64_t ld = side ? p.ld[1] : p.ld[0];
+  uint4 w[kPasses];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = __vmaxu2(top, xs[i] & 0x7FFF7FFFu);
-  top = max(top & 0xFFFFu, top >> 16);
+  for (int i = 0; i < kPasses; ++i) {
+    const int64_t t = t0 + i * kRows + tid / LPR;
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (in && t < p.T) w[i] = ld_global_u4(src + t * ld);
+  }
+  kv_places(p, tile, t0);
+  __syncthreads();
+  const int G = kv_groups(p.D);
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(mask, top, d));
-  if (!ok || !in) return;
-  uint16_t scale = 0x7E00u;   // NaN: a group with a value that is not finite reads as NaN
-  uint32_t code = 0x88888888u;
-  if (top < 0x7F80u) {
-    const __half s = __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top << 16), 7.f), 65504.f));
-    const float sf = __half2float(s);
-    scale = __half_as_ushort(s);
-    if (sf > 0.f) {
-      code = 0;
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = i * kRows + tid / LPR;
+    const uint32_t xs[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t top = 0;   // magnitudes of bf16 compare as their bits; above 0x7F7F: not finite
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = i & 1 ? bf16hi(xs[i >> 1]) : bf16lo(xs[i >> 1]);
-        const float q = fminf(fmaxf(rintf(__fdiv_rn(x, sf)), -8.f), 7.f);
-        code |= (uint32_t)((int)q + 8) << (4 * i);
+    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, xs[e] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    uint16_t scale = 0x7E00u;   // NaN: a group with a value that is not finite reads as NaN
+    uint32_t code = 0x88888888u;
+    if (top < 0x7F80u) {
+      const __half s = __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top << 16), 7.f), 65504.f));
+      const float sf = __half2float(s);
+      scale = __half_as_ushort(s);
+      if (sf > 0.f) {
+        const float inv = __frcp_rn(sf);
+        code = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = e & 1 ? bf16hi(xs[e >> 1]) : bf16lo(xs[e >> 1]);
+          // 1.5 * 2^23 + 8: the sum's last bits are the code
+          constexpr float magic = 12582920.f;
+          float q = fminf(fmaxf(x * inv, -8.f), 7.f), n = q + magic;
+          if (fabsf(q - (n - magic)) > 0.499f) n = fminf(fmaxf(__fdiv_rn(x, sf), -8.f), 7.f) + magic;
+          code |= (__float_as_uint(n) & 15u) << (4 * e);
+        }
       }
     }
+    const int64_t page = tile.page[r];
+    if (side == 1 && in) words[r][b] = code;
+    if (page < 0 || !in) continue;
+    uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D);
+    const int o = tile.place[r];
+    if (side == 0) *reinterpret_cast<uint32_t*>(rec + o * (p.D / 2) + ((b & 3) * (p.D / 32) + (b >> 2)) * 4) = code;
+    if ((b & 7) == 0) reinterpret_cast<uint16_t*>(rec + 64 * p.D)[side * kPage * G + o * G + (b >> 3)] = scale;
   }
-  uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D);
-  if (side == 0) {
-    *reinterpret_cast<uint32_t*>(rec + o * (p.D / 2) + ((b & 3) * (p.D / 32) + (b >> 2)) * 4) = code;
-  } else {
-    uint8_t* v = rec + 32 * p.D + 4 * b * kPage + v_place(o);
+  if (side == 0) return;
+  __syncthreads();
+  const int r = tid % kTokTile;
+  const int64_t page = tile.page[r];
+  if (page < 0) return;
+  uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D) + 32 * p.D + v_place(tile.place[r]);
+  for (int b0 = tid / kTokTile; b0 < p.D / 8; b0 += kTokThreads / kTokTile) {
+    const uint32_t code = words[r][b0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i * kPage] = (uint8_t)(code >> (8 * i));
-  }
-  if ((b & 7) == 0) {
-    const int G = kv_groups(p.D);
-    reinterpret_cast<uint16_t*>(rec + 64 * p.D)[side * kPage * G + o * G + (b >> 3)] = scale;
+    for (int i = 0; i < 4; ++i) rec[(4 * b0 + i) * kPage] = (uint8_t)(code >> (8 * i));
   }
 }
 
 template <int LPR>
 __global__ void __launch_bounds__(kTokThreads) q4_kv_read_kernel(const KvTokParams p) {
+  constexpr int kRows = kTokThreads / LPR, kPasses = kTokTile / kRows;
+  __shared__ KvTile tile;
+  __shared__ uint32_t words[kTokTile][17];
+  const int tid = threadIdx.x, b = tid % LPR;
+  const int side = (int)blockIdx.y >= p.Hk ? 1 : 0, h = (int)blockIdx.y - side * p.Hk;
+  const int64_t t0 = (int64_t)blockIdx.x * kTokTile;
   pdl_launch_dependents();
   pdl_wait_previous();
-  const int64_t unit = ((int64_t)blockIdx.x * kTokThreads + threadIdx.x) / LPR;
-  const int b = threadIdx.x % LPR;
-  const int64_t t = unit / (2 * p.Hk);
-  if (t >= p.T || 8 * b >= p.D) return;
-  const int sh = (int)(unit - t * 2 * p.Hk), side = sh >= p.Hk ? 1 : 0, h = sh - side * p.Hk;
-  int64_t page;
-  int o;
-  if (!kv_slot(p, t, page, o)) return;
-  const uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D);
-  uint32_t code = 0;
-  if (side == 0) {
-    code = ld_global_u32(rec + o * (p.D / 2) + ((b & 3) * (p.D / 32) + (b >> 2)) * 4);
-  } else {
-    const volatile uint8_t* v = rec + 32 * p.D + 4 * b * kPage + v_place(o);
+  kv_places(p, tile, t0);
+  __syncthreads();
+  if (side == 1) {
+    const int r = tid % kTokTile;
+    const int64_t page = tile.page[r];
+    if (page >= 0) {
+      const volatile uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D) + 32 * p.D + v_place(tile.place[r]);
+#pragma unroll 4
+      for (int b0 = tid / kTokTile; b0 < p.D / 8; b0 += kTokThreads / kTokTile) {
+        uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) code |= (uint32_t)v[i * kPage] << (8 * i);
+        for (int i = 0; i < 4; ++i) c[i] = rec[(4 * b0 + i) * kPage];
+        words[r][b0] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+      }
+    }
+    __syncthreads();
   }
+  if (8 * b >= p.D) return;
   const int G = kv_groups(p.D);
-  const float s = fp16_bits_to_float(
-      reinterpret_cast<const volatile uint16_t*>(rec + 64 * p.D)[side * kPage * G + o * G + (b >> 3)]);
-  uint32_t out[4];
+  uint16_t* dst = (side ? p.dst[1] : p.dst[0]) + (int64_t)h * p.D + 8 * b;
+  const int64_t ld = side ? p.ld[1] : p.ld[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = (float)((int)((code >> (8 * i)) & 15u) - kZeroPoint) * s;
-    const float hi = (float)((int)((code >> (8 * i + 4)) & 15u) - kZeroPoint) * s;
-    out[i] = (uint32_t)float_to_bf16_bits(lo) | (uint32_t)float_to_bf16_bits(hi) << 16;
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = i * kRows + tid / LPR;
+    const int64_t page = tile.page[r];
+    if (page < 0) continue;
+    const uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D);
+    const int o = tile.place[r];
+    const uint32_t code = side ? words[r][b] : ld_global_u32(rec + o * (p.D / 2) + ((b & 3) * (p.D / 32) + (b >> 2)) * 4);
+    const float s = fp16_bits_to_float(
+        reinterpret_cast<const volatile uint16_t*>(rec + 64 * p.D)[side * kPage * G + o * G + (b >> 3)]);
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float lo = (float)((int)((code >> (8 * e)) & 15u) - kZeroPoint) * s;
+      const float hi = (float)((int)((code >> (8 * e + 4)) & 15u) - kZeroPoint) * s;
+      out[e] = (uint32_t)float_to_bf16_bits(lo) | (uint32_t)float_to_bf16_bits(hi) << 16;
+    }
+    *reinterpret_cast<uint4*>(dst + (t0 + r) * ld) = make_uint4(out[0], out[1], out[2], out[3]);
   }
-  *reinterpret_cast<uint4*>(p.dst[side] + t * p.ld[side] + (int64_t)h * p.D + 8 * b) =
-      make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 template <class Kernel>
-int pdl_launch(Kernel kernel, const char* what, unsigned blocks, unsigned threads, size_t smem, cudaStream_t stream, const void* params) {
+int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, size_t smem, cudaStream_t stream, const void* params) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.gridDim = blocks;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -812,7 +870,7 @@ int kv_attention_run(const KvParams& p, cudaStream_t stream) {
     if (dev < 64) set[dev] = true;
   }
   const int sms = kv_sms();
-  const int st = pdl_launch(q4_kv_attention_kernel<J, kTiles>, "kv4_attention: kernel launch", (unsigned)sms, kKvThreads, SM::alloc, stream, &p);
+  const int st = pdl_launch(q4_kv_attention_kernel<J, kTiles>, "kv4_attention: kernel launch", dim3((unsigned)sms, 1, 1), kKvThreads, SM::alloc, stream, &p);
   if (st != Q4LIN_OK) return st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -852,16 +910,16 @@ int kv_tokens_launch(const KvTokArgs& a, bool append) {
   p.Hk = (int)a.Hk;
   p.D = (int)a.D;
   const int lpr = a.D == 64 ? 8 : 16;
-  const int64_t blocks = (a.T * 2 * a.Hk * lpr + kTokThreads - 1) / kTokThreads;
-  if (blocks > 0x7fffffff) {
-    set_error_detail("kv4: too many tokens for one launch");
+  const dim3 blocks((unsigned)((a.T + kTokTile - 1) / kTokTile), (unsigned)(2 * a.Hk), 1);
+  if (blocks.y > 65535) {
+    set_error_detail("kv4: too many heads for one launch");
     return Q4LIN_ERR_UNSUPPORTED_SHAPE;
   }
   if (append)
-    return lpr == 8 ? pdl_launch(q4_kv_append_kernel<8>, "kv4_append: kernel launch", (unsigned)blocks, kTokThreads, 0, a.stream, &p)
-                    : pdl_launch(q4_kv_append_kernel<16>, "kv4_append: kernel launch", (unsigned)blocks, kTokThreads, 0, a.stream, &p);
-  return lpr == 8 ? pdl_launch(q4_kv_read_kernel<8>, "kv4_read: kernel launch", (unsigned)blocks, kTokThreads, 0, a.stream, &p)
-                  : pdl_launch(q4_kv_read_kernel<16>, "kv4_read: kernel launch", (unsigned)blocks, kTokThreads, 0, a.stream, &p);
+    return lpr == 8 ? pdl_launch(q4_kv_append_kernel<8>, "kv4_append: kernel launch", blocks, kTokThreads, 0, a.stream, &p)
+                    : pdl_launch(q4_kv_append_kernel<16>, "kv4_append: kernel launch", blocks, kTokThreads, 0, a.stream, &p);
+  return lpr == 8 ? pdl_launch(q4_kv_read_kernel<8>, "kv4_read: kernel launch", blocks, kTokThreads, 0, a.stream, &p)
+                  : pdl_launch(q4_kv_read_kernel<16>, "kv4_read: kernel launch", blocks, kTokThreads, 0, a.stream, &p);
 }
 
 int kv_attention_launch(const KvAttnArgs& a) {

@@ -12,11 +12,10 @@
 //
 // Split: a row belongs to a cluster of 1 .. 8 CTAs (as many as fill the GPU, with few rows), its
 // 16-byte chunks dealt to the cluster's threads in turn; what lies before the first and behind
-// the last whole chunk goes to the first CTA's and the last CTA's single threads.  A warp's
-// chunks come in ascending order, so a list that takes only larger logits keeps ties by the
-// lowest token.  Lists: lane i of every warp holds the warp's i-th; a vote per chunk of 32
+// the last whole chunk goes to the first CTA's and the last CTA's single threads.  Lists: lane i of every warp holds the warp's i-th; a vote per chunk of 32
 // vectors decides whether any of its logits beats the last entry, which is rare after the
-// first few.  Warps, then CTAs (distributed shared memory) are merged in order.
+// first few (the first batch meets a bar made of the lanes' maxima).  Warps, then CTAs
+// (distributed shared memory) are merged in order.
 #include <cfloat>
 
 #include "q4_internal.h"
@@ -29,6 +28,7 @@ namespace {
 constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxTop = 32;
+constexpr int kMaxCluster = 8;
 constexpr float kSlack = 40.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -76,16 +76,15 @@ __device__ __forceinline__ void shift_to(float m, Sums& o) {
   o.m = m;
 }
 
-__device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && (uint32_t)i < (uint32_t)j); }
-
 // The warp's list: lane i holds the i-th largest (value, token), i < k; unused entries are (-inf, -1).
+// Equal values stand in the order of their tokens.
 struct TopList {
   float v;
   int id;
 };
 
 __device__ __forceinline__ void list_insert(TopList& l, float x, int id, int k, int lane) {
-  const int at = __popc(__ballot_sync(0xffffffffu, lane < k && l.v >= x));   // equal ones came before
+  const int at = __popc(__ballot_sync(0xffffffffu, lane < k && (l.v > x || (l.v == x && l.id < id))));
   const float pv = __shfl_up_sync(0xffffffffu, l.v, 1);
   const int pi = __shfl_up_sync(0xffffffffu, l.id, 1);
   if (lane > at) {
@@ -98,8 +97,24 @@ __device__ __forceinline__ void list_insert(TopList& l, float x, int id, int k, 
   }
 }
 
-// Merge of `lists` sorted lists of k entries (value and token arrays `stride` entries apart) into lane i's
-// i-th of the result: every lane walks one list.
+// Floats above -inf as integers in their order, above 0 (-inf and NaN: 0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return v > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
+}
+
+// The k-th largest of the lanes' keys (0: there are fewer above 0).
+__device__ __forceinline__ uint32_t kth_key(uint32_t key, int k, int lane) {
+  uint32_t top = 0;
+  for (int r = 0; r < k; ++r) {
+    top = __reduce_max_sync(0xffffffffu, key);
+    if (top == 0) return 0;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, key == top)) - 1) key = 0;
+  }
+  return top;
+}
+
+// Merge of `lists` sorted lists of k entries into lane i's i-th of the result: every lane walks one list.
 template <class Load>
 __device__ __forceinline__ TopList merge_lists(int lists, int k, int lane, Load load) {
   int at = 0;
@@ -108,21 +123,13 @@ __device__ __forceinline__ TopList merge_lists(int lists, int k, int lane, Load 
   if (lane < lists) load(lane, 0, v, id);
   TopList out{-INFINITY, -1};
   for (int r = 0; r < k; ++r) {
-    float bv = v;
-    int bi = id, bl = lane;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, o), ol = __shfl_xor_sync(0xffffffffu, bl, o);
-      if (before(ov, oi, bv, bi) || (ov == bv && oi == bi && ol < bl)) {
-        bv = ov;
-        bi = oi;
-        bl = ol;
-      }
-    }
-    if (bi < 0) break;   // (uniform: nothing is left)
-    if (lane == r) out = TopList{bv, bi};
-    if (lane == bl) {
+    const uint32_t key = order_key(v), top = __reduce_max_sync(0xffffffffu, key);
+    if (top == 0) break;   // (uniform: nothing is left)
+    const uint32_t first = __reduce_min_sync(0xffffffffu, key == top ? (uint32_t)id : 0xffffffffu);
+    const bool mine = key == top && (uint32_t)id == first;
+    const float win = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, mine)) - 1);
+    if (lane == r) out = TopList{win, (int)first};
+    if (mine) {
       ++at;
       v = -INFINITY;
       id = -1;
@@ -196,12 +203,12 @@ __device__ __forceinline__ void add_values(Sums& r, float& limit, const float2 (
 }
 
 struct LpShared {
-  Sums sums[kLpWarps];
+  alignas(16) Sums sums[kLpWarps];
   float lv[kLpWarps][kMaxTop];
   int li[kLpWarps][kMaxTop];
-  Sums cta;                  // this CTA's, read by the cluster's first
-  float cv[kMaxTop];
-  int ci[kMaxTop];
+  alignas(16) Sums cta[kMaxCluster];     // (the cluster's first CTA) what its CTAs have sent
+  float cv[kMaxCluster][kMaxTop];
+  int ci[kMaxCluster][kMaxTop];
   float row[2];              // M, ln S
 };
 
@@ -231,6 +238,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4_logprobs_kernel(const LpPara
   const int64_t row = blockIdx.x / (unsigned)p.cs;
   const int rank = (int)(blockIdx.x - (unsigned)row * (unsigned)p.cs);
   pdl_launch_dependents();
+  if (p.cs > 1) cluster_arrive();   // (waited for before anything is sent)
   pdl_wait_previous();
   constexpr int64_t esize = kF32 ? 4 : 2;
   const char* x = static_cast<const char*>(p.x) + row * p.ld * esize;
@@ -243,10 +251,24 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4_logprobs_kernel(const LpPara
   float limit = -INFINITY;
   TopList list{-INFINITY, -1};
   float last = -INFINITY;     // the list's last entry
-  auto offer = [&](float v, int id) {   // (uniform)
-    if (v > last) {
-      list_insert(list, v, id, p.k, lane);
-      last = __shfl_sync(0xffffffffu, list.v, p.k - 1);
+  int last_id = -1;
+  // every lane offers a value (uniform); those that beat the last entry go in, one after the other
+  auto offer = [&](float v, int id) {
+    uint32_t some = __ballot_sync(0xffffffffu, v > last || (v == last && id < last_id));
+    while (some) {
+      const int from = __ffs(some) - 1;
+      some &= some - 1;
+      const float x = __shfl_sync(0xffffffffu, v, from);
+      const int i = __shfl_sync(0xffffffffu, id, from);
+      if (x > last || (x == last && i < last_id)) {   // (uniform)
+        list_insert(list, x, i, p.k, lane);
+        const float lv = __shfl_sync(0xffffffffu, list.v, p.k - 1);
+        const int li = __shfl_sync(0xffffffffu, list.id, p.k - 1);
+        if (lv > -INFINITY) {   // the list is full: its last entry is the bar now
+          last = lv;
+          last_id = li;
+        }
+      }
     }
   };
   // single logits, one per lane (first: warp 0 of the first CTA; last: the last warp of the last)
@@ -255,18 +277,38 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4_logprobs_kernel(const LpPara
     if (lane < count) v = V::one(x, from + lane);
     const float2 pair[1] = {make_float2(v, -INFINITY)};
     if (lane < count) add_values<1>(r, limit, pair, v);
-    if constexpr (kTop)
-      for (int j = 0; j < count; ++j) offer(__shfl_sync(0xffffffffu, v, j), from + j);
+    if constexpr (kTop) offer(v, from + lane);
   };
   if (rank == 0 && warp == 0 && head > 0) singles(0, head);
 
   const int step = p.cs * kLpThreads;
+  bool first = true;
   for (int c0 = rank * kLpThreads + warp * 32; c0 < chunks; c0 += kBatch * step) {
     uint4 w[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int c = c0 + b * step + lane;
       if (c < chunks) w[b] = ld_global_u4(body + (int64_t)c * 16);
+    }
+    if constexpr (kTop) {
+      if (first) {   // a bar for the first batch, where everything would beat the empty list: the k-th largest of
+                     // the lanes' maxima (k values at least reach it)
+        first = false;
+        float most = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (c0 + b * step + lane < chunks) {
+            float2 v[V::n / 2];
+            V::unpack(w[b], v);
+#pragma unroll
+            for (int i = 0; i < V::n / 2; ++i) most = fmaxf(most, fmaxf(v[i].x, v[i].y));
+          }
+        const uint32_t bar = kth_key(order_key(most), p.k, lane);
+        if (bar != 0 && last == -INFINITY) {
+          last = __uint_as_float(bar & 0x80000000u ? bar & 0x7fffffffu : ~bar);
+          last_id = 0x7fffffff;   // (its equals go in)
+        }
+      }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
@@ -281,15 +323,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4_logprobs_kernel(const LpPara
         add_values<V::n / 2>(r, limit, v, vm);
       }
       if constexpr (kTop) {
-        uint32_t some = __ballot_sync(0xffffffffu, vm > last);
-        while (some) {
-          const int from = __ffs(some) - 1;
-          some &= some - 1;
-          const int id = head + (c0 + b * step + from) * V::n;
+        if (__any_sync(0xffffffffu, vm >= last && vm > -INFINITY)) {
+          const int id = head + c * V::n;
+          const float none = -INFINITY;
 #pragma unroll
           for (int i = 0; i < V::n / 2; ++i) {
-            offer(__shfl_sync(0xffffffffu, v[i].x, from), id + 2 * i);
-            offer(__shfl_sync(0xffffffffu, v[i].y, from), id + 2 * i + 1);
+            offer(c < chunks ? v[i].x : none, id + 2 * i);
+            offer(c < chunks ? v[i].y : none, id + 2 * i + 1);
           }
         }
       }
@@ -310,33 +350,24 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4_logprobs_kernel(const LpPara
     q = warp_join(q);
     if (kTop)
       list = merge_lists(kLpWarps, p.k, lane, [&](int l, int i, float& v, int& id) { v = sh.lv[l][i]; id = sh.li[l][i]; });
-    if (p.cs > 1) {
-      if (lane == 0) sh.cta = q;
-      sh.cv[lane] = list.v;
-      sh.ci[lane] = list.id;
-    }
     r = q;
   }
   if (p.cs > 1) {
-    cluster_sync();
-    if (rank == 0 && warp == 0) {
-      Sums q{0.f, 0.f, 0.f, -INFINITY};
-      if (lane < p.cs) {
-        const uint32_t at = mapa_shared(smem_u32(&sh.cta), (uint32_t)lane);
-        q.m = __uint_as_float(ld_cluster_u32(at));
-        q.s = __uint_as_float(ld_cluster_u32(at + 4));
-        q.a = __uint_as_float(ld_cluster_u32(at + 8));
-        q.top = __uint_as_float(ld_cluster_u32(at + 12));
+    cluster_wait();   // the cluster's first CTA is there
+    if (warp == 0) {
+      if (lane == 0)
+        st_cluster_v4(mapa_shared(smem_u32(&sh.cta[rank]), 0), r.m, r.s, r.a, r.top);
+      if (kTop) {
+        st_cluster_u32(mapa_shared(smem_u32(&sh.cv[rank][lane]), 0), __float_as_uint(list.v));
+        st_cluster_u32(mapa_shared(smem_u32(&sh.ci[rank][lane]), 0), (uint32_t)list.id);
       }
-      r = warp_join(q);
-      if (kTop)
-        list = merge_lists(p.cs, p.k, lane, [&](int l, int i, float& v, int& id) {
-          v = __uint_as_float(ld_cluster_u32(mapa_shared(smem_u32(&sh.cv[i]), (uint32_t)l)));
-          id = (int)ld_cluster_u32(mapa_shared(smem_u32(&sh.ci[i]), (uint32_t)l));
-        });
     }
-    cluster_sync();   // no CTA leaves while its shared memory is read
+    cluster_sync();
     if (rank != 0) return;
+    if (warp == 0) {
+      r = warp_join(lane < p.cs ? sh.cta[lane] : Sums{0.f, 0.f, 0.f, -INFINITY});
+      if (kTop) list = merge_lists(p.cs, p.k, lane, [&](int l, int i, float& v, int& id) { v = sh.cv[l][i]; id = sh.ci[l][i]; });
+    }
   }
   if (warp == 0) {
     // r.s NaN: a logit was NaN; none above -inf: no distribution
@@ -387,7 +418,7 @@ int logprobs_launch(const LogprobArgs& a) {
   LpParams p{a.logits, a.ld, a.targets, a.logprobs, a.entropy, a.top_ids, a.top_logprobs, a.T, (int)a.V, (int)a.n, a.k, 1};
   // CTAs per row: as many as keep all rows' on the GPU at once, each with two batches of chunks at least
   const int64_t chunks = a.V * (a.fp32 ? 4 : 2) / 16;
-  while (p.cs < 8 && a.T * p.cs * 2 <= 304 && chunks >= (int64_t)p.cs * 2 * kLpThreads * 2) p.cs *= 2;
+  while (p.cs < kMaxCluster && a.T * p.cs * 2 <= 304 && chunks >= (int64_t)p.cs * 2 * kLpThreads * 2) p.cs *= 2;
   const int64_t blocks = a.T * p.cs;
   if (blocks > 0x7fffffff) {
     set_error_detail("token_logprobs: too many rows for one launch");
