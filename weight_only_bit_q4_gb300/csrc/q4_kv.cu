@@ -239,9 +239,9 @@ int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, s
 // Bound: the bytes of the codes and scales, read once per 16 columns.
 //
 // Split: the pages of all sequences and heads in a row are cut into equal shares, whatever the
-// lengths are.  A share belongs to a group of warps of a CTA (one CTA per SM; a group per 8 columns:
-// its warps take the same pages, 8 columns each) with a ring of record copies and a running
-// (m, sum, O) of its own: no barrier joins the groups.  A (sequence, head) inside one share is
+// lengths are.  A share belongs to one warp of a CTA (one CTA per SM) with a ring of record copies and
+// a running (m, sum, O) of its own, 8 or 16 columns wide; for 17 to 32 columns to a group of two
+// warps that take the same pages.  No barrier joins the groups.  A (sequence, head) inside one share is
 // finished there, others leave FP32 partial sums (at most two per share) that a second kernel
 // joins in order.
 struct KvParams {
@@ -251,15 +251,23 @@ struct KvParams {
   const uint8_t* cache;
   const int32_t* table;
   const int32_t* len;
-  float* part;              // [shares][2][kTiles][part_floats]
+  float* part;              // [shares][2][tiles][part_floats]
   int64_t P;
-  int S, M, n, G, Hk, cols, passes;   // columns of a head (n * G) and passes of 8 kTiles over them
+  int S, M, n, G, Hk, cols, passes;   // columns of a head (n * G) and passes over them
   float c;                  // scale * log2 e
 };
 
-constexpr int kKvWarps = 12;
-constexpr int kKvThreads = 32 * kKvWarps;
-constexpr int kKvRecords = 24;    // records in shared memory: 2 per warp, so 2, 4 or 8 per ring
+constexpr int kKvRecords = 24;    // records in shared memory, over all rings
+
+// A warp takes NT tiles of 8 columns (its codes are decoded once for all of them); kGroup warps share
+// a ring and its pages.
+template <int NT, int kGroup>
+struct KvShape {
+  static constexpr int warps = NT == 1 ? 12 : 8;   // (the registers of two tiles' states leave no more)
+  static constexpr int threads = 32 * warps;
+  static constexpr int rings = warps / kGroup, stages = kKvRecords / rings;
+  static constexpr int tiles = NT * kGroup;        // tiles of a pass
+};
 
 __host__ __device__ constexpr int part_floats(int D) { return 8 * (D + 2); }
 
@@ -361,6 +369,14 @@ __device__ __forceinline__ float kv_ex2(float t) {
   return e;
 }
 
+__device__ __forceinline__ float2 kv_fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -373,104 +389,111 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // A warp's running state over the pages of a segment.
-template <int J>
+template <int J, int NT>
 struct KvState {
   static constexpr int D = 32 * J, G = kv_groups(D);
-  float o[2 * J][4];        // 2^-24 sum q P s; rows of odd values 16 times that
-  float z[G][4];            // the same with q = 8 everywhere
-  float mm[2], l[2];        // the columns' references, and this thread's tokens' sum of 2^(x - mm)
+  float o[2 * J][NT][4];        // 2^-24 sum q P s; rows of odd values 16 times that
+  float z[G][NT][4];        // the same with q = 8 everywhere
+  float mm[NT][2], l[NT][2];   // the columns' references, and this thread's tokens' sum of 2^(x - mm)
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 2 * J; ++i)
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+      for (int i = 0; i < 2 * J; ++i)
 #pragma unroll
-    for (int i = 0; i < G; ++i)
+        for (int e = 0; e < 4; ++e) o[i][t][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[i][e] = 0.f;
-    mm[0] = mm[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[i][t][e] = 0.f;
+      mm[t][0] = mm[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
   }
-  __device__ __forceinline__ void scale(float f0, float f1) {
+  __device__ __forceinline__ void scale(int t, float f0, float f1) {
 #pragma unroll
     for (int i = 0; i < 2 * J; ++i) {
-      o[i][0] *= f0; o[i][1] *= f1; o[i][2] *= f0; o[i][3] *= f1;
+      o[i][t][0] *= f0; o[i][t][1] *= f1; o[i][t][2] *= f0; o[i][t][3] *= f1;
     }
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      z[i][0] *= f0; z[i][1] *= f1; z[i][2] *= f0; z[i][3] *= f1;
+      z[i][t][0] *= f0; z[i][t][1] *= f1; z[i][t][2] *= f0; z[i][t][3] *= f1;
     }
-    l[0] *= f0;
-    l[1] *= f1;
+    l[t][0] *= f0;
+    l[t][1] *= f1;
   }
 };
 
-// A tile of 8 query columns as B fragments, and the scores' factors.
-template <int J>
+// A warp's query columns as B fragments, and the scores' factors.
+template <int J, int NT>
 struct KvQuery {
   static constexpr int G = kv_groups(32 * J);
-  uint32_t b[J][4];         // b0, b1 of the word's two k-steps
-  float f[2], z[G][2];
-  int seen[2];              // tokens that columns 2c and 2c + 1 see (columns that are not there: none)
+  uint32_t b[NT][J][4];     // b0, b1 of the word's two k-steps
+  float f[NT][2], z[NT][G][2];
+  int seen[NT][2];            // tokens that columns 2c and 2c + 1 see (columns that are not there: none)
 
   __device__ __forceinline__ void load(const KvParams& p, int s, int L, int h, int col0, int lane) {
-    const int g = lane >> 2, c = lane & 3, col = col0 + g;
-    uint4 w[J];
+    const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int j = 0; j < J; ++j) w[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (col < p.cols) {
-      const int i = col / p.G;
-      const uint16_t* row = p.q + ((int64_t)s * p.n + i) * p.ldq + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
+    for (int t = 0; t < NT; ++t) {
+      const int col = col0 + 8 * t + g;
+      uint4 w[J];
 #pragma unroll
-      for (int j = 0; j < J; ++j) w[j] = ld_global_u4(row + 8 * (4 * j + c));
-    }
-    uint32_t top = 0;
+      for (int j = 0; j < J; ++j) w[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (col < p.cols) {
+        const int i = col / p.G;
+        const uint16_t* row = p.q + ((int64_t)s * p.n + i) * p.ldq + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu),
-                                   __vmaxu2(w[j].z & 0x7FFF7FFFu, w[j].w & 0x7FFF7FFFu)));
-    top = max(top & 0xFFFFu, top >> 16);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^-e puts the largest value (exponent field top >> 7) in [2^14, 2^15)
-    const int e = min(max((int)(top >> 7), 1), 254) - 127 - 14;
-    const int d1 = min(-e, 127);
-    const float down = exp2i(d1), down2 = exp2i(-e - d1);
-    float zg[G];
-#pragma unroll
-    for (int i = 0; i < G; ++i) zg[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-      float x[8], sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] = (i & 1 ? bf16hi(ws[i >> 1]) : bf16lo(ws[i >> 1]));
-        sum += x[i];
-        x[i] = x[i] * down * down2;
+        for (int j = 0; j < J; ++j) w[j] = ld_global_u4(row + 8 * (4 * j + c));
       }
-      zg[j >> 1] += sum;
-      b[j][0] = pack_f16(x[0], x[4]);
-      b[j][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
-      b[j][2] = pack_f16(x[2], x[6]);
-      b[j][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
-    }
-    // (2^(24 + e) may pass FP32's range only where the scores do)
-    const float fc = exp2i(min(24 + e, 127)) * p.c;
+      uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 1);
-      zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 2);
-      zg[i] *= -8.f * p.c;
-    }
+      for (int j = 0; j < J; ++j)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[j].x & 0x7FFF7FFFu, w[j].y & 0x7FFF7FFFu),
+                                     __vmaxu2(w[j].z & 0x7FFF7FFFu, w[j].w & 0x7FFF7FFFu)));
+      top = max(top & 0xFFFFu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^-e puts the largest value (exponent field top >> 7) in [2^14, 2^15)
+      const int e = min(max((int)(top >> 7), 1), 254) - 127 - 14;
+      const int d1 = min(-e, 127);
+      const float down = exp2i(d1), down2 = exp2i(-e - d1);
+      float zg[G];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int from = 4 * (2 * c + k);   // a lane of column 2c + k
-      f[k] = __shfl_sync(0xffffffffu, fc, from);
+      for (int i = 0; i < G; ++i) zg[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < G; ++i) z[i][k] = __shfl_sync(0xffffffffu, zg[i], from);
-      const int mine = col0 + 2 * c + k;
-      seen[k] = mine < p.cols ? L - p.n + 1 + mine / p.G : 0;
+      for (int j = 0; j < J; ++j) {
+        const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        float x[8], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = (i & 1 ? bf16hi(ws[i >> 1]) : bf16lo(ws[i >> 1]));
+          sum += x[i];
+          x[i] = x[i] * down * down2;
+        }
+        zg[j >> 1] += sum;
+        b[t][j][0] = pack_f16(x[0], x[4]);
+        b[t][j][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
+        b[t][j][2] = pack_f16(x[2], x[6]);
+        b[t][j][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
+      }
+      // (2^(24 + e) may pass FP32's range only where the scores do)
+      const float fc = exp2i(min(24 + e, 127)) * p.c;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 1);
+        zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 2);
+        zg[i] *= -8.f * p.c;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int from = 4 * (2 * c + k);   // a lane of column 2c + k
+        f[t][k] = __shfl_sync(0xffffffffu, fc, from);
+#pragma unroll
+        for (int i = 0; i < G; ++i) z[t][i][k] = __shfl_sync(0xffffffffu, zg[i], from);
+        const int mine = col0 + 8 * t + 2 * c + k;
+        seen[t][k] = mine < p.cols ? L - p.n + 1 + mine / p.G : 0;
+      }
     }
   }
 };
@@ -492,22 +515,31 @@ __device__ __forceinline__ void kv_scales(uint32_t at, float (&v)[G]) {
 }
 
 // One page (64 tokens from token0 on) joins the warp's state; kEnd: not every column sees all of it.
-template <int J, bool kEnd>
-__device__ __forceinline__ void kv_page(KvState<J>& st, const KvQuery<J>& qy, uint32_t rec, int token0, int lane) {
+template <int J, int NT, bool kEnd>
+__device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>& qy, uint32_t rec, int token0, int lane) {
   constexpr int D = 32 * J, G = kv_groups(D);
   constexpr uint32_t M0 = 0x000F000Fu, M1 = 0x00F000F0u;
   const int g = lane >> 2, c = lane & 3;
   const uint32_t kbase = rec + (uint32_t)(g * (D / 2) + c * J * 4), sbase = rec + 64u * D + (uint32_t)(g * 2 * G);
-  float x[4][4];
+  float x[4][NT][4];
   float vs[4][2][G];   // V scales of this thread's tokens
   float vtop = 0.f;
+  int any = 0;         // tokens that some column sees
+  if (kEnd) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) any = max(any, max(qy.seen[t][0], qy.seen[t][1]));
+    any = max(any, __shfl_xor_sync(0xffffffffu, any, 1));
+    any = max(any, __shfl_xor_sync(0xffffffffu, any, 2));
+  }
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
-    float d[G][4];
+    float d[G][NT][4];
 #pragma unroll
     for (int i = 0; i < G; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[i][t][e] = 0.f;
     uint32_t w[2][J];
     float ks[2][G];
 #pragma unroll
@@ -529,86 +561,108 @@ __device__ __forceinline__ void kv_page(KvState<J>& st, const KvQuery<J>& qy, ui
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const uint32_t h0 = w[0][j] >> 8, h1 = w[1][j] >> 8;
-      mma_16816(d[j >> 1], w[0][j] & M0, w[1][j] & M0, w[0][j] & M1, w[1][j] & M1, qy.b[j][0], qy.b[j][1]);
-      mma_16816(d[j >> 1], h0 & M0, h1 & M0, h0 & M1, h1 & M1, qy.b[j][2], qy.b[j][3]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma_16816(d[j >> 1][t], w[0][j] & M0, w[1][j] & M0, w[0][j] & M1, w[1][j] & M1, qy.b[t][j][0], qy.b[t][j][1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma_16816(d[j >> 1][t], h0 & M0, h1 & M0, h0 & M1, h1 & M1, qy.b[t][j][2], qy.b[t][j][3]);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float s = 0.f;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < G; ++i) s = fmaf(ks[e >> 1][i], fmaf(qy.f[e & 1], d[i][e], qy.z[i][e & 1]), s);
-      if (kEnd && token0 + 16 * mt + g + 8 * (e >> 1) >= qy.seen[e & 1]) s = -INFINITY;
-      x[mt][e] = s;
-    }
+      for (int r = 0; r < 2; ++r) {   // (columns 2c and 2c + 1 of a token together)
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          s = ffma2(make_float2(ks[r][i], ks[r][i]),
+                    ffma2(make_float2(qy.f[t][0], qy.f[t][1]), make_float2(d[i][t][2 * r], d[i][t][2 * r + 1]),
+                          make_float2(qy.z[t][i][0], qy.z[t][i][1])), s);
+        if (kEnd) {
+          const int token = token0 + 16 * mt + g + 8 * r;
+          if (token >= qy.seen[t][0]) s.x = -INFINITY;
+          if (token >= qy.seen[t][1]) s.y = -INFINITY;
+        }
+        x[mt][t][2 * r] = s.x;
+        x[mt][t][2 * r + 1] = s.y;
+      }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       // tokens that no column sees: whatever their scales hold, they are left out
-      if (kEnd) {
-        int any = max(qy.seen[0], qy.seen[1]);
-        any = max(any, __shfl_xor_sync(0xffffffffu, any, 1));
-        any = max(any, __shfl_xor_sync(0xffffffffu, any, 2));
-        if (token0 + 16 * mt + g + 8 * r >= any)
+      if (kEnd && token0 + 16 * mt + g + 8 * r >= any)
 #pragma unroll
-          for (int i = 0; i < G; ++i) vs[mt][r][i] = 0.f;
-      }
+        for (int i = 0; i < G; ++i) vs[mt][r][i] = 0.f;
 #pragma unroll
       for (int i = 0; i < G; ++i) vtop = fmaxf(vtop, fabsf(vs[mt][r][i]));
     }
   }
-  float top[2];
+  float top[NT][2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    top[k] = fmaxf(fmaxf(fmaxf(x[0][k], x[0][2 + k]), fmaxf(x[1][k], x[1][2 + k])),
-                   fmaxf(fmaxf(x[2][k], x[2][2 + k]), fmaxf(x[3][k], x[3][2 + k])));
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      top[t][k] = fmaxf(fmaxf(fmaxf(x[0][t][k], x[0][t][2 + k]), fmaxf(x[1][t][k], x[1][t][2 + k])),
+                        fmaxf(fmaxf(x[2][t][k], x[2][t][2 + k]), fmaxf(x[3][t][k], x[3][t][2 + k])));
 #pragma unroll
   for (int o = 4; o <= 16; o <<= 1) {
     vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-    top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
-    top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) top[t][k] = fmaxf(top[t][k], __shfl_xor_sync(0xffffffffu, top[t][k], o));
   }
   // the page's largest V scale is below 2^ve
   const float ve = (float)(max((int)(__float_as_uint(vtop) >> 23), 127 - 25) - 126);
-  top[0] += ve - 14.f;
-  top[1] += ve - 14.f;
-  if (__any_sync(0xffffffffu, top[0] > st.mm[0] + 1.f || top[1] > st.mm[1] + 1.f)) {
-    float f[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float m = fmaxf(st.mm[k], top[k]);
-      f[k] = st.mm[k] == m ? 1.f : kv_ex2(st.mm[k] - m);
-      st.mm[k] = m;
+  for (int t = 0; t < NT; ++t) {
+    top[t][0] += ve - 14.f;
+    top[t][1] += ve - 14.f;
+    if (__any_sync(0xffffffffu, top[t][0] > st.mm[t][0] + 1.f || top[t][1] > st.mm[t][1] + 1.f)) {
+      float f[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float m = fmaxf(st.mm[t][k], top[t][k]);
+        f[k] = st.mm[t][k] == m ? 1.f : kv_ex2(st.mm[t][k] - m);
+        st.mm[t][k] = m;
+      }
+      st.scale(t, f[0], f[1]);
     }
-    st.scale(f[0], f[1]);
   }
-  // P s as B fragments: [k-step][scale group]
-  uint32_t pb[4][G][2];
-  // (a column that has seen nothing yet: its x are -inf, its P 0)
-  const float m0 = st.mm[0] == -INFINITY ? 0.f : st.mm[0], m1 = st.mm[1] == -INFINITY ? 0.f : st.mm[1];
+  // P s as B fragments: [k-step][scale group][tile]
+  uint32_t pb[4][G][NT][2];
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) {
-    float pr[4];
+  for (int t = 0; t < NT; ++t) {
+    // (a column that has seen nothing yet: its x are -inf, its P 0)
+    const float2 m = make_float2(st.mm[t][0] == -INFINITY ? 0.f : -st.mm[t][0], st.mm[t][1] == -INFINITY ? 0.f : -st.mm[t][1]);
+    float2 l = make_float2(st.l[t][0], st.l[t][1]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) pr[e] = kv_ex2(x[mt][e] - (e & 1 ? m1 : m0));
-    st.l[0] += pr[0] + pr[2];
-    st.l[1] += pr[1] + pr[3];
-#pragma unroll
-    for (int i = 0; i < G; ++i)
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float a = pr[2 * r] * vs[mt][r][i], b = pr[2 * r + 1] * vs[mt][r][i];
-        if (kEnd) {   // a scale that is not finite stays with the columns that see its token
-          if (x[mt][2 * r] == -INFINITY) a = 0.f;
-          if (x[mt][2 * r + 1] == -INFINITY) b = 0.f;
+        const float2 e = fadd2(make_float2(x[mt][t][2 * r], x[mt][t][2 * r + 1]), m);
+        const float2 pr = make_float2(kv_ex2(e.x), kv_ex2(e.y));
+        l = fadd2(l, pr);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          float2 ps = kv_fmul2(pr, make_float2(vs[mt][r][i], vs[mt][r][i]));
+          if (kEnd) {   // a scale that is not finite stays with the columns that see its token
+            if (x[mt][t][2 * r] == -INFINITY) ps.x = 0.f;
+            if (x[mt][t][2 * r + 1] == -INFINITY) ps.y = 0.f;
+          }
+          pb[mt][i][t][r] = movmatrix(pack_f16(ps.x, ps.y));
         }
-        pb[mt][i][r] = movmatrix(pack_f16(a, b));
       }
+    st.l[t][0] = l.x;
+    st.l[t][1] = l.y;
   }
   const uint32_t vbase = rec + 32u * D + (uint32_t)(g * kPage + 16 * c);
 #pragma unroll
   for (int i = 0; i < G; ++i)
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      mma_16816(st.z[i], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, pb[s][i][0], pb[s][i][1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma_16816(st.z[i][t], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, pb[s][i][t][0], pb[s][i][t][1]);
 #pragma unroll
   for (int md = 0; md < 2 * J; ++md) {
     const uint4 v = ld_shared_v4(vbase + (uint32_t)(md * 8 * kPage));
@@ -616,61 +670,71 @@ __device__ __forceinline__ void kv_page(KvState<J>& st, const KvQuery<J>& qy, ui
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const uint32_t h = ws[s] >> 8;
-      mma_16816(st.o[md], ws[s] & M0, ws[s] & M1, h & M0, h & M1, pb[s][md >> 2][0], pb[s][md >> 2][1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma_16816(st.o[md][t], ws[s] & M0, ws[s] & M1, h & M0, h & M1, pb[s][md >> 2][t][0], pb[s][md >> 2][t][1]);
     }
   }
 }
 
 // The state's columns in FP32: o in true units times 2^-mm, l over all tokens.
-template <int J>
-__device__ __forceinline__ void kv_finish_state(KvState<J>& st) {
+template <int J, int NT>
+__device__ __forceinline__ void kv_finish_state(KvState<J, NT>& st) {
   constexpr float up = 16777216.f;   // 2^24
 #pragma unroll
-  for (int md = 0; md < 2 * J; ++md)
+  for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) st.o[md][e] = (st.o[md][e] - st.z[md >> 2][e]) * (e < 2 ? up : up / 16.f);
+    for (int md = 0; md < 2 * J; ++md)
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+      for (int e = 0; e < 4; ++e) st.o[md][t][e] = (st.o[md][t][e] - st.z[md >> 2][t][e]) * (e < 2 ? up : up / 16.f);
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], o);
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) st.l[t][k] += __shfl_xor_sync(0xffffffffu, st.l[t][k], o);
+  }
 }
 
-// They as [8][D] values, then the references, then the sums.
-template <int J>
-__device__ __forceinline__ void kv_put(float* dst, const KvState<J>& st, int lane) {
+// They as tiles of [8][D] values, then the references, then the sums.
+template <int J, int NT>
+__device__ __forceinline__ void kv_put(float* dst, const KvState<J, NT>& st, int lane) {
   constexpr int D = 32 * J;
   const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int t = 0; t < NT; ++t, dst += part_floats(D)) {
 #pragma unroll
-    for (int md = 0; md < 2 * J; ++md)
-      *reinterpret_cast<float2*>(dst + (2 * c + k) * D + 16 * md + 2 * g) = make_float2(st.o[md][k], st.o[md][2 + k]);
-  if (g == 0)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      dst[8 * D + 2 * c + k] = st.mm[k];
-      dst[8 * (D + 1) + 2 * c + k] = st.l[k];
-    }
+      for (int md = 0; md < 2 * J; ++md)
+        *reinterpret_cast<float2*>(dst + (2 * c + k) * D + 16 * md + 2 * g) = make_float2(st.o[md][t][k], st.o[md][t][2 + k]);
+    if (g == 0)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        dst[8 * D + 2 * c + k] = st.mm[t][k];
+        dst[8 * (D + 1) + 2 * c + k] = st.l[t][k];
+      }
+  }
 }
 
 // The finished columns as bf16 rows; a column that saw no token gives zeros.
-template <int J>
-__device__ __forceinline__ void kv_write(const KvParams& p, int s, int h, int col0, const KvState<J>& st, int lane) {
+template <int J, int NT>
+__device__ __forceinline__ void kv_write(const KvParams& p, int s, int h, int col0, const KvState<J, NT>& st, int lane) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int col = col0 + 2 * (lane & 3) + k;
-    if (col >= p.cols) continue;
-    const int i = col / p.G;
-    const bool empty = st.mm[k] == -INFINITY && st.l[k] == 0.f;
-    const float r = 1.f / st.l[k];
-    uint16_t* row = p.out + ((int64_t)s * p.n + i) * p.ldo + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int md = 0; md < 2 * J; ++md) {
-      const float a = empty ? 0.f : st.o[md][k] * r, b = empty ? 0.f : st.o[md][2 + k] * r;
-      *reinterpret_cast<uint32_t*>(row + 16 * md + 2 * (lane >> 2)) =
-          (uint32_t)float_to_bf16_bits(a) | (uint32_t)float_to_bf16_bits(b) << 16;
+    for (int k = 0; k < 2; ++k) {
+      const int col = col0 + 8 * t + 2 * (lane & 3) + k;
+      if (col >= p.cols) continue;
+      const int i = col / p.G;
+      const bool empty = st.mm[t][k] == -INFINITY && st.l[t][k] == 0.f;
+      const float r = 1.f / st.l[t][k];
+      uint16_t* row = p.out + ((int64_t)s * p.n + i) * p.ldo + (int64_t)(h * p.G + col - i * p.G) * (32 * J);
+#pragma unroll
+      for (int md = 0; md < 2 * J; ++md) {
+        const float a = empty ? 0.f : st.o[md][t][k] * r, b = empty ? 0.f : st.o[md][t][2 + k] * r;
+        *reinterpret_cast<uint32_t*>(row + 16 * md + 2 * (lane >> 2)) =
+            (uint32_t)float_to_bf16_bits(a) | (uint32_t)float_to_bf16_bits(b) << 16;
+      }
     }
-  }
 }
 
 template <int J>
@@ -680,20 +744,21 @@ struct KvSmem {
   static constexpr int alloc = bars + kKvRecords * 16;
 };
 
-template <int J, int kTiles>
-__global__ void __launch_bounds__(kKvThreads, 1) q4_kv_attention_kernel(const KvParams p) {
+template <int J, int NT, int kGroup>
+__global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attention_kernel(const KvParams p) {
   using SM = KvSmem<J>;
-  constexpr int kRings = kKvWarps / kTiles, kStages = kKvRecords / kRings;
+  using Shape = KvShape<NT, kGroup>;
+  constexpr int kKvThreads = Shape::threads, kRings = Shape::rings, kStages = Shape::stages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int ends[kKvThreads], sums[kKvWarps];
+  __shared__ int ends[kKvThreads], sums[Shape::warps];
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp / kTiles, tile = warp % kTiles;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp / kGroup, member = warp % kGroup;
   const uint32_t base = smem_u32(smem);
   const uint32_t ring = base + (uint32_t)(group * kStages * SM::rec), bars = base + SM::bars + 16u * (uint32_t)(group * kStages);
   pdl_launch_dependents();
   if (tid < kKvRecords) {
     mbar_init(base + SM::bars + 16u * tid, 1);
-    mbar_init(base + SM::bars + 16u * tid + 8, kTiles);
+    mbar_init(base + SM::bars + 16u * tid + 8, kGroup);
   }
   if (tid == 0) abort_flag = 0;
   fence_mbar_init();
@@ -723,7 +788,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) q4_kv_attention_kernel(const Kv
     const int st = filled % kStages;
     const bool good = page >= 0 && page < p.P;   // a page that is not there: its tokens are left out
     there = good ? there | 1u << st : there & ~(1u << st);
-    if (good && tile == 0 && lane == 0) {
+    if (good && member == 0 && lane == 0) {
       const uint32_t bar = bars + 16u * (uint32_t)st;
       mbar_expect_tx(bar, SM::rec);
       bulk_load(ring + (uint32_t)(st * SM::rec), p.cache + ((int64_t)page * p.Hk + ahead.seg / p.passes) * SM::rec, SM::rec, bar);
@@ -736,13 +801,13 @@ __global__ void __launch_bounds__(kKvThreads, 1) q4_kv_attention_kernel(const Kv
   look();
   for (int i = 0; i < kStages; ++i) issue();
 
-  KvState<J> st;
-  KvQuery<J> qy;
+  KvState<J, NT> st;
+  KvQuery<J, NT> qy;
   uint32_t phases = 0;      // per stage: the parity of its next copy
   for (int u = u0; u < u1 && ok;) {
     here.seek(p, u);
     const int end = min(here.seg0 + here.pages, u1);   // this share's units of the segment
-    const int h = here.seg / p.passes, col0 = ((here.seg - h * p.passes) * kTiles + tile) * 8;
+    const int h = here.seg / p.passes, col0 = ((here.seg - h * p.passes) * kGroup + member) * 8 * NT;
     const bool whole = end - u == here.pages;
     st.clear();
     qy.load(p, here.s, here.L, h, col0, lane);
@@ -755,11 +820,11 @@ __global__ void __launch_bounds__(kKvThreads, 1) q4_kv_attention_kernel(const Kv
         const int token0 = (u - here.seg0) * kPage;
         // (the last n - 1 tokens are seen by some columns only)
         if (token0 + kPage <= here.L - p.n + 1)
-          kv_page<J, false>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
+          kv_page<J, NT, false>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
         else
-          kv_page<J, true>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
+          kv_page<J, NT, true>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
       }
-      if constexpr (kTiles == 1) {
+      if constexpr (kGroup == 1) {
         ++used;
         __threadfence_block();
         __syncwarp();
@@ -770,7 +835,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) q4_kv_attention_kernel(const Kv
         const int b = used - 1;
         ++used;
         if (b >= 0) {
-          if (tile == 0 && next < u1) {
+          if (member == 0 && next < u1) {
             ok = warp_wait_vote(bars + 16u * (uint32_t)(b % kStages) + 8, (uint32_t)(b / kStages) & 1u, &abort_flag, &g_kv_status);
             if (!ok) break;
           }
@@ -785,65 +850,105 @@ __global__ void __launch_bounds__(kKvThreads, 1) q4_kv_attention_kernel(const Kv
     } else {
       // (a share's first segment may have begun in an earlier share, its last may go on: slots 0 and 1)
       const int slot = here.seg0 > u0 ? 1 : 0;
-      kv_put(p.part + (((int64_t)share * 2 + slot) * kTiles + tile) * part_floats(32 * J), st, lane);
+      kv_put(p.part + (((int64_t)share * 2 + slot) * kGroup + member) * NT * part_floats(32 * J), st, lane);
     }
   }
   // nothing is left in flight, after a wait that ran out either
-  if (!ok && tile == 0 && lane == 0)
+  if (!ok && member == 0 && lane == 0)
     for (int i = used; i < filled; ++i)
       if (there >> (i % kStages) & 1u) mbar_drain(bars + 16u * (uint32_t)(i % kStages), phases >> (i % kStages) & 1u);
 }
 
-// Segments that lie in several shares, and sequences without tokens.
+// Segments that lie in several shares, and sequences without tokens.  D / 2 threads hold a column, two
+// values each.  kSplit: a CTA takes one column, its groups of threads the partial sums in turn (few
+// long segments); otherwise a CTA takes a segment, its groups the columns (many short ones: a CTA
+// per column would be more of them than the GPU holds at once, each with a scan of the lengths).
 constexpr int kKvJoin = 256;
-template <int J, int kTiles>
+template <int J, int kTiles, bool kSplit>
 __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p, int most) {
-  constexpr int D = 32 * J;
+  constexpr int D = 32 * J, kLanes = kKvJoin / (D / 2);
   __shared__ int ends[kKvJoin], sums[kKvJoin / 32];
   pdl_launch_dependents();
   pdl_wait_previous();
-  const int per = p.Hk * p.passes, s = blockIdx.x / per, seg = blockIdx.x - s * per;
+  const int tid = threadIdx.x, per = p.Hk * p.passes, s = blockIdx.x / per, seg = blockIdx.x - s * per;
+  const int h = seg / p.passes, pass = seg - h * p.passes, cols = min(8 * kTiles, p.cols - pass * 8 * kTiles);
+  if ((int)blockIdx.y >= cols) return;   // (a narrower last pass)
   const int total = kv_scan<kKvJoin>(p, ends, sums);
   const int shares = kv_shares_used(total, most);
   const int run = (p.S + kKvJoin - 1) / kKvJoin, t = s / run;
   int L, a = t > 0 ? ends[t - 1] : 0;
   for (int i = t * run; i < s; ++i) a += kv_pages(p, i, L) * per;
   const int pages = kv_pages(p, s, L);
-  const int h = seg / p.passes, pass = seg - h * p.passes;
   a += seg * pages;
-  int c0 = 0, c1 = -1;
+  int c0 = 0, n = 0;   // the shares of the segment
   if (pages > 0) {
-    // the shares of the segment's first and last unit
     c0 = (int)((((int64_t)a + 1) * shares - 1) / total);
-    c1 = (int)(((int64_t)(a + pages) * shares - 1) / total);
-    if (c0 == c1) return;   // finished by its share
+    n = (int)(((int64_t)(a + pages) * shares - 1) / total) - c0 + 1;
+    if (n == 1) return;   // finished by its share
   }
-  for (int e = threadIdx.x; e < 8 * kTiles * (D / 2); e += kKvJoin) {
-    const int local = e / (D / 2), d = 2 * (e - local * (D / 2)), col = pass * 8 * kTiles + local;
-    if (col >= p.cols) break;
-    // a share's slot: 1 only where the segment begins inside it, behind another (that is its first share's case)
-    const int64_t pitch = (int64_t)2 * kTiles * part_floats(D);
-    const float* part = p.part + (local >> 3) * part_floats(D) + c0 * pitch;
-    const int64_t head = c1 >= c0 && a > kv_share_start(total, c0, shares) ? kTiles * part_floats(D) : 0;
-    const int col8 = local & 7;
-    float m = -INFINITY;
+  // a share's slot: 1 only where the segment begins inside it, behind another (that is its first share's case)
+  const int64_t pitch = (int64_t)2 * kTiles * part_floats(D);
+  const int64_t head = n > 0 && a > kv_share_start(total, c0, shares) ? kTiles * part_floats(D) : 0;
+  auto at = [&](int c, int local) {
+    return p.part + (c0 + c) * pitch + (c == 0 ? head : 0) + (local >> 3) * part_floats(D);
+  };
+  auto join = [&](int local, int d, int from, int step, float m, float2& o, float& l) {
+    const int v = (local & 7) * D + 2 * d, k = 8 * D + (local & 7);
 #pragma unroll 4
-    for (int c = 0; c <= c1 - c0; ++c) m = fmaxf(m, part[c * pitch + (c == 0 ? head : 0) + 8 * D + col8]);
-    float l = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll 4
-    for (int c = 0; c <= c1 - c0; ++c) {
-      const float* q = part + c * pitch + (c == 0 ? head : 0);
-      const float mc = q[8 * D + col8], f = mc == m ? 1.f : kv_ex2(mc - m);
-      const float2 v = *reinterpret_cast<const float2*>(q + col8 * D + d);
-      l += q[8 * (D + 1) + col8] * f;
-      o0 += v.x * f;
-      o1 += v.y * f;
+    for (int c = from; c < n; c += step) {
+      const float* q = at(c, local);
+      const float f = q[k] == m ? 1.f : kv_ex2(q[k] - m);
+      o = ffma2(*reinterpret_cast<const float2*>(q + v), make_float2(f, f), o);
+      l = fmaf(q[k + 8], f, l);
     }
-    const int i = col / p.G;
+  };
+  auto write = [&](int local, int d, float m, float2 o, float l) {
+    const int col = pass * 8 * kTiles + local, i = col / p.G;
     const bool empty = m == -INFINITY && l == 0.f;
     const float r = 1.f / l;
     uint16_t* row = p.out + ((int64_t)s * p.n + i) * p.ldo + (int64_t)(h * p.G + col - i * p.G) * D;
-    *reinterpret_cast<uint32_t*>(row + d) = empty ? 0u : (uint32_t)float_to_bf16_bits(o0 * r) | (uint32_t)float_to_bf16_bits(o1 * r) << 16;
+    *reinterpret_cast<uint32_t*>(row + 2 * d) =
+        empty ? 0u : (uint32_t)float_to_bf16_bits(o.x * r) | (uint32_t)float_to_bf16_bits(o.y * r) << 16;
+  };
+  const int lane = tid / (D / 2), d = tid - lane * (D / 2);
+  if constexpr (!kSplit) {
+    if (lane >= kLanes) return;
+    for (int local = lane; local < cols; local += kLanes) {
+      float m = -INFINITY, l = 0.f;
+      float2 o = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int c = 0; c < n; ++c) m = fmaxf(m, at(c, local)[8 * D + (local & 7)]);
+      join(local, d, 0, 1, m, o, l);
+      write(local, d, m, o, l);
+    }
+  } else {
+    __shared__ float2 red[kLanes][D / 2];
+    __shared__ float tops[kKvJoin / 32], ls[kLanes];
+    const int local = blockIdx.y;
+    float m = -INFINITY, l = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+    for (int c = tid; c < n; c += kKvJoin) m = fmaxf(m, at(c, local)[8 * D + (local & 7)]);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+    if ((tid & 31) == 0) tops[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kKvJoin / 32; ++w) m = fmaxf(m, tops[w]);
+    if (lane < kLanes) {
+      join(local, d, lane, kLanes, m, o, l);
+      red[lane][d] = o;
+      if (d == 0) ls[lane] = l;
+    }
+    __syncthreads();
+    if (tid >= D / 2) return;
+    l = 0.f;
+    o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) {
+      l += ls[i];
+      o = fadd2(o, red[i][tid]);
+    }
+    write(local, tid, m, o, l);
   }
 }
 
@@ -857,43 +962,48 @@ int kv_sms() {
   return sms;
 }
 
-template <int J, int kTiles>
+template <int J, int NT, int kGroup>
 int kv_attention_run(const KvParams& p, cudaStream_t stream) {
   using SM = KvSmem<J>;
   static bool set[64] = {};
   int dev = 0;
   if (cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return Q4LIN_ERR_CUDA;
   if (dev >= 64 || !set[dev]) {
-    if (cuda_check(cudaFuncSetAttribute(q4_kv_attention_kernel<J, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::alloc),
+    if (cuda_check(cudaFuncSetAttribute(q4_kv_attention_kernel<J, NT, kGroup>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::alloc),
                    "kv4_attention: cudaFuncSetAttribute(max dynamic shared memory)"))
       return Q4LIN_ERR_CUDA;
     if (dev < 64) set[dev] = true;
   }
   const int sms = kv_sms();
-  const int st = pdl_launch(q4_kv_attention_kernel<J, kTiles>, "kv4_attention: kernel launch", dim3((unsigned)sms, 1, 1), kKvThreads, SM::alloc, stream, &p);
+  const int st = pdl_launch(q4_kv_attention_kernel<J, NT, kGroup>, "kv4_attention: kernel launch", dim3((unsigned)sms, 1, 1), KvShape<NT, kGroup>::threads, SM::alloc, stream, &p);
   if (st != Q4LIN_OK) return st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.S * p.Hk * p.passes), 1, 1);
+  const int64_t segments = (int64_t)p.S * p.Hk * p.passes;
+  const int cols = p.cols < 8 * NT * kGroup ? p.cols : 8 * NT * kGroup;
+  const bool split = segments * cols <= 8 * sms;   // (CTAs of 256 threads that the GPU holds at once)
+  cfg.gridDim = dim3((unsigned)segments, (unsigned)(split ? cols : 1), 1);
   cfg.blockDim = dim3(kKvJoin, 1, 1);
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, q4_kv_combine_kernel<J, kTiles>, p, sms * (kKvWarps / kTiles)), "kv4_attention: combine launch");
+  const int shares = sms * KvShape<NT, kGroup>::rings;
+  return cuda_check(split ? cudaLaunchKernelEx(&cfg, q4_kv_combine_kernel<J, NT * kGroup, true>, p, shares)
+                          : cudaLaunchKernelEx(&cfg, q4_kv_combine_kernel<J, NT * kGroup, false>, p, shares),
+                    "kv4_attention: combine launch");
 }
 
-// Tiles of 8 columns that share a record: all of them up to four (24 columns take a group of four, one
-// warp of it idle).
+// Tiles of a pass, 8 columns each: one warp with one or two, or two warps with two each.
 int kv_tiles(int64_t cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
 }  // namespace
 
 int64_t kv_page_bytes(int64_t D) { return kv_record((int)D); }
 
-// Two partial sums per share and tile: kKvWarps tiles per SM, however they are grouped.
-int64_t kv_workspace_bytes(int64_t D) { return (int64_t)kv_sms() * kKvWarps * 2 * part_floats((int)D) * 4; }
+// Two partial sums per share and tile: 12 or 16 tiles per SM.
+int64_t kv_workspace_bytes(int64_t D) { return (int64_t)kv_sms() * 16 * 2 * part_floats((int)D) * 4; }
 
 int64_t kv_passes(int64_t cols) { return (cols + 8 * kv_tiles(cols) - 1) / (8 * kv_tiles(cols)); }
 
@@ -939,7 +1049,9 @@ int kv_attention_launch(const KvAttnArgs& a) {
   const int tiles = kv_tiles(p.cols);
   auto pick = [&](auto j) {
     constexpr int J = decltype(j)::value;
-    return tiles == 1 ? kv_attention_run<J, 1>(p, a.stream) : tiles == 2 ? kv_attention_run<J, 2>(p, a.stream) : kv_attention_run<J, 4>(p, a.stream);
+    return tiles == 1   ? kv_attention_run<J, 1, 1>(p, a.stream)
+           : tiles == 2 ? kv_attention_run<J, 2, 1>(p, a.stream)
+                        : kv_attention_run<J, 2, 2>(p, a.stream);
   };
   if (a.D == 64) return pick(std::integral_constant<int, 2>{});
   if (a.D == 96) return pick(std::integral_constant<int, 3>{});
