@@ -755,7 +755,6 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp / kGroup, member = warp % kGroup;
   const uint32_t base = smem_u32(smem);
   const uint32_t ring = base + (uint32_t)(group * kStages * SM::rec), bars = base + SM::bars + 16u * (uint32_t)(group * kStages);
-  pdl_launch_dependents();
   if (tid < kKvRecords) {
     mbar_init(base + SM::bars + 16u * tid, 1);
     mbar_init(base + SM::bars + 16u * tid + 8, kGroup);
@@ -763,6 +762,8 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
   if (tid == 0) abort_flag = 0;
   fence_mbar_init();
   pdl_wait_previous();
+  // (not before the wait: the second kernel reads the lengths as soon as it runs)
+  pdl_launch_dependents();
   const int total = kv_scan<kKvThreads>(p, ends, sums);
   // (few units: their shares lie in as many CTAs as there are)
   const int shares = kv_shares_used(total, (int)gridDim.x * kRings), share = group * (int)gridDim.x + (int)blockIdx.x;
@@ -868,11 +869,10 @@ template <int J, int kTiles, bool kSplit>
 __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p, int most) {
   constexpr int D = 32 * J, kLanes = kKvJoin / (D / 2);
   __shared__ int ends[kKvJoin], sums[kKvJoin / 32];
-  pdl_launch_dependents();
-  pdl_wait_previous();
+  // Ahead of the wait for the first kernel stand the lengths only: that kernel lets this one start after
+  // its own wait, so what it found complete is complete here.
   const int tid = threadIdx.x, per = p.Hk * p.passes, s = blockIdx.x / per, seg = blockIdx.x - s * per;
   const int h = seg / p.passes, pass = seg - h * p.passes, cols = min(8 * kTiles, p.cols - pass * 8 * kTiles);
-  if ((int)blockIdx.y >= cols) return;   // (a narrower last pass)
   const int total = kv_scan<kKvJoin>(p, ends, sums);
   const int shares = kv_shares_used(total, most);
   const int run = (p.S + kKvJoin - 1) / kKvJoin, t = s / run;
@@ -884,11 +884,13 @@ __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p
   if (pages > 0) {
     c0 = (int)((((int64_t)a + 1) * shares - 1) / total);
     n = (int)(((int64_t)(a + pages) * shares - 1) / total) - c0 + 1;
-    if (n == 1) return;   // finished by its share
   }
   // a share's slot: 1 only where the segment begins inside it, behind another (that is its first share's case)
   const int64_t pitch = (int64_t)2 * kTiles * part_floats(D);
   const int64_t head = n > 0 && a > kv_share_start(total, c0, shares) ? kTiles * part_floats(D) : 0;
+  pdl_launch_dependents();
+  pdl_wait_previous();   // (by every CTA: this kernel does not end before the first one)
+  if (n == 1 || (int)blockIdx.y >= cols) return;   // finished by its share; a narrower last pass
   auto at = [&](int c, int local) {
     return p.part + (c0 + c) * pitch + (c == 0 ? head : 0) + (local >> 3) * part_floats(D);
   };
@@ -916,7 +918,7 @@ __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p
     for (int local = lane; local < cols; local += kLanes) {
       float m = -INFINITY, l = 0.f;
       float2 o = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
       for (int c = 0; c < n; ++c) m = fmaxf(m, at(c, local)[8 * D + (local & 7)]);
       join(local, d, 0, 1, m, o, l);
       write(local, d, m, o, l);

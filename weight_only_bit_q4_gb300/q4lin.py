@@ -693,15 +693,21 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps: float = 1e-6
 # ---------------------------------------------------------------- attention, its 4-bit cache, and the logits' answers
 
 KV_PAGE = 64   # tokens of a cache page
+_PAGE_BYTES = {}
+
+
+def _page_bytes(D):
+    if D not in _PAGE_BYTES:
+        _PAGE_BYTES[D] = int(load().q4lin_kv4_page_bytes(D))
+    return _PAGE_BYTES[D]
 
 
 def _run(device, fn, *args):
     """The library works on the current device: ``device`` becomes it for the call if it is another."""
-    torch = _t()
-    if torch._C._cuda_getDevice() == device.index:
+    if _torch._C._cuda_getDevice() == device.index:
         st = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with _torch.cuda.device(device):
             st = fn(*args)
     if st != OK:
         raise Q4LinError(st)
@@ -711,6 +717,14 @@ def _same_device(device, *tensors):
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError(f"all tensors must be on one device; got {t.device} beside {device}")
+
+
+def _out(t, name, shape, dtype, device, stream):
+    """(address, tensor) of an output: the one given, checked, or a new one."""
+    if t is None:
+        t = _new(shape, dtype, device, stream)
+        return t.data_ptr(), t
+    return _need(name, t, dtype, shape), t
 
 
 def prompt_attention(q, k, v, cu_seqlens, scale: float | None = None, out=None, stream=None):
@@ -747,7 +761,7 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float | None = None, out=None, 
 
 def kv4_page_bytes(D: int) -> int:
     """Bytes that a page of the cache (KV_PAGE tokens) holds per head of D values; 0 for sizes it does not take."""
-    return int(load().q4lin_kv4_page_bytes(D))
+    return _page_bytes(D)
 
 
 def _cache(cache, page_table, D):
@@ -757,7 +771,7 @@ def _cache(cache, page_table, D):
         raise ValueError("cache must be [pages, Hk, page bytes] and page_table [S, max_pages]")
     P, hk, _ = cache.shape
     S, M = page_table.shape
-    nb = load().q4lin_kv4_page_bytes(D)
+    nb = _page_bytes(D)
     if nb == 0:
         raise ValueError(f"the cache takes heads of 64, 96 or 128 values, not {D}")
     return (_need("cache", cache, torch.uint8, (P, hk, nb)), _need("page_table", page_table, torch.int32, (S, M)), P, hk, S, M)
@@ -871,18 +885,12 @@ def token_logprobs(logits, targets, top_k: int = 0, logprobs=None, entropy=None,
         raise ValueError("targets must be [T] or [T, n]")
     n = 1 if targets.dim() == 1 else targets.shape[1]
     f32 = torch.float32
-    if logprobs is None:
-        logprobs = _new(targets.shape, f32, dev, stream)
-    if entropy is None:
-        entropy = _new((T,), f32, dev, stream)
-    if top_ids is None:
-        top_ids = _new((T, top_k), torch.int32, dev, stream)
-    if top_logprobs is None:
-        top_logprobs = _new((T, top_k), f32, dev, stream)
     _same_device(dev, targets, logprobs, entropy, top_ids, top_logprobs)
+    tok = _need("targets", targets, torch.int32, (T,) + tuple(targets.shape[1:]))
+    lp, logprobs = _out(logprobs, "logprobs", targets.shape, f32, dev, stream)
+    ep, entropy = _out(entropy, "entropy", (T,), f32, dev, stream)
+    ip, top_ids = _out(top_ids, "top_ids", (T, top_k), torch.int32, dev, stream)
+    tp, top_logprobs = _out(top_logprobs, "top_logprobs", (T, top_k), f32, dev, stream)
     _run(dev, load().q4lin_token_logprobs, logits.data_ptr(), 1 if logits.dtype is f32 else 0,
-         logits.stride(0) if T > 1 else V, _need("targets", targets, torch.int32, (T,) + tuple(targets.shape[1:])),
-         _need("logprobs", logprobs, f32, targets.shape), _need("entropy", entropy, f32, (T,)),
-         _need("top_ids", top_ids, torch.int32, (T, top_k)), _need("top_logprobs", top_logprobs, f32, (T, top_k)), T, V, n,
-         top_k, _stream_ptr(stream, dev))
+         logits.stride(0) if T > 1 else V, tok, lp, ep, ip, tp, T, V, n, top_k, _stream_ptr(stream, dev))
     return logprobs, entropy, top_ids, top_logprobs
