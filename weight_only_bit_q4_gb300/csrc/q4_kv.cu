@@ -29,6 +29,14 @@ __host__ __device__ constexpr int kv_record(int D) { return kPage * D + 4 * kPag
 // Byte of token o in a row of V codes.
 __device__ __forceinline__ int v_place(int o) { return 16 * ((o & 7) >> 1) + 4 * (o >> 4) + 2 * (o & 1) + ((o & 15) >> 3); }
 
+__device__ __forceinline__ float2 kv_fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
 // ------------------------------------------------------------------ tokens in and out
 struct KvTokParams {
   const uint16_t* src[2];   // k, v rows (append)
@@ -60,25 +68,69 @@ constexpr int kTokTile = 64;   // tokens of a CTA
 // record's order (a lane has a token's byte of a row), so that tokens of a page are written and
 // read a row at a time.
 struct KvTile {
-  int64_t page[kTokTile];   // < 0: the token has no place
+  int64_t rec[kTokTile];    // byte of the token's record in the cache; < 0: the token has no place
   int place[kTokTile];
 };
 
-__device__ __forceinline__ void kv_places(const KvTokParams& p, KvTile& tile, int64_t t0) {
+__device__ __forceinline__ void kv_places(const KvTokParams& p, KvTile& tile, int64_t t0, int h) {
   if (threadIdx.x < kTokTile) {
     int64_t page = -1;
     int o = 0;
     const int64_t t = t0 + threadIdx.x;
-    if (t >= p.T || !kv_slot(p, t, page, o)) page = -1;
-    tile.page[threadIdx.x] = page;
+    const bool there = t < p.T && kv_slot(p, t, page, o);
+    tile.rec[threadIdx.x] = there ? (page * p.Hk + h) * (int64_t)kv_record(p.D) : -1;
     tile.place[threadIdx.x] = o;
   }
 }
 
-// The eight lanes of a scale group agree on its largest magnitude by shuffles.  q = rint(x / s): x
-// times 1 / s decides, unless it lies so near a half that its error (below 2^-19) could matter;
-// then the quotient itself: of an 8-bit by an 11-bit significand it is never so near a half that
-// FP32's rounding would reach it.
+// Codes (low nibble first) and scale of a lane's eight bf16 values x; top: the bits of the group's largest
+// magnitude.  q = rint(x / s) decided by x times 1 / s, unless a value lies so near a half that its
+// error (below 2^-18) could matter; then by the quotient itself: of an 8-bit by an 11-bit significand it is
+// never so near a half that FP32's rounding would reach it.  Likewise s = fp16(top / 7) by a product:
+// top / 7 keeps 2^-15 away from the midpoints of normal fp16 numbers.
+__device__ __forceinline__ uint32_t kv_codes(const uint32_t (&x)[4], uint32_t top, uint16_t& scale) {
+  scale = 0x7E00u;   // NaN: a group with a value that is not finite reads as NaN
+  if (top >= 0x7F80u) return 0x88888888u;
+  const float tf = __uint_as_float(top << 16);
+  // 1.5 * 2^23 + 8: a sum's last bits are the code
+  constexpr float magic = 12582920.f;
+  const float2 up = make_float2(magic, magic), down = make_float2(-magic, -magic);
+  const bool plain = tf >= 0.0005f && tf <= 458000.f;   // (s a normal number, and not cut off)
+  if (plain) {
+    const __half s = __float2half_rn(tf * 0.14285714924335479736f);
+    scale = __half_as_ushort(s);
+    const float inv = __fdividef(1.f, __half2float(s));
+    float far = 0.f;   // the largest distance to the integer taken
+    uint32_t even[4], odd[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = kv_fmul2(make_float2(bf16lo(x[i]), bf16hi(x[i])), make_float2(inv, inv));
+      const float2 n = fadd2(q, up), d = fadd2(n, down);
+      far = fmaxf(far, fmaxf(fabsf(q.x - d.x), fabsf(q.y - d.y)));
+      even[i] = __float_as_uint(n.x);
+      odd[i] = __float_as_uint(n.y);
+    }
+    if (far <= 0.49999f) {   // the sums' last bytes side by side
+      auto bytes = [](const uint32_t (&v)[4]) {
+        return __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410) & 0x0F0F0F0Fu;
+      };
+      return bytes(even) | bytes(odd) << 4;
+    }
+  }
+  const __half s = __float2half_rn(fminf(__fdiv_rn(tf, 7.f), 65504.f));
+  const float sf = __half2float(s);
+  scale = __half_as_ushort(s);
+  if (sf == 0.f) return 0x88888888u;
+  uint32_t code = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 2 ? x[0] : i < 4 ? x[1] : i < 6 ? x[2] : x[3];
+    const float q = __fdiv_rn(__uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16), sf);
+    code |= (__float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + magic) & 15u) << (4 * i);
+  }
+  return code;
+}
+
 template <int LPR>
 __global__ void __launch_bounds__(kTokThreads) q4_kv_append_kernel(const KvTokParams p) {
   constexpr int kRows = kTokThreads / LPR, kPasses = kTokTile / kRows;
@@ -90,18 +142,18 @@ __global__ void __launch_bounds__(kTokThreads) q4_kv_append_kernel(const KvTokPa
   pdl_launch_dependents();
   pdl_wait_previous();
   const bool in = 8 * b < p.D;
-  const uint16_t* src = (side ? p.src[1] : p.src[0]) + (int64_t)h * p.D + 8 * b;
   const int64_t ld = side ? p.ld[1] : p.ld[0];
+  const uint16_t* src = (side ? p.src[1] : p.src[0]) + (t0 + tid / LPR) * ld + h * p.D + 8 * b;
+  const int left = (int)min((int64_t)kTokTile, p.T - t0);
   uint4 w[kPasses];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t t = t0 + i * kRows + tid / LPR;
+  for (int i = 0; i < kPasses; ++i, src += kRows * ld) {
     w[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && t < p.T) w[i] = ld_global_u4(src + t * ld);
+    if (in && i * kRows + tid / LPR < left) w[i] = ld_global_u4(src);
   }
-  kv_places(p, tile, t0);
+  kv_places(p, tile, t0, h);
   __syncthreads();
-  const int G = kv_groups(p.D);
+  const int G = kv_groups(p.D), word = ((b & 3) * (p.D / 32) + (b >> 2)) * 4;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = i * kRows + tid / LPR;
@@ -112,40 +164,22 @@ __global__ void __launch_bounds__(kTokThreads) q4_kv_append_kernel(const KvTokPa
     top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    uint16_t scale = 0x7E00u;   // NaN: a group with a value that is not finite reads as NaN
-    uint32_t code = 0x88888888u;
-    if (top < 0x7F80u) {
-      const __half s = __float2half_rn(fminf(__fdiv_rn(__uint_as_float(top << 16), 7.f), 65504.f));
-      const float sf = __half2float(s);
-      scale = __half_as_ushort(s);
-      if (sf > 0.f) {
-        const float inv = __frcp_rn(sf);
-        code = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = e & 1 ? bf16hi(xs[e >> 1]) : bf16lo(xs[e >> 1]);
-          // 1.5 * 2^23 + 8: the sum's last bits are the code
-          constexpr float magic = 12582920.f;
-          float q = fminf(fmaxf(x * inv, -8.f), 7.f), n = q + magic;
-          if (fabsf(q - (n - magic)) > 0.499f) n = fminf(fmaxf(__fdiv_rn(x, sf), -8.f), 7.f) + magic;
-          code |= (__float_as_uint(n) & 15u) << (4 * e);
-        }
-      }
-    }
-    const int64_t page = tile.page[r];
+    uint16_t scale;
+    const uint32_t code = kv_codes(xs, top, scale);
     if (side == 1 && in) words[r][b] = code;
-    if (page < 0 || !in) continue;
-    uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D);
+    const int64_t at = tile.rec[r];
+    if (at < 0 || !in) continue;
+    uint8_t* rec = p.cache + at;
     const int o = tile.place[r];
-    if (side == 0) *reinterpret_cast<uint32_t*>(rec + o * (p.D / 2) + ((b & 3) * (p.D / 32) + (b >> 2)) * 4) = code;
+    if (side == 0) *reinterpret_cast<uint32_t*>(rec + o * (p.D / 2) + word) = code;
     if ((b & 7) == 0) reinterpret_cast<uint16_t*>(rec + 64 * p.D)[side * kPage * G + o * G + (b >> 3)] = scale;
   }
   if (side == 0) return;
   __syncthreads();
   const int r = tid % kTokTile;
-  const int64_t page = tile.page[r];
-  if (page < 0) return;
-  uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D) + 32 * p.D + v_place(tile.place[r]);
+  const int64_t at = tile.rec[r];
+  if (at < 0) return;
+  uint8_t* rec = p.cache + at + 32 * p.D + v_place(tile.place[r]);
   for (int b0 = tid / kTokTile; b0 < p.D / 8; b0 += kTokThreads / kTokTile) {
     const uint32_t code = words[r][b0];
 #pragma unroll
@@ -163,13 +197,13 @@ __global__ void __launch_bounds__(kTokThreads) q4_kv_read_kernel(const KvTokPara
   const int64_t t0 = (int64_t)blockIdx.x * kTokTile;
   pdl_launch_dependents();
   pdl_wait_previous();
-  kv_places(p, tile, t0);
+  kv_places(p, tile, t0, h);
   __syncthreads();
   if (side == 1) {
     const int r = tid % kTokTile;
-    const int64_t page = tile.page[r];
-    if (page >= 0) {
-      const volatile uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D) + 32 * p.D + v_place(tile.place[r]);
+    const int64_t at = tile.rec[r];
+    if (at >= 0) {
+      const volatile uint8_t* rec = p.cache + at + 32 * p.D + v_place(tile.place[r]);
 #pragma unroll 4
       for (int b0 = tid / kTokTile; b0 < p.D / 8; b0 += kTokThreads / kTokTile) {
         uint32_t c[4];
@@ -182,26 +216,37 @@ __global__ void __launch_bounds__(kTokThreads) q4_kv_read_kernel(const KvTokPara
   }
   if (8 * b >= p.D) return;
   const int G = kv_groups(p.D);
-  uint16_t* dst = (side ? p.dst[1] : p.dst[0]) + (int64_t)h * p.D + 8 * b;
   const int64_t ld = side ? p.ld[1] : p.ld[0];
+  uint16_t* dst = (side ? p.dst[1] : p.dst[0]) + (t0 + tid / LPR) * ld + h * p.D + 8 * b;
+  const int word = ((b & 3) * (p.D / 32) + (b >> 2)) * 4;
+  uint32_t codes[kPasses];
+  uint16_t scales[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int r = i * kRows + tid / LPR;
-    const int64_t page = tile.page[r];
-    if (page < 0) continue;
-    const uint8_t* rec = p.cache + (page * p.Hk + h) * (int64_t)kv_record(p.D);
+    const int64_t at = tile.rec[r];
+    if (at < 0) continue;
+    const uint8_t* rec = p.cache + at;
     const int o = tile.place[r];
-    const uint32_t code = side ? words[r][b] : ld_global_u32(rec + o * (p.D / 2) + ((b & 3) * (p.D / 32) + (b >> 2)) * 4);
-    const float s = fp16_bits_to_float(
-        reinterpret_cast<const volatile uint16_t*>(rec + 64 * p.D)[side * kPage * G + o * G + (b >> 3)]);
-    uint32_t out[4];
+    codes[i] = side ? words[r][b] : ld_global_u32(rec + o * (p.D / 2) + word);
+    scales[i] = reinterpret_cast<const volatile uint16_t*>(rec + 64 * p.D)[side * kPage * G + o * G + (b >> 3)];
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = (float)((int)((code >> (8 * e)) & 15u) - kZeroPoint) * s;
-      const float hi = (float)((int)((code >> (8 * e + 4)) & 15u) - kZeroPoint) * s;
-      out[e] = (uint32_t)float_to_bf16_bits(lo) | (uint32_t)float_to_bf16_bits(hi) << 16;
-    }
-    *reinterpret_cast<uint4*>(dst + (t0 + r) * ld) = make_uint4(out[0], out[1], out[2], out[3]);
+  for (int i = 0; i < kPasses; ++i, dst += kRows * ld) {
+    if (tile.rec[i * kRows + tid / LPR] < 0) continue;
+    const uint32_t code = codes[i];
+    const float s = fp16_bits_to_float(scales[i]);
+    // the nibbles as FP32 128 + q, then (q - 8) s
+    const uint32_t even = code & 0x0F0F0F0Fu, odd = (code >> 4) & 0x0F0F0F0Fu;
+    const float2 zero = make_float2(-136.f, -136.f), s2 = make_float2(s, s);
+    auto pair = [&](float lo, float hi) {
+      const float2 v = kv_fmul2(fadd2(make_float2(lo, hi), zero), s2);
+      const __nv_bfloat162 h2 = __floats2bfloat162_rn(v.x, v.y);
+      return *reinterpret_cast<const uint32_t*>(&h2);
+    };
+    const uint32_t out[4] = {pair(f128_plus_byte<0>(even), f128_plus_byte<0>(odd)), pair(f128_plus_byte<1>(even), f128_plus_byte<1>(odd)),
+                             pair(f128_plus_byte<2>(even), f128_plus_byte<2>(odd)), pair(f128_plus_byte<3>(even), f128_plus_byte<3>(odd))};
+    *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
@@ -367,14 +412,6 @@ __device__ __forceinline__ float kv_ex2(float t) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   return e;
-}
-
-__device__ __forceinline__ float2 kv_fmul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
