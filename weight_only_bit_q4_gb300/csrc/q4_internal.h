@@ -105,9 +105,6 @@ bool tc_supported(int64_t N, int64_t K, int64_t T);
 // driver's encoder is unavailable or refuses the arguments.
 bool encode_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
-// A 3-D tensor map (extents, byte strides of dimensions 1 and 2, box).
-bool encode_map_3d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[3],
-                   const uint64_t (&strides)[2], const uint32_t (&box)[3], CUtensorMapSwizzle swizzle);
 // A 4-D tensor map (extents, byte strides of dimensions 1..3, box).
 bool encode_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
                    const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle);

@@ -774,6 +774,18 @@ __device__ __forceinline__ void kv_write(const KvParams& p, int s, int h, int co
     }
 }
 
+// Bounded wait with every lane polling and the warp voting: no branch on one lane, no shuffle, so a wait
+// whose phase has completed already costs a query and a vote.
+__device__ __forceinline__ bool kv_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag)) return false;
+  }
+  *abort_flag = 1;
+  if ((threadIdx.x & 31) == 0) atomicExch(status, (int)Q4LIN_ERR_TIMEOUT);
+  return false;
+}
+
 template <int J>
 struct KvSmem {
   static constexpr int rec = kv_record(32 * J);
@@ -852,7 +864,7 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
     for (; u < end; ++u) {
       const int s = used % kStages;
       if (there >> s & 1u) {
-        ok = warp_wait_vote(bars + 16u * (uint32_t)s, phases >> s & 1u, &abort_flag, &g_kv_status);
+        ok = kv_wait(bars + 16u * (uint32_t)s, phases >> s & 1u, &abort_flag, &g_kv_status);
         if (!ok) break;
         phases ^= 1u << s;
         const int token0 = (u - here.seg0) * kPage;
@@ -874,7 +886,7 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
         ++used;
         if (b >= 0) {
           if (member == 0 && next < u1) {
-            ok = warp_wait_vote(bars + 16u * (uint32_t)(b % kStages) + 8, (uint32_t)(b / kStages) & 1u, &abort_flag, &g_kv_status);
+            ok = kv_wait(bars + 16u * (uint32_t)(b % kStages) + 8, (uint32_t)(b / kStages) & 1u, &abort_flag, &g_kv_status);
             if (!ok) break;
           }
           issue();

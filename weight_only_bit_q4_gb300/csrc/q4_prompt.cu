@@ -49,7 +49,7 @@ constexpr int kPtK = 2, kPtV = 3;     // stages of K and of V (all that shared m
 __device__ int g_prompt_status = 0;
 
 struct PtParams {
-  CUtensorMap mq, mk, mv;   // (D, heads, T)
+  CUtensorMap mq, mk, mv;   // (D, heads, T, 1)
   const uint16_t* v;
   uint16_t* out;
   int64_t ldv, ldo;
@@ -61,6 +61,43 @@ struct PtParams {
   float c;                  // |scale| log2 e
   int negate;               // the scale is negative: Q enters negated
 };
+
+// Bounded wait with every lane polling and the warp voting: no branch on one lane, no shuffle, so a wait
+// whose phase has completed already costs a query and a vote.
+__device__ __forceinline__ bool warp_wait_vote(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag)) return false;
+  }
+  *abort_flag = 1;
+  if ((threadIdx.x & 31) == 0) atomicExch(status, (int)Q4LIN_ERR_TIMEOUT);
+  return false;
+}
+
+// Whether the phase has completed, without waiting; the warp's common answer.
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
+// One lane of a converged warp, the same every time.  Code under it stays uniform to the compiler,
+// where a test of the lane's number would make it a divergent branch.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
 
 // Rows [a, b) of sequence s, within the tensors whatever cu holds.
 __device__ __forceinline__ void pt_rows(const PtParams& p, int s, int64_t& a, int64_t& b) {
@@ -228,9 +265,9 @@ __device__ __forceinline__ bool pt_taken(uint32_t answer, uint32_t& block) {
 
 __device__ __forceinline__ void pt_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int d, int h, int t) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(d), "r"(h), "r"(t)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(d), "r"(h), "r"(t), "r"(0)
       : "memory");
 }
 
@@ -723,10 +760,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// Rows of heads as a tensor (D, heads, T) of boxes of 64 columns of a head and 128 rows.
+// Rows of heads as a tensor (D, heads, T, 1) of boxes of 64 columns of a head and 128 rows.
 bool pt_map(CUtensorMap* m, const void* base, int64_t D, int64_t heads, int64_t T, int64_t ld) {
-  return encode_map_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, {(uint64_t)D, (uint64_t)heads, (uint64_t)T},
-                       {(uint64_t)D * 2, (uint64_t)ld * 2}, {64, 1, kPtTile}, CU_TENSOR_MAP_SWIZZLE_128B);
+  const uint64_t row = (uint64_t)ld * 2;
+  return encode_map_4d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, {(uint64_t)D, (uint64_t)heads, (uint64_t)T, 1},
+                       {(uint64_t)D * 2, row, row}, {64, 1, kPtTile, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int DB>
