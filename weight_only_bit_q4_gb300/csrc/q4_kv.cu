@@ -396,7 +396,7 @@ struct KvCursor {
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -404,7 +404,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
@@ -537,27 +537,24 @@ struct KvQuery {
 
 // The scales of a token's groups.
 template <int G>
-__device__ __forceinline__ void kv_scales(uint32_t at, float (&v)[G]) {
+__device__ __forceinline__ void kv_scales(const uint8_t* at, float (&v)[G]) {
   if constexpr (G == 2) {
-    uint32_t w;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(at));
     v[0] = f.x;
     v[1] = f.y;
   } else {
-    uint16_t h;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
-    v[0] = fp16_bits_to_float(h);
+    v[0] = __half2float(*reinterpret_cast<const __half*>(at));
   }
 }
 
 // One page (64 tokens from token0 on) joins the warp's state; kEnd: not every column sees all of it.
 template <int J, int NT, bool kEnd>
-__device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>& qy, uint32_t rec, int token0, int lane) {
+__device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>& qy, const uint8_t* rec, int token0, int lane) {
   constexpr int D = 32 * J, G = kv_groups(D);
   constexpr uint32_t M0 = 0x000F000Fu, M1 = 0x00F000F0u;
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t kbase = rec + (uint32_t)(g * (D / 2) + c * J * 4), sbase = rec + 64u * D + (uint32_t)(g * 2 * G);
+  // (plain loads: the compiler may move them ahead of the products before them)
+  const uint8_t *kbase = rec + g * (D / 2) + c * J * 4, *sbase = rec + 64 * D + g * 2 * G;
   float x[4][NT][4];
   float vs[4][2][G];   // V scales of this thread's tokens
   float vtop = 0.f;
@@ -581,19 +578,19 @@ __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>
     float ks[2][G];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint32_t at = kbase + (uint32_t)((16 * mt + 8 * r) * (D / 2));
+      const uint8_t* at = kbase + (16 * mt + 8 * r) * (D / 2);
       if constexpr (J == 4) {
-        const uint4 v = ld_shared_v4(at);
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
         w[r][0] = v.x; w[r][1] = v.y; w[r][2] = v.z; w[r][3] = v.w;
       } else if constexpr (J == 2) {
-        const uint2 v = ld_shared_u64(at);
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
         w[r][0] = v.x; w[r][1] = v.y;
       } else {
 #pragma unroll
-        for (int j = 0; j < J; ++j) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[r][j]) : "r"(at + 4u * j));
+        for (int j = 0; j < J; ++j) w[r][j] = reinterpret_cast<const uint32_t*>(at)[j];
       }
-      kv_scales<G>(sbase + (uint32_t)((16 * mt + 8 * r) * 2 * G), ks[r]);
-      kv_scales<G>(sbase + (uint32_t)((16 * mt + 8 * r) * 2 * G) + 128u * G, vs[mt][r]);
+      kv_scales<G>(sbase + (16 * mt + 8 * r) * 2 * G, ks[r]);
+      kv_scales<G>(sbase + (16 * mt + 8 * r) * 2 * G + 128 * G, vs[mt][r]);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -692,7 +689,7 @@ __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>
     st.l[t][0] = l.x;
     st.l[t][1] = l.y;
   }
-  const uint32_t vbase = rec + 32u * D + (uint32_t)(g * kPage + 16 * c);
+  const uint8_t* vbase = rec + 32 * D + g * kPage + 16 * c;
 #pragma unroll
   for (int i = 0; i < G; ++i)
 #pragma unroll
@@ -702,7 +699,7 @@ __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>
         mma_16816(st.z[i][t], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, pb[s][i][t][0], pb[s][i][t][1]);
 #pragma unroll
   for (int md = 0; md < 2 * J; ++md) {
-    const uint4 v = ld_shared_v4(vbase + (uint32_t)(md * 8 * kPage));
+    const uint4 v = *reinterpret_cast<const uint4*>(vbase + md * 8 * kPage);
     const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -870,9 +867,9 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
         const int token0 = (u - here.seg0) * kPage;
         // (the last n - 1 tokens are seen by some columns only)
         if (token0 + kPage <= here.L - p.n + 1)
-          kv_page<J, NT, false>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
+          kv_page<J, NT, false>(st, qy, smem + (group * kStages + s) * SM::rec, token0, lane);
         else
-          kv_page<J, NT, true>(st, qy, ring + (uint32_t)(s * SM::rec), token0, lane);
+          kv_page<J, NT, true>(st, qy, smem + (group * kStages + s) * SM::rec, token0, lane);
       }
       if constexpr (kGroup == 1) {
         ++used;
