@@ -84,49 +84,47 @@ __device__ __forceinline__ void kv_places(const KvTokParams& p, KvTile& tile, in
 }
 
 // Codes (low nibble first) and scale of a lane's eight bf16 values x; top: the bits of the group's largest
-// magnitude.  q = rint(x / s) decided by x times 1 / s, unless a value lies so near a half that its
-// error (below 2^-18) could matter; then by the quotient itself: of an 8-bit by an 11-bit significand it is
-// never so near a half that FP32's rounding would reach it.  Likewise s = fp16(top / 7) by a product:
-// top / 7 keeps 2^-15 away from the midpoints of normal fp16 numbers.
+// magnitude.  q = rint(x / s) comes from a fixed-point sum with 16 bits behind the point, x (65536 / s) +
+// 65536 (8 + 1/2) + 1 (off by less than 0.7 of its last place): its upper half's low nibble is the
+// code, unless the lower half is 0, 1 or 2 for one of the values, which then may lie at a half (one value
+// in 600 does so exactly).  Those lanes compare x with h s, h the half next to x / s: a product of 5 by
+// 11 bits, so that one FMA gives the exact difference's sign.  s = fp16(top / 7) by a product: top / 7
+// keeps 2^-15 away from the midpoints of normal fp16 numbers.
 __device__ __forceinline__ uint32_t kv_codes(const uint32_t (&x)[4], uint32_t top, uint16_t& scale) {
   scale = 0x7E00u;   // NaN: a group with a value that is not finite reads as NaN
   if (top >= 0x7F80u) return 0x88888888u;
   const float tf = __uint_as_float(top << 16);
-  // 1.5 * 2^23 + 8: a sum's last bits are the code
-  constexpr float magic = 12582920.f;
-  const float2 up = make_float2(magic, magic), down = make_float2(-magic, -magic);
   const bool plain = tf >= 0.0005f && tf <= 458000.f;   // (s a normal number, and not cut off)
+  const __half s = __float2half_rn(plain ? tf * 0.14285714924335479736f : fminf(__fdiv_rn(tf, 7.f), 65504.f));
+  const float sf = __half2float(s), inv = __fdividef(1.f, sf);
+  scale = __half_as_ushort(s);
   if (plain) {
-    const __half s = __float2half_rn(tf * 0.14285714924335479736f);
-    scale = __half_as_ushort(s);
-    const float inv = __fdividef(1.f, __half2float(s));
-    float far = 0.f;   // the largest distance to the integer taken
-    uint32_t even[4], odd[4];
+    constexpr float base = 12582912.f + 557057.f;   // 1.5 * 2^23: the sum's mantissa counts whole units
+    const float up = inv * 65536.f;
+    uint32_t n[8], low = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 q = kv_fmul2(make_float2(bf16lo(x[i]), bf16hi(x[i])), make_float2(inv, inv));
-      const float2 n = fadd2(q, up), d = fadd2(n, down);
-      far = fmaxf(far, fmaxf(fabsf(q.x - d.x), fabsf(q.y - d.y)));
-      even[i] = __float_as_uint(n.x);
-      odd[i] = __float_as_uint(n.y);
+      n[2 * i] = __float_as_uint(fmaf(bf16lo(x[i]), up, base));
+      n[2 * i + 1] = __float_as_uint(fmaf(bf16hi(x[i]), up, base));
+      low = __vminu2(low, __byte_perm(n[2 * i], n[2 * i + 1], 0x5410));
     }
-    if (far <= 0.49999f) {   // the sums' last bytes side by side
-      auto bytes = [](const uint32_t (&v)[4]) {
-        return __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410) & 0x0F0F0F0Fu;
+    if (min(low & 0xFFFFu, low >> 16) > 2u) {
+      auto thirds = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {   // the third bytes side by side
+        return __byte_perm(__byte_perm(a, b, 0x0062), __byte_perm(c, d, 0x0062), 0x5410);
       };
-      return bytes(even) | bytes(odd) << 4;
+      return (thirds(n[0], n[2], n[4], n[6]) & 0x0F0F0F0Fu) | (thirds(n[1], n[3], n[5], n[7]) << 4 & 0xF0F0F0F0u);
     }
+  } else if (sf == 0.f) {
+    return 0x88888888u;
   }
-  const __half s = __float2half_rn(fminf(__fdiv_rn(tf, 7.f), 65504.f));
-  const float sf = __half2float(s);
-  scale = __half_as_ushort(s);
-  if (sf == 0.f) return 0x88888888u;
+  constexpr float magic = 12582912.f;   // adding and taking it off rounds to integers, halves to even
   uint32_t code = 0;
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t w = i < 2 ? x[0] : i < 4 ? x[1] : i < 6 ? x[2] : x[3];
-    const float q = __fdiv_rn(__uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16), sf);
-    code |= (__float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + magic) & 15u) << (4 * i);
+    const float v = i & 1 ? bf16hi(x[i >> 1]) : bf16lo(x[i >> 1]);
+    const float h = (fminf(fmaxf(v * inv, -9.f), 8.f) - 0.5f + magic) - magic + 0.5f, r = fmaf(-h, sf, v);
+    const float q = r == 0.f ? (h + magic) - magic : r > 0.f ? h + 0.5f : h - 0.5f;
+    code |= (__float_as_uint(fminf(fmaxf(q, -8.f), 7.f) + (magic + 8.f)) & 15u) << (4 * i);
   }
   return code;
 }
