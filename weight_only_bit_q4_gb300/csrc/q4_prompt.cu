@@ -68,6 +68,7 @@ struct PtParams {
   int pairs;                // units per run of rows
   float c;                  // |scale| log2 e
   int negate;               // the scale is negative: Q enters negated
+  int wide;                 // the output's rows of heads are 32-byte aligned
 };
 
 // Bounded wait with every lane polling and the warp voting: no branch on one lane, no shuffle, so a wait
@@ -126,6 +127,12 @@ __device__ __forceinline__ uint32_t pt_pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {   // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ float2 pt_fmul2(float2 a, float2 b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;"
@@ -161,8 +168,9 @@ struct PtUnit {
 // numbers of runs of sequences l, l + 32, .. .  With more sequences than kPtSorted the runs are taken
 // sequence by sequence, the last run first (they are short then).
 constexpr int kPtSorted = 256;
+template <int kHeld>   // sequences held per lane: 1 (up to 32 of them) or 8
 struct PtOrder {
-  int n[kPtSorted / 32];
+  int n[kHeld], row0, len;   // (row0, len: of sequence l, with one per lane)
   int most, level;   // the highest number plus one; that of the last run found
   int64_t before;    // (not sorted) runs of the sequences before s
   int s;
@@ -171,15 +179,17 @@ struct PtOrder {
   __device__ __forceinline__ void start(const PtParams& p, int rows, int lane) {
     sorted = p.S <= kPtSorted;
     before = 0;
-    s = most = 0;
+    s = most = row0 = len = 0;
     if (!sorted) return;
 #pragma unroll
-    for (int k = 0; k < kPtSorted / 32; ++k) {
+    for (int k = 0; k < kHeld; ++k) {
       n[k] = 0;
       if (32 * k + lane < p.S) {
         int64_t a, b;
         pt_rows(p, 32 * k + lane, a, b);
-        n[k] = (int)((b - a + rows - 1) / rows);
+        row0 = (int)a;
+        len = (int)(b - a);
+        n[k] = (int)(((unsigned)len + (unsigned)rows - 1u) / (unsigned)rows);
       }
       most = max(most, n[k]);
     }
@@ -190,12 +200,26 @@ struct PtOrder {
   __device__ __forceinline__ int64_t runs_from(int j) const {
     unsigned c = 0;
 #pragma unroll
-    for (int k = 0; k < kPtSorted / 32; ++k) c += (unsigned)max(0, n[k] - j);
+    for (int k = 0; k < kHeld; ++k) c += (unsigned)max(0, n[k] - j);
     return (int64_t)__reduce_add_sync(0xffffffffu, c);   // (below T / rows + S)
   }
 
-  // Sequence and run of the index-th run; false: there are fewer.
-  __device__ __forceinline__ bool find(const PtParams& p, int rows, int64_t index, int lane, int& seq, int& run) {
+  // The index-th run: its sequence's first row and length, and its number; false: there are fewer.
+  __device__ __forceinline__ bool find(const PtParams& p, int rows, int64_t index, int lane, int& first, int& length, int& run) {
+    int seq = -1;
+    if (!search(p, rows, index, lane, seq, run)) return false;
+    if (kHeld == 1 && sorted) {
+      first = __shfl_sync(0xffffffffu, row0, seq);
+      length = __shfl_sync(0xffffffffu, len, seq);
+    } else {
+      int64_t a, b;
+      pt_rows(p, seq, a, b);
+      first = (int)a;
+      length = (int)(b - a);
+    }
+    return true;
+  }
+  __device__ __forceinline__ bool search(const PtParams& p, int rows, int64_t index, int lane, int& seq, int& run) {
     if (sorted) {
       if (runs_from(0) <= index) return false;
       // the largest number whose runs and those above it are more than index: often the last one's
@@ -212,7 +236,7 @@ struct PtOrder {
       run = lo;
       seq = -1;
 #pragma unroll
-      for (int k = 0; k < kPtSorted / 32; ++k) {
+      for (int k = 0; k < kHeld; ++k) {
         const unsigned has = __ballot_sync(0xffffffffu, n[k] > lo);
         if (seq < 0 && rank < __popc(has)) {
           const bool mine = (has >> lane & 1u) && __popc(has & ((1u << lane) - 1u)) == rank;
@@ -393,10 +417,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
         if (kb * kPtTile + kPtTile - 1 > qx) {
           const int see = row - kb * kPtTile;   // keys 0 .. see of the block
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j) {
+            // (bits, which become predicates several at a time)
+            const int last = see - 32 * j;
+            const uint32_t keep = last >= 31 ? 0xFFFFFFFFu : last < 0 ? 0u : (2u << last) - 1u;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * j + e > see) r[j][e] = 0xFF800000u;
+              if (!(keep >> e & 1u)) r[j][e] = 0xFF800000u;
+          }
         }
         float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll
@@ -470,16 +498,22 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
               }
             }
           }
-        if (row < w.len)
+        uint32_t ow[16];
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (32 * j + 8 * b < p.D) {
-              uint32_t ow[4];
+        for (int e = 0; e < 16; ++e) ow[e] = pt_pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        if (row < w.len) {
+          // (a lane's store is a line of its own, whatever its width: the wider the fewer)
+          if (p.wide) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                ow[e] = pt_pack(__uint_as_float(o[8 * b + 2 * e]) * inv, __uint_as_float(o[8 * b + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * j + 8 * b) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-            }
+            for (int b = 0; b < 2; ++b)
+              if (32 * j + 16 * b < p.D) st_global_32(dst + 32 * j + 16 * b, &ow[8 * b]);
+          } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if (32 * j + 8 * b < p.D)
+                *reinterpret_cast<uint4*>(dst + 32 * j + 8 * b) = make_uint4(ow[4 * b], ow[4 * b + 1], ow[4 * b + 2], ow[4 * b + 3]);
+          }
+        }
       }
       tc_fence_before();   // (ahead of the arrival that lets the next unit's P V overwrite O)
     }
@@ -703,62 +737,64 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
       // A unit is a run of rows and a head (pair); the CTA begins with its own number and takes those
       // of CTAs that have not started, so that long and short runs even out.
       const int rows = p.heads2 ? kPtTile : 2 * kPtTile;
-      PtOrder order;
-      order.start(p, rows, lane);
-      uint32_t block = blockIdx.x;
-      bool found = true;
-      int taken = 0;
-      for (int u = 0;; ++u) {
-        int seq = 0, run = 0;
-        if (found) {
-          found = order.find(p, rows, block / (uint32_t)p.pairs, lane, seq, run);
-          if (u >= 2 && !wait(base + SM::ue + 8 * (u & 1), ((uint32_t)(u >> 1) & 1u) ^ 1u)) break;
-          if (lane == 0) {
-            PtUnit v{};
-            if (found) {
-              int64_t a, b;
-              pt_rows(p, seq, a, b);
-              v.row0 = (int)a;
-              v.len = (int)(b - a);
-              v.q0 = run * rows;
-              v.q1 = v.q0 + (p.heads2 ? 0 : kPtTile);
-              v.head = (int)(block % (uint32_t)p.pairs) * (p.heads2 ? 2 : 1);
-              v.n0 = (min(v.len, v.q0 + kPtTile) + kPtTile - 1) / kPtTile;
-              v.n1 = v.q1 < v.len ? (min(v.len, v.q1 + kPtTile) + kPtTile - 1) / kPtTile : 0;
-              v.there = 1;
-            }
-            units[u & 1] = v;
-          }
-          warp_release(base + SM::uf + 8 * (u & 1), lane);
-        }
-        // (the next unit is taken when this one is nearly done: what has been taken early cannot be
-        // evened out any more)
-        if (found && !wait(base + SM::go, (uint32_t)u & 1u)) break;
-        // (behind the last unit there may be CTAs of the launch that have nothing to do: they are taken
-        // off too, which costs less than their start)
-        if (lane == 0) {
-          fence_proxy_async();   // (the last answer has been read)
-          mbar_expect_tx(base + SM::tk, 16);
-          pt_take(smem_u32(answer), base + SM::tk);
-        }
-        __syncwarp();
-        if (!wait(base + SM::tk, (uint32_t)taken & 1u)) {
-          if (lane == 0) mbar_drain(base + SM::tk, (uint32_t)taken & 1u);
-          break;
-        }
-        ++taken;
-        const bool more = pt_taken(smem_u32(answer), block);
-        __syncwarp();
-        if (!more) {   // the end, unless the units have ended before
+      auto hand_out = [&](auto order) {
+        order.start(p, rows, lane);
+        uint32_t block = blockIdx.x;
+        bool found = true;
+        int taken = 0;
+        for (int u = 0;; ++u) {
+          int first = 0, length = 0, run = 0;
           if (found) {
-            ++u;
+            const uint32_t at = block / (uint32_t)p.pairs, unit = block - at * (uint32_t)p.pairs;
+            found = order.find(p, rows, at, lane, first, length, run);
             if (u >= 2 && !wait(base + SM::ue + 8 * (u & 1), ((uint32_t)(u >> 1) & 1u) ^ 1u)) break;
-            if (lane == 0) units[u & 1] = PtUnit{};
+            if (lane == 0) {
+              PtUnit v{};
+              if (found) {
+                v.row0 = first;
+                v.len = length;
+                v.q0 = run * rows;
+                v.q1 = v.q0 + (p.heads2 ? 0 : kPtTile);
+                v.head = (int)unit * (p.heads2 ? 2 : 1);
+                v.n0 = (min(v.len, v.q0 + kPtTile) + kPtTile - 1) / kPtTile;
+                v.n1 = v.q1 < v.len ? (min(v.len, v.q1 + kPtTile) + kPtTile - 1) / kPtTile : 0;
+                v.there = 1;
+              }
+              units[u & 1] = v;
+            }
             warp_release(base + SM::uf + 8 * (u & 1), lane);
           }
-          break;
+          // (the next unit is taken when this one is nearly done: what has been taken early cannot be
+          // evened out any more)
+          if (found && !wait(base + SM::go, (uint32_t)u & 1u)) break;
+          // (behind the last unit there may be CTAs of the launch that have nothing to do: they are taken
+          // off too, which costs less than their start)
+          if (lane == 0) {
+            fence_proxy_async();   // (the last answer has been read)
+            mbar_expect_tx(base + SM::tk, 16);
+            pt_take(smem_u32(answer), base + SM::tk);
+          }
+          __syncwarp();
+          if (!wait(base + SM::tk, (uint32_t)taken & 1u)) {
+            if (lane == 0) mbar_drain(base + SM::tk, (uint32_t)taken & 1u);
+            break;
+          }
+          ++taken;
+          const bool more = pt_taken(smem_u32(answer), block);
+          __syncwarp();
+          if (!more) {   // the end, unless the units have ended before
+            if (found) {
+              ++u;
+              if (u >= 2 && !wait(base + SM::ue + 8 * (u & 1), ((uint32_t)(u >> 1) & 1u) ^ 1u)) break;
+              if (lane == 0) units[u & 1] = PtUnit{};
+              warp_release(base + SM::uf + 8 * (u & 1), lane);
+            }
+            break;
+          }
         }
-      }
+      };
+      if (p.S <= 32) hand_out(PtOrder<1>{});
+      else hand_out(PtOrder<kPtSorted / 32>{});
     }
     __syncwarp();
     tc_fence_before();
@@ -825,6 +861,7 @@ int prompt_launch(const PromptArgs& a) {
   // (a scale of 0 becomes the smallest that keeps a masked -inf one)
   p.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, FLT_TRUE_MIN);
   p.negate = a.scale < 0.f;
+  p.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.ldo % 16 == 0 && a.D % 16 == 0;
   // runs of rows: at most one that is not full per sequence
   const int64_t rows = p.heads2 ? kPtTile : 2 * kPtTile;
   const int64_t blocks = ((a.T + rows - 1) / rows + a.S) * p.pairs;
