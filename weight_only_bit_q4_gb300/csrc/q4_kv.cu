@@ -318,7 +318,6 @@ struct KvShape {
   static constexpr int warps = NT == 1 ? 12 : 8;   // (the registers of two tiles' states leave no more)
   static constexpr int threads = 32 * warps;
   static constexpr int rings = warps / kGroup, stages = kKvRecords / rings;
-  static constexpr int tiles = NT * kGroup;        // tiles of a pass
 };
 
 __host__ __device__ constexpr int part_floats(int D) { return 8 * (D + 2); }
@@ -947,14 +946,39 @@ __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p
   auto at = [&](int c, int local) {
     return p.part + (c0 + c) * pitch + (c == 0 ? head : 0) + (local >> 3) * part_floats(D);
   };
-  auto join = [&](int local, int d, int from, int step, float m, float2& o, float& l) {
+  // partial sums from, from + step, .. of column `local`, two values of it: eight at a time on their way
+  auto join = [&](int local, int d, int from, int step, float& m, float2& o, float& l) {
     const int v = (local & 7) * D + 2 * d, k = 8 * D + (local & 7);
-#pragma unroll 4
-    for (int c = from; c < n; c += step) {
-      const float* q = at(c, local);
-      const float f = q[k] == m ? 1.f : kv_ex2(q[k] - m);
-      o = ffma2(*reinterpret_cast<const float2*>(q + v), make_float2(f, f), o);
-      l = fmaf(q[k + 8], f, l);
+    m = -INFINITY;
+    l = 0.f;
+    o = make_float2(0.f, 0.f);
+    for (int c = from; c < n; c += 8 * step) {
+      float mc[8], lc[8], top = m;
+      float2 oc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        mc[i] = -INFINITY;
+        lc[i] = 0.f;
+        oc[i] = make_float2(0.f, 0.f);
+        if (c + i * step < n) {
+          const float* q = at(c + i * step, local);
+          mc[i] = q[k];
+          lc[i] = q[k + 8];
+          oc[i] = *reinterpret_cast<const float2*>(q + v);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, mc[i]);
+      const float f0 = m == top ? 1.f : kv_ex2(m - top);   // (equal references, both -inf among them, need no factor)
+      o = kv_fmul2(o, make_float2(f0, f0));
+      l *= f0;
+      m = top;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = mc[i] == m ? 1.f : kv_ex2(mc[i] - m);
+        o = ffma2(oc[i], make_float2(f, f), o);
+        l = fmaf(lc[i], f, l);
+      }
     }
   };
   auto write = [&](int local, int d, float m, float2 o, float l) {
@@ -966,44 +990,40 @@ __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p
         empty ? 0u : (uint32_t)float_to_bf16_bits(o.x * r) | (uint32_t)float_to_bf16_bits(o.y * r) << 16;
   };
   const int lane = tid / (D / 2), d = tid - lane * (D / 2);
+  float m, l;
+  float2 o;
   if constexpr (!kSplit) {
     if (lane >= kLanes) return;
     for (int local = lane; local < cols; local += kLanes) {
-      float m = -INFINITY, l = 0.f;
-      float2 o = make_float2(0.f, 0.f);
-#pragma unroll 8
-      for (int c = 0; c < n; ++c) m = fmaxf(m, at(c, local)[8 * D + (local & 7)]);
       join(local, d, 0, 1, m, o, l);
       write(local, d, m, o, l);
     }
   } else {
     __shared__ float2 red[kLanes][D / 2];
-    __shared__ float tops[kKvJoin / 32], ls[kLanes];
+    __shared__ float ms[kLanes], ls[kLanes];
     const int local = blockIdx.y;
-    float m = -INFINITY, l = 0.f;
-    float2 o = make_float2(0.f, 0.f);
-    for (int c = tid; c < n; c += kKvJoin) m = fmaxf(m, at(c, local)[8 * D + (local & 7)]);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    if ((tid & 31) == 0) tops[tid >> 5] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kKvJoin / 32; ++w) m = fmaxf(m, tops[w]);
     if (lane < kLanes) {
       join(local, d, lane, kLanes, m, o, l);
       red[lane][d] = o;
-      if (d == 0) ls[lane] = l;
+      if (d == 0) {
+        ms[lane] = m;
+        ls[lane] = l;
+      }
     }
     __syncthreads();
     if (tid >= D / 2) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) top = fmaxf(top, ms[i]);
     l = 0.f;
     o = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kLanes; ++i) {
-      l += ls[i];
-      o = fadd2(o, red[i][tid]);
+      const float f = ms[i] == top ? 1.f : kv_ex2(ms[i] - top);
+      l = fmaf(ls[i], f, l);
+      o = ffma2(red[i][tid], make_float2(f, f), o);
     }
-    write(local, tid, m, o, l);
+    write(local, tid, top, o, l);
   }
 }
 
