@@ -828,17 +828,21 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
   KvCursor ahead = here;
   int next = u0, used = 0, filled = 0;
   uint32_t there = 0;       // per stage: a page was copied
-  int32_t page = -1;        // of unit `next`
+  int32_t held = -1;        // lane l: page of unit held0 + l, up to held1 (of one segment)
+  int held0 = u0, held1 = u0;
   bool ok = true;
   auto look = [&]() {
-    if (next < u1) {
+    if (next < u1 && next >= held1) {
       ahead.seek(p, next);
-      page = (int32_t)ld_global_u32(p.table + (int64_t)ahead.s * p.M + (next - ahead.seg0));
+      held0 = next;
+      held1 = min(min(ahead.seg0 + ahead.pages, u1), next + 32);
+      if (next + lane < held1) held = (int32_t)ld_global_u32(p.table + (int64_t)ahead.s * p.M + (next - ahead.seg0) + lane);
     }
   };
   auto issue = [&]() {      // (every warp keeps the books)
     if (next >= u1) return;
     const int st = filled % kStages;
+    const int32_t page = __shfl_sync(0xffffffffu, held, next - held0);
     const bool good = page >= 0 && page < p.P;   // a page that is not there: its tokens are left out
     there = good ? there | 1u << st : there & ~(1u << st);
     if (good && member == 0 && lane == 0) {
