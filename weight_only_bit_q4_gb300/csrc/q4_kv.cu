@@ -918,8 +918,7 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
 
 // Segments that lie in several shares, and sequences without tokens.  D / 2 threads hold a column, two
 // values each.  kSplit: a CTA takes one column, its groups of threads the partial sums in turn (few
-// long segments); otherwise a CTA takes a segment, its groups the columns (many short ones: a CTA
-// per column would be more of them than the GPU holds at once, each with a scan of the lengths).
+// long segments); otherwise a CTA takes a segment, its groups the columns (many short ones).
 constexpr int kKvJoin = 256;
 template <int J, int kTiles, bool kSplit>
 __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p, int most) {
@@ -1062,7 +1061,11 @@ int kv_attention_run(const KvParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   const int64_t segments = (int64_t)p.S * p.Hk * p.passes;
   const int cols = p.cols < 8 * NT * kGroup ? p.cols : 8 * NT * kGroup;
-  const bool split = segments * cols <= 8 * sms;   // (CTAs of 256 threads that the GPU holds at once)
+  // rounds of eight partial sums that a thread takes: all of a column's, for its columns one after the other, or
+  // a quarter of one column's, in as many waves as the GPU holds CTAs of 256 threads
+  const int64_t parts = (sms * KvShape<NT, kGroup>::rings + segments - 1) / segments;   // (of a segment of mean length)
+  const int64_t whole = ((cols + 3) / 4) * ((parts + 7) / 8), quarter = ((segments * cols + 8 * sms - 1) / (8 * sms)) * ((parts + 31) / 32);
+  const bool split = quarter < whole;
   cfg.gridDim = dim3((unsigned)segments, (unsigned)(split ? cols : 1), 1);
   cfg.blockDim = dim3(kKvJoin, 1, 1);
   cfg.stream = stream;

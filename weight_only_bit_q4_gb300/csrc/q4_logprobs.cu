@@ -14,7 +14,7 @@
 // 16-byte chunks dealt to the cluster's threads in turn; what lies before the first and behind
 // the last whole chunk goes to the first CTA's and the last CTA's single threads.  Lists: lane i of every warp holds the warp's i-th; a vote per chunk of 32
 // vectors decides whether any of its logits beats the last entry, which is rare after the
-// first few (the first batch meets a bar made of the lanes' maxima).  Warps, then CTAs
+// first few: a bar made of all threads' maxima over their first batch stands before the lists.  Warps, then CTAs
 // (distributed shared memory) are merged in order.
 //
 // Measured: 1024 rows of 131072 bf16 logits 44.6 us, 6.0 TB/s (0.90 of the measured copy rate); 75 rows of
@@ -115,13 +115,26 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return v > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
 }
 
-// The k-th largest of the lanes' keys (0: there are fewer above 0).
-__device__ __forceinline__ uint32_t kth_key(uint32_t key, int k, int lane) {
-  uint32_t top = 0;
+// Lane r gets the r-th largest of the lanes' keys (0 where there are no more above 0), r < k.
+__device__ __forceinline__ uint32_t top_keys(uint32_t key, int k, int lane) {
+  uint32_t mine = 0;
+  for (int r = 0; r < k; ++r) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+    if (top == 0) break;
+    if (lane == r) mine = top;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, key == top)) - 1) key = 0;
+  }
+  return mine;
+}
+
+// The k-th largest of `lists` sorted lists of keys; 0: there are fewer above 0.
+__device__ __forceinline__ uint32_t kth_of_lists(const uint32_t (*keys)[kMaxTop], int lists, int k, int lane) {
+  int at = 0;
+  uint32_t key = lane < lists ? keys[lane][0] : 0u, top = 0;
   for (int r = 0; r < k; ++r) {
     top = __reduce_max_sync(0xffffffffu, key);
-    if (top == 0) return 0;
-    if (lane == __ffs(__ballot_sync(0xffffffffu, key == top)) - 1) key = 0;
+    if (top == 0) break;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, key == top)) - 1) key = ++at < k ? keys[lane][at] : 0u;
   }
   return top;
 }
@@ -222,6 +235,7 @@ struct LpShared {
   float cv[kMaxCluster][kMaxTop];
   int ci[kMaxCluster][kMaxTop];
   float row[2];              // M, ln S
+  uint32_t keys[kLpMaxWarps][kMaxTop];   // the warps' largest lane maxima of the first batch, in order
 };
 
 __device__ __forceinline__ Sums warp_join(Sums r) {
@@ -263,23 +277,25 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_ker
   Sums r{0.f, 0.f, 0.f, -INFINITY};
   float limit = -INFINITY;
   TopList list{-INFINITY, -1};
-  float last = -INFINITY;     // the list's last entry
+  // What a value has to beat: the list's last entry once it is full, and a bar that k of the CTA's logits
+  // reach (its equals still count, for their tokens).
+  float last = -INFINITY, bar = -INFINITY;
   int last_id = -1;
-  // every lane offers a value (uniform); those that beat the last entry go in, one after the other
+  // every lane offers a value (uniform); those that pass go in, one after the other
   auto offer = [&](float v, int id) {
-    uint32_t some = __ballot_sync(0xffffffffu, v > last || (v == last && id < last_id));
+    auto passes = [&](float x, int i) { return x > -INFINITY && x >= bar && (x > last || (x == last && i < last_id)); };
+    uint32_t some = __ballot_sync(0xffffffffu, passes(v, id));
     while (some) {
       const int from = __ffs(some) - 1;
       some &= some - 1;
       const float x = __shfl_sync(0xffffffffu, v, from);
       const int i = __shfl_sync(0xffffffffu, id, from);
-      if (x > last || (x == last && i < last_id)) {   // (uniform)
+      if (passes(x, i)) {   // (uniform)
         list_insert(list, x, i, p.k, lane);
         const float lv = __shfl_sync(0xffffffffu, list.v, p.k - 1);
-        const int li = __shfl_sync(0xffffffffu, list.id, p.k - 1);
-        if (lv > -INFINITY) {   // the list is full: its last entry is the bar now
+        if (lv > -INFINITY) {   // the list is full
           last = lv;
-          last_id = li;
+          last_id = __shfl_sync(0xffffffffu, list.id, p.k - 1);
         }
       }
     }
@@ -295,7 +311,6 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_ker
   if (rank == 0 && warp == 0 && head > 0) singles(0, head);
 
   const int step = p.cs * kLpThreads;
-  bool first = true;
   // the next batch is on its way while this one is added up
   uint4 w[kBatch], ahead[kBatch];
   auto fetch = [&](int c0, uint4 (&v)[kBatch]) {
@@ -307,28 +322,27 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_ker
   };
   int c0 = rank * kLpThreads + warp * 32;
   fetch(c0, w);
+  if constexpr (kTop) {
+    // The bar: the k-th largest of the threads' maxima over the first batch, which k values at least reach.
+    // (Without it the first chunks would all go through the lists; from the warps' own maxima alone it
+    // would let 16 times as many values pass for the rest of the row.)
+    float most = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (c0 + b * step + lane < chunks) {
+        float2 v[V::n / 2];
+        V::unpack(w[b], v);
+#pragma unroll
+        for (int i = 0; i < V::n / 2; ++i) most = fmaxf(most, fmaxf(v[i].x, v[i].y));
+      }
+    const uint32_t mine = top_keys(order_key(most), p.k, lane);
+    sh.keys[warp][lane] = mine;
+    __syncthreads();
+    const uint32_t key = kth_of_lists(sh.keys, kLpWarps, p.k, lane);
+    if (key != 0) bar = __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+  }
   for (; c0 < chunks; c0 += kBatch * step) {
     fetch(c0 + kBatch * step, ahead);
-    if constexpr (kTop) {
-      if (first) {   // a bar for the first batch, where everything would beat the empty list: the k-th largest of
-                     // the lanes' maxima (k values at least reach it)
-        first = false;
-        float most = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-          if (c0 + b * step + lane < chunks) {
-            float2 v[V::n / 2];
-            V::unpack(w[b], v);
-#pragma unroll
-            for (int i = 0; i < V::n / 2; ++i) most = fmaxf(most, fmaxf(v[i].x, v[i].y));
-          }
-        const uint32_t bar = kth_key(order_key(most), p.k, lane);
-        if (bar != 0 && last == -INFINITY) {
-          last = __uint_as_float(bar & 0x80000000u ? bar & 0x7fffffffu : ~bar);
-          last_id = 0x7fffffff;   // (its equals go in)
-        }
-      }
-    }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int c = c0 + b * step + lane;
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_ker
         add_values<V::n / 2>(r, limit, v, vm);
       }
       if constexpr (kTop) {
-        if (__any_sync(0xffffffffu, vm >= last && vm > -INFINITY)) {
+        if (__any_sync(0xffffffffu, vm >= last && vm >= bar && vm > -INFINITY)) {
           const int id = head + c * V::n;
           const float none = -INFINITY;
 #pragma unroll
