@@ -259,7 +259,7 @@ template <bool kF32, bool kTop, int kLpThreads>
 __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_kernel(const LpParams p) {
   using V = Vec<kF32>;
   constexpr int kLpWarps = kLpThreads / 32;
-  constexpr int kBatch = 4;   // chunks in flight per thread
+  constexpr int kBatch = 4;   // chunks added up together per thread, as many more on their way
   __shared__ LpShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / (unsigned)p.cs;
@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_ker
   }
   for (; c0 < chunks; c0 += kBatch * step) {
     fetch(c0 + kBatch * step, ahead);
+    uint32_t some[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int c = c0 + b * step + lane;
@@ -355,14 +356,24 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_ker
         for (int i = 1; i < V::n / 2; ++i) vm = fmaxf(vm, fmaxf(v[i].x, v[i].y));
         add_values<V::n / 2>(r, limit, v, vm);
       }
-      if constexpr (kTop) {
-        if (__any_sync(0xffffffffu, vm >= last && vm >= bar && vm > -INFINITY)) {
-          const int id = head + c * V::n;
-          const float none = -INFINITY;
+      if constexpr (kTop)
+        some[b] = __ballot_sync(0xffffffffu, vm > -INFINITY && vm >= bar && (vm > last || (vm == last && head + c * V::n < last_id)));
+    }
+    if constexpr (kTop) {
+      // Chunks with a value that may go in, one after the other: read again, a value per lane.  (One place in the
+      // code for all of them: with the lists' code behind every value, unrolled, each use of it came from
+      // outside the instruction cache, and 128 rows of 131072 took 32 us.)
+      uint32_t any = 0;
 #pragma unroll
-          for (int i = 0; i < V::n / 2; ++i) {
-            offer(c < chunks ? v[i].x : none, id + 2 * i);
-            offer(c < chunks ? v[i].y : none, id + 2 * i + 1);
+      for (int b = 0; b < kBatch; ++b) any |= some[b];
+      if (any) {
+#pragma unroll 1
+        for (int b = 0; b < kBatch; ++b) {
+          uint32_t left = b == 0 ? some[0] : b == 1 ? some[1] : b == 2 ? some[2] : some[3];
+          while (left) {
+            const int from = __ffs(left) - 1, id = head + (c0 + b * step + from) * V::n + lane;
+            left &= left - 1;
+            offer(lane < V::n ? V::one(x, id) : -INFINITY, id);
           }
         }
       }
