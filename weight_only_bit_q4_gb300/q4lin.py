@@ -702,21 +702,25 @@ def _page_bytes(D):
     return _PAGE_BYTES[D]
 
 
-def _run(device, fn, *args):
-    """The library works on the current device: ``device`` becomes it for the call if it is another."""
-    if _torch._C._cuda_getDevice() == device.index:
+def _run(index, fn, *args):
+    """The library works on the current device: device ``index`` becomes it for the call if it is another."""
+    if _torch._C._cuda_getDevice() == index:
         st = fn(*args)
     else:
-        with _torch.cuda.device(device):
+        with _torch.cuda.device(index):
             st = fn(*args)
     if st != OK:
         raise Q4LinError(st)
 
 
-def _same_device(device, *tensors):
+def _same_device(index, *tensors):
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on one device; got {t.device} beside {device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on one device; got {t.device} beside cuda:{index}")
+
+
+def _raw_stream(stream, index):
+    return _torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _out(t, name, shape, dtype, device, stream):
@@ -739,9 +743,8 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float | None = None, out=None, 
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
     T, hq, D = q.shape
-    dev = q.device
     if out is None:
-        out = _new((T, hq, D), torch.bfloat16, dev, stream)
+        out = _new((T, hq, D), torch.bfloat16, q.device, stream)
     bf16 = torch.bfloat16
     qp, ldq, _ = _rows("q", q, D, bf16)
     kp, ldk, hk = _rows("k", k, D, bf16)
@@ -752,10 +755,11 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float | None = None, out=None, 
     S = cu_seqlens.shape[0] - 1
     if S < 0:
         raise ValueError("cu_seqlens holds one value more than there are sequences")
+    dev = q.get_device()
     _same_device(dev, k, v, cu_seqlens, out)
     _run(dev, load().q4lin_prompt_attention, qp, ldq, kp, ldk, vp, ldv,
          _need("cu_seqlens", cu_seqlens, torch.int32, (S + 1,)), op, ldo, T, S, hq, hk, D,
-         D ** -0.5 if scale is None and D else scale or 0.0, _stream_ptr(stream, dev))
+         D ** -0.5 if scale is None and D else scale or 0.0, _raw_stream(stream, dev))
     return out
 
 
@@ -789,7 +793,7 @@ def kv4_append(k, v, cache, page_table, positions, rows=None, stream=None):
     if k.dim() != 3:
         raise ValueError("k must be [T, Hk, D]")
     T, hk, D = k.shape
-    dev = k.device
+    dev = k.get_device()
     cp, tp, P, hc, S, M = _cache(cache, page_table, D)
     kp, ldk, _ = _rows("k", k, D, torch.bfloat16)
     vp, ldv, hv = _rows("v", v, D, torch.bfloat16)
@@ -800,7 +804,7 @@ def kv4_append(k, v, cache, page_table, positions, rows=None, stream=None):
     _same_device(dev, v, cache, page_table, positions, rows)
     _run(dev, load().q4lin_kv4_append, kp, ldk, vp, ldv, cp, tp,
          None if rows is None else _need("rows", rows, torch.int32, (T,)), _need("positions", positions, torch.int32, (T,)),
-         T, S, M, P, hk, D, _stream_ptr(stream, dev))
+         T, S, M, P, hk, D, _raw_stream(stream, dev))
     return cache
 
 
@@ -809,11 +813,11 @@ def kv4_read(cache, page_table, positions, D: int, rows=None, k=None, v=None, st
     tokens that are out of range are left as they are (zeros where k and v are made here)."""
     torch = _t()
     T = positions.shape[0]
-    dev = cache.device
+    dev = cache.get_device()
     cp, tp, P, hk, S, M = _cache(cache, page_table, D)
 
     def fresh():
-        t = _new((T, hk, D), torch.bfloat16, dev, stream)
+        t = _new((T, hk, D), torch.bfloat16, cache.device, stream)
         with torch.cuda.stream(stream):
             return t.zero_()
 
@@ -827,13 +831,21 @@ def kv4_read(cache, page_table, positions, D: int, rows=None, k=None, v=None, st
         raise ValueError("without rows token t belongs to sequence t: more tokens than sequences")
     _same_device(dev, page_table, positions, rows, k, v)
     _run(dev, load().q4lin_kv4_read, cp, tp, None if rows is None else _need("rows", rows, torch.int32, (T,)),
-         _need("positions", positions, torch.int32, (T,)), kp, ldk, vp, ldv, T, S, M, P, hk, D, _stream_ptr(stream, dev))
+         _need("positions", positions, torch.int32, (T,)), kp, ldk, vp, ldv, T, S, M, P, hk, D, _raw_stream(stream, dev))
     return k, v
+
+
+_KV_NEED = {}   # (S, q_len, Hq, Hk, D, max_pages): workspace bytes
 
 
 def kv4_workspace_bytes(S: int, q_len: int, Hq: int, Hk: int, D: int, max_pages: int) -> int:
     """Workspace bytes of kv4_attention."""
-    return int(load().q4lin_kv4_workspace_bytes(S, q_len, Hq, Hk, D, max_pages))
+    sizes = (S, q_len, Hq, Hk, D, max_pages)
+    if sizes not in _KV_NEED:
+        if len(_KV_NEED) > 4096:
+            _KV_NEED.clear()
+        _KV_NEED[sizes] = int(load().q4lin_kv4_workspace_bytes(*sizes))
+    return _KV_NEED[sizes]
 
 
 def kv4_attention(q, cache, page_table, lengths, scale: float | None = None, out=None, workspace=None, stream=None):
@@ -848,22 +860,21 @@ def kv4_attention(q, cache, page_table, lengths, scale: float | None = None, out
     if q.dim() != 3:
         raise ValueError("q must be [S * q_len, Hq, D]")
     T, hq, D = q.shape
-    dev = q.device
     cp, tp, P, hk, S, M = _cache(cache, page_table, D)
     n = T // S if S else 0
     if n * S != T:
         raise ValueError("q must hold the same number of tokens for every sequence")
     if out is None:
-        out = _new((T, hq, D), torch.bfloat16, dev, stream)
+        out = _new((T, hq, D), torch.bfloat16, q.device, stream)
     qp, ldq, _ = _rows("q", q, D, torch.bfloat16)
     op, ldo, ho = _rows("out", out, D, torch.bfloat16)
     if ho != hq or out.shape[0] != T:
         raise ValueError("out must have q's tokens and heads")
+    dev = q.get_device()
     _same_device(dev, cache, page_table, lengths, out, workspace)
-    lib = load()
-    ws, ws_keep = _scratch(workspace, lib.q4lin_kv4_workspace_bytes(S, n, hq, hk, D, M), dev, stream)
-    _run(dev, lib.q4lin_kv4_attention, qp, ldq, cp, tp, _need("lengths", lengths, torch.int32, (S,)), op, ldo, S, n, hq, hk, D,
-         M, P, D ** -0.5 if scale is None else scale, ws, _stream_ptr(stream, dev))
+    ws, ws_keep = _scratch(workspace, kv4_workspace_bytes(S, n, hq, hk, D, M), q.device, stream)
+    _run(dev, load().q4lin_kv4_attention, qp, ldq, cp, tp, _need("lengths", lengths, torch.int32, (S,)), op, ldo, S, n, hq, hk, D,
+         M, P, D ** -0.5 if scale is None else scale, ws, _raw_stream(stream, dev))
     return out
 
 
@@ -878,19 +889,25 @@ def token_logprobs(logits, targets, top_k: int = 0, logprobs=None, entropy=None,
     """
     torch = _t()
     T, V = logits.shape
-    dev = logits.device
-    if logits.dtype not in (torch.bfloat16, torch.float32) or not logits.is_cuda or (logits.stride(1) != 1 and V > 1):
+    if top_k < 0:
+        raise ValueError("top_k must not be negative")
+    wide = logits.dtype is torch.float32
+    if not (wide or logits.dtype is torch.bfloat16) or not logits.is_cuda or (logits.stride(1) != 1 and V > 1):
         raise ValueError("logits must be a bf16 or fp32 CUDA tensor [T, V] with contiguous rows")
     if targets.dim() not in (1, 2):
         raise ValueError("targets must be [T] or [T, n]")
     n = 1 if targets.dim() == 1 else targets.shape[1]
     f32 = torch.float32
-    _same_device(dev, targets, logprobs, entropy, top_ids, top_logprobs)
-    tok = _need("targets", targets, torch.int32, (T,) + tuple(targets.shape[1:]))
-    lp, logprobs = _out(logprobs, "logprobs", targets.shape, f32, dev, stream)
+    index, dev = logits.get_device(), logits.device
+    _same_device(index, targets, logprobs, entropy, top_ids, top_logprobs)
+    shape = targets.shape
+    if shape[0] != T:
+        raise ValueError("targets must have a row per row of logits")
+    tok = _need("targets", targets, torch.int32, shape)
+    lp, logprobs = _out(logprobs, "logprobs", shape, f32, dev, stream)
     ep, entropy = _out(entropy, "entropy", (T,), f32, dev, stream)
     ip, top_ids = _out(top_ids, "top_ids", (T, top_k), torch.int32, dev, stream)
     tp, top_logprobs = _out(top_logprobs, "top_logprobs", (T, top_k), f32, dev, stream)
-    _run(dev, load().q4lin_token_logprobs, logits.data_ptr(), 1 if logits.dtype is f32 else 0,
-         logits.stride(0) if T > 1 else V, tok, lp, ep, ip, tp, T, V, n, top_k, _stream_ptr(stream, dev))
+    _run(index, load().q4lin_token_logprobs, logits.data_ptr(), 1 if wide else 0,
+         logits.stride(0) if T > 1 else V, tok, lp, ep, ip, tp, T, V, n, top_k, _raw_stream(stream, index))
     return logprobs, entropy, top_ids, top_logprobs
