@@ -926,22 +926,23 @@ __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p
   __shared__ int ends[kKvJoin], sums[kKvJoin / 32];
   // Ahead of the wait for the first kernel stand the lengths only: that kernel lets this one start after
   // its own wait, so what it found complete is complete here.
-  const int tid = threadIdx.x, per = p.Hk * p.passes, s = blockIdx.x / per, seg = blockIdx.x - s * per;
-  const int h = seg / p.passes, pass = seg - h * p.passes, cols = min(8 * kTiles, p.cols - pass * 8 * kTiles);
+  const int tid = threadIdx.x, per = p.Hk * p.passes, lane = tid / (D / 2), d = tid - lane * (D / 2);
   const int total = kv_scan<kKvJoin>(p, ends, sums);
   const int shares = kv_shares_used(total, most);
-  const int run = (p.S + kKvJoin - 1) / kKvJoin, t = s / run;
+  const int run = (p.S + kKvJoin - 1) / kKvJoin;
+  const int64_t pitch = (int64_t)2 * kTiles * part_floats(D);
+  const int s = blockIdx.x / per, seg = blockIdx.x - s * per, h = seg / p.passes, pass = seg - h * p.passes, t = s / run;
+  const int cols = min(8 * kTiles, p.cols - pass * 8 * kTiles);
   int L, a = t > 0 ? ends[t - 1] : 0;
   for (int i = t * run; i < s; ++i) a += kv_pages(p, i, L) * per;
   const int pages = kv_pages(p, s, L);
   a += seg * pages;
-  int c0 = 0, n = 0;   // the shares of the segment
+  int c0 = 0, n = 0;   // the segment's shares
   if (pages > 0) {
     c0 = (int)((((int64_t)a + 1) * shares - 1) / total);
     n = (int)(((int64_t)(a + pages) * shares - 1) / total) - c0 + 1;
   }
   // a share's slot: 1 only where the segment begins inside it, behind another (that is its first share's case)
-  const int64_t pitch = (int64_t)2 * kTiles * part_floats(D);
   const int64_t head = n > 0 && a > kv_share_start(total, c0, shares) ? kTiles * part_floats(D) : 0;
   pdl_launch_dependents();
   pdl_wait_previous();   // (by every CTA: this kernel does not end before the first one)
@@ -992,7 +993,6 @@ __global__ void __launch_bounds__(kKvJoin) q4_kv_combine_kernel(const KvParams p
     *reinterpret_cast<uint32_t*>(row + 2 * d) =
         empty ? 0u : (uint32_t)float_to_bf16_bits(o.x * r) | (uint32_t)float_to_bf16_bits(o.y * r) << 16;
   };
-  const int lane = tid / (D / 2), d = tid - lane * (D / 2);
   float m, l;
   float2 o;
   if constexpr (!kSplit) {
@@ -1061,10 +1061,12 @@ int kv_attention_run(const KvParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   const int64_t segments = (int64_t)p.S * p.Hk * p.passes;
   const int cols = p.cols < 8 * NT * kGroup ? p.cols : 8 * NT * kGroup;
-  // rounds of eight partial sums that a thread takes: all of a column's, for its columns one after the other, or
-  // a quarter of one column's, in as many waves as the GPU holds CTAs of 256 threads
-  const int64_t parts = (sms * KvShape<NT, kGroup>::rings + segments - 1) / segments;   // (of a segment of mean length)
-  const int64_t whole = ((cols + 3) / 4) * ((parts + 7) / 8), quarter = ((segments * cols + 8 * sms - 1) / (8 * sms)) * ((parts + 31) / 32);
+  // In rounds of eight partial sums on their way, a CTA's beginning counted as two, for a segment three times as
+  // long as the mean: the columns of a segment one after the other, or a CTA per column (its groups of
+  // threads share the sums) in as many waves as the GPU holds of them, four per SM.  (16 sequences of up to
+  // 8192 tokens, 16 columns: 47 us and 35; 32 columns in two passes: 77 and 95.)
+  const int64_t parts = 3 * sms * KvShape<NT, kGroup>::rings / segments + 1, held = 4 * sms;
+  const int64_t whole = 2 + (cols + 3) / 4 * ((parts + 7) / 8), quarter = (segments * cols + held - 1) / held * (2 + (parts + 31) / 32);
   const bool split = quarter < whole;
   cfg.gridDim = dim3((unsigned)segments, (unsigned)(split ? cols : 1), 1);
   cfg.blockDim = dim3(kKvJoin, 1, 1);
