@@ -14,8 +14,8 @@
 //
 // Measured: 8192 tokens in and out, 8 heads of 128: 26.1 us (85 MB; bound by issue and by the chain of
 // position, page and row of each tile of tokens); attention of 64 sequences of up to 8192 tokens, 32 + 8
-// heads of 128: 45.2 us, 4.0 TB/s of codes and scales; five sequences of up to 70001 tokens, four new
-// tokens each, 28 + 4 heads of 96: 61.5 us; one sequence of 1000 tokens: 8.2 us.
+// heads of 128: 42.3 us, 4.3 TB/s of codes and scales; five sequences of up to 70001 tokens, four new
+// tokens each, 28 + 4 heads of 96: 59.2 us; one sequence of 1000 tokens: 7.2 us.
 #include <type_traits>
 
 #include "q4_internal.h"
@@ -285,9 +285,9 @@ int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, s
 // against a fragment of eights.
 //
 // Bound: the bytes of the codes and scales, read once per 32 columns.  Up to 8 columns the decode's issue is
-// close behind (integer pipe 48 %, 1.96 instructions a cycle); with more, the MMAs and the decode of
-// two warps per scheduler, all that two tiles' states in registers leave room for (HMMA pipe 37 %; ten or
-// twelve warps spill: 74 and 67 us for 61 on the five long sequences).
+// close behind (integer pipe 40 %, 1.5 instructions a cycle); with more, the MMAs and the decode of
+// two warps per scheduler, all that two tiles' states in registers leave room for (tensor pipe 33 %; ten or
+// twelve warps spill: 74 and 67 us where eight took 61 on the five long sequences).
 //
 // Split: the pages of all sequences and heads in a row are cut into equal shares, whatever the
 // lengths are.  A share belongs to one warp of a CTA (one CTA per SM) with a ring of record copies and

@@ -18,7 +18,7 @@
 // (distributed shared memory) are merged in order.
 //
 // Measured: 1024 rows of 131072 bf16 logits 44.6 us, 6.0 TB/s (0.90 of the measured copy rate); 75 rows of
-// 50001 FP32 logits with the top 5 15.3 us and one row of 131072 with the top 8 10.7 us, which are
+// 50001 FP32 logits with the top 5 11.0 us and one row of 131072 with the top 8 8.5 us, which are
 // the latencies of the loads, the lists and their merges (without the first batch's bar 36 and 29 us).
 #include <cfloat>
 #include <type_traits>
@@ -462,8 +462,8 @@ int lp_launch(const LpParams& p, unsigned blocks, cudaStream_t stream) {
 
 int logprobs_launch(const LogprobArgs& a) {
   LpParams p{a.logits, a.ld, a.targets, a.logprobs, a.entropy, a.top_ids, a.top_logprobs, a.T, (int)a.V, (int)a.n, a.k, 1};
-  // CTAs per row: as many as leave one per SM (75 rows of 50001 FP32 logits, top 5: 15.1 us with two, 17.7 with
-  // one, 18.7 with four), each with two batches of chunks at least
+  // CTAs per row: as many as leave one per SM (75 rows of 50001 FP32 logits, top 5: 11.0 us with two, 13.0 with
+  // one, 14.6 with four), each with two batches of chunks at least
   const int64_t chunks = a.V * (a.fp32 ? 4 : 2) / 16;
   while (p.cs < kMaxCluster && a.T * p.cs * 2 <= 152 && chunks >= (int64_t)p.cs * 2 * 512 * 2) p.cs *= 2;
   const int64_t blocks = a.T * p.cs;

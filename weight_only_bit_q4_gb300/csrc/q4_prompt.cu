@@ -28,10 +28,12 @@
 //                    that see such a key add it at the end.
 //   warp 3           finds the units, one ahead of the other roles.
 //
-// Measured: 8192 tokens, 32 + 8 heads of 128: 340 us, 1620 TFLOP/s (0.83 of the measured bf16 rate); 16384
-// tokens of seven prompts, 32 + 4 heads: 365 us; 2000 tokens of nine prompts, 28 + 4 heads of 96: 22.8 us;
-// 133 tokens: 9.9 us.  In the middle of a long prompt a block of both tiles takes 2600 to 2700 cycles, 2048
-// of them the MMAs' at their nominal rate: Q K^T reads both operands from shared memory, which at 128
+// Measured: 8192 tokens, 32 + 8 heads of 128: 330 us, 1665 TFLOP/s (0.86 of the measured bf16 rate); 16384
+// tokens of seven prompts, 32 + 4 heads: 340 us; 2000 tokens of nine prompts, 28 + 4 heads of 96: 19.1 us;
+// 133 tokens: 8.4 us.  With 8192 tokens, 32 + 8 heads of 96 take 310 us, of 64 270: softmax, P V and
+// Q K^T of one tile follow one another, and the other tile's products are too short to hide that.
+// In the middle of a long prompt (heads of 128) a block of both tiles takes 2600 to 2700 cycles, 2048 of them
+// the MMAs' at their nominal rate: Q K^T reads both operands from shared memory, which at 128
 // bytes a cycle is all it gives, and the copies write there too (105 cycles for one of these MMAs, 65
 // to 75 for one of P V).  A unit costs some 5000 cycles beyond its blocks: its first scores and its
 // last P V have nothing of their own beside them, only the neighbouring units'.
