@@ -167,3 +167,39 @@ def test_two_graphs_share_a_workspace():
         t.cuda.synchronize()
         for o, w in zip(outs, want):
             assert t.equal(o.view(t.int16), w.view(t.int16))
+
+
+@pytest.mark.parametrize("lens,Hq,Hk,D", [([391, 346], 21, 7, 128), ([700, 3, 300], 4, 4, 64), ([600, 401], 6, 3, 96),
+                                          ([1100], 3, 1, 40)])
+def test_prompts_from_a_cold_cache(lens, Hq, Hk, D):
+    """Blocks that arrive late: another buffer, larger than the L2 cache, is written ahead of every call."""
+    t = torch()
+    T = sum(lens)
+    q, k, v = (bits((T, h, D), i, s) for i, h, s in ((1, Hq, 1.5), (2, Hk, 1.0), (3, Hk, 1.0)))
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    qd, kd, vd, cd = x_to_dev(q), x_to_dev(k), x_to_dev(v), dev(cu)
+    want = q4lin.prompt_attention(qd, kd, vd, cd)
+    want = q4lin.prompt_attention(qd, kd, vd, cd)
+    check_prompt(y_bits(want), q, k, v, cu)
+    other = t.empty(1 << 28, dtype=t.uint8, device="cuda")
+    for i in range(20):
+        other.fill_(i)
+        t.cuda.synchronize()
+        assert t.equal(q4lin.prompt_attention(qd, kd, vd, cd).view(t.int16), want.view(t.int16))
+
+
+def test_cache_and_logits_from_a_cold_cache():
+    t = torch()
+    cache, table = filled(3, [3000, 40, 1900], 47, 2, 96, 3)
+    c, tb, ln = dev(cache), dev(table), dev(np.array([3000, 40, 1900], dtype=np.int32))
+    qs = [x_to_dev(bits((3 * n, 6, 96), n)) for n in (1, 4, 9)]
+    x = x_to_dev(bits((40, 30011), 5, 3.0))
+    tok = t.arange(40, dtype=t.int32, device="cuda")[:, None]
+    run = lambda: [q4lin.kv4_attention(q, c, tb, ln) for q in qs] + list(q4lin.token_logprobs(x, tok, 5))
+    want = run()
+    other = t.empty(1 << 28, dtype=t.uint8, device="cuda")
+    for i in range(10):
+        other.fill_(i)
+        t.cuda.synchronize()
+        for a, b in zip(run(), want):
+            assert t.equal(a.view(t.int16 if a.dtype == t.bfloat16 else t.int32), b.view(t.int16 if a.dtype == t.bfloat16 else t.int32))

@@ -592,6 +592,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
         const int n = max(w.n0, w.n1);
         // block i of the loop is keys (n - 1 - i) * 128 on; tile x takes part from its own last block on
         const int from0 = n - w.n0, from1 = w.n1 > 0 ? n - w.n1 : n;
+        // (A begins with the second block: it has had no P yet, so no word of that block's K either)
+        if (from0 > 0 && !wait(base + SM::kf + 8 * ks, kph)) break;
         for (int i = 0; i < n; ++i) {
           const bool more = i + 1 < n;
           if (i == max(0, n - 4)) commit(base + SM::go);
