@@ -203,3 +203,35 @@ def test_cache_and_logits_from_a_cold_cache():
         t.cuda.synchronize()
         for a, b in zip(run(), want):
             assert t.equal(a.view(t.int16 if a.dtype == t.bfloat16 else t.int32), b.view(t.int16 if a.dtype == t.bfloat16 else t.int32))
+
+
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (3, 1)])
+def test_rows_of_prompts_behind_the_4_gib_mark(Hq, Hk):
+    """Heads as columns of very wide rows, with values that are not finite (which are fetched again by their addresses)."""
+    t = torch()
+    T, D, wide = 310, 64, 1 << 23
+    cu = np.array([0, 30, 310], dtype=np.int32)
+    wq, wk, wv = bits((T, Hq, D), 1), bits((T, Hk, D), 2), bits((T, Hk, D), 3)
+    wv[300, 0, 5], wv[40, -1, 60] = 0x7F80, 0x7FC0
+    rows = t.empty((T, wide), dtype=t.bfloat16, device="cuda")
+    parts, at = [], 8
+    for x in (wq, wk, wv, np.zeros_like(wq)):
+        part = rows[:, at:at + x.shape[1] * D].unflatten(1, (x.shape[1], D))
+        part.copy_(x_to_dev(x))
+        parts.append(part)
+        at = wide - 40 * D if at == 8 else at + x.shape[1] * D
+    q, k, v, out = parts
+    assert 256 * wide * 2 == 4 << 30   # rows 256 and on
+    got = q4lin.prompt_attention(q, k, v, dev(cu), out=out)
+    check_prompt(y_bits(got.contiguous()), wq, wk, wv, cu)
+    assert t.equal(q.contiguous().view(t.int16), x_to_dev(wq).view(t.int16))
+
+
+def test_rows_of_logits_behind_the_4_gib_mark():
+    t = torch()
+    x = bits((3, 5000), 4, 3.0)
+    rows = t.empty((2 * ((1 << 31) + 8) + 5000,), dtype=t.bfloat16, device="cuda").as_strided((3, 5000), ((1 << 31) + 8, 1))
+    rows.copy_(x_to_dev(x))
+    tok = dev(np.array([[7], [4999], [0]], dtype=np.int32))
+    for a, b in zip(q4lin.token_logprobs(rows, tok, 4), q4lin.token_logprobs(x_to_dev(x), tok, 4)):
+        assert t.equal(a, b)
