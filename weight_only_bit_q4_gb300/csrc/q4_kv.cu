@@ -887,12 +887,14 @@ __global__ void __launch_bounds__(KvShape<NT, kGroup>::threads, 1) q4_kv_attenti
         __syncwarp();
         issue();
       } else {
-        // the record before this one is refilled: the group's other warps are likely done with it
+        // The record before this one is refilled: the group's other warps are likely done with it.  Every warp waits
+        // for that: a run of pages that are not there has no copies to hold the others back, and the phase's one
+        // bit does not tell two rounds of the ring apart.
         warp_release(bars + 16u * (uint32_t)s + 8, lane);
         const int b = used - 1;
         ++used;
         if (b >= 0) {
-          if (member == 0 && next < u1) {
+          if (next < u1) {
             ok = kv_wait(bars + 16u * (uint32_t)(b % kStages) + 8, (uint32_t)(b / kStages) & 1u, &abort_flag, &g_kv_status);
             if (!ok) break;
           }
