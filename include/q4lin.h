@@ -370,7 +370,8 @@ int q4lin_kv4_read(const uint8_t* cache, const int32_t* page_table, const int32_
  * A token that sees nothing gives zeros.  lengths int32 [S] (taken into [0, 64 max_pages]).  Tokens
  * of a page whose id lies outside [0, pages) are left out.
  *   q, out bf16 [S * q_len rows], strides and alignment as above; out must not overlap q
- *   workspace: >= q4lin_kv4_workspace_bytes(...) bytes, 256-byte aligned
+ *   workspace: >= q4lin_kv4_workspace_bytes(...) bytes, asked for with the call's device as the
+ *     current one (the answer goes by its number of SMs), 256-byte aligned
  * The codes' products are exact, q enters exactly down to 2^-28 of its head's largest value, group
  * scales, maxima and sums are FP32; each weight times its token's scale enters the product with
  * the codes as fp16 (2^-12 of it).  A cache may hold more than 2^32 values.  Two kernels.

@@ -835,17 +835,21 @@ def kv4_read(cache, page_table, positions, D: int, rows=None, k=None, v=None, st
     return k, v
 
 
-_KV_NEED = {}   # (S, q_len, Hq, Hk, D, max_pages): workspace bytes
+_KV_NEED = {}   # (device, S, q_len, Hq, Hk, D, max_pages): workspace bytes
 
 
-def kv4_workspace_bytes(S: int, q_len: int, Hq: int, Hk: int, D: int, max_pages: int) -> int:
-    """Workspace bytes of kv4_attention."""
+def kv4_workspace_bytes(S: int, q_len: int, Hq: int, Hk: int, D: int, max_pages: int, device: int | None = None) -> int:
+    """Workspace bytes of kv4_attention on a device (its index; None: the current one)."""
     sizes = (S, q_len, Hq, Hk, D, max_pages)
-    if sizes not in _KV_NEED:
+    if device is None:
+        return int(load().q4lin_kv4_workspace_bytes(*sizes))
+    key = (device, *sizes)
+    if key not in _KV_NEED:
         if len(_KV_NEED) > 4096:
             _KV_NEED.clear()
-        _KV_NEED[sizes] = int(load().q4lin_kv4_workspace_bytes(*sizes))
-    return _KV_NEED[sizes]
+        with _t().cuda.device(device):   # (the library answers for the current device)
+            _KV_NEED[key] = int(load().q4lin_kv4_workspace_bytes(*sizes))
+    return _KV_NEED[key]
 
 
 def kv4_attention(q, cache, page_table, lengths, scale: float | None = None, out=None, workspace=None, stream=None):
@@ -872,7 +876,7 @@ def kv4_attention(q, cache, page_table, lengths, scale: float | None = None, out
         raise ValueError("out must have q's tokens and heads")
     dev = q.get_device()
     _same_device(dev, cache, page_table, lengths, out, workspace)
-    ws, ws_keep = _scratch(workspace, kv4_workspace_bytes(S, n, hq, hk, D, M), q.device, stream)
+    ws, ws_keep = _scratch(workspace, kv4_workspace_bytes(S, n, hq, hk, D, M, dev), q.device, stream)
     _run(dev, load().q4lin_kv4_attention, qp, ldq, cp, tp, _need("lengths", lengths, torch.int32, (S,)), op, ldo, S, n, hq, hk, D,
          M, P, D ** -0.5 if scale is None else scale, ws, _raw_stream(stream, dev))
     return out
