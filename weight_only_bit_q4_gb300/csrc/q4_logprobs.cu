@@ -109,9 +109,10 @@ __device__ __forceinline__ void list_insert(TopList& l, float x, int id, int k, 
   }
 }
 
-// Floats above -inf as integers in their order, above 0 (-inf and NaN: 0).
+// Floats above -inf as integers in their order, above 0 (-inf and NaN: 0).  Equal floats have equal keys: adding 0
+// makes -0 a +0.
 __device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(v);
+  const uint32_t b = __float_as_uint(v + 0.f);
   return v > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
 }
 
