@@ -73,15 +73,16 @@ __device__ __forceinline__ float2 lp_fmul2(float2 a, float2 b) {
 
 // Sums about the reference m (in units of ln 2 for a): s = sum 2^t, a = sum 2^t t.
 struct Sums {
-  float m, s, a, top;   // top: the largest logit so far; -inf: none (the reference is at most FLT_MAX)
+  float m, s, a, top;   // top: the largest logit so far; -inf: none
 };
 
-// The sums of `o` brought to the reference of `r` (o.m <= r.m up to rounding, or o empty).
+// The sums of `o` brought to the reference m (o.m <= m up to rounding, or o empty).  About +inf they hold the
+// number of infinite logits, and what is finite has nothing.
 __device__ __forceinline__ void shift_to(float m, Sums& o) {
   if (o.s == 0.f) {
     o.a = 0.f;
   } else {
-    const float t = (o.m - m) * kLog2e, f = ex2(t);
+    const float t = o.m == m ? 0.f : (o.m - m) * kLog2e, f = ex2(t);
     o.a = f == 0.f && o.s == o.s ? 0.f : f * (o.a + o.s * t);
     o.s *= f;
   }
@@ -198,11 +199,10 @@ struct Vec<true> {
 template <int NP>
 __device__ __forceinline__ void add_values(Sums& r, float& limit, const float2 (&x)[NP], float vm) {
   if (vm > limit) {   // (the first values at all, or far above the reference)
-    const float m = fminf(vm, FLT_MAX);
-    shift_to(m, r);
-    limit = m + kSlack;
+    shift_to(vm, r);
+    limit = vm + kSlack;
     if (vm == INFINITY) {   // every +inf counts as 1, whatever is finite as 0
-      limit = FLT_MAX;
+      limit = FLT_MAX;      // (the next one comes here too)
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float e[2] = {x[i].x, x[i].y};
@@ -243,16 +243,14 @@ __device__ __forceinline__ Sums warp_join(Sums r) {
   float m = r.top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = fminf(m, FLT_MAX);
-  if (m > -INFINITY) shift_to(ref, r);
+  if (m > -INFINITY) shift_to(m, r);
   // a fixed tree: the same bits every time
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
     r.a += __shfl_xor_sync(0xffffffffu, r.a, o);
   }
-  r.m = ref;
-  r.top = m;
+  r.m = r.top = m;
   return r;
 }
 
