@@ -2,10 +2,13 @@
 //
 // For a row x of V logits, M = max x, S = sum e^(x_v - M):
 //     logp(v) = x_v - M - ln S,     entropy = ln S - (sum e^(x_v - M) (x_v - M)) / S,
-// and the k largest x in order, ties by the lowest token.  Both terms of the entropy are >= 0,
-// so nothing cancels.  FP32 sums; every thread's are taken about a reference of its own that
-// moves only when a logit lies more than kSlack above it (the sums then hold terms up to
-// e^kSlack, far from FP32's end), and are brought to M at the end.
+// and the k largest x in order, ties by the lowest token.  FP32 sums; every thread's are taken about a
+// reference of its own that moves only when a logit lies more than kSlack above it, and are brought to M at
+// the end.  Both terms of the entropy are >= 0 about M; about a thread's own reference its second sum
+// holds terms of both signs, up to kSlack / ln 2 times the first, so what is left of it at M is off by some
+// kSlack 2^-23 of the terms above the reference.  With kSlack 8 that is 1e-6 where the entropy is not small,
+// and nothing where one logit stands further out (then it is the reference); what rounding leaves below
+// 0 is 0.  (With kSlack 40 rows certain to 1e-12 came out as up to 1e-6 of either sign.)
 //
 // Bound: the bytes of the logits, read once.  One pass: the exponentials, both sums, the
 // maximum and the candidates of the top list come from the same registers.
@@ -33,7 +36,7 @@ namespace {
 constexpr int kLpMaxWarps = 16;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
-constexpr float kSlack = 40.f;
+constexpr float kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -421,7 +424,8 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) q4_logprobs_ker
     if (lane == 0) {
       sh.row[0] = r.top;
       sh.row[1] = none ? INFINITY : ls;
-      if (p.entropy != nullptr) p.entropy[row] = none ? 0.f : ls - r.a / r.s * kLn2;
+      const float h = ls - r.a / r.s * kLn2;
+      if (p.entropy != nullptr) p.entropy[row] = none || h < 0.f ? 0.f : h;
     }
     if (kTop && lane < p.k) {
       p.ids[row * p.k + lane] = list.id;
