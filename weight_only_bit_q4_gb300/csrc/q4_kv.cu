@@ -277,7 +277,7 @@ int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, s
 // by one AND per pair (q 2^-24; the odd nibbles 16 q 2^-24 meet q / 16), the query enters as fp16
 // at a power of two per column that puts its largest value in [2^14, 2^15) (exact down to 2^-28 of
 // that), every scale group sums in FP32 and is scaled there:
-//     x = sum_g s_g (F D_g + Z_g),  F = 2^24 2^e scale log2 e,  Z_g = -8 sum x scale log2 e.
+//     x = sum_g s_g (F D_g + Z_g),  F = 2^24 2^e scale log2 e,  Z_g = -8 2^-24 F sum (x 2^-e).
 // Values O^T = V^T P^T likewise, with P_j s_j (per scale group) as the fp16 operand: its rounding,
 // 2^-12 of each weight, is an eighth of the output's own.  The reference m of a column absorbs
 // the scales' size (m >= max x log2 e + log2 of the page's largest V scale - 14), so that P s
@@ -511,8 +511,8 @@ struct KvQuery {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[i] = (i & 1 ? bf16hi(ws[i >> 1]) : bf16lo(ws[i >> 1]));
-          sum += x[i];
           x[i] = x[i] * down * down2;
+          sum += x[i];
         }
         zg[j >> 1] += sum;
         b[t][j][0] = pack_f16(x[0], x[4]);
@@ -520,13 +520,15 @@ struct KvQuery {
         b[t][j][2] = pack_f16(x[2], x[6]);
         b[t][j][3] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
       }
-      // (2^(24 + e) may pass FP32's range only where the scores do)
-      const float fc = exp2i(min(24 + e, 127)) * p.c;
+      // 2^(24 + e) c in two steps, and the zero points' sums over the scaled values: neither leaves FP32's range
+      // before the scores do
+      const int half = (24 + e) / 2;
+      const float fc = p.c * exp2i(half) * exp2i(24 + e - half);
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 1);
         zg[i] += __shfl_xor_sync(0xffffffffu, zg[i], 2);
-        zg[i] *= -8.f * p.c;
+        zg[i] *= -8.f / 16777216.f * fc;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
