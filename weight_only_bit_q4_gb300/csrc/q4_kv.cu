@@ -281,7 +281,8 @@ int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, s
 // Values O^T = V^T P^T likewise, with P_j s_j (per scale group) as the fp16 operand: its rounding,
 // 2^-12 of each weight, is an eighth of the output's own.  The reference m of a column absorbs
 // the scales' size (m >= max x log2 e + log2 of the page's largest V scale - 14), so that P s
-// stays below 2^15 whatever the scales are.  The zero points' share, 8 sum P s, comes from one more MMA
+// stays below 2^15 whatever the scales are; what lies 2^28 and more below a page's largest weight times its
+// largest scale is a subnormal fp16, off by up to 2^-38 of that product.  The zero points' share, 8 sum P s, comes from one more MMA
 // against a fragment of eights.
 //
 // Bound: the bytes of the codes and scales, read once per 32 columns.  Up to 8 columns the decode's issue is
@@ -555,6 +556,12 @@ __device__ __forceinline__ void kv_scales(const uint8_t* at, float (&v)[G]) {
   }
 }
 
+// e with v < 2^e, from fp16's smallest to its largest (infinity counts as that), of v >= 0: the exponent's field as the
+// mantissa of 2^23, which takes no conversion.
+__device__ __forceinline__ float kv_exponent(float v) {
+  return __uint_as_float(0x4B000000u + min(max(__float_as_uint(v) >> 23, 127u - 25u), 127u + 15u)) - (8388608.f + 126.f);
+}
+
 // One page (64 tokens from token0 on) joins the warp's state; kEnd: not every column sees all of it.
 template <int J, int NT, bool kEnd>
 __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>& qy, const uint8_t* rec, int token0, int lane) {
@@ -638,23 +645,40 @@ __device__ __forceinline__ void kv_page(KvState<J, NT>& st, const KvQuery<J, NT>
       for (int i = 0; i < G; ++i) vtop = fmaxf(vtop, fabsf(vs[mt][r][i]));
     }
   }
+  // What a column's reference has to stay above, + 14: its largest x plus the exponent of the page's largest V scale
+  // (NaN does not count).  At a sequence's end the columns see different tokens, and one's scale must not
+  // cost the others their bits: there every x is taken with its own token's scale.
   float top[NT][2];
+  if constexpr (kEnd) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) top[t][0] = top[t][1] = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      top[t][k] = fmaxf(fmaxf(fmaxf(x[0][t][k], x[0][t][2 + k]), fmaxf(x[1][t][k], x[1][t][2 + k])),
-                        fmaxf(fmaxf(x[2][t][k], x[2][t][2 + k]), fmaxf(x[3][t][k], x[3][t][2 + k])));
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float ve = kv_exponent(G == 2 ? fmaxf(fabsf(vs[mt][r][0]), fabsf(vs[mt][r][G - 1])) : fabsf(vs[mt][r][0]));
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) top[t][k] = fmaxf(top[t][k], x[mt][t][2 * r + k] + ve);
+      }
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        top[t][k] = fmaxf(fmaxf(fmaxf(x[0][t][k], x[0][t][2 + k]), fmaxf(x[1][t][k], x[1][t][2 + k])),
+                          fmaxf(fmaxf(x[2][t][k], x[2][t][2 + k]), fmaxf(x[3][t][k], x[3][t][2 + k])));
+  }
 #pragma unroll
   for (int o = 4; o <= 16; o <<= 1) {
-    vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+    if (!kEnd) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) top[t][k] = fmaxf(top[t][k], __shfl_xor_sync(0xffffffffu, top[t][k], o));
   }
-  // the page's largest V scale is below 2^ve
-  const float ve = (float)(max((int)(__float_as_uint(vtop) >> 23), 127 - 25) - 126);
+  const float ve = kEnd ? 0.f : kv_exponent(vtop);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     top[t][0] += ve - 14.f;
