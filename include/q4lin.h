@@ -322,8 +322,8 @@ int q4lin_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_
  *     it).  Sequences may be empty.  Rows of out before the first and behind the last one stay as
  *     they are.
  *   D a multiple of 8 up to 128; Hq a multiple of Hk; strides (in elements) multiples of 8 and at
- *     least heads * D; q, k, v, out 16-byte aligned; scale finite.
- * Scores, maxima and sums are FP32; the weights p enter the product with v as bf16 (2^-9 each).
+ *     least heads * D; q, k, v, out 16-byte aligned; scale finite, up to 2.35e38.
+ * q . k, scores, maxima and sums are FP32; the weights p enter the product with v as bf16 (2^-9 each).
  * Inf and NaN in k or v reach only rows that see that token.  A row whose scores are all -inf, or
  * one of +inf or NaN, gives NaN.  One kernel, no workspace.
  */
@@ -369,7 +369,8 @@ int q4lin_kv4_read(const uint8_t* cache, const int32_t* page_table, const int32_
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  head h over the cache's h / (Hq / Hk).
  * A token that sees nothing gives zeros.  lengths int32 [S] (taken into [0, 64 max_pages]).  Tokens
  * of a page whose id lies outside [0, pages) are left out.
- *   q, out bf16 [S * q_len rows], strides and alignment as above; out must not overlap q
+ *   q, out bf16 [S * q_len rows], strides and alignment as above; out must not overlap q;
+ *     scale finite, up to 2.35e38
  *   workspace: >= q4lin_kv4_workspace_bytes(...) bytes, asked for with the call's device as the
  *     current one (the answer goes by its number of SMs), 256-byte aligned
  * The codes' products are exact, q enters exactly down to 2^-28 of its head's largest value, group

@@ -474,11 +474,14 @@ int check_rows(const char* what, const void* ptr, int64_t ld, int64_t T, int64_t
   return Q4LIN_OK;
 }
 
+// scale * log2 e, which the kernels take, is finite.
+bool scale_ok(float scale) { return scale >= -FLT_MAX / 1.4427f && scale <= FLT_MAX / 1.4427f; }
+
 int run_prompt(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
                const int32_t* cu, uint16_t* out, int64_t ldo, int64_t T, int64_t S, int64_t Hq, int64_t Hk, int64_t D,
                float scale, void* stream) {
   if (T < 0 || S < 0 || Hq < 0 || Hk < 0 || D < 0) return Q4LIN_ERR_INVALID_ARG;
-  if (!(scale >= -FLT_MAX && scale <= FLT_MAX)) return refuse("prompt_attention: the scale must be a finite number");
+  if (!scale_ok(scale)) return refuse("prompt_attention: the scale must be a finite number up to 2.35e38");
   if (D % 8 != 0 || D > 128) return refuse("prompt_attention: D a multiple of 8 up to 128", Q4LIN_ERR_UNSUPPORTED_SHAPE);
   if (Hq > 65536 || Hk > 65536 || T >= (int64_t)1 << 31 || S >= (int64_t)1 << 31) return Q4LIN_ERR_INVALID_ARG;
   if (T == 0 || S == 0 || Hq == 0 || D == 0) return Q4LIN_OK;
@@ -558,7 +561,7 @@ int run_kv_attention(const uint16_t* q, int64_t ldq, const uint8_t* cache, const
   int st = validate_kv_attention(S, q_len, Hq, Hk, D, max_pages);
   if (st == Q4LIN_OK) st = validate_cache(pages, S, max_pages, Hk, D);
   if (st != Q4LIN_OK) return st;
-  if (!(scale >= -FLT_MAX && scale <= FLT_MAX)) return refuse("kv4_attention: the scale must be a finite number");
+  if (!scale_ok(scale)) return refuse("kv4_attention: the scale must be a finite number up to 2.35e38");
   if (S == 0 || q_len == 0 || Hq == 0) return Q4LIN_OK;
   static const char* const kShort = "kv4_attention: a row stride is shorter than the heads of a row (or overflows)";
   st = check_rows(kShort, q, ldq, S * q_len, Hq, D);
