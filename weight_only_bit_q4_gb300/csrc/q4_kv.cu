@@ -12,10 +12,11 @@
 //      byte 16 c + 4 j + 2 e + h (j = o / 16, h = o % 16 / 8, c = o % 8 / 2, e = o % 2): word j of
 //      thread c holds its four tokens of k-step j, two values each.
 //
-// Measured: 8192 tokens in and out, 8 heads of 128: 26.1 us (85 MB; bound by issue and by the chain of
-// position, page and row of each tile of tokens); attention of 64 sequences of up to 8192 tokens, 32 + 8
-// heads of 128: 42.3 us, 4.3 TB/s of codes and scales; five sequences of up to 70001 tokens, four new
-// tokens each, 28 + 4 heads of 96: 59.2 us; one sequence of 1000 tokens: 7.2 us.
+// Measured (captured calls): 8192 tokens in and out, 8 heads of 128: 26.3 us (85 MB; bound by issue and by the
+// chain of position, page and row of each tile of tokens); attention of 64 sequences of up to 8192
+// tokens, 32 + 8 heads of 128: 42.7 us, 4.3 TB/s of codes and scales, with four new tokens each (16 columns)
+// 75; five sequences of up to 70001 tokens, four new tokens each, 28 + 4 heads of 64, 96, 128: 44, 59,
+// 72 us; one sequence of 1000 tokens: 7.5 us.
 #include <type_traits>
 
 #include "q4_internal.h"
@@ -287,8 +288,10 @@ int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, s
 //
 // Bound: the bytes of the codes and scales, read once per 32 columns.  Up to 8 columns the decode's issue is
 // close behind (integer pipe 40 %, 1.5 instructions a cycle); with more, the MMAs and the decode of
-// two warps per scheduler, all that two tiles' states in registers leave room for (tensor pipe 33 %; ten or
-// twelve warps spill: 74 and 67 us where eight took 61 on the five long sequences).
+// two warps per scheduler, all that two tiles' states in registers leave room for (tensor pipe 33 %; with heads of
+// 96 ten or twelve warps spill: 74 and 67 us where eight took 61 on the five long sequences).  Heads of
+// 128 do not fit with eight warps either: 156 to 172 bytes a thread are spilled, some of them in the
+// loop over pages.
 //
 // Split: the pages of all sequences and heads in a row are cut into equal shares, whatever the
 // lengths are.  A share belongs to one warp of a CTA (one CTA per SM) with a ring of record copies and
@@ -316,7 +319,7 @@ constexpr int kKvRecords = 24;    // records in shared memory, over all rings
 // a ring and its pages.
 template <int NT, int kGroup>
 struct KvShape {
-  static constexpr int warps = NT == 1 ? 12 : 8;   // (the registers of two tiles' states leave no more)
+  static constexpr int warps = NT == 1 ? 12 : 8;   // (two tiles' states leave no more; heads of 128 spill)
   static constexpr int threads = 32 * warps;
   static constexpr int rings = warps / kGroup, stages = kKvRecords / rings;
 };

@@ -20,9 +20,11 @@
 // first few: a bar made of all threads' maxima over their first batch stands before the lists.  Warps, then CTAs
 // (distributed shared memory) are merged in order.
 //
-// Measured: 1024 rows of 131072 bf16 logits 44.6 us, 6.0 TB/s (0.90 of the measured copy rate); 75 rows of
-// 50001 FP32 logits with the top 5 11.0 us and one row of 131072 with the top 8 8.5 us, which are
-// the latencies of the loads, the lists and their merges (without the first batch's bar 36 and 29 us).
+// Measured (captured calls): 1024 rows of 131072 bf16 logits 44.5 us, 6.0 TB/s (0.90 of the measured copy rate); 75
+// rows of 50001 FP32 logits with the top 5 11.1 us and one row of 131072 with the top 8 8.6 us, which are
+// the latencies of the loads, the lists and their merges (without the first batch's bar 36 and 29 us).  The
+// lists show with many rows too: 128, 256, 512 rows of 131072 take 13.8, 14.8, 27.5 us, with the top 8
+// 24.8, 26.3, 47.7.
 #include <cfloat>
 #include <type_traits>
 
@@ -465,8 +467,9 @@ int lp_launch(const LpParams& p, unsigned blocks, cudaStream_t stream) {
 
 int logprobs_launch(const LogprobArgs& a) {
   LpParams p{a.logits, a.ld, a.targets, a.logprobs, a.entropy, a.top_ids, a.top_logprobs, a.T, (int)a.V, (int)a.n, a.k, 1};
-  // CTAs per row: as many as leave one per SM (75 rows of 50001 FP32 logits, top 5: 11.0 us with two, 13.0 with
-  // one, 14.6 with four), each with two batches of chunks at least
+  // CTAs per row: as many as leave one per SM, each with two batches of chunks at least.  (Measured at one
+  // shape: 75 rows of 50001 FP32 logits, top 5, 11.0 us with two, 13.0 with one, 14.6 with four.  It leaves 77
+  // to 152 rows of any length one CTA each.)
   const int64_t chunks = a.V * (a.fp32 ? 4 : 2) / 16;
   while (p.cs < kMaxCluster && a.T * p.cs * 2 <= 152 && chunks >= (int64_t)p.cs * 2 * 512 * 2) p.cs *= 2;
   const int64_t blocks = a.T * p.cs;
