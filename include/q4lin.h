@@ -324,8 +324,9 @@ int q4lin_qk_norm_rope(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_
  *   D a multiple of 8 up to 128; Hq a multiple of Hk; strides (in elements) multiples of 8 and at
  *     least heads * D; q, k, v, out 16-byte aligned; scale finite, up to 2.35e38.
  * q . k, scores, maxima and sums are FP32; the weights p enter the product with v as bf16 (2^-9 each).
- * Inf and NaN in k or v reach only rows that see that token.  A row whose scores are all -inf, or
- * one of +inf or NaN, gives NaN.  One kernel, no workspace.
+ * Inf and NaN in k or v reach only rows that see that token; a weight of 0 (a score of -inf) times
+ * one of them is NaN.  A row whose scores are all -inf, or one of +inf or NaN, gives NaN.  One
+ * kernel, no workspace.
  */
 int q4lin_prompt_attention(const uint16_t* q, int64_t ldq, const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
                            const int32_t* cu_seqlens, uint16_t* out, int64_t ldo, int64_t T, int64_t S, int64_t Hq,

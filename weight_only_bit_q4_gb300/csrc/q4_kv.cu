@@ -283,8 +283,8 @@ int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, s
 // 2^-12 of each weight, is an eighth of the output's own.  The reference m of a column absorbs
 // the scales' size (m >= max x log2 e + log2 of the page's largest V scale - 14), so that P s
 // stays below 2^15 whatever the scales are; what lies 2^28 and more below a page's largest weight times its
-// largest scale is a subnormal fp16, off by up to 2^-38 of that product.  The zero points' share, 8 sum P s, comes from one more MMA
-// against a fragment of eights.
+// largest scale is a subnormal fp16, off by up to 2^-38 of that product.  The zero points' share,
+// 8 sum P s, comes from one more MMA against a fragment of eights.
 //
 // Bound: the bytes of the codes and scales, read once per 32 columns.  Up to 8 columns the decode's issue is
 // close behind (integer pipe 40 %, 1.5 instructions a cycle); with more, the MMAs and the decode of

@@ -61,9 +61,9 @@ __device__ int g_prompt_status = 0;
 
 struct PtParams {
   CUtensorMap mq, mk, mv;   // (D, heads, T, 1)
-  const uint16_t* v;
+  const uint16_t *k, *v;
   uint16_t* out;
-  int64_t ldv, ldo;
+  int64_t ldk, ldv, ldo;
   const int32_t* cu;        // [S + 1]
   int64_t T;
   int S, Hq, Hk, G, D;
@@ -159,6 +159,14 @@ __device__ __forceinline__ uint4 finite_only(uint4 w) {
     if ((x[i] & 0x7F800000u) == 0x7F800000u) x[i] &= 0xFFFFu;
   }
   return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// Whether one of a row's D values is.  (Not inlined: it is hardly ever called, and its code changed the order of the
+// kernel's own: 336 us for 329.)
+__device__ __noinline__ bool pt_not_finite(const uint16_t* x, int D) {
+  bool any = false;
+  for (int d = 0; d < D; d += 8) any = any || not_finite(ld_global_u4(x + d));
+  return any;
 }
 
 // A unit of work: rows [row0, row0 + len) are its sequence, tiles A and B start at rows q0, q1 of it and
@@ -477,7 +485,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
       if (!wait(base + SM::of + 8 * x, oph)) break;
       oph ^= 1u;
       tc_fence_after();
-      const float inv = 1.f / (l.x + l.y);
+      const float sum = l.x + l.y, inv = sum > 0.f ? 1.f / sum : __int_as_float(0x7FC00000);   // (no weight at all: NaN)
       const bool odd = odd_flag != 0;
       uint16_t* dst = p.out + ((int64_t)w.row0 + row) * p.ldo + (int64_t)(w.head + (p.heads2 ? x : 0)) * p.D;
 #pragma unroll 1
@@ -493,11 +501,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) q4_prompt_kernel(const __grid_c
               if (32 * j + 8 * b >= p.D) break;
               const uint4 v = ld_global_u4(src + 8 * b);
               if (!not_finite(v)) continue;
+              // (a score that is not finite is -inf, or the row is NaN in any case: weight 0 times this value)
+              const bool none = pt_not_finite(p.k + ((int64_t)w.row0 + key) * p.ldk + (int64_t)(w.head / p.G) * p.D, p.D);
               const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const float val = e & 1 ? bf16hi(vs[e >> 1]) : bf16lo(vs[e >> 1]);
-                if (!(fabsf(val) <= FLT_MAX)) o[8 * b + e] = __float_as_uint(__uint_as_float(o[8 * b + e]) + val);
+                if (!(fabsf(val) <= FLT_MAX))
+                  o[8 * b + e] = none ? 0x7FC00000u : __float_as_uint(__uint_as_float(o[8 * b + e]) + val);
               }
             }
           }
@@ -850,8 +861,10 @@ int prompt_launch(const PromptArgs& a) {
     set_error_detail("prompt_attention: the tensors cannot be described to the copy engine");
     return Q4LIN_ERR_CUDA;
   }
+  p.k = a.k;
   p.v = a.v;
   p.out = a.out;
+  p.ldk = a.ldk;
   p.ldv = a.ldv;
   p.ldo = a.ldo;
   p.cu = a.cu;
