@@ -378,7 +378,8 @@ int q4lin_kv4_read(const uint8_t* cache, const int32_t* page_table, const int32_
  * scales, maxima and sums are FP32; each weight times its token's scale enters the product with
  * the codes as fp16 (off by 2^-12 of it, or by 2^-38 of the largest weight times the largest scale,
  * 65504 for an infinite one, of a page where that is more; tokens that a row does not see do not
- * count).  A cache may hold more than 2^32 values.  Two kernels.
+ * count).  Of every 16 tokens (16 i to 16 i + 15) products with codes below 2^-15 of their largest
+ * weight times scale are cut off, in all at most 17 2^-15 of that.  A cache may hold more than 2^32 values.  Two kernels.
  */
 size_t q4lin_kv4_workspace_bytes(int64_t S, int64_t q_len, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages);
 int q4lin_kv4_attention(const uint16_t* q, int64_t ldq, const uint8_t* cache, const int32_t* page_table,

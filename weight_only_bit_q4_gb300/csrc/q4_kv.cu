@@ -284,7 +284,13 @@ int pdl_launch(Kernel kernel, const char* what, dim3 blocks, unsigned threads, s
 // the scales' size (m >= max x log2 e + log2 of the page's largest V scale - 14), so that P s
 // stays below 2^15 whatever the scales are; what lies 2^28 and more below a page's largest weight times its
 // largest scale is a subnormal fp16, off by up to 2^-38 of that product.  The zero points' share,
-// 8 sum P s, comes from one more MMA against a fragment of eights.
+// 8 sum P s, comes from one more MMA against a fragment of eights.  A subnormal operand is aligned by its
+// exponent, not by its leading bit: of the 16 tokens of an MMA, products below 2^-15 of the largest P s
+// (odd values 2^-19) are cut off, at most 17 2^-15 of it in all.  That is as much as the
+// output's own rounding where that token's value is of its scale's size, and matters only to what stands beside a value
+// of 0.  Codes shifted up by 6 bits in their halves would leave 2^-21, for three more shifts a word (64 sequences
+// 43.3 us for 42.6, five long ones 60.3 for 58.7).
+// (Scores do not show it: neighbours 0.01 apart at 2400 are off by 4e-4, FP32's last place there being 2e-4.)
 //
 // Bound: the bytes of the codes and scales, read once per 32 columns.  Up to 8 columns the decode's issue is
 // close behind (integer pipe 40 %, 1.5 instructions a cycle); with more, the MMAs and the decode of
