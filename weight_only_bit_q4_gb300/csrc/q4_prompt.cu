@@ -30,8 +30,8 @@
 //
 // Measured (captured calls; in a long row of calls, under the power cap, the first takes 355 to 360 us): 8192
 // tokens, 32 + 8 heads of 128: 330 us, 1665 TFLOP/s (0.86 of the measured bf16 rate); 16384
-// tokens of seven prompts, 32 + 4 heads: 340 us; 2000 tokens of nine prompts, 28 + 4 heads of 96: 19.1 us;
-// 133 tokens: 8.4 us.  With 8192 tokens, 32 + 8 heads of 96 take 310 us, of 64 270: softmax, P V and
+// tokens of seven prompts, 32 + 4 heads: 345 us; 2000 tokens of nine prompts, 28 + 4 heads of 96: 19.1 us;
+// 133 tokens: 8.5 us.  With 8192 tokens, 32 + 8 heads of 96 take 310 us, of 64 270: softmax, P V and
 // Q K^T of one tile follow one another, and the other tile's products are too short to hide that.
 // In the middle of a long prompt (heads of 128) a block of both tiles takes 2600 to 2700 cycles, 2048 of them
 // the MMAs' at their nominal rate: Q K^T reads both operands from shared memory, which at 128
